@@ -12,6 +12,9 @@ not been built: there is no other implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
+import functools
+import math
 import os
 
 import torch
@@ -29,12 +32,25 @@ DCP_OK, DCP_ERR_INVALID_ARG, DCP_ERR_UNSUPPORTED, DCP_ERR_CUDA, DCP_ERR_TIMEOUT,
 DCP_ATTN_GQA, DCP_ATTN_MLA = 0, 1
 DCP_KERNEL_NONE, DCP_KERNEL_MLA_TC, DCP_KERNEL_GQA_TC, DCP_KERNEL_SIMT = range(4)
 KINDS = {"gqa": DCP_ATTN_GQA, "mla": DCP_ATTN_MLA}
+DCP_TREE_MAX_NODES = 256
+DCP_COMMIT_MAX_ACCEPT = 256
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class DcpAttnDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "kind", "batch", "q_len", "num_q_heads", "num_kv_heads", "head_dim_qk", "head_dim_v",
         "block_size", "num_blocks", "max_local_blocks")]
+
+
+class DcpRopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rot_dim", "rot_offset", "layout", "scaling", "original_max_position")] + [
+        ("mscale", ctypes.c_float)] + [(n, ctypes.c_double) for n in ("base", "factor", "beta_fast", "beta_slow")]
+
+
+class DcpAppendStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("k_batch", "k_token", "v_batch", "v_token", "q_batch", "q_token")]
 
 
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -59,6 +75,25 @@ _lib.dcp_decode_attn_launches.restype = _i32
 _lib.dcp_decode_attn_launches.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
 _lib.dcp_get_last_device_status.restype = _i32
 _lib.dcp_get_last_device_status.argtypes = [_vp]
+_i64 = ctypes.c_int64
+_lib.dcp_rope_steps.restype = _i32
+_lib.dcp_rope_steps.argtypes = [ctypes.POINTER(DcpRopeDesc), _vp, _vp]
+_lib.dcp_kv_cache_append.restype = _i32
+_lib.dcp_kv_cache_append.argtypes = [ctypes.POINTER(DcpAttnDesc), ctypes.POINTER(DcpRopeDesc), _vp, _vp, _vp, _vp,
+                                     ctypes.POINTER(DcpAppendStrides), _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32,
+                                     _vp]
+_lib.dcp_tree_attn_workspace_size.restype = _sz
+_lib.dcp_tree_attn_workspace_size.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
+_lib.dcp_tree_attn.restype = _i32
+_lib.dcp_tree_attn.argtypes = [ctypes.POINTER(DcpAttnDesc), _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _vp,
+                               _vp, _vp, _sz, _vp]
+_lib.dcp_tree_attn_kernel_kind.restype = _i32
+_lib.dcp_tree_attn_kernel_kind.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
+_lib.dcp_tree_attn_launches.restype = _i32
+_lib.dcp_tree_attn_launches.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
+_lib.dcp_kv_cache_commit.restype = _i32
+_lib.dcp_kv_cache_commit.argtypes = [ctypes.POINTER(DcpAttnDesc), _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32,
+                                     _vp]
 _lib.dcp_status_string.restype = ctypes.c_char_p
 _lib.dcp_status_string.argtypes = [_i32]
 
@@ -199,6 +234,239 @@ def dcp_merge(partial_out, lse, dcp_size, out=None, out_lse=None, want_lse=True,
     _check(_lib.dcp_merge(_ptr(partial_out), _ptr(lse), dcp_size, B, Lq, Hq, Dv, _ptr(out),
                           _ptr(out_lse), _stream(stream)), "dcp_merge")
     return out, out_lse
+
+
+# ---------------------------------------------------------------------------
+# Speculative verify: rotary append, drafted-tree attention, commit
+# ---------------------------------------------------------------------------
+
+def _need(ok, what):
+    if not ok:
+        raise DcpError(DCP_ERR_INVALID_ARG, what)
+
+
+def _need_tensors(what, dtype, *tensors):
+    """The tensors (None: skipped) are of ``dtype`` on the current device, and contiguous."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None:
+            _need(t.dtype is dtype and t.get_device() == device and t.is_contiguous(),
+                  f"{what}: a tensor is not a contiguous {dtype} tensor on the current device")
+
+
+@functools.lru_cache(maxsize=1024)
+def _cached_desc(*fields) -> DcpAttnDesc:
+    return DcpAttnDesc(*fields)
+
+
+def _cache_fields(what, kind, kv_cache, block_tables, batch, dcp_size):
+    """(kind, Hkv, Dqk, block_size, num_blocks, max_local_blocks) from the cache's tensors."""
+    kind = KINDS.get(kind, kind)
+    if kind == DCP_ATTN_GQA:
+        _need(kv_cache.dim() == 5 and kv_cache.shape[0] == 2, f"{what}: a GQA cache is [2][blocks][block_size][Hkv][D]")
+        _, nb, bs, hkv, dim = kv_cache.shape
+    else:
+        _need(kv_cache.dim() == 3, f"{what}: an MLA cache is [blocks][block_size][Dqk]")
+        (nb, bs, dim), hkv = kv_cache.shape, 1
+    _need(block_tables.dim() == 3 and block_tables.shape[0] == dcp_size and block_tables.shape[1] == batch,
+          f"{what}: block_tables is [dcp_size][batch][max_local_blocks]")
+    return kind, hkv, dim, bs, nb, block_tables.shape[2]
+
+
+def _need_lens(what, batch, *tensors):
+    for t in tensors:
+        _need(t is None or (t.dim() == 1 and t.shape[0] == batch), f"{what}: lengths are [batch]")
+
+
+@dataclasses.dataclass(frozen=True)
+class RopeTable:
+    """A rotation (``desc``) and its frequency table on the device (``steps``, int64 [rot_dim / 2])."""
+    desc: DcpRopeDesc
+    steps: torch.Tensor
+
+
+def dcp_rope_table(rot_dim, base=10000.0, layout="half", rot_offset=0, scaling="none", factor=1.0,
+                   original_max_position=0, beta_fast=32.0, beta_slow=1.0, mscale=None, inv_freq=None,
+                   device="cuda") -> RopeTable:
+    """The rotation of dims [rot_offset, rot_offset + rot_dim) of every head, made once and passed
+    to every dcp_kv_cache_append.  ``scaling``: "none", "linear", "ntk" or "yarn", by ``factor``;
+    ``mscale`` multiplies the rotated values (None: 1, and 0.1 ln(factor) + 1 for "yarn" with
+    factor > 1); ``inv_freq`` (a float64 sequence of rot_dim / 2) replaces base and scaling."""
+    _need(layout in ROPE_LAYOUTS and scaling in ROPE_SCALINGS, "dcp_rope_table: layout or scaling")
+    if mscale is None:
+        mscale = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0
+    desc = DcpRopeDesc(rot_dim, rot_offset, ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], int(original_max_position or 0),
+                       mscale, base, factor, beta_fast, beta_slow)
+    steps = torch.empty((max(rot_dim // 2, 1),), dtype=torch.int64)
+    freqs = None
+    if inv_freq is not None:
+        freqs = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+        _need(freqs.dim() == 1 and freqs.numel() == rot_dim // 2, "dcp_rope_table: inv_freq is [rot_dim / 2]")
+    _check(_lib.dcp_rope_steps(ctypes.byref(desc), _ptr(freqs), _ptr(steps)), "dcp_rope_table")
+    return RopeTable(desc, steps.to(device))
+
+
+def tree_mask(parents):
+    """(mask int32 [.][L][ceil(L / 32)], depths int32 [.][L]) on the host of trees given by their
+    nodes' parents, an integer array [L] or [.][L] with -1 at a root and parents before children:
+    every node sees itself and its ancestors.  For trees that are the same from step to step;
+    move both to the device once and pass them as ``tree_mask`` and ``pos_offsets``."""
+    parents = torch.as_tensor(parents)
+    flat = parents.reshape(-1, parents.shape[-1]).tolist()
+    words = (parents.shape[-1] + 31) // 32
+    masks, depths = [], []
+    for row in flat:
+        seen, depth = [], []
+        for i, p in enumerate(row):
+            _need(-1 <= p < i, "tree_mask: a parent comes before its child, -1 at a root")
+            seen.append((seen[p] if p >= 0 else 0) | 1 << i)
+            depth.append(depth[p] + 1 if p >= 0 else 0)
+        words_of = [[(s >> (32 * w)) & 0xFFFFFFFF for w in range(words)] for s in seen]
+        masks.append([[w - (1 << 32) if w >> 31 else w for w in ws] for ws in words_of])
+        depths.append(depth)
+    shape = parents.shape[:-1]
+    return (torch.tensor(masks, dtype=torch.int32).view(*shape, -1, words),
+            torch.tensor(depths, dtype=torch.int32).view(*shape, -1))
+
+
+def _row_strides(what, t, batch, n, row_shape):
+    """(batch, token) strides in elements of rows [batch][n][*row_shape], each row contiguous."""
+    _need(t.dtype is torch.bfloat16 and t.get_device() == torch.cuda.current_device(),
+          f"{what}: rows are bfloat16 on the current device")
+    _need(t.shape == (batch, n, *row_shape), f"{what}: rows are {(batch, n, *row_shape)}, got {tuple(t.shape)}")
+    stride = t.stride()
+    inner = stride[-1] == 1 and (len(row_shape) == 1 or row_shape[0] == 1 or stride[-2] == row_shape[-1])
+    _need(inner, f"{what}: a token's row is contiguous")
+    # the stride of a dimension of one entry says nothing: the contiguous one stands for it
+    width = row_shape[-1] * (row_shape[0] if len(row_shape) == 2 else 1)
+    token = stride[1] if n > 1 else width
+    return (stride[0] if batch > 1 else token * n), token
+
+
+def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dcp_size, interleave, rope, q=None,
+                        q_out=None, q_lens=None, pos_offsets=None, stream=None):
+    """Store new tokens' rows in their shards' cache cells, keys rotated, and rotate their queries.
+
+    new_k/new_v bf16: GQA [B][n][Hkv][D], MLA new_k [B][n][Dqk] and new_v None; q [B][n][Hq][Dqk] or
+    None.  A token's row is contiguous, tokens may lie apart (slices of a fused projection).
+    ``rope``: a RopeTable.  ``q_lens`` int32 [B]: tokens of each request (None: n).  ``pos_offsets``
+    int32 [B or 1][n]: a token's rotary position relative to the request's first new token (None:
+    0, 1, 2, ...; a tree passes its depths).  kv_cache and q_out are written in place, rows behind a
+    request's q_lens are left alone.  Returns (kv_cache, q_out); q_out may be q, and without one a
+    zeroed tensor is allocated."""
+    what = "dcp_kv_cache_append"
+    B, n = new_k.shape[:2]
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(what, kind, kv_cache, block_tables, B, dcp_size)
+    gqa = kind == DCP_ATTN_GQA
+    row = (hkv, dim) if gqa else (dim,)
+    _need((new_v is not None) == gqa, f"{what}: GQA takes new_v, MLA none")
+    _need_tensors(what, torch.bfloat16, kv_cache, q_out if q_out is not q else None)
+    _need_tensors(what, torch.int32, block_tables, seq_lens, q_lens, pos_offsets)
+    _need_lens(what, B, seq_lens, q_lens)
+    _need(rope.steps.get_device() == kv_cache.get_device(), f"{what}: the rope table is on another device")
+    k_batch, k_token = _row_strides(what, new_k, B, n, row)
+    v_batch, v_token = _row_strides(what, new_v, B, n, row) if gqa else (0, 0)
+    hq, q_batch, q_token = hkv, 0, 0
+    if q is not None:
+        _need(q.dim() == 4, f"{what}: q is [batch][n][Hq][Dqk]")
+        hq = q.shape[2]
+        q_batch, q_token = _row_strides(what, q, B, n, (hq, dim))
+        if q_out is None:
+            with torch.cuda.stream(stream):
+                q_out = torch.zeros((B, n, hq, dim), dtype=torch.bfloat16, device=q.device)
+        _need(q_out.shape == q.shape, f"{what}: q_out is shaped as q")
+    offsets_stride = 0
+    if pos_offsets is not None:
+        _need(pos_offsets.dim() == 2 and pos_offsets.shape[1] == n and pos_offsets.shape[0] in (1, B),
+              f"{what}: pos_offsets is [batch or 1][n]")
+        offsets_stride = n if pos_offsets.shape[0] == B else 0
+    desc = _cached_desc(kind, B, n, hq, hkv, dim, dim, bs, nb, max_lb)
+    strides = DcpAppendStrides(k_batch, k_token, v_batch, v_token, q_batch, q_token)
+    _check(_lib.dcp_kv_cache_append(desc, rope.desc, rope.steps.data_ptr(), new_k.data_ptr(), _ptr(new_v), _ptr(q),
+                                    strides, _ptr(q_out), _ptr(pos_offsets), offsets_stride, _ptr(q_lens),
+                                    kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), dcp_size,
+                                    interleave, _stream(stream)), what)
+    return kv_cache, q_out
+
+
+def dcp_tree_attn_workspace_size(desc: DcpAttnDesc, dcp_size: int) -> int:
+    return int(_lib.dcp_tree_attn_workspace_size(ctypes.byref(desc), dcp_size))
+
+
+def dcp_tree_attn_launches(desc: DcpAttnDesc, dcp_size: int) -> int:
+    """Kernels one dcp_tree_attn call enqueues for this shape (0: invalid)."""
+    return int(_lib.dcp_tree_attn_launches(ctypes.byref(desc), dcp_size))
+
+
+def dcp_tree_attn_kernel_kind(desc: DcpAttnDesc, dcp_size: int) -> int:
+    """Which kernel dcp_tree_attn runs for this shape (DCP_KERNEL_*)."""
+    return int(_lib.dcp_tree_attn_kernel_kind(ctypes.byref(desc), dcp_size))
+
+
+def dcp_tree_attn(kind, q, kv_cache, block_tables, seq_lens, tree_mask, dcp_size, interleave, scale, head_dim_v,
+                  q_lens=None, partial_out=None, lse=None, workspace=None, stream=None):
+    """Attention of a tree of drafted tokens over the sharded cache: per-shard partial outputs fp32
+    [N][B][Lq][Hq][Dv] and lse fp32 [N][B][Lq][Hq], for dcp_merge.
+
+    seq_lens count the nodes, which sit in a request's last q_lens positions (None: Lq each).
+    tree_mask int32 [B or 1][Lq][ceil(Lq / 32)]: bit j % 32 of word j / 32 of row i set where node i
+    sees node j; the context is seen by all (``tree_mask`` of this module packs parents)."""
+    what = "dcp_tree_attn"
+    _need(q.dim() == 4, f"{what}: q is [batch][Lq][Hq][Dqk]")
+    B, Lq, Hq, Dqk = q.shape
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(what, kind, kv_cache, block_tables, B, dcp_size)
+    words = (Lq + 31) // 32
+    _need(dim == Dqk, f"{what}: q and the cache differ in their head dim")
+    _need(tree_mask.dim() == 3 and tree_mask.shape[0] in (1, B) and tree_mask.shape[1:] == (Lq, words),
+          f"{what}: tree_mask is [batch or 1][Lq][ceil(Lq / 32)]")
+    _need_tensors(what, torch.bfloat16, q, kv_cache)
+    _need_tensors(what, torch.int32, block_tables, seq_lens, q_lens, tree_mask)
+    _need_lens(what, B, seq_lens, q_lens)
+    desc = _cached_desc(kind, B, Lq, Hq, hkv, Dqk, head_dim_v, bs, nb, max_lb)
+    if partial_out is None or lse is None or workspace is None:
+        # allocated for the stream that the kernels run on
+        with torch.cuda.stream(stream):
+            if partial_out is None:
+                partial_out = torch.empty((dcp_size, B, Lq, Hq, head_dim_v), dtype=torch.float32, device=q.device)
+            if lse is None:
+                lse = torch.empty((dcp_size, B, Lq, Hq), dtype=torch.float32, device=q.device)
+            size = dcp_tree_attn_workspace_size(desc, dcp_size)
+            if workspace is None and size:
+                workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
+    _need_tensors(what, torch.float32, partial_out, lse)
+    _need(partial_out.numel() == dcp_size * B * Lq * Hq * head_dim_v and lse.numel() == dcp_size * B * Lq * Hq,
+          f"{what}: partial_out is [N][B][Lq][Hq][Dv] and lse [N][B][Lq][Hq]")
+    ws_bytes = 0
+    if workspace is not None:
+        _need(workspace.get_device() == q.get_device() and workspace.is_contiguous(), f"{what}: workspace")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(_lib.dcp_tree_attn(desc, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+                              _ptr(q_lens), tree_mask.data_ptr(), Lq * words if tree_mask.shape[0] == B else 0, dcp_size,
+                              interleave, scale, partial_out.data_ptr(), lse.data_ptr(), _ptr(workspace), ws_bytes,
+                              _stream(stream)), what)
+    return partial_out, lse
+
+
+def dcp_kv_cache_commit(kind, kv_cache, block_tables, seq_lens, q_len, accepted, num_accepted, dcp_size, interleave,
+                        q_lens=None, new_seq_lens=None, stream=None):
+    """Move the cache rows of each request's accepted nodes (accepted int32 [B][max_accept], strictly
+    increasing, the first num_accepted[b] of them) to the positions right behind its context, in
+    place; returns the new lengths int32 [B] (``new_seq_lens`` may be seq_lens itself)."""
+    what = "dcp_kv_cache_commit"
+    _need(accepted.dim() == 2, f"{what}: accepted is [batch][max_accept]")
+    B, max_accept = accepted.shape
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(what, kind, kv_cache, block_tables, B, dcp_size)
+    if new_seq_lens is None:
+        with torch.cuda.stream(stream):
+            new_seq_lens = torch.empty((B,), dtype=torch.int32, device=kv_cache.device)
+    _need_tensors(what, torch.bfloat16, kv_cache)
+    _need_tensors(what, torch.int32, block_tables, seq_lens, q_lens, accepted, num_accepted, new_seq_lens)
+    _need_lens(what, B, seq_lens, q_lens, num_accepted, new_seq_lens)
+    desc = _cached_desc(kind, B, q_len, hkv, hkv, dim, dim, bs, nb, max_lb)
+    _check(_lib.dcp_kv_cache_commit(desc, kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+                                    _ptr(q_lens), accepted.data_ptr(), num_accepted.data_ptr(), max_accept,
+                                    new_seq_lens.data_ptr(), dcp_size, interleave, _stream(stream)), what)
+    return new_seq_lens
 
 
 def dcp_get_last_device_status(stream=None) -> int:

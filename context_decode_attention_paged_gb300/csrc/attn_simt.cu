@@ -8,10 +8,15 @@
 // rows of that KV head).  Rows of KV head g are (query i, head h) with
 // h in g's group; the causal limit of query i is a prefix of the shard-local
 // keys (local tokens are in global order), so masking is a per-row count.
+//
+// kTree: the drafted-tree form.  A row sees the shard's context keys and the
+// nodes its mask row has; a hidden key's weight is exactly 0 and its value is
+// not touched, so what it holds (NaN, infinities) stays out of the row.
 #include <cuda_bf16.h>
 
 #include "dcp_device.cuh"
 #include "dcp_internal.h"
+#include "dcp_tree.cuh"
 
 namespace dcp {
 namespace {
@@ -27,6 +32,7 @@ struct SimtParams {
   float* dst_lse;
 };
 
+template <bool kTree>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
   const AttnArgs& a = P.a;
   extern __shared__ float4 smem_f4[];
@@ -52,7 +58,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
   int* lim_s = reinterpret_cast<int*>(alpha_s + kRows);  // visible local keys per row
 
   const int S = a.seq_lens[b];
-  const bool bad_len = S < a.Lq;
+  TreeReq tree{};
+  if constexpr (kTree) tree = tree_request(a.seq_lens, a.q_lens, a.Lq, b);
+  const bool bad_len = kTree ? tree.bad : S < a.Lq;
   if (bad_len && tid == 0) set_status(a.status, DCP_ERR_BOUNDS);
   int L = bad_len ? 0 : local_len(S, r, a.I, a.N);
   if ((long long)L > (long long)a.max_lb * a.bs) {   // block table too short for seq_len
@@ -92,9 +100,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
     const int i = row / gsize;
     m_s[tid] = -INFINITY;
     l_s[tid] = 0.f;
-    lim_s[tid] = (row < rows_total && !bad_len)
-                     ? min(j_end, local_count_upto((long long)S - a.Lq + i, r, a.I, a.N))
-                     : j_begin;
+    if constexpr (kTree)   // context keys; the nodes behind them go by the mask
+      lim_s[tid] = (row < rows_total && i < tree.n) ? min(j_end, local_count_upto(tree.base - 1, r, a.I, a.N)) : -1;
+    else
+      lim_s[tid] = (row < rows_total && !bad_len)
+                       ? min(j_end, local_count_upto((long long)S - a.Lq + i, r, a.I, a.N))
+                       : j_begin;
   }
   __syncthreads();
 
@@ -123,7 +134,14 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
     for (int idx = tid; idx < kRows * kTile; idx += kThreads) {
       const int rr = idx / kTile, tt = idx % kTile;
       float sc = -INFINITY;
-      if (j0 + tt < lim_s[rr]) {
+      bool sees = j0 + tt < lim_s[rr];
+      if constexpr (kTree) {
+        if (lim_s[rr] >= 0 && !sees && tt < nt) {
+          const int node = (int)(global_pos(j0 + tt, r, a.I, a.N) - tree.base), i = (row0 + rr) / gsize;
+          sees = tree_bit(a.tree_mask + b * a.tree_mask_stride + (long long)i * a.tree_words, node);
+        }
+      }
+      if (sees) {
         float acc = 0.f;
         const float* qr = q_s + rr * a.Dqk;
         const float* kr = k_s + tt * a.Dqk;
@@ -138,7 +156,17 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       float mx = m_s[tid];
       for (int tt = 0; tt < kTile; ++tt) mx = fmaxf(mx, p_s[tid * kTile + tt]);
       float alpha = 1.f, sum = 0.f;
-      if (mx != -INFINITY) {
+      if constexpr (kTree) {
+        // a NaN score is no maximum, but it makes the row NaN
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        alpha = (m_s[tid] == -INFINITY) ? 0.f : expf(m_s[tid] - ref);
+        for (int tt = 0; tt < kTile; ++tt) {
+          const float sc = p_s[tid * kTile + tt];
+          const float p = (sc == -INFINITY) ? 0.f : expf(sc - ref);
+          p_s[tid * kTile + tt] = p;
+          sum += p;
+        }
+      } else if (mx != -INFINITY) {
         alpha = (m_s[tid] == -INFINITY) ? 0.f : expf(m_s[tid] - mx);
         for (int tt = 0; tt < kTile; ++tt) {
           const float sc = p_s[tid * kTile + tt];
@@ -161,7 +189,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       const int rr = idx / a.Dv, d = idx % a.Dv;
       float acc = o_s[idx] * alpha_s[rr];
       const float* pr = p_s + rr * kTile;
-      for (int tt = 0; tt < nt; ++tt) acc = fmaf(pr[tt], vsrc[tt * vstride + d], acc);
+      for (int tt = 0; tt < nt; ++tt) {
+        if (kTree && pr[tt] == 0.f) continue;
+        acc = fmaf(pr[tt], vsrc[tt * vstride + d], acc);
+      }
       o_s[idx] = acc;
     }
     __syncthreads();
@@ -175,7 +206,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
     const int i = row / gsize, h = g * gsize + row % gsize;
     const float l = l_s[rr];
     const long long unit_row = ((((long long)r * a.B + b) * a.Lq + i) * P.n_split + s) * a.Hq + h;
-    P.dst_o[unit_row * a.Dv + d] = l > 0.f ? o_s[idx] / l : 0.f;
+    const bool any = kTree ? !(l == 0.f) : l > 0.f;
+    P.dst_o[unit_row * a.Dv + d] = any ? o_s[idx] / l : 0.f;
   }
   if (tid < kRows) {
     const int row = row0 + tid;
@@ -184,7 +216,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       const float l = l_s[tid];
       const long long unit_row =
           ((((long long)r * a.B + b) * a.Lq + i) * P.n_split + s) * a.Hq + h;
-      P.dst_lse[unit_row] = l > 0.f ? m_s[tid] + logf(l) : -INFINITY;
+      const bool any = kTree ? !(l == 0.f) : l > 0.f;
+      P.dst_lse[unit_row] = any ? m_s[tid] + logf(l) : -INFINITY;
     }
   }
 }
@@ -220,13 +253,13 @@ cudaError_t launch_attn_simt(const AttnArgs& a, const SplitPlan& p) {
     P.dst_lse = a.lse;
   }
   const size_t smem = simt_smem_bytes(a);
-  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  void (*kern)(SimtParams) = a.tree_mask ? attn_simt_kernel<true> : attn_simt_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int gsize = a.Hq / a.Hkv;
   dim3 grid((unsigned)(a.N * a.B * p.n_split), (unsigned)a.Hkv,
             (unsigned)((a.Lq * gsize + kRows - 1) / kRows));
-  attn_simt_kernel<<<grid, kThreads, smem, a.stream>>>(P);
+  kern<<<grid, kThreads, smem, a.stream>>>(P);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.n_split <= 1) return e;
   return launch_split_combine(a, p);

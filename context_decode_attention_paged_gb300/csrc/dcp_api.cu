@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -104,6 +105,7 @@ dcp_status_t make_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t inter
 enum class Impl { kSimt, kMlaTc, kGqaTc };
 
 Impl select_impl(const AttnArgs& a) {
+  if (a.tree_words > 0) return Impl::kSimt;
   if (mla_tc_supported(a)) return Impl::kMlaTc;
   if (gqa_tc_supported(a)) return Impl::kGqaTc;
   return Impl::kSimt;
@@ -119,6 +121,51 @@ SplitPlan plan_for(const AttnArgs& a, Impl impl, int sm_count) {
     default:
       return plan_attn_simt(a, sm_count);
   }
+}
+
+// Run the planned kernel of a call whose arguments have been checked.
+dcp_status_t launch_impl(const AttnArgs& a, Impl impl, const SplitPlan& plan) {
+  switch (impl) {
+    case Impl::kMlaTc:
+      return from_cuda(launch_attn_mla_tc(a, plan));
+    case Impl::kGqaTc:
+      return from_cuda(launch_attn_gqa_tc(a, plan));
+    case Impl::kSimt:
+    default:
+      return from_cuda(launch_attn_simt(a, plan));
+  }
+}
+
+int32_t kind_of(Impl impl) {
+  return impl == Impl::kMlaTc ? DCP_KERNEL_MLA_TC : impl == Impl::kGqaTc ? DCP_KERNEL_GQA_TC : DCP_KERNEL_SIMT;
+}
+
+// Arguments of a drafted-tree call: those of dcp_decode_attn and the node limit.
+dcp_status_t make_tree_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave, float scale, AttnArgs* a) {
+  const dcp_status_t st = make_args(d, dcp_size, interleave, scale, d ? d->q_len : 1, a);
+  if (st != DCP_OK) return st;
+  if (d->q_len > DCP_TREE_MAX_NODES) return DCP_ERR_UNSUPPORTED;
+  a->tree_words = (d->q_len + 31) / 32;
+  return DCP_OK;
+}
+
+// The cache side of an append or commit call (the checks of dcp_kv_cache_write).
+bool cache_desc_ok(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave) {
+  if (d->kind != DCP_ATTN_GQA && d->kind != DCP_ATTN_MLA) return false;
+  if (d->batch < 1 || d->q_len < 1 || d->num_kv_heads < 1 || d->head_dim_qk < 1 || d->block_size < 1 ||
+      d->num_blocks < 1 || d->max_local_blocks < 1 || dcp_size < 1 || interleave < 1)
+    return false;
+  if (d->kind == DCP_ATTN_MLA && d->num_kv_heads != 1) return false;
+  const long long row_bytes = 2LL * d->head_dim_qk * d->num_kv_heads;
+  if (d->head_dim_qk % 8 || row_bytes > (1LL << 20)) return false;
+  return (long long)d->batch * dcp_size <= (1LL << 31) &&
+         (long long)d->batch * dcp_size * d->max_local_blocks <= (1LL << 31) &&
+         (long long)d->num_blocks * d->block_size <= (1LL << 31);
+}
+
+bool rope_ok(const dcp_rope_desc_t* r) {
+  return r && r->rot_dim >= 2 && r->rot_dim % 2 == 0 && r->rot_dim <= 1024 && r->rot_offset >= 0 &&
+         (r->layout == DCP_ROPE_HALF || r->layout == DCP_ROPE_INTERLEAVED) && std::isfinite(r->mscale);
 }
 
 }  // namespace
@@ -254,15 +301,7 @@ dcp_status_t dcp_decode_attn(const dcp_attn_desc_t* d, const void* q, const void
   a.status = status_ptr(static_cast<cudaStream_t>(stream));
   if (!a.status) return DCP_ERR_CUDA;
   a.stream = static_cast<cudaStream_t>(stream);
-  switch (impl) {
-    case Impl::kMlaTc:
-      return from_cuda(launch_attn_mla_tc(a, plan));
-    case Impl::kGqaTc:
-      return from_cuda(launch_attn_gqa_tc(a, plan));
-    case Impl::kSimt:
-    default:
-      return from_cuda(launch_attn_simt(a, plan));
-  }
+  return launch_impl(a, impl, plan);
 }
 
 dcp_status_t dcp_kv_cache_write(const dcp_attn_desc_t* d, const void* new_k, const void* new_v,
@@ -337,12 +376,181 @@ int32_t dcp_decode_attn_launches(const dcp_attn_desc_t* d, int32_t dcp_size) {
 int32_t dcp_decode_attn_kernel_kind(const dcp_attn_desc_t* d, int32_t dcp_size) {
   AttnArgs a{};
   if (make_args(d, dcp_size, 1, 1.0f, d ? d->q_len : 1, &a) != DCP_OK) return DCP_KERNEL_NONE;
-  switch (select_impl(a)) {
-    case Impl::kMlaTc: return DCP_KERNEL_MLA_TC;
-    case Impl::kGqaTc: return DCP_KERNEL_GQA_TC;
-    case Impl::kSimt:
-    default: return DCP_KERNEL_SIMT;
+  return kind_of(select_impl(a));
+}
+
+size_t dcp_tree_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dcp_size) {
+  AttnArgs a{};
+  if (make_tree_args(d, dcp_size, 1, 1.0f, &a) != DCP_OK) return 0;
+  return plan_for(a, select_impl(a), device_sm_count()).ws_bytes;
+}
+
+int32_t dcp_tree_attn_launches(const dcp_attn_desc_t* d, int32_t dcp_size) {
+  AttnArgs a{};
+  if (make_tree_args(d, dcp_size, 1, 1.0f, &a) != DCP_OK) return 0;
+  const SplitPlan plan = plan_for(a, select_impl(a), device_sm_count());
+  return 1 + (plan.n_split > 1 ? 1 : 0) + (plan.lpt_order ? 1 : 0);
+}
+
+int32_t dcp_tree_attn_kernel_kind(const dcp_attn_desc_t* d, int32_t dcp_size) {
+  AttnArgs a{};
+  if (make_tree_args(d, dcp_size, 1, 1.0f, &a) != DCP_OK) return DCP_KERNEL_NONE;
+  return kind_of(select_impl(a));
+}
+
+dcp_status_t dcp_tree_attn(const dcp_attn_desc_t* d, const void* q, const void* kv_cache,
+                           const int32_t* block_tables, const int32_t* seq_lens,
+                           const int32_t* q_lens, const uint32_t* tree_mask, int64_t tree_mask_stride,
+                           int32_t dcp_size, int32_t interleave, float scale, float* partial_out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange range("dcp_tree_attn");
+  AttnArgs a{};
+  const dcp_status_t st = make_tree_args(d, dcp_size, interleave, scale, &a);
+  if (st != DCP_OK) return st;
+  if (!q || !kv_cache || !block_tables || !seq_lens || !tree_mask || !partial_out || !lse)
+    return DCP_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(partial_out, 16) || !aligned(lse, 4) ||
+      !aligned(tree_mask, 4))
+    return DCP_ERR_INVALID_ARG;
+  if (tree_mask_stride != 0 && tree_mask_stride < (int64_t)a.Lq * a.tree_words) return DCP_ERR_INVALID_ARG;
+  const Impl impl = select_impl(a);
+  const SplitPlan plan = plan_for(a, impl, device_sm_count());
+  if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes || !aligned(workspace, 256)))
+    return DCP_ERR_INVALID_ARG;
+  a.q = q;
+  a.kv = kv_cache;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.q_lens = q_lens;
+  a.tree_mask = tree_mask;
+  a.tree_mask_stride = tree_mask_stride;
+  a.partial_out = partial_out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.status = status_ptr(a.stream);
+  if (!a.status) return DCP_ERR_CUDA;
+  return launch_impl(a, impl, plan);
+}
+
+dcp_status_t dcp_rope_steps(const dcp_rope_desc_t* r, const double* inv_freq, uint64_t* steps) {
+  if (!rope_ok(r) || !steps) return DCP_ERR_INVALID_ARG;
+  const int pairs = r->rot_dim / 2;
+  const double two_pi = 6.283185307179586;
+  double base = r->base, lo = 0, hi = 0;
+  if (!inv_freq) {
+    if (!std::isfinite(base) || !(base > 1.0)) return DCP_ERR_INVALID_ARG;
+    if (r->scaling < DCP_ROPE_SCALE_NONE || r->scaling > DCP_ROPE_SCALE_YARN) return DCP_ERR_INVALID_ARG;
+    if (r->scaling != DCP_ROPE_SCALE_NONE && !(std::isfinite(r->factor) && r->factor > 0.0)) return DCP_ERR_INVALID_ARG;
+    if (r->scaling == DCP_ROPE_SCALE_NTK) {
+      if (r->rot_dim < 4) return DCP_ERR_INVALID_ARG;
+      base *= std::pow(r->factor, (double)r->rot_dim / (r->rot_dim - 2));
+    }
+    if (r->scaling == DCP_ROPE_SCALE_YARN) {
+      if (r->original_max_position < 1 || !(r->beta_slow > 0.0) || !(r->beta_fast > r->beta_slow) ||
+          !std::isfinite(r->beta_fast))
+        return DCP_ERR_INVALID_ARG;
+      auto pair_of = [&](double turns) {
+        return r->rot_dim * std::log(r->original_max_position / (turns * two_pi)) / (2.0 * std::log(base));
+      };
+      lo = std::max(std::floor(pair_of(r->beta_fast)), 0.0);
+      hi = std::min(std::ceil(pair_of(r->beta_slow)), (double)(r->rot_dim - 1));
+    }
   }
+  for (int k = 0; k < pairs; ++k) {
+    double f;
+    if (inv_freq) {
+      f = inv_freq[k];
+      if (!std::isfinite(f)) return DCP_ERR_INVALID_ARG;
+    } else {
+      f = std::pow(base, -2.0 * k / r->rot_dim);
+      if (r->scaling == DCP_ROPE_SCALE_LINEAR) f /= r->factor;
+      if (r->scaling == DCP_ROPE_SCALE_YARN) {
+        const double ramp = std::min(std::max((k - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+        f = f / r->factor * ramp + f * (1.0 - ramp);
+      }
+    }
+    const double turns = f / two_pi;
+    const double frac = turns - std::floor(turns);          // [0, 1); 1 after rounding is a whole turn
+    steps[k] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0;
+  }
+  return DCP_OK;
+}
+
+dcp_status_t dcp_kv_cache_append(const dcp_attn_desc_t* d, const dcp_rope_desc_t* rope, const uint64_t* rope_steps,
+                                 const void* new_k, const void* new_v, const void* q,
+                                 const dcp_append_strides_t* strides, void* q_out, const int32_t* pos_offsets,
+                                 int64_t pos_offsets_stride, const int32_t* q_lens, void* kv_cache,
+                                 const int32_t* block_tables, const int32_t* seq_lens, int32_t dcp_size,
+                                 int32_t interleave, void* stream) {
+  NvtxRange range("dcp_kv_cache_append");
+  if (!d || !rope_steps || !new_k || !kv_cache || !block_tables || !seq_lens) return DCP_ERR_INVALID_ARG;
+  if (!cache_desc_ok(d, dcp_size, interleave) || !rope_ok(rope)) return DCP_ERR_INVALID_ARG;
+  const bool gqa = d->kind == DCP_ATTN_GQA;
+  if (gqa != (new_v != nullptr) || (q != nullptr) != (q_out != nullptr)) return DCP_ERR_INVALID_ARG;
+  if (rope->rot_offset > d->head_dim_qk - rope->rot_dim) return DCP_ERR_INVALID_ARG;
+  if (q && (d->num_q_heads < 1 || (long long)d->num_q_heads * d->head_dim_qk > (1LL << 24))) return DCP_ERR_INVALID_ARG;
+  if (!aligned(new_k, 16) || !aligned(kv_cache, 16) || !aligned(rope_steps, 8) || (new_v && !aligned(new_v, 16)) ||
+      (q && (!aligned(q, 16) || !aligned(q_out, 16))) || (pos_offsets && !aligned(pos_offsets, 4)))
+    return DCP_ERR_INVALID_ARG;
+  if (pos_offsets && pos_offsets_stride != 0 && pos_offsets_stride < d->q_len) return DCP_ERR_INVALID_ARG;
+  if ((long long)d->batch * d->q_len > INT_MAX) return DCP_ERR_INVALID_ARG;
+  const long long k_row = (long long)d->num_kv_heads * d->head_dim_qk;
+  const long long q_row = q ? (long long)d->num_q_heads * d->head_dim_qk : 0;
+  AppendArgs a{};
+  a.k_batch = k_row * d->q_len, a.k_token = k_row;
+  a.v_batch = k_row * d->q_len, a.v_token = k_row;
+  a.q_batch = q_row * d->q_len, a.q_token = q_row;
+  if (strides) {
+    auto stride_ok = [](int64_t batch, int64_t token, long long row) {
+      return batch % 8 == 0 && token % 8 == 0 && batch >= 0 && (token == 0 || token >= row);
+    };
+    if (!stride_ok(strides->k_batch, strides->k_token, k_row) ||
+        (gqa && !stride_ok(strides->v_batch, strides->v_token, k_row)) ||
+        (q && !stride_ok(strides->q_batch, strides->q_token, q_row)))
+      return DCP_ERR_INVALID_ARG;
+    if (q && q == q_out && (strides->q_token != a.q_token || strides->q_batch != a.q_batch)) return DCP_ERR_INVALID_ARG;
+    a.k_batch = strides->k_batch, a.k_token = strides->k_token;
+    a.v_batch = strides->v_batch, a.v_token = strides->v_token;
+    a.q_batch = strides->q_batch, a.q_token = strides->q_token;
+  }
+  a.k = new_k, a.v = new_v, a.q = q, a.q_out = q_out;
+  a.steps = reinterpret_cast<const unsigned long long*>(rope_steps);
+  a.pos_offsets = pos_offsets, a.pos_stride = pos_offsets_stride, a.q_lens = q_lens;
+  a.cache = kv_cache, a.block_tables = block_tables, a.seq_lens = seq_lens;
+  a.B = d->batch, a.L = d->q_len, a.Hq = q ? d->num_q_heads : 0, a.Hkv = d->num_kv_heads, a.D = d->head_dim_qk;
+  a.bs = d->block_size, a.num_blocks = d->num_blocks, a.max_lb = d->max_local_blocks, a.N = dcp_size, a.I = interleave;
+  a.rot_dim = rope->rot_dim, a.rot_offset = rope->rot_offset;
+  a.interleaved = rope->layout == DCP_ROPE_INTERLEAVED, a.mscale = rope->mscale;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.status = status_ptr(a.stream);
+  if (!a.status) return DCP_ERR_CUDA;
+  return from_cuda(launch_kv_append(a));
+}
+
+dcp_status_t dcp_kv_cache_commit(const dcp_attn_desc_t* d, void* kv_cache, const int32_t* block_tables,
+                                 const int32_t* seq_lens, const int32_t* q_lens, const int32_t* accepted,
+                                 const int32_t* num_accepted, int32_t max_accept, int32_t* new_seq_lens,
+                                 int32_t dcp_size, int32_t interleave, void* stream) {
+  NvtxRange range("dcp_kv_cache_commit");
+  if (!d || !kv_cache || !block_tables || !seq_lens || !accepted || !num_accepted || !new_seq_lens)
+    return DCP_ERR_INVALID_ARG;
+  if (!cache_desc_ok(d, dcp_size, interleave) || max_accept < 1) return DCP_ERR_INVALID_ARG;
+  if (max_accept > DCP_COMMIT_MAX_ACCEPT) return DCP_ERR_UNSUPPORTED;
+  if (!aligned(kv_cache, 16)) return DCP_ERR_INVALID_ARG;
+  CommitArgs a{};
+  a.cache = kv_cache;
+  a.gqa = d->kind == DCP_ATTN_GQA;
+  a.block_tables = block_tables, a.seq_lens = seq_lens, a.q_lens = q_lens;
+  a.accepted = accepted, a.num_accepted = num_accepted, a.new_seq_lens = new_seq_lens;
+  a.B = d->batch, a.L = d->q_len, a.max_accept = max_accept;
+  a.row16 = d->num_kv_heads * d->head_dim_qk / 8;
+  a.bs = d->block_size, a.num_blocks = d->num_blocks, a.max_lb = d->max_local_blocks, a.N = dcp_size, a.I = interleave;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.status = status_ptr(a.stream);
+  if (!a.status) return DCP_ERR_CUDA;
+  return from_cuda(launch_kv_commit(a));
 }
 
 }  // extern "C"

@@ -25,6 +25,11 @@ struct AttnArgs {
   size_t workspace_bytes;
   int* status;           // device status word
   cudaStream_t stream;
+  // drafted-tree attention (null tree_mask: causal queries)
+  const uint32_t* tree_mask;       // [B][Lq][tree_words], requests tree_mask_stride words apart
+  long long tree_mask_stride;
+  int tree_words;                  // ceil(Lq / 32)
+  const int32_t* q_lens;           // [B] nodes per request, or null (Lq each)
 };
 
 // How a call is cut into work units along the local KV axis.
@@ -69,6 +74,38 @@ cudaError_t launch_merge(const float* partial_out, const float* lse, int N, int 
 cudaError_t launch_kv_write(const void* new_k, const void* new_v, void* kv_cache, const int32_t* block_tables,
                             const int32_t* seq_lens, int B, int n_new, int N, int I, int bs, int max_lb,
                             int num_blocks, int row_bytes, int* status, cudaStream_t stream);
+
+// Rotary append: see dcp_kv_cache_append (strides in elements).
+struct AppendArgs {
+  const void *k, *v, *q;
+  void* q_out;
+  long long k_batch, k_token, v_batch, v_token, q_batch, q_token;
+  const unsigned long long* steps;
+  const int32_t* pos_offsets;
+  long long pos_stride;
+  const int32_t* q_lens;
+  void* cache;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  int B, L, Hq, Hkv, D, bs, num_blocks, max_lb, N, I;
+  int rot_dim, rot_offset, interleaved;
+  float mscale;
+  int* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv_append(const AppendArgs& a);
+
+// Move the accepted nodes' rows behind the context: see dcp_kv_cache_commit.
+struct CommitArgs {
+  void* cache;
+  bool gqa;
+  const int32_t *block_tables, *seq_lens, *q_lens, *accepted, *num_accepted;
+  int32_t* new_seq_lens;
+  int B, L, max_accept, row16, bs, num_blocks, max_lb, N, I;
+  int* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv_commit(const CommitArgs& a);
 
 // Combine n_split workspace partials into partial_out / lse (row a5).
 cudaError_t launch_split_combine(const AttnArgs& a, const SplitPlan& p);

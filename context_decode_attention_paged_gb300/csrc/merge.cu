@@ -17,14 +17,16 @@ namespace {
 constexpr int kWarpsPerBlock = 8;
 
 // Weights for up to 32 sources, one per lane: returns this lane's weight and
-// writes the merged LSE.  lane_lse is -inf for lanes >= n.
+// writes the merged LSE.  lane_lse is -inf for lanes >= n; a NaN makes the
+// merged row NaN, also where every other source is empty.
 __device__ __forceinline__ float lse_weights(float lane_lse, float* merged_lse) {
   float m = lane_lse;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (m == -INFINITY) {
-    *merged_lse = -INFINITY;
-    return 0.f;
+    const bool nan = __any_sync(0xffffffffu, lane_lse != lane_lse);
+    *merged_lse = nan ? NAN : -INFINITY;
+    return nan ? NAN : 0.f;
   }
   float e = (lane_lse == -INFINITY) ? 0.f : expf(lane_lse - m);
   float s = e;

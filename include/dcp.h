@@ -270,6 +270,161 @@ DCP_API int32_t dcp_decode_attn_kernel_kind(const dcp_attn_desc_t* d, int32_t dc
  * 129 to 16384 requests.  0 for an invalid descriptor.  Host only. */
 DCP_API int32_t dcp_decode_attn_launches(const dcp_attn_desc_t* d, int32_t dcp_size);
 
+/* ---------------------------------------------------------------------------
+ * Speculative verify over the sharded cache: append the drafted tokens' rows
+ * with their rotary position (dcp_kv_cache_append), attend with a tree mask
+ * (dcp_tree_attn, then dcp_merge), keep the accepted path (dcp_kv_cache_commit).
+ *
+ * Source: vLLM DCP blog, "未來發展藍圖" / speculative decoding with MTP (several
+ * drafted tokens verified in one step); the pages describe the chain form,
+ * which dcp_decode_attn computes.  In the tree form request b holds
+ * n_b = q_lens[b] nodes (q_len of them when q_lens is NULL) in its last n_b
+ * cache positions: node i sits at position S_b - n_b + i, S_b = seq_lens[b]
+ * counting the nodes.  The positions below S_b - n_b are its context.
+ *
+ * q_lens [B] may hold any value in [0, q_len]; a value outside it, or
+ * S_b < n_b, sets DCP_ERR_BOUNDS and the request is skipped.
+ * ------------------------------------------------------------------------- */
+
+/* Most tree nodes a request may have (q_len of dcp_tree_attn). */
+#define DCP_TREE_MAX_NODES 256
+/* Most nodes one dcp_kv_cache_commit may accept per request (max_accept). */
+#define DCP_COMMIT_MAX_ACCEPT 256
+
+typedef enum {
+  DCP_ROPE_HALF = 0,         /* pair k: dims k and k + rot_dim / 2 of the rotated part */
+  DCP_ROPE_INTERLEAVED = 1   /* pair k: dims 2k and 2k + 1                             */
+} dcp_rope_layout_t;
+
+typedef enum {
+  DCP_ROPE_SCALE_NONE = 0,   /* f_k = base^(-2k / rot_dim)                             */
+  DCP_ROPE_SCALE_LINEAR = 1, /* f_k / factor                                           */
+  DCP_ROPE_SCALE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) as the base    */
+  DCP_ROPE_SCALE_YARN = 3    /* f_k (1 - r_k) + f_k / factor r_k, r_k the ramp from the
+                                pair that turns beta_fast times within
+                                original_max_position to the one that turns beta_slow
+                                times: r_k = clamp((k - lo) / max(hi - lo, 1e-3), 0, 1),
+                                lo = max(floor(c(beta_fast)), 0),
+                                hi = min(ceil(c(beta_slow)), rot_dim - 1),
+                                c(n) = rot_dim ln(original / (2 pi n)) / (2 ln base)     */
+} dcp_rope_scaling_t;
+
+/* Rotary positions.  The pair (x0, x1) of a row at position p becomes
+ *   mscale * (x0 cos(p f_k) - x1 sin(p f_k),  x1 cos(p f_k) + x0 sin(p f_k)).
+ * Dims outside [rot_offset, rot_offset + rot_dim) are left as they are. */
+typedef struct {
+  int32_t rot_dim;               /* even, >= 2 (NTK: >= 4)                              */
+  int32_t rot_offset;            /* first rotated dim of a head                         */
+  int32_t layout;                /* dcp_rope_layout_t                                   */
+  int32_t scaling;               /* dcp_rope_scaling_t (used by dcp_rope_steps only)    */
+  int32_t original_max_position; /* YaRN                                                */
+  float mscale;                  /* finite; 1 for a plain rotation                      */
+  double base, factor;           /* base > 1 (unless inv_freq is given), factor > 0     */
+  double beta_fast, beta_slow;   /* YaRN, beta_fast > beta_slow > 0                     */
+} dcp_rope_desc_t;
+
+/* The frequency table of a rotation, on the HOST: steps[k] = frac(f_k / 2 pi) * 2^64,
+ * the part of a turn that one position adds to pair k, for k < rot_dim / 2.
+ * p * steps[k] modulo 2^64 is the exact phase of position p in the table's units, so far
+ * positions lose nothing.  inv_freq (host, [rot_dim / 2], finite) replaces base, scaling
+ * and factor when it is not NULL.  Copy the table to the device once and pass it to
+ * dcp_kv_cache_append.  Host only, no GPU work.
+ * Errors: INVALID_ARG. */
+DCP_API dcp_status_t dcp_rope_steps(const dcp_rope_desc_t* rope, const double* inv_freq,
+                                    uint64_t* steps);
+
+/* Strides of the rows dcp_kv_cache_append reads, in elements (multiples of 8): the rows of
+ * one token are contiguous ([Hkv][Dqk], [Hq][Dqk]), tokens and requests may lie apart (the
+ * slices of a fused projection).  The token stride is at least a token's row, or 0. */
+typedef struct {
+  int64_t k_batch, k_token, v_batch, v_token, q_batch, q_token;
+} dcp_append_strides_t;
+
+/* dcp_kv_cache_write with the rotary position applied on the way, and the queries of the
+ * same tokens rotated in the same launch.
+ * Node i < n_b of request b: its key (GQA: every KV head; MLA: the 576-value row) is
+ * rotated at position S_b - n_b + pos_offsets[b][i] and stored in the cache cell of
+ * position S_b - n_b + i; its value row is stored as it is; its query heads are rotated at
+ * the same position into q_out.  Products and sums run in fp32 (angles exactly, see
+ * dcp_rope_steps), each rotated value is rounded to bf16 once.  Nodes i >= n_b are not
+ * read and their rows of q_out are left as they were.
+ *  d             kind, batch, q_len, num_kv_heads, head_dim_qk, block_size, num_blocks,
+ *                max_local_blocks are used, and num_q_heads with q
+ *  rope_steps    uint64 [rot_dim / 2], from dcp_rope_steps
+ *  new_k, new_v, q   bf16 rows by `strides` (NULL: contiguous [B][q_len][...]); new_v is
+ *                NULL for MLA; q and q_out are both set or both NULL
+ *  q_out         bf16 [B][q_len][Hq][Dqk] out, contiguous; may be q itself (with q's
+ *                strides contiguous) but not overlap it otherwise
+ *  pos_offsets   int32 rows of q_len, pos_offsets_stride apart (0: one row for all
+ *                requests); NULL means i.  A tree passes its nodes' depths
+ *  q_lens        int32 [B] or NULL
+ *  kv_cache, block_tables, seq_lens as in dcp_kv_cache_write
+ * Alignment: the bf16 pointers and rows 16 bytes, rope_steps 8.
+ * Errors: INVALID_ARG; on the device, a local index past the block table or a block id
+ * >= num_blocks sets DCP_ERR_BOUNDS and that token's cache rows are skipped. */
+DCP_API dcp_status_t dcp_kv_cache_append(const dcp_attn_desc_t* d, const dcp_rope_desc_t* rope,
+                                         const uint64_t* rope_steps, const void* new_k,
+                                         const void* new_v, const void* q,
+                                         const dcp_append_strides_t* strides, void* q_out,
+                                         const int32_t* pos_offsets, int64_t pos_offsets_stride,
+                                         const int32_t* q_lens, void* kv_cache,
+                                         const int32_t* block_tables, const int32_t* seq_lens,
+                                         int32_t dcp_size, int32_t interleave, void* stream);
+
+/* Bytes of device scratch dcp_tree_attn needs for this shape, as
+ * dcp_decode_attn_workspace_size. */
+DCP_API size_t dcp_tree_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dcp_size);
+
+/* dcp_decode_attn for a tree of drafted tokens: query i < n_b of request b sees every key of
+ * the context (position < S_b - n_b) and the key of node j < n_b exactly when bit j % 32 of
+ * word tree_mask[b][i][j / 32] is set (a node that should see itself sets its own bit).
+ * Everything else is as there: partial_out fp32 [dcp][B][Lq][Hq][Dv] and lse fp32
+ * [dcp][B][Lq][Hq] per shard, for dcp_merge.  A row that sees no key of a shard, and every
+ * row i >= n_b, gives partial_out = 0 and lse = -inf there.
+ * Keys and values that a row does not see never reach it, whatever they hold (NaN,
+ * infinities); those that it sees propagate as the formula has it.
+ *  tree_mask     uint32 [B][q_len][words], words = ceil(q_len / 32); requests lie
+ *                tree_mask_stride words apart (0: one tree for all requests); bits of
+ *                nodes >= n_b are ignored
+ *  q_lens        int32 [B] or NULL
+ *  workspace     >= dcp_tree_attn_workspace_size(d, dcp_size) bytes, 256-byte aligned; two
+ *                calls (or two captured graphs) that may run at the same time need one each
+ * Errors: as dcp_decode_attn; UNSUPPORTED for q_len > DCP_TREE_MAX_NODES; INVALID_ARG for
+ * tree_mask NULL, not 4-byte aligned, or a stride that is neither 0 nor >= q_len * words.
+ * A block id >= num_blocks among a unit's visible keys skips the unit as there. */
+DCP_API dcp_status_t dcp_tree_attn(const dcp_attn_desc_t* d, const void* q, const void* kv_cache,
+                                   const int32_t* block_tables, const int32_t* seq_lens,
+                                   const int32_t* q_lens, const uint32_t* tree_mask,
+                                   int64_t tree_mask_stride, int32_t dcp_size,
+                                   int32_t interleave, float scale, float* partial_out,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* dcp_decode_attn_kernel_kind and dcp_decode_attn_launches for dcp_tree_attn. */
+DCP_API int32_t dcp_tree_attn_kernel_kind(const dcp_attn_desc_t* d, int32_t dcp_size);
+DCP_API int32_t dcp_tree_attn_launches(const dcp_attn_desc_t* d, int32_t dcp_size);
+
+/* Keeps the accepted path of a verified tree: the cache row (GQA: key and value) of node
+ * accepted[b][k] moves to position S_b - n_b + k, for k < num_accepted[b], and
+ * new_seq_lens[b] = S_b - n_b + num_accepted[b].  The path's keys were rotated at
+ * base + depth, which is where they end up, so the rows move as they are.
+ *  d             kind, batch, q_len, num_kv_heads, head_dim_qk, block_size, num_blocks,
+ *                max_local_blocks are used
+ *  q_lens        int32 [B] or NULL (every request holds q_len nodes)
+ *  accepted      int32 [B][max_accept], strictly increasing within a request (a path from
+ *                the root, nodes numbered parents first)
+ *  num_accepted  int32 [B], each in [0, min(max_accept, n_b)]
+ *  new_seq_lens  int32 [B] out; may be seq_lens itself
+ * Errors: INVALID_ARG; UNSUPPORTED for max_accept > DCP_COMMIT_MAX_ACCEPT; on the device, a
+ * count, a path or a block id out of range sets DCP_ERR_BOUNDS, the request's rows stay as
+ * they were and new_seq_lens[b] = seq_lens[b]. */
+DCP_API dcp_status_t dcp_kv_cache_commit(const dcp_attn_desc_t* d, void* kv_cache,
+                                         const int32_t* block_tables, const int32_t* seq_lens,
+                                         const int32_t* q_lens, const int32_t* accepted,
+                                         const int32_t* num_accepted, int32_t max_accept,
+                                         int32_t* new_seq_lens, int32_t dcp_size,
+                                         int32_t interleave, void* stream);
+
 /* Reads `stream`'s status word (the first device-side error of the calls
  * enqueued on that stream since the last read; DCP_OK if none) and clears it.
  * The read and the clear are enqueued on `stream` and the call then waits for

@@ -1,0 +1,721 @@
+// Drafted-tree attention for GQA on tcgen05 tensor cores.
+//
+// Compute step of the vLLM DCP blog ("DCP 執行流程") for a tree of drafted
+// tokens ("未來發展藍圖", speculative decoding): every shard attends the nodes'
+// queries to its local keys and returns a partial output with its LSE.
+//
+// Mathematics, for one row (node i, query head h) over the shard's keys:
+//   m = max_t x_t,  l = sum_t 2^(x_t - m),  o = sum_t 2^(x_t - m) v_t,
+//   x_t = scale log2(e) q . k_t  for the keys the row sees, -inf for the others,
+// in one pass with a running m that moves lazily (only past 2^8), so that o is
+// rescaled a few times in all; partial = o / l, lse = (m + log2 l) ln 2.
+//
+// A tree of n nodes puts n * Hq / Hkv query rows against each KV head: 64
+// nodes of a 16-head group are 1024 rows, 1024 flop per cache byte, four times
+// the ridge.  So rows sit on the 128 lanes of the MMA (M), unlike the decode
+// kernel, which has few rows and puts the keys there:
+//   S = Q K^T   (M = 128 rows, N = 128 keys, K = D; both K-major in shared memory)
+//   O += P V    (M = 128 rows, N = D, K = 128 keys; P from TMEM, V MN-major)
+// P carries two bf16 terms, P = bf16(p) + bf16(p - bf16(p)), as in the decode
+// kernel: 16 bits of each probability reach the product.
+//
+// Work unit = (shard, request, KV head, row block, KV split), one CTA with two
+// streams, each a 128-lane score/probability tile and an output tile in TMEM
+// and a warpgroup of 128 threads (thread = row):
+//   more than 128 rows: stream w takes rows [128 w, +128) of the block of 256
+//     and both go over every key tile, so each tile in shared memory serves
+//     256 rows;
+//   128 rows or fewer: both streams hold the same rows and take the key tiles
+//     in turn, two independent running softmaxes joined at the end.
+// Either way one stream's MMAs run while the other's probabilities are made:
+// the issuer sends PV(t), then S(t + 1) of a stream, then of the other.
+// P(t) overwrites S(t) in TMEM; MMAs of one thread complete in order, so
+// S(t + 1), behind PV(t), needs no barrier of its own, and the commit that
+// announces it also says that O is at rest and may be rescaled.
+//
+// Masks.  A shard's keys are dense in global order: context keys, then the
+// nodes it owns.  Tiles of context keys alone take no mask; in the others a
+// thread builds its row's 128 visibility bits from the mask words.  The value
+// product mixes all rows of a tile, so a value no row may see must not be
+// there: rows past the key range are zeroed in shared memory, and entries of
+// node values that are not finite are replaced by 0 and added in the epilogue
+// to the rows that see them.
+//
+// Warp roles (384 threads; setmaxnreg moves registers to the softmax warps):
+// warp 0 TMA producer (ring of K and V tiles), warp 1 MMA issuer and TMEM
+// owner, warps 4-7 and 8-11 the two streams.  Every wait is bounded; on expiry
+// the kernel records DCP_ERR_TIMEOUT, drains its copies and MMAs and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "dcp_device.cuh"
+#include "dcp_internal.h"
+#include "dcp_sm100.cuh"
+#include "dcp_tma.h"
+#include "dcp_tree.cuh"
+
+namespace dcp {
+namespace {
+
+using namespace sm100;
+
+constexpr int kNt = 128;                      // keys per tile, rows per stream
+constexpr int kMaxSlots = 12;                 // K or V tiles in the ring
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168, kCtrlRegs = 40, kSoftRegs = 232;
+static_assert(128 * kCtrlRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
+constexpr size_t kSmemLimit = 232448;         // dynamic shared memory per CTA
+constexpr float kLazyLog2 = 8.0f;             // m moves when scores pass it by more than this
+constexpr uint32_t kBarEpi = 1;               // named barrier of the two streams
+constexpr int kLptMaxBatch = 128;             // longest-first unit order up to this batch
+// TMEM columns (512 allocated): S and P of stream w at 128 w, O at 256 + 128 w
+constexpr uint32_t kColO = 256;
+
+struct Params {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* v_pool;
+  const int32_t *block_tables, *seq_lens, *q_lens;
+  const uint32_t* mask;
+  long long mask_stride;
+  float* dst_o;
+  float* dst_lse;
+  int* status;
+  int B, Lq, Hq, Hkv, N, I, max_lb, bs, num_blocks, n_split, split_tokens, words;
+  int row_blocks, block_rows;      // row blocks of a KV head and their rows (128 or 256)
+  int slots;
+  float scale_log2;
+  unsigned long long wait_ns;
+  int skip_tile;
+};
+
+struct Smem {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem_base;
+  int abort;
+  int req;
+  uint32_t odd[8];                 // node keys of this unit whose values are not all finite (bit: key - first)
+  uint8_t node[8][kNt];            // per softmax warp: the node at each key of a masked tile
+};
+
+template <int D>
+constexpr size_t tile_bytes() { return (size_t)kNt * D * 2; }
+
+template <int D>
+size_t smem_bytes(int q_tiles, int slots) {
+  return 1024 + (q_tiles + slots) * tile_bytes<D>() + sizeof(Smem) + 16;
+}
+
+template <int D>
+int ring_slots(int q_tiles) {
+  const int n = (int)((kSmemLimit - smem_bytes<D>(q_tiles, 0)) / tile_bytes<D>());
+  return std::min(n, kMaxSlots);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Paired fp32 arithmetic (each half rounds as the scalar operation does).
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// One unit: which rows and which keys of the shard.
+struct Unit {
+  int b, r, g, s_idx;
+  int row0, R, R_out;      // first row, rows that attend, rows to write
+  int kb, ke, ctx;         // keys [kb, ke), context keys of the shard
+  int T;                   // key tiles
+  bool turns;              // the streams take the tiles in turn
+  long long base;
+  // key tile of step s of stream w, and how many steps it has
+  __device__ __forceinline__ int tile(int w, int s) const { return turns ? 2 * s + w : s; }
+  __device__ __forceinline__ int steps(int w) const { return turns ? (T + 1 - w) / 2 : T; }
+  // place of a K or V tile in the ring's load order: the order in which the
+  // issuer consumes them (in turn: K0 K1 V0 K2 V1 K3 ...; else K0 V0 K1 V1 ...)
+  __device__ __forceinline__ int k_at(int t) const { return turns ? (t < 2 ? t : 2 * t - 1) : 2 * t; }
+  __device__ __forceinline__ int v_at(int t) const { return turns ? 2 * t + 2 : 2 * t + 1; }
+};
+
+// The 128 visibility bits of one row in the tile of keys [j0, j0 + 128):
+// context keys, and nodes whose bit the row's mask has.  nodes: the tile's
+// node numbers (valid at node keys); row null: a row without nodes.
+__device__ __forceinline__ void visibility(const Unit& u, int j0, const uint8_t* nodes, const uint32_t* row,
+                                           uint32_t (&vis)[4]) {
+  const int c = min(max(u.ctx - j0, 0), kNt), e = min(max(u.ke - j0, 0), kNt);   // context below c, nodes in [c, e)
+  int at = -1;
+  uint32_t word = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int cw = min(max(min(c, e) - 32 * w, 0), 32);
+    vis[w] = cw == 32 ? 0xffffffffu : (1u << cw) - 1u;
+    if (row != nullptr) {
+#pragma unroll 1
+      for (int k = max(c, 32 * w); k < min(e, 32 * w + 32); ++k) {
+        const int node = nodes[k];
+        if ((node >> 5) != at) {
+          at = node >> 5;
+          word = __ldg(row + at);
+        }
+        vis[w] |= ((word >> (node & 31)) & 1u) << (k & 31);
+      }
+    }
+  }
+}
+
+// Keep non-finite values out of the product: key `k` of the tile at `v`
+// (chunks of 64 dims, 128-byte rows).  Past the range the whole row becomes 0;
+// a node's row loses the entries that are not finite and is marked.
+template <int D>
+__device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t* v, int j0, int k) {
+  const int jj = j0 + k;
+  const bool past = jj >= u.ke;
+  if (!past && jj < u.ctx) return;
+  bool odd = false;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    // every 16-byte piece of the row, whatever its place under the swizzle
+    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * (kNt * 128) + k * 128 + (c & 7) * 16);
+    if (past) {
+      *p = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    uint4 x = *p;
+    uint32_t* w = &x.x;
+    bool touched = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, touched = true;
+      if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu, touched = true;
+    }
+    if (touched) *p = x, odd = true;
+  }
+  if (odd) {
+    const int bit = jj - max(u.kb, u.ctx);
+    atomicOr(&sm.odd[bit >> 5], 1u << (bit & 31));
+  }
+}
+
+// Softmax of one stream (128 threads, thread = row), and its share of the output.
+template <int D>
+__device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u, uint8_t* ring, float* share,
+                                       uint32_t tmem, int warp, int lane) {
+  const int w = (warp - 4) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
+  const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+  const uint32_t tS = lanes + 128u * w, tO = lanes + kColO + 128u * w;
+  const int gsize = p.Hq / p.Hkv;
+  const int row = u.turns ? lrow : 128 * w + lrow;         // row of the block
+  const float sl2 = p.scale_log2;
+  volatile int* abort_flag = &sm.abort;
+  const int steps = u.steps(w);
+  const uint32_t* mask_row = nullptr;
+  if (row < u.R)
+    mask_row = p.mask + u.b * p.mask_stride + (long long)((u.row0 + row) / gsize) * p.words;
+
+  float m = -INFINITY, l = 0.f;
+  bool bad = false;
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    const int t = u.tile(w, s), j0 = u.kb + t * kNt;
+    if (!__all_sync(0xffffffffu,
+                    *abort_flag == 0 && mbar_wait(smem_u32(&sm.s_full[w]), (uint32_t)s & 1u, p.wait_ns))) {
+      bad = true;
+      break;
+    }
+    uint32_t x[kNt];
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
+    tmem_wait_ld();
+    if (j0 + kNt > min(u.ctx, u.ke)) {
+      // nodes or the end of the range in this tile
+      uint8_t* nodes = sm.node[warp - 4];
+      __syncwarp();
+      for (int k = lane; k < kNt; k += 32) {
+        const int jj = j0 + k;
+        if (jj >= u.ctx && jj < u.ke) nodes[k] = (uint8_t)(global_pos(jj, u.r, p.I, p.N) - u.base);
+      }
+      __syncwarp();
+      uint32_t vis[4];
+      visibility(u, j0, nodes, mask_row, vis);
+#pragma unroll
+      for (int k = 0; k < kNt; ++k)
+        if (!((vis[k >> 5] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
+      // the values of the tile, before this stream's product reads them (with
+      // both streams on one tile the first one's product goes out first)
+      if (u.turns || w == 0) {
+        const int at = u.v_at(t);
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[at % p.slots]), (uint32_t)(at / p.slots) & 1u,
+                                               p.wait_ns))) {
+          bad = true;
+          break;
+        }
+        clean_value_row<D>(u, sm, ring + (at % p.slots) * tile_bytes<D>(), j0, lrow);
+        fence_proxy_async_smem();
+      }
+    }
+    auto f = [&](int k) { return __uint_as_float(x[k]); };
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int k = 0; k < kNt; k += 8)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], f(k + e), f(k + 4 + e));
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+    const bool moves = top > m + kLazyLog2;
+    if (__any_sync(0xffffffffu, moves)) {
+      const float to = moves ? top : m;
+      const float alpha = !moves ? 1.f : m == -INFINITY ? 0.f : ex2(m - to);
+      m = to;
+      l *= alpha;
+      if (s > 0) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st32(tO + c, o);
+        }
+      }
+    }
+    const float ref = m == -INFINITY ? 0.f : -m;
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int a = 32 * c + 2 * k;
+        const float2 y = ffma2(make_float2(f(a), f(a + 1)), make_float2(sl2, sl2), make_float2(ref, ref));
+        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        sum[k & 1] = fadd2(sum[k & 1], e);
+        hi[k] = pack_bf16x2(e.x, e.y);
+        lo[k] = pack_bf16x2(e.x - bf16_lo(hi[k]), e.y - bf16_hi(hi[k]));
+      }
+      tmem_st16(tS + 16 * c, hi);
+      tmem_st16(tS + 64 + 16 * c, lo);
+    }
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(smem_u32(&sm.p_full[w]));
+  }
+  bool have = !bad;
+  if (have && steps > 0)
+    have = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.o_full[w]), 0u, p.wait_ns));
+  if (!have) {
+    set_status(p.status, DCP_ERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  // one decision for the CTA: every product landed (the query's shared memory
+  // is idle from here on and carries the streams' m and l)
+  have = !bar_red_or(kBarEpi, 256, !have);
+  tc_fence_after();
+  share[(2 * w) * kNt + lrow] = m;
+  share[(2 * w + 1) * kNt + lrow] = l;
+  named_bar_sync(kBarEpi, 256);
+
+  // in turn: both streams hold the row, each writes half of its dims
+  float w0 = 1.f, w1 = 0.f;             // weights of this stream's and the other's O
+  const bool other = u.turns && u.steps(w ^ 1) > 0;
+  if (u.turns) {
+    const float m2 = share[(2 * (w ^ 1)) * kNt + lrow], l2 = share[(2 * (w ^ 1) + 1) * kNt + lrow];
+    const float top = fmaxf(m, m2);
+    const float ref = top == -INFINITY ? 0.f : top;
+    w0 = ex2(m - ref);
+    w1 = ex2(m2 - ref);
+    l = l * w0 + l2 * w1;
+    m = top;
+  }
+  const bool live = have && row < u.R && !(l == 0.f);
+  const float inv = live ? 1.f / l : 0.f;
+  w0 *= inv;
+  w1 *= inv;
+  const int d0 = u.turns ? w * (D / 2) : 0, d1 = u.turns ? d0 + D / 2 : D;
+  const uint32_t tOther = lanes + kColO + 128u * (w ^ 1);
+  auto dst_row = [&](int rr) {
+    const int i = rr / gsize, head = u.g * gsize + rr % gsize;
+    return ((((long long)u.r * p.B + u.b) * p.Lq + i) * p.n_split + u.s_idx) * p.Hq + head;
+  };
+  bool any_odd = false;
+  for (int k = 0; k < 8; ++k) any_odd |= sm.odd[k] != 0;
+  // 32 dims at a time through 4 KB of the idle ring, so that a row's part goes
+  // out as one 128-byte line
+  uint8_t* mine = ring + (warp - 4) * 4096;
+  // an aborted unit writes its zeros from registers: copies may still land in the ring
+  const bool staged = have;
+  const int out_row0 = u.turns ? quad * 32 : 128 * w + quad * 32;   // first row of this warp in the block
+#pragma unroll 1
+  for (int c = d0; c < d1; c += 32) {
+    uint32_t o[32];
+    if (have && steps > 0) {
+      tmem_ld32(tO + c, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] = live && steps > 0 ? __float_as_uint(__uint_as_float(o[k]) * w0) : 0u;
+    if (other && have) {
+      uint32_t o2[32];
+      tmem_ld32(tOther + c, o2);
+      tmem_wait_ld();
+      if (live) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), w1, __uint_as_float(o[k])));
+      }
+    }
+    if (any_odd && live) {
+      // values of nodes that are not finite: added to the rows that see them
+      for (int bit = 0; bit < DCP_TREE_MAX_NODES; ++bit) {
+        if (!((sm.odd[bit >> 5] >> (bit & 31)) & 1u)) continue;
+        const int jj = max(u.kb, u.ctx) + bit;
+        if (!tree_bit(mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - u.base))) continue;
+        const int blk = p.block_tables[((long long)u.r * p.B + u.b) * p.max_lb + jj / p.bs];
+        const __nv_bfloat16* v = p.v_pool + (((long long)blk * p.bs + jj % p.bs) * p.Hkv + u.g) * D + c;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float e = __bfloat162float(v[k]);
+          if (!(fabsf(e) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + e);
+        }
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<uint4*>(mine + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+          make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const int rr = it * 4 + (lane >> 3), k = lane & 7;
+      if (out_row0 + rr < u.R_out) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (staged) v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((k ^ (rr & 7)) << 4));
+        *reinterpret_cast<uint4*>(p.dst_o + dst_row(u.row0 + out_row0 + rr) * D + c + 4 * k) = v;
+      }
+    }
+  }
+  // in turn, a block of 256 rows: the rows of absent nodes behind the first 128
+  for (int rr = kNt + (warp - 4); u.turns && rr < u.R_out; rr += 8) {
+    const long long to = dst_row(u.row0 + rr);
+    for (int c = 4 * lane; c < D; c += 128)
+      *reinterpret_cast<uint4*>(p.dst_o + to * D + c) = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) p.dst_lse[to] = -INFINITY;
+  }
+  if (row < u.R_out && (!u.turns || w == 0))
+    p.dst_lse[dst_row(u.row0 + row)] = live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr uint32_t kTile = (uint32_t)tile_bytes<D>();
+  uint8_t* ring = qs + (p.block_rows / kNt) * kTile;
+  Smem& sm = *reinterpret_cast<Smem*>(ring + p.slots * kTile);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // units, longest request first (as in the decode kernel)
+  const long long per_req = (long long)p.N * p.Hkv * p.row_blocks * p.n_split;
+  const int k_req = (int)(blockIdx.x / per_req);
+  const long long rest = blockIdx.x % per_req;
+  Unit u;
+  u.b = k_req;
+  if (p.B <= kLptMaxBatch) {
+    for (int j = tid; j < p.B; j += kThreads) {
+      const int sj = p.seq_lens[j];
+      int rank = 0;
+      for (int i = 0; i < p.B; ++i) {
+        const int si = p.seq_lens[i];
+        rank += (si > sj) || (si == sj && i < j);
+      }
+      if (rank == k_req) sm.req = j;
+    }
+    __syncthreads();
+    u.b = sm.req;
+  }
+  u.s_idx = (int)(rest % p.n_split);
+  const int mb = (int)((rest / p.n_split) % p.row_blocks);
+  u.g = (int)((rest / ((long long)p.n_split * p.row_blocks)) % p.Hkv);
+  u.r = (int)(rest / ((long long)p.n_split * p.row_blocks * p.Hkv));
+  const int gsize = p.Hq / p.Hkv;
+  const TreeReq tr = tree_request(p.seq_lens, p.q_lens, p.Lq, u.b);
+  const int S = p.seq_lens[u.b];
+  u.base = tr.base;
+  u.row0 = mb * p.block_rows;
+  u.R_out = min(p.block_rows, p.Lq * gsize - u.row0);
+  u.R = min(max(tr.n * gsize - u.row0, 0), u.R_out);
+  u.turns = u.R <= kNt;
+  int L = tr.bad ? 0 : local_len(S, u.r, p.I, p.N);
+  const bool short_table = (long long)L > (long long)p.max_lb * p.bs;
+  if (short_table) L = p.max_lb * p.bs;
+  u.ctx = local_count_upto(tr.base - 1, u.r, p.I, p.N);
+  u.kb = min(L, u.s_idx * p.split_tokens);
+  u.ke = min(L, u.kb + p.split_tokens);
+  u.T = u.R > 0 ? (u.ke - u.kb + kNt - 1) / kNt : 0;
+  const int32_t* bt = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
+  {
+    // a block id past the pool among the shard's keys skips the unit
+    bool bad_blk = false;
+    for (int jb = tid; jb < (L + p.bs - 1) / p.bs; jb += kThreads) bad_blk |= (unsigned)bt[jb] >= (unsigned)p.num_blocks;
+    bad_blk = __syncthreads_or(bad_blk);
+    if (bad_blk) u.T = 0;
+    if (tid == 0 && (tr.bad || short_table || bad_blk)) set_status(p.status, DCP_ERR_BOUNDS);
+  }
+
+  if (tid == 0) {
+    for (int k = 0; k < p.slots; ++k) {
+      mbar_init(smem_u32(&sm.full[k]), 1);
+      mbar_init(smem_u32(&sm.empty[k]), 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&sm.s_full[k]), 1);
+      mbar_init(smem_u32(&sm.p_full[k]), kNt);
+      mbar_init(smem_u32(&sm.o_full[k]), 1);
+    }
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid < 8) sm.odd[tid] = 0;
+  if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), 512);
+  if (warp >= 4 && u.T > 0) {
+    // query rows -> shared memory, K-major with the 128-byte swizzle (rows past R are zero)
+    const int rows = u.turns ? kNt : 2 * kNt;
+    constexpr int kPer = D / 8;                            // 16-byte pieces of a row
+    for (int idx = tid - 128; idx < rows * kPer; idx += 256) {
+      const int rr = idx / kPer, c = idx % kPer;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (rr < u.R) {
+        const int i = (u.row0 + rr) / gsize, head = u.g * gsize + (u.row0 + rr) % gsize;
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + (((long long)u.b * p.Lq + i) * p.Hq + head) * D) + c);
+      }
+      const int lr = rr & 127;
+      *reinterpret_cast<uint4*>(qs + (rr >> 7) * kTile + (c >> 3) * (kNt * 128) + lr * 128 +
+                                (((c & 7) ^ (lr & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort;
+  auto fail = [&](void) {
+    set_status(p.status, DCP_ERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kCtrlRegs));
+    if (warp == 0 && lane == 0 && u.T > 0) {
+      // ---------------- TMA producer ----------------
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      const int box_rows = p.bs < kNt ? p.bs : kNt;
+      int last = -1;                                       // last place loaded
+      auto load = [&](const CUtensorMap* tm, int t, int at) -> bool {
+        const int slot = at % p.slots;
+        if (*abort_flag || (at >= p.slots && !mbar_wait(smem_u32(&sm.empty[slot]), (uint32_t)(at / p.slots - 1) & 1u,
+                                                        p.wait_ns)))
+          return false;
+        const uint32_t full = smem_u32(&sm.full[slot]);
+        uint8_t* dst = ring + slot * kTile;
+        mbar_arrive_expect_tx(full, kTile);
+        for (int k = 0; k < kNt; k += box_rows) {
+          const int j = u.kb + t * kNt + k;
+          // boxes past the key range read pool row 0 (masked, values zeroed)
+          const int row = j < u.ke ? bt[j / p.bs] * p.bs + j % p.bs : 0;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(smem_u32(dst + c * (kNt * 128) + k * 128), tm, 64 * c, u.g, row, full);
+        }
+        last = at;
+        return true;
+      };
+      bool ok = true;
+      if (u.turns) {
+        for (int t = 0; t < min(u.T, 2) && ok; ++t) ok = t == p.skip_tile || load(&tm_k, t, u.k_at(t));
+        for (int t = 0; t < u.T && ok; ++t) {
+          ok = load(&tm_v, t, u.v_at(t));
+          if (ok && t + 2 < u.T) ok = load(&tm_k, t + 2, u.k_at(t + 2));
+        }
+      } else {
+        for (int t = 0; t < u.T && ok; ++t) {
+          ok = (t == p.skip_tile || load(&tm_k, t, u.k_at(t))) && load(&tm_v, t, u.v_at(t));
+        }
+      }
+      if (!ok) fail();
+      if (*abort_flag) {
+        // let every copy this thread issued land before the CTA exits
+        for (int at = max(0, last - p.slots + 1); at <= last; ++at)
+          mbar_wait(smem_u32(&sm.full[at % p.slots]), (uint32_t)(at / p.slots) & 1u, p.wait_ns);
+      }
+    } else if (warp == 1 && lane == 0 && u.T > 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t id_qk = idesc_bf16(128, kNt, false);
+      constexpr uint32_t id_pv = idesc_bf16(128, D, true);
+      auto landed = [&](int at) {
+        return !*abort_flag && mbar_wait(smem_u32(&sm.full[at % p.slots]), (uint32_t)(at / p.slots) & 1u, p.wait_ns);
+      };
+      // S of stream w over key tile t, announced on s_full; frees the tile after its last reader
+      auto qk = [&](int w, int t) -> bool {
+        const int at = u.k_at(t), slot = at % p.slots;
+        if (!landed(at)) return false;
+        tc_fence_after();
+        const uint8_t* kt = ring + slot * kTile;
+        const uint8_t* qt = qs + (u.turns ? 0 : w) * kTile;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + 128u * w, smem_desc(smem_u32(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32), 16, 1024, kSw128),
+                 smem_desc(smem_u32(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32), 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
+        mma_commit(smem_u32(&sm.s_full[w]));
+        if (u.turns || w == 1) mma_commit(smem_u32(&sm.empty[slot]));
+        return true;
+      };
+      auto pv = [&](int w, int s, int t) -> bool {
+        const int at = u.v_at(t), slot = at % p.slots;
+        if (!landed(at) || !mbar_wait(smem_u32(&sm.p_full[w]), (uint32_t)s & 1u, p.wait_ns)) return false;
+        tc_fence_after();
+        const uint8_t* vt = ring + slot * kTile;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < kNt / 16; ++k)
+            mma_ts(tmem + kColO + 128u * w, tmem + 128u * w + 64 * part + 8 * k,
+                   smem_desc(smem_u32(vt + k * 2048), kNt * 128, 1024, kSw128), id_pv,
+                   (s > 0 || part > 0 || k > 0) ? 1u : 0u);
+        if (s + 1 == u.steps(w)) mma_commit(smem_u32(&sm.o_full[w]));
+        if (u.turns || w == 1) mma_commit(smem_u32(&sm.empty[slot]));
+        return true;
+      };
+      bool ok = true;
+      for (int w = 0; w < 2 && ok; ++w)
+        if (u.steps(w) > 0) ok = qk(w, u.tile(w, 0));
+      for (int s = 0; s < u.steps(0) && ok; ++s)
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (s < u.steps(w)) ok = pv(w, s, u.tile(w, s));
+          if (ok && s + 1 < u.steps(w)) ok = qk(w, u.tile(w, s + 1));
+        }
+      if (!ok) fail();
+      mma_commit(smem_u32(&sm.drain));
+      if (!mbar_wait(smem_u32(&sm.drain), 0, p.wait_ns)) fail();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
+    stream<D>(p, sm, u, ring, reinterpret_cast<float*>(qs), tmem, warp, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int rows_of(const AttnArgs& a) { return a.Lq * (a.Hq / a.Hkv); }
+int block_rows_of(const AttnArgs& a) { return rows_of(a) > kNt ? 2 * kNt : kNt; }
+int row_blocks_of(const AttnArgs& a) { return (rows_of(a) + block_rows_of(a) - 1) / block_rows_of(a); }
+
+template <int D>
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, Params& p, long long units, cudaStream_t stream) {
+  const int q_tiles = p.block_rows / kNt;
+  p.slots = ring_slots<D>(q_tiles);
+  const size_t smem = smem_bytes<D>(q_tiles, p.slots);
+  // the register split assumes the compiled launch count; refuse to launch
+  // otherwise (setmaxnreg.inc would wait for registers that do not exist)
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, tree_gqa_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * kThreads < 128 * kCtrlRegs + 256 * kSoftRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(tree_gqa_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  tree_gqa_kernel<D><<<(unsigned)units, kThreads, smem, stream>>>(tm_k, tm_v, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Head dim 64 or 128; block sizes as the decode kernel takes them.
+bool tree_gqa_supported(const AttnArgs& a) {
+  if (a.kind != DCP_ATTN_GQA || (a.Dqk != 64 && a.Dqk != 128) || a.Dv != a.Dqk) return false;
+  if (a.bs % 8 || (a.bs >= kNt ? a.bs % kNt : kNt % a.bs)) return false;
+  if ((long long)a.Lq * (a.Hq / a.Hkv) > (1LL << 20)) return false;
+  return (long long)a.num_blocks * a.bs < (1LL << 31);
+}
+
+SplitPlan plan_tree_gqa(const AttnArgs& a, int sm_count) {
+  return plan_splits(a, sm_count, kNt, a.Hkv * row_blocks_of(a));
+}
+
+cudaError_t launch_tree_gqa(const AttnArgs& a, const SplitPlan& plan) {
+  CUtensorMap tm_k, tm_v;
+  const uint64_t rows = (uint64_t)a.num_blocks * a.bs;
+  const uint64_t dims[3] = {(uint64_t)a.Dqk, (uint64_t)a.Hkv, rows};
+  const uint64_t strides[2] = {(uint64_t)a.Dqk * 2, (uint64_t)a.Hkv * a.Dqk * 2};
+  const uint32_t box[3] = {64, 1, (uint32_t)(a.bs < kNt ? a.bs : kNt)};
+  const char* k_pool = static_cast<const char*>(a.kv);
+  const char* v_pool = k_pool + rows * a.Hkv * a.Dqk * 2;
+  if (!make_tensor_map_bf16(&tm_k, k_pool, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tensor_map_bf16(&tm_v, v_pool, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  Params p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.v_pool = reinterpret_cast<const __nv_bfloat16*>(v_pool);
+  p.block_tables = a.block_tables;
+  p.seq_lens = a.seq_lens;
+  p.q_lens = a.q_lens;
+  p.mask = a.tree_mask;
+  p.mask_stride = a.tree_mask_stride;
+  p.words = a.tree_words;
+  p.status = a.status;
+  p.B = a.B, p.Lq = a.Lq, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.I = a.I;
+  p.max_lb = a.max_lb, p.bs = a.bs, p.num_blocks = a.num_blocks;
+  p.n_split = plan.n_split, p.split_tokens = plan.split_tokens;
+  p.row_blocks = row_blocks_of(a), p.block_rows = block_rows_of(a);
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.wait_ns = test_hooks().wait_ns;
+  p.skip_tile = test_hooks().skip_tile;
+  p.dst_o = a.partial_out;
+  p.dst_lse = a.lse;
+  if (plan.n_split > 1) {
+    const size_t o_bytes = (size_t)a.N * a.B * a.Lq * a.Hq * plan.n_split * a.Dv * sizeof(float);
+    p.dst_o = static_cast<float*>(a.workspace);
+    p.dst_lse = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + ((o_bytes + 255) & ~size_t(255)));
+  }
+  const long long units = (long long)a.N * a.B * a.Hkv * p.row_blocks * plan.n_split;
+  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  const cudaError_t e = a.Dqk == 128 ? launch<128>(tm_k, tm_v, p, units, a.stream)
+                                     : launch<64>(tm_k, tm_v, p, units, a.stream);
+  if (e != cudaSuccess || plan.n_split <= 1) return e;
+  return launch_split_combine(a, plan);
+}
+
+}  // namespace dcp

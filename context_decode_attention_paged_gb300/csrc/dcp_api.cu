@@ -102,10 +102,10 @@ dcp_status_t make_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t inter
 }
 
 // The kernel that will run for these arguments, and its split plan.
-enum class Impl { kSimt, kMlaTc, kGqaTc };
+enum class Impl { kSimt, kMlaTc, kGqaTc, kTreeGqa };
 
 Impl select_impl(const AttnArgs& a) {
-  if (a.tree_words > 0) return Impl::kSimt;
+  if (a.tree_words > 0) return tree_gqa_supported(a) ? Impl::kTreeGqa : Impl::kSimt;
   if (mla_tc_supported(a)) return Impl::kMlaTc;
   if (gqa_tc_supported(a)) return Impl::kGqaTc;
   return Impl::kSimt;
@@ -117,6 +117,8 @@ SplitPlan plan_for(const AttnArgs& a, Impl impl, int sm_count) {
       return plan_attn_mla_tc(a, sm_count);
     case Impl::kGqaTc:
       return plan_attn_gqa_tc(a, sm_count);
+    case Impl::kTreeGqa:
+      return plan_tree_gqa(a, sm_count);
     case Impl::kSimt:
     default:
       return plan_attn_simt(a, sm_count);
@@ -130,6 +132,8 @@ dcp_status_t launch_impl(const AttnArgs& a, Impl impl, const SplitPlan& plan) {
       return from_cuda(launch_attn_mla_tc(a, plan));
     case Impl::kGqaTc:
       return from_cuda(launch_attn_gqa_tc(a, plan));
+    case Impl::kTreeGqa:
+      return from_cuda(launch_tree_gqa(a, plan));
     case Impl::kSimt:
     default:
       return from_cuda(launch_attn_simt(a, plan));
@@ -137,7 +141,13 @@ dcp_status_t launch_impl(const AttnArgs& a, Impl impl, const SplitPlan& plan) {
 }
 
 int32_t kind_of(Impl impl) {
-  return impl == Impl::kMlaTc ? DCP_KERNEL_MLA_TC : impl == Impl::kGqaTc ? DCP_KERNEL_GQA_TC : DCP_KERNEL_SIMT;
+  switch (impl) {
+    case Impl::kMlaTc: return DCP_KERNEL_MLA_TC;
+    case Impl::kGqaTc:
+    case Impl::kTreeGqa: return DCP_KERNEL_GQA_TC;
+    case Impl::kSimt:
+    default: return DCP_KERNEL_SIMT;
+  }
 }
 
 // Arguments of a drafted-tree call: those of dcp_decode_attn and the node limit.

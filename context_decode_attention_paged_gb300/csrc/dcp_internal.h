@@ -75,6 +75,11 @@ cudaError_t launch_kv_write(const void* new_k, const void* new_v, void* kv_cache
                             const int32_t* seq_lens, int B, int n_new, int N, int I, int bs, int max_lb,
                             int num_blocks, int row_bytes, int* status, cudaStream_t stream);
 
+// Drafted-tree GQA on tcgen05 (head dim 64/128, block sizes of the decode kernel).
+bool tree_gqa_supported(const AttnArgs& a);
+SplitPlan plan_tree_gqa(const AttnArgs& a, int sm_count);
+cudaError_t launch_tree_gqa(const AttnArgs& a, const SplitPlan& p);
+
 // Rotary append: see dcp_kv_cache_append (strides in elements).
 struct AppendArgs {
   const void *k, *v, *q;

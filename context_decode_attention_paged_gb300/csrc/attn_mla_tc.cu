@@ -57,6 +57,15 @@
 //               scores out of TMEM and push them to the peer
 // Every wait is bounded; on expiry the kernel records DCP_ERR_TIMEOUT, drains
 // its own copies and MMAs, frees TMEM and returns.
+//
+// kTree: the drafted-tree form.  A unit is one node, so its mask is the same
+// for every head: a 32-bit word per half tile says which tokens the node sees
+// (all of them in tiles of context keys alone).  Hidden tokens are dropped
+// from the softmax as the tokens past a ragged end are, their value rows are
+// zeroed, and their scores do not reach the exchange's scale; a score that is
+// not finite is sent as a NaN scale, so that the row becomes NaN as the
+// formula has it.  Tiles that the node sees nothing of are possible, so the
+// running reference may stay -inf past the first tile.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -64,6 +73,7 @@
 #include "dcp_internal.h"
 #include "dcp_sm100.cuh"
 #include "dcp_tma.h"
+#include "dcp_tree.cuh"
 
 namespace dcp {
 namespace {
@@ -128,6 +138,16 @@ struct MlaParams {
   float scale_log2;    // scale * log2(e)
   unsigned long long wait_ns;   // limit of every bounded wait
   int skip_tile;                // test hook: CTA 0 never loads this tile (-1: off)
+};
+
+template <bool kTree>
+struct KernelParams : MlaParams {};
+template <>
+struct KernelParams<true> : MlaParams {
+  const uint32_t* mask;
+  long long mask_stride;
+  const int32_t* q_lens;
+  int words;
 };
 
 struct Smem {
@@ -233,16 +253,39 @@ struct Unit {
   int r, b, i_q, s_idx, kb, ke, T;
 };
 
+// kTree: what a unit's node sees
+template <bool kTree>
+struct View {};
+template <>
+struct View<true> {
+  int ctx;                        // context keys of the shard
+  long long base;                 // the first node's position
+  const uint32_t* mask_row;       // the mask words of this unit's node
+};
+
 // valid tokens of tile t in half `half` (tokens [32 half, +32)) of the tile
 __device__ __forceinline__ int valid_of_half(const Unit& u, int t, int half) {
   const int tv = min(kNt, u.ke - (u.kb + t * kNt));
   return min(kHalf, max(0, tv - kHalf * half));
 }
 
+// kTree: bit k set where the node sees token 32 half + k of tile t (whole warp)
+__device__ __forceinline__ uint32_t seen_of_half(const MlaParams& p, const Unit& u, const View<true>& view, int t,
+                                                 int half, int lane) {
+  const int j0 = u.kb + t * kNt + kHalf * half;
+  if (j0 + kHalf <= min(view.ctx, u.ke)) return 0xffffffffu;
+  const int jj = j0 + lane;
+  bool sees = jj < u.ke;
+  if (sees && jj >= view.ctx) sees = tree_bit(view.mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - view.base));
+  return __ballot_sync(0xffffffffu, sees);
+}
+
 // ---------------------------------------------------------------------------
 // softmax warpgroup w (tiles w, w + 2, ...)
 // ---------------------------------------------------------------------------
+template <bool kTree>
 __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap& tm_out, Smem& sm, const Unit& u,
+                                           const View<kTree>& view,
                                            uint8_t* stages,
                                            const uint8_t* scbuf, const uint8_t* pmbuf, const float* mxbuf,
                                            uint32_t tmem, uint32_t cta, int warp, int lane) {
@@ -341,7 +384,14 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
       }
     }
     // local maximum of the valid tokens (log2 units)
-    const int valid = valid_of_half(u, t, (int)cta);
+    int valid = 0;
+    uint32_t seen = 0;
+    if constexpr (kTree) {
+      seen = seen_of_half(p, u, view, t, (int)cta, lane);
+      valid = seen == 0xffffffffu ? kHalf : 0;
+    } else {
+      valid = valid_of_half(u, t, (int)cta);
+    }
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if (valid == kHalf) {
 #pragma unroll
@@ -350,7 +400,7 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
         for (int j = 0; j < 4; ++j) m4[j] = fmax3(m4[j], x[k + j], x[k + 4 + j]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], (k < valid) ? x[k] : -INFINITY);
+      for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], (kTree ? ((seen >> k) & 1u) != 0 : k < valid) ? x[k] : -INFINITY);
     }
     const float ml = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
     // every received score has been used (the maximum depends on all of
@@ -380,7 +430,7 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     } else {
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        e[k] = (k < valid) ? ex2(fmaf(x[k], sl2, nml)) : 0.f;
+        e[k] = (kTree ? ((seen >> k) & 1u) != 0 : k < valid) ? ex2(fmaf(x[k], sl2, nml)) : 0.f;
         l4[k & 3] += e[k];
       }
     }
@@ -427,7 +477,10 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
       pp[4 * k] = v.x; pp[4 * k + 1] = v.y; pp[4 * k + 2] = v.z; pp[4 * k + 3] = v.w;
     }
     const float l_peer = reinterpret_cast<const float*>(pmbuf + kMsgCodes)[h];
-    lw = lw * ex2(rw - R) + (lsum + l_peer);
+    if constexpr (kTree)
+      lw = lw * (rw == R ? 1.f : ex2(rw - R)) + (lsum + l_peer);
+    else
+      lw = lw * ex2(rw - R) + (lsum + l_peer);
     rw = R;
     // the P buffer and O: PV(t-1) must be done (it implies every earlier PV,
     // and the wait for PV(t-3) before tile t-2's P keeps the parity unambiguous)
@@ -449,7 +502,19 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     // holds; zero them so that 0 * (NaN/Inf) cannot reach O (whole 128-byte
     // rows, so the swizzle does not matter)
     const int tv = min(kNt, u.ke - (u.kb + t * kNt));
-    if (tv < kNt) {
+    if constexpr (kTree) {
+      const uint32_t s0 = cta == 0 ? seen : seen_of_half(p, u, view, t, 0, lane);
+      const uint32_t s1 = cta == 1 ? seen : seen_of_half(p, u, view, t, 1, lane);
+      if ((s0 & s1) != 0xffffffffu) {
+        // hidden tokens: 8 threads a row, all four chunks
+        uint4* st = reinterpret_cast<uint4*>(stages + (t % kStages) * kStageBytes);
+        for (int row = mt >> 3; row < kNt; row += 16)
+          if (!(((row < kHalf ? s0 : s1) >> (row & 31)) & 1u))
+#pragma unroll
+            for (int c = 0; c < 4; ++c) st[(c * kChunkBytes) / 16 + row * 8 + (mt & 7)] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      }
+    } else if (tv < kNt) {
       uint4* st = reinterpret_cast<uint4*>(stages + (t % kStages) * kStageBytes);
       const int n16 = (kNt - tv) * 8;
       for (int idx = mt; idx < 4 * n16; idx += 128) {
@@ -491,9 +556,15 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
   float l_tot = 0.f, r_fin = -INFINITY;
   if (have) {
     r_fin = sm.rlast[(T - 1) & 1][h];
-    l_tot = sm.lw[0][h] * ex2(sm.rlast[0][h] - r_fin) + sm.lw[1][h] * ex2(sm.rlast[1][h] - r_fin);
+    if constexpr (kTree) {
+      const float l0 = sm.lw[0][h], l1 = sm.lw[1][h];
+      l_tot = (l0 == 0.f ? 0.f : l0 * ex2(sm.rlast[0][h] - r_fin)) + (l1 == 0.f ? 0.f : l1 * ex2(sm.rlast[1][h] - r_fin));
+    } else {
+      l_tot = sm.lw[0][h] * ex2(sm.rlast[0][h] - r_fin) + sm.lw[1][h] * ex2(sm.rlast[1][h] - r_fin);
+    }
   }
-  const float inv = l_tot > 0.f ? 1.f / l_tot : 0.f;
+  // (kTree: a NaN sum makes a NaN row)
+  const float inv = (kTree ? !(l_tot == 0.f) : l_tot > 0.f) ? 1.f / l_tot : 0.f;
   const long long row0 = ((((long long)u.r * p.B + u.b) * p.Lq + u.i_q) * p.n_split + u.s_idx) * p.Hq;
   if (have) {
     // this CTA's 256 output dims of head h, scaled by 1 / l, into shared
@@ -537,13 +608,14 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     }
   }
   if (cta == 0 && w == 0 && h < p.Hq)
-    p.dst_lse[row0 + h] = (have && l_tot > 0.f) ? (r_fin + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
+    p.dst_lse[row0 + h] = (have && (kTree ? !(l_tot == 0.f) : l_tot > 0.f)) ? (r_fin + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
 // score senders (warps 12..15): the peer's 32 tokens of every tile
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const Unit& u, const uint8_t* scbuf,
+template <bool kTree>
+__device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const Unit& u, const View<kTree>& view, const uint8_t* scbuf,
                                              uint32_t tmem, uint32_t cta, int warp, int lane) {
   const uint32_t peer = cta ^ 1u;
   const int lg = warp & 3;                          // this warp's heads [32 lg, +32)
@@ -571,25 +643,50 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
     mbar_arrive(smem_u32(&sm.s_free[xb]));
     // columns past the end of a ragged tile hold scores of stale cache rows:
     // zero them so they cannot set the scale (the peer masks them anyway)
-    const int vp = valid_of_half(u, t, (int)peer);
-    if (vp < kHalf) {
+    if constexpr (kTree) {
+      const uint32_t seen = seen_of_half(p, u, view, t, (int)peer, lane);
+      if (seen != 0xffffffffu) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (k >= vp) v[k] = 0u;
+        for (int k = 0; k < 32; ++k)
+          if (!((seen >> k) & 1u)) v[k] = 0u;
+      }
+    } else {
+      const int vp = valid_of_half(u, t, (int)peer);
+      if (vp < kHalf) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (k >= vp) v[k] = 0u;
+      }
     }
-    float a8[8];
+    float amax;
+    bool odd = false;            // some score of this head is not finite
+    if constexpr (kTree) {
+      // the largest magnitude as bits: infinities and NaN lie above every finite value
+      uint32_t b8[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) a8[k] = fmaxf(fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 8])));
+      for (int k = 0; k < 8; ++k) b8[k] = max(v[k] & 0x7fffffffu, v[k + 8] & 0x7fffffffu);
 #pragma unroll
-    for (int k = 16; k < 32; k += 8)
+      for (int k = 16; k < 32; k += 8)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a8[j] = fmaxf(a8[j], fabsf(__uint_as_float(v[k + j])));
-    const float amax =
-        fmaxf(fmaxf(fmaxf(a8[0], a8[1]), fmaxf(a8[2], a8[3])), fmaxf(fmaxf(a8[4], a8[5]), fmaxf(a8[6], a8[7])));
+        for (int j = 0; j < 8; ++j) b8[j] = max(b8[j], v[k + j] & 0x7fffffffu);
+      const uint32_t top = max(max(max(b8[0], b8[1]), max(b8[2], b8[3])), max(max(b8[4], b8[5]), max(b8[6], b8[7])));
+      odd = top >= 0x7f800000u;
+      amax = odd ? 0.f : __uint_as_float(top);
+    } else {
+      float a8[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a8[k] = fmaxf(fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 8])));
+#pragma unroll
+      for (int k = 16; k < 32; k += 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a8[j] = fmaxf(a8[j], fabsf(__uint_as_float(v[k + j])));
+      amax = fmaxf(fmaxf(fmaxf(a8[0], a8[1]), fmaxf(a8[2], a8[3])), fmaxf(fmaxf(a8[4], a8[5]), fmaxf(a8[6], a8[7])));
+    }
     // large partials in this warp's heads: the residual follows (same for the warp)
     const bool flag = __any_sync(0xffffffffu, amax * sl2 > kResidualLog2);
     float enc, dec;
     bfp_scales(amax, enc, dec);
+    if (odd) dec = NAN;
     // the peer has read tile t-1 out of its one slot
     if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.sc_free[(t - 1) & 1][lg]), (uint32_t)((t - 1) >> 1) & 1u, p.wait_ns))) {
       bad = true;
@@ -637,12 +734,12 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
   }
 }
 
-template <bool kLpt, bool kSmallBlocks>
+template <bool kLpt, bool kSmallBlocks, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                 const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qrope,
                 const __grid_constant__ CUtensorMap tm_out,
-                const MlaParams p) {
+                const KernelParams<kTree> p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = base;                                        // kStages x 36 KB
@@ -726,11 +823,22 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
 
   // key range of this unit (shard-local indices [kb, ke))
   const int S = p.seq_lens[u.b];
-  const bool bad_len = S < p.Lq;
+  TreeReq tree{};
+  if constexpr (kTree) tree = tree_request(p.seq_lens, p.q_lens, p.Lq, u.b);
+  const bool bad_len = kTree ? tree.bad : S < p.Lq;
   int L = bad_len ? 0 : local_len(S, u.r, p.I, p.N);
   const bool short_table = (long long)L > (long long)p.max_lb * p.bs;
   if (short_table) L = p.max_lb * p.bs;
-  const int vis = bad_len ? 0 : min(L, local_count_upto((long long)S - p.Lq + u.i_q, u.r, p.I, p.N));
+  View<kTree> view;
+  int vis = 0;
+  if constexpr (kTree) {
+    vis = u.i_q < tree.n ? L : 0;          // rows behind the request's nodes see nothing
+    view.base = tree.base;
+    view.ctx = local_count_upto(tree.base - 1, u.r, p.I, p.N);
+    view.mask_row = p.mask + u.b * p.mask_stride + (long long)u.i_q * p.words;
+  } else {
+    vis = bad_len ? 0 : min(L, local_count_upto((long long)S - p.Lq + u.i_q, u.r, p.I, p.N));
+  }
   u.kb = min(vis, u.s_idx * p.split_tokens);
   u.ke = min(vis, u.kb + p.split_tokens);
   u.T = (u.ke - u.kb + kNt - 1) / kNt;
@@ -946,10 +1054,10 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
-    softmax_wg(p, tm_out, sm, u, stages, scbuf, pmbuf, mxbuf, tmem, cta, warp, lane);
+    softmax_wg<kTree>(p, tm_out, sm, u, view, stages, scbuf, pmbuf, mxbuf, tmem, cta, warp, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kSendRegs));
-    score_sender(p, sm, u, scbuf, tmem, cta, warp, lane);
+    score_sender<kTree>(p, sm, u, view, scbuf, tmem, cta, warp, lane);
   }
 
   // teardown: the peer no longer touches our shared memory, then free TMEM
@@ -1003,7 +1111,8 @@ SplitPlan plan_attn_mla_tc(const AttnArgs& a, int sm_count) {
   return pl;
 }
 
-cudaError_t launch_attn_mla_tc(const AttnArgs& a, const SplitPlan& plan) {
+template <bool kTree>
+static cudaError_t launch_mla(const AttnArgs& a, const SplitPlan& plan) {
   CUtensorMap tm_lat, tm_rope;
   const uint64_t dims[2] = {(uint64_t)kDqk, (uint64_t)a.num_blocks * a.bs};
   const uint64_t strides[1] = {(uint64_t)kDqk * 2};
@@ -1021,7 +1130,7 @@ cudaError_t launch_attn_mla_tc(const AttnArgs& a, const SplitPlan& plan) {
   if (!make_tensor_map_bf16(&tm_qlat, a.q, 2, qdims, strides, qbox_lat, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tensor_map_bf16(&tm_qrope, a.q, 2, qdims, strides, qbox_rope, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  MlaParams p;
+  KernelParams<kTree> p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.block_tables = a.block_tables;
   p.seq_lens = a.seq_lens;
@@ -1037,6 +1146,12 @@ cudaError_t launch_attn_mla_tc(const AttnArgs& a, const SplitPlan& plan) {
   p.n_split = plan.n_split;
   p.split_tokens = plan.split_tokens;
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  if constexpr (kTree) {
+    p.mask = a.tree_mask;
+    p.mask_stride = a.tree_mask_stride;
+    p.q_lens = a.q_lens;
+    p.words = a.tree_words;
+  }
   p.wait_ns = test_hooks().wait_ns;
   p.skip_tile = test_hooks().skip_tile;
   if (plan.n_split > 1) {
@@ -1071,9 +1186,9 @@ cudaError_t launch_attn_mla_tc(const AttnArgs& a, const SplitPlan& plan) {
     p.order = order;
   }
   void (*kern)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
-               const MlaParams) =
-      lpt ? (small ? mla_attn_kernel<true, true> : mla_attn_kernel<true, false>)
-          : (small ? mla_attn_kernel<false, true> : mla_attn_kernel<false, false>);
+               const KernelParams<kTree>) =
+      lpt ? (small ? mla_attn_kernel<true, true, kTree> : mla_attn_kernel<true, false, kTree>)
+          : (small ? mla_attn_kernel<false, true, kTree> : mla_attn_kernel<false, false, kTree>);
   // the register split assumes the compiled launch count; refuse to launch
   // otherwise (setmaxnreg.inc would wait for registers that do not exist)
   cudaFuncAttributes fa;
@@ -1087,6 +1202,10 @@ cudaError_t launch_attn_mla_tc(const AttnArgs& a, const SplitPlan& plan) {
   e = cudaGetLastError();
   if (e != cudaSuccess || plan.n_split <= 1) return e;
   return launch_split_combine(a, plan);
+}
+
+cudaError_t launch_attn_mla_tc(const AttnArgs& a, const SplitPlan& plan) {
+  return a.tree_mask != nullptr ? launch_mla<true>(a, plan) : launch_mla<false>(a, plan);
 }
 
 }  // namespace dcp

@@ -105,9 +105,9 @@ dcp_status_t make_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t inter
 enum class Impl { kSimt, kMlaTc, kGqaTc, kTreeGqa };
 
 Impl select_impl(const AttnArgs& a) {
-  if (a.tree_words > 0) return tree_gqa_supported(a) ? Impl::kTreeGqa : Impl::kSimt;
+  if (a.tree_words > 0 && tree_gqa_supported(a)) return Impl::kTreeGqa;
   if (mla_tc_supported(a)) return Impl::kMlaTc;
-  if (gqa_tc_supported(a)) return Impl::kGqaTc;
+  if (a.tree_words == 0 && gqa_tc_supported(a)) return Impl::kGqaTc;
   return Impl::kSimt;
 }
 

@@ -140,12 +140,9 @@ def test_hidden_nodes_may_hold_anything(name, L, kw, value):
     assert not np.isfinite(got["out"][:, :, [2, L - 1]]).any()
 
 
-@pytest.mark.parametrize("name,L,kw", SPECIAL)
+@pytest.mark.parametrize("name,L,kw", [c for c in SPECIAL if c[0] != "mla_32"])
 def test_a_seen_value_that_is_not_finite_reaches_its_dims_alone(name, L, kw):
-    """An infinite value entry of a seen node (MLA: of its latent part, which the scores read too,
-    so GQA only) makes that output entry infinite, and no other."""
-    if kw.get("num_kv_heads") == 1 or name.startswith("mla"):
-        pytest.skip("the value is part of the key")
+    """An infinite value entry of a seen node makes that output entry infinite, and no other."""
     inst, _, _ = T.tree_case(name, L, **kw)
     sees = np.tril(np.ones((1, L, L), dtype=bool))
     sees[:, 3:, 2] = False
@@ -161,6 +158,31 @@ def test_a_seen_value_that_is_not_finite_reaches_its_dims_alone(name, L, kw):
     want[hit] = 0
     got["out"][hit] = 0
     assert_close(got["out"], want, "every other entry")
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dim", [0, 5, -1])
+@pytest.mark.parametrize("name,L,kw", SPECIAL)
+def test_a_seen_key_that_is_not_finite_makes_its_rows_nan(name, L, kw, dim, value):
+    """One entry of node 2's key (MLA: of its rope part, which is no value): the rows that see it
+    are NaN (an infinite score against itself), the others are what they are without it."""
+    inst, _, _ = T.tree_case(name, L, **kw)
+    sees = np.tril(np.ones((1, L, L), dtype=bool))
+    sees[:, 3:, 2] = False
+    mask = T.pack(sees)
+    ref = T.oracle_tree(inst, mask)
+    blk, slot = T.cell(inst, 0, int(inst.seq_lens[0]) - L + 2)
+    if inst.w.kind == "gqa":
+        inst.q[:, 2, :, dim] = inst.q[:, 2, :, dim].abs() + 0.1          # +inf scores
+        inst.kv_cache[0, blk, slot, :, dim] = value
+    else:
+        d = 575 if dim == -1 else 512 + 32 * (dim > 0) + dim
+        inst.q[:, 2, :, d] = inst.q[:, 2, :, d].abs() + 0.1
+        inst.kv_cache[blk, slot, d] = value
+    rows = [i for i in range(L) if i != 2]
+    got = T.run_tree(inst, mask)
+    assert np.isnan(got["out"][:, :, 2]).all()
+    assert_close(got["out"][:, :, rows], ref["out"][:, :, rows], "rows that do not see it")
 
 
 def test_stress_inputs_hold_the_bar():

@@ -42,7 +42,7 @@
 // to the rows that see them.
 //
 // Warp roles (384 threads; setmaxnreg moves registers to the softmax warps):
-// warp 0 TMA producer (ring of K and V tiles), warp 1 MMA issuer and TMEM
+// warps 0 and 3 TMA producers (ring of K and V tiles), warp 1 MMA issuer and TMEM
 // owner, warps 4-7 and 8-11 the two streams.  Every wait is bounded; on expiry
 // the kernel records DCP_ERR_TIMEOUT, drains its copies and MMAs and returns.
 #include <cuda.h>
@@ -64,10 +64,11 @@ using namespace sm100;
 constexpr int kNt = 128;                      // keys per tile, rows per stream
 constexpr int kMaxSlots = 12;                 // K or V tiles in the ring
 constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168, kCtrlRegs = 40, kSoftRegs = 232;
+constexpr int kLaunchRegs = 168, kCtrlRegs = 72, kSoftRegs = 216;
 static_assert(128 * kCtrlRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr size_t kSmemLimit = 232448;         // dynamic shared memory per CTA
 constexpr float kLazyLog2 = 8.0f;             // m moves when scores pass it by more than this
+constexpr float kHeavyLog2 = 3.0f;            // a probability above 2^-3 of its row's sum so far takes its second term
 constexpr uint32_t kBarEpi = 1;               // named barrier of the two streams
 constexpr int kLptMaxBatch = 128;             // longest-first unit order up to this batch
 // TMEM columns (512 allocated): S and P of stream w at 128 w, O at 256 + 128 w
@@ -90,14 +91,39 @@ struct Params {
   int skip_tile;
 };
 
+// One unit: which rows and which keys of the shard.
+struct Unit {
+  int b, r, g, s_idx;
+  int row0, R, R_out;      // first row, rows that attend, rows to write
+  int kb, ke, ctx;         // keys [kb, ke), context keys of the shard
+  int T;                   // key tiles
+  bool turns;              // the streams take the tiles in turn
+  long long base;
+  // key tile of step s of stream w, and how many steps it has
+  __device__ __forceinline__ int tile(int w, int s) const { return turns ? 2 * s + w : s; }
+  __device__ __forceinline__ int steps(int w) const { return turns ? (T + 1 - w) / 2 : T; }
+  // Ring: a stream's step s uses items 2 s (K) and 2 s + 1 (V).  In turn each
+  // stream has half of the slots to itself, else both read every item, so that
+  // a stream that waits for an item has consumed the slot's last one (a barrier
+  // a whole lap ahead of its waiter would look complete).
+  __device__ __forceinline__ int len(int slots) const { return turns ? slots / 2 : slots; }
+  __device__ __forceinline__ int slot(int w, int at, int slots) const {
+    return turns ? w * (slots / 2) + at % (slots / 2) : at % slots;
+  }
+  __device__ __forceinline__ uint32_t lap(int at, int slots) const { return (uint32_t)(at / len(slots)); }
+};
+
 struct Smem {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2], p_full[2], o_full[2], drain;
   uint32_t tmem_base;
   int abort;
   int req;
+  Unit unit;                       // for the streams: read where it is needed, to save registers
   uint32_t odd[8];                 // node keys of this unit whose values are not all finite (bit: key - first)
-  uint8_t node[8][kNt];            // per softmax warp: the node at each key of a masked tile
+  int heavy[2];                    // per stream: the last step with a heavy probability
+  uint8_t node[2][kNt];            // per stream: the node at each key of a masked tile (four warps write the
+                                   // same bytes, each before it reads them)
 };
 
 template <int D>
@@ -145,26 +171,9 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   return d;
 }
 
-// One unit: which rows and which keys of the shard.
-struct Unit {
-  int b, r, g, s_idx;
-  int row0, R, R_out;      // first row, rows that attend, rows to write
-  int kb, ke, ctx;         // keys [kb, ke), context keys of the shard
-  int T;                   // key tiles
-  bool turns;              // the streams take the tiles in turn
-  long long base;
-  // key tile of step s of stream w, and how many steps it has
-  __device__ __forceinline__ int tile(int w, int s) const { return turns ? 2 * s + w : s; }
-  __device__ __forceinline__ int steps(int w) const { return turns ? (T + 1 - w) / 2 : T; }
-  // place of a K or V tile in the ring's load order: the order in which the
-  // issuer consumes them (in turn: K0 K1 V0 K2 V1 K3 ...; else K0 V0 K1 V1 ...)
-  __device__ __forceinline__ int k_at(int t) const { return turns ? (t < 2 ? t : 2 * t - 1) : 2 * t; }
-  __device__ __forceinline__ int v_at(int t) const { return turns ? 2 * t + 2 : 2 * t + 1; }
-};
-
-// The 128 visibility bits of one row in the tile of keys [j0, j0 + 128):
-// context keys, and nodes whose bit the row's mask has.  nodes: the tile's
-// node numbers (valid at node keys); row null: a row without nodes.
+// The 128 visibility bits of one row for the keys [j0, j0 + 128): context keys,
+// and nodes whose bit the row's mask has.  nodes: the node at each key (valid
+// at node keys); row null: a row without nodes.
 __device__ __forceinline__ void visibility(const Unit& u, int j0, const uint8_t* nodes, const uint32_t* row,
                                            uint32_t (&vis)[4]) {
   const int c = min(max(u.ctx - j0, 0), kNt), e = min(max(u.ke - j0, 0), kNt);   // context below c, nodes in [c, e)
@@ -188,9 +197,9 @@ __device__ __forceinline__ void visibility(const Unit& u, int j0, const uint8_t*
   }
 }
 
-// Keep non-finite values out of the product: key `k` of the tile at `v`
-// (chunks of 64 dims, 128-byte rows).  Past the range the whole row becomes 0;
-// a node's row loses the entries that are not finite and is marked.
+// Keep non-finite values out of the product: the row of key `k` of the tile at
+// `v` (chunks of 64 dims, 128-byte rows).  Past the range the row becomes 0; a
+// node's row loses the entries that are not finite and is marked.
 template <int D>
 __device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t* v, int j0, int k) {
   const int jj = j0 + k;
@@ -201,11 +210,11 @@ __device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t
   for (int c = 0; c < D / 8; ++c) {
     // every 16-byte piece of the row, whatever its place under the swizzle
     uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * (kNt * 128) + k * 128 + (c & 7) * 16);
+    uint4 x = *p;
     if (past) {
-      *p = make_uint4(0u, 0u, 0u, 0u);
+      if ((x.x | x.y | x.z | x.w) != 0u) *p = make_uint4(0u, 0u, 0u, 0u);
       continue;
     }
-    uint4 x = *p;
     uint32_t* w = &x.x;
     bool touched = false;
 #pragma unroll
@@ -223,25 +232,29 @@ __device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t
 
 // Softmax of one stream (128 threads, thread = row), and its share of the output.
 template <int D>
-__device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u, uint8_t* ring, float* share,
-                                       uint32_t tmem, int warp, int lane) {
+__device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring, float* share, uint32_t tmem,
+                                       int warp, int lane) {
+  const Unit& u = sm.unit;
   const int w = (warp - 4) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   const uint32_t tS = lanes + 128u * w, tO = lanes + kColO + 128u * w;
-  const int gsize = p.Hq / p.Hkv;
-  const int row = u.turns ? lrow : 128 * w + lrow;         // row of the block
   const float sl2 = p.scale_log2;
   volatile int* abort_flag = &sm.abort;
   const int steps = u.steps(w);
-  const uint32_t* mask_row = nullptr;
-  if (row < u.R)
-    mask_row = p.mask + u.b * p.mask_stride + (long long)((u.row0 + row) / gsize) * p.words;
+  // steps below this one are on tiles of context keys alone
+  const int plain_tiles = max(min(u.ctx, u.ke) - u.kb, 0) / kNt;
+  const int plain = u.turns ? (plain_tiles + 1 - w) / 2 : plain_tiles;
+  auto row_of = [&]() { return u.turns ? lrow : 128 * w + lrow; };             // row of the block
+  auto mask_of = [&]() -> const uint32_t* {                                     // null: a row without a node
+    const int row = row_of();
+    if (row >= u.R) return nullptr;
+    return p.mask + u.b * p.mask_stride + (long long)((u.row0 + row) / (p.Hq / p.Hkv)) * p.words;
+  };
 
   float m = -INFINITY, l = 0.f;
   bool bad = false;
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
-    const int t = u.tile(w, s), j0 = u.kb + t * kNt;
     if (!__all_sync(0xffffffffu,
                     *abort_flag == 0 && mbar_wait(smem_u32(&sm.s_full[w]), (uint32_t)s & 1u, p.wait_ns))) {
       bad = true;
@@ -252,9 +265,10 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u,
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
     tmem_wait_ld();
-    if (j0 + kNt > min(u.ctx, u.ke)) {
+    if (s >= plain) {
       // nodes or the end of the range in this tile
-      uint8_t* nodes = sm.node[warp - 4];
+      const int j0 = u.kb + u.tile(w, s) * kNt;
+      uint8_t* nodes = sm.node[w];
       __syncwarp();
       for (int k = lane; k < kNt; k += 32) {
         const int jj = j0 + k;
@@ -262,22 +276,19 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u,
       }
       __syncwarp();
       uint32_t vis[4];
-      visibility(u, j0, nodes, mask_row, vis);
+      visibility(u, j0, nodes, mask_of(), vis);
 #pragma unroll
       for (int k = 0; k < kNt; ++k)
         if (!((vis[k >> 5] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
-      // the values of the tile, before this stream's product reads them (with
-      // both streams on one tile the first one's product goes out first)
-      if (u.turns || w == 0) {
-        const int at = u.v_at(t);
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[at % p.slots]), (uint32_t)(at / p.slots) & 1u,
-                                               p.wait_ns))) {
-          bad = true;
-          break;
-        }
-        clean_value_row<D>(u, sm, ring + (at % p.slots) * tile_bytes<D>(), j0, lrow);
-        fence_proxy_async_smem();
+      // the values of the tile, before this stream's product reads them (on a
+      // tile that both streams use, each cleans it: the second finds nothing to do)
+      const int at = 2 * s + 1, slot = u.slot(w, at, p.slots);
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[slot]), u.lap(at, p.slots) & 1u, p.wait_ns))) {
+        bad = true;
+        break;
       }
+      clean_value_row<D>(u, sm, ring + slot * tile_bytes<D>(), j0, lrow);
+      fence_proxy_async_smem();
     }
     auto f = [&](int k) { return __uint_as_float(x[k]); };
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -304,11 +315,13 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u,
         }
       }
     }
+    // whether a probability of this warp's rows is heavy (l = 0: before the first keys, all are)
+    const bool heavy = __any_sync(0xffffffffu, top > m + __log2f(l) - kHeavyLog2);
     const float ref = m == -INFINITY ? 0.f : -m;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      uint32_t hi[16], lo[16];
+      uint32_t hi[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const int a = 32 * c + 2 * k;
@@ -316,15 +329,35 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u,
         const float2 e = make_float2(ex2(y.x), ex2(y.y));
         sum[k & 1] = fadd2(sum[k & 1], e);
         hi[k] = pack_bf16x2(e.x, e.y);
-        lo[k] = pack_bf16x2(e.x - bf16_lo(hi[k]), e.y - bf16_hi(hi[k]));
+        x[a] = __float_as_uint(e.x);
+        x[a + 1] = __float_as_uint(e.y);
       }
       tmem_st16(tS + 16 * c, hi);
-      tmem_st16(tS + 64 + 16 * c, lo);
+    }
+    // the second terms; warps without a heavy one leave zeros, in case another has
+    if (heavy) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t rest[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float e0 = f(32 * c + 2 * k), e1 = f(32 * c + 2 * k + 1);
+          const uint32_t h = pack_bf16x2(e0, e1);
+          rest[k] = pack_bf16x2(e0 - bf16_lo(h), e1 - bf16_hi(h));
+        }
+        tmem_st16(tS + 64 + 16 * c, rest);
+      }
+      if (lane == 0) *(volatile int*)&sm.heavy[w] = s;
+    } else {
+      const uint32_t zero[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_st16(tS + 64 + 16 * c, zero);
     }
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     tmem_wait_st();
     tc_fence_before();
-    mbar_arrive(smem_u32(&sm.p_full[w]));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[w]));
   }
   bool have = !bad;
   if (have && steps > 0)
@@ -334,14 +367,17 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u,
     *abort_flag = 1;
   }
   // one decision for the CTA: every product landed (the query's shared memory
-  // is idle from here on and carries the streams' m and l)
+  // is idle from here on and carries the rows' m and l)
   have = !bar_red_or(kBarEpi, 256, !have);
   tc_fence_after();
   share[(2 * w) * kNt + lrow] = m;
   share[(2 * w + 1) * kNt + lrow] = l;
   named_bar_sync(kBarEpi, 256);
 
-  // in turn: both streams hold the row, each writes half of its dims
+  const int gsize = p.Hq / p.Hkv;
+  const int row = row_of();
+  const uint32_t* mask_row = mask_of();
+  // in turn, both streams hold the row: each writes half of its dims
   float w0 = 1.f, w1 = 0.f;             // weights of this stream's and the other's O
   const bool other = u.turns && u.steps(w ^ 1) > 0;
   if (u.turns) {
@@ -392,6 +428,7 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, const Unit& u,
     }
     if (any_odd && live) {
       // values of nodes that are not finite: added to the rows that see them
+#pragma unroll 1
       for (int bit = 0; bit < DCP_TREE_MAX_NODES; ++bit) {
         if (!((sm.odd[bit >> 5] >> (bit & 31)) & 1u)) continue;
         const int jj = max(u.kb, u.ctx) + bit;
@@ -497,7 +534,8 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&sm.s_full[k]), 1);
-      mbar_init(smem_u32(&sm.p_full[k]), kNt);
+      mbar_init(smem_u32(&sm.p_full[k]), 4);       // warps of the stream
+      sm.heavy[k] = -1;
       mbar_init(smem_u32(&sm.o_full[k]), 1);
     }
     mbar_init(smem_u32(&sm.drain), 1);
@@ -505,6 +543,7 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     fence_mbar_init();
   }
   if (tid < 8) sm.odd[tid] = 0;
+  if (tid == 0) sm.unit = u;
   if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), 512);
   if (warp >= 4 && u.T > 0) {
     // query rows -> shared memory, K-major with the 128-byte swizzle (rows past R are zero)
@@ -535,18 +574,26 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kCtrlRegs));
-    if (warp == 0 && lane == 0 && u.T > 0) {
-      // ---------------- TMA producer ----------------
+    if ((warp == 0 || warp == 3) && lane == 0 && u.T > 0) {
+      // ---------------- TMA producers ----------------
+      // in turn: warp 0 loads stream 0's tiles, warp 3 stream 1's; else warp 0 K, warp 3 V
+      const int w = warp == 0 ? 0 : 1;
       prefetch_tmap(&tm_k);
       prefetch_tmap(&tm_v);
       const int box_rows = p.bs < kNt ? p.bs : kNt;
-      int last = -1;                                       // last place loaded
-      auto load = [&](const CUtensorMap* tm, int t, int at) -> bool {
-        const int slot = at % p.slots;
-        if (*abort_flag || (at >= p.slots && !mbar_wait(smem_u32(&sm.empty[slot]), (uint32_t)(at / p.slots - 1) & 1u,
-                                                        p.wait_ns)))
-          return false;
+      const int steps = u.steps(w), first = u.turns ? 0 : w, by = u.turns ? 1 : 2, items = 2 * steps;
+      int at = first;
+      for (; at < items; at += by) {
+        const int slot = u.slot(w, at, p.slots);
+        const uint32_t lap = u.lap(at, p.slots);
+        if (*abort_flag || (lap > 0 && !mbar_wait(smem_u32(&sm.empty[slot]), (lap - 1) & 1u, p.wait_ns))) {
+          fail();
+          break;
+        }
+        const int t = u.tile(w, at >> 1);
+        const CUtensorMap* tm = (at & 1) ? &tm_v : &tm_k;
         const uint32_t full = smem_u32(&sm.full[slot]);
+        if (t == p.skip_tile && !(at & 1)) continue;        // test hook: a tile that never comes
         uint8_t* dst = ring + slot * kTile;
         mbar_arrive_expect_tx(full, kTile);
         for (int k = 0; k < kNt; k += box_rows) {
@@ -557,80 +604,81 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(smem_u32(dst + c * (kNt * 128) + k * 128), tm, 64 * c, u.g, row, full);
         }
-        last = at;
-        return true;
-      };
-      bool ok = true;
-      if (u.turns) {
-        for (int t = 0; t < min(u.T, 2) && ok; ++t) ok = t == p.skip_tile || load(&tm_k, t, u.k_at(t));
-        for (int t = 0; t < u.T && ok; ++t) {
-          ok = load(&tm_v, t, u.v_at(t));
-          if (ok && t + 2 < u.T) ok = load(&tm_k, t + 2, u.k_at(t + 2));
-        }
-      } else {
-        for (int t = 0; t < u.T && ok; ++t) {
-          ok = (t == p.skip_tile || load(&tm_k, t, u.k_at(t))) && load(&tm_v, t, u.v_at(t));
-        }
       }
-      if (!ok) fail();
       if (*abort_flag) {
-        // let every copy this thread issued land before the CTA exits
-        for (int at = max(0, last - p.slots + 1); at <= last; ++at)
-          mbar_wait(smem_u32(&sm.full[at % p.slots]), (uint32_t)(at / p.slots) & 1u, p.wait_ns);
+        // let every copy this thread issued land before the CTA exits (an item's last lap of its slot)
+        for (int back = at - by; back >= first && back > at - by - u.len(p.slots); back -= by)
+          mbar_wait(smem_u32(&sm.full[u.slot(w, back, p.slots)]), u.lap(back, p.slots) & 1u, p.wait_ns);
       }
     } else if (warp == 1 && lane == 0 && u.T > 0) {
       // ---------------- MMA issuer ----------------
+      // one stream's PV(s) and S(s + 1), then the other's: while the tensor
+      // pipe works for one, the other's probabilities are made
       constexpr uint32_t id_qk = idesc_bf16(128, kNt, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
-      auto landed = [&](int at) {
-        return !*abort_flag && mbar_wait(smem_u32(&sm.full[at % p.slots]), (uint32_t)(at / p.slots) & 1u, p.wait_ns);
+      const bool turns = u.turns;
+      const int len = u.len(p.slots), steps0 = u.steps(0), steps1 = u.steps(1);
+      const uint32_t ring_addr = smem_u32(ring), qs_addr = smem_u32(qs);
+      const uint32_t full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
+      // a cursor per stream over its items (K, V, K, V, ...): slot and lap parity
+      int slot[2] = {0, turns ? len : 0};
+      uint32_t par[2] = {0u, 0u};
+      auto next = [&](int w) {
+        if (++slot[w] == (turns && w == 1 ? 2 * len : len)) {
+          slot[w] -= len;
+          par[w] ^= 1u;
+        }
       };
-      // S of stream w over key tile t, announced on s_full; frees the tile after its last reader
-      auto qk = [&](int w, int t) -> bool {
-        const int at = u.k_at(t), slot = at % p.slots;
-        if (!landed(at)) return false;
+      auto qk = [&](int w) -> bool {
+        const int at = slot[w];
+        if (*abort_flag || !mbar_wait(full + 8 * at, par[w], p.wait_ns)) return false;
         tc_fence_after();
-        const uint8_t* kt = ring + slot * kTile;
-        const uint8_t* qt = qs + (u.turns ? 0 : w) * kTile;
+        const uint32_t kt = ring_addr + at * kTile, qt = qs_addr + (turns ? 0u : w * kTile);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + 128u * w, smem_desc(smem_u32(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32), 16, 1024, kSw128),
-                 smem_desc(smem_u32(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32), 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
+          mma_ss(tmem + 128u * w, smem_desc(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128),
+                 smem_desc(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
         mma_commit(smem_u32(&sm.s_full[w]));
-        if (u.turns || w == 1) mma_commit(smem_u32(&sm.empty[slot]));
+        if (turns || w == 1) mma_commit(empty + 8 * at);
+        next(w);
         return true;
       };
-      auto pv = [&](int w, int s, int t) -> bool {
-        const int at = u.v_at(t), slot = at % p.slots;
-        if (!landed(at) || !mbar_wait(smem_u32(&sm.p_full[w]), (uint32_t)s & 1u, p.wait_ns)) return false;
+      auto pv = [&](int w, int s, bool last) -> bool {
+        const int at = slot[w];
+        if (*abort_flag || !mbar_wait(full + 8 * at, par[w], p.wait_ns) ||
+            !mbar_wait(smem_u32(&sm.p_full[w]), (uint32_t)s & 1u, p.wait_ns))
+          return false;
         tc_fence_after();
-        const uint8_t* vt = ring + slot * kTile;
+        const uint32_t vt = ring_addr + at * kTile;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int k = 0; k < kNt / 16; ++k)
+          mma_ts(tmem + kColO + 128u * w, tmem + 128u * w + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128),
+                 id_pv, (s > 0 || k > 0) ? 1u : 0u);
+        if (*(volatile int*)&sm.heavy[w] == s) {
 #pragma unroll
           for (int k = 0; k < kNt / 16; ++k)
-            mma_ts(tmem + kColO + 128u * w, tmem + 128u * w + 64 * part + 8 * k,
-                   smem_desc(smem_u32(vt + k * 2048), kNt * 128, 1024, kSw128), id_pv,
-                   (s > 0 || part > 0 || k > 0) ? 1u : 0u);
-        if (s + 1 == u.steps(w)) mma_commit(smem_u32(&sm.o_full[w]));
-        if (u.turns || w == 1) mma_commit(smem_u32(&sm.empty[slot]));
+            mma_ts(tmem + kColO + 128u * w, tmem + 128u * w + 64 + 8 * k,
+                   smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv, 1u);
+        }
+        if (last) mma_commit(smem_u32(&sm.o_full[w]));
+        if (turns || w == 1) mma_commit(empty + 8 * at);
+        next(w);
         return true;
       };
-      bool ok = true;
-      for (int w = 0; w < 2 && ok; ++w)
-        if (u.steps(w) > 0) ok = qk(w, u.tile(w, 0));
-      for (int s = 0; s < u.steps(0) && ok; ++s)
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (s < u.steps(w)) ok = pv(w, s, u.tile(w, s));
-          if (ok && s + 1 < u.steps(w)) ok = qk(w, u.tile(w, s + 1));
-        }
+      bool ok = qk(0) && (steps1 == 0 || qk(1));
+      for (int s = 0; s < steps0 && ok; ++s) {
+        ok = pv(0, s, s + 1 == steps0);
+        if (ok && s + 1 < steps0) ok = qk(0);
+        if (ok && s < steps1) ok = pv(1, s, s + 1 == steps1);
+        if (ok && s + 1 < steps1) ok = qk(1);
+      }
       if (!ok) fail();
       mma_commit(smem_u32(&sm.drain));
       if (!mbar_wait(smem_u32(&sm.drain), 0, p.wait_ns)) fail();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
-    stream<D>(p, sm, u, ring, reinterpret_cast<float*>(qs), tmem, warp, lane);
+    stream<D>(p, sm, ring, reinterpret_cast<float*>(qs), tmem, warp, lane);
   }
   tc_fence_before();
   __syncthreads();

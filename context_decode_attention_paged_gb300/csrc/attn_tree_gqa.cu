@@ -610,70 +610,80 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int back = at - by; back >= first && back > at - by - u.len(p.slots); back -= by)
           mbar_wait(smem_u32(&sm.full[u.slot(w, back, p.slots)]), u.lap(back, p.slots) & 1u, p.wait_ns);
       }
-    } else if (warp == 1 && lane == 0 && u.T > 0) {
+    } else if (warp == 1 && u.T > 0) {
       // ---------------- MMA issuer ----------------
       // one stream's PV(s) and S(s + 1), then the other's: while the tensor
-      // pipe works for one, the other's probabilities are made
+      // pipe works for one, the other's probabilities are made.  The whole warp
+      // runs the loop on uniform values and one lane issues: with a single
+      // lane in the loop each MMA cost 65-90 clocks to issue, as long as it runs
       constexpr uint32_t id_qk = idesc_bf16(128, kNt, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
-      const bool turns = u.turns;
-      const int len = u.len(p.slots), steps0 = u.steps(0), steps1 = u.steps(1);
-      const uint32_t ring_addr = smem_u32(ring), qs_addr = smem_u32(qs);
-      const uint32_t full = smem_u32(&sm.full[0]), empty = smem_u32(&sm.empty[0]);
+      const bool turns = uniform(u.turns) != 0, lead = elect_one();
+      const int len = (int)uniform((uint32_t)u.len(p.slots));
+      const int steps0 = (int)uniform((uint32_t)u.steps(0)), steps1 = (int)uniform((uint32_t)u.steps(1));
+      const uint32_t tm = uniform(tmem);
+      const uint32_t ring_addr = uniform(smem_u32(ring)), qs_addr = uniform(smem_u32(qs));
+      const uint32_t full = uniform(smem_u32(&sm.full[0])), empty = uniform(smem_u32(&sm.empty[0]));
+      const uint32_t s_full = uniform(smem_u32(&sm.s_full[0])), p_full = uniform(smem_u32(&sm.p_full[0]));
+      const uint32_t o_full = uniform(smem_u32(&sm.o_full[0]));
       // a cursor per stream over its items (K, V, K, V, ...): slot and lap parity
-      int slot[2] = {0, turns ? len : 0};
-      uint32_t par[2] = {0u, 0u};
-      auto next = [&](int w) {
-        if (++slot[w] == (turns && w == 1 ? 2 * len : len)) {
-          slot[w] -= len;
-          par[w] ^= 1u;
+      int slot0 = 0, slot1 = turns ? len : 0;
+      uint32_t par0 = 0u, par1 = 0u;
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(bar, par, p.wait_ns));
+      };
+      auto next = [&](int w, int& slot, uint32_t& par) {
+        if (++slot == (turns && w == 1 ? 2 * len : len)) {
+          slot -= len;
+          par ^= 1u;
         }
       };
-      auto qk = [&](int w) -> bool {
-        const int at = slot[w];
-        if (*abort_flag || !mbar_wait(full + 8 * at, par[w], p.wait_ns)) return false;
+      auto qk = [&](int w, int& slot, uint32_t& par) -> bool {
+        if (!wait(full + 8 * slot, par)) return false;
         tc_fence_after();
-        const uint32_t kt = ring_addr + at * kTile, qt = qs_addr + (turns ? 0u : w * kTile);
+        const uint32_t kt = ring_addr + slot * kTile, qt = qs_addr + (turns ? 0u : w * kTile);
+        if (lead) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + 128u * w, smem_desc(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128),
-                 smem_desc(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
-        mma_commit(smem_u32(&sm.s_full[w]));
-        if (turns || w == 1) mma_commit(empty + 8 * at);
-        next(w);
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tm + 128u * w, smem_desc(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128),
+                   smem_desc(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
+          mma_commit(s_full + 8 * w);
+          if (turns || w == 1) mma_commit(empty + 8 * slot);
+        }
+        next(w, slot, par);
         return true;
       };
-      auto pv = [&](int w, int s, bool last) -> bool {
-        const int at = slot[w];
-        if (*abort_flag || !mbar_wait(full + 8 * at, par[w], p.wait_ns) ||
-            !mbar_wait(smem_u32(&sm.p_full[w]), (uint32_t)s & 1u, p.wait_ns))
-          return false;
+      auto pv = [&](int w, int& slot, uint32_t& par, int s, bool last) -> bool {
+        if (!wait(full + 8 * slot, par) || !wait(p_full + 8 * w, (uint32_t)s & 1u)) return false;
         tc_fence_after();
-        const uint32_t vt = ring_addr + at * kTile;
-#pragma unroll
-        for (int k = 0; k < kNt / 16; ++k)
-          mma_ts(tmem + kColO + 128u * w, tmem + 128u * w + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128),
-                 id_pv, (s > 0 || k > 0) ? 1u : 0u);
-        if (*(volatile int*)&sm.heavy[w] == s) {
+        const uint32_t vt = ring_addr + slot * kTile;
+        const bool heavy = __any_sync(0xffffffffu, *(volatile int*)&sm.heavy[w] == s);
+        if (lead) {
 #pragma unroll
           for (int k = 0; k < kNt / 16; ++k)
-            mma_ts(tmem + kColO + 128u * w, tmem + 128u * w + 64 + 8 * k,
-                   smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv, 1u);
+            mma_ts(tm + kColO + 128u * w, tm + 128u * w + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128),
+                   id_pv, (s > 0 || k > 0) ? 1u : 0u);
+          if (heavy) {
+#pragma unroll
+            for (int k = 0; k < kNt / 16; ++k)
+              mma_ts(tm + kColO + 128u * w, tm + 128u * w + 64 + 8 * k,
+                     smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv, 1u);
+          }
+          if (last) mma_commit(o_full + 8 * w);
+          if (turns || w == 1) mma_commit(empty + 8 * slot);
         }
-        if (last) mma_commit(smem_u32(&sm.o_full[w]));
-        if (turns || w == 1) mma_commit(empty + 8 * at);
-        next(w);
+        next(w, slot, par);
         return true;
       };
-      bool ok = qk(0) && (steps1 == 0 || qk(1));
+      bool ok = qk(0, slot0, par0) && (steps1 == 0 || qk(1, slot1, par1));
       for (int s = 0; s < steps0 && ok; ++s) {
-        ok = pv(0, s, s + 1 == steps0);
-        if (ok && s + 1 < steps0) ok = qk(0);
-        if (ok && s < steps1) ok = pv(1, s, s + 1 == steps1);
-        if (ok && s + 1 < steps1) ok = qk(1);
+        ok = pv(0, slot0, par0, s, s + 1 == steps0);
+        if (ok && s + 1 < steps0) ok = qk(0, slot0, par0);
+        if (ok && s < steps1) ok = pv(1, slot1, par1, s, s + 1 == steps1);
+        if (ok && s + 1 < steps1) ok = qk(1, slot1, par1);
       }
       if (!ok) fail();
-      mma_commit(smem_u32(&sm.drain));
+      if (lead) mma_commit(smem_u32(&sm.drain));
       if (!mbar_wait(smem_u32(&sm.drain), 0, p.wait_ns)) fail();
     }
   } else {

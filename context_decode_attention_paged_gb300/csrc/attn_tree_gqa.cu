@@ -115,15 +115,13 @@ struct Unit {
 
 struct Smem {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint64_t s_full[2], p_full[2], o_full[2], q_full, drain;
   uint32_t tmem_base;
   int abort;
   int req;
   Unit unit;                       // for the streams: read where it is needed, to save registers
   uint32_t odd[8];                 // node keys of this unit whose values are not all finite (bit: key - first)
   int heavy[2];                    // per stream: the last step with a heavy probability
-  uint8_t node[2][kNt];            // per stream: the node at each key of a masked tile (four warps write the
-                                   // same bytes, each before it reads them)
 };
 
 template <int D>
@@ -172,28 +170,38 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 }
 
 // The 128 visibility bits of one row for the keys [j0, j0 + 128): context keys,
-// and nodes whose bit the row's mask has.  nodes: the node at each key (valid
-// at node keys); row null: a row without nodes.
-__device__ __forceinline__ void visibility(const Unit& u, int j0, const uint8_t* nodes, const uint32_t* row,
+// and nodes whose bit the row's mask has (row null: none).  A shard's keys come
+// in runs of I consecutive positions, so the bits of a run are one cut out of
+// the mask words.
+__device__ __forceinline__ void visibility(const Params& p, const Unit& u, int j0, const uint32_t* row,
                                            uint32_t (&vis)[4]) {
   const int c = min(max(u.ctx - j0, 0), kNt), e = min(max(u.ke - j0, 0), kNt);   // context below c, nodes in [c, e)
-  int at = -1;
-  uint32_t word = 0;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const int cw = min(max(min(c, e) - 32 * w, 0), 32);
     vis[w] = cw == 32 ? 0xffffffffu : (1u << cw) - 1u;
-    if (row != nullptr) {
-#pragma unroll 1
-      for (int k = max(c, 32 * w); k < min(e, 32 * w + 32); ++k) {
-        const int node = nodes[k];
-        if ((node >> 5) != at) {
-          at = node >> 5;
-          word = __ldg(row + at);
-        }
-        vis[w] |= ((word >> (node & 31)) & 1u) << (k & 31);
-      }
+  }
+  int left = 0, node = 0;                    // of the run at k
+  for (int k = c; k < e;) {
+    if (left == 0) {
+      const int jj = j0 + k;
+      node = (int)(global_pos(jj, u.r, p.I, p.N) - u.base);
+      left = p.N == 1 ? e - k : min(p.I - jj % p.I, e - k);
     }
+    const int len = min(left, 32 - (k & 31));
+    if (row != nullptr) {
+      const int wi = node >> 5;
+      const uint32_t lo = __ldg(row + wi), hi = wi + 1 < p.words ? __ldg(row + wi + 1) : 0u;
+      uint32_t bits = __funnelshift_r(lo, hi, node & 31);
+      if (len < 32) bits &= (1u << len) - 1u;
+      bits <<= k & 31;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (w == k >> 5) vis[w] |= bits;
+    }
+    k += len;
+    node += len;
+    left -= len;
   }
 }
 
@@ -206,10 +214,11 @@ __device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t
   const bool past = jj >= u.ke;
   if (!past && jj < u.ctx) return;
   bool odd = false;
-#pragma unroll 1
+#pragma unroll 4
   for (int c = 0; c < D / 8; ++c) {
     // every 16-byte piece of the row, whatever its place under the swizzle
-    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * (kNt * 128) + k * 128 + (c & 7) * 16);
+    // (threads start at different pieces, so that their rows do not meet in a bank)
+    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * (kNt * 128) + k * 128 + ((c ^ k) & 7) * 16);
     uint4 x = *p;
     if (past) {
       if ((x.x | x.y | x.z | x.w) != 0u) *p = make_uint4(0u, 0u, 0u, 0u);
@@ -268,18 +277,15 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
     if (s >= plain) {
       // nodes or the end of the range in this tile
       const int j0 = u.kb + u.tile(w, s) * kNt;
-      uint8_t* nodes = sm.node[w];
-      __syncwarp();
-      for (int k = lane; k < kNt; k += 32) {
-        const int jj = j0 + k;
-        if (jj >= u.ctx && jj < u.ke) nodes[k] = (uint8_t)(global_pos(jj, u.r, p.I, p.N) - u.base);
-      }
-      __syncwarp();
       uint32_t vis[4];
-      visibility(u, j0, nodes, mask_of(), vis);
+      visibility(p, u, j0, mask_of(), vis);
 #pragma unroll
-      for (int k = 0; k < kNt; ++k)
-        if (!((vis[k >> 5] >> (k & 31)) & 1u)) x[k] = 0xff800000u;
+      for (int c = 0; c < 4; ++c)
+        if (__any_sync(0xffffffffu, vis[c] != 0xffffffffu)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!((vis[c] >> k) & 1u)) x[32 * c + k] = 0xff800000u;
+        }
       // the values of the tile, before this stream's product reads them (on a
       // tile that both streams use, each cleans it: the second finds nothing to do)
       const int at = 2 * s + 1, slot = u.slot(w, at, p.slots);
@@ -393,7 +399,7 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
   const float inv = live ? 1.f / l : 0.f;
   w0 *= inv;
   w1 *= inv;
-  const int d0 = u.turns ? w * (D / 2) : 0, d1 = u.turns ? d0 + D / 2 : D;
+  const int d0 = u.turns ? w * (D / 2) : 0;
   const uint32_t tOther = lanes + kColO + 128u * (w ^ 1);
   auto dst_row = [&](int rr) {
     const int i = rr / gsize, head = u.g * gsize + rr % gsize;
@@ -401,22 +407,25 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
   };
   bool any_odd = false;
   for (int k = 0; k < 8; ++k) any_odd |= sm.odd[k] != 0;
-  // 32 dims at a time through 4 KB of the idle ring, so that a row's part goes
-  // out as one 128-byte line
-  uint8_t* mine = ring + (warp - 4) * 4096;
-  // an aborted unit writes its zeros from registers: copies may still land in the ring
-  const bool staged = have;
-  const int out_row0 = u.turns ? quad * 32 : 128 * w + quad * 32;   // first row of this warp in the block
-#pragma unroll 1
-  for (int c = d0; c < d1; c += 32) {
+  const bool writes = row < u.R_out;
+  const unsigned long long out = writes ? (unsigned long long)(p.dst_o + dst_row(u.row0 + row) * D) : 0ull;
+  // through 4 KB of the idle ring for 32 dims, so that a row's part goes out as
+  // one 128-byte line (an aborted unit writes zeros from registers: copies may
+  // still land in the ring)
+  uint8_t* mine = ring + (warp - 4) * (D * 128);
+  const int chunks = (u.turns ? D / 2 : D) / 32;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    if (i >= chunks || !have) break;
+    const int c = d0 + 32 * i;
     uint32_t o[32];
-    if (have && steps > 0) {
+    if (steps > 0) {
       tmem_ld32(tO + c, o);
       tmem_wait_ld();
     }
 #pragma unroll
     for (int k = 0; k < 32; ++k) o[k] = live && steps > 0 ? __float_as_uint(__uint_as_float(o[k]) * w0) : 0u;
-    if (other && have) {
+    if (other) {
       uint32_t o2[32];
       tmem_ld32(tOther + c, o2);
       tmem_wait_ld();
@@ -442,20 +451,22 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
         }
       }
     }
-    __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      *reinterpret_cast<uint4*>(mine + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+      *reinterpret_cast<uint4*>(mine + i * 4096 + lane * 128 + ((k ^ (lane & 7)) << 4)) =
           make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-    __syncwarp();
+  }
+  __syncwarp();
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int rr = it * 4 + (lane >> 3), k = lane & 7;
-      if (out_row0 + rr < u.R_out) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (staged) v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((k ^ (rr & 7)) << 4));
-        *reinterpret_cast<uint4*>(p.dst_o + dst_row(u.row0 + out_row0 + rr) * D + c + 4 * k) = v;
-      }
+  for (int it = 0; it < 8; ++it) {
+    const int rr = it * 4 + (lane >> 3), k = lane & 7;
+    const unsigned long long to = __shfl_sync(0xffffffffu, out, rr);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      if (i >= chunks || to == 0ull) break;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (have) v = *reinterpret_cast<const uint4*>(mine + i * 4096 + rr * 128 + ((k ^ (rr & 7)) << 4));
+      *reinterpret_cast<uint4*>(reinterpret_cast<float*>(to) + d0 + 32 * i + 4 * k) = v;
     }
   }
   // in turn, a block of 256 rows: the rows of absent nodes behind the first 128
@@ -465,7 +476,7 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
       *reinterpret_cast<uint4*>(p.dst_o + to * D + c) = make_uint4(0u, 0u, 0u, 0u);
     if (lane == 0) p.dst_lse[to] = -INFINITY;
   }
-  if (row < u.R_out && (!u.turns || w == 0))
+  if (writes && (!u.turns || w == 0))
     p.dst_lse[dst_row(u.row0 + row)] = live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
@@ -478,6 +489,10 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   uint8_t* ring = qs + (p.block_rows / kNt) * kTile;
   Smem& sm = *reinterpret_cast<Smem*>(ring + p.slots * kTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
 
   // units, longest request first (as in the decode kernel)
   const long long per_req = (long long)p.N * p.Hkv * p.row_blocks * p.n_split;
@@ -486,15 +501,20 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   Unit u;
   u.b = k_req;
   if (p.B <= kLptMaxBatch) {
-    for (int j = tid; j < p.B; j += kThreads) {
-      const int sj = p.seq_lens[j];
+    int* lens = reinterpret_cast<int*>(ring);              // idle until the first load
+    const int sj = tid < p.B ? p.seq_lens[tid] : 0;
+    if (tid < p.B) lens[tid] = sj;
+    __syncthreads();
+    if (tid < p.B) {
       int rank = 0;
+#pragma unroll 8
       for (int i = 0; i < p.B; ++i) {
-        const int si = p.seq_lens[i];
-        rank += (si > sj) || (si == sj && i < j);
+        const int si = lens[i];
+        rank += (si > sj) || (si == sj && i < tid);
       }
-      if (rank == k_req) sm.req = j;
+      if (rank == k_req) sm.req = tid;
     }
+    fence_proxy_async_smem();                              // before the loads into the ring
     __syncthreads();
     u.b = sm.req;
   }
@@ -538,6 +558,7 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       sm.heavy[k] = -1;
       mbar_init(smem_u32(&sm.o_full[k]), 1);
     }
+    mbar_init(smem_u32(&sm.q_full), 8);
     mbar_init(smem_u32(&sm.drain), 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -545,23 +566,6 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (tid < 8) sm.odd[tid] = 0;
   if (tid == 0) sm.unit = u;
   if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), 512);
-  if (warp >= 4 && u.T > 0) {
-    // query rows -> shared memory, K-major with the 128-byte swizzle (rows past R are zero)
-    const int rows = u.turns ? kNt : 2 * kNt;
-    constexpr int kPer = D / 8;                            // 16-byte pieces of a row
-    for (int idx = tid - 128; idx < rows * kPer; idx += 256) {
-      const int rr = idx / kPer, c = idx % kPer;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < u.R) {
-        const int i = (u.row0 + rr) / gsize, head = u.g * gsize + (u.row0 + rr) % gsize;
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + (((long long)u.b * p.Lq + i) * p.Hq + head) * D) + c);
-      }
-      const int lr = rr & 127;
-      *reinterpret_cast<uint4*>(qs + (rr >> 7) * kTile + (c >> 3) * (kNt * 128) + lr * 128 +
-                                (((c & 7) ^ (lr & 7)) << 4)) = v;
-    }
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -578,8 +582,6 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       // ---------------- TMA producers ----------------
       // in turn: warp 0 loads stream 0's tiles, warp 3 stream 1's; else warp 0 K, warp 3 V
       const int w = warp == 0 ? 0 : 1;
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
       const int box_rows = p.bs < kNt ? p.bs : kNt;
       const int steps = u.steps(w), first = u.turns ? 0 : w, by = u.turns ? 1 : 2, items = 2 * steps;
       int at = first;
@@ -675,7 +677,7 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         next(w, slot, par);
         return true;
       };
-      bool ok = qk(0, slot0, par0) && (steps1 == 0 || qk(1, slot1, par1));
+      bool ok = wait(smem_u32(&sm.q_full), 0u) && qk(0, slot0, par0) && (steps1 == 0 || qk(1, slot1, par1));
       for (int s = 0; s < steps0 && ok; ++s) {
         ok = pv(0, slot0, par0, s, s + 1 == steps0);
         if (ok && s + 1 < steps0) ok = qk(0, slot0, par0);
@@ -688,6 +690,25 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
+    if (u.T > 0) {
+      // query rows -> shared memory, K-major with the 128-byte swizzle (rows
+      // past R are zero), while the first tiles are on their way
+      const int rows = u.turns ? kNt : 2 * kNt;
+      constexpr int kPer = D / 8;                          // 16-byte pieces of a row
+      const int c = (tid - 128) % kPer;
+      for (int rr = (tid - 128) / kPer; rr < rows; rr += 256 / kPer) {
+        const int lr = rr & 127;
+        const uint32_t dst = smem_u32(qs + (rr >> 7) * kTile + (c >> 3) * (kNt * 128) + lr * 128 + (((c & 7) ^ (lr & 7)) << 4));
+        // (a row past R: zero bytes from an address inside the query)
+        const int row = rr < u.R ? u.row0 + rr : u.row0;
+        const int i = row / gsize, head = u.g * gsize + row % gsize;
+        cp_async_16(dst, p.q + (((long long)u.b * p.Lq + i) * p.Hq + head) * D + 8 * c, rr < u.R ? 16u : 0u);
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+    }
     stream<D>(p, sm, ring, reinterpret_cast<float*>(qs), tmem, warp, lane);
   }
   tc_fence_before();

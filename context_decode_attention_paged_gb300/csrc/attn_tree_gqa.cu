@@ -62,6 +62,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kNt = 128;                      // keys per tile, rows per stream
+constexpr int kNs = 64;                       // keys per step: half a tile
 constexpr int kMaxSlots = 12;                 // K or V tiles in the ring
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kCtrlRegs = 72, kSoftRegs = 216;
@@ -71,7 +72,8 @@ constexpr float kLazyLog2 = 8.0f;             // m moves when scores pass it by 
 constexpr float kHeavyLog2 = 3.0f;            // a probability above 2^-3 of its row's sum so far takes its second term
 constexpr uint32_t kBarEpi = 1;               // named barrier of the two streams
 constexpr int kLptMaxBatch = 128;             // longest-first unit order up to this batch
-// TMEM columns (512 allocated): S and P of stream w at 128 w, O at 256 + 128 w
+// TMEM columns (512 allocated): scores of step s of stream w, and P over them,
+// at 128 w + 64 (s & 1); O at 256 + 128 w
 constexpr uint32_t kColO = 256;
 
 struct Params {
@@ -99,10 +101,16 @@ struct Unit {
   int T;                   // key tiles
   bool turns;              // the streams take the tiles in turn
   long long base;
-  // key tile of step s of stream w, and how many steps it has
-  __device__ __forceinline__ int tile(int w, int s) const { return turns ? 2 * s + w : s; }
-  __device__ __forceinline__ int steps(int w) const { return turns ? (T + 1 - w) / 2 : T; }
-  // Ring: a stream's step s uses items 2 s (K) and 2 s + 1 (V).  In turn each
+  // key tile n of stream w, how many it has, and its steps (the last half tile may be empty)
+  __device__ __forceinline__ int tile(int w, int n) const { return turns ? 2 * n + w : n; }
+  __device__ __forceinline__ int tiles(int w) const { return turns ? (T + 1 - w) / 2 : T; }
+  __device__ __forceinline__ int steps(int w) const {
+    const int n = tiles(w);
+    return n > 0 && kb + tile(w, n - 1) * kNt + kNs >= ke ? 2 * n - 1 : 2 * n;
+  }
+  // first key of step s
+  __device__ __forceinline__ int key(int w, int s) const { return kb + tile(w, s >> 1) * kNt + (s & 1) * kNs; }
+  // Ring: a stream's tile n uses items 2 n (K) and 2 n + 1 (V).  In turn each
   // stream has half of the slots to itself, else both read every item, so that
   // a stream that waits for an item has consumed the slot's last one (a barrier
   // a whole lap ahead of its waiter would look complete).
@@ -115,13 +123,13 @@ struct Unit {
 
 struct Smem {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full, drain;
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], q_full, drain[2];   // [stream][step parity]
   uint32_t tmem_base;
   int abort;
   int req;
   Unit unit;                       // for the streams: read where it is needed, to save registers
   uint32_t odd[8];                 // node keys of this unit whose values are not all finite (bit: key - first)
-  int heavy[2];                    // per stream: the last step with a heavy probability
+  int heavy[2][2];                 // per stream and step parity: the last step with a heavy probability
 };
 
 template <int D>
@@ -169,15 +177,15 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   return d;
 }
 
-// The 128 visibility bits of one row for the keys [j0, j0 + 128): context keys,
+// The 64 visibility bits of one row for the keys [j0, j0 + 64): context keys,
 // and nodes whose bit the row's mask has (row null: none).  A shard's keys come
 // in runs of I consecutive positions, so the bits of a run are one cut out of
 // the mask words.
 __device__ __forceinline__ void visibility(const Params& p, const Unit& u, int j0, const uint32_t* row,
-                                           uint32_t (&vis)[4]) {
-  const int c = min(max(u.ctx - j0, 0), kNt), e = min(max(u.ke - j0, 0), kNt);   // context below c, nodes in [c, e)
+                                           uint32_t (&vis)[2]) {
+  const int c = min(max(u.ctx - j0, 0), kNs), e = min(max(u.ke - j0, 0), kNs);   // context below c, nodes in [c, e)
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < 2; ++w) {
     const int cw = min(max(min(c, e) - 32 * w, 0), 32);
     vis[w] = cw == 32 ? 0xffffffffu : (1u << cw) - 1u;
   }
@@ -196,7 +204,7 @@ __device__ __forceinline__ void visibility(const Params& p, const Unit& u, int j
       if (len < 32) bits &= (1u << len) - 1u;
       bits <<= k & 31;
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+      for (int w = 0; w < 2; ++w)
         if (w == k >> 5) vis[w] |= bits;
     }
     k += len;
@@ -205,20 +213,20 @@ __device__ __forceinline__ void visibility(const Params& p, const Unit& u, int j
   }
 }
 
-// Keep non-finite values out of the product: the row of key `k` of the tile at
+// Keep non-finite values out of the product: half `hf` of the row of key j at
 // `v` (chunks of 64 dims, 128-byte rows).  Past the range the row becomes 0; a
 // node's row loses the entries that are not finite and is marked.
 template <int D>
-__device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t* v, int j0, int k) {
-  const int jj = j0 + k;
+__device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t* v, int jj, int hf) {
   const bool past = jj >= u.ke;
   if (!past && jj < u.ctx) return;
   bool odd = false;
 #pragma unroll 4
-  for (int c = 0; c < D / 8; ++c) {
-    // every 16-byte piece of the row, whatever its place under the swizzle
+  for (int i = 0; i < D / 16; ++i) {
+    // 16-byte pieces of the row, whatever their place under the swizzle
     // (threads start at different pieces, so that their rows do not meet in a bank)
-    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * (kNt * 128) + k * 128 + ((c ^ k) & 7) * 16);
+    const int c = hf * (D / 16) + i;
+    uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * (kNt * 128) + (D == 64 ? (c ^ jj) & 3 | c & 4 : (c ^ jj) & 7) * 16);
     uint4 x = *p;
     if (past) {
       if ((x.x | x.y | x.z | x.w) != 0u) *p = make_uint4(0u, 0u, 0u, 0u);
@@ -250,9 +258,8 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
   const float sl2 = p.scale_log2;
   volatile int* abort_flag = &sm.abort;
   const int steps = u.steps(w);
-  // steps below this one are on tiles of context keys alone
-  const int plain_tiles = max(min(u.ctx, u.ke) - u.kb, 0) / kNt;
-  const int plain = u.turns ? (plain_tiles + 1 - w) / 2 : plain_tiles;
+  // steps whose first key is at most this one hold context keys alone
+  const int plain = min(u.ctx, u.ke) - kNs;
   auto row_of = [&]() { return u.turns ? lrow : 128 * w + lrow; };             // row of the block
   auto mask_of = [&]() -> const uint32_t* {                                     // null: a row without a node
     const int row = row_of();
@@ -261,109 +268,114 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
   };
 
   float m = -INFINITY, l = 0.f;
+  float heavy_at = -INFINITY;            // a score above it is heavy, or moves the reference
   bool bad = false;
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
-    if (!__all_sync(0xffffffffu,
-                    *abort_flag == 0 && mbar_wait(smem_u32(&sm.s_full[w]), (uint32_t)s & 1u, p.wait_ns))) {
+    const int buf = s & 1;
+    const uint32_t tB = tS + kNs * buf;
+    if (!__all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&sm.s_full[w][buf]), (uint32_t)(s >> 1) & 1u,
+                                                               p.wait_ns))) {
       bad = true;
       break;
     }
-    uint32_t x[kNt];
+    uint32_t x[kNs];
     tc_fence_after();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
+    for (int c = 0; c < 2; ++c) tmem_ld32(tB + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
     tmem_wait_ld();
-    if (s >= plain) {
-      // nodes or the end of the range in this tile
-      const int j0 = u.kb + u.tile(w, s) * kNt;
-      uint32_t vis[4];
+    {
+      // the second terms are zero unless this warp finds a heavy probability
+      // below (another warp of the stream may have one)
+      const uint32_t zero[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      tmem_st16(tB + 32, zero);
+      tmem_st16(tB + 48, zero);
+    }
+    const int j0 = u.key(w, s);
+    if (j0 > plain) {
+      // nodes or the end of the range
+      uint32_t vis[2];
       visibility(p, u, j0, mask_of(), vis);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 2; ++c)
         if (__any_sync(0xffffffffu, vis[c] != 0xffffffffu)) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (!((vis[c] >> k) & 1u)) x[32 * c + k] = 0xff800000u;
         }
-      // the values of the tile, before this stream's product reads them (on a
-      // tile that both streams use, each cleans it: the second finds nothing to do)
-      const int at = 2 * s + 1, slot = u.slot(w, at, p.slots);
+      // the values, before this stream's product reads them (on a tile that
+      // both streams use, each cleans it: the second finds nothing to do)
+      const int at = (s | 1), slot = u.slot(w, at, p.slots);
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[slot]), u.lap(at, p.slots) & 1u, p.wait_ns))) {
         bad = true;
         break;
       }
-      clean_value_row<D>(u, sm, ring + slot * tile_bytes<D>(), j0, lrow);
+      const int k = (s & 1) * kNs + (lrow & 63);
+      clean_value_row<D>(u, sm, ring + slot * tile_bytes<D>() + k * 128, j0 + (lrow & 63), lrow >> 6);
       fence_proxy_async_smem();
     }
     auto f = [&](int k) { return __uint_as_float(x[k]); };
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int k = 0; k < kNt; k += 8)
+    for (int k = 0; k < kNs; k += 8)
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], f(k + e), f(k + 4 + e));
     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-    const bool moves = top > m + kLazyLog2;
-    if (__any_sync(0xffffffffu, moves)) {
-      const float to = moves ? top : m;
-      const float alpha = !moves ? 1.f : m == -INFINITY ? 0.f : ex2(m - to);
-      m = to;
-      l *= alpha;
-      if (s > 0) {
+    const bool heavy = __any_sync(0xffffffffu, top > heavy_at);
+    if (heavy) {
+      const bool moves = top > m + kLazyLog2;
+      if (__any_sync(0xffffffffu, moves)) {
+        const float to = moves ? top : m;
+        const float alpha = !moves ? 1.f : m == -INFINITY ? 0.f : ex2(m - to);
+        m = to;
+        l *= alpha;
+        if (s > 0) {
+          // O moves with the reference, once the previous product has landed
+          // (the one before it did before this step's scores went out, so the
+          // parity is unambiguous)
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.pv_done[w]), (uint32_t)(s - 1) & 1u, p.wait_ns))) {
+            bad = true;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + c, o);
-          tmem_wait_ld();
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st32(tO + c, o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(tO + c, o);
+          }
         }
       }
     }
-    // whether a probability of this warp's rows is heavy (l = 0: before the first keys, all are)
-    const bool heavy = __any_sync(0xffffffffu, top > m + __log2f(l) - kHeavyLog2);
     const float ref = m == -INFINITY ? 0.f : -m;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t hi[32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t hi[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int a = 32 * c + 2 * k;
-        const float2 y = ffma2(make_float2(f(a), f(a + 1)), make_float2(sl2, sl2), make_float2(ref, ref));
-        const float2 e = make_float2(ex2(y.x), ex2(y.y));
-        sum[k & 1] = fadd2(sum[k & 1], e);
-        hi[k] = pack_bf16x2(e.x, e.y);
-        x[a] = __float_as_uint(e.x);
-        x[a + 1] = __float_as_uint(e.y);
-      }
-      tmem_st16(tS + 16 * c, hi);
+    for (int k = 0; k < 32; ++k) {
+      const float2 y = ffma2(make_float2(f(2 * k), f(2 * k + 1)), make_float2(sl2, sl2), make_float2(ref, ref));
+      const float2 e = make_float2(ex2(y.x), ex2(y.y));
+      sum[k & 1] = fadd2(sum[k & 1], e);
+      hi[k] = pack_bf16x2(e.x, e.y);
+      x[2 * k] = __float_as_uint(e.x);
+      x[2 * k + 1] = __float_as_uint(e.y);
     }
-    // the second terms; warps without a heavy one leave zeros, in case another has
+    tmem_st32(tB, hi);
     if (heavy) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t rest[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float e0 = f(32 * c + 2 * k), e1 = f(32 * c + 2 * k + 1);
-          const uint32_t h = pack_bf16x2(e0, e1);
-          rest[k] = pack_bf16x2(e0 - bf16_lo(h), e1 - bf16_hi(h));
-        }
-        tmem_st16(tS + 64 + 16 * c, rest);
-      }
-      if (lane == 0) *(volatile int*)&sm.heavy[w] = s;
-    } else {
-      const uint32_t zero[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st16(tS + 64 + 16 * c, zero);
+      for (int k = 0; k < 32; ++k)
+        hi[k] = pack_bf16x2(f(2 * k) - bf16_lo(hi[k]), f(2 * k + 1) - bf16_hi(hi[k]));
+      tmem_st32(tB + 32, hi);
+      if (lane == 0) *(volatile int*)&sm.heavy[w][buf] = s;
     }
-    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[w]));
+    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[w][buf]));
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    heavy_at = fminf(m + __log2f(l) - kHeavyLog2, m + kLazyLog2);
   }
   bool have = !bad;
   if (have && steps > 0)
@@ -550,16 +562,20 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (tid == 0) {
     for (int k = 0; k < p.slots; ++k) {
       mbar_init(smem_u32(&sm.full[k]), 1);
-      mbar_init(smem_u32(&sm.empty[k]), 1);
+      mbar_init(smem_u32(&sm.empty[k]), u.turns ? 1 : 2);   // streams that read the tile
     }
     for (int k = 0; k < 2; ++k) {
-      mbar_init(smem_u32(&sm.s_full[k]), 1);
-      mbar_init(smem_u32(&sm.p_full[k]), 4);       // warps of the stream
-      sm.heavy[k] = -1;
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&sm.s_full[k][b]), 1);
+        mbar_init(smem_u32(&sm.p_full[k][b]), 4);    // warps of the stream
+        sm.heavy[k][b] = -1;
+      }
+      mbar_init(smem_u32(&sm.pv_done[k]), 1);
       mbar_init(smem_u32(&sm.o_full[k]), 1);
     }
     mbar_init(smem_u32(&sm.q_full), 8);
-    mbar_init(smem_u32(&sm.drain), 1);
+    mbar_init(smem_u32(&sm.drain[0]), 1);
+    mbar_init(smem_u32(&sm.drain[1]), 1);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -583,7 +599,7 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       // in turn: warp 0 loads stream 0's tiles, warp 3 stream 1's; else warp 0 K, warp 3 V
       const int w = warp == 0 ? 0 : 1;
       const int box_rows = p.bs < kNt ? p.bs : kNt;
-      const int steps = u.steps(w), first = u.turns ? 0 : w, by = u.turns ? 1 : 2, items = 2 * steps;
+      const int first = u.turns ? 0 : w, by = u.turns ? 1 : 2, items = 2 * u.tiles(w);
       int at = first;
       for (; at < items; at += by) {
         const int slot = u.slot(w, at, p.slots);
@@ -612,81 +628,88 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int back = at - by; back >= first && back > at - by - u.len(p.slots); back -= by)
           mbar_wait(smem_u32(&sm.full[u.slot(w, back, p.slots)]), u.lap(back, p.slots) & 1u, p.wait_ns);
       }
-    } else if (warp == 1 && u.T > 0) {
+    } else if ((warp == 1 || warp == 2) && u.tiles(warp - 1) > 0) {
+      const int w = (int)uniform((uint32_t)warp - 1u);
       // ---------------- MMA issuer ----------------
       // one stream's PV(s) and S(s + 1), then the other's: while the tensor
       // pipe works for one, the other's probabilities are made.  The whole warp
       // runs the loop on uniform values and one lane issues: with a single
       // lane in the loop each MMA cost 65-90 clocks to issue, as long as it runs
-      constexpr uint32_t id_qk = idesc_bf16(128, kNt, false);
+      constexpr uint32_t id_qk = idesc_bf16(128, kNs, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
       const bool turns = uniform(u.turns) != 0, lead = elect_one();
       const int len = (int)uniform((uint32_t)u.len(p.slots));
-      const int steps0 = (int)uniform((uint32_t)u.steps(0)), steps1 = (int)uniform((uint32_t)u.steps(1));
+      const int steps = (int)uniform((uint32_t)u.steps(w));
       const uint32_t tm = uniform(tmem);
       const uint32_t ring_addr = uniform(smem_u32(ring)), qs_addr = uniform(smem_u32(qs));
       const uint32_t full = uniform(smem_u32(&sm.full[0])), empty = uniform(smem_u32(&sm.empty[0]));
-      const uint32_t s_full = uniform(smem_u32(&sm.s_full[0])), p_full = uniform(smem_u32(&sm.p_full[0]));
-      const uint32_t o_full = uniform(smem_u32(&sm.o_full[0]));
-      // a cursor per stream over its items (K, V, K, V, ...): slot and lap parity
-      int slot0 = 0, slot1 = turns ? len : 0;
-      uint32_t par0 = 0u, par1 = 0u;
+      const uint32_t s_full = uniform(smem_u32(&sm.s_full[0][0])), p_full = uniform(smem_u32(&sm.p_full[0][0]));
+      const uint32_t pv_done = uniform(smem_u32(&sm.pv_done[0])), o_full = uniform(smem_u32(&sm.o_full[0]));
+      // per stream: cursors over the K and the V tiles (slot and lap parity; a
+      // tile serves two steps), as items K V K V ... of its part of the ring
+      struct Cursor {
+        int slot;
+        uint32_t par;
+      };
       auto wait = [&](uint32_t bar, uint32_t par) {
         return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(bar, par, p.wait_ns));
       };
-      auto next = [&](int w, int& slot, uint32_t& par) {
-        if (++slot == (turns && w == 1 ? 2 * len : len)) {
-          slot -= len;
-          par ^= 1u;
+      auto next = [&](Cursor& c) {          // two items on
+        c.slot += 2;
+        if (c.slot >= (turns && w == 1 ? 2 * len : len)) {
+          c.slot -= len;
+          c.par ^= 1u;
         }
       };
-      auto qk = [&](int w, int& slot, uint32_t& par) -> bool {
-        if (!wait(full + 8 * slot, par)) return false;
-        tc_fence_after();
-        const uint32_t kt = ring_addr + slot * kTile, qt = qs_addr + (turns ? 0u : w * kTile);
+      // scores of step s into their buffer
+      auto qk = [&](Cursor& c, int s) -> bool {
+        if (!(s & 1) && !wait(full + 8 * c.slot, c.par)) return false;
+        const uint32_t kt = ring_addr + c.slot * kTile + (s & 1) * (kNs * 128), qt = qs_addr + (turns ? 0u : w * kTile);
+        const bool done = (s & 1) || s + 1 == steps;      // the tile's last step
         if (lead) {
+          tc_fence_after();
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tm + 128u * w, smem_desc(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128),
+            mma_ss(tm + 128u * w + kNs * (s & 1), smem_desc(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128),
                    smem_desc(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
-          mma_commit(s_full + 8 * w);
-          if (turns || w == 1) mma_commit(empty + 8 * slot);
+          mma_commit(s_full + 16 * w + 8 * (s & 1));
+          if (done) mma_commit(empty + 8 * c.slot);
         }
-        next(w, slot, par);
+        if (done) next(c);
         return true;
       };
-      auto pv = [&](int w, int& slot, uint32_t& par, int s, bool last) -> bool {
-        if (!wait(full + 8 * slot, par) || !wait(p_full + 8 * w, (uint32_t)s & 1u)) return false;
+      auto pv = [&](Cursor& c, int s) -> bool {
+        if ((!(s & 1) && !wait(full + 8 * c.slot, c.par)) ||
+            !wait(p_full + 16 * w + 8 * (s & 1), (uint32_t)(s >> 1) & 1u))
+          return false;
         tc_fence_after();
-        const uint32_t vt = ring_addr + slot * kTile;
-        const bool heavy = __any_sync(0xffffffffu, *(volatile int*)&sm.heavy[w] == s);
+        const uint32_t vt = ring_addr + c.slot * kTile + (s & 1) * (kNs * 128), pt = tm + 128u * w + kNs * (s & 1);
+        const bool heavy = __any_sync(0xffffffffu, *(volatile int*)&sm.heavy[w][s & 1] == s);
+        const bool done = (s & 1) || s + 1 == steps;
         if (lead) {
 #pragma unroll
-          for (int k = 0; k < kNt / 16; ++k)
-            mma_ts(tm + kColO + 128u * w, tm + 128u * w + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128),
-                   id_pv, (s > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < kNs / 16; ++k)
+            mma_ts(tm + kColO + 128u * w, pt + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv,
+                   (s > 0 || k > 0) ? 1u : 0u);
           if (heavy) {
 #pragma unroll
-            for (int k = 0; k < kNt / 16; ++k)
-              mma_ts(tm + kColO + 128u * w, tm + 128u * w + 64 + 8 * k,
-                     smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv, 1u);
+            for (int k = 0; k < kNs / 16; ++k)
+              mma_ts(tm + kColO + 128u * w, pt + 32 + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv, 1u);
           }
-          if (last) mma_commit(o_full + 8 * w);
-          if (turns || w == 1) mma_commit(empty + 8 * slot);
+          mma_commit(pv_done + 8 * w);
+          if (s + 1 == steps) mma_commit(o_full + 8 * w);
+          if (done) mma_commit(empty + 8 * c.slot);
         }
-        next(w, slot, par);
+        if (done) next(c);
         return true;
       };
-      bool ok = wait(smem_u32(&sm.q_full), 0u) && qk(0, slot0, par0) && (steps1 == 0 || qk(1, slot1, par1));
-      for (int s = 0; s < steps0 && ok; ++s) {
-        ok = pv(0, slot0, par0, s, s + 1 == steps0);
-        if (ok && s + 1 < steps0) ok = qk(0, slot0, par0);
-        if (ok && s < steps1) ok = pv(1, slot1, par1, s, s + 1 == steps1);
-        if (ok && s + 1 < steps1) ok = qk(1, slot1, par1);
-      }
+      const int at0 = turns && w == 1 ? len : 0;
+      Cursor kc = {at0, 0u}, vc = {at0 + 1, 0u};
+      bool ok = wait(smem_u32(&sm.q_full), 0u) && qk(kc, 0) && (steps < 2 || qk(kc, 1));
+      for (int s = 0; s < steps && ok; ++s) ok = pv(vc, s) && (s + 2 >= steps || qk(kc, s + 2));
       if (!ok) fail();
-      if (lead) mma_commit(smem_u32(&sm.drain));
-      if (!mbar_wait(smem_u32(&sm.drain), 0, p.wait_ns)) fail();
+      if (lead) mma_commit(smem_u32(&sm.drain[w]));
+      if (!mbar_wait(smem_u32(&sm.drain[w]), 0, p.wait_ns)) fail();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));

@@ -112,9 +112,15 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it (3 us a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _check(code: int, what: str):
@@ -240,42 +246,50 @@ def dcp_merge(partial_out, lse, dcp_size, out=None, out_lse=None, want_lse=True,
 # Speculative verify: rotary append, drafted-tree attention, commit
 # ---------------------------------------------------------------------------
 
-def _need(ok, what):
-    if not ok:
-        raise DcpError(DCP_ERR_INVALID_ARG, what)
+def _refuse(call, what):
+    raise DcpError(DCP_ERR_INVALID_ARG, f"{call}: {what}")
 
 
-def _need_tensors(what, dtype, *tensors):
-    """The tensors (None: skipped) are of ``dtype`` on the current device, and contiguous."""
-    device = torch.cuda.current_device()
+def _check_tensors(call, dtype, device, tensors):
+    """The tensors (None: skipped) are of ``dtype`` on ``device``, and contiguous."""
     for t in tensors:
-        if t is not None:
-            _need(t.dtype is dtype and t.get_device() == device and t.is_contiguous(),
-                  f"{what}: a tensor is not a contiguous {dtype} tensor on the current device")
+        if t is not None and (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
+            _refuse(call, f"a tensor is not a contiguous {dtype} tensor on the current device")
 
 
 @functools.lru_cache(maxsize=1024)
-def _cached_desc(*fields) -> DcpAttnDesc:
-    return DcpAttnDesc(*fields)
+def _cached_desc(*fields):
+    """Pointer to the descriptor of a shape (descriptors are never written)."""
+    return ctypes.pointer(DcpAttnDesc(*fields))
 
 
-def _cache_fields(what, kind, kv_cache, block_tables, batch, dcp_size):
+@functools.lru_cache(maxsize=1024)
+def _cached_strides(*fields):
+    return ctypes.pointer(DcpAppendStrides(*fields))
+
+
+def _cache_fields(call, kind, kv_cache, block_tables, batch, dcp_size):
     """(kind, Hkv, Dqk, block_size, num_blocks, max_local_blocks) from the cache's tensors."""
     kind = KINDS.get(kind, kind)
+    shape = kv_cache.shape
     if kind == DCP_ATTN_GQA:
-        _need(kv_cache.dim() == 5 and kv_cache.shape[0] == 2, f"{what}: a GQA cache is [2][blocks][block_size][Hkv][D]")
-        _, nb, bs, hkv, dim = kv_cache.shape
+        if len(shape) != 5 or shape[0] != 2:
+            _refuse(call, "a GQA cache is [2][blocks][block_size][Hkv][D]")
+        _, nb, bs, hkv, dim = shape
     else:
-        _need(kv_cache.dim() == 3, f"{what}: an MLA cache is [blocks][block_size][Dqk]")
-        (nb, bs, dim), hkv = kv_cache.shape, 1
-    _need(block_tables.dim() == 3 and block_tables.shape[0] == dcp_size and block_tables.shape[1] == batch,
-          f"{what}: block_tables is [dcp_size][batch][max_local_blocks]")
-    return kind, hkv, dim, bs, nb, block_tables.shape[2]
+        if len(shape) != 3:
+            _refuse(call, "an MLA cache is [blocks][block_size][Dqk]")
+        (nb, bs, dim), hkv = shape, 1
+    tables = block_tables.shape
+    if len(tables) != 3 or tables[0] != dcp_size or tables[1] != batch:
+        _refuse(call, "block_tables is [dcp_size][batch][max_local_blocks]")
+    return kind, hkv, dim, bs, nb, tables[2]
 
 
-def _need_lens(what, batch, *tensors):
+def _check_lens(call, batch, tensors):
     for t in tensors:
-        _need(t is None or (t.dim() == 1 and t.shape[0] == batch), f"{what}: lengths are [batch]")
+        if t is not None and (t.dim() != 1 or t.shape[0] != batch):
+            _refuse(call, "lengths are [batch]")
 
 
 @dataclasses.dataclass(frozen=True)
@@ -292,7 +306,9 @@ def dcp_rope_table(rot_dim, base=10000.0, layout="half", rot_offset=0, scaling="
     to every dcp_kv_cache_append.  ``scaling``: "none", "linear", "ntk" or "yarn", by ``factor``;
     ``mscale`` multiplies the rotated values (None: 1, and 0.1 ln(factor) + 1 for "yarn" with
     factor > 1); ``inv_freq`` (a float64 sequence of rot_dim / 2) replaces base and scaling."""
-    _need(layout in ROPE_LAYOUTS and scaling in ROPE_SCALINGS, "dcp_rope_table: layout or scaling")
+    call = "dcp_rope_table"
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        _refuse(call, "layout or scaling")
     if mscale is None:
         mscale = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0
     desc = DcpRopeDesc(rot_dim, rot_offset, ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], int(original_max_position or 0),
@@ -301,8 +317,9 @@ def dcp_rope_table(rot_dim, base=10000.0, layout="half", rot_offset=0, scaling="
     freqs = None
     if inv_freq is not None:
         freqs = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
-        _need(freqs.dim() == 1 and freqs.numel() == rot_dim // 2, "dcp_rope_table: inv_freq is [rot_dim / 2]")
-    _check(_lib.dcp_rope_steps(ctypes.byref(desc), _ptr(freqs), _ptr(steps)), "dcp_rope_table")
+        if freqs.dim() != 1 or freqs.numel() != rot_dim // 2:
+            _refuse(call, "inv_freq is [rot_dim / 2]")
+    _check(_lib.dcp_rope_steps(ctypes.byref(desc), _ptr(freqs), _ptr(steps)), call)
     return RopeTable(desc, steps.to(device))
 
 
@@ -318,7 +335,8 @@ def tree_mask(parents):
     for row in flat:
         seen, depth = [], []
         for i, p in enumerate(row):
-            _need(-1 <= p < i, "tree_mask: a parent comes before its child, -1 at a root")
+            if not -1 <= p < i:
+                _refuse("tree_mask", "a parent comes before its child, -1 at a root")
             seen.append((seen[p] if p >= 0 else 0) | 1 << i)
             depth.append(depth[p] + 1 if p >= 0 else 0)
         words_of = [[(s >> (32 * w)) & 0xFFFFFFFF for w in range(words)] for s in seen]
@@ -329,18 +347,23 @@ def tree_mask(parents):
             torch.tensor(depths, dtype=torch.int32).view(*shape, -1))
 
 
-def _row_strides(what, t, batch, n, row_shape):
-    """(batch, token) strides in elements of rows [batch][n][*row_shape], each row contiguous."""
-    _need(t.dtype is torch.bfloat16 and t.get_device() == torch.cuda.current_device(),
-          f"{what}: rows are bfloat16 on the current device")
-    _need(t.shape == (batch, n, *row_shape), f"{what}: rows are {(batch, n, *row_shape)}, got {tuple(t.shape)}")
+def _row_strides(call, t, device, shape):
+    """(batch, token) strides in elements of rows [batch][n][...], each token's row contiguous."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != device:
+        _refuse(call, "rows are bfloat16 on the current device")
+    if t.shape != shape:
+        _refuse(call, f"rows are {shape}, got {tuple(t.shape)}")
     stride = t.stride()
-    inner = stride[-1] == 1 and (len(row_shape) == 1 or row_shape[0] == 1 or stride[-2] == row_shape[-1])
-    _need(inner, f"{what}: a token's row is contiguous")
+    width = shape[-1]
+    if len(shape) == 4:
+        if stride[2] != width and shape[2] > 1:
+            _refuse(call, "a token's row is contiguous")
+        width *= shape[2]
+    if stride[-1] != 1:
+        _refuse(call, "a token's row is contiguous")
     # the stride of a dimension of one entry says nothing: the contiguous one stands for it
-    width = row_shape[-1] * (row_shape[0] if len(row_shape) == 2 else 1)
-    token = stride[1] if n > 1 else width
-    return (stride[0] if batch > 1 else token * n), token
+    token = stride[1] if shape[1] > 1 else width
+    return (stride[0] if shape[0] > 1 else token * shape[1]), token
 
 
 def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dcp_size, interleave, rope, q=None,
@@ -354,38 +377,47 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
     0, 1, 2, ...; a tree passes its depths).  kv_cache and q_out are written in place, rows behind a
     request's q_lens are left alone.  Returns (kv_cache, q_out); q_out may be q, and without one a
     zeroed tensor is allocated."""
-    what = "dcp_kv_cache_append"
+    call = "dcp_kv_cache_append"
     B, n = new_k.shape[:2]
-    kind, hkv, dim, bs, nb, max_lb = _cache_fields(what, kind, kv_cache, block_tables, B, dcp_size)
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
     gqa = kind == DCP_ATTN_GQA
-    row = (hkv, dim) if gqa else (dim,)
-    _need((new_v is not None) == gqa, f"{what}: GQA takes new_v, MLA none")
-    _need_tensors(what, torch.bfloat16, kv_cache, q_out if q_out is not q else None)
-    _need_tensors(what, torch.int32, block_tables, seq_lens, q_lens, pos_offsets)
-    _need_lens(what, B, seq_lens, q_lens)
-    _need(rope.steps.get_device() == kv_cache.get_device(), f"{what}: the rope table is on another device")
-    k_batch, k_token = _row_strides(what, new_k, B, n, row)
-    v_batch, v_token = _row_strides(what, new_v, B, n, row) if gqa else (0, 0)
+    rows = (B, n, hkv, dim) if gqa else (B, n, dim)
+    if (new_v is not None) != gqa:
+        _refuse(call, "GQA takes new_v, MLA none")
+    device = torch.cuda.current_device()
+    _check_tensors(call, torch.bfloat16, device, (kv_cache, None if q_out is q else q_out))
+    _check_tensors(call, torch.int32, device, (block_tables, seq_lens, q_lens, pos_offsets))
+    _check_lens(call, B, (seq_lens, q_lens))
+    steps = rope.steps
+    if steps.get_device() != device:
+        _refuse(call, "the rope table is not on the current device")
+    k_batch, k_token = _row_strides(call, new_k, device, rows)
+    v_batch, v_token = _row_strides(call, new_v, device, rows) if gqa else (0, 0)
     hq, q_batch, q_token = hkv, 0, 0
     if q is not None:
-        _need(q.dim() == 4, f"{what}: q is [batch][n][Hq][Dqk]")
+        if q.dim() != 4:
+            _refuse(call, "q is [batch][n][Hq][Dqk]")
         hq = q.shape[2]
-        q_batch, q_token = _row_strides(what, q, B, n, (hq, dim))
+        q_batch, q_token = _row_strides(call, q, device, (B, n, hq, dim))
         if q_out is None:
             with torch.cuda.stream(stream):
                 q_out = torch.zeros((B, n, hq, dim), dtype=torch.bfloat16, device=q.device)
-        _need(q_out.shape == q.shape, f"{what}: q_out is shaped as q")
+        elif q_out.shape != q.shape:
+            _refuse(call, "q_out is shaped as q")
     offsets_stride = 0
     if pos_offsets is not None:
-        _need(pos_offsets.dim() == 2 and pos_offsets.shape[1] == n and pos_offsets.shape[0] in (1, B),
-              f"{what}: pos_offsets is [batch or 1][n]")
+        if pos_offsets.dim() != 2 or pos_offsets.shape[1] != n or pos_offsets.shape[0] not in (1, B):
+            _refuse(call, "pos_offsets is [batch or 1][n]")
         offsets_stride = n if pos_offsets.shape[0] == B else 0
-    desc = _cached_desc(kind, B, n, hq, hkv, dim, dim, bs, nb, max_lb)
-    strides = DcpAppendStrides(k_batch, k_token, v_batch, v_token, q_batch, q_token)
-    _check(_lib.dcp_kv_cache_append(desc, rope.desc, rope.steps.data_ptr(), new_k.data_ptr(), _ptr(new_v), _ptr(q),
-                                    strides, _ptr(q_out), _ptr(pos_offsets), offsets_stride, _ptr(q_lens),
-                                    kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), dcp_size,
-                                    interleave, _stream(stream)), what)
+    code = _lib.dcp_kv_cache_append(
+        _cached_desc(kind, B, n, hq, hkv, dim, dim, bs, nb, max_lb), rope.desc, steps.data_ptr(), new_k.data_ptr(),
+        new_v.data_ptr() if gqa else None, None if q is None else q.data_ptr(),
+        _cached_strides(k_batch, k_token, v_batch, v_token, q_batch, q_token), None if q is None else q_out.data_ptr(),
+        None if pos_offsets is None else pos_offsets.data_ptr(), offsets_stride,
+        None if q_lens is None else q_lens.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        dcp_size, interleave, _stream(stream))
+    if code != DCP_OK:
+        raise DcpError(code, call)
     return kv_cache, q_out
 
 
@@ -411,17 +443,21 @@ def dcp_tree_attn(kind, q, kv_cache, block_tables, seq_lens, tree_mask, dcp_size
     seq_lens count the nodes, which sit in a request's last q_lens positions (None: Lq each).
     tree_mask int32 [B or 1][Lq][ceil(Lq / 32)]: bit j % 32 of word j / 32 of row i set where node i
     sees node j; the context is seen by all (``tree_mask`` of this module packs parents)."""
-    what = "dcp_tree_attn"
-    _need(q.dim() == 4, f"{what}: q is [batch][Lq][Hq][Dqk]")
+    call = "dcp_tree_attn"
+    if q.dim() != 4:
+        _refuse(call, "q is [batch][Lq][Hq][Dqk]")
     B, Lq, Hq, Dqk = q.shape
-    kind, hkv, dim, bs, nb, max_lb = _cache_fields(what, kind, kv_cache, block_tables, B, dcp_size)
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
     words = (Lq + 31) // 32
-    _need(dim == Dqk, f"{what}: q and the cache differ in their head dim")
-    _need(tree_mask.dim() == 3 and tree_mask.shape[0] in (1, B) and tree_mask.shape[1:] == (Lq, words),
-          f"{what}: tree_mask is [batch or 1][Lq][ceil(Lq / 32)]")
-    _need_tensors(what, torch.bfloat16, q, kv_cache)
-    _need_tensors(what, torch.int32, block_tables, seq_lens, q_lens, tree_mask)
-    _need_lens(what, B, seq_lens, q_lens)
+    if dim != Dqk:
+        _refuse(call, "q and the cache differ in their head dim")
+    trees = tree_mask.shape
+    if len(trees) != 3 or trees[0] not in (1, B) or trees[1] != Lq or trees[2] != words:
+        _refuse(call, "tree_mask is [batch or 1][Lq][ceil(Lq / 32)]")
+    device = torch.cuda.current_device()
+    _check_tensors(call, torch.bfloat16, device, (q, kv_cache))
+    _check_tensors(call, torch.int32, device, (block_tables, seq_lens, q_lens, tree_mask))
+    _check_lens(call, B, (seq_lens, q_lens))
     desc = _cached_desc(kind, B, Lq, Hq, hkv, Dqk, head_dim_v, bs, nb, max_lb)
     if partial_out is None or lse is None or workspace is None:
         # allocated for the stream that the kernels run on
@@ -430,20 +466,24 @@ def dcp_tree_attn(kind, q, kv_cache, block_tables, seq_lens, tree_mask, dcp_size
                 partial_out = torch.empty((dcp_size, B, Lq, Hq, head_dim_v), dtype=torch.float32, device=q.device)
             if lse is None:
                 lse = torch.empty((dcp_size, B, Lq, Hq), dtype=torch.float32, device=q.device)
-            size = dcp_tree_attn_workspace_size(desc, dcp_size)
+            size = int(_lib.dcp_tree_attn_workspace_size(desc, dcp_size))
             if workspace is None and size:
                 workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
-    _need_tensors(what, torch.float32, partial_out, lse)
-    _need(partial_out.numel() == dcp_size * B * Lq * Hq * head_dim_v and lse.numel() == dcp_size * B * Lq * Hq,
-          f"{what}: partial_out is [N][B][Lq][Hq][Dv] and lse [N][B][Lq][Hq]")
+    _check_tensors(call, torch.float32, device, (partial_out, lse))
+    if partial_out.numel() != dcp_size * B * Lq * Hq * head_dim_v or lse.numel() != dcp_size * B * Lq * Hq:
+        _refuse(call, "partial_out is [N][B][Lq][Hq][Dv] and lse [N][B][Lq][Hq]")
     ws_bytes = 0
     if workspace is not None:
-        _need(workspace.get_device() == q.get_device() and workspace.is_contiguous(), f"{what}: workspace")
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            _refuse(call, "the workspace is not contiguous on the current device")
         ws_bytes = workspace.numel() * workspace.element_size()
-    _check(_lib.dcp_tree_attn(desc, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-                              _ptr(q_lens), tree_mask.data_ptr(), Lq * words if tree_mask.shape[0] == B else 0, dcp_size,
-                              interleave, scale, partial_out.data_ptr(), lse.data_ptr(), _ptr(workspace), ws_bytes,
-                              _stream(stream)), what)
+    code = _lib.dcp_tree_attn(
+        desc, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        None if q_lens is None else q_lens.data_ptr(), tree_mask.data_ptr(), Lq * words if trees[0] == B else 0, dcp_size,
+        interleave, scale, partial_out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        ws_bytes, _stream(stream))
+    if code != DCP_OK:
+        raise DcpError(code, call)
     return partial_out, lse
 
 
@@ -452,20 +492,24 @@ def dcp_kv_cache_commit(kind, kv_cache, block_tables, seq_lens, q_len, accepted,
     """Move the cache rows of each request's accepted nodes (accepted int32 [B][max_accept], strictly
     increasing, the first num_accepted[b] of them) to the positions right behind its context, in
     place; returns the new lengths int32 [B] (``new_seq_lens`` may be seq_lens itself)."""
-    what = "dcp_kv_cache_commit"
-    _need(accepted.dim() == 2, f"{what}: accepted is [batch][max_accept]")
+    call = "dcp_kv_cache_commit"
+    if accepted.dim() != 2:
+        _refuse(call, "accepted is [batch][max_accept]")
     B, max_accept = accepted.shape
-    kind, hkv, dim, bs, nb, max_lb = _cache_fields(what, kind, kv_cache, block_tables, B, dcp_size)
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
     if new_seq_lens is None:
         with torch.cuda.stream(stream):
             new_seq_lens = torch.empty((B,), dtype=torch.int32, device=kv_cache.device)
-    _need_tensors(what, torch.bfloat16, kv_cache)
-    _need_tensors(what, torch.int32, block_tables, seq_lens, q_lens, accepted, num_accepted, new_seq_lens)
-    _need_lens(what, B, seq_lens, q_lens, num_accepted, new_seq_lens)
-    desc = _cached_desc(kind, B, q_len, hkv, hkv, dim, dim, bs, nb, max_lb)
-    _check(_lib.dcp_kv_cache_commit(desc, kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-                                    _ptr(q_lens), accepted.data_ptr(), num_accepted.data_ptr(), max_accept,
-                                    new_seq_lens.data_ptr(), dcp_size, interleave, _stream(stream)), what)
+    device = torch.cuda.current_device()
+    _check_tensors(call, torch.bfloat16, device, (kv_cache,))
+    _check_tensors(call, torch.int32, device, (block_tables, seq_lens, q_lens, accepted, num_accepted, new_seq_lens))
+    _check_lens(call, B, (seq_lens, q_lens, num_accepted, new_seq_lens))
+    code = _lib.dcp_kv_cache_commit(
+        _cached_desc(kind, B, q_len, hkv, hkv, dim, dim, bs, nb, max_lb), kv_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(),
+        max_accept, new_seq_lens.data_ptr(), dcp_size, interleave, _stream(stream))
+    if code != DCP_OK:
+        raise DcpError(code, call)
     return new_seq_lens
 
 

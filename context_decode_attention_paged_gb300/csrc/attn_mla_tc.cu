@@ -981,74 +981,91 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
       }
     } else if (warp == 1) {
       // ---------------- PV issuer (and TMEM owner) ----------------
-      if (lane == 0 && T > 0) {
-        const uint32_t id_pv = idesc_bf16(128, 256, true);
+      // (both issuers: the whole warp runs the loop on uniform values and one
+      // lane issues, so that an MMA's operands need no move to uniform registers)
+      if (T > 0) {
+        constexpr uint32_t id_pv = idesc_bf16(128, 256, true);
+        const bool lead = elect_one();
+        const uint32_t tm = uniform(tmem), ring = uniform(smem_u32(stages));
         bool ok = true;
+        int st = 0;
         for (int t = 0; t < T; ++t) {
-          if (*abort_flag || !mbar_wait(smem_u32(&sm.p_full[t & 1]), (uint32_t)(t >> 1) & 1u, p.wait_ns)) {
+          if (!__all_sync(0xffffffffu,
+                          *abort_flag == 0 && mbar_wait(smem_u32(&sm.p_full[t & 1]), (uint32_t)(t >> 1) & 1u, p.wait_ns))) {
             ok = false;
             break;
           }
-          // the score MMAs of tile t+2 go first (bounded spin on the QK issuer's count)
+          // the score MMAs of tile t+1 go first (bounded spin on the QK issuer's count)
           const int need = min(t + kPvGate, T - 1);
-          const uint64_t g0 = globaltimer_ns();
-          while (*(volatile int*)&sm.qk_issued < need) {
-            if (*abort_flag || globaltimer_ns() - g0 > p.wait_ns) {
-              ok = false;
-              break;
+          if (__any_sync(0xffffffffu, *(volatile int*)&sm.qk_issued < need)) {
+            const uint64_t g0 = globaltimer_ns();
+            while (__any_sync(0xffffffffu, *(volatile int*)&sm.qk_issued < need)) {
+              if (__any_sync(0xffffffffu, *abort_flag != 0 || globaltimer_ns() - g0 > p.wait_ns)) {
+                ok = false;
+                break;
+              }
             }
+            if (!ok) break;
           }
-          if (!ok) break;
           tc_fence_after();
-          const uint8_t* st = stages + (t % kStages) * kStageBytes;
+          const uint32_t vt = ring + st * kStageBytes;
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < kNt / 16; ++k) {
-            const uint64_t bdesc = smem_desc(smem_u32(st + k * 2048), kChunkBytes, 1024, kSw128);
-            mma_ts(tmem + kColO, tmem + kColP + 8 * k, bdesc, id_pv, (t > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kNt / 16; ++k)
+              mma_ts(tm + kColO, tm + kColP + 8 * k, smem_desc(vt + k * 2048, kChunkBytes, 1024, kSw128), id_pv,
+                     (t > 0 || k > 0) ? 1u : 0u);
+            mma_commit(smem_u32(&sm.pv_done[t & 1]));
+            // the score MMAs of tile t completed before its softmax produced P(t)
+            mma_commit(smem_u32(&sm.kv_empty[st]));
           }
-          mma_commit(smem_u32(&sm.pv_done[t & 1]));
-          // the score MMAs of tile t completed before its softmax produced P(t)
-          mma_commit(smem_u32(&sm.kv_empty[t % kStages]));
+          st = st + 1 == kStages ? 0 : st + 1;
         }
         if (!ok) fail();
-        mma_commit(smem_u32(&sm.drain));
+        if (lead) mma_commit(smem_u32(&sm.drain));
         if (!mbar_wait(smem_u32(&sm.drain), 0, p.wait_ns)) fail();
       }
     } else if (warp == 2) {
       // ---------------- score (QK^T) issuer ----------------
-      if (lane == 0 && T > 0) {
-        const uint32_t id_qk = idesc_bf16(128, kNt, false);
+      if (T > 0) {
+        constexpr uint32_t id_qk = idesc_bf16(128, kNt, false);
+        const bool lead = elect_one();
+        const uint32_t tm = uniform(tmem), ring = uniform(smem_u32(stages));
+        const uint32_t ql = uniform(smem_u32(qlat0)), qr = uniform(smem_u32(qrope));
         // the query's shared-memory parts came by TMA (already waited for by
         // the softmax warps before the cluster barrier)
-        bool ok = mbar_wait(smem_u32(&sm.q_full), 0u, p.wait_ns);
+        bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.q_full), 0u, p.wait_ns));
+        int st = 0;
+        uint32_t lap = 0;
         for (int t = 0; t < T && ok; ++t) {
-          const int st = t % kStages;
-          if (*abort_flag || !mbar_wait(smem_u32(&sm.kv_full[st]), (uint32_t)(t / kStages) & 1u, p.wait_ns) ||
-              (t >= 2 && !mbar_wait(smem_u32(&sm.s_free[t & 1]), (uint32_t)((t >> 1) - 1) & 1u, p.wait_ns))) {
+          if (!__all_sync(0xffffffffu,
+                          *abort_flag == 0 && mbar_wait(smem_u32(&sm.kv_full[st]), lap, p.wait_ns) &&
+                              (t < 2 || mbar_wait(smem_u32(&sm.s_free[t & 1]), (uint32_t)((t >> 1) - 1) & 1u, p.wait_ns)))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint8_t* sb = stages + st * kStageBytes;
-          const uint32_t dS = tmem + kColS + 64u * (uint32_t)(t & 1);
+          const uint32_t sb = ring + st * kStageBytes;
+          const uint32_t dS = tm + kColS + 64u * (uint32_t)(t & 1);
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(dS, smem_desc(smem_u32(qlat0 + k * 32), 16, 1024, kSw128),
-                   smem_desc(smem_u32(sb + k * 32), 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              mma_ss(dS, smem_desc(ql + k * 32, 16, 1024, kSw128), smem_desc(sb + k * 32, 16, 1024, kSw128), id_qk,
+                     k > 0 ? 1u : 0u);
 #pragma unroll
-          for (int k = 4; k < 16; ++k) {
-            const uint64_t bdesc = smem_desc(smem_u32(sb + (k >> 2) * kChunkBytes + (k & 3) * 32), 16, 1024, kSw128);
-            mma_ts(dS, tmem + kColQ + 8 * (k - 4), bdesc, id_qk, 1u);
+            for (int k = 4; k < 16; ++k)
+              mma_ts(dS, tm + kColQ + 8 * (k - 4),
+                     smem_desc(sb + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024, kSw128), id_qk, 1u);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mma_ss(dS, smem_desc(qr + k * 32, 16, 512, kSw64),
+                     smem_desc(sb + 4 * kChunkBytes + k * 32, 16, 512, kSw64), id_qk, 1u);
+            mma_commit(smem_u32(&sm.s_full[t & 1]));
+            *(volatile int*)&sm.qk_issued = t;
           }
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            mma_ss(dS, smem_desc(smem_u32(qrope + k * 32), 16, 512, kSw64),
-                   smem_desc(smem_u32(sb + 4 * kChunkBytes + k * 32), 16, 512, kSw64), id_qk, 1u);
-          mma_commit(smem_u32(&sm.s_full[t & 1]));
-          *(volatile int*)&sm.qk_issued = t;
+          if (++st == kStages) st = 0, lap ^= 1u;
         }
         if (!ok) fail();
-        mma_commit(smem_u32(&sm.drain_qk));
+        if (lead) mma_commit(smem_u32(&sm.drain_qk));
         if (!mbar_wait(smem_u32(&sm.drain_qk), 0, p.wait_ns)) fail();
       }
     }

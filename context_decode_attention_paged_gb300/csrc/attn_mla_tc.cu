@@ -58,14 +58,17 @@
 // Every wait is bounded; on expiry the kernel records DCP_ERR_TIMEOUT, drains
 // its own copies and MMAs, frees TMEM and returns.
 //
-// kTree: the drafted-tree form.  A unit is one node, so its mask is the same
-// for every head: a 32-bit word per half tile says which tokens the node sees
-// (all of them in tiles of context keys alone).  Hidden tokens are dropped
-// from the softmax as the tokens past a ragged end are, their value rows are
-// zeroed, and their scores do not reach the exchange's scale; a score that is
-// not finite is sent as a NaN scale, so that the row becomes NaN as the
-// formula has it.  Tiles that the node sees nothing of are possible, so the
-// running reference may stay -inf past the first tile.
+// kTree: the drafted-tree form.  The 128 rows of a unit are as many nodes as
+// fit with all their heads (one node of 128 heads, eight of 16), so a tile of
+// keys serves them all.  Tiles of context keys alone take no mask; in the others
+// a thread has a 32-bit word that says which tokens of its half its row sees.
+// Hidden tokens are dropped from the softmax as the tokens past a ragged end
+// are, and their scores do not reach the exchange's scale; a score that is not
+// finite is sent as a NaN scale, so that the row becomes NaN as the formula has
+// it.  Node values that are not finite would reach every row through the
+// product: such entries are replaced by 0 in shared memory and added in the
+// epilogue to the rows that see them.  Tiles that a row sees nothing of are
+// possible, so its running reference may stay -inf past the first tile.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -144,10 +147,12 @@ template <bool kTree>
 struct KernelParams : MlaParams {};
 template <>
 struct KernelParams<true> : MlaParams {
+  const __nv_bfloat16* kv;
   const uint32_t* mask;
   long long mask_stride;
   const int32_t* q_lens;
   int words;
+  int nodes, groups;            // nodes of a unit, units of a request's nodes
 };
 
 struct Smem {
@@ -175,6 +180,7 @@ struct Smem {
   float rref[2][kHeads];       // R(t) by tile parity
   float lw[2][kHeads];         // final: each warpgroup's row sum
   float rlast[2][kHeads];      // final: the reference of that row sum
+  uint32_t odd[8];             // kTree: node keys whose values are not all finite (bit: key - first node key)
 };
 
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kQRopeBytes + kQLat0Bytes + kScMsgBytes +
@@ -253,14 +259,16 @@ struct Unit {
   int r, b, i_q, s_idx, kb, ke, T;
 };
 
-// kTree: what a unit's node sees
+// kTree: what this thread's row (head h of the unit's node) sees
 template <bool kTree>
 struct View {};
 template <>
 struct View<true> {
   int ctx;                        // context keys of the shard
   long long base;                 // the first node's position
-  const uint32_t* mask_row;       // the mask words of this unit's node
+  const uint32_t* mask_row;       // the mask words of its node (null: no node)
+  int words, nodes;               // words of a mask row, nodes of the unit
+  const __nv_bfloat16* kv;
 };
 
 // valid tokens of tile t in half `half` (tokens [32 half, +32)) of the tile
@@ -269,15 +277,12 @@ __device__ __forceinline__ int valid_of_half(const Unit& u, int t, int half) {
   return min(kHalf, max(0, tv - kHalf * half));
 }
 
-// kTree: bit k set where the node sees token 32 half + k of tile t (whole warp)
+// kTree: bit k set where the row sees token 32 half + k of tile t
 __device__ __forceinline__ uint32_t seen_of_half(const MlaParams& p, const Unit& u, const View<true>& view, int t,
-                                                 int half, int lane) {
+                                                 int half) {
   const int j0 = u.kb + t * kNt + kHalf * half;
   if (j0 + kHalf <= min(view.ctx, u.ke)) return 0xffffffffu;
-  const int jj = j0 + lane;
-  bool sees = jj < u.ke;
-  if (sees && jj >= view.ctx) sees = tree_bit(view.mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - view.base));
-  return __ballot_sync(0xffffffffu, sees);
+  return tree_sees32(view.mask_row, view.words, view.ctx, u.ke, view.base, u.r, p.I, p.N, j0);
 }
 
 // ---------------------------------------------------------------------------
@@ -387,8 +392,8 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     int valid = 0;
     uint32_t seen = 0;
     if constexpr (kTree) {
-      seen = seen_of_half(p, u, view, t, (int)cta, lane);
-      valid = seen == 0xffffffffu ? kHalf : 0;
+      seen = seen_of_half(p, u, view, t, (int)cta);
+      valid = __all_sync(0xffffffffu, seen == 0xffffffffu) ? kHalf : 0;
     } else {
       valid = valid_of_half(u, t, (int)cta);
     }
@@ -503,15 +508,28 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     // rows, so the swizzle does not matter)
     const int tv = min(kNt, u.ke - (u.kb + t * kNt));
     if constexpr (kTree) {
-      const uint32_t s0 = cta == 0 ? seen : seen_of_half(p, u, view, t, 0, lane);
-      const uint32_t s1 = cta == 1 ? seen : seen_of_half(p, u, view, t, 1, lane);
-      if ((s0 & s1) != 0xffffffffu) {
-        // hidden tokens: 8 threads a row, all four chunks
-        uint4* st = reinterpret_cast<uint4*>(stages + (t % kStages) * kStageBytes);
-        for (int row = mt >> 3; row < kNt; row += 16)
-          if (!(((row < kHalf ? s0 : s1) >> (row & 31)) & 1u))
-#pragma unroll
-            for (int c = 0; c < 4; ++c) st[(c * kChunkBytes) / 16 + row * 8 + (mt & 7)] = make_uint4(0u, 0u, 0u, 0u);
+      if (u.kb + (t + 1) * kNt > min(view.ctx, u.ke)) {
+        // rows past the range become 0, node rows lose what is not finite: two
+        // threads a row (its score products are done)
+        const int row = mt >> 1, jj = u.kb + t * kNt + row;
+        if (jj >= view.ctx || jj >= u.ke) {
+          uint8_t* v = stages + (t % kStages) * kStageBytes + row * 128;
+          bool odd = false;
+#pragma unroll 2
+          for (int i = 0; i < 16; ++i) {
+            uint4* piece = reinterpret_cast<uint4*>(v + (2 * (mt & 1) + (i >> 3)) * kChunkBytes + ((i ^ row) & 7) * 16);
+            if (jj >= u.ke) {
+              *piece = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              uint4 x = *piece;
+              if (drop_non_finite(x)) *piece = x, odd = true;
+            }
+          }
+          if (odd) {
+            const int bit = jj - max(u.kb, view.ctx);
+            atomicOr(&sm.odd[bit >> 5], 1u << (bit & 31));
+          }
+        }
         fence_proxy_async_smem();
       }
     } else if (tv < kNt) {
@@ -565,6 +583,74 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
   }
   // (kTree: a NaN sum makes a NaN row)
   const float inv = (kTree ? !(l_tot == 0.f) : l_tot > 0.f) ? 1.f / l_tot : 0.f;
+  if constexpr (kTree) {
+    // output row of MMA row hr: node i_q + hr / Hq, head hr % Hq; -1: no such node
+    auto row_of = [&](int hr) -> long long {
+      const int node = u.i_q + hr / p.Hq;
+      if (hr >= view.nodes * p.Hq || node >= p.Lq) return -1;
+      return ((((long long)u.r * p.B + u.b) * p.Lq + node) * p.n_split + u.s_idx) * p.Hq + hr % p.Hq;
+    };
+    const bool live = have && view.mask_row != nullptr;       // (a row without a node gives 0 and -inf)
+    if (have) {
+      bool any_odd = false;
+      for (int k = 0; k < 8; ++k) any_odd |= sm.odd[k] != 0;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(lane_addr + kColO + 128 * w + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = live ? __float_as_uint(__uint_as_float(v[k]) * inv) : 0u;
+        if (any_odd && live) {
+          // values of nodes that are not finite: added to the rows that see them
+#pragma unroll 1
+          for (int bit = 0; bit < DCP_TREE_MAX_NODES; ++bit) {
+            if (!((sm.odd[bit >> 5] >> (bit & 31)) & 1u)) continue;
+            const int jj = max(u.kb, view.ctx) + bit;
+            if (!tree_bit(view.mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - view.base))) continue;
+            const int blk = p.block_tables[((long long)u.r * p.B + u.b) * p.max_lb + jj / p.bs];
+            const __nv_bfloat16* vr = view.kv + ((long long)blk * p.bs + jj % p.bs) * kDqk + 256 * cta + 128 * w + c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float e = __bfloat162float(vr[k]);
+              if (!(fabsf(e) < INFINITY)) v[k] = __float_as_uint(__uint_as_float(v[k]) + e);
+            }
+          }
+        }
+        uint8_t* row = stages + (4 * w + c / 32) * kOBoxBytes + h * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(row + ((k ^ (h & 7)) << 4)) =
+              make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(kBarEpi, 256);
+      if (w == 0 && lg == 0 && lane == 0) {
+        // Hq rows a node and box (the rows of a node start at a multiple of 8 when there are several)
+#pragma unroll 1
+        for (int j = 0; j < view.nodes && u.i_q + j < p.Lq; ++j)
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k)
+            tma_store_2d(&tm_out, smem_u32(stages + k * kOBoxBytes + j * p.Hq * 128), 256 * (int)cta + 32 * k,
+                         (int32_t)row_of(j * p.Hq));
+        bulk_commit();
+        bulk_wait_read0();
+      }
+    } else {
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int hr = 16 * (4 * w + lg); hr < 16 * (4 * w + lg) + 16; ++hr) {
+        const long long to = row_of(hr);
+        if (to < 0) continue;
+        float4* g = reinterpret_cast<float4*>(p.dst_o + to * kDv + 256 * cta);
+        g[lane] = z;
+        g[32 + lane] = z;
+      }
+    }
+    const long long to = row_of(h);
+    if (cta == 0 && w == 0 && to >= 0)
+      p.dst_lse[to] = (live && !(l_tot == 0.f)) ? (r_fin + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
+    return;
+  }
   const long long row0 = ((((long long)u.r * p.B + u.b) * p.Lq + u.i_q) * p.n_split + u.s_idx) * p.Hq;
   if (have) {
     // this CTA's 256 output dims of head h, scaled by 1 / l, into shared
@@ -608,7 +694,7 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     }
   }
   if (cta == 0 && w == 0 && h < p.Hq)
-    p.dst_lse[row0 + h] = (have && (kTree ? !(l_tot == 0.f) : l_tot > 0.f)) ? (r_fin + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
+    p.dst_lse[row0 + h] = (have && l_tot > 0.f) ? (r_fin + log2f(l_tot)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -644,8 +730,8 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
     // columns past the end of a ragged tile hold scores of stale cache rows:
     // zero them so they cannot set the scale (the peer masks them anyway)
     if constexpr (kTree) {
-      const uint32_t seen = seen_of_half(p, u, view, t, (int)peer, lane);
-      if (seen != 0xffffffffu) {
+      const uint32_t seen = seen_of_half(p, u, view, t, (int)peer);
+      if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           if (!((seen >> k) & 1u)) v[k] = 0u;
@@ -734,6 +820,10 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
   }
 }
 
+// Units of a request's queries in a shard and KV split.
+__device__ __forceinline__ int row_units(const KernelParams<false>& p) { return p.Lq; }
+__device__ __forceinline__ int row_units(const KernelParams<true>& p) { return p.groups; }
+
 template <bool kLpt, bool kSmallBlocks, bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
@@ -760,7 +850,7 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
   const long long unit = blockIdx.x >> 1;
   int b_lpt = 0;
   if (kLpt) {
-    const long long per_req = (long long)p.N * p.Lq * p.n_split;
+    const long long per_req = (long long)p.N * row_units(p) * p.n_split;
     const int k_req = (int)(unit / per_req);
     if (p.order != nullptr && tid == 0) sm.req = p.order[k_req];
     for (int j = tid; p.order == nullptr && j < p.B; j += kThreads) {
@@ -779,10 +869,11 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
   Unit u;
   {
     // 32-bit index arithmetic (the launcher keeps units below 2^31)
-    const unsigned un = (unsigned)unit, per_q = (unsigned)(p.n_split * p.Lq);
+    const unsigned un = (unsigned)unit, per_q = (unsigned)(p.n_split * row_units(p));
     const unsigned rest = kLpt ? un % ((unsigned)p.N * per_q) : un;
     u.s_idx = (int)(rest % (unsigned)p.n_split);
-    u.i_q = (int)((rest / (unsigned)p.n_split) % (unsigned)p.Lq);
+    u.i_q = (int)((rest / (unsigned)p.n_split) % (unsigned)row_units(p));
+    if constexpr (kTree) u.i_q *= p.nodes;                   // the unit's first node
     u.b = kLpt ? b_lpt : (int)((un / per_q) % (unsigned)p.B);
     u.r = kLpt ? (int)(rest / per_q) : (int)(un / (per_q * (unsigned)p.B));
   }
@@ -835,7 +926,13 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
     vis = u.i_q < tree.n ? L : 0;          // rows behind the request's nodes see nothing
     view.base = tree.base;
     view.ctx = local_count_upto(tree.base - 1, u.r, p.I, p.N);
-    view.mask_row = p.mask + u.b * p.mask_stride + (long long)u.i_q * p.words;
+    const int h = tid & 127, node = u.i_q + h / p.Hq;
+    view.mask_row = h < p.nodes * p.Hq && node < tree.n
+                        ? p.mask + u.b * p.mask_stride + (long long)node * p.words : nullptr;
+    view.words = p.words;
+    view.nodes = p.nodes;
+    view.kv = p.kv;
+    if (tid < 8) sm.odd[tid] = 0;
   } else {
     vis = bad_len ? 0 : min(L, local_count_upto((long long)S - p.Lq + u.i_q, u.r, p.I, p.N));
   }
@@ -1118,8 +1215,16 @@ bool mla_tc_supported(const AttnArgs& a) {
          (long long)a.num_blocks * a.bs < (1LL << 31);
 }
 
+// Nodes of one unit of a drafted-tree call: as many as fill the 128 MMA rows
+// with their heads.  Their output rows leave shared memory by TMA from multiples
+// of 8 rows, so other head counts take one node a unit.
+static int tree_nodes(const AttnArgs& a) {
+  return a.tree_words > 0 && a.Hq % 8 == 0 ? kHeads / a.Hq : 1;
+}
+
 SplitPlan plan_attn_mla_tc(const AttnArgs& a, int sm_count) {
-  SplitPlan pl = plan_splits(a, sm_count, kNt, 2 * a.Lq);
+  const int nodes = tree_nodes(a);
+  SplitPlan pl = plan_splits(a, sm_count, kNt, 2 * ((a.Lq + nodes - 1) / nodes));
   if (a.B > kLptMaxBatch && a.B <= kLptOrderMaxBatch) {
     pl.lpt_order = true;
     pl.order_offset = (pl.ws_bytes + 255) & ~size_t(255);
@@ -1164,6 +1269,9 @@ static cudaError_t launch_mla(const AttnArgs& a, const SplitPlan& plan) {
   p.split_tokens = plan.split_tokens;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   if constexpr (kTree) {
+    p.kv = static_cast<const __nv_bfloat16*>(a.kv);
+    p.nodes = tree_nodes(a);
+    p.groups = (a.Lq + p.nodes - 1) / p.nodes;
     p.mask = a.tree_mask;
     p.mask_stride = a.tree_mask_stride;
     p.q_lens = a.q_lens;
@@ -1182,9 +1290,10 @@ static cudaError_t launch_mla(const AttnArgs& a, const SplitPlan& plan) {
   }
   // the fp32 output rows [units x Hq][512], stored in 32-dim x Hq-row boxes
   // (row coordinates are 32-bit)
-  const long long units = (long long)a.N * a.B * a.Lq * plan.n_split;
+  long long units = (long long)a.N * a.B * a.Lq * plan.n_split;
   if (units == 0) return cudaSuccess;
   if (units * a.Hq >= (1LL << 31)) return cudaErrorInvalidValue;
+  if constexpr (kTree) units = (long long)a.N * a.B * p.groups * plan.n_split;
   CUtensorMap tm_out;
   const uint64_t odims[2] = {(uint64_t)kDv, (uint64_t)a.N * a.B * a.Lq * plan.n_split * a.Hq};
   const uint64_t ostrides[1] = {(uint64_t)kDv * 4};

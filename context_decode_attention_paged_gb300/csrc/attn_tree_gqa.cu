@@ -177,42 +177,6 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   return d;
 }
 
-// The 64 visibility bits of one row for the keys [j0, j0 + 64): context keys,
-// and nodes whose bit the row's mask has (row null: none).  A shard's keys come
-// in runs of I consecutive positions, so the bits of a run are one cut out of
-// the mask words.
-__device__ __forceinline__ void visibility(const Params& p, const Unit& u, int j0, const uint32_t* row,
-                                           uint32_t (&vis)[2]) {
-  const int c = min(max(u.ctx - j0, 0), kNs), e = min(max(u.ke - j0, 0), kNs);   // context below c, nodes in [c, e)
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int cw = min(max(min(c, e) - 32 * w, 0), 32);
-    vis[w] = cw == 32 ? 0xffffffffu : (1u << cw) - 1u;
-  }
-  int left = 0, node = 0;                    // of the run at k
-  for (int k = c; k < e;) {
-    if (left == 0) {
-      const int jj = j0 + k;
-      node = (int)(global_pos(jj, u.r, p.I, p.N) - u.base);
-      left = p.N == 1 ? e - k : min(p.I - jj % p.I, e - k);
-    }
-    const int len = min(left, 32 - (k & 31));
-    if (row != nullptr) {
-      const int wi = node >> 5;
-      const uint32_t lo = __ldg(row + wi), hi = wi + 1 < p.words ? __ldg(row + wi + 1) : 0u;
-      uint32_t bits = __funnelshift_r(lo, hi, node & 31);
-      if (len < 32) bits &= (1u << len) - 1u;
-      bits <<= k & 31;
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (w == k >> 5) vis[w] |= bits;
-    }
-    k += len;
-    node += len;
-    left -= len;
-  }
-}
-
 // Keep non-finite values out of the product: half `hf` of the row of key j at
 // `v` (chunks of 64 dims, 128-byte rows).  Past the range the row becomes 0; a
 // node's row loses the entries that are not finite and is marked.
@@ -232,14 +196,7 @@ __device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t
       if ((x.x | x.y | x.z | x.w) != 0u) *p = make_uint4(0u, 0u, 0u, 0u);
       continue;
     }
-    uint32_t* w = &x.x;
-    bool touched = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, touched = true;
-      if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu, touched = true;
-    }
-    if (touched) *p = x, odd = true;
+    if (drop_non_finite(x)) *p = x, odd = true;
   }
   if (odd) {
     const int bit = jj - max(u.kb, u.ctx);
@@ -294,15 +251,16 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
     const int j0 = u.key(w, s);
     if (j0 > plain) {
       // nodes or the end of the range
-      uint32_t vis[2];
-      visibility(p, u, j0, mask_of(), vis);
+      const uint32_t* mask_row = mask_of();
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (__any_sync(0xffffffffu, vis[c] != 0xffffffffu)) {
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t sees = tree_sees32(mask_row, p.words, u.ctx, u.ke, u.base, u.r, p.I, p.N, j0 + 32 * c);
+        if (__any_sync(0xffffffffu, sees != 0xffffffffu)) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (!((vis[c] >> k) & 1u)) x[32 * c + k] = 0xff800000u;
+            if (!((sees >> k) & 1u)) x[32 * c + k] = 0xff800000u;
         }
+      }
       // the values, before this stream's product reads them (on a tile that
       // both streams use, each cleans it: the second finds nothing to do)
       const int at = (s | 1), slot = u.slot(w, at, p.slots);

@@ -79,6 +79,12 @@ CASES = [
     ("mla_32", 70, dict(batch=1, num_q_heads=16, lengths=("fixed", 600), dcp_size=2), {}),
     ("mla_32", 11, dict(batch=2, num_q_heads=32, lengths=("uniform", 30, 600), dcp_size=2), {}),
     ("mla_32", 3, dict(batch=2, num_q_heads=48, lengths=("uniform", 30, 600), dcp_size=2), {}),
+    ("mla_32", 20, dict(batch=2, num_q_heads=16, lengths=("uniform", 30, 600), dcp_size=2, interleave=1),
+     dict(mask="random", q_lens=[20, 9])),                                          # eight nodes a unit, partly there
+    ("mla_32", 9, dict(batch=2, num_q_heads=64, lengths=("uniform", 9, 600), dcp_size=4, interleave=3),
+     dict(mask="random")),                                                          # two nodes a unit
+    ("mla_32", 7, dict(batch=3, num_q_heads=20, lengths=("uniform", 30, 600), dcp_size=2), {}),   # not a multiple of 8
+    ("mla_32", 40, dict(batch=1, num_q_heads=16, lengths=("fixed", 20000), dcp_size=1), {}),      # KV splits
     ("mla_32", 5, dict(batch=2, num_q_heads=4, lengths=("uniform", 30, 300), dcp_size=2), {}),     # CUDA-core kernel
     ("mla_32", 7, dict(batch=2, block_size=16, lengths=("uniform", 100, 700), dcp_size=2, interleave=16), {}),
     ("mla_32", 7, dict(batch=2, block_size=64, lengths=("uniform", 100, 700), dcp_size=2, interleave=1), {}),
@@ -113,6 +119,7 @@ SPECIAL = [
     ("qwen_gqa", 20, dict(batch=1, lengths=("fixed", 500), dcp_size=1)),
     ("mla_32", 6, dict(batch=1, lengths=("fixed", 300), dcp_size=2, interleave=1)),
     ("mla_32", 12, dict(batch=1, num_q_heads=32, lengths=("fixed", 300), dcp_size=1)),
+    ("mla_32", 12, dict(batch=1, num_q_heads=16, lengths=("fixed", 300), dcp_size=2, interleave=1)),
 ]
 
 

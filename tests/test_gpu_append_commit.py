@@ -41,6 +41,8 @@ ROPES = {
     "half_part": dict(rot_dim=32, rot_offset=16),
     "half_odd_offset": dict(rot_dim=20, rot_offset=6),          # value by value
     "half_short": dict(rot_dim=8),                              # half a vector of pairs: value by value
+    "half_three": dict(rot_dim=48),                             # three vectors: one block a token
+    "inter_three": dict(rot_dim=24, rot_offset=16, layout="interleaved"),
     "inter": dict(rot_dim=64, layout="interleaved"),
     "inter_part": dict(rot_dim=24, rot_offset=8, layout="interleaved"),
     "inter_odd": dict(rot_dim=2, rot_offset=5, layout="interleaved"),
@@ -128,6 +130,27 @@ def test_append_trees_of_different_sizes(name, kw, rope, shared):
     rng = np.random.default_rng(4)
     offsets = rng.integers(0, 5, size=(1 if shared else 4, 6)).tolist()
     _append(inst, 6, rope, q_lens=[6, 0, 1, 5], offsets=offsets)
+
+
+def test_append_many_tokens_of_ragged_requests():
+    """More tasks than the SMs hold at once: the blocks number them over the tokens that are there
+    (empty requests among them, a bad one reported and skipped)."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    inst = H.build_instance(H.small("tiny_gqa", batch=9, num_q_heads=64, num_kv_heads=8, lengths=("fixed", 700),
+                                    dcp_size=2))
+    lens = [500, 0, 1, 700, 33, 0, 256, 700, 0]
+    _append(inst, 700, dict(rot_dim=64), q_lens=lens)
+    w = inst.w
+    k, v, q = T.append_inputs(w, 700, 5)
+    ql = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ql[3] = 701
+    kv = inst.kv_cache.cuda()
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    dcp.dcp_kv_cache_append(w.kind, T.to_gpu(k), T.to_gpu(v), kv, inst.block_tables.cuda(), inst.seq_lens.cuda(),
+                            w.dcp_size, w.interleave, dcp.dcp_rope_table(64), q=T.to_gpu(q), q_out=out, q_lens=ql)
+    assert dcp.dcp_get_last_device_status() == dcp.DCP_ERR_BOUNDS
+    assert (out[3] == 7).all() and (out[0, 500:] == 7).all() and not (out[0, :500] == 7).all(dim=-1).any()
+    assert not (out[7] == 7).all(dim=-1).any() and not (out[2, 0] == 7).all(dim=-1).any()
 
 
 def test_append_far_and_negative_positions_keep_their_angle():

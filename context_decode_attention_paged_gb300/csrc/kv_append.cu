@@ -156,10 +156,20 @@ __device__ __forceinline__ long long cell_of(const AppendArgs& a, int b, long lo
 // A warp copies n vectors, vector c from src + at(c) to dst + at(c).
 template <typename At>
 __device__ __forceinline__ void copy_vectors(const uint4* src, uint4* dst, int n, int lane, At at) {
-  for (int c = lane; c < n; c += 32 * kCopies) {
-    uint4 v[kCopies];
-    int off[kCopies];
-    // (past the end the last vector again: the same value to the same place)
+  uint4 v[kCopies];
+  int off[kCopies];
+  int c = lane;
+  for (; c + 32 * (kCopies - 1) < n; c += 32 * kCopies) {
+#pragma unroll
+    for (int m = 0; m < kCopies; ++m) {
+      off[m] = at(c + 32 * m);
+      v[m] = src[off[m]];
+    }
+#pragma unroll
+    for (int m = 0; m < kCopies; ++m) dst[off[m]] = v[m];
+  }
+  if (c < n) {
+    // past the end the last vector again: the same value to the same place
 #pragma unroll
     for (int m = 0; m < kCopies; ++m) {
       off[m] = at(min(c + 32 * m, n - 1));

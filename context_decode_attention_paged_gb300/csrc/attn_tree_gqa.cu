@@ -87,7 +87,8 @@ struct Params {
   int* status;
   int B, Lq, Hq, Hkv, N, I, max_lb, bs, num_blocks, n_split, split_tokens, words;
   int row_blocks, block_rows;      // row blocks of a KV head and their rows (128 or 256)
-  int slots;
+  bool turns;                      // 128 rows: the streams take the key tiles in turn
+  int units, slots, q_bytes;
   float scale_log2;
   unsigned long long wait_ns;
   int skip_tile;
@@ -98,8 +99,8 @@ struct Unit {
   int b, r, g, s_idx;
   int row0, R, R_out;      // first row, rows that attend, rows to write
   int kb, ke, ctx;         // keys [kb, ke), context keys of the shard
-  int T;                   // key tiles
-  bool turns;              // the streams take the tiles in turn
+  int L, T;                // keys of the shard, key tiles of the unit
+  bool turns, bad;
   long long base;
   // key tile n of stream w, how many it has, and its steps (the last half tile may be empty)
   __device__ __forceinline__ int tile(int w, int n) const { return turns ? 2 * n + w : n; }
@@ -110,39 +111,76 @@ struct Unit {
   }
   // first key of step s
   __device__ __forceinline__ int key(int w, int s) const { return kb + tile(w, s >> 1) * kNt + (s & 1) * kNs; }
-  // Ring: a stream's tile n uses items 2 n (K) and 2 n + 1 (V).  In turn each
-  // stream has half of the slots to itself, else both read every item, so that
-  // a stream that waits for an item has consumed the slot's last one (a barrier
-  // a whole lap ahead of its waiter would look complete).
-  __device__ __forceinline__ int len(int slots) const { return turns ? slots / 2 : slots; }
-  __device__ __forceinline__ int slot(int w, int at, int slots) const {
-    return turns ? w * (slots / 2) + at % (slots / 2) : at % slots;
-  }
-  __device__ __forceinline__ uint32_t lap(int at, int slots) const { return (uint32_t)(at / len(slots)); }
+};
+
+// Ring.  A tile is two items, K then V, numbered through the CTA's units.  In
+// turn each stream has its own items in its half of the slots, else both read
+// every item: either way a stream that waits for an item has consumed the last
+// one in that slot (a barrier a whole lap behind its waiter would look done).
+struct Ring {
+  int first, len;          // slots of the stream
+  __device__ __forceinline__ Ring(const Params& p, int w)
+      : first(p.turns ? w * (p.slots / 2) : 0), len(p.turns ? p.slots / 2 : p.slots) {}
+  __device__ __forceinline__ int slot(unsigned item) const { return first + (int)(item % (unsigned)len); }
+  __device__ __forceinline__ uint32_t lap(unsigned item) const { return item / (unsigned)len; }
 };
 
 struct Smem {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], q_full, drain[2];   // [stream][step parity]
+  uint64_t unit_full[2], unit_free[2];
   uint32_t tmem_base;
   int abort;
-  int req;
-  Unit unit;                       // for the streams: read where it is needed, to save registers
-  uint32_t odd[8];                 // node keys of this unit whose values are not all finite (bit: key - first)
-  int heavy[2][2];                 // per stream and step parity: the last step with a heavy probability
+  Unit unit[2];                    // by turns: the unit at hand and the next
+  uint32_t odd[2][8];              // node keys of the unit whose values are not all finite (bit: key - first)
+  unsigned heavy[2][2];            // per stream and step parity: 1 + the last step with a heavy probability
+  uint8_t order[kLptMaxBatch];     // requests, longest first
 };
+
+// Unit n of this CTA, -1 past the last.  CTAs take the units back and forth, so
+// that each gets long and short ones.
+__device__ __forceinline__ int unit_of(const Params& p, int n) {
+  const long long at = (long long)n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  return at < p.units ? (int)at : -1;
+}
+
+__device__ __forceinline__ Unit make_unit(const Params& p, const Smem& sm, int unit) {
+  Unit u;
+  const int per_req = p.N * p.Hkv * p.row_blocks * p.n_split;       // (units fit in 32 bits)
+  const int k_req = unit / per_req, rest = unit % per_req;
+  u.b = p.B <= kLptMaxBatch ? sm.order[k_req] : k_req;
+  u.s_idx = rest % p.n_split;
+  const int mb = rest / p.n_split % p.row_blocks;
+  u.g = rest / (p.n_split * p.row_blocks) % p.Hkv;
+  u.r = rest / (p.n_split * p.row_blocks * p.Hkv);
+  const int gsize = p.Hq / p.Hkv;
+  const TreeReq tr = tree_request(p.seq_lens, p.q_lens, p.Lq, u.b);
+  u.base = tr.base;
+  u.turns = p.turns;
+  u.row0 = mb * p.block_rows;
+  u.R_out = min(p.block_rows, p.Lq * gsize - u.row0);
+  u.R = min(max(tr.n * gsize - u.row0, 0), u.R_out);
+  u.L = tr.bad ? 0 : local_len(p.seq_lens[u.b], u.r, p.I, p.N);
+  u.bad = tr.bad || (long long)u.L > (long long)p.max_lb * p.bs;     // (a short table: what it has)
+  u.L = (int)min((long long)u.L, (long long)p.max_lb * p.bs);
+  u.ctx = local_count_upto(tr.base - 1, u.r, p.I, p.N);
+  u.kb = min(u.L, u.s_idx * p.split_tokens);
+  u.ke = min(u.L, u.kb + p.split_tokens);
+  u.T = u.R > 0 ? (u.ke - u.kb + kNt - 1) / kNt : 0;
+  return u;
+}
 
 template <int D>
 constexpr size_t tile_bytes() { return (size_t)kNt * D * 2; }
 
 template <int D>
-size_t smem_bytes(int q_tiles, int slots) {
-  return 1024 + (q_tiles + slots) * tile_bytes<D>() + sizeof(Smem) + 16;
+size_t smem_bytes(int q_bytes, int slots) {
+  return 1024 + q_bytes + slots * tile_bytes<D>() + sizeof(Smem) + 16;
 }
 
 template <int D>
-int ring_slots(int q_tiles) {
-  const int n = (int)((kSmemLimit - smem_bytes<D>(q_tiles, 0)) / tile_bytes<D>());
+int ring_slots(int q_bytes) {
+  const int n = (int)((kSmemLimit - smem_bytes<D>(q_bytes, 0)) / tile_bytes<D>());
   return std::min(n, kMaxSlots);
 }
 
@@ -181,7 +219,7 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 // `v` (chunks of 64 dims, 128-byte rows).  Past the range the row becomes 0; a
 // node's row loses the entries that are not finite and is marked.
 template <int D>
-__device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t* v, int jj, int hf) {
+__device__ __forceinline__ void clean_value_row(const Unit& u, uint32_t* odd_keys, uint8_t* v, int jj, int hf) {
   const bool past = jj >= u.ke;
   if (!past && jj < u.ctx) return;
   bool odd = false;
@@ -200,15 +238,21 @@ __device__ __forceinline__ void clean_value_row(const Unit& u, Smem& sm, uint8_t
   }
   if (odd) {
     const int bit = jj - max(u.kb, u.ctx);
-    atomicOr(&sm.odd[bit >> 5], 1u << (bit & 31));
+    atomicOr(&odd_keys[bit >> 5], 1u << (bit & 31));
   }
 }
 
-// Softmax of one stream (128 threads, thread = row), and its share of the output.
+// What a stream's softmax carries from unit to unit.
+struct StreamState {
+  unsigned item = 0, step = 0;     // ring items and steps so far
+  uint32_t o_par = 0;              // parity of the next unit's o_full
+};
+
+// Softmax of one stream (128 threads, thread = row) over one unit, and its share
+// of the output; false: the unit was aborted (its rows are 0 and -inf).
 template <int D>
-__device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring, float* share, uint32_t tmem,
-                                       int warp, int lane) {
-  const Unit& u = sm.unit;
+__device__ __forceinline__ bool stream(const Params& p, Smem& sm, const Unit& u, uint32_t* odd_keys, StreamState& st,
+                                       uint8_t* qs, uint8_t* ring, uint32_t tmem, int warp, int lane) {
   const int w = (warp - 4) >> 2, quad = warp & 3, lrow = quad * 32 + lane;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
   const uint32_t tS = lanes + 128u * w, tO = lanes + kColO + 128u * w;
@@ -229,10 +273,10 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
   bool bad = false;
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
-    const int buf = s & 1;
+    const unsigned gs = st.step + s;
+    const int buf = gs & 1;
     const uint32_t tB = tS + kNs * buf;
-    if (!__all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&sm.s_full[w][buf]), (uint32_t)(s >> 1) & 1u,
-                                                               p.wait_ns))) {
+    if (!__all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&sm.s_full[w][buf]), (gs >> 1) & 1u, p.wait_ns))) {
       bad = true;
       break;
     }
@@ -263,13 +307,15 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
       }
       // the values, before this stream's product reads them (on a tile that
       // both streams use, each cleans it: the second finds nothing to do)
-      const int at = (s | 1), slot = u.slot(w, at, p.slots);
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[slot]), u.lap(at, p.slots) & 1u, p.wait_ns))) {
+      const Ring rg(p, w);
+      const unsigned item = st.item + (unsigned)(s | 1);
+      const int slot = rg.slot(item);
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[slot]), rg.lap(item) & 1u, p.wait_ns))) {
         bad = true;
         break;
       }
       const int k = (s & 1) * kNs + (lrow & 63);
-      clean_value_row<D>(u, sm, ring + slot * tile_bytes<D>() + k * 128, j0 + (lrow & 63), lrow >> 6);
+      clean_value_row<D>(u, odd_keys, ring + slot * tile_bytes<D>() + k * 128, j0 + (lrow & 63), lrow >> 6);
       fence_proxy_async_smem();
     }
     auto f = [&](int k) { return __uint_as_float(x[k]); };
@@ -291,7 +337,7 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
           // O moves with the reference, once the previous product has landed
           // (the one before it did before this step's scores went out, so the
           // parity is unambiguous)
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.pv_done[w]), (uint32_t)(s - 1) & 1u, p.wait_ns))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.pv_done[w]), (gs - 1) & 1u, p.wait_ns))) {
             bad = true;
             break;
           }
@@ -326,7 +372,7 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
       for (int k = 0; k < 32; ++k)
         hi[k] = pack_bf16x2(f(2 * k) - bf16_lo(hi[k]), f(2 * k + 1) - bf16_hi(hi[k]));
       tmem_st32(tB + 32, hi);
-      if (lane == 0) *(volatile int*)&sm.heavy[w][buf] = s;
+      if (lane == 0) *(volatile unsigned*)&sm.heavy[w][buf] = gs + 1;
     }
     tmem_wait_st();
     tc_fence_before();
@@ -337,18 +383,18 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
   }
   bool have = !bad;
   if (have && steps > 0)
-    have = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.o_full[w]), 0u, p.wait_ns));
+    have = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.o_full[w]), st.o_par, p.wait_ns));
   if (!have) {
     set_status(p.status, DCP_ERR_TIMEOUT);
     *abort_flag = 1;
   }
   // one decision for the CTA: every product landed (the query's shared memory
-  // is idle from here on and carries the rows' m and l)
+  // is idle from here on: it carries m and l across the streams, then stages O)
   have = !bar_red_or(kBarEpi, 256, !have);
   tc_fence_after();
-  share[(2 * w) * kNt + lrow] = m;
-  share[(2 * w + 1) * kNt + lrow] = l;
-  named_bar_sync(kBarEpi, 256);
+  st.step += (unsigned)steps;
+  st.item += 2u * (unsigned)u.tiles(w);
+  st.o_par ^= steps > 0 ? 1u : 0u;
 
   const int gsize = p.Hq / p.Hkv;
   const int row = row_of();
@@ -357,7 +403,12 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
   float w0 = 1.f, w1 = 0.f;             // weights of this stream's and the other's O
   const bool other = u.turns && u.steps(w ^ 1) > 0;
   if (u.turns) {
+    float* share = reinterpret_cast<float*>(qs);
+    share[(2 * w) * kNt + lrow] = m;
+    share[(2 * w + 1) * kNt + lrow] = l;
+    named_bar_sync(kBarEpi, 256);
     const float m2 = share[(2 * (w ^ 1)) * kNt + lrow], l2 = share[(2 * (w ^ 1) + 1) * kNt + lrow];
+    named_bar_sync(kBarEpi, 256);
     const float top = fmaxf(m, m2);
     const float ref = top == -INFINITY ? 0.f : top;
     w0 = ex2(m - ref);
@@ -376,78 +427,91 @@ __device__ __forceinline__ void stream(const Params& p, Smem& sm, uint8_t* ring,
     return ((((long long)u.r * p.B + u.b) * p.Lq + i) * p.n_split + u.s_idx) * p.Hq + head;
   };
   bool any_odd = false;
-  for (int k = 0; k < 8; ++k) any_odd |= sm.odd[k] != 0;
+  for (int k = 0; k < 8; ++k) any_odd |= odd_keys[k] != 0;
   const bool writes = row < u.R_out;
   const unsigned long long out = writes ? (unsigned long long)(p.dst_o + dst_row(u.row0 + row) * D) : 0ull;
-  // through 4 KB of the idle ring for 32 dims, so that a row's part goes out as
-  // one 128-byte line (an aborted unit writes zeros from registers: copies may
-  // still land in the ring)
-  uint8_t* mine = ring + (warp - 4) * (D * 128);
-  const int chunks = (u.turns ? D / 2 : D) / 32;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    if (i >= chunks || !have) break;
-    const int c = d0 + 32 * i;
-    uint32_t o[32];
-    if (steps > 0) {
-      tmem_ld32(tO + c, o);
-      tmem_wait_ld();
-    }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) o[k] = live && steps > 0 ? __float_as_uint(__uint_as_float(o[k]) * w0) : 0u;
-    if (other) {
-      uint32_t o2[32];
-      tmem_ld32(tOther + c, o2);
-      tmem_wait_ld();
-      if (live) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), w1, __uint_as_float(o[k])));
-      }
-    }
-    if (any_odd && live) {
-      // values of nodes that are not finite: added to the rows that see them
+  // through 4 KB of the query's memory for 32 dims, so that a row's part goes
+  // out as one 128-byte line; kPass of them at a time
+  const int chunks = (u.turns ? D / 2 : D) / 32, pass = p.q_bytes / (8 * 4096);
+  uint8_t* mine = qs + (warp - 4) * (p.q_bytes / 8);
 #pragma unroll 1
-      for (int bit = 0; bit < DCP_TREE_MAX_NODES; ++bit) {
-        if (!((sm.odd[bit >> 5] >> (bit & 31)) & 1u)) continue;
-        const int jj = max(u.kb, u.ctx) + bit;
-        if (!tree_bit(mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - u.base))) continue;
-        const int blk = p.block_tables[((long long)u.r * p.B + u.b) * p.max_lb + jj / p.bs];
-        const __nv_bfloat16* v = p.v_pool + (((long long)blk * p.bs + jj % p.bs) * p.Hkv + u.g) * D + c;
+  for (int i0 = 0; i0 < chunks; i0 += pass) {
+    if (have) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float e = __bfloat162float(v[k]);
-          if (!(fabsf(e) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + e);
+      for (int j = 0; j < 2; ++j) {
+        if (j >= pass) break;
+        const int c = d0 + 32 * (i0 + j);
+        uint32_t o[32];
+        if (steps > 0) {
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld();
         }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = live && steps > 0 ? __float_as_uint(__uint_as_float(o[k]) * w0) : 0u;
+        if (other) {
+          uint32_t o2[32];
+          tmem_ld32(tOther + c, o2);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), w1, __uint_as_float(o[k])));
+          }
+        }
+        if (any_odd && live) {
+          // values of nodes that are not finite: added to the rows that see them
+#pragma unroll 1
+          for (int bit = 0; bit < DCP_TREE_MAX_NODES; ++bit) {
+            if (!((odd_keys[bit >> 5] >> (bit & 31)) & 1u)) continue;
+            const int jj = max(u.kb, u.ctx) + bit;
+            if (!tree_bit(mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - u.base))) continue;
+            const int blk = p.block_tables[((long long)u.r * p.B + u.b) * p.max_lb + jj / p.bs];
+            const __nv_bfloat16* v = p.v_pool + (((long long)blk * p.bs + jj % p.bs) * p.Hkv + u.g) * D + c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float e = __bfloat162float(v[k]);
+              if (!(fabsf(e) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + e);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(mine + j * 4096 + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
     }
+    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      *reinterpret_cast<uint4*>(mine + i * 4096 + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-          make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-  }
-  __syncwarp();
+    for (int it = 0; it < 8; ++it) {
+      const int rr = it * 4 + (lane >> 3), k = lane & 7;
+      const unsigned long long to = __shfl_sync(0xffffffffu, out, rr);
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int rr = it * 4 + (lane >> 3), k = lane & 7;
-    const unsigned long long to = __shfl_sync(0xffffffffu, out, rr);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      if (i >= chunks || to == 0ull) break;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (have) v = *reinterpret_cast<const uint4*>(mine + i * 4096 + rr * 128 + ((k ^ (rr & 7)) << 4));
-      *reinterpret_cast<uint4*>(reinterpret_cast<float*>(to) + d0 + 32 * i + 4 * k) = v;
+      for (int j = 0; j < 2; ++j) {
+        if (j >= pass || to == 0ull) break;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (have) v = *reinterpret_cast<const uint4*>(mine + j * 4096 + rr * 128 + ((k ^ (rr & 7)) << 4));
+        *reinterpret_cast<uint4*>(reinterpret_cast<float*>(to) + d0 + 32 * (i0 + j) + 4 * k) = v;
+      }
     }
+    __syncwarp();
   }
-  // in turn, a block of 256 rows: the rows of absent nodes behind the first 128
-  for (int rr = kNt + (warp - 4); u.turns && rr < u.R_out; rr += 8) {
-    const long long to = dst_row(u.row0 + rr);
+  if (writes && (!u.turns || w == 0))
+    p.dst_lse[dst_row(u.row0 + row)] = live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  named_bar_sync(kBarEpi, 256);          // the query's memory may be written again
+  return have;
+}
+
+// Zeros and -inf for a unit that is not run (256 threads).
+template <int D>
+__device__ __forceinline__ void write_empty(const Params& p, const Unit& u, int warp, int lane) {
+  const int gsize = p.Hq / p.Hkv;
+  for (int rr = warp - 4; rr < u.R_out; rr += 8) {
+    const int i = (u.row0 + rr) / gsize, head = u.g * gsize + (u.row0 + rr) % gsize;
+    const long long to = ((((long long)u.r * p.B + u.b) * p.Lq + i) * p.n_split + u.s_idx) * p.Hq + head;
     for (int c = 4 * lane; c < D; c += 128)
       *reinterpret_cast<uint4*>(p.dst_o + to * D + c) = make_uint4(0u, 0u, 0u, 0u);
     if (lane == 0) p.dst_lse[to] = -INFINITY;
   }
-  if (writes && (!u.turns || w == 0))
-    p.dst_lse[dst_row(u.row0 + row)] = live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int D>
@@ -456,21 +520,35 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr uint32_t kTile = (uint32_t)tile_bytes<D>();
-  uint8_t* ring = qs + (p.block_rows / kNt) * kTile;
+  uint8_t* ring = qs + p.q_bytes;
   Smem& sm = *reinterpret_cast<Smem*>(ring + p.slots * kTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
+    for (int k = 0; k < p.slots; ++k) {
+      mbar_init(smem_u32(&sm.full[k]), 1);
+      mbar_init(smem_u32(&sm.empty[k]), p.turns ? 1 : 2);   // streams that read the tile
+    }
+    for (int k = 0; k < 2; ++k) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&sm.s_full[k][b]), 1);
+        mbar_init(smem_u32(&sm.p_full[k][b]), 4);    // warps of the stream
+        sm.heavy[k][b] = 0;
+      }
+      mbar_init(smem_u32(&sm.pv_done[k]), 1);
+      mbar_init(smem_u32(&sm.o_full[k]), 1);
+      mbar_init(smem_u32(&sm.drain[k]), 1);
+      mbar_init(smem_u32(&sm.unit_full[k]), 1);
+      mbar_init(smem_u32(&sm.unit_free[k]), 11);     // a producer, two issuers, eight softmax warps
+    }
+    mbar_init(smem_u32(&sm.q_full), 8);
+    sm.abort = 0;
+    fence_mbar_init();
   }
-
-  // units, longest request first (as in the decode kernel)
-  const long long per_req = (long long)p.N * p.Hkv * p.row_blocks * p.n_split;
-  const int k_req = (int)(blockIdx.x / per_req);
-  const long long rest = blockIdx.x % per_req;
-  Unit u;
-  u.b = k_req;
+  if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), 512);
   if (p.B <= kLptMaxBatch) {
+    // units go longest request first: rank the requests by counting
     int* lens = reinterpret_cast<int*>(ring);              // idle until the first load
     const int sj = tid < p.B ? p.seq_lens[tid] : 0;
     if (tid < p.B) lens[tid] = sj;
@@ -482,64 +560,10 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int si = lens[i];
         rank += (si > sj) || (si == sj && i < tid);
       }
-      if (rank == k_req) sm.req = tid;
+      sm.order[rank] = (uint8_t)tid;
     }
     fence_proxy_async_smem();                              // before the loads into the ring
-    __syncthreads();
-    u.b = sm.req;
   }
-  u.s_idx = (int)(rest % p.n_split);
-  const int mb = (int)((rest / p.n_split) % p.row_blocks);
-  u.g = (int)((rest / ((long long)p.n_split * p.row_blocks)) % p.Hkv);
-  u.r = (int)(rest / ((long long)p.n_split * p.row_blocks * p.Hkv));
-  const int gsize = p.Hq / p.Hkv;
-  const TreeReq tr = tree_request(p.seq_lens, p.q_lens, p.Lq, u.b);
-  const int S = p.seq_lens[u.b];
-  u.base = tr.base;
-  u.row0 = mb * p.block_rows;
-  u.R_out = min(p.block_rows, p.Lq * gsize - u.row0);
-  u.R = min(max(tr.n * gsize - u.row0, 0), u.R_out);
-  u.turns = u.R <= kNt;
-  int L = tr.bad ? 0 : local_len(S, u.r, p.I, p.N);
-  const bool short_table = (long long)L > (long long)p.max_lb * p.bs;
-  if (short_table) L = p.max_lb * p.bs;
-  u.ctx = local_count_upto(tr.base - 1, u.r, p.I, p.N);
-  u.kb = min(L, u.s_idx * p.split_tokens);
-  u.ke = min(L, u.kb + p.split_tokens);
-  u.T = u.R > 0 ? (u.ke - u.kb + kNt - 1) / kNt : 0;
-  const int32_t* bt = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
-  {
-    // a block id past the pool among the shard's keys skips the unit
-    bool bad_blk = false;
-    for (int jb = tid; jb < (L + p.bs - 1) / p.bs; jb += kThreads) bad_blk |= (unsigned)bt[jb] >= (unsigned)p.num_blocks;
-    bad_blk = __syncthreads_or(bad_blk);
-    if (bad_blk) u.T = 0;
-    if (tid == 0 && (tr.bad || short_table || bad_blk)) set_status(p.status, DCP_ERR_BOUNDS);
-  }
-
-  if (tid == 0) {
-    for (int k = 0; k < p.slots; ++k) {
-      mbar_init(smem_u32(&sm.full[k]), 1);
-      mbar_init(smem_u32(&sm.empty[k]), u.turns ? 1 : 2);   // streams that read the tile
-    }
-    for (int k = 0; k < 2; ++k) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(smem_u32(&sm.s_full[k][b]), 1);
-        mbar_init(smem_u32(&sm.p_full[k][b]), 4);    // warps of the stream
-        sm.heavy[k][b] = -1;
-      }
-      mbar_init(smem_u32(&sm.pv_done[k]), 1);
-      mbar_init(smem_u32(&sm.o_full[k]), 1);
-    }
-    mbar_init(smem_u32(&sm.q_full), 8);
-    mbar_init(smem_u32(&sm.drain[0]), 1);
-    mbar_init(smem_u32(&sm.drain[1]), 1);
-    sm.abort = 0;
-    fence_mbar_init();
-  }
-  if (tid < 8) sm.odd[tid] = 0;
-  if (tid == 0) sm.unit = u;
-  if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -549,62 +573,111 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     set_status(p.status, DCP_ERR_TIMEOUT);
     *abort_flag = 1;
   };
+  // unit n, once warp 0 has put it there
+  auto unit_ready = [&](int n) {
+    return *abort_flag == 0 && mbar_wait(smem_u32(&sm.unit_full[n & 1]), (uint32_t)(n >> 1) & 1u, p.wait_ns);
+  };
+  auto unit_done = [&](int n) { mbar_arrive(smem_u32(&sm.unit_free[n & 1])); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kCtrlRegs));
-    if ((warp == 0 || warp == 3) && lane == 0 && u.T > 0) {
-      // ---------------- TMA producers ----------------
+    if (warp == 0 || warp == 3) {
+      // ---------------- TMA producers; warp 0 also makes the units ----------------
       // in turn: warp 0 loads stream 0's tiles, warp 3 stream 1's; else warp 0 K, warp 3 V
       const int w = warp == 0 ? 0 : 1;
       const int box_rows = p.bs < kNt ? p.bs : kNt;
-      const int first = u.turns ? 0 : w, by = u.turns ? 1 : 2, items = 2 * u.tiles(w);
-      int at = first;
-      for (; at < items; at += by) {
-        const int slot = u.slot(w, at, p.slots);
-        const uint32_t lap = u.lap(at, p.slots);
-        if (*abort_flag || (lap > 0 && !mbar_wait(smem_u32(&sm.empty[slot]), (lap - 1) & 1u, p.wait_ns))) {
-          fail();
+      const int from = p.turns ? 0 : w, by = p.turns ? 1 : 2;
+      const Ring rg(p, w);
+      unsigned item0 = 0, end = 0;                         // items before this unit; one past the last loaded
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const int index = unit_of(p, n);
+        if (index < 0) break;
+        Unit& u = sm.unit[n & 1];
+        if (warp == 0) {
+          if (n >= 2 && !__all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&sm.unit_free[n & 1]),
+                                                                             (uint32_t)((n >> 1) - 1) & 1u, p.wait_ns))) {
+            ok = false;
+            break;
+          }
+          Unit v = make_unit(p, sm, index);
+          // a block id past the pool among the shard's keys skips the unit
+          const int32_t* bt = p.block_tables + ((long long)v.r * p.B + v.b) * p.max_lb;
+          bool bad_blk = false;
+          for (int jb = lane; jb < (v.L + p.bs - 1) / p.bs; jb += 32) bad_blk |= (unsigned)bt[jb] >= (unsigned)p.num_blocks;
+          bad_blk = __any_sync(0xffffffffu, bad_blk);
+          if (bad_blk) v.T = 0;
+          if (lane < 8) sm.odd[n & 1][lane] = 0;
+          if (lane == 0) {
+            if (v.bad || bad_blk) set_status(p.status, DCP_ERR_BOUNDS);
+            u = v;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.unit_full[n & 1]));
+        } else if (!__all_sync(0xffffffffu, unit_ready(n))) {
+          ok = false;
           break;
         }
-        const int t = u.tile(w, at >> 1);
-        const CUtensorMap* tm = (at & 1) ? &tm_v : &tm_k;
-        const uint32_t full = smem_u32(&sm.full[slot]);
-        if (t == p.skip_tile && !(at & 1)) continue;        // test hook: a tile that never comes
-        uint8_t* dst = ring + slot * kTile;
-        mbar_arrive_expect_tx(full, kTile);
-        for (int k = 0; k < kNt; k += box_rows) {
-          const int j = u.kb + t * kNt + k;
-          // boxes past the key range read pool row 0 (masked, values zeroed)
-          const int row = j < u.ke ? bt[j / p.bs] * p.bs + j % p.bs : 0;
+        const int items = 2 * u.tiles(w);
+        if (lane == 0) {
+          const int32_t* bt = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
+          const int kb = u.kb, ke = u.ke, g = u.g;
+          for (int at = from; at < items; at += by) {
+            const unsigned item = item0 + (unsigned)at;
+            const int slot = rg.slot(item);
+            const uint32_t lap = rg.lap(item);
+            if (*abort_flag || (lap > 0 && !mbar_wait(smem_u32(&sm.empty[slot]), (lap - 1) & 1u, p.wait_ns))) {
+              ok = false;
+              break;
+            }
+            const int t = u.tile(w, at >> 1);
+            if (t == p.skip_tile && !(at & 1)) continue;    // test hook: a tile that never comes
+            const CUtensorMap* tm = (at & 1) ? &tm_v : &tm_k;
+            const uint32_t full = smem_u32(&sm.full[slot]);
+            uint8_t* dst = ring + slot * kTile;
+            mbar_arrive_expect_tx(full, kTile);
+            for (int k = 0; k < kNt; k += box_rows) {
+              const int j = kb + t * kNt + k;
+              // boxes past the key range read pool row 0 (masked, values zeroed)
+              const int row = j < ke ? bt[j / p.bs] * p.bs + j % p.bs : 0;
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem_u32(dst + c * (kNt * 128) + k * 128), tm, 64 * c, u.g, row, full);
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(smem_u32(dst + c * (kNt * 128) + k * 128), tm, 64 * c, g, row, full);
+            }
+            end = item + 1;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        item0 += (unsigned)items;
+        if (warp == 3 && lane == 0) unit_done(n);
+      }
+      if (!ok) fail();
+      if (lane == 0 && *abort_flag) {
+        // let every copy this thread issued land before the CTA exits (the last lap of each slot)
+        for (unsigned back = 1; back <= (unsigned)rg.len && back <= end; ++back) {
+          const unsigned item = end - back;
+          if (p.turns || (item & 1u) == (unsigned)w)
+            mbar_wait(smem_u32(&sm.full[rg.slot(item)]), rg.lap(item) & 1u, p.wait_ns);
         }
       }
-      if (*abort_flag) {
-        // let every copy this thread issued land before the CTA exits (an item's last lap of its slot)
-        for (int back = at - by; back >= first && back > at - by - u.len(p.slots); back -= by)
-          mbar_wait(smem_u32(&sm.full[u.slot(w, back, p.slots)]), u.lap(back, p.slots) & 1u, p.wait_ns);
-      }
-    } else if ((warp == 1 || warp == 2) && u.tiles(warp - 1) > 0) {
+    } else {
+      // ---------------- MMA issuers, warp 1 + w for stream w ----------------
+      // PV(s), then the scores of step s + 2, whose buffer P(s) leaves.  The
+      // whole warp runs the loop on uniform values and one lane issues: with a
+      // single lane in the loop each MMA cost 65-90 clocks to issue, as long as
+      // it runs
       const int w = (int)uniform((uint32_t)warp - 1u);
-      // ---------------- MMA issuer ----------------
-      // one stream's PV(s) and S(s + 1), then the other's: while the tensor
-      // pipe works for one, the other's probabilities are made.  The whole warp
-      // runs the loop on uniform values and one lane issues: with a single
-      // lane in the loop each MMA cost 65-90 clocks to issue, as long as it runs
       constexpr uint32_t id_qk = idesc_bf16(128, kNs, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
-      const bool turns = uniform(u.turns) != 0, lead = elect_one();
-      const int len = (int)uniform((uint32_t)u.len(p.slots));
-      const int steps = (int)uniform((uint32_t)u.steps(w));
+      const bool turns = p.turns, lead = elect_one();
+      const Ring rg(p, w);
+      const int first = (int)uniform((uint32_t)rg.first), limit = first + (int)uniform((uint32_t)rg.len);
       const uint32_t tm = uniform(tmem);
-      const uint32_t ring_addr = uniform(smem_u32(ring)), qs_addr = uniform(smem_u32(qs));
+      const uint32_t ring_addr = uniform(smem_u32(ring)), qt = uniform(smem_u32(qs) + (turns ? 0u : w * kTile));
       const uint32_t full = uniform(smem_u32(&sm.full[0])), empty = uniform(smem_u32(&sm.empty[0]));
-      const uint32_t s_full = uniform(smem_u32(&sm.s_full[0][0])), p_full = uniform(smem_u32(&sm.p_full[0][0]));
-      const uint32_t pv_done = uniform(smem_u32(&sm.pv_done[0])), o_full = uniform(smem_u32(&sm.o_full[0]));
-      // per stream: cursors over the K and the V tiles (slot and lap parity; a
-      // tile serves two steps), as items K V K V ... of its part of the ring
+      const uint32_t s_full = uniform(smem_u32(&sm.s_full[w][0])), p_full = uniform(smem_u32(&sm.p_full[w][0]));
+      const uint32_t pv_done = uniform(smem_u32(&sm.pv_done[w])), o_full = uniform(smem_u32(&sm.o_full[w]));
+      // cursors over the K and the V tiles: slot and lap parity (a tile serves two steps)
       struct Cursor {
         int slot;
         uint32_t par;
@@ -614,83 +687,118 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       };
       auto next = [&](Cursor& c) {          // two items on
         c.slot += 2;
-        if (c.slot >= (turns && w == 1 ? 2 * len : len)) {
-          c.slot -= len;
+        if (c.slot >= limit) {
+          c.slot -= limit - first;
           c.par ^= 1u;
         }
       };
-      // scores of step s into their buffer
-      auto qk = [&](Cursor& c, int s) -> bool {
-        if (!(s & 1) && !wait(full + 8 * c.slot, c.par)) return false;
-        const uint32_t kt = ring_addr + c.slot * kTile + (s & 1) * (kNs * 128), qt = qs_addr + (turns ? 0u : w * kTile);
-        const bool done = (s & 1) || s + 1 == steps;      // the tile's last step
-        if (lead) {
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(tm + 128u * w + kNs * (s & 1), smem_desc(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128),
-                   smem_desc(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
-          mma_commit(s_full + 16 * w + 8 * (s & 1));
-          if (done) mma_commit(empty + 8 * c.slot);
+      Cursor kc = {first, 0u}, vc = {first + 1, 0u};
+      unsigned step0 = 0;                   // steps before this unit
+      uint32_t q_par = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        if (unit_of(p, n) < 0) break;
+        if (!__all_sync(0xffffffffu, unit_ready(n))) {
+          ok = false;
+          break;
         }
-        if (done) next(c);
-        return true;
-      };
-      auto pv = [&](Cursor& c, int s) -> bool {
-        if ((!(s & 1) && !wait(full + 8 * c.slot, c.par)) ||
-            !wait(p_full + 16 * w + 8 * (s & 1), (uint32_t)(s >> 1) & 1u))
-          return false;
-        tc_fence_after();
-        const uint32_t vt = ring_addr + c.slot * kTile + (s & 1) * (kNs * 128), pt = tm + 128u * w + kNs * (s & 1);
-        const bool heavy = __any_sync(0xffffffffu, *(volatile int*)&sm.heavy[w][s & 1] == s);
-        const bool done = (s & 1) || s + 1 == steps;
-        if (lead) {
+        const int steps = (int)uniform((uint32_t)sm.unit[n & 1].steps(w));
+        const bool runs = uniform((uint32_t)sm.unit[n & 1].T) > 0;
+        if (lead) unit_done(n);
+        // scores of step s into their buffer
+        auto qk = [&](int s) -> bool {
+          if (!(s & 1) && !wait(full + 8 * kc.slot, kc.par)) return false;
+          const uint32_t kt = ring_addr + kc.slot * kTile + (s & 1) * (kNs * 128), buf = (step0 + s) & 1u;
+          const bool done = (s & 1) || s + 1 == steps;      // the tile's last step
+          if (lead) {
+            tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < kNs / 16; ++k)
-            mma_ts(tm + kColO + 128u * w, pt + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv,
-                   (s > 0 || k > 0) ? 1u : 0u);
-          if (heavy) {
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tm + 128u * w + kNs * buf, smem_desc(qt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128),
+                     smem_desc(kt + (k >> 2) * (kNt * 128) + (k & 3) * 32, 16, 1024, kSw128), id_qk, k > 0 ? 1u : 0u);
+            mma_commit(s_full + 8 * buf);
+            if (done) mma_commit(empty + 8 * kc.slot);
+          }
+          if (done) next(kc);
+          return true;
+        };
+        auto pv = [&](int s) -> bool {
+          const uint32_t gs = step0 + s, buf = gs & 1u;
+          if ((!(s & 1) && !wait(full + 8 * vc.slot, vc.par)) || !wait(p_full + 8 * buf, (gs >> 1) & 1u)) return false;
+          tc_fence_after();
+          const uint32_t vt = ring_addr + vc.slot * kTile + (s & 1) * (kNs * 128), pt = tm + 128u * w + kNs * buf;
+          const bool heavy = __any_sync(0xffffffffu, *(volatile unsigned*)&sm.heavy[w][buf] == gs + 1);
+          const bool done = (s & 1) || s + 1 == steps;
+          if (lead) {
 #pragma unroll
             for (int k = 0; k < kNs / 16; ++k)
-              mma_ts(tm + kColO + 128u * w, pt + 32 + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv, 1u);
+              mma_ts(tm + kColO + 128u * w, pt + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv,
+                     (s > 0 || k > 0) ? 1u : 0u);
+            if (heavy) {
+#pragma unroll
+              for (int k = 0; k < kNs / 16; ++k)
+                mma_ts(tm + kColO + 128u * w, pt + 32 + 8 * k, smem_desc(vt + k * 2048, kNt * 128, 1024, kSw128), id_pv, 1u);
+            }
+            mma_commit(pv_done);
+            if (s + 1 == steps) mma_commit(o_full);
+            if (done) mma_commit(empty + 8 * vc.slot);
           }
-          mma_commit(pv_done + 8 * w);
-          if (s + 1 == steps) mma_commit(o_full + 8 * w);
-          if (done) mma_commit(empty + 8 * c.slot);
-        }
-        if (done) next(c);
-        return true;
-      };
-      const int at0 = turns && w == 1 ? len : 0;
-      Cursor kc = {at0, 0u}, vc = {at0 + 1, 0u};
-      bool ok = wait(smem_u32(&sm.q_full), 0u) && qk(kc, 0) && (steps < 2 || qk(kc, 1));
-      for (int s = 0; s < steps && ok; ++s) ok = pv(vc, s) && (s + 2 >= steps || qk(kc, s + 2));
+          if (done) next(vc);
+          return true;
+        };
+        if (steps > 0) ok = wait(smem_u32(&sm.q_full), q_par) && qk(0) && (steps < 2 || qk(1));
+        for (int s = 0; s < steps && ok; ++s) ok = pv(s) && (s + 2 >= steps || qk(s + 2));
+        step0 += (unsigned)steps;
+        q_par ^= runs ? 1u : 0u;
+      }
       if (!ok) fail();
       if (lead) mma_commit(smem_u32(&sm.drain[w]));
       if (!mbar_wait(smem_u32(&sm.drain[w]), 0, p.wait_ns)) fail();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
-    if (u.T > 0) {
-      // query rows -> shared memory, K-major with the 128-byte swizzle (rows
-      // past R are zero), while the first tiles are on their way
-      const int rows = u.turns ? kNt : 2 * kNt;
-      constexpr int kPer = D / 8;                          // 16-byte pieces of a row
-      const int c = (tid - 128) % kPer;
-      for (int rr = (tid - 128) / kPer; rr < rows; rr += 256 / kPer) {
-        const int lr = rr & 127;
-        const uint32_t dst = smem_u32(qs + (rr >> 7) * kTile + (c >> 3) * (kNt * 128) + lr * 128 + (((c & 7) ^ (lr & 7)) << 4));
-        // (a row past R: zero bytes from an address inside the query)
-        const int row = rr < u.R ? u.row0 + rr : u.row0;
-        const int i = row / gsize, head = u.g * gsize + row % gsize;
-        cp_async_16(dst, p.q + (((long long)u.b * p.Lq + i) * p.Hq + head) * D + 8 * c, rr < u.R ? 16u : 0u);
+    StreamState st;
+    const int gsize = p.Hq / p.Hkv;
+    bool ok = true;
+    int n = 0;
+    for (; unit_of(p, n) >= 0; ++n) {
+      // (the streams leave the loop together: stream() decides for the CTA)
+      const bool ready = !bar_red_or(kBarEpi, 256, !unit_ready(n));
+      if (!ready) {
+        ok = false;
+        break;
       }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
+      const Unit& u = sm.unit[n & 1];
+      if (u.T > 0) {
+        // query rows -> shared memory, K-major with the 128-byte swizzle (rows
+        // past R are zero), while the first tiles are on their way
+        const int rows = p.turns ? kNt : 2 * kNt;
+        constexpr int kPer = D / 8;                        // 16-byte pieces of a row
+        const int c = (tid - 128) % kPer;
+        for (int rr = (tid - 128) / kPer; rr < rows; rr += 256 / kPer) {
+          const int lr = rr & 127;
+          const uint32_t dst = smem_u32(qs + (rr >> 7) * kTile + (c >> 3) * (kNt * 128) + lr * 128 + (((c & 7) ^ (lr & 7)) << 4));
+          // (a row past R: zero bytes from an address inside the query)
+          const int row = rr < u.R ? u.row0 + rr : u.row0;
+          const int i = row / gsize, head = u.g * gsize + row % gsize;
+          cp_async_16(dst, p.q + (((long long)u.b * p.Lq + i) * p.Hq + head) * D + 8 * c, rr < u.R ? 16u : 0u);
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+      }
+      ok = stream<D>(p, sm, u, sm.odd[n & 1], st, qs, ring, tmem, warp, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+      if (lane == 0) unit_done(n);
+      if (!ok) {
+        ++n;
+        break;
+      }
     }
-    stream<D>(p, sm, ring, reinterpret_cast<float*>(qs), tmem, warp, lane);
+    // after an abort: the CTA's other units are empty
+    if (!ok)
+      for (int index; (index = unit_of(p, n)) >= 0; ++n) write_empty<D>(p, make_unit(p, sm, index), warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -705,10 +813,11 @@ int block_rows_of(const AttnArgs& a) { return rows_of(a) > kNt ? 2 * kNt : kNt; 
 int row_blocks_of(const AttnArgs& a) { return (rows_of(a) + block_rows_of(a) - 1) / block_rows_of(a); }
 
 template <int D>
-cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, Params& p, long long units, cudaStream_t stream) {
-  const int q_tiles = p.block_rows / kNt;
-  p.slots = ring_slots<D>(q_tiles);
-  const size_t smem = smem_bytes<D>(q_tiles, p.slots);
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, Params& p, cudaStream_t stream) {
+  // (the query's memory also stages the output: 4 KB a softmax warp at the least)
+  p.q_bytes = std::max(p.block_rows / kNt * (int)tile_bytes<D>(), 8 * 4096);
+  p.slots = ring_slots<D>(p.q_bytes);
+  const size_t smem = smem_bytes<D>(p.q_bytes, p.slots);
   // the register split assumes the compiled launch count; refuse to launch
   // otherwise (setmaxnreg.inc would wait for registers that do not exist)
   cudaFuncAttributes fa;
@@ -717,7 +826,8 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, Params& p, 
   if (fa.numRegs * kThreads < 128 * kCtrlRegs + 256 * kSoftRegs) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(tree_gqa_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  tree_gqa_kernel<D><<<(unsigned)units, kThreads, smem, stream>>>(tm_k, tm_v, p);
+  const int grid = std::min(p.units, device_sm_count());
+  tree_gqa_kernel<D><<<(unsigned)grid, kThreads, smem, stream>>>(tm_k, tm_v, p);
   return cudaGetLastError();
 }
 
@@ -772,8 +882,9 @@ cudaError_t launch_tree_gqa(const AttnArgs& a, const SplitPlan& plan) {
   }
   const long long units = (long long)a.N * a.B * a.Hkv * p.row_blocks * plan.n_split;
   if (units > INT32_MAX) return cudaErrorInvalidValue;
-  const cudaError_t e = a.Dqk == 128 ? launch<128>(tm_k, tm_v, p, units, a.stream)
-                                     : launch<64>(tm_k, tm_v, p, units, a.stream);
+  p.units = (int)units;
+  p.turns = p.block_rows == kNt;
+  const cudaError_t e = a.Dqk == 128 ? launch<128>(tm_k, tm_v, p, a.stream) : launch<64>(tm_k, tm_v, p, a.stream);
   if (e != cudaSuccess || plan.n_split <= 1) return e;
   return launch_split_combine(a, plan);
 }

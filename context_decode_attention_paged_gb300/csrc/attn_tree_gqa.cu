@@ -430,74 +430,68 @@ __device__ __forceinline__ bool stream(const Params& p, Smem& sm, const Unit& u,
   for (int k = 0; k < 8; ++k) any_odd |= odd_keys[k] != 0;
   const bool writes = row < u.R_out;
   const unsigned long long out = writes ? (unsigned long long)(p.dst_o + dst_row(u.row0 + row) * D) : 0ull;
-  // through 4 KB of the query's memory for 32 dims, so that a row's part goes
-  // out as one 128-byte line; kPass of them at a time
-  const int chunks = (u.turns ? D / 2 : D) / 32, pass = p.q_bytes / (8 * 4096);
-  uint8_t* mine = qs + (warp - 4) * (p.q_bytes / 8);
+  // 32 dims at a time through 4 KB of the query's memory, so that a row's part
+  // goes out as one 128-byte line (a rolled loop: the code runs once a unit, and
+  // fetching it is what it costs)
+  const int chunks = (u.turns ? D / 2 : D) / 32;
+  uint8_t* mine = qs + (warp - 4) * 4096;
 #pragma unroll 1
-  for (int i0 = 0; i0 < chunks; i0 += pass) {
+  for (int i = 0; i < chunks; ++i) {
     if (have) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (j >= pass) break;
-        const int c = d0 + 32 * (i0 + j);
-        uint32_t o[32];
-        if (steps > 0) {
-          tmem_ld32(tO + c, o);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = live && steps > 0 ? __float_as_uint(__uint_as_float(o[k]) * w0) : 0u;
-        if (other) {
-          uint32_t o2[32];
-          tmem_ld32(tOther + c, o2);
-          tmem_wait_ld();
-          if (live) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), w1, __uint_as_float(o[k])));
-          }
-        }
-        if (any_odd && live) {
-          // values of nodes that are not finite: added to the rows that see them
-#pragma unroll 1
-          for (int bit = 0; bit < DCP_TREE_MAX_NODES; ++bit) {
-            if (!((odd_keys[bit >> 5] >> (bit & 31)) & 1u)) continue;
-            const int jj = max(u.kb, u.ctx) + bit;
-            if (!tree_bit(mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - u.base))) continue;
-            const int blk = p.block_tables[((long long)u.r * p.B + u.b) * p.max_lb + jj / p.bs];
-            const __nv_bfloat16* v = p.v_pool + (((long long)blk * p.bs + jj % p.bs) * p.Hkv + u.g) * D + c;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float e = __bfloat162float(v[k]);
-              if (!(fabsf(e) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + e);
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(mine + j * 4096 + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      const int c = d0 + 32 * i;
+      uint32_t o[32];
+      if (steps > 0) {
+        tmem_ld32(tO + c, o);
+        tmem_wait_ld();
       }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = live && steps > 0 ? __float_as_uint(__uint_as_float(o[k]) * w0) : 0u;
+      if (other) {
+        uint32_t o2[32];
+        tmem_ld32(tOther + c, o2);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), w1, __uint_as_float(o[k])));
+        }
+      }
+      if (any_odd && live) {
+        // values of nodes that are not finite: added to the rows that see them
+#pragma unroll 1
+        for (int bit = 0; bit < DCP_TREE_MAX_NODES; ++bit) {
+          if (!((odd_keys[bit >> 5] >> (bit & 31)) & 1u)) continue;
+          const int jj = max(u.kb, u.ctx) + bit;
+          if (!tree_bit(mask_row, (int)(global_pos(jj, u.r, p.I, p.N) - u.base))) continue;
+          const int blk = p.block_tables[((long long)u.r * p.B + u.b) * p.max_lb + jj / p.bs];
+          const __nv_bfloat16* v = p.v_pool + (((long long)blk * p.bs + jj % p.bs) * p.Hkv + u.g) * D + c;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float e = __bfloat162float(v[k]);
+            if (!(fabsf(e) < INFINITY)) o[k] = __float_as_uint(__uint_as_float(o[k]) + e);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4*>(mine + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+            make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
     }
     __syncwarp();
-#pragma unroll
+#pragma unroll 4
     for (int it = 0; it < 8; ++it) {
       const int rr = it * 4 + (lane >> 3), k = lane & 7;
       const unsigned long long to = __shfl_sync(0xffffffffu, out, rr);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (j >= pass || to == 0ull) break;
+      if (to != 0ull) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (have) v = *reinterpret_cast<const uint4*>(mine + j * 4096 + rr * 128 + ((k ^ (rr & 7)) << 4));
-        *reinterpret_cast<uint4*>(reinterpret_cast<float*>(to) + d0 + 32 * (i0 + j) + 4 * k) = v;
+        if (have) v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((k ^ (rr & 7)) << 4));
+        *reinterpret_cast<uint4*>(reinterpret_cast<float*>(to) + d0 + 32 * i + 4 * k) = v;
       }
     }
     __syncwarp();
   }
   if (writes && (!u.turns || w == 0))
     p.dst_lse[dst_row(u.row0 + row)] = live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-  named_bar_sync(kBarEpi, 256);          // the query's memory may be written again
   return have;
 }
 
@@ -762,9 +756,10 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     bool ok = true;
     int n = 0;
     for (; unit_of(p, n) >= 0; ++n) {
-      // (the streams leave the loop together: stream() decides for the CTA)
-      const bool ready = !bar_red_or(kBarEpi, 256, !unit_ready(n));
-      if (!ready) {
+      // the last unit's output has left the query's memory; the streams leave
+      // the loop together
+      const bool ready = unit_ready(n);
+      if (bar_red_or(kBarEpi, 256, !ready)) {
         ok = false;
         break;
       }
@@ -774,14 +769,21 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // past R are zero), while the first tiles are on their way
         const int rows = p.turns ? kNt : 2 * kNt;
         constexpr int kPer = D / 8;                        // 16-byte pieces of a row
+        constexpr int kStep = 256 / kPer;
         const int c = (tid - 128) % kPer;
-        for (int rr = (tid - 128) / kPer; rr < rows; rr += 256 / kPer) {
+        int i = (u.row0 + (tid - 128) / kPer) / gsize, hh = (u.row0 + (tid - 128) / kPer) % gsize;   // node and head of row rr
+        const int di = kStep / gsize, dh = kStep % gsize;
+        const __nv_bfloat16* q = p.q + (((long long)u.b * p.Lq) * p.Hq + u.g * gsize) * D + 8 * c;
+#pragma unroll 2
+        for (int rr = (tid - 128) / kPer; rr < rows; rr += kStep) {
           const int lr = rr & 127;
           const uint32_t dst = smem_u32(qs + (rr >> 7) * kTile + (c >> 3) * (kNt * 128) + lr * 128 + (((c & 7) ^ (lr & 7)) << 4));
           // (a row past R: zero bytes from an address inside the query)
-          const int row = rr < u.R ? u.row0 + rr : u.row0;
-          const int i = row / gsize, head = u.g * gsize + row % gsize;
-          cp_async_16(dst, p.q + (((long long)u.b * p.Lq + i) * p.Hq + head) * D + 8 * c, rr < u.R ? 16u : 0u);
+          const bool there = rr < u.R;
+          cp_async_16(dst, there ? q + ((long long)i * p.Hq + hh) * D : q, there ? 16u : 0u);
+          i += di;
+          hh += dh;
+          if (hh >= gsize) hh -= gsize, ++i;
         }
         cp_async_wait_all();
         fence_proxy_async_smem();

@@ -853,15 +853,21 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
     const long long per_req = (long long)p.N * row_units(p) * p.n_split;
     const int k_req = (int)(unit / per_req);
     if (p.order != nullptr && tid == 0) sm.req = p.order[k_req];
-    for (int j = tid; p.order == nullptr && j < p.B; j += kThreads) {
-      const int sj = p.seq_lens[j];
-      int rank = 0;
-#pragma unroll 1
-      for (int i = 0; i < p.B; ++i) {
-        const int si = p.seq_lens[i];
-        rank += (si > sj) || (si == sj && i < j);
+    if (p.order == nullptr) {
+      // (the lengths through shared memory: at most kLptMaxBatch of them)
+      int* lens = reinterpret_cast<int*>(sm.lw);
+      const int sj = tid < p.B ? p.seq_lens[tid] : 0;
+      if (tid < p.B) lens[tid] = sj;
+      __syncthreads();
+      if (tid < p.B) {
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < p.B; ++i) {
+          const int si = lens[i];
+          rank += (si > sj) || (si == sj && i < tid);
+        }
+        if (rank == k_req) sm.req = tid;
       }
-      if (rank == k_req) sm.req = j;
     }
     __syncthreads();
     b_lpt = *(volatile int*)&sm.req;

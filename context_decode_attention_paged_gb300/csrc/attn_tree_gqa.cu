@@ -268,6 +268,7 @@ __device__ __forceinline__ bool stream(const Params& p, Smem& sm, const Unit& u,
     return p.mask + u.b * p.mask_stride + (long long)((u.row0 + row) / (p.Hq / p.Hkv)) * p.words;
   };
 
+  const bool idle = (u.turns ? quad * 32 : 128 * w + quad * 32) >= u.R;
   float m = -INFINITY, l = 0.f;
   float heavy_at = -INFINITY;            // a score above it is heavy, or moves the reference
   bool bad = false;
@@ -317,6 +318,15 @@ __device__ __forceinline__ bool stream(const Params& p, Smem& sm, const Unit& u,
       const int k = (s & 1) * kNs + (lrow & 63);
       clean_value_row<D>(u, odd_keys, ring + slot * tile_bytes<D>() + k * 128, j0 + (lrow & 63), lrow >> 6);
       fence_proxy_async_smem();
+    }
+    if (idle) {
+      // no row of this warp attends: its probabilities are the scores' own bits,
+      // which meet no other row
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[w][buf]));
+      continue;
     }
     auto f = [&](int k) { return __uint_as_float(x[k]); };
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

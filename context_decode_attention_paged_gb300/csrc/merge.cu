@@ -36,23 +36,41 @@ __device__ __forceinline__ float lse_weights(float lane_lse, float* merged_lse) 
   return e / s;
 }
 
+constexpr int kBatch = 4;          // sources of a lane in flight
+
+// Vector c of sources k0 .. k0 + kBatch - 1 (those below n).
+__device__ __forceinline__ void load_batch(const float* __restrict__ src, long long src_stride, int n, int k0, int c,
+                                           float4 (&v)[kBatch]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k)
+    if (k0 + k < n) v[k] = __ldcs(reinterpret_cast<const float4*>(src + (k0 + k) * src_stride) + c);
+}
+
 // out row = sum over n sources (stride src_stride floats) of w_k * src_k.
-// Dv4 = Dv / 4 float4 per row.
+// Dv4 = Dv / 4 float4 per row.  Loads go out kBatch sources at a time, the first
+// ones (in `v`, vector `lane`) before the weights are known; a source of weight
+// 0 is not looked at, whatever it holds.
 template <bool kBf16Out>
 __device__ __forceinline__ void weighted_row(const float* __restrict__ src, long long src_stride,
-                                             int n, float w_lane, int Dv4, void* dst_row) {
+                                             int n, float w_lane, int Dv4, float4 (&v)[kBatch], void* dst_row) {
   const int lane = threadIdx.x & 31;
-  for (int c = lane; c < Dv4; c += 32) {
+  for (int c = lane; c - lane < Dv4; c += 32) {
+    const bool in = c < Dv4;                         // (the shuffles below take the whole warp)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < n; ++k) {
-      const float w = __shfl_sync(0xffffffffu, w_lane, k);
-      if (w == 0.f) continue;
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(src + k * src_stride) + c);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+      if (in && (c != lane || k0 > 0)) load_batch(src, src_stride, n, k0, c, v);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (k0 + k >= n) break;
+        const float w = __shfl_sync(0xffffffffu, w_lane, k0 + k);
+        if (w == 0.f) continue;
+        acc.x = fmaf(w, v[k].x, acc.x);
+        acc.y = fmaf(w, v[k].y, acc.y);
+        acc.z = fmaf(w, v[k].z, acc.z);
+        acc.w = fmaf(w, v[k].w, acc.w);
+      }
     }
+    if (!in) continue;
     if (kBf16Out) {
       __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
       __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
@@ -76,6 +94,10 @@ merge_kernel(const float* __restrict__ partial_out, const float* __restrict__ ls
   const int lane = threadIdx.x & 31;
   // row = (b * Lq + i) * Hq + h ; partial rows of shard r at r * rows + row
   const float lane_lse = lane < N ? lse[(long long)lane * rows + row] : -INFINITY;
+  const float* src = partial_out + row * Dv;
+  const long long stride = rows * (long long)Dv;
+  float4 v[kBatch];
+  if (lane < Dv / 4) load_batch(src, stride, N, 0, lane, v);
   float merged;
   const float w = lse_weights(lane_lse, &merged);
   const int h = (int)(row % Hq);
@@ -83,7 +105,7 @@ merge_kernel(const float* __restrict__ partial_out, const float* __restrict__ ls
   const int hs = Hq / N;
   const int r = h / hs;
   const long long dst = (((long long)r * B * Lq + bi) * hs + (h % hs));
-  weighted_row<true>(partial_out + row * Dv, rows * (long long)Dv, N, w, Dv / 4, out + dst * Dv);
+  weighted_row<true>(src, stride, N, w, Dv / 4, v, out + dst * Dv);
   if (out_lse && lane == 0) out_lse[dst] = merged;
 }
 
@@ -100,10 +122,13 @@ split_combine_kernel(const float* __restrict__ ws_o, const float* __restrict__ w
   const int h = (int)(row % Hq);
   const long long base = unit * n_split * Hq + h;
   const float lane_lse = lane < n_split ? ws_lse[base + (long long)lane * Hq] : -INFINITY;
+  const float* src = ws_o + base * Dv;
+  const long long stride = (long long)Hq * Dv;
+  float4 v[kBatch];
+  if (lane < Dv / 4) load_batch(src, stride, n_split, 0, lane, v);
   float merged;
   const float w = lse_weights(lane_lse, &merged);
-  weighted_row<false>(ws_o + base * Dv, (long long)Hq * Dv, n_split, w, Dv / 4,
-                      partial_out + row * Dv);
+  weighted_row<false>(src, stride, n_split, w, Dv / 4, v, partial_out + row * Dv);
   if (lane == 0) lse[row] = merged;
 }
 

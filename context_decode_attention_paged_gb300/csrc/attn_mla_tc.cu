@@ -71,6 +71,7 @@
 // possible, so its running reference may stay -inf past the first tile.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <stddef.h>
 
 #include "dcp_device.cuh"
 #include "dcp_internal.h"
@@ -125,7 +126,7 @@ constexpr uint32_t kColP = 224;    // 32 cols: P (128 rows x 64 bf16)
 constexpr uint32_t kColO = 256;    // 256 cols fp32 output
 constexpr float kLazyLog2 = 8.0f;       // R moves when scores pass it by more than this
 constexpr float kResidualLog2 = 8.0f;   // |partial| * scale above this (log2 units): send a residual
-constexpr uint32_t kBarEpi = 1;         // named barrier of the two softmax warpgroups (epilogue)
+constexpr uint32_t kBarEpi = 1;         // named barriers of the epilogue: both softmax warpgroups, then one of each
 constexpr uint32_t kOBoxBytes = kHeads * 128;   // staged output box: 128 rows x 32 fp32
 constexpr int kPvGate = 1;              // PV(t) waits for the score MMAs of tile t + kPvGate
 
@@ -183,6 +184,7 @@ struct Smem {
   uint32_t odd[8];             // kTree: node keys whose values are not all finite (bit: key - first node key)
 };
 
+constexpr int kBarriers = (int)(offsetof(Smem, tmem_base) / sizeof(uint64_t));   // the barriers lead the struct
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kQRopeBytes + kQLat0Bytes + kScMsgBytes +
                               kPmMsgBytes + 2 * kMxMsgBytes + sizeof(Smem) + 64;
 static_assert(kSmemBytes <= 232448, "shared memory of the MLA kernel");
@@ -622,20 +624,19 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<uint4*>(row + ((k ^ (h & 7)) << 4)) =
               make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-      }
-      fence_proxy_async_smem();
-      named_bar_sync(kBarEpi, 256);
-      if (w == 0 && lg == 0 && lane == 0) {
-        // Hq rows a node and box (the rows of a node start at a multiple of 8 when there are several)
+        fence_proxy_async_smem();
+        named_bar_sync(kBarEpi + 1 + (uint32_t)w, 128);
+        if (mt == 0) {
+          // Hq rows a node and box (the rows of a node start at a multiple of 8 when there are several)
+          const int k = 4 * w + c / 32;
 #pragma unroll 1
-        for (int j = 0; j < view.nodes && u.i_q + j < p.Lq; ++j)
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k)
+          for (int j = 0; j < view.nodes && u.i_q + j < p.Lq; ++j)
             tma_store_2d(&tm_out, smem_u32(stages + k * kOBoxBytes + j * p.Hq * 128), 256 * (int)cta + 32 * k,
                          (int32_t)row_of(j * p.Hq));
-        bulk_commit();
-        bulk_wait_read0();
+          bulk_commit();
+        }
       }
+      if (mt == 0) bulk_wait_read0();
     } else {
       const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int hr = 16 * (4 * w + lg); hr < 16 * (4 * w + lg) + 16; ++hr) {
@@ -663,26 +664,23 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
       uint32_t v[32];
       tmem_ld32(lane_addr + kColO + 128 * w + c, v);
       tmem_wait_ld();
-      uint8_t* row = ostage + (4 * w + c / 32) * kOBoxBytes + h * 128;
+      uint8_t* box = ostage + (4 * w + c / 32) * kOBoxBytes;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        *reinterpret_cast<float4*>(row + ((k ^ (h & 7)) << 4)) =
+        *reinterpret_cast<float4*>(box + h * 128 + ((k ^ (h & 7)) << 4)) =
             make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
                         __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
+      // ... and out to HBM by TMA, each box as soon as it is staged (Hq rows:
+      // with fewer than 128 query heads the MMA rows past Hq hold the next query
+      // rows of the tensor, computed and never written)
+      fence_proxy_async_smem();
+      named_bar_sync(kBarEpi + 1 + (uint32_t)w, 128);
+      if (mt == 0) {
+        tma_store_2d(&tm_out, smem_u32(box), 256 * (int)cta + 128 * w + c, (int32_t)row0);
+        bulk_commit();
+      }
     }
-    fence_proxy_async_smem();
-    named_bar_sync(kBarEpi, 256);
-    // ... and out to HBM by TMA: one thread stores the boxes (Hq rows each:
-    // with fewer than 128 query heads the MMA rows past Hq hold the next query
-    // rows of the tensor, computed and never written) and waits only until
-    // they have been read out of shared memory
-    if (w == 0 && lg == 0 && lane == 0) {
-#pragma unroll 1
-      for (int k = 0; k < 8; ++k)
-        tma_store_2d(&tm_out, smem_u32(ostage + k * kOBoxBytes), 256 * (int)cta + 32 * k, (int32_t)row0);
-      bulk_commit();
-      bulk_wait_read0();
-    }
+    if (mt == 0) bulk_wait_read0();       // the boxes have been read out of shared memory
   } else {
     // no product (an empty range, a skipped or an aborted unit): zeros, by
     // plain stores (copies of an aborted unit may still be landing in the ring)
@@ -842,86 +840,80 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t cta = cluster_ctarank();          // 0 or 1
+  // barriers and tensor memory first: they depend on no loaded data
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_lat);
+    prefetch_tmap(&tm_rope);
+    prefetch_tmap(&tm_qlat);
+    prefetch_tmap(&tm_qrope);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), 512);
+  if (warp == 2) {
+    for (int k = lane; k < kBarriers; k += 32) {
+      uint64_t* bar = sm.kv_full + k;
+      uint32_t count = 1;
+      if (bar == &sm.s_free[0] || bar == &sm.s_free[1] || bar == &sm.fin) count = 256;   // (s_free: senders and softmax)
+      if (bar == &sm.p_full[0] || bar == &sm.p_full[1]) count = 128;
+      mbar_init(smem_u32(bar), count);
+    }
+    fence_mbar_init();
+    if (lane == 0) {
+      sm.abort = 0;
+      sm.qk_issued = -1;
+    }
+  }
   // kLpt: units in longest-request-first order (length descending, index
   // ascending).  The block scheduler starts clusters in index order, so short
   // units fill the tail.  Batches up to kLptMaxBatch find rank k by counting
   // in the kernel; larger ones read it from the pre-pass's order.  Both CTAs
   // of the pair take the same request.
-  const long long unit = blockIdx.x >> 1;
+  const unsigned unit = blockIdx.x >> 1;             // (the launcher keeps units below 2^31)
+  int* lens = reinterpret_cast<int*>(sm.lw[0]);      // the lengths through shared memory: at most kLptMaxBatch of them
+  int* qlens = reinterpret_cast<int*>(sm.lw[1]);
+  const bool ranks = kLpt && p.order == nullptr;
+  const int rt = tid - 128;
+  if (ranks && rt >= 0 && rt < p.B) {
+    lens[rt] = p.seq_lens[rt];
+    if constexpr (kTree) {
+      if (p.q_lens != nullptr) qlens[rt] = p.q_lens[rt];
+    }
+  }
+  const unsigned per_q = (unsigned)(p.n_split * row_units(p)), per_req = (unsigned)p.N * per_q;
+  const int k_req = kLpt ? (int)(unit / per_req) : 0;
+  if (kLpt && !ranks && tid == 0) sm.req = p.order[k_req];
+  __syncthreads();
+  cluster_arrive();          // this CTA's barriers are initialised (the peer waits below)
   int b_lpt = 0;
   if (kLpt) {
-    const long long per_req = (long long)p.N * row_units(p) * p.n_split;
-    const int k_req = (int)(unit / per_req);
-    if (p.order != nullptr && tid == 0) sm.req = p.order[k_req];
-    if (p.order == nullptr) {
-      // (the lengths through shared memory: at most kLptMaxBatch of them)
-      int* lens = reinterpret_cast<int*>(sm.lw);
-      const int sj = tid < p.B ? p.seq_lens[tid] : 0;
-      if (tid < p.B) lens[tid] = sj;
-      __syncthreads();
-      if (tid < p.B) {
-        int rank = 0;
+    if (ranks && rt >= 0 && rt < p.B) {
+      const int sj = lens[rt];
+      int rank = 0;
 #pragma unroll 4
-        for (int i = 0; i < p.B; ++i) {
-          const int si = lens[i];
-          rank += (si > sj) || (si == sj && i < tid);
-        }
-        if (rank == k_req) sm.req = tid;
+      for (int i = 0; i < p.B; ++i) {
+        const int si = lens[i];
+        rank += (si > sj) || (si == sj && i < rt);
       }
+      if (rank == k_req) sm.req = rt;
     }
     __syncthreads();
     b_lpt = *(volatile int*)&sm.req;
   }
   Unit u;
   {
-    // 32-bit index arithmetic (the launcher keeps units below 2^31)
-    const unsigned un = (unsigned)unit, per_q = (unsigned)(p.n_split * row_units(p));
-    const unsigned rest = kLpt ? un % ((unsigned)p.N * per_q) : un;
-    u.s_idx = (int)(rest % (unsigned)p.n_split);
-    u.i_q = (int)((rest / (unsigned)p.n_split) % (unsigned)row_units(p));
+    const unsigned rest = unit - (unsigned)k_req * per_req;
+    const unsigned q = rest / per_q, in_q = rest - q * per_q;
+    const unsigned i = p.n_split == 1 ? in_q : in_q / (unsigned)p.n_split;
+    u.s_idx = (int)(in_q - i * (unsigned)p.n_split);
+    u.i_q = (int)i;
     if constexpr (kTree) u.i_q *= p.nodes;                   // the unit's first node
-    u.b = kLpt ? b_lpt : (int)((un / per_q) % (unsigned)p.B);
-    u.r = kLpt ? (int)(rest / per_q) : (int)(un / (per_q * (unsigned)p.B));
+    u.r = kLpt ? (int)q : (int)(q / (unsigned)p.B);
+    u.b = kLpt ? b_lpt : (int)(q - (unsigned)u.r * (unsigned)p.B);
   }
-  // barriers and tensor memory first: they depend on no loaded data
-  if (tid == 0) {
-    for (int k = 0; k < kStages; ++k) {
-      mbar_init(smem_u32(&sm.kv_full[k]), 1);
-      mbar_init(smem_u32(&sm.kv_empty[k]), 1);
-    }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(smem_u32(&sm.s_free[k]), 256);     // senders and the tile's softmax warpgroup
-      mbar_init(smem_u32(&sm.s_full[k]), 1);
-
-      for (int q = 0; q < 4; ++q) {
-        mbar_init(smem_u32(&sm.sc_recv[k][q]), 1);
-        mbar_init(smem_u32(&sm.sc_free[k][q]), 1);
-        mbar_init(smem_u32(&sm.pm_recv[k][q]), 1);
-        mbar_init(smem_u32(&sm.pm_free[k][q]), 1);
-        mbar_init(smem_u32(&sm.r_pub[k][q]), 1);
-        mbar_init(smem_u32(&sm.sc_res[k][q]), 1);
-        mbar_init(smem_u32(&sm.sc_mfree[k][q]), 1);
-        mbar_init(smem_u32(&sm.mx_recv[k][q]), 1);
-      }
-
-      mbar_init(smem_u32(&sm.p_full[k]), 128);
-      mbar_init(smem_u32(&sm.pv_done[k]), 1);
-
-    }
-    mbar_init(smem_u32(&sm.fin), 256);
-    mbar_init(smem_u32(&sm.q_full), 1);
-    mbar_init(smem_u32(&sm.drain), 1);
-    mbar_init(smem_u32(&sm.drain_qk), 1);
-    sm.abort = 0;
-    sm.qk_issued = -1;
-    fence_mbar_init();
-  }
-  if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), 512);
-
   // key range of this unit (shard-local indices [kb, ke))
-  const int S = p.seq_lens[u.b];
+  const int S = ranks ? lens[u.b] : p.seq_lens[u.b];
   TreeReq tree{};
-  if constexpr (kTree) tree = tree_request(p.seq_lens, p.q_lens, p.Lq, u.b);
+  if constexpr (kTree) tree = ranks ? tree_request(lens, p.q_lens != nullptr ? qlens : nullptr, p.Lq, u.b)
+                               : tree_request(p.seq_lens, p.q_lens, p.Lq, u.b);
   const bool bad_len = kTree ? tree.bad : S < p.Lq;
   int L = bad_len ? 0 : local_len(S, u.r, p.I, p.N);
   const bool short_table = (long long)L > (long long)p.max_lb * p.bs;
@@ -946,78 +938,85 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
   u.ke = min(vis, u.kb + p.split_tokens);
   u.T = (u.ke - u.kb + kNt - 1) / kNt;
   if (tid == 0 && cta == 0 && (bad_len || short_table)) set_status(p.status, DCP_ERR_BOUNDS);
+  // TMA producer state (warp 0, lane 0): the query and the first stages are on
+  // their way while the set-up goes on
+  volatile int* abort_flag = &sm.abort;
+  const int32_t* bt_row = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
+  int issued[kStages];
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) issued[k] = 0;
+  // pool rows [row, ...) into a stage: the tile's 64 rows (one block), or with
+  // blocks of 8, 16 or 32 tokens those of its k-th block
+  auto load_rows = [&](uint8_t* dst, int k, int row, uint32_t full) {
+    if (!kSmallBlocks) {
+      tma_load_3d(smem_u32(dst), &tm_lat, 0, row, 4 * (int)cta, full);
+      tma_load_2d(smem_u32(dst + 4 * kChunkBytes), &tm_rope, kLatent + 32 * (int)cta, row, full);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tma_load_3d(smem_u32(dst + c * kChunkBytes + k * p.bs * 128), &tm_lat, 0, row, 4 * (int)cta + c, full);
+      tma_load_2d(smem_u32(dst + 4 * kChunkBytes + k * p.bs * 64), &tm_rope, kLatent + 32 * (int)cta, row, full);
+    }
+  };
+  // the query slice by TMA: latent dims 0-63 and the rope dims straight into
+  // their shared-memory operands, latent dims 64-255 into ring stages 3-4
+  // (idle until the first tiles have been issued) for the copy into TMEM
+  uint8_t* qstage = stages + (kStages - 2) * kStageBytes;
+  const int t_early = min(u.T, kStages - 2);
+  if (warp == 0 && u.T > 0) {
+    // the early tiles' blocks, one a lane (the scan of the table runs meanwhile:
+    // an id outside the pool keeps the early loads from going out here, and
+    // ends the unit there)
+    const int step = kSmallBlocks ? p.bs : kNt;
+    const int j = u.kb + lane * step;
+    const bool mine = lane * step < t_early * kNt && j < u.ke;
+    const int id = mine ? bt_row[j / p.bs] : 0;
+    const int row = id * p.bs + (mine && !kSmallBlocks ? j % p.bs : 0);
+    if (lane == 0) {
+      const int32_t qr = (int32_t)(((long long)u.b * p.Lq + u.i_q) * p.Hq);
+      const uint32_t qf = smem_u32(&sm.q_full);
+      mbar_arrive_expect_tx(qf, kQLat0Bytes * 4 + kQRopeBytes);
+      tma_load_2d(smem_u32(qlat0), &tm_qlat, 256 * (int)cta, qr, qf);
+#pragma unroll
+      for (int c = 1; c < 4; ++c) tma_load_2d(smem_u32(qstage + (c - 1) * kQLat0Bytes), &tm_qlat, 256 * (int)cta + 64 * c, qr, qf);
+      tma_load_2d(smem_u32(qrope), &tm_qrope, kLatent + 32 * (int)cta, qr, qf);
+    }
+    const bool in_pool = !__any_sync(0xffffffffu, (unsigned)id >= (unsigned)p.num_blocks);
+    const int per = kSmallBlocks ? kNt / p.bs : 1;
+    for (int t = 0; t < t_early && in_pool; ++t) {
+      if (t == p.skip_tile && cta == 0) continue;
+      const uint32_t full = smem_u32(&sm.kv_full[t]);
+      uint8_t* dst = stages + t * kStageBytes;
+      if (lane == 0) mbar_arrive_expect_tx(full, kStageBytes);
+      for (int k = 0; k < per; ++k) {
+        const int to = __shfl_sync(0xffffffffu, row, t * per + k);
+        if (lane == 0) load_rows(dst, k, to, full);
+      }
+      ++issued[t];
+    }
+  }
   {
     // a block id past the pool among the query's visible keys skips the unit
     // (every KV split of it: zero partial, -inf LSE) and reports
     // DCP_ERR_BOUNDS; both CTAs of the pair read the same entries
-    const int32_t* bt = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
     bool bad_blk = false;
     for (int jb = tid; jb < (vis + p.bs - 1) / p.bs; jb += (int)kThreads)   // every split of the query
-      bad_blk |= (unsigned)bt[jb] >= (unsigned)p.num_blocks;
+      bad_blk |= (unsigned)bt_row[jb] >= (unsigned)p.num_blocks;
     if (__syncthreads_or(bad_blk)) {
+      if (warp == 0 && lane == 0 && u.T > 0) {
+        // the early copies land before the CTA exits
+        mbar_wait(smem_u32(&sm.q_full), 0u, p.wait_ns);
+        for (int k = 0; k < kStages; ++k)
+          if (issued[k] > 0) mbar_wait(smem_u32(&sm.kv_full[k]), 0u, p.wait_ns);
+      }
       u.T = 0;
       if (tid == 0 && cta == 0) set_status(p.status, DCP_ERR_BOUNDS);
     }
   }
   const int T = u.T;
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;     // the barrier above made the allocation visible
+  const uint32_t tmem = sm.tmem_base;     // the barriers above made the allocation visible
 
-  // TMA producer state (warp 0, lane 0): the first stages are issued before
-  // the query is staged, so their HBM latency overlaps the set-up
-  volatile int* abort_flag = &sm.abort;
-  const int32_t* bt_row = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
-  int issued[kStages];
-#pragma unroll
-  for (int k = 0; k < kStages; ++k) issued[k] = 0;
-  auto issue_tile = [&](int t) {
-    // test hook: CTA 0 never loads this tile, so the bounded waits on it run
-    // out and the unit unwinds
-    if (t == p.skip_tile && cta == 0) return;
-    const int st = t % kStages;
-    const uint32_t full = smem_u32(&sm.kv_full[st]);
-    uint8_t* dst = stages + st * kStageBytes;
-    mbar_arrive_expect_tx(full, kStageBytes);
-    if (!kSmallBlocks) {
-      // blocks of 64 tokens or a multiple: the tile is one box inside one block
-      const int j = u.kb + t * kNt;
-      const int row = bt_row[j / p.bs] * p.bs + (j % p.bs);   // ids checked against the pool above
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        tma_load_2d(smem_u32(dst + c * kChunkBytes), &tm_lat, 256 * (int)cta + 64 * c, row, full);
-      tma_load_2d(smem_u32(dst + 4 * kChunkBytes), &tm_rope, kLatent + 32 * (int)cta, row, full);
-    } else {
-      // blocks of 8, 16 or 32 tokens: one box per block; boxes past the key
-      // range read pool row 0 (masked, values zeroed) so that no stale table
-      // entry is followed
-      for (int k = 0; k < kNt / p.bs; ++k) {
-        const int j = u.kb + t * kNt + k * p.bs;
-        const int row = j < u.ke ? bt_row[j / p.bs] * p.bs : 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tma_load_2d(smem_u32(dst + c * kChunkBytes + k * p.bs * 128), &tm_lat, 256 * (int)cta + 64 * c, row, full);
-        tma_load_2d(smem_u32(dst + 4 * kChunkBytes + k * p.bs * 64), &tm_rope, kLatent + 32 * (int)cta, row, full);
-      }
-    }
-    ++issued[st];
-  };
-  // the query slice by TMA: latent dims 0-63 and the rope dims straight into
-  // their shared-memory operands, latent dims 64-255 into ring stages 3-4
-  // (idle until the first tiles have been issued) for the copy into TMEM
-  uint8_t* qstage = stages + (kStages - 2) * kStageBytes;
-  const int t_early = min(T, kStages - 2);
-  if (warp == 0 && lane == 0 && T > 0) {
-    prefetch_tmap(&tm_lat);
-    prefetch_tmap(&tm_rope);
-    const int32_t qr = (int32_t)(((long long)u.b * p.Lq + u.i_q) * p.Hq);
-    const uint32_t qf = smem_u32(&sm.q_full);
-    mbar_arrive_expect_tx(qf, kQLat0Bytes * 4 + kQRopeBytes);
-    tma_load_2d(smem_u32(qlat0), &tm_qlat, 256 * (int)cta, qr, qf);
-#pragma unroll
-    for (int c = 1; c < 4; ++c) tma_load_2d(smem_u32(qstage + (c - 1) * kQLat0Bytes), &tm_qlat, 256 * (int)cta + 64 * c, qr, qf);
-    tma_load_2d(smem_u32(qrope), &tm_qrope, kLatent + 32 * (int)cta, qr, qf);
-    for (int t = 0; t < t_early; ++t) issue_tile(t);
-  }
   // latent dims 64-255 of the slice -> TMEM (row = head = TMEM lane, bf16
   // pairs per column): the two softmax warps of a lane quadrant take 12 of the
   // 24 16-byte chunks of each row (128B-swizzled, so a warp's reads of one
@@ -1053,7 +1052,8 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
     *abort_flag = 1;
   }
   tc_fence_before();
-  cluster_sync();            // barriers of both CTAs initialised, query staged
+  __syncthreads();           // query staged
+  cluster_wait();            // the peer's barriers are initialised
   tc_fence_after();
 
   auto fail = [&](void) {
@@ -1066,18 +1066,42 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kCtrlRegs));
     if (warp == 0) {
       // ---------------- TMA producer ----------------
-      if (lane == 0 && T > 0) {
+      if (T > 0) {
+        const bool lead = elect_one();
+        const uint32_t ring = uniform(smem_u32(stages)), full0 = uniform(smem_u32(&sm.kv_full[0]));
+        int st = t_early % kStages;
+        uint32_t ph = 0;                              // (t_early < kStages: the first lap)
         for (int t = t_early; t < T; ++t) {
-          const int st = t % kStages;
-          const uint32_t ph = (uint32_t)(t / kStages) & 1u;
-          if (*abort_flag || !mbar_wait(smem_u32(&sm.kv_empty[st]), ph ^ 1u, p.wait_ns)) {
-            fail();
+          if (!__all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&sm.kv_empty[st]), ph ^ 1u, p.wait_ns))) {
+            if (lane == 0) fail();
             break;
           }
-          issue_tile(t);
+          // (test hook: CTA 0 never loads tile skip_tile, so the bounded waits on
+          // it run out and the unit unwinds)
+          if (!(t == p.skip_tile && cta == 0)) {
+            const uint32_t full = full0 + 8u * (uint32_t)st, dst = ring + (uint32_t)st * kStageBytes;
+            const int j = u.kb + t * kNt;              // (ids checked against the pool above)
+            if (!kSmallBlocks) {
+              // blocks of 64 tokens or a multiple: the tile is one box inside one block
+              const int row = bt_row[j / p.bs] * p.bs + (j % p.bs);
+              if (lead) {
+                mbar_arrive_expect_tx(full, kStageBytes);
+                tma_load_3d(dst, &tm_lat, 0, row, 4 * (int)cta, full);
+                tma_load_2d(dst + 4 * kChunkBytes, &tm_rope, kLatent + 32 * (int)cta, row, full);
+              }
+            } else if (lane == 0) {
+              // one box per block; boxes past the key range read pool row 0
+              // (masked, values zeroed) so that no stale table entry is followed
+              mbar_arrive_expect_tx(full, kStageBytes);
+              for (int k = 0; k < kNt / p.bs; ++k)
+                load_rows(stages + st * kStageBytes, k, j + k * p.bs < u.ke ? bt_row[j / p.bs + k] * p.bs : 0, full);
+            }
+            ++issued[st];
+          }
+          if (++st == kStages) st = 0, ph ^= 1u;
         }
-        if (*abort_flag) {
-          // let every copy this thread issued land before the CTA exits
+        if (lane == 0 && *abort_flag) {
+          // let every copy this warp issued land before the CTA exits
           for (int k = 0; k < kStages; ++k)
             if (issued[k] > 0) mbar_wait(smem_u32(&sm.kv_full[k]), (uint32_t)(issued[k] - 1) & 1u, p.wait_ns);
         }
@@ -1230,7 +1254,11 @@ static int tree_nodes(const AttnArgs& a) {
 
 SplitPlan plan_attn_mla_tc(const AttnArgs& a, int sm_count) {
   const int nodes = tree_nodes(a);
-  SplitPlan pl = plan_splits(a, sm_count, kNt, 2 * ((a.Lq + nodes - 1) / nodes));
+  // A drafted tree has few, equal units of many tiles: the last of 3.4 waves
+  // leaves the SMs idle for as long as the first three take, and two splits of
+  // each unit (6.7 waves of half the length) end sooner.  A split writes and
+  // rereads 2 x 256 KB of partial rows, the time of about 5 tiles.
+  SplitPlan pl = plan_splits(a, sm_count, kNt, 2 * ((a.Lq + nodes - 1) / nodes), a.tree_words > 0 ? 5 : 0);
   if (a.B > kLptMaxBatch && a.B <= kLptOrderMaxBatch) {
     pl.lpt_order = true;
     pl.order_offset = (pl.ws_bytes + 255) & ~size_t(255);
@@ -1245,9 +1273,13 @@ static cudaError_t launch_mla(const AttnArgs& a, const SplitPlan& plan) {
   const uint64_t dims[2] = {(uint64_t)kDqk, (uint64_t)a.num_blocks * a.bs};
   const uint64_t strides[1] = {(uint64_t)kDqk * 2};
   const uint32_t box_rows = (uint32_t)(a.bs < kNt ? a.bs : kNt);
-  const uint32_t box_lat[2] = {64, box_rows};
+  // latent chunks of 64 dims as the outermost dimension: one box brings a CTA's
+  // four chunks of a tile (one chunk at a time where a tile takes several blocks)
+  const uint64_t lat_dims[3] = {64, dims[1], (uint64_t)(kLatent / 64)};
+  const uint64_t lat_strides[2] = {(uint64_t)kDqk * 2, 128};
+  const uint32_t box_lat[3] = {64, box_rows, a.bs < kNt ? 1u : 4u};
   const uint32_t box_rope[2] = {32, box_rows};
-  if (!make_tensor_map_bf16(&tm_lat, a.kv, 2, dims, strides, box_lat, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!make_tensor_map_bf16(&tm_lat, a.kv, 3, lat_dims, lat_strides, box_lat, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tensor_map_bf16(&tm_rope, a.kv, 2, dims, strides, box_rope, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   // the query as [B * Lq * Hq][576]: one box of 128 head rows per chunk

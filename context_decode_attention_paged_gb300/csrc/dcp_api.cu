@@ -198,23 +198,25 @@ int device_sm_count() {
   return n;
 }
 
-SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int units_per_split) {
+SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int units_per_split, int join_tiles) {
   SplitPlan p;
   const long long max_local = (long long)a.max_lb * a.bs;
   const long long base_units = (long long)a.N * a.B * units_per_split;
   const long long target = 2LL * sm_count;
   long long n = 1;
-  if (base_units < target && max_local > 4LL * tile_tokens) {
+  const bool small = base_units < target;
+  if ((small || (join_tiles > 0 && base_units < 8 * target)) && max_local > 4LL * tile_tokens) {
     // Split count by a wave model: units run in waves of sm_count CTAs and a
     // unit costs its tiles plus about kUnitStartTiles of start-up and drain,
     // so pick the count with the fewest waves x (tiles per split + start-up).
     constexpr long long kUnitStartTiles = 4;
     const long long tiles = (max_local + tile_tokens - 1) / tile_tokens;
-    const long long n_hi = std::max<long long>(1, std::min<long long>(32, max_local / (4LL * tile_tokens)));
+    const long long n_hi = std::max<long long>(1, std::min<long long>(small ? 32 : 4, max_local / (4LL * tile_tokens)));
     long long best = -1;
     for (long long c = 1; c <= n_hi; ++c) {
       const long long waves = (base_units * c + sm_count - 1) / sm_count;
-      const long long cost = waves * ((tiles + c - 1) / c + kUnitStartTiles);
+      const long long join = !small && c > 1 ? join_tiles : 0;
+      const long long cost = waves * ((tiles + c - 1) / c + kUnitStartTiles + join);
       if (best < 0 || cost < best) {
         best = cost;
         n = c;

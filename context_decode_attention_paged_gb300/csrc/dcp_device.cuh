@@ -18,8 +18,15 @@ __device__ __forceinline__ void set_status(int* status, int code) {
 // (closed form of the (t / I) % N rule; tokens packed in global order).
 __device__ __forceinline__ int local_len(int S, int r, int I, int N) {
   const long long period = (long long)I * N;
-  const long long full = (long long)(S / period) * I;
-  long long rem = (long long)(S % period) - (long long)r * I;
+  long long full, rem;
+  if (S >= 0 && period <= 0x7fffffffLL) {      // (a 64-bit division costs several times as much)
+    const unsigned n = (unsigned)S / (unsigned)period;
+    full = (long long)n * I;
+    rem = (long long)((unsigned)S - n * (unsigned)period) - (long long)r * I;
+  } else {
+    full = (long long)(S / period) * I;
+    rem = (long long)(S % period) - (long long)r * I;
+  }
   rem = rem < 0 ? 0 : (rem > I ? I : rem);
   return (int)(full + rem);
 }

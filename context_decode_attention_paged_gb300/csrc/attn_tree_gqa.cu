@@ -16,22 +16,28 @@
 // kernel, which has few rows and puts the keys there:
 //   S = Q K^T   (M = 128 rows, N = 128 keys, K = D; both K-major in shared memory)
 //   O += P V    (M = 128 rows, N = D, K = 128 keys; P from TMEM, V MN-major)
-// P carries two bf16 terms, P = bf16(p) + bf16(p - bf16(p)), as in the decode
-// kernel: 16 bits of each probability reach the product.
+// A probability is rounded to bf16 once unless it is heavy, above 2^-3 of its
+// row's sum so far: then bf16(p - bf16(p)) goes along as a second term, so that
+// 16 bits of it reach the product.  Of a row at most a few probabilities are
+// heavy at any time, and they alone could lose half a bf16 step of the output; a
+// warp that holds none skips the second term, its half of the PV product too.
 //
-// Work unit = (shard, request, KV head, row block, KV split), one CTA with two
-// streams, each a 128-lane score/probability tile and an output tile in TMEM
-// and a warpgroup of 128 threads (thread = row):
+// Work unit = (shard, request, KV head, row block, KV split).  A CTA holds an SM
+// and takes units in turn (longest requests first, forth and back over the CTAs),
+// so that the next unit's tiles load while the last one ends.  It runs two
+// streams, each two 64-key score/probability buffers and an output tile in
+// TMEM, an MMA issuer warp, and a warpgroup of 128 threads (thread = row):
 //   more than 128 rows: stream w takes rows [128 w, +128) of the block of 256
 //     and both go over every key tile, so each tile in shared memory serves
 //     256 rows;
 //   128 rows or fewer: both streams hold the same rows and take the key tiles
-//     in turn, two independent running softmaxes joined at the end.
-// Either way one stream's MMAs run while the other's probabilities are made:
-// the issuer sends PV(t), then S(t + 1) of a stream, then of the other.
-// P(t) overwrites S(t) in TMEM; MMAs of one thread complete in order, so
-// S(t + 1), behind PV(t), needs no barrier of its own, and the commit that
-// announces it also says that O is at rest and may be rescaled.
+//     in turn, each through half of the ring, two independent running softmaxes
+//     joined at the end.
+// A tile of 128 keys is two steps of 64: S(s + 1) is issued while the
+// probabilities of step s are made, and the other stream's MMAs fill what is
+// left.  P(s) overwrites S(s) in TMEM (its first 32 columns the first terms, its
+// last 32 the second); a thread's MMAs complete in order, so the commit behind
+// PV(s) also says that O is at rest and may be rescaled.
 //
 // Masks.  A shard's keys are dense in global order: context keys, then the
 // nodes it owns.  Tiles of context keys alone take no mask; in the others a
@@ -42,9 +48,24 @@
 // to the rows that see them.
 //
 // Warp roles (384 threads; setmaxnreg moves registers to the softmax warps):
-// warps 0 and 3 TMA producers (ring of K and V tiles), warp 1 MMA issuer and TMEM
-// owner, warps 4-7 and 8-11 the two streams.  Every wait is bounded; on expiry
-// the kernel records DCP_ERR_TIMEOUT, drains its copies and MMAs and returns.
+// warps 0 and 3 TMA producers (ring of K and V tiles; warp 0 also makes the
+// units), warps 1 and 2 the streams' MMA issuers (whole warps on uniform values,
+// one elected lane issues: 30-37 cycles an MMA instead of 65-90 from one lane's
+// branch), warps 4-7 and 8-11 the two streams; warps without a row skip the
+// softmax.  Every wait is bounded; on expiry the kernel records DCP_ERR_TIMEOUT,
+// drains its copies and MMAs and returns.
+//
+// Measured (GB300, 2.07 GHz, D = 128, 64 query and 4 KV heads):
+//   32 requests of up to 67,000 tokens, 8 nodes: 385 us, 6.1 TB/s (HBM);
+//   8 requests of 32,768, 64 nodes (1024 rows): 550 us, 1.0 PFLOP/s (the softmax
+//     and its MMAs: 128 rows x 64 keys are ~500 cycles of exponentials, packing
+//     and TMEM traffic against 256 of tensor time);
+//   one row a KV head, short units: a unit's first and last tiles cost ~20,000 of
+//     its ~40,000 cycles.
+// Slower when tried: two threads a row (no gain for 640 threads), exponentials
+// before the maximum is known (745 us against 624 at the time), one issuer for
+// both streams with two score buffers (869 against 581), the second term for
+// every probability.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -488,15 +509,19 @@ __device__ __forceinline__ bool stream(const Params& p, Smem& sm, const Unit& u,
             make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
     }
     __syncwarp();
-#pragma unroll 4
+    // (all reads before the first store: branch by branch they took 170 cycles each)
+    uint4 v[8];
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const int rr = it * 4 + (lane >> 3), k = lane & 7;
+      v[it] = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((k ^ (rr & 7)) << 4));
+    }
+#pragma unroll
     for (int it = 0; it < 8; ++it) {
       const int rr = it * 4 + (lane >> 3), k = lane & 7;
       const unsigned long long to = __shfl_sync(0xffffffffu, out, rr);
-      if (to != 0ull) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (have) v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((k ^ (rr & 7)) << 4));
-        *reinterpret_cast<uint4*>(reinterpret_cast<float*>(to) + d0 + 32 * i + 4 * k) = v;
-      }
+      if (!have) v[it] = make_uint4(0u, 0u, 0u, 0u);
+      if (to != 0ull) *reinterpret_cast<uint4*>(reinterpret_cast<float*>(to) + d0 + 32 * i + 4 * k) = v[it];
     }
     __syncwarp();
   }

@@ -20,9 +20,16 @@
 // lengths say that the token is there; position, angles and cache cell are
 // found under them.  With lengths of their own, absent tokens have no tasks:
 // every block first sums the counts (up to kScan requests; when there are more
-// tasks than the SMs hold at once) and a warp finds its token in the sums.  Rotated parts whose vectors do not divide a warp (rot_dim
-// 96 in the half layout, say) or do not fall on vectors go unit by unit with the
-// angles in shared memory, one block a token.
+// tasks than the SMs hold at once) and a warp finds its token in the sums.
+// Rotated parts whose vectors do not divide a warp (rot_dim 96 in the half
+// layout, say) or do not fall on vectors go unit by unit with the angles in
+// shared memory, one block a token.
+//
+// Measured (GB300; time in a graph): 64 tokens of 64 + 4 + 4 heads of 128 (2.4 MB
+// moved) 6.3 us, launch and dependent loads; 512 tokens of 128 heads of 576
+// (152 MB) 28.9 us, 5.3 TB/s; 4,096 tokens of 64 + 4 + 4 heads (79 MB with ragged
+// counts) 18.5 us.  One block a token took 38 and 33 us: a block holds an SM's
+// slot while it waits for its few loads.
 #include <cuda_bf16.h>
 
 #include <algorithm>

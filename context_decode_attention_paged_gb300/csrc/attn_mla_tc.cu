@@ -73,15 +73,15 @@
 // epilogue to the rows that see them.  Tiles that a row sees nothing of are
 // possible, so its running reference may stay -inf past the first tile.
 //
-// Measured (GB300, 2.07 GHz).  Tree, 32 requests of up to 67,000 tokens, 8 nodes
-// of 128 heads: 1.08 ms, 0.94 PFLOP/s (1.02 TFLOP; the cache is 0.79 GB);
+// Measured (GB300, 2.07 GHz).  Tree, 32 requests of 4,096 to 67,000 tokens, 8
+// nodes of 128 heads: 1.08 ms, 0.94 PFLOP/s (1.02 TFLOP, 0.89 GB);
 // 200,000 tokens, 32 nodes: 1.41 ms, 1.27 PFLOP/s.  Decode, batch 512 (41.6 GB):
 // 8.2 ms, 5.1 TB/s.  Neither the tensor cores nor memory bind: a tile's MMAs
 // take ~1,200 cycles, a tile every ~1,900 comes out of a softmax warpgroup's
 // chain of ~3,900 (about 1,500 of them waits on the peer, on the other warpgroup
-// and on the MMAs) over two warpgroups.  With none of the loads the tree case
-// takes 4% less, with a quarter of the MMAs 9%, with a quarter of the exchanged
-// bytes 5%, with all three 13%.  A unit's start and end cost ~25,000 cycles.
+// and on the MMAs) over two warpgroups.  Without the loads the tree case takes 4%
+// less, with a quarter of the MMAs 9%, with a quarter of the exchanged bytes 5%,
+// with both of these 13%.  A unit's start and end cost ~25,000 cycles.
 // Measured against it and slower: three softmax warpgroups (1.27 ms: five ring
 // stages do not feed them), two message slots with four stages (1.28), an L2
 // prefetch before each load (1.23), references agreed on after the exponentials

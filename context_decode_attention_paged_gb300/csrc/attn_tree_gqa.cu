@@ -55,13 +55,15 @@
 // softmax.  Every wait is bounded; on expiry the kernel records DCP_ERR_TIMEOUT,
 // drains its copies and MMAs and returns.
 //
-// Measured (GB300, 2.07 GHz, D = 128, 64 query and 4 KV heads):
-//   32 requests of up to 67,000 tokens, 8 nodes: 385 us, 6.1 TB/s (HBM);
-//   8 requests of 32,768, 64 nodes (1024 rows): 550 us, 1.0 PFLOP/s (the softmax
-//     and its MMAs: 128 rows x 64 keys are ~500 cycles of exponentials, packing
-//     and TMEM traffic against 256 of tensor time);
-//   one row a KV head, short units: a unit's first and last tiles cost ~20,000 of
-//     its ~40,000 cycles.
+// Measured (GB300, 2.07 GHz, D = 128, 64 query and 4 KV heads, 4 shards):
+//   64 requests of 8,192 to 32,768 tokens, 5 nodes: 381 us, 6.1 TB/s (HBM);
+//   16 of them, 64 nodes (1024 rows a KV head): 540 us, 1.12 PFLOP/s: a step of
+//     both streams takes ~1,740 cycles, ~1,260 of them tensor time (the scores'
+//     operands come out of shared memory, 47 cycles an MMA of 32); a unit's
+//     start and end are ~14,000 of ~128,000 cycles;
+//   64 of 1,000 to 16,384 tokens, 1 node: 149 us, 4.9 TB/s: start and end are
+//     ~12,000 of a unit's ~38,000 cycles, and the last CTAs end ~8 us after the
+//     rest.
 // Slower when tried: two threads a row (no gain for 640 threads), exponentials
 // before the maximum is known (745 us against 624 at the time), one issuer for
 // both streams with two score buffers (869 against 581), the second term for

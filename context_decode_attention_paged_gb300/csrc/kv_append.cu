@@ -26,10 +26,9 @@
 // shared memory, one block a token.
 //
 // Measured (GB300; time in a graph): 64 tokens of 64 + 4 + 4 heads of 128 (2.4 MB
-// moved) 6.3 us, launch and dependent loads; 512 tokens of 128 heads of 576
-// (152 MB) 28.9 us, 5.3 TB/s; 4,096 tokens of 64 + 4 + 4 heads (79 MB with ragged
-// counts) 18.5 us.  One block a token took 38 and 33 us: a block holds an SM's
-// slot while it waits for its few loads.
+// moved) 6.5 us, launch and dependent loads; 512 tokens of 128 + 1 heads of 576
+// (152 MB) 29 us, 5.2 TB/s; 6 ragged prompt chunks of up to 2,048 tokens (79 MB)
+// 18.7 us, 4.2 TB/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>

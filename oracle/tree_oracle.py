@@ -93,8 +93,10 @@ def unpack(mask, L):
     return np.stack([(words[..., j // 32] >> (j % 32)) & 1 for j in range(L)], axis=-1).astype(bool)
 
 
-def ref_tree(kind, q, cache, table, seq_lens, mask, dcp_size, interleave, block_size, scale, dv, q_lens=None):
-    """partial_out [N][B][L][Hq][dv], lse [N][B][L][Hq] and the merged out / out_lse of dcp_oracle."""
+def ref_tree(kind, q, cache, table, seq_lens, mask, dcp_size, interleave, block_size, scale, dv, q_lens=None,
+             rows=None):
+    """partial_out [N][B][L][Hq][dv], lse [N][B][L][Hq] and the merged out / out_lse of dcp_oracle
+    (``rows``: of these nodes alone, the others as empty)."""
     B, L, Hq, _ = q.shape
     sees = unpack(mask, L)
     o = np.zeros((dcp_size, B, L, Hq, dv))
@@ -110,7 +112,7 @@ def ref_tree(kind, q, cache, table, seq_lens, mask, dcp_size, interleave, block_
             if kind == "mla":
                 v = k[:, :, :dv]
             group = Hq // k.shape[1]
-            for i in range(n):
+            for i in range(n) if rows is None else rows:
                 keep = np.array([t < S - n or sees[b if len(sees) > 1 else 0, i, t - (S - n)] for t in tokens])
                 if not keep.any():
                     continue

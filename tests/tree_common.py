@@ -112,3 +112,11 @@ def to_gpu(t):
 
 __all__ = ["random_parents", "pack", "tree_case", "oracle_tree", "run_tree", "cell", "append_inputs", "to_gpu", "orc",
            "tro"]
+
+
+def oracle_rows(inst, mask, rows):
+    """oracle_tree of some of the nodes: their queries and mask rows, over the whole cache."""
+    w = inst.w
+    q, kv, bt, sl = H.oracle_inputs(inst)
+    return tro.ref_tree(w.kind, q, kv, bt, sl, mask, w.dcp_size, w.interleave, w.block_size, w.scale, w.head_dim_v,
+                        rows=rows)

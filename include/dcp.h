@@ -189,7 +189,8 @@ DCP_API dcp_status_t dcp_decode_attn(const dcp_attn_desc_t* d, const void* q, co
  *   LSE = m + log sum_r exp(lse_r - m),  m = max_r lse_r
  *   o   = sum_r exp(lse_r - LSE) * partial_out_r
  * out[r][b][i][h'] = o[b][i][r * Hq/dcp + h'] (bf16, round to nearest even).
- * All shards -inf gives out = 0 and out_lse = -inf.
+ * All shards -inf gives out = 0 and out_lse = -inf.  A NaN lse makes the merged row NaN;
+ * a shard of lse -inf is not read into the sum, whatever its partial row holds.
  *  partial_out fp32 [dcp][B][Lq][Hq][Dv], lse fp32 [dcp][B][Lq][Hq]
  *  out     bf16 [dcp][B][Lq][Hq/dcp][Dv] out
  *  out_lse fp32 [dcp][B][Lq][Hq/dcp] out, optional (NULL to skip)
@@ -382,13 +383,18 @@ DCP_API size_t dcp_tree_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dc
  * [dcp][B][Lq][Hq] per shard, for dcp_merge.  A row that sees no key of a shard, and every
  * row i >= n_b, gives partial_out = 0 and lse = -inf there.
  * Keys and values that a row does not see never reach it, whatever they hold (NaN,
- * infinities); those that it sees propagate as the formula has it.
+ * infinities).  A score that is not finite and not -inf makes its row NaN; a value entry
+ * that is not finite makes that entry of the output not finite (of a node's value, in the
+ * rows that see the node, and infinite where the formula has it so).
  *  tree_mask     uint32 [B][q_len][words], words = ceil(q_len / 32); requests lie
  *                tree_mask_stride words apart (0: one tree for all requests); bits of
  *                nodes >= n_b are ignored
  *  q_lens        int32 [B] or NULL
  *  workspace     >= dcp_tree_attn_workspace_size(d, dcp_size) bytes, 256-byte aligned; two
  *                calls (or two captured graphs) that may run at the same time need one each
+ * Accuracy: the bar of dcp_decode_attn.  The GQA tensor-core kernel rounds a probability to
+ * bf16 once (half a step is 2^-8 of it) unless it is above 2^-3 of its row's sum so far;
+ * those carry a second bf16 term, about 16 bits.  The MLA kernel is as there.
  * Errors: as dcp_decode_attn; UNSUPPORTED for q_len > DCP_TREE_MAX_NODES; INVALID_ARG for
  * tree_mask NULL, not 4-byte aligned, or a stride that is neither 0 nor >= q_len * words.
  * A block id >= num_blocks among a unit's visible keys skips the unit as there. */

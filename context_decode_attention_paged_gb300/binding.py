@@ -116,9 +116,9 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, device=None):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -246,15 +246,29 @@ def dcp_merge(partial_out, lse, dcp_size, out=None, out_lse=None, want_lse=True,
 # Speculative verify: rotary append, drafted-tree attention, commit
 # ---------------------------------------------------------------------------
 
+_bf16, _int32 = torch.bfloat16, torch.int32
+
+
 def _refuse(call, what):
     raise DcpError(DCP_ERR_INVALID_ARG, f"{call}: {what}")
 
 
-def _check_tensors(call, dtype, device, tensors):
+def _check_tensors(call, dtype, device, *tensors):
     """The tensors (None: skipped) are of ``dtype`` on ``device``, and contiguous."""
     for t in tensors:
         if t is not None and (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
             _refuse(call, f"a tensor is not a contiguous {dtype} tensor on the current device")
+
+
+def _check_lens(call, batch, device, *tensors):
+    """The tensors (None: skipped) are contiguous int32 [batch] on ``device``."""
+    shape = (batch,)
+    for t in tensors:
+        if t is not None:
+            if t.shape != shape:
+                _refuse(call, "lengths are [batch]")
+            if t.dtype is not _int32 or t.get_device() != device or not t.is_contiguous():
+                _refuse(call, f"a tensor is not a contiguous {_int32} tensor on the current device")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -284,12 +298,6 @@ def _cache_fields(call, kind, kv_cache, block_tables, batch, dcp_size):
     if len(tables) != 3 or tables[0] != dcp_size or tables[1] != batch:
         _refuse(call, "block_tables is [dcp_size][batch][max_local_blocks]")
     return kind, hkv, dim, bs, nb, tables[2]
-
-
-def _check_lens(call, batch, tensors):
-    for t in tensors:
-        if t is not None and (t.dim() != 1 or t.shape[0] != batch):
-            _refuse(call, "lengths are [batch]")
 
 
 @dataclasses.dataclass(frozen=True)
@@ -349,7 +357,7 @@ def tree_mask(parents):
 
 def _row_strides(call, t, device, shape):
     """(batch, token) strides in elements of rows [batch][n][...], each token's row contiguous."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != device:
+    if t.dtype is not _bf16 or t.get_device() != device:
         _refuse(call, "rows are bfloat16 on the current device")
     if t.shape != shape:
         _refuse(call, f"rows are {shape}, got {tuple(t.shape)}")
@@ -385,9 +393,9 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
     if (new_v is not None) != gqa:
         _refuse(call, "GQA takes new_v, MLA none")
     device = torch.cuda.current_device()
-    _check_tensors(call, torch.bfloat16, device, (kv_cache, None if q_out is q else q_out))
-    _check_tensors(call, torch.int32, device, (block_tables, seq_lens, q_lens, pos_offsets))
-    _check_lens(call, B, (seq_lens, q_lens))
+    _check_tensors(call, _bf16, device, kv_cache, None if q_out is q else q_out)
+    _check_tensors(call, _int32, device, block_tables, pos_offsets)
+    _check_lens(call, B, device, seq_lens, q_lens)
     steps = rope.steps
     if steps.get_device() != device:
         _refuse(call, "the rope table is not on the current device")
@@ -415,7 +423,7 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
         _cached_strides(k_batch, k_token, v_batch, v_token, q_batch, q_token), None if q is None else q_out.data_ptr(),
         None if pos_offsets is None else pos_offsets.data_ptr(), offsets_stride,
         None if q_lens is None else q_lens.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-        dcp_size, interleave, _stream(stream))
+        dcp_size, interleave, _stream(stream, device))
     if code != DCP_OK:
         raise DcpError(code, call)
     return kv_cache, q_out
@@ -455,9 +463,9 @@ def dcp_tree_attn(kind, q, kv_cache, block_tables, seq_lens, tree_mask, dcp_size
     if len(trees) != 3 or trees[0] not in (1, B) or trees[1] != Lq or trees[2] != words:
         _refuse(call, "tree_mask is [batch or 1][Lq][ceil(Lq / 32)]")
     device = torch.cuda.current_device()
-    _check_tensors(call, torch.bfloat16, device, (q, kv_cache))
-    _check_tensors(call, torch.int32, device, (block_tables, seq_lens, q_lens, tree_mask))
-    _check_lens(call, B, (seq_lens, q_lens))
+    _check_tensors(call, _bf16, device, q, kv_cache)
+    _check_tensors(call, _int32, device, block_tables, tree_mask)
+    _check_lens(call, B, device, seq_lens, q_lens)
     desc = _cached_desc(kind, B, Lq, Hq, hkv, Dqk, head_dim_v, bs, nb, max_lb)
     if partial_out is None or lse is None or workspace is None:
         # allocated for the stream that the kernels run on
@@ -469,7 +477,7 @@ def dcp_tree_attn(kind, q, kv_cache, block_tables, seq_lens, tree_mask, dcp_size
             size = int(_lib.dcp_tree_attn_workspace_size(desc, dcp_size))
             if workspace is None and size:
                 workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
-    _check_tensors(call, torch.float32, device, (partial_out, lse))
+    _check_tensors(call, torch.float32, device, partial_out, lse)
     if partial_out.numel() != dcp_size * B * Lq * Hq * head_dim_v or lse.numel() != dcp_size * B * Lq * Hq:
         _refuse(call, "partial_out is [N][B][Lq][Hq][Dv] and lse [N][B][Lq][Hq]")
     ws_bytes = 0
@@ -481,7 +489,7 @@ def dcp_tree_attn(kind, q, kv_cache, block_tables, seq_lens, tree_mask, dcp_size
         desc, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
         None if q_lens is None else q_lens.data_ptr(), tree_mask.data_ptr(), Lq * words if trees[0] == B else 0, dcp_size,
         interleave, scale, partial_out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        ws_bytes, _stream(stream))
+        ws_bytes, _stream(stream, device))
     if code != DCP_OK:
         raise DcpError(code, call)
     return partial_out, lse
@@ -501,13 +509,13 @@ def dcp_kv_cache_commit(kind, kv_cache, block_tables, seq_lens, q_len, accepted,
         with torch.cuda.stream(stream):
             new_seq_lens = torch.empty((B,), dtype=torch.int32, device=kv_cache.device)
     device = torch.cuda.current_device()
-    _check_tensors(call, torch.bfloat16, device, (kv_cache,))
-    _check_tensors(call, torch.int32, device, (block_tables, seq_lens, q_lens, accepted, num_accepted, new_seq_lens))
-    _check_lens(call, B, (seq_lens, q_lens, num_accepted, new_seq_lens))
+    _check_tensors(call, _bf16, device, kv_cache)
+    _check_tensors(call, _int32, device, block_tables, accepted)
+    _check_lens(call, B, device, seq_lens, q_lens, num_accepted, new_seq_lens)
     code = _lib.dcp_kv_cache_commit(
         _cached_desc(kind, B, q_len, hkv, hkv, dim, dim, bs, nb, max_lb), kv_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(),
-        max_accept, new_seq_lens.data_ptr(), dcp_size, interleave, _stream(stream))
+        max_accept, new_seq_lens.data_ptr(), dcp_size, interleave, _stream(stream, device))
     if code != DCP_OK:
         raise DcpError(code, call)
     return new_seq_lens

@@ -1088,7 +1088,19 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
         const uint32_t ring = uniform(smem_u32(stages)), full0 = uniform(smem_u32(&sm.kv_full[0]));
         int st = t_early % kStages;
         uint32_t ph = 0;                              // (t_early < kStages: the first lap)
+        // pool row of tile t, or of its block `lane` where a tile takes several
+        // (those past the key range read row 0 (masked, values zeroed) so that no
+        // stale table entry is followed), found a tile ahead; ids were checked
+        // against the pool above
+        auto row_of = [&](int t) {
+          const int j = u.kb + t * kNt + (kSmallBlocks ? lane * p.bs : 0);
+          if (kSmallBlocks && (lane * p.bs >= kNt || j >= u.ke)) return 0;
+          return bt_row[j / p.bs] * p.bs + (kSmallBlocks ? 0 : j % p.bs);
+        };
+        int next = t_early < T ? row_of(t_early) : 0;
         for (int t = t_early; t < T; ++t) {
+          const int row = next;
+          if (t + 1 < T) next = row_of(t + 1);
           if (!__all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&sm.kv_empty[st]), ph ^ 1u, p.wait_ns))) {
             if (lane == 0) fail();
             break;
@@ -1097,21 +1109,20 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
           // it run out and the unit unwinds)
           if (!(t == p.skip_tile && cta == 0)) {
             const uint32_t full = full0 + 8u * (uint32_t)st, dst = ring + (uint32_t)st * kStageBytes;
-            const int j = u.kb + t * kNt;              // (ids checked against the pool above)
             if (!kSmallBlocks) {
               // blocks of 64 tokens or a multiple: the tile is one box inside one block
-              const int row = bt_row[j / p.bs] * p.bs + (j % p.bs);
               if (lead) {
                 mbar_arrive_expect_tx(full, kStageBytes);
                 tma_load_3d(dst, &tm_lat, 0, row, 4 * (int)cta, full);
                 tma_load_2d(dst + 4 * kChunkBytes, &tm_rope, kLatent + 32 * (int)cta, row, full);
               }
-            } else if (lane == 0) {
-              // one box per block; boxes past the key range read pool row 0
-              // (masked, values zeroed) so that no stale table entry is followed
-              mbar_arrive_expect_tx(full, kStageBytes);
-              for (int k = 0; k < kNt / p.bs; ++k)
-                load_rows(stages + st * kStageBytes, k, j + k * p.bs < u.ke ? bt_row[j / p.bs + k] * p.bs : 0, full);
+            } else {
+              // one box per block
+              if (lane == 0) mbar_arrive_expect_tx(full, kStageBytes);
+              for (int k = 0; k < kNt / p.bs; ++k) {
+                const int to = __shfl_sync(0xffffffffu, row, k);
+                if (lane == 0) load_rows(stages + st * kStageBytes, k, to, full);
+              }
             }
             ++issued[st];
           }

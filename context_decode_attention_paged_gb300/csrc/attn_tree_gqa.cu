@@ -650,35 +650,43 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           break;
         }
         const int items = 2 * u.tiles(w);
-        if (lane == 0) {
-          const int32_t* bt = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
-          const int kb = u.kb, ke = u.ke, g = u.g;
-          for (int at = from; at < items; at += by) {
-            const unsigned item = item0 + (unsigned)at;
-            const int slot = rg.slot(item);
-            const uint32_t lap = rg.lap(item);
-            if (*abort_flag || (lap > 0 && !mbar_wait(smem_u32(&sm.empty[slot]), (lap - 1) & 1u, p.wait_ns))) {
-              ok = false;
-              break;
-            }
-            const int t = u.tile(w, at >> 1);
-            if (t == p.skip_tile && !(at & 1)) continue;    // test hook: a tile that never comes
-            const CUtensorMap* tm = (at & 1) ? &tm_v : &tm_k;
-            const uint32_t full = smem_u32(&sm.full[slot]);
-            uint8_t* dst = ring + slot * kTile;
-            mbar_arrive_expect_tx(full, kTile);
-            for (int k = 0; k < kNt; k += box_rows) {
-              const int j = kb + t * kNt + k;
-              // boxes past the key range read pool row 0 (masked, values zeroed)
-              const int row = j < ke ? bt[j / p.bs] * p.bs + j % p.bs : 0;
+        const int32_t* bt = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
+        const int kb = u.kb, ke = u.ke, g = u.g;
+        // pool row of box `lane` of key tile t (boxes past the key range read row
+        // 0: masked, values zeroed), found a tile ahead
+        auto row_of = [&](int t) {
+          const int j = kb + t * kNt + lane * box_rows;
+          return lane * box_rows < kNt && j < ke ? bt[j / p.bs] * p.bs + j % p.bs : 0;
+        };
+        int next = from < items ? row_of(u.tile(w, from >> 1)) : 0, row = 0;
+        for (int at = from; at < items; at += by) {
+          const unsigned item = item0 + (unsigned)at;
+          const int slot = rg.slot(item);
+          const uint32_t lap = rg.lap(item);
+          if (by == 2 || !(at & 1)) {                       // (V's rows are K's)
+            row = next;
+            if ((at >> 1) + 1 < items / 2) next = row_of(u.tile(w, (at >> 1) + 1));
+          }
+          if (!__all_sync(0xffffffffu, *abort_flag == 0 && (lap == 0 || mbar_wait(smem_u32(&sm.empty[slot]), (lap - 1) & 1u,
+                                                                                   p.wait_ns)))) {
+            ok = false;
+            break;
+          }
+          if (u.tile(w, at >> 1) == p.skip_tile && !(at & 1)) continue;    // test hook: a tile that never comes
+          const CUtensorMap* tm = (at & 1) ? &tm_v : &tm_k;
+          const uint32_t full = smem_u32(&sm.full[slot]);
+          uint8_t* dst = ring + slot * kTile;
+          if (lane == 0) mbar_arrive_expect_tx(full, kTile);
+          for (int k = 0; k < kNt; k += box_rows) {
+            const int to = __shfl_sync(0xffffffffu, row, k / box_rows);
+            if (lane == 0) {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(smem_u32(dst + c * (kNt * 128) + k * 128), tm, 64 * c, g, row, full);
+                tma_load_3d(smem_u32(dst + c * (kNt * 128) + k * 128), tm, 64 * c, g, to, full);
             }
-            end = item + 1;
           }
+          end = item + 1;
         }
-        ok = __all_sync(0xffffffffu, ok);
         item0 += (unsigned)items;
         if (warp == 3 && lane == 0) unit_done(n);
       }

@@ -200,7 +200,8 @@ int device_sm_count() {
 
 SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int units_per_split, int join_tiles) {
   SplitPlan p;
-  const long long max_local = (long long)a.max_lb * a.bs;
+  // (lengths are 32-bit, whatever the table could hold: a split's first token is too)
+  const long long max_local = std::min<long long>((long long)a.max_lb * a.bs, INT32_MAX);
   const long long base_units = (long long)a.N * a.B * units_per_split;
   const long long target = 2LL * sm_count;
   long long n = 1;

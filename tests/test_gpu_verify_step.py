@@ -122,3 +122,16 @@ def test_a_captured_verify_step_replays(name, kw, rope):
         assert torch.equal(s.out[0], out) and torch.equal(s.out[1], out_lse)
     assert torch.equal(s.kv, eager.kv) and torch.equal(s.lens, eager.lens)
     assert s.lens.tolist() == [800 + 3 * 3 + L, 511 + 2 * 3 + L, 100 + 3 + L]
+
+
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("name", ["mla_32", "qwen_gqa"])
+def test_a_table_wider_than_any_length(name, tree):
+    """2^20 entries of 4,096 tokens: the splits' first tokens stay 32-bit."""
+    inst, mask, _ = T.tree_case(name, 4, batch=1, lengths=("fixed", 9000), dcp_size=1, block_size=4096)
+    inst.block_tables = torch.nn.functional.pad(inst.block_tables, (0, (1 << 20) - inst.block_tables.shape[2]))
+    if tree:
+        check(inst, mask)
+    else:
+        from gpu_common import check_against_oracle
+        check_against_oracle(inst)

@@ -74,18 +74,19 @@
 // possible, so its running reference may stay -inf past the first tile.
 //
 // Measured (GB300, 2.07 GHz).  Tree, 32 requests of 4,096 to 67,000 tokens, 8
-// nodes of 128 heads: 1.08 ms, 0.94 PFLOP/s (1.02 TFLOP, 0.89 GB);
-// 200,000 tokens, 32 nodes: 1.41 ms, 1.27 PFLOP/s.  Decode, batch 512 (41.6 GB):
-// 8.2 ms, 5.1 TB/s.  Neither the tensor cores nor memory bind: a tile's MMAs
+// nodes of 128 heads: 1.06 ms, 0.96 PFLOP/s (1.02 TFLOP, 0.89 GB);
+// 200,000 tokens, 32 nodes: 1.37 ms, 1.30 PFLOP/s.  Decode, batch 512 (41.6 GB):
+// 7.8 to 8.1 ms, 5.1 to 5.3 TB/s.  Neither the tensor cores nor memory bind: a tile's MMAs
 // take ~1,200 cycles, a tile every ~1,900 comes out of a softmax warpgroup's
 // chain of ~3,900 (about 1,500 of them waits on the peer, on the other warpgroup
 // and on the MMAs) over two warpgroups.  Without the loads the tree case takes 4%
 // less, with a quarter of the MMAs 9%, with a quarter of the exchanged bytes 5%,
-// with both of these 13%.  A unit's start and end cost ~25,000 cycles.
-// Measured against it and slower: three softmax warpgroups (1.27 ms: five ring
+// with both of these 13%.  A unit's start and end cost ~23,000 cycles.
+// Measured against it (1.08 to 1.12 ms) and slower: three softmax warpgroups (1.27 ms: five ring
 // stages do not feed them), two message slots with four stages (1.28), an L2
 // prefetch before each load (1.23), references agreed on after the exponentials
-// (two messages a tile, 1.14), slots freed before the P buffer is (1.09).
+// (two messages a tile, 1.14), slots freed before the P buffer is (1.09), score
+// MMAs that start on half a stage (1.10).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stddef.h>
@@ -899,7 +900,7 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
   const int k_req = kLpt ? (int)(unit / per_req) : 0;
   if (kLpt && !ranks && tid == 0) sm.req = p.order[k_req];
   __syncthreads();
-  cluster_arrive();          // this CTA's barriers are initialised (the peer waits below)
+  cluster_arrive_relaxed();  // this CTA's barriers are initialised and fenced (the peer waits below)
   int b_lpt = 0;
   if (kLpt) {
     if (ranks && rt >= 0 && rt < p.B) {
@@ -925,6 +926,14 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
     if constexpr (kTree) u.i_q *= p.nodes;                   // the unit's first node
     u.r = kLpt ? (int)q : (int)(q / (unsigned)p.B);
     u.b = kLpt ? b_lpt : (int)(q - (unsigned)u.r * (unsigned)p.B);
+  }
+  // the early tiles' blocks, one a lane: read while the key range is found
+  const int32_t* bt_row = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
+  const int early_step = kSmallBlocks ? p.bs : kNt;
+  int early_id = 0;
+  if (warp == 0 && lane * early_step < (kStages - 2) * kNt) {
+    const unsigned jb = ((unsigned)u.s_idx * (unsigned)p.split_tokens + (unsigned)(lane * early_step)) / (unsigned)p.bs;
+    if (jb < (unsigned)p.max_lb) early_id = bt_row[jb];
   }
   // key range of this unit (shard-local indices [kb, ke))
   const int S = ranks ? lens[u.b] : p.seq_lens[u.b];
@@ -958,7 +967,6 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
   // TMA producer state (warp 0, lane 0): the query and the first stages are on
   // their way while the set-up goes on
   volatile int* abort_flag = &sm.abort;
-  const int32_t* bt_row = p.block_tables + ((long long)u.r * p.B + u.b) * p.max_lb;
   int issued[kStages];
 #pragma unroll
   for (int k = 0; k < kStages; ++k) issued[k] = 0;
@@ -981,13 +989,11 @@ mla_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constan
   uint8_t* qstage = stages + (kStages - 2) * kStageBytes;
   const int t_early = min(u.T, kStages - 2);
   if (warp == 0 && u.T > 0) {
-    // the early tiles' blocks, one a lane (the scan of the table runs meanwhile:
-    // an id outside the pool keeps the early loads from going out here, and
-    // ends the unit there)
-    const int step = kSmallBlocks ? p.bs : kNt;
-    const int j = u.kb + lane * step;
-    const bool mine = lane * step < t_early * kNt && j < u.ke;
-    const int id = mine ? bt_row[j / p.bs] : 0;
+    // (the scan of the table runs meanwhile: an id outside the pool keeps the
+    // early loads from going out here, and ends the unit there)
+    const int j = u.kb + lane * early_step;
+    const bool mine = lane * early_step < t_early * kNt && j < u.ke;
+    const int id = mine ? early_id : 0;
     const int row = id * p.bs + (mine && !kSmallBlocks ? j % p.bs : 0);
     if (lane == 0) {
       const int32_t qr = (int32_t)(((long long)u.b * p.Lq + u.i_q) * p.Hq);

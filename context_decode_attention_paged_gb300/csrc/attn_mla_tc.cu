@@ -1288,11 +1288,14 @@ static int tree_nodes(const AttnArgs& a) {
 
 SplitPlan plan_attn_mla_tc(const AttnArgs& a, int sm_count) {
   const int nodes = tree_nodes(a);
-  // A drafted tree has few, equal units of many tiles: the last of 3.4 waves
+  // A drafted tree may have few, equal units of many tiles: the last of 3.4 waves
   // leaves the SMs idle for as long as the first three take, and two splits of
-  // each unit (6.7 waves of half the length) end sooner.  A split writes and
-  // rereads 2 x 256 KB of partial rows, the time of about 5 tiles.
-  SplitPlan pl = plan_splits(a, sm_count, kNt, 2 * ((a.Lq + nodes - 1) / nodes), a.tree_words > 0 ? 5 : 0);
+  // each unit (6.7 waves of half the length) end sooner (200,000 tokens, 32 nodes:
+  // 1,525 -> 1,417 us), although starting one costs about 12 tiles and writing and
+  // rereading 2 x 256 KB of partial rows 5.  Units that are shorter lose (33
+  // requests, 102 tiles: 282 us whole, 341 in two).
+  const int units = 2 * ((a.Lq + nodes - 1) / nodes);
+  SplitPlan pl = a.tree_words > 0 ? plan_splits(a, sm_count, kNt, units, 12, 5) : plan_splits(a, sm_count, kNt, units);
   if (a.B > kLptMaxBatch && a.B <= kLptOrderMaxBatch) {
     pl.lpt_order = true;
     pl.order_offset = (pl.ws_bytes + 255) & ~size_t(255);

@@ -856,7 +856,14 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 }
 
 int rows_of(const AttnArgs& a) { return a.Lq * (a.Hq / a.Hkv); }
-int block_rows_of(const AttnArgs& a) { return rows_of(a) > kNt ? 2 * kNt : kNt; }
+// Rows of a block.  Pairs of 128 share a key tile; with three or five of them the
+// odd one would hold an SM for a pair's time (330 rows: 195 us in pairs, 162 in
+// turn; 576 rows: 177 and 128), with more the passes over the cache count for more
+// (29: 242 us in pairs, 261 in turn).
+int block_rows_of(const AttnArgs& a) {
+  const int n = (rows_of(a) + kNt - 1) / kNt;
+  return n == 1 || n == 3 || n == 5 ? kNt : 2 * kNt;
+}
 int row_blocks_of(const AttnArgs& a) { return (rows_of(a) + block_rows_of(a) - 1) / block_rows_of(a); }
 
 template <int D>

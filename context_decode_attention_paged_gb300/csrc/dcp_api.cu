@@ -198,7 +198,8 @@ int device_sm_count() {
   return n;
 }
 
-SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int units_per_split, int join_tiles) {
+SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int units_per_split, int start_tiles,
+                      int join_tiles) {
   SplitPlan p;
   // (lengths are 32-bit, whatever the table could hold: a split's first token is too)
   const long long max_local = std::min<long long>((long long)a.max_lb * a.bs, INT32_MAX);
@@ -206,22 +207,26 @@ SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int unit
   const long long target = 2LL * sm_count;
   long long n = 1;
   const bool small = base_units < target;
-  if ((small || (join_tiles > 0 && base_units < 8 * target)) && max_local > 4LL * tile_tokens) {
+  if ((small || (start_tiles > 0 && base_units < 8 * target)) && max_local > 4LL * tile_tokens) {
     // Split count by a wave model: units run in waves of sm_count CTAs and a
     // unit costs its tiles plus about kUnitStartTiles of start-up and drain,
     // so pick the count with the fewest waves x (tiles per split + start-up).
+    // Drafted trees, whose kernels take units longest first, take the largest
+    // count within 2% of that: more units even out requests of unlike lengths.
     constexpr long long kUnitStartTiles = 4;
     const long long tiles = (max_local + tile_tokens - 1) / tile_tokens;
     const long long n_hi = std::max<long long>(1, std::min<long long>(small ? 32 : 4, max_local / (4LL * tile_tokens)));
-    long long best = -1;
-    for (long long c = 1; c <= n_hi; ++c) {
+    auto cost = [&](long long c) {
       const long long waves = (base_units * c + sm_count - 1) / sm_count;
-      const long long join = !small && c > 1 ? join_tiles : 0;
-      const long long cost = waves * ((tiles + c - 1) / c + kUnitStartTiles + join);
-      if (best < 0 || cost < best) {
-        best = cost;
-        n = c;
-      }
+      const long long extra = small ? kUnitStartTiles : start_tiles + (c > 1 ? join_tiles : 0);
+      return waves * ((tiles + c - 1) / c + extra);
+    };
+    for (long long c = 2; c <= n_hi; ++c)
+      if (cost(c) < cost(n)) n = c;
+    if (small && a.tree_words > 0) {
+      const long long limit = cost(n) + cost(n) / 50;
+      for (long long c = n + 1; c <= n_hi; ++c)
+        if (cost(c) <= limit) n = c;
     }
   }
   long long per = (max_local + n - 1) / n;

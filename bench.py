@@ -82,9 +82,9 @@ def algorithmic(w: wl.Workload, seq_lens) -> dict:
 # source the counters were taken on: once the source changes, traffic is
 # reported as null.
 NCU_TRAFFIC_RATIO = {
-    "mla": ("9447a4f56c1331f7", 1.00602, "attn_mla_tc.cu"),
+    "mla": ("f62d43de02f9f18b", 1.00602, "attn_mla_tc.cu"),
     "gqa": ("f6e04d4ccaedbfff", 1.00386, "attn_gqa_tc.cu"),
-    "mla_chunk64": ("9447a4f56c1331f7", 1.04774, "attn_mla_tc.cu"),
+    "mla_chunk64": ("f62d43de02f9f18b", 1.04165, "attn_mla_tc.cu"),
 }
 
 

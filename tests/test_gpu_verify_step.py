@@ -135,3 +135,18 @@ def test_a_table_wider_than_any_length(name, tree):
     else:
         from gpu_common import check_against_oracle
         check_against_oracle(inst)
+
+
+@pytest.mark.parametrize("name,L,kw,opt", [
+    ("qwen_gqa", 20, dict(batch=3, lengths=("uniform", 100, 900), dcp_size=2), dict(q_lens=[20, 5, 0])),
+    ("qwen_gqa", 40, dict(batch=2, lengths=("uniform", 100, 900), dcp_size=2, interleave=1),
+     dict(q_lens=[40, 9], mask="random")),
+    ("qwen_gqa", 33, dict(batch=2, num_q_heads=40, lengths=("uniform", 100, 1500), dcp_size=1), dict(q_lens=[33, 13])),
+    ("qwen_gqa", 33, dict(batch=1, num_q_heads=40, lengths=("fixed", 33), dcp_size=2), {}),
+    ("qwen_gqa", 19, dict(batch=2, num_q_heads=64, num_kv_heads=2, lengths=("uniform", 100, 1500)), {}),
+    ("tiny_gqa", 150, dict(batch=2, lengths=("uniform", 150, 600), dcp_size=2), dict(q_lens=[150, 31])),
+])
+def test_odd_numbers_of_row_blocks(name, L, kw, opt):
+    """Three and five blocks of 128 rows, the last one partly there, nodes that lie across two
+    blocks, and requests that end before a block."""
+    check(*T.tree_case(name, L, **kw, **opt))

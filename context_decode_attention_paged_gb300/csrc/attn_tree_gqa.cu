@@ -150,7 +150,8 @@ struct Ring {
 
 struct Smem {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], q_full, drain[2];   // [stream][step parity]
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_full[2], drain[2];   // [stream][step parity]
+  uint64_t q_full[2];              // by unit parity: see the issuers
   uint64_t unit_full[2], unit_free[2];
   uint32_t tmem_base;
   int abort;
@@ -570,10 +571,10 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       mbar_init(smem_u32(&sm.pv_done[k]), 1);
       mbar_init(smem_u32(&sm.o_full[k]), 1);
       mbar_init(smem_u32(&sm.drain[k]), 1);
+      mbar_init(smem_u32(&sm.q_full[k]), 8);         // softmax warps
       mbar_init(smem_u32(&sm.unit_full[k]), 1);
       mbar_init(smem_u32(&sm.unit_free[k]), 11);     // a producer, two issuers, eight softmax warps
     }
-    mbar_init(smem_u32(&sm.q_full), 8);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -704,7 +705,14 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       // PV(s), then the scores of step s + 2, whose buffer P(s) leaves.  The
       // whole warp runs the loop on uniform values and one lane issues: with a
       // single lane in the loop each MMA cost 65-90 clocks to issue, as long as
-      // it runs
+      // it runs.
+      // The query's barrier goes by the unit's parity.  In turn a stream may have
+      // no step in a unit (one tile) and pass it while its query is still being
+      // staged; on one barrier its next wait would then be a phase ahead of the
+      // open one and pass at once, and if it waited for the unit it has no part
+      // in, the other stream could be two phases on before it looks.  A unit is
+      // published only when the one two before it has left, so on its own barrier
+      // every earlier phase is over, and the next one needs this stream's output.
       const int w = (int)uniform((uint32_t)warp - 1u);
       constexpr uint32_t id_qk = idesc_bf16(128, kNs, false);
       constexpr uint32_t id_pv = idesc_bf16(128, D, true);
@@ -716,6 +724,7 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const uint32_t full = uniform(smem_u32(&sm.full[0])), empty = uniform(smem_u32(&sm.empty[0]));
       const uint32_t s_full = uniform(smem_u32(&sm.s_full[w][0])), p_full = uniform(smem_u32(&sm.p_full[w][0]));
       const uint32_t pv_done = uniform(smem_u32(&sm.pv_done[w])), o_full = uniform(smem_u32(&sm.o_full[w]));
+      const uint32_t q_full = uniform(smem_u32(&sm.q_full[0]));
       // cursors over the K and the V tiles: slot and lap parity (a tile serves two steps)
       struct Cursor {
         int slot;
@@ -733,7 +742,7 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       };
       Cursor kc = {first, 0u}, vc = {first + 1, 0u};
       unsigned step0 = 0;                   // steps before this unit
-      uint32_t q_par = 0;
+      uint32_t q_par = 0;                   // bit n & 1: parity of that barrier's next phase
       bool ok = true;
       for (int n = 0; ok; ++n) {
         if (unit_of(p, n) < 0) break;
@@ -785,10 +794,10 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           if (done) next(vc);
           return true;
         };
-        if (steps > 0) ok = wait(smem_u32(&sm.q_full), q_par) && qk(0) && (steps < 2 || qk(1));
+        if (steps > 0) ok = wait(q_full + 8 * (n & 1), (q_par >> (n & 1)) & 1u) && qk(0) && (steps < 2 || qk(1));
         for (int s = 0; s < steps && ok; ++s) ok = pv(s) && (s + 2 >= steps || qk(s + 2));
         step0 += (unsigned)steps;
-        q_par ^= runs ? 1u : 0u;
+        q_par ^= runs ? 1u << (n & 1) : 0u;
       }
       if (!ok) fail();
       if (lead) mma_commit(smem_u32(&sm.drain[w]));
@@ -833,7 +842,7 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[n & 1]));
       }
       ok = stream<D>(p, sm, u, sm.odd[n & 1], st, qs, ring, tmem, warp, lane);
       __syncwarp();

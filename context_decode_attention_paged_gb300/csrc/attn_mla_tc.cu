@@ -510,9 +510,11 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     // the P buffer and O: PV(t-1) must be done (it implies every earlier PV,
     // and the wait for PV(t-3) before tile t-2's P keeps the parity unambiguous)
     if (t >= 1 && !wwait(smem_u32(&sm.pv_done[xb ^ 1]), (uint32_t)((t - 1) >> 1) & 1u)) { ok = false; break; }
-    // O moves from R(t-1) to R(t) (rare)
-    const float alpha = ex2(r_prev - R);
+    // O moves from R(t-1) to R(t) (rare; the whole warp does when one of its rows
+    // moves, and a kTree row that has seen nothing yet stays at -inf, whose
+    // difference would be NaN)
     if (t >= 1 && __any_sync(0xffffffffu, R != r_prev)) {
+      const float alpha = kTree && R == r_prev ? 1.f : ex2(r_prev - R);
       tc_fence_after();
       for (int c = 0; c < 256; c += 32) {
         uint32_t v[32];

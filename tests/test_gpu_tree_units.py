@@ -53,3 +53,46 @@ def test_units_of_one_step_between_long_ones(name, L, kw, length):
     for key in ("partial_out", "lse", "out", "out_lse"):
         got[key] = np.ascontiguousarray(got[key][:, few])
     check(part, np.ascontiguousarray(mask[few]), got=got)
+
+
+# ---------------------------------------------------------------------------
+# MLA: rows of several nodes in one warp, tiles that only some of them see anything of
+# ---------------------------------------------------------------------------
+
+def mla_nodes(L, heads, sees, **kw):
+    inst, _, _ = T.tree_case("mla_32", L, batch=1, num_q_heads=heads, **kw)
+    return inst, T.pack(sees)
+
+
+@pytest.mark.parametrize("heads", [16, 24, 40, 48, 56, 64, 128])
+def test_a_row_waits_tiles_for_its_first_key(heads):
+    """256 nodes without context, four tiles: node 200 sees a key of the second tile, its neighbours
+    in the warp none before the fourth."""
+    L = 256
+    sees = np.eye(L, dtype=bool)[None]
+    sees[0, 200, 70] = True
+    check(*mla_nodes(L, heads, sees, lengths=("fixed", L), dcp_size=1))
+
+
+@pytest.mark.parametrize("heads", [16, 24, 40, 48, 56])
+@pytest.mark.parametrize("dcp_size,interleave", [(1, 128), (2, 1)])
+def test_rows_that_see_nothing_are_zero_among_rows_that_do(heads, dcp_size, interleave):
+    """Two tiles of node keys a shard; odd nodes see nothing at all."""
+    L = 128 * dcp_size
+    sees = np.eye(L, dtype=bool)[None]
+    sees[0, 1::2] = False
+    inst, mask = mla_nodes(L, heads, sees, lengths=("fixed", L), dcp_size=dcp_size, interleave=interleave)
+    got = check(inst, mask)
+    assert (got["partial_out"][:, :, 1::2] == 0).all() and (got["lse"][:, :, 1::2] == -np.inf).all()
+
+
+@pytest.mark.parametrize("L,length", [(256, 560), (200, 520), (256, 576)])
+def test_sparse_masks_over_splits_that_start_among_the_nodes(L, length):
+    """Two KV splits of 320 keys: the second starts with a node."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    sees = np.random.default_rng(5).random((1, L, L)) < 0.01
+    inst, mask = mla_nodes(L, 16, sees, lengths=("fixed", length), dcp_size=1)
+    desc = dcp.desc_from_tensors("mla", inst.q, inst.kv_cache, inst.block_tables, 512)
+    rows = L * 16
+    assert dcp.dcp_tree_attn_workspace_size(desc, 1) == rows * 2 * 512 * 4 + rows * 2 * 4
+    check(inst, mask)

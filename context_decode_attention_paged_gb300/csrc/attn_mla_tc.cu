@@ -66,11 +66,13 @@
 // keys serves them all.  Tiles of context keys alone take no mask; in the others
 // a thread has a 32-bit word that says which tokens of its half its row sees.
 // Hidden tokens are dropped from the softmax as the tokens past a ragged end
-// are, and their scores do not reach the exchange's scale; a score that is not
-// finite is sent as a NaN scale, so that the row becomes NaN as the formula has
-// it.  Node values that are not finite would reach every row through the
-// product: such entries are replaced by 0 in shared memory and added in the
-// epilogue to the rows that see them.  Tiles that a row sees nothing of are
+// are, and their scores do not reach the exchange's scale.  A head with a partial
+// score that is not finite in a tile sends the upper halves of its partials' bits
+// in place of the codes, with a scale of 0, and the lower halves in place of the
+// residual: a score of -inf then weighs 0 and one of +inf or NaN makes the row NaN,
+// as the formula has it.  Node values that are not finite would reach every row
+// through the product: such entries are replaced by 0 in shared memory and added
+// in the epilogue to the rows that see them.  Tiles that a row sees nothing of are
 // possible, so its running reference may stay -inf past the first tile.
 //
 // Measured (GB300, 2.07 GHz).  Tree, 32 requests of 4,096 to 67,000 tokens, 8
@@ -367,7 +369,8 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     {
       const uint8_t* slot = scbuf;
       float dec = reinterpret_cast<const float*>(slot + kMsgCodes)[h];
-      const bool flagged = dec < 0.f;               // same for every head of the tile
+      // (same for every head of the warp; by the sign bit: the scale may be a zero)
+      const bool flagged = kTree ? __float_as_int(dec) < 0 : dec < 0.f;
       dec = fabsf(dec);
       const float bias = -kDecBias * dec;
 #pragma unroll
@@ -384,7 +387,18 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
       if (__any_sync(0xffffffffu, flagged)) {
         // large partials of this warp's heads: the 16-bit residual of every
         // code follows in the same slot once this warp has read the codes
-        const unsigned used = __ballot_sync(0xffffffffu, x[0] + x[31] > 0.f);
+        bool seen_codes = false;
+        uint32_t upper[16];
+        if constexpr (kTree) {
+          // of a head whose partials come as they are (the codes added nothing)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 q4 = reinterpret_cast<const uint4*>(slot)[k * kHeads + h];
+            upper[4 * k] = q4.x, upper[4 * k + 1] = q4.y, upper[4 * k + 2] = q4.z, upper[4 * k + 3] = q4.w;
+          }
+          seen_codes = (upper[3] ^ upper[7] ^ upper[11] ^ upper[15]) == 1u;
+        }
+        const unsigned used = __ballot_sync(0xffffffffu, x[0] + x[31] > 0.f || seen_codes);
         asm volatile("" :: "r"(used));
         if (lane == 0) {
           mbar_arrive_expect_tx(smem_u32(&sm.sc_res[w][lg]), 32 * 4 * 16);
@@ -406,14 +420,32 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
             x[8 * k + 2 * j + 1] = s.y;
           }
         }
+        if (kTree && __any_sync(0xffffffffu, dec == 0.f)) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 q4 = reinterpret_cast<const uint4*>(rs)[k * kHeads + h];
+            const uint32_t wq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t lo = wq[j], up = upper[4 * k + j];
+              x[8 * k + 2 * j] += dec == 0.f ? __uint_as_float(__byte_perm(lo, up, 0x5410)) : 0.f;
+              x[8 * k + 2 * j + 1] += dec == 0.f ? __uint_as_float(__byte_perm(lo, up, 0x7632)) : 0.f;
+            }
+          }
+        }
       }
     }
     // local maximum of the valid tokens (log2 units)
-    int valid = 0;
-    uint32_t seen = 0;
+    int valid = kHalf;
     if constexpr (kTree) {
-      seen = seen_of_half(p, u, view, t, (int)cta);
-      valid = __all_sync(0xffffffffu, seen == 0xffffffffu) ? kHalf : 0;
+      // hidden tokens drop out as scores of -inf (a second copy of the maximum and
+      // the exponentials would not fit the instruction cache beside the rest)
+      const uint32_t seen = seen_of_half(p, u, view, t, (int)cta);
+      if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (!((seen >> k) & 1u)) x[k] = -INFINITY;
+      }
     } else {
       valid = valid_of_half(u, t, (int)cta);
     }
@@ -425,7 +457,7 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
         for (int j = 0; j < 4; ++j) m4[j] = fmax3(m4[j], x[k + j], x[k + 4 + j]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], (kTree ? ((seen >> k) & 1u) != 0 : k < valid) ? x[k] : -INFINITY);
+      for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], k < valid ? x[k] : -INFINITY);
     }
     const float ml = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
     // every received score has been used (the maximum depends on all of
@@ -455,7 +487,7 @@ __device__ __forceinline__ void softmax_wg(const MlaParams& p, const CUtensorMap
     } else {
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        e[k] = (kTree ? ((seen >> k) & 1u) != 0 : k < valid) ? ex2(fmaf(x[k], sl2, nml)) : 0.f;
+        e[k] = k < valid ? ex2(fmaf(x[k], sl2, nml)) : 0.f;
         l4[k & 3] += e[k];
       }
     }
@@ -763,7 +795,7 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
       }
     }
     float amax;
-    bool odd = false;            // some score of this head is not finite
+    bool raw = false;            // some partial of this head is not finite
     if constexpr (kTree) {
       // the largest magnitude as bits: infinities and NaN lie above every finite value
       uint32_t b8[8];
@@ -774,8 +806,8 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
 #pragma unroll
         for (int j = 0; j < 8; ++j) b8[j] = max(b8[j], v[k + j] & 0x7fffffffu);
       const uint32_t top = max(max(max(b8[0], b8[1]), max(b8[2], b8[3])), max(max(b8[4], b8[5]), max(b8[6], b8[7])));
-      odd = top >= 0x7f800000u;
-      amax = odd ? 0.f : __uint_as_float(top);
+      raw = top >= 0x7f800000u;
+      amax = __uint_as_float(top);
     } else {
       float a8[8];
 #pragma unroll
@@ -786,11 +818,17 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
         for (int j = 0; j < 8; ++j) a8[j] = fmaxf(a8[j], fabsf(__uint_as_float(v[k + j])));
       amax = fmaxf(fmaxf(fmaxf(a8[0], a8[1]), fmaxf(a8[2], a8[3])), fmaxf(fmaxf(a8[4], a8[5]), fmaxf(a8[6], a8[7])));
     }
-    // large partials in this warp's heads: the residual follows (same for the warp)
-    const bool flag = __any_sync(0xffffffffu, amax * sl2 > kResidualLog2);
+    // large partials in this warp's heads, or some that are not finite: the
+    // residual follows (same for the warp)
+    const bool flag = __any_sync(0xffffffffu, (kTree && raw) || amax * sl2 > kResidualLog2);
     float enc, dec;
     bfp_scales(amax, enc, dec);
-    if (odd) dec = NAN;
+    // the 16-bit codes of two partials, or of a raw head their upper halves
+    auto codes = [&](int k) {
+      const uint32_t w = bfp_pack2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), enc);
+      return __uint_as_float(kTree && raw ? __byte_perm(v[k], v[k + 1], 0x7632) : w);
+    };
+    if (kTree && raw) dec = 0.f;
     // the peer has read tile t-1 out of its one slot
     if (t >= 1 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.sc_free[(t - 1) & 1][lg]), (uint32_t)((t - 1) >> 1) & 1u, p.wait_ns))) {
       bad = true;
@@ -800,12 +838,7 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
     // chunk k carries tokens [8k, 8k + 8): two per word
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      st_async_v4(peer_x + k * (kHeads * 16),
-                  __uint_as_float(bfp_pack2(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1]), enc)),
-                  __uint_as_float(bfp_pack2(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3]), enc)),
-                  __uint_as_float(bfp_pack2(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5]), enc)),
-                  __uint_as_float(bfp_pack2(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]), enc)),
-                  bar);
+      st_async_v4(peer_x + k * (kHeads * 16), codes(8 * k), codes(8 * k + 2), codes(8 * k + 4), codes(8 * k + 6), bar);
     st_async_b32(peer_xs, __float_as_uint(flag ? -dec : dec), bar);
     if (flag) {
       // once the peer's warp has read the codes: the residual of every code,
@@ -826,6 +859,7 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
           const float a = __uint_as_float(v[8 * k + 2 * j]), b = __uint_as_float(v[8 * k + 2 * j + 1]);
           const float2 q = bfp_round2(a, b, enc, dec);
           wd[j] = bfp_pack2(a - q.x, b - q.y, enc_r);
+          if (kTree && raw) wd[j] = __byte_perm(v[8 * k + 2 * j], v[8 * k + 2 * j + 1], 0x5410);
         }
         st_async_v4(peer_x + k * (kHeads * 16), __uint_as_float(wd[0]), __uint_as_float(wd[1]),
                     __uint_as_float(wd[2]), __uint_as_float(wd[3]), barr);

@@ -10,7 +10,10 @@
 // loads; the N weights come from one lse load per lane and warp shuffles.  A warp
 // has four sources in flight, the first four requested before the weights are
 // known.  Measured (GB300): 512 x 128 rows of 8 sources of 512 floats (1.14 GB)
-// 0.166 ms, 6.9 TB/s; source after source it was 0.201 ms.
+// 0.166 ms, 6.9 TB/s; source after source it was 0.201 ms.  Sources behind the last
+// that counts are not read: with 2 of the 8 holding keys (requests of a few tokens)
+// 0.065 ms, 0.166 if all are read.  Five blocks an SM (48 registers) matter: with
+// 60 registers, four, 1024 x 64 rows of 4 sources of 128 floats take 35 us, not 31.
 #include "dcp_device.cuh"
 #include "dcp_internal.h"
 
@@ -52,11 +55,14 @@ __device__ __forceinline__ void load_batch(const float* __restrict__ src, long l
 // out row = sum over n sources (stride src_stride floats) of w_k * src_k.
 // Dv4 = Dv / 4 float4 per row.  Loads go out kBatch sources at a time, the first
 // ones (in `v`, vector `lane`) before the weights are known; a source of weight
-// 0 is not looked at, whatever it holds.
+// 0 does not count, whatever it holds.
 template <bool kBf16Out>
 __device__ __forceinline__ void weighted_row(const float* __restrict__ src, long long src_stride,
                                              int n, float w_lane, int Dv4, float4 (&v)[kBatch], void* dst_row) {
   const int lane = threadIdx.x & 31;
+  // tokens and splits are dealt from the first source on, so those without keys are
+  // the last ones
+  n = 32 - __clz(__ballot_sync(0xffffffffu, w_lane != 0.f));
   for (int c = lane; c - lane < Dv4; c += 32) {
     const bool in = c < Dv4;                         // (the shuffles below take the whole warp)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -88,7 +94,7 @@ __device__ __forceinline__ void weighted_row(const float* __restrict__ src, long
 }
 
 // One warp per (b, i, h): merge N shard partials; write rank h / (Hq/N)'s slice.
-__global__ void __launch_bounds__(kWarpsPerBlock * 32)
+__global__ void __launch_bounds__(kWarpsPerBlock * 32, 5)
 merge_kernel(const float* __restrict__ partial_out, const float* __restrict__ lse, int N, int B,
              int Lq, int Hq, int Dv, __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse) {
   const long long row = (long long)blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
@@ -113,7 +119,7 @@ merge_kernel(const float* __restrict__ partial_out, const float* __restrict__ ls
 }
 
 // One warp per (r, b, i, h): merge n_split workspace partials into partial_out.
-__global__ void __launch_bounds__(kWarpsPerBlock * 32)
+__global__ void __launch_bounds__(kWarpsPerBlock * 32, 5)
 split_combine_kernel(const float* __restrict__ ws_o, const float* __restrict__ ws_lse, int n_split,
                      long long rows, int Hq, int Dv, float* __restrict__ partial_out,
                      float* __restrict__ lse) {

@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
     if (tid == 0) set_status(a.status, DCP_ERR_BOUNDS);
     L = a.max_lb * a.bs;
   }
+  if (kTree && tree.n == 0) L = 0;                   // (its table is not read: a padded request may have none)
   const int j_begin = min(L, s * P.split_tokens);
   int j_end = min(L, j_begin + P.split_tokens);
   {

@@ -633,10 +633,12 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             break;
           }
           Unit v = make_unit(p, sm, index);
-          // a block id past the pool among the shard's keys skips the unit
+          // a block id past the pool among the shard's keys skips the unit, and with
+          // it every row of the request in the shard (without a row to attend, as in
+          // a padded request, the table is not read)
           const int32_t* bt = p.block_tables + ((long long)v.r * p.B + v.b) * p.max_lb;
           bool bad_blk = false;
-          for (int jb = lane; jb < (v.L + p.bs - 1) / p.bs; jb += 32) bad_blk |= (unsigned)bt[jb] >= (unsigned)p.num_blocks;
+          for (int jb = lane; v.R > 0 && jb < (v.L + p.bs - 1) / p.bs; jb += 32) bad_blk |= (unsigned)bt[jb] >= (unsigned)p.num_blocks;
           bad_blk = __any_sync(0xffffffffu, bad_blk);
           if (bad_blk) v.T = 0;
           if (lane < 8) sm.odd[n & 1][lane] = 0;

@@ -397,7 +397,9 @@ DCP_API size_t dcp_tree_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dc
  * those carry a second bf16 term, about 16 bits.  The MLA kernel is as there.
  * Errors: as dcp_decode_attn; UNSUPPORTED for q_len > DCP_TREE_MAX_NODES; INVALID_ARG for
  * tree_mask NULL, not 4-byte aligned, or a stride that is neither 0 nor >= q_len * words.
- * A block id >= num_blocks among a unit's visible keys skips the unit as there. */
+ * A block id >= num_blocks among the keys that a shard holds of a request sets
+ * DCP_ERR_BOUNDS on the device and leaves all of the request's rows in that shard 0 and
+ * -inf.  Of a request without nodes (n_b = 0) the lengths alone are read. */
 DCP_API dcp_status_t dcp_tree_attn(const dcp_attn_desc_t* d, const void* q, const void* kv_cache,
                                    const int32_t* block_tables, const int32_t* seq_lens,
                                    const int32_t* q_lens, const uint32_t* tree_mask,

@@ -22,8 +22,8 @@
 // every block first sums the counts (up to kScan requests; when there are more
 // tasks than the SMs hold at once) and a warp finds its token in the sums.
 // Rotated parts whose vectors do not divide a warp (rot_dim 96 in the half
-// layout, say) or do not fall on vectors go unit by unit with the angles in
-// shared memory, one block a token.
+// layout, say) or do not fall on vectors, and heads of 65,000 dims and more, go
+// unit by unit with the angles in shared memory, one block a token.
 //
 // Measured (GB300; time in a graph): 64 tokens of 64 + 4 + 4 heads of 128 (2.4 MB
 // moved) 6.5 us, launch and dependent loads; 512 tokens of 128 + 1 heads of 576
@@ -371,7 +371,10 @@ cudaError_t launch_kv_append(const AppendArgs& a) {
   const int copies = p.units_rot - p.turned;
   p.per_copies = copies > 1 ? (unsigned)(((1ull << 32) + copies - 1) / copies) : 0u;
   p.units_total = (p.a.Hq + a.Hkv) * p.units_rot + (a.v ? a.Hkv * (vec ? a.D / 8 : a.D) : 0);
-  if (vec && p.turned <= 32 && 32 % p.turned == 0) {
+  // per_copies finds the quotient of a vector number below 2^32 / copies; a task has
+  // at most about two passes of heads, or kTaskBytes, of vectors
+  auto quotients_fit = [&]() { return (2LL * (32 / p.turned) * copies + kTaskBytes / 8) * copies < (1LL << 32); };
+  if (vec && p.turned <= 32 && 32 % p.turned == 0 && quotients_fit()) {
     // heads of a task: up to kTaskBytes of rows, fewer when the tokens alone
     // would not fill the SMs' warps (a pass of 32 / turned heads at the least)
     const int sms = device_sm_count(), heads = p.a.Hq + a.Hkv, step = 32 / p.turned;

@@ -276,3 +276,24 @@ def test_commit_reports_bad_blocks():
                                        w.interleave)
         assert dcp.dcp_get_last_device_status() == dcp.DCP_ERR_BOUNDS
         assert lens.tolist() == sl.tolist() and torch.equal(kv.cpu(), inst.kv_cache)
+
+
+@pytest.mark.parametrize("dim,rope", [(400008, dict(rot_dim=64, rot_offset=8)), (262136, dict(rot_dim=128)),
+                                      (524280, dict(rot_dim=64, rot_offset=64, layout="interleaved"))])
+def test_heads_of_hundreds_of_thousands_of_dims(dim, rope):
+    """Every vector that does not turn is copied, up to rows of 1 MB."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    g = torch.Generator().manual_seed(2)
+    k, q = torch.randn((1, 1, dim), generator=g).to(torch.bfloat16), torch.randn((1, 1, 8, dim), generator=g).to(torch.bfloat16)
+    cache = torch.zeros((2, 1, dim), dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[[0, 1]]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([2], dtype=torch.int32, device="cuda")
+    _, q_out = dcp.dcp_kv_cache_append("mla", k.cuda(), None, cache, table, lens, 1, 1, dcp.dcp_rope_table(**rope), q=q.cuda())
+    assert dcp.dcp_get_last_device_status() == dcp.DCP_OK
+    f = tro.rope_freqs(rope["rot_dim"], 1e4)
+    args = f, rope.get("layout", "half"), rope.get("rot_offset", 0), 1.0
+    for got, x in ((cache[1, 0], k[0, 0]), (q_out[0, 0], q[0, 0])):
+        _assert_rotated(orc.to_f64(got.cpu()), tro.rotate(orc.to_f64(x), 1, *args), orc.to_f64(x), 1.0, "row")
+    lo, hi = rope.get("rot_offset", 0), rope.get("rot_offset", 0) + rope["rot_dim"]
+    assert torch.equal(cache[1, 0, hi:].cpu(), k[0, 0, hi:]) and torch.equal(q_out[..., hi:].cpu(), q[..., hi:])
+    assert torch.equal(q_out[..., :lo].cpu(), q[..., :lo]) and (cache[0] == 0).all()

@@ -34,6 +34,7 @@ DCP_KERNEL_NONE, DCP_KERNEL_MLA_TC, DCP_KERNEL_GQA_TC, DCP_KERNEL_SIMT = range(4
 KINDS = {"gqa": DCP_ATTN_GQA, "mla": DCP_ATTN_MLA}
 DCP_TREE_MAX_NODES = 256
 DCP_COMMIT_MAX_ACCEPT = 256
+DCP_ROPE_MAX_DIM = 1024
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 

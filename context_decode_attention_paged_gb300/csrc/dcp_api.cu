@@ -174,7 +174,7 @@ bool cache_desc_ok(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleav
 }
 
 bool rope_ok(const dcp_rope_desc_t* r) {
-  return r && r->rot_dim >= 2 && r->rot_dim % 2 == 0 && r->rot_dim <= 1024 && r->rot_offset >= 0 &&
+  return r && r->rot_dim >= 2 && r->rot_dim % 2 == 0 && r->rot_dim <= DCP_ROPE_MAX_DIM && r->rot_offset >= 0 &&
          (r->layout == DCP_ROPE_HALF || r->layout == DCP_ROPE_INTERLEAVED) && std::isfinite(r->mscale);
 }
 

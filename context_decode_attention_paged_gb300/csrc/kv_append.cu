@@ -44,7 +44,7 @@ constexpr int kBlocks = 3;         // resident blocks of an SM
 constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
 constexpr int kCopies = 8;         // vectors of a lane in flight while copying
 constexpr int kTaskBytes = 8192;   // rows of a task, at most (when tokens abound)
-constexpr int kMaxPairs = 512;     // rotated pairs of a head (shared memory)
+constexpr int kMaxPairs = DCP_ROPE_MAX_DIM / 2;   // rotated pairs of a head (shared memory)
 constexpr int kScan = 1024;        // requests whose token counts a block sums
 
 enum Mode { kHalf = 0, kInterleaved = 1, kScalar = 2 };

@@ -291,6 +291,8 @@ DCP_API int32_t dcp_decode_attn_launches(const dcp_attn_desc_t* d, int32_t dcp_s
 #define DCP_TREE_MAX_NODES 256
 /* Most nodes one dcp_kv_cache_commit may accept per request (max_accept). */
 #define DCP_COMMIT_MAX_ACCEPT 256
+/* Most rotated dims of a head (rot_dim). */
+#define DCP_ROPE_MAX_DIM 1024
 
 typedef enum {
   DCP_ROPE_HALF = 0,         /* pair k: dims k and k + rot_dim / 2 of the rotated part */
@@ -314,7 +316,7 @@ typedef enum {
  *   mscale * (x0 cos(p f_k) - x1 sin(p f_k),  x1 cos(p f_k) + x0 sin(p f_k)).
  * Dims outside [rot_offset, rot_offset + rot_dim) are left as they are. */
 typedef struct {
-  int32_t rot_dim;               /* even, >= 2 (NTK: >= 4)                              */
+  int32_t rot_dim;               /* even, 2 (NTK: 4) to DCP_ROPE_MAX_DIM                */
   int32_t rot_offset;            /* first rotated dim of a head                         */
   int32_t layout;                /* dcp_rope_layout_t                                   */
   int32_t scaling;               /* dcp_rope_scaling_t (used by dcp_rope_steps only)    */

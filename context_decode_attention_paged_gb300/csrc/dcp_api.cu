@@ -480,7 +480,6 @@ dcp_status_t dcp_rope_steps(const dcp_rope_desc_t* r, const double* inv_freq, ui
     double f;
     if (inv_freq) {
       f = inv_freq[k];
-      if (!std::isfinite(f)) return DCP_ERR_INVALID_ARG;
     } else {
       f = std::pow(base, -2.0 * k / r->rot_dim);
       if (r->scaling == DCP_ROPE_SCALE_LINEAR) f /= r->factor;
@@ -489,6 +488,7 @@ dcp_status_t dcp_rope_steps(const dcp_rope_desc_t* r, const double* inv_freq, ui
         f = f / r->factor * ramp + f * (1.0 - ramp);
       }
     }
+    if (!std::isfinite(f)) return DCP_ERR_INVALID_ARG;      // (a factor that takes the base or f past a double's range)
     const double turns = f / two_pi;
     const double frac = turns - std::floor(turns);          // [0, 1); 1 after rounding is a whole turn
     steps[k] = frac < 1.0 ? (uint64_t)std::ldexp(frac, 64) : 0;

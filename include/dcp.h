@@ -332,7 +332,7 @@ typedef struct {
  * positions lose nothing.  inv_freq (host, [rot_dim / 2], finite) replaces base, scaling
  * and factor when it is not NULL.  Copy the table to the device once and pass it to
  * dcp_kv_cache_append.  Host only, no GPU work.
- * Errors: INVALID_ARG. */
+ * Errors: INVALID_ARG, also for a frequency that is not finite. */
 DCP_API dcp_status_t dcp_rope_steps(const dcp_rope_desc_t* rope, const double* inv_freq,
                                     uint64_t* steps);
 

@@ -7,7 +7,6 @@ import os
 import re
 
 import pytest
-import torch
 
 from test_tree_cpu import _append, _desc, _rope, lib    # noqa: F401  (the fixture builds the library)
 
@@ -27,3 +26,19 @@ def test_rot_dim_ends_at_its_limit(lib):    # noqa: F811
         lib.dcp_rope_table(most + 2, device="cpu")
     d = _desc(lib, head_dim_qk=2 * most, head_dim_v=2 * most)
     assert _append(lib, d, rope=_rope(lib, rot_dim=most + 2)) == lib.DCP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(scaling=1, factor=1e-310), dict(scaling=2, factor=1e-320, rot_dim=4),
+                                dict(scaling=3, factor=1e-310, original_max_position=4096)])
+def test_frequencies_past_the_range_of_a_double_are_refused(lib, kw):    # noqa: F811
+    """A tiny factor divides a frequency to infinity (or takes the NTK base to 0): no rotation at all
+    came of it before."""
+    out = (ctypes.c_uint64 * 512)()
+    assert lib.raw_lib().dcp_rope_steps(ctypes.byref(_rope(lib, **kw)), None, out) == lib.DCP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(scaling=1, factor=1e-300), dict(scaling=2, factor=0.5),
+                                dict(scaling=3, factor=0.25, original_max_position=4096)])
+def test_factors_below_one_are_taken(lib, kw):    # noqa: F811
+    out = (ctypes.c_uint64 * 512)()
+    assert lib.raw_lib().dcp_rope_steps(ctypes.byref(_rope(lib, **kw)), None, out) == lib.DCP_OK

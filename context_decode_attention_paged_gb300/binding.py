@@ -400,6 +400,8 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
     steps = rope.steps
     if steps.get_device() != device:
         _refuse(call, "the rope table is not on the current device")
+    if steps.dtype is not torch.int64 or not steps.is_contiguous() or 2 * steps.numel() < rope.desc.rot_dim:
+        _refuse(call, "the rope table is not contiguous int64 [rot_dim / 2]")
     k_batch, k_token = _row_strides(call, new_k, device, rows)
     v_batch, v_token = _row_strides(call, new_v, device, rows) if gqa else (0, 0)
     hq, q_batch, q_token = hkv, 0, 0

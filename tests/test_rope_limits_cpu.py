@@ -7,6 +7,7 @@ import os
 import re
 
 import pytest
+import torch
 
 from test_tree_cpu import _append, _desc, _rope, lib    # noqa: F401  (the fixture builds the library)
 
@@ -42,3 +43,16 @@ def test_frequencies_past_the_range_of_a_double_are_refused(lib, kw):    # noqa:
 def test_factors_below_one_are_taken(lib, kw):    # noqa: F811
     out = (ctypes.c_uint64 * 512)()
     assert lib.raw_lib().dcp_rope_steps(ctypes.byref(_rope(lib, **kw)), None, out) == lib.DCP_OK
+
+
+@pytest.mark.parametrize("steps", [torch.zeros(31, dtype=torch.int64), torch.zeros(32, dtype=torch.int32),
+                                   torch.zeros(64, dtype=torch.int64)[::2], torch.zeros(0, dtype=torch.int64)])
+def test_the_binding_refuses_a_table_that_is_not_the_rotations(lib, monkeypatch, steps):    # noqa: F811
+    """A table made by hand, or for fewer dims: the kernel would read past its end."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)      # (where CPU tensors are)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)                 # noqa: E731
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)               # noqa: E731
+    rope = lib.RopeTable(lib.dcp_rope_table(64, device="cpu").desc, steps)
+    with pytest.raises(lib.DcpError, match="rope table"):
+        lib.dcp_kv_cache_append("gqa", bf(1, 1, 2, 64), bf(1, 1, 2, 64), bf(2, 4, 16, 2, 64), i32(2, 1, 2), i32(1), 2, 16,
+                                rope)

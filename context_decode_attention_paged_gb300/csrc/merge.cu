@@ -62,7 +62,8 @@ __device__ __forceinline__ void weighted_row(const float* __restrict__ src, long
   const int lane = threadIdx.x & 31;
   // tokens and splits are dealt from the first source on, so those without keys are
   // the last ones
-  n = 32 - __clz(__ballot_sync(0xffffffffu, w_lane != 0.f));
+  // (a NaN LSE makes the weights of lanes without a source NaN too)
+  n = 32 - __clz(__ballot_sync(0xffffffffu, lane < n && w_lane != 0.f));
   for (int c = lane; c - lane < Dv4; c += 32) {
     const bool in = c < Dv4;                         // (the shuffles below take the whole warp)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

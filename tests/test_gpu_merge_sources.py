@@ -69,3 +69,27 @@ def test_rows_differ_in_the_shards_that_count():
     got = out_lse.double().cpu().numpy()
     some = ref_lse > -np.inf
     assert np.array_equal(got == -np.inf, ~some) and (np.abs(got[some] - ref_lse[some]) <= 1e-5).all()
+
+
+@pytest.mark.parametrize("N", [1, 2, 5, 8, 31, 32])
+@pytest.mark.parametrize("others", [-float("inf"), 0.5])
+def test_a_nan_lse_makes_its_rows_nan_and_no_others(N, others):
+    """The partials end with the last shard's rows: nothing lies behind them."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    g = torch.Generator().manual_seed(N)
+    po = torch.randn((N, 2, 1, N * 2, 128), generator=g)
+    lse = torch.full((N, 2, 1, N * 2), others)
+    lse[N // 2, 1, 0, 1::2] = float("nan")
+    lse[:, 0] = torch.randn((N, 1, N * 2), generator=g)
+    clean = lse.clone()
+    clean[:, 1, 0, 1::2] = -float("inf")
+    ref, ref_lse = orc.ref_merge(po.double().numpy(), clean.double().numpy())
+    out, out_lse = dcp.dcp_merge(po.cuda(), lse.cuda(), N)
+    out, out_lse = out.double().cpu().numpy(), out_lse.double().cpu().numpy()
+    hit = np.zeros(out_lse.shape, dtype=bool)
+    hit[:, 1, 0, 1::2] = True
+    assert np.isnan(out[hit]).all() and np.isnan(out_lse[hit]).all()
+    assert (np.abs(out[~hit] - ref[~hit]) <= 2.0 ** -8 * np.abs(ref[~hit]) + 1e-5 * 6).all()
+    got, want = out_lse[~hit], ref_lse[~hit]
+    some = want > -np.inf
+    assert np.array_equal(got == -np.inf, ~some) and (np.abs(got[some] - want[some]) <= 1e-5).all()

@@ -10,9 +10,12 @@
 // keys (local tokens are in global order), so masking is a per-row count.
 //
 // kTree: the drafted-tree form.  A row sees the shard's context keys and the
-// nodes its mask row has; a hidden key's weight is exactly 0 and its value is
-// not touched, so what it holds (NaN, infinities) stays out of the row.
+// nodes its mask row has; a hidden key's value is not touched, so what it holds
+// (NaN, infinities) stays out of the row.  A seen value that is not finite reaches
+// the row however small its weight: neither the weight nor a later rescale may
+// round to 0 there.
 #include <cuda_bf16.h>
+#include <float.h>
 
 #include "dcp_device.cuh"
 #include "dcp_internal.h"
@@ -160,11 +163,11 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       if constexpr (kTree) {
         // a NaN score is no maximum, but it makes the row NaN
         const float ref = mx == -INFINITY ? 0.f : mx;
-        alpha = (m_s[tid] == -INFINITY) ? 0.f : expf(m_s[tid] - ref);
+        alpha = (m_s[tid] == -INFINITY) ? 0.f : fmaxf(expf(m_s[tid] - ref), FLT_MIN);
         for (int tt = 0; tt < kTile; ++tt) {
           const float sc = p_s[tid * kTile + tt];
           const float p = (sc == -INFINITY) ? 0.f : expf(sc - ref);
-          p_s[tid * kTile + tt] = p;
+          p_s[tid * kTile + tt] = (sc == -INFINITY) ? -1.f : p;      // (-1: hidden)
           sum += p;
         }
       } else if (mx != -INFINITY) {
@@ -191,8 +194,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       float acc = o_s[idx] * alpha_s[rr];
       const float* pr = p_s + rr * kTile;
       for (int tt = 0; tt < nt; ++tt) {
-        if (kTree && pr[tt] == 0.f) continue;
-        acc = fmaf(pr[tt], vsrc[tt * vstride + d], acc);
+        const float v = vsrc[tt * vstride + d];
+        if (kTree && pr[tt] < 0.f) continue;
+        acc = kTree && !(fabsf(v) < INFINITY) ? acc + v : fmaf(pr[tt], v, acc);
       }
       o_s[idx] = acc;
     }

@@ -387,7 +387,8 @@ DCP_API size_t dcp_tree_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dc
  * Keys and values that a row does not see never reach it, whatever they hold (NaN,
  * infinities).  A score that is not finite and not -inf makes its row NaN; a value entry
  * that is not finite makes that entry of the output not finite (of a node's value, in the
- * rows that see the node, and infinite where the formula has it so).
+ * rows that see the node, and infinite where the formula has it so), except where a shard or
+ * a KV split weighs 0 in fp32 against the row's others: it does not count then.
  *  tree_mask     uint32 [B][q_len][words], words = ceil(q_len / 32); requests lie
  *                tree_mask_stride words apart (0: one tree for all requests); bits of
  *                nodes >= n_b are ignored

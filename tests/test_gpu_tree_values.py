@@ -95,3 +95,32 @@ def test_infinities_of_both_signs_in_one_key_make_its_rows_nan(name, kw, dims):
         got = T.run_tree(inst, mask)
         assert np.isnan(got["out"][:, :, sees[:, 5]]).all()
         assert_close(got["out"][:, :, ~sees[:, 5]], ref["out"][:, :, ~sees[:, 5]], "rows that do not see it")
+
+
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("name,kw", [(c[0], dict(c[1], dcp_size=1)) for c in KEYS if c[0] != "mla_32"])
+def test_a_seen_value_that_is_not_finite_counts_however_small_its_weight(name, kw, value, first):
+    """Node 2's score lies 300 below the others (or 300 above the context's, and node 40's 300 above
+    it): its weight is 0 in fp32, its value is infinite in one dim."""
+    inst, mask, _ = T.tree_case(name, L, mask="full", **kw)
+    w = inst.w
+    inst.q[..., 0] = 8.0
+    base = int(inst.seq_lens[0]) - L
+    keys = [(2, -300)] if not first else [(2, 300), (40, 600)]
+    for node, score in keys:
+        blk, slot = T.cell(inst, 0, base + node)
+        inst.kv_cache[0, blk, slot, :, 0] = score / (8.0 * w.scale)
+    sees = T.tro.unpack(mask, L)
+    sees[:, ::2, 2] = False
+    ref = T.oracle_tree(inst, T.pack(sees))
+    blk, slot = T.cell(inst, 0, base + 2)
+    inst.kv_cache[1, blk, slot, :, 7] = value
+    got = T.run_tree(inst, T.pack(sees))
+    hit = np.zeros(ref["out"].shape, dtype=bool)
+    hit[:, :, 1::2, :, 7] = True
+    want = np.full(1, value)
+    assert np.array_equal(got["out"][hit], np.broadcast_to(want, got["out"][hit].shape), equal_nan=True)
+    got["out"][hit] = ref["out"][hit] = 0
+    assert_close(got["out"], ref["out"], "every other entry")
+    assert_lse_close(got["out_lse"], ref["out_lse"], "out_lse")

@@ -45,9 +45,9 @@ struct SplitPlan {
 //   ws_o   fp32 [N][B][Lq][n_split][Hq][Dv]
 //   ws_lse fp32 [N][B][Lq][n_split][Hq]       (after ws_o, 256-byte aligned)
 // then, 256-byte aligned, the request order when lpt_order is set.
-// (start_tiles > 0: up to 4 splits are weighed for grids of 2 to 16 waves too,
-// where a unit's start and end cost that many tiles of time and joining
-// join_tiles more.)
+// (start_tiles > 0: a unit's start and end cost that many tiles of time, and up to 4
+// splits are weighed for grids of 2 to 16 waves too, where joining costs join_tiles
+// more.)
 SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int units_per_split, int start_tiles = 0,
                       int join_tiles = 0);
 

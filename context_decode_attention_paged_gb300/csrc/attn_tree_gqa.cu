@@ -14,8 +14,9 @@
 // nodes of a 16-head group are 1024 rows, 1024 flop per cache byte, four times
 // the ridge.  So rows sit on the 128 lanes of the MMA (M), unlike the decode
 // kernel, which has few rows and puts the keys there:
-//   S = Q K^T   (M = 128 rows, N = 128 keys, K = D; both K-major in shared memory)
-//   O += P V    (M = 128 rows, N = D, K = 128 keys; P from TMEM, V MN-major)
+//   S = Q K^T   (M = 128 rows, N = 64 keys, K = D; both K-major in shared memory)
+//   O += P V    (M = 128 rows, N = D, K = 64 keys; P from TMEM, V MN-major)
+// in steps of 64 keys, two to a tile of 128.
 // A probability is rounded to bf16 once unless it is heavy, above 2^-3 of its
 // row's sum so far: then bf16(p - bf16(p)) goes along as a second term, so that
 // 16 bits of it reach the product.  Of a row at most a few probabilities are
@@ -867,10 +868,17 @@ tree_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 }
 
 int rows_of(const AttnArgs& a) { return a.Lq * (a.Hq / a.Hkv); }
-// Rows of a block.  Pairs of 128 share a key tile; with three or five of them the
-// odd one would hold an SM for a pair's time (330 rows: 195 us in pairs, 162 in
-// turn; 576 rows: 177 and 128), with more the passes over the cache count for more
-// (29: 242 us in pairs, 261 in turn).
+// Rows of a block.  Pairs of 128 share a key tile; an odd one holds an SM for a
+// pair's time, which counts for most where there are few; in turn there are twice the
+// units, which fill the SMs better.  Time in turn against in pairs, over 25 to 40
+// shapes each (1 to 64 requests of unlike lengths up to 60,000, 1 to 8 KV heads, 1
+// to 4 shards), geometric mean and range: two blocks 0.94 (0.67-1.46), three 0.84
+// (0.51-1.18), four 0.94 (0.68-1.22), five 0.86 (0.57-1.15), six 0.96 (0.68-1.45),
+// seven 0.90 (0.62-1.26).  Where many equal units fill the SMs either way the passes
+// over the cache decide (64 requests of 2,048 tokens, 64 and 4 heads, 4 shards):
+// three blocks 1.00, five 1.06, seven 1.12, even ones 1.20 and more, 15 to 31 1.21 to
+// 1.28; 16 requests of 8,192: three and five 0.91, seven 1.00, 9 to 31 1.02 to 1.13.
+// So three and five go in turn, where the gain is the largest and the loss small.
 int block_rows_of(const AttnArgs& a) {
   const int n = (rows_of(a) + kNt - 1) / kNt;
   return n == 1 || n == 3 || n == 5 ? kNt : 2 * kNt;

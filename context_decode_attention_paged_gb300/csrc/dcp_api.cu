@@ -214,9 +214,9 @@ SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int unit
     // and 16 nodes takes 785 us in 7 splits, at 12 729 in 4; of 50,000, 32 nodes of
     // 16 heads 89 and 74; three of 40,000, 5 nodes 188 and 164; ten other shapes
     // differ by less than 2.5%), so pick the count with the fewest
-    // waves x (tiles per split + start-up).
-    // Drafted trees, whose kernels take units longest first, take the largest
-    // count within 2% of that: more units even out requests of unlike lengths.
+    // waves x (tiles per split + start-up).  (Drafted trees: the largest count
+    // within 2% of that instead, to even out requests of unlike lengths, took 4%
+    // longer over 90 shapes of 1 to 16 requests: 0.71 to 1.72 of the time.)
     constexpr long long kUnitStartTiles = 4;
     const long long tiles = (max_local + tile_tokens - 1) / tile_tokens;
     const long long n_hi = std::max<long long>(1, std::min<long long>(small ? 32 : 4, max_local / (4LL * tile_tokens)));
@@ -227,11 +227,6 @@ SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int unit
     };
     for (long long c = 2; c <= n_hi; ++c)
       if (cost(c) < cost(n)) n = c;
-    if (small && a.tree_words > 0) {
-      const long long limit = cost(n) + cost(n) / 50;
-      for (long long c = n + 1; c <= n_hi; ++c)
-        if (cost(c) <= limit) n = c;
-    }
   }
   long long per = (max_local + n - 1) / n;
   per = (per + tile_tokens - 1) / tile_tokens * tile_tokens;

@@ -806,8 +806,9 @@ __device__ __forceinline__ void score_sender(const MlaParams& p, Smem& sm, const
 #pragma unroll
         for (int j = 0; j < 8; ++j) b8[j] = max(b8[j], v[k + j] & 0x7fffffffu);
       const uint32_t top = max(max(max(b8[0], b8[1]), max(b8[2], b8[3])), max(max(b8[4], b8[5]), max(b8[6], b8[7])));
-      raw = top >= 0x7f800000u;
-      amax = __uint_as_float(top);
+      // (a row without a node may hold anything: it asks for no residual)
+      raw = view.mask_row != nullptr && top >= 0x7f800000u;
+      amax = view.mask_row != nullptr ? __uint_as_float(top) : 0.f;
     } else {
       float a8[8];
 #pragma unroll

@@ -53,3 +53,21 @@ def test_a_bad_block_empties_the_request_in_its_shard_alone(name, L, kw):
     ref["partial_out"][0, 1], ref["lse"][0, 1] = 0.0, -np.inf
     assert_close(got["partial_out"], ref["partial_out"], "partial_out")
     assert_lse_close(got["lse"], ref["lse"], "lse")
+
+
+@pytest.mark.parametrize("name,L,kw", CASES + [("mla_32", 11, dict(lengths=("fixed", 400), dcp_size=1, num_q_heads=20))])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
+def test_query_rows_behind_a_request_may_hold_anything(name, L, kw, value):
+    """They share MMA tiles and messages with the rows that are there."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    n = [L, max(1, L // 2), 1]
+    inst, mask, ql = T.tree_case(name, L, batch=3, q_lens=n, **kw)
+    ref = T.oracle_tree(inst, mask, ql)
+    for b in range(3):
+        inst.q[b, n[b]:] = value
+    got = T.run_tree(inst, mask, ql)
+    assert got["status"] == dcp.DCP_OK
+    for key in ("partial_out", "out"):
+        assert_close(got[key], ref[key], key)
+    for key in ("lse", "out_lse"):
+        assert_lse_close(got[key], ref[key], key)

@@ -76,9 +76,10 @@
 // possible, so its running reference may stay -inf past the first tile.
 //
 // Measured (GB300, 2.07 GHz).  Tree, 32 requests of 4,096 to 67,000 tokens, 8
-// nodes of 128 heads: 1.06 ms, 0.96 PFLOP/s (1.02 TFLOP, 0.89 GB);
-// 200,000 tokens, 32 nodes: 1.37 ms, 1.30 PFLOP/s.  Decode, batch 512 (41.6 GB):
-// 7.8 to 8.1 ms, 5.1 to 5.3 TB/s.  Neither the tensor cores nor memory bind: a tile's MMAs
+// nodes of 128 heads: 1.03 ms, 0.98 PFLOP/s (1.02 TFLOP, 0.89 GB);
+// 200,000 tokens, 32 nodes: 1.43 ms, 1.25 PFLOP/s (1.37 in a graph).  Decode, batch
+// 512 (41.6 GB): 7.6 to 8.4 ms, 5.0 to 5.5 TB/s.  The loops' code fills the instruction
+// cache: a block that never runs costs time by its size when it stands in them.  Neither the tensor cores nor memory bind: a tile's MMAs
 // take ~1,200 cycles, a tile every ~1,900 comes out of a softmax warpgroup's
 // chain of ~3,900 (about 1,500 of them waits on the peer, on the other warpgroup
 // and on the MMAs) over two warpgroups.  Without the loads the tree case takes 4%

@@ -25,10 +25,10 @@
 // layout, say) or do not fall on vectors, and heads of 65,000 dims and more, go
 // unit by unit with the angles in shared memory, one block a token.
 //
-// Measured (GB300; time in a graph): 64 tokens of 64 + 4 + 4 heads of 128 (2.4 MB
-// moved) 6.5 us, launch and dependent loads; 512 tokens of 128 + 1 heads of 576
-// (152 MB) 29 us, 5.2 TB/s; 6 ragged prompt chunks of up to 2,048 tokens (79 MB)
-// 18.7 us, 4.2 TB/s.
+// Measured (GB300; one of five in a graph): 64 tokens of 64 + 4 + 4 heads of 128
+// (2.4 MB moved) 4.8 us, launch and dependent loads; 512 tokens of 128 + 1 heads of
+// 576 (152 MB) 27.3 us, 5.6 TB/s; 6 ragged prompt chunks of up to 2,048 tokens (79
+// MB) 15.9 us (L2 holds part of them by then; 20.6 as calls of their own, 3.9 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>

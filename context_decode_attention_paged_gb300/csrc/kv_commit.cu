@@ -11,8 +11,8 @@
 // A request moves a few KB, so the launch and the chain of dependent loads
 // (lengths, path, table, row) bound it: one block of 256 threads per request,
 // thread k < num_accepted finding and checking the cells of step k.  Measured
-// (GB300, in a graph): 64 requests of up to 8 accepted nodes (1 MB) 6.4 us; 512 of
-// up to 16, rows of 1,152 bytes (8.4 MB), 8.4 us.
+// (GB300, one of five in a graph): 64 requests of up to 8 accepted nodes (1 MB) 4.6
+// us; 512 of up to 16, rows of 1,152 bytes (8.4 MB), 5.8 us.
 #include "dcp_device.cuh"
 #include "dcp_internal.h"
 

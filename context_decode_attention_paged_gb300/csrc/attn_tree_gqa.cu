@@ -57,8 +57,9 @@
 // drains its copies and MMAs and returns.
 //
 // Measured (GB300, 2.07 GHz, D = 128, 64 query and 4 KV heads, 4 shards):
-//   64 requests of 8,192 to 32,768 tokens, 5 nodes: 381 us, 6.1 TB/s (HBM);
-//   16 of them, 64 nodes (1024 rows a KV head): 540 us, 1.12 PFLOP/s: a step of
+//   64 requests of 8,192 to 32,768 tokens, 5 nodes: 379 us, 6.2 TB/s (HBM);
+//   16 of them, 64 nodes (1024 rows a KV head): 534 us in a graph, 1.13 PFLOP/s
+//     (559 as a call of its own; the merge is part of both): a step of
 //     both streams takes ~1,740 cycles, ~1,260 of them tensor time (the scores'
 //     operands come out of shared memory, 47 cycles an MMA of 32); a unit's
 //     start and end are ~14,000 of ~128,000 cycles;
@@ -68,7 +69,8 @@
 // Slower when tried: two threads a row (no gain for 640 threads), exponentials
 // before the maximum is known (745 us against 624 at the time), one issuer for
 // both streams with two score buffers (869 against 581), the second term for
-// every probability.
+// every probability (3% on the first of these cases, 18% on the second, 5 to 20% on
+// small batches of 128 rows or fewer).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

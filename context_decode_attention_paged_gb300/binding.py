@@ -54,6 +54,11 @@ class DcpAppendStrides(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("k_batch", "k_token", "v_batch", "v_token", "q_batch", "q_token")]
 
 
+class DcpNormDesc(ctypes.Structure):
+    _fields_ = [("norm_dim", ctypes.c_int32), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 _lib.dcp_build_slot_map.restype = _i32
 _lib.dcp_build_slot_map.argtypes = [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp]
@@ -95,6 +100,25 @@ _lib.dcp_tree_attn_launches.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
 _lib.dcp_kv_cache_commit.restype = _i32
 _lib.dcp_kv_cache_commit.argtypes = [ctypes.POINTER(DcpAttnDesc), _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32,
                                      _vp]
+_lib.dcp_kv_cache_append_norm.restype = _i32
+_lib.dcp_kv_cache_append_norm.argtypes = [ctypes.POINTER(DcpAttnDesc), ctypes.POINTER(DcpRopeDesc), _vp,
+                                          ctypes.POINTER(DcpNormDesc), _vp, _vp, _vp, ctypes.POINTER(DcpAppendStrides),
+                                          _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _vp]
+_lib.dcp_kv8_append.restype = _i32
+_lib.dcp_kv8_append.argtypes = [ctypes.POINTER(DcpAttnDesc), ctypes.POINTER(DcpRopeDesc), _vp,
+                                ctypes.POINTER(DcpNormDesc), _vp, _vp, _vp, ctypes.POINTER(DcpAppendStrides), _vp, _vp,
+                                _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp]
+_lib.dcp_kv8_read.restype = _i32
+_lib.dcp_kv8_read.argtypes = [ctypes.POINTER(DcpAttnDesc), _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp]
+_lib.dcp_kv8_decode_attn_workspace_size.restype = _sz
+_lib.dcp_kv8_decode_attn_workspace_size.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
+_lib.dcp_kv8_decode_attn.restype = _i32
+_lib.dcp_kv8_decode_attn.argtypes = [ctypes.POINTER(DcpAttnDesc), _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _f32, _i32,
+                                     _vp, _vp, _vp, _sz, _vp]
+_lib.dcp_kv8_decode_attn_kernel_kind.restype = _i32
+_lib.dcp_kv8_decode_attn_kernel_kind.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
+_lib.dcp_kv8_decode_attn_launches.restype = _i32
+_lib.dcp_kv8_decode_attn_launches.argtypes = [ctypes.POINTER(DcpAttnDesc), _i32]
 _lib.dcp_status_string.restype = ctypes.c_char_p
 _lib.dcp_status_string.argtypes = [_i32]
 
@@ -375,18 +399,33 @@ def _row_strides(call, t, device, shape):
     return (stride[0] if shape[0] > 1 else token * shape[1]), token
 
 
-def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dcp_size, interleave, rope, q=None,
-                        q_out=None, q_lens=None, pos_offsets=None, stream=None):
-    """Store new tokens' rows in their shards' cache cells, keys rotated, and rotate their queries.
+def _attn_buffers(call, size_of, desc, dcp_size, shape, on, device, partial_out, lse, workspace, stream):
+    """(partial_out, lse, workspace, its bytes) of an attention call of shape (B, Lq, Hq, Dv): checked, allocated
+    where they are not given."""
+    if partial_out is None or lse is None or workspace is None:
+        # allocated for the stream that the kernels run on
+        with torch.cuda.stream(stream):
+            if partial_out is None:
+                partial_out = torch.empty((dcp_size, *shape), dtype=torch.float32, device=on)
+            if lse is None:
+                lse = torch.empty((dcp_size, *shape[:3]), dtype=torch.float32, device=on)
+            size = int(size_of(desc, dcp_size))
+            if workspace is None and size:
+                workspace = torch.empty((size,), dtype=torch.uint8, device=on)
+    _check_tensors(call, torch.float32, device, partial_out, lse)
+    if partial_out.numel() != dcp_size * math.prod(shape) or lse.numel() != dcp_size * math.prod(shape[:3]):
+        _refuse(call, "partial_out is [N][B][Lq][Hq][Dv] and lse [N][B][Lq][Hq]")
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            _refuse(call, "the workspace is not contiguous on the current device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    return partial_out, lse, workspace, ws_bytes
 
-    new_k/new_v bf16: GQA [B][n][Hkv][D], MLA new_k [B][n][Dqk] and new_v None; q [B][n][Hq][Dqk] or
-    None.  A token's row is contiguous, tokens may lie apart (slices of a fused projection).
-    ``rope``: a RopeTable.  ``q_lens`` int32 [B]: tokens of each request (None: n).  ``pos_offsets``
-    int32 [B or 1][n]: a token's rotary position relative to the request's first new token (None:
-    0, 1, 2, ...; a tree passes its depths).  kv_cache and q_out are written in place, rows behind a
-    request's q_lens are left alone.  Returns (kv_cache, q_out); q_out may be q, and without one a
-    zeroed tensor is allocated."""
-    call = "dcp_kv_cache_append"
+
+def _append_args(call, kind, new_k, new_v, kv_cache, scales, block_tables, seq_lens, dcp_size, rope, q, q_out, q_lens,
+                 pos_offsets, stream):
+    """The checked arguments of an append: (desc, rope desc, rope steps), (new_k .. q_lens pointers), q_out, device."""
     B, n = new_k.shape[:2]
     kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
     gqa = kind == DCP_ATTN_GQA
@@ -394,14 +433,18 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
     if (new_v is not None) != gqa:
         _refuse(call, "GQA takes new_v, MLA none")
     device = torch.cuda.current_device()
-    _check_tensors(call, _bf16, device, kv_cache, None if q_out is q else q_out)
+    _check_tensors(call, kv_cache.dtype if scales is not None else _bf16, device, kv_cache)
+    _check_tensors(call, _bf16, device, None if q_out is q else q_out)
     _check_tensors(call, _int32, device, block_tables, pos_offsets)
     _check_lens(call, B, device, seq_lens, q_lens)
-    steps = rope.steps
-    if steps.get_device() != device:
-        _refuse(call, "the rope table is not on the current device")
-    if steps.dtype is not torch.int64 or not steps.is_contiguous() or 2 * steps.numel() < rope.desc.rot_dim:
-        _refuse(call, "the rope table is not contiguous int64 [rot_dim / 2]")
+    rotation = None, None
+    if rope is not None:
+        steps = rope.steps
+        if steps.get_device() != device:
+            _refuse(call, "the rope table is not on the current device")
+        if steps.dtype is not torch.int64 or not steps.is_contiguous() or 2 * steps.numel() < rope.desc.rot_dim:
+            _refuse(call, "the rope table is not contiguous int64 [rot_dim / 2]")
+        rotation = rope.desc, steps.data_ptr()
     k_batch, k_token = _row_strides(call, new_k, device, rows)
     v_batch, v_token = _row_strides(call, new_v, device, rows) if gqa else (0, 0)
     hq, q_batch, q_token = hkv, 0, 0
@@ -420,16 +463,181 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
         if pos_offsets.dim() != 2 or pos_offsets.shape[1] != n or pos_offsets.shape[0] not in (1, B):
             _refuse(call, "pos_offsets is [batch or 1][n]")
         offsets_stride = n if pos_offsets.shape[0] == B else 0
-    code = _lib.dcp_kv_cache_append(
-        _cached_desc(kind, B, n, hq, hkv, dim, dim, bs, nb, max_lb), rope.desc, steps.data_ptr(), new_k.data_ptr(),
-        new_v.data_ptr() if gqa else None, None if q is None else q.data_ptr(),
-        _cached_strides(k_batch, k_token, v_batch, v_token, q_batch, q_token), None if q is None else q_out.data_ptr(),
-        None if pos_offsets is None else pos_offsets.data_ptr(), offsets_stride,
-        None if q_lens is None else q_lens.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-        dcp_size, interleave, _stream(stream, device))
+    shape = _cached_desc(kind, B, n, hq, hkv, dim, dim, bs, nb, max_lb)
+    rows = (new_k.data_ptr(), new_v.data_ptr() if gqa else None, None if q is None else q.data_ptr(),
+            _cached_strides(k_batch, k_token, v_batch, v_token, q_batch, q_token), None if q is None else q_out.data_ptr(),
+            None if pos_offsets is None else pos_offsets.data_ptr(), offsets_stride,
+            None if q_lens is None else q_lens.data_ptr())
+    return (shape, *rotation), rows, q_out, device
+
+
+def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dcp_size, interleave, rope, q=None,
+                        q_out=None, q_lens=None, pos_offsets=None, stream=None):
+    """Store new tokens' rows in their shards' cache cells, keys rotated, and rotate their queries.
+
+    new_k/new_v bf16: GQA [B][n][Hkv][D], MLA new_k [B][n][Dqk] and new_v None; q [B][n][Hq][Dqk] or
+    None.  A token's row is contiguous, tokens may lie apart (slices of a fused projection).
+    ``rope``: a RopeTable.  ``q_lens`` int32 [B]: tokens of each request (None: n).  ``pos_offsets``
+    int32 [B or 1][n]: a token's rotary position relative to the request's first new token (None:
+    0, 1, 2, ...; a tree passes its depths).  kv_cache and q_out are written in place, rows behind a
+    request's q_lens are left alone.  Returns (kv_cache, q_out); q_out may be q, and without one a
+    zeroed tensor is allocated."""
+    call = "dcp_kv_cache_append"
+    if rope is None:
+        _refuse(call, "rope is a RopeTable")
+    shape, rows, q_out, device = _append_args(call, kind, new_k, new_v, kv_cache, None, block_tables, seq_lens, dcp_size,
+                                              rope, q, q_out, q_lens, pos_offsets, stream)
+    code = _lib.dcp_kv_cache_append(*shape, *rows, kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+                                    dcp_size, interleave, _stream(stream, device))
     if code != DCP_OK:
         raise DcpError(code, call)
     return kv_cache, q_out
+
+
+# ---------------------------------------------------------------------------
+# Norms of the heads in the append, and the cache in 8 bits
+# ---------------------------------------------------------------------------
+
+_codes = (torch.float8_e4m3fn, torch.uint8)
+_scales = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _norm_desc(call, device, q_weight, k_weight, eps):
+    """The norms' descriptor (None: none); the weights are fp32 [norm_dim]."""
+    if q_weight is None and k_weight is None:
+        return None
+    _check_tensors(call, torch.float32, device, q_weight, k_weight)
+    dims = {w.numel() for w in (q_weight, k_weight) if w is not None}
+    if len(dims) != 1 or any(w is not None and w.dim() != 1 for w in (q_weight, k_weight)):
+        _refuse(call, "norm weights are [norm_dim], both of one length")
+    return DcpNormDesc(dims.pop(), eps, None if q_weight is None else q_weight.data_ptr(),
+                       None if k_weight is None else k_weight.data_ptr())
+
+
+def _check_kv8(call, device, kind, kv_cache, kv_scales):
+    """The codes and scales of an 8-bit cache."""
+    for t, types, what in ((kv_cache, _codes, "cache is float8_e4m3fn"), (kv_scales, _scales, "scales are float8_e8m0fnu")):
+        if t.dtype not in types or t.get_device() != device or not t.is_contiguous():
+            _refuse(call, f"the {what} or uint8, contiguous on the current device")
+    shape = kv_cache.shape
+    want = (2, shape[1], shape[3]) if kind == DCP_ATTN_GQA else (shape[0],)
+    if kv_scales.shape != want:
+        _refuse(call, "kv_scales is [2][blocks][Hkv] (GQA) or [blocks] (MLA)")
+
+
+def dcp_kv_cache_append_norm(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dcp_size, interleave, rope=None,
+                             k_weight=None, q_weight=None, eps=1e-6, q=None, q_out=None, q_lens=None, pos_offsets=None,
+                             stream=None):
+    """dcp_kv_cache_append with RMS norms of the key heads (k_weight) and the query heads (q_weight)
+    before the rotation: y = x w / sqrt(mean(x^2) + eps) over a head's first len(w) dims (fp32
+    weights [D]; MLA: k_weight [512] normalises the latent part of the row).  ``rope`` None: no
+    rotation.  Returns (kv_cache, q_out)."""
+    call = "dcp_kv_cache_append_norm"
+    shape, rows, q_out, device = _append_args(call, kind, new_k, new_v, kv_cache, None, block_tables, seq_lens, dcp_size,
+                                              rope, q, q_out, q_lens, pos_offsets, stream)
+    code = _lib.dcp_kv_cache_append_norm(*shape, _norm_desc(call, device, q_weight, k_weight, eps), *rows,
+                                         kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), dcp_size,
+                                         interleave, _stream(stream, device))
+    if code != DCP_OK:
+        raise DcpError(code, call)
+    return kv_cache, q_out
+
+
+def dcp_kv8_append(kind, new_k, new_v, kv_cache, kv_scales, block_tables, seq_lens, dcp_size, interleave, rope=None,
+                   k_weight=None, q_weight=None, eps=1e-6, q=None, q_out=None, q_lens=None, pos_offsets=None,
+                   stream=None):
+    """dcp_kv_cache_append_norm into the 8-bit cache: codes (float8_e4m3fn or uint8, shaped as the bf16
+    cache) with a factor 2^(byte - 127) per block and KV head in kv_scales (float8_e8m0fnu or uint8,
+    GQA [2][blocks][Hkv], MLA [blocks]), both written in place.  A block whose scale is too small for
+    the new rows gets a larger one and its earlier rows are rounded to it.  Returns (kv_cache,
+    kv_scales, q_out); queries stay bf16."""
+    call = "dcp_kv8_append"
+    shape, rows, q_out, device = _append_args(call, kind, new_k, new_v, kv_cache, kv_scales, block_tables, seq_lens,
+                                              dcp_size, rope, q, q_out, q_lens, pos_offsets, stream)
+    _check_kv8(call, device, KINDS.get(kind, kind), kv_cache, kv_scales)
+    code = _lib.dcp_kv8_append(*shape, _norm_desc(call, device, q_weight, k_weight, eps), *rows, kv_cache.data_ptr(),
+                               kv_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), dcp_size, interleave,
+                               _stream(stream, device))
+    if code != DCP_OK:
+        raise DcpError(code, call)
+    return kv_cache, kv_scales, q_out
+
+
+def dcp_kv8_read(kind, kv_cache, kv_scales, block_tables, seq_lens, n, dcp_size, interleave, starts=None, out_k=None,
+                 out_v=None, stream=None):
+    """Rows of positions starts[b] + i (i < n, below seq_lens[b]; starts int32 [B], None: 0) of the 8-bit
+    cache as bf16: (out_k, out_v), GQA [B][n][Hkv][D] each, MLA out_k [B][n][Dqk] and None.  Other
+    rows are left as they were; outputs that are not given are allocated zeroed (GQA: where one is
+    given, that one alone is read)."""
+    call = "dcp_kv8_read"
+    B = seq_lens.shape[0]
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
+    gqa = kind == DCP_ATTN_GQA
+    device = torch.cuda.current_device()
+    _check_kv8(call, device, kind, kv_cache, kv_scales)
+    _check_tensors(call, _int32, device, block_tables)
+    _check_lens(call, B, device, seq_lens, starts)
+    shape = (B, n, hkv, dim) if gqa else (B, n, dim)
+    if out_k is None and out_v is None and n > 0:
+        with torch.cuda.stream(stream):
+            out_k = torch.zeros(shape, dtype=torch.bfloat16, device=kv_cache.device)
+            out_v = torch.zeros_like(out_k) if gqa else None
+    _check_tensors(call, _bf16, device, out_k, out_v)
+    for t in (out_k, out_v):
+        if t is not None and t.shape != shape:
+            _refuse(call, f"outputs are {shape}, got {tuple(t.shape)}")
+    code = _lib.dcp_kv8_read(
+        _cached_desc(kind, B, 1, hkv, hkv, dim, dim, bs, nb, max_lb), kv_cache.data_ptr(), kv_scales.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), None if starts is None else starts.data_ptr(), n,
+        None if out_k is None else out_k.data_ptr(), None if out_v is None else out_v.data_ptr(), dcp_size, interleave,
+        _stream(stream, device))
+    if code != DCP_OK:
+        raise DcpError(code, call)
+    return out_k, out_v
+
+
+def dcp_kv8_decode_attn_workspace_size(desc: DcpAttnDesc, dcp_size: int) -> int:
+    return int(_lib.dcp_kv8_decode_attn_workspace_size(ctypes.byref(desc), dcp_size))
+
+
+def dcp_kv8_decode_attn_launches(desc: DcpAttnDesc, dcp_size: int) -> int:
+    """Kernels one dcp_kv8_decode_attn call enqueues for this shape (0: invalid)."""
+    return int(_lib.dcp_kv8_decode_attn_launches(ctypes.byref(desc), dcp_size))
+
+
+def dcp_kv8_decode_attn_kernel_kind(desc: DcpAttnDesc, dcp_size: int) -> int:
+    """Which kernel dcp_kv8_decode_attn runs for this shape (DCP_KERNEL_*)."""
+    return int(_lib.dcp_kv8_decode_attn_kernel_kind(ctypes.byref(desc), dcp_size))
+
+
+def dcp_kv8_decode_attn(kind, q, kv_cache, kv_scales, block_tables, seq_lens, dcp_size, interleave, scale, causal_q_len,
+                        head_dim_v, q_lens=None, partial_out=None, lse=None, workspace=None, stream=None):
+    """dcp_decode_attn over the 8-bit cache: per-shard partial outputs fp32 [N][B][Lq][Hq][Dv] and lse
+    fp32 [N][B][Lq][Hq], for dcp_merge.  ``q_lens`` int32 [B]: queries of each request, in its last
+    positions (None: Lq each); rows behind them are 0 and -inf."""
+    call = "dcp_kv8_decode_attn"
+    if q.dim() != 4:
+        _refuse(call, "q is [batch][Lq][Hq][Dqk]")
+    B, Lq, Hq, Dqk = q.shape
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
+    if dim != Dqk:
+        _refuse(call, "q and the cache differ in their head dim")
+    device = torch.cuda.current_device()
+    _check_kv8(call, device, kind, kv_cache, kv_scales)
+    _check_tensors(call, _bf16, device, q)
+    _check_tensors(call, _int32, device, block_tables)
+    _check_lens(call, B, device, seq_lens, q_lens)
+    desc = _cached_desc(kind, B, Lq, Hq, hkv, Dqk, head_dim_v, bs, nb, max_lb)
+    partial_out, lse, workspace, ws_bytes = _attn_buffers(
+        call, _lib.dcp_kv8_decode_attn_workspace_size, desc, dcp_size, (B, Lq, Hq, head_dim_v), q.device, device,
+        partial_out, lse, workspace, stream)
+    code = _lib.dcp_kv8_decode_attn(
+        desc, q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        None if q_lens is None else q_lens.data_ptr(), dcp_size, interleave, scale, causal_q_len, partial_out.data_ptr(),
+        lse.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(stream, device))
+    if code != DCP_OK:
+        raise DcpError(code, call)
+    return partial_out, lse
 
 
 def dcp_tree_attn_workspace_size(desc: DcpAttnDesc, dcp_size: int) -> int:
@@ -470,24 +678,9 @@ def dcp_tree_attn(kind, q, kv_cache, block_tables, seq_lens, tree_mask, dcp_size
     _check_tensors(call, _int32, device, block_tables, tree_mask)
     _check_lens(call, B, device, seq_lens, q_lens)
     desc = _cached_desc(kind, B, Lq, Hq, hkv, Dqk, head_dim_v, bs, nb, max_lb)
-    if partial_out is None or lse is None or workspace is None:
-        # allocated for the stream that the kernels run on
-        with torch.cuda.stream(stream):
-            if partial_out is None:
-                partial_out = torch.empty((dcp_size, B, Lq, Hq, head_dim_v), dtype=torch.float32, device=q.device)
-            if lse is None:
-                lse = torch.empty((dcp_size, B, Lq, Hq), dtype=torch.float32, device=q.device)
-            size = int(_lib.dcp_tree_attn_workspace_size(desc, dcp_size))
-            if workspace is None and size:
-                workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
-    _check_tensors(call, torch.float32, device, partial_out, lse)
-    if partial_out.numel() != dcp_size * B * Lq * Hq * head_dim_v or lse.numel() != dcp_size * B * Lq * Hq:
-        _refuse(call, "partial_out is [N][B][Lq][Hq][Dv] and lse [N][B][Lq][Hq]")
-    ws_bytes = 0
-    if workspace is not None:
-        if workspace.get_device() != device or not workspace.is_contiguous():
-            _refuse(call, "the workspace is not contiguous on the current device")
-        ws_bytes = workspace.numel() * workspace.element_size()
+    partial_out, lse, workspace, ws_bytes = _attn_buffers(
+        call, _lib.dcp_tree_attn_workspace_size, desc, dcp_size, (B, Lq, Hq, head_dim_v), q.device, device, partial_out, lse,
+        workspace, stream)
     code = _lib.dcp_tree_attn(
         desc, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
         None if q_lens is None else q_lens.data_ptr(), tree_mask.data_ptr(), Lq * words if trees[0] == B else 0, dcp_size,

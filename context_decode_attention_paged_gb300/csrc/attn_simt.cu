@@ -14,7 +14,11 @@
 // (NaN, infinities) stays out of the row.  A seen value that is not finite reaches
 // the row however small its weight: neither the weight nor a later rescale may
 // round to 0 there.
+// kKv8: the 8-bit cache (codes times 2^(byte - 127) of their block and KV head),
+// causal queries with counts of their own; hidden and non-finite values as in the
+// tree form.
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <float.h>
 
 #include "dcp_device.cuh"
@@ -35,8 +39,9 @@ struct SimtParams {
   float* dst_lse;
 };
 
-template <bool kTree>
+template <bool kTree, bool kKv8>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
+  constexpr bool kStrict = kTree || kKv8;            // what a row does not see may hold anything
   const AttnArgs& a = P.a;
   extern __shared__ float4 smem_f4[];
   float* smem = reinterpret_cast<float*>(smem_f4);
@@ -63,14 +68,16 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
   const int S = a.seq_lens[b];
   TreeReq tree{};
   if constexpr (kTree) tree = tree_request(a.seq_lens, a.q_lens, a.Lq, b);
-  const bool bad_len = kTree ? tree.bad : S < a.Lq;
+  int n_q = a.Lq;                                    // queries of this request
+  if constexpr (kKv8) n_q = a.q_lens ? a.q_lens[b] : a.Lq;
+  const bool bad_len = kTree ? tree.bad : n_q < 0 || n_q > a.Lq || S < n_q;
   if (bad_len && tid == 0) set_status(a.status, DCP_ERR_BOUNDS);
   int L = bad_len ? 0 : local_len(S, r, a.I, a.N);
   if ((long long)L > (long long)a.max_lb * a.bs) {   // block table too short for seq_len
     if (tid == 0) set_status(a.status, DCP_ERR_BOUNDS);
     L = a.max_lb * a.bs;
   }
-  if (kTree && tree.n == 0) L = 0;                   // (its table is not read: a padded request may have none)
+  if ((kTree && tree.n == 0) || n_q == 0) L = 0;                   // (its table is not read: a padded request may have none)
   const int j_begin = min(L, s * P.split_tokens);
   int j_end = min(L, j_begin + P.split_tokens);
   {
@@ -107,8 +114,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
     if constexpr (kTree)   // context keys; the nodes behind them go by the mask
       lim_s[tid] = (row < rows_total && i < tree.n) ? min(j_end, local_count_upto(tree.base - 1, r, a.I, a.N)) : -1;
     else
-      lim_s[tid] = (row < rows_total && !bad_len)
-                       ? min(j_end, local_count_upto((long long)S - a.Lq + i, r, a.I, a.N))
+      lim_s[tid] = (row < rows_total && !bad_len && i < n_q)
+                       ? min(j_end, local_count_upto((long long)S - n_q + i, r, a.I, a.N))
                        : j_begin;
   }
   __syncthreads();
@@ -127,8 +134,16 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
         const int j = j0 + tt;
         const int blk = bt[j / a.bs];                 // checked against the pool above
         const long long off = (((long long)blk * a.bs + j % a.bs) * a.Hkv + g) * a.Dqk + d;
-        kval = __bfloat162float(kv[off]);
-        if (a.kind == DCP_ATTN_GQA && d < a.Dv) vval = __bfloat162float(kv[pool_elems + off]);
+        if constexpr (kKv8) {
+          const __nv_fp8_e4m3* codes = static_cast<const __nv_fp8_e4m3*>(a.kv);
+          const uint8_t* scales = a.kv_scales + (long long)blk * a.Hkv + g;
+          kval = (float)codes[off] * scale_factor(*scales);
+          if (a.kind == DCP_ATTN_GQA && d < a.Dv)
+            vval = (float)codes[pool_elems + off] * scale_factor(scales[(long long)a.num_blocks * a.Hkv]);
+        } else {
+          kval = __bfloat162float(kv[off]);
+          if (a.kind == DCP_ATTN_GQA && d < a.Dv) vval = __bfloat162float(kv[pool_elems + off]);
+        }
       }
       k_s[idx] = kval;
       if (a.kind == DCP_ATTN_GQA && d < a.Dv) v_s[tt * a.Dv + d] = vval;
@@ -160,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       float mx = m_s[tid];
       for (int tt = 0; tt < kTile; ++tt) mx = fmaxf(mx, p_s[tid * kTile + tt]);
       float alpha = 1.f, sum = 0.f;
-      if constexpr (kTree) {
+      if constexpr (kStrict) {
         // a NaN score is no maximum, but it makes the row NaN
         const float ref = mx == -INFINITY ? 0.f : mx;
         alpha = (m_s[tid] == -INFINITY) ? 0.f : fmaxf(expf(m_s[tid] - ref), FLT_MIN);
@@ -195,8 +210,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       const float* pr = p_s + rr * kTile;
       for (int tt = 0; tt < nt; ++tt) {
         const float v = vsrc[tt * vstride + d];
-        if (kTree && pr[tt] < 0.f) continue;
-        acc = kTree && !(fabsf(v) < INFINITY) ? acc + v : fmaf(pr[tt], v, acc);
+        if (kStrict && pr[tt] < 0.f) continue;
+        acc = kStrict && !(fabsf(v) < INFINITY) ? acc + v : fmaf(pr[tt], v, acc);
       }
       o_s[idx] = acc;
     }
@@ -211,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
     const int i = row / gsize, h = g * gsize + row % gsize;
     const float l = l_s[rr];
     const long long unit_row = ((((long long)r * a.B + b) * a.Lq + i) * P.n_split + s) * a.Hq + h;
-    const bool any = kTree ? !(l == 0.f) : l > 0.f;
+    const bool any = kStrict ? !(l == 0.f) : l > 0.f;
     P.dst_o[unit_row * a.Dv + d] = any ? o_s[idx] / l : 0.f;
   }
   if (tid < kRows) {
@@ -221,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
       const float l = l_s[tid];
       const long long unit_row =
           ((((long long)r * a.B + b) * a.Lq + i) * P.n_split + s) * a.Hq + h;
-      const bool any = kTree ? !(l == 0.f) : l > 0.f;
+      const bool any = kStrict ? !(l == 0.f) : l > 0.f;
       P.dst_lse[unit_row] = any ? m_s[tid] + logf(l) : -INFINITY;
     }
   }
@@ -258,7 +273,9 @@ cudaError_t launch_attn_simt(const AttnArgs& a, const SplitPlan& p) {
     P.dst_lse = a.lse;
   }
   const size_t smem = simt_smem_bytes(a);
-  void (*kern)(SimtParams) = a.tree_mask ? attn_simt_kernel<true> : attn_simt_kernel<false>;
+  void (*kern)(SimtParams) = a.kv_scales   ? attn_simt_kernel<false, true>
+                             : a.tree_mask ? attn_simt_kernel<true, false>
+                                           : attn_simt_kernel<false, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int gsize = a.Hq / a.Hkv;

@@ -105,6 +105,7 @@ dcp_status_t make_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t inter
 enum class Impl { kSimt, kMlaTc, kGqaTc, kTreeGqa };
 
 Impl select_impl(const AttnArgs& a) {
+  if (a.kv_scales != nullptr) return Impl::kSimt;
   if (a.tree_words > 0 && tree_gqa_supported(a)) return Impl::kTreeGqa;
   if (mla_tc_supported(a)) return Impl::kMlaTc;
   if (a.tree_words == 0 && gqa_tc_supported(a)) return Impl::kGqaTc;
@@ -176,6 +177,85 @@ bool cache_desc_ok(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleav
 bool rope_ok(const dcp_rope_desc_t* r) {
   return r && r->rot_dim >= 2 && r->rot_dim % 2 == 0 && r->rot_dim <= DCP_ROPE_MAX_DIM && r->rot_offset >= 0 &&
          (r->layout == DCP_ROPE_HALF || r->layout == DCP_ROPE_INTERLEAVED) && std::isfinite(r->mscale);
+}
+
+// Checks and arguments of an append (rope and rope_steps both null: no rotation).
+dcp_status_t make_append_args(const dcp_attn_desc_t* d, const dcp_rope_desc_t* rope, const uint64_t* rope_steps,
+                              const void* new_k, const void* new_v, const void* q,
+                              const dcp_append_strides_t* strides, void* q_out, const int32_t* pos_offsets,
+                              int64_t pos_offsets_stride, const int32_t* q_lens, void* kv_cache,
+                              const int32_t* block_tables, const int32_t* seq_lens, int32_t dcp_size,
+                              int32_t interleave, void* stream, AppendArgs* out) {
+  if (!d || !new_k || !kv_cache || !block_tables || !seq_lens) return DCP_ERR_INVALID_ARG;
+  if (!cache_desc_ok(d, dcp_size, interleave)) return DCP_ERR_INVALID_ARG;
+  if ((rope != nullptr) != (rope_steps != nullptr) || (rope && !rope_ok(rope))) return DCP_ERR_INVALID_ARG;
+  const bool gqa = d->kind == DCP_ATTN_GQA;
+  if (gqa != (new_v != nullptr) || (q != nullptr) != (q_out != nullptr)) return DCP_ERR_INVALID_ARG;
+  if (rope && rope->rot_offset > d->head_dim_qk - rope->rot_dim) return DCP_ERR_INVALID_ARG;
+  if (q && (d->num_q_heads < 1 || (long long)d->num_q_heads * d->head_dim_qk > (1LL << 24))) return DCP_ERR_INVALID_ARG;
+  if (!aligned(new_k, 16) || !aligned(kv_cache, 16) || (rope_steps && !aligned(rope_steps, 8)) || (new_v && !aligned(new_v, 16)) ||
+      (q && (!aligned(q, 16) || !aligned(q_out, 16))) || (pos_offsets && !aligned(pos_offsets, 4)))
+    return DCP_ERR_INVALID_ARG;
+  if (pos_offsets && pos_offsets_stride != 0 && pos_offsets_stride < d->q_len) return DCP_ERR_INVALID_ARG;
+  if ((long long)d->batch * d->q_len > INT_MAX) return DCP_ERR_INVALID_ARG;
+  const long long k_row = (long long)d->num_kv_heads * d->head_dim_qk;
+  const long long q_row = q ? (long long)d->num_q_heads * d->head_dim_qk : 0;
+  AppendArgs& a = *out;
+  a.k_batch = k_row * d->q_len, a.k_token = k_row;
+  a.v_batch = k_row * d->q_len, a.v_token = k_row;
+  a.q_batch = q_row * d->q_len, a.q_token = q_row;
+  if (strides) {
+    auto stride_ok = [](int64_t batch, int64_t token, long long row) {
+      return batch % 8 == 0 && token % 8 == 0 && batch >= 0 && (token == 0 || token >= row);
+    };
+    if (!stride_ok(strides->k_batch, strides->k_token, k_row) ||
+        (gqa && !stride_ok(strides->v_batch, strides->v_token, k_row)) ||
+        (q && !stride_ok(strides->q_batch, strides->q_token, q_row)))
+      return DCP_ERR_INVALID_ARG;
+    if (q && q == q_out && (strides->q_token != a.q_token || strides->q_batch != a.q_batch)) return DCP_ERR_INVALID_ARG;
+    a.k_batch = strides->k_batch, a.k_token = strides->k_token;
+    a.v_batch = strides->v_batch, a.v_token = strides->v_token;
+    a.q_batch = strides->q_batch, a.q_token = strides->q_token;
+  }
+  a.k = new_k, a.v = new_v, a.q = q, a.q_out = q_out;
+  a.steps = reinterpret_cast<const unsigned long long*>(rope_steps);
+  a.pos_offsets = pos_offsets, a.pos_stride = pos_offsets_stride, a.q_lens = q_lens;
+  a.cache = kv_cache, a.block_tables = block_tables, a.seq_lens = seq_lens;
+  a.B = d->batch, a.L = d->q_len, a.Hq = q ? d->num_q_heads : 0, a.Hkv = d->num_kv_heads, a.D = d->head_dim_qk;
+  a.bs = d->block_size, a.num_blocks = d->num_blocks, a.max_lb = d->max_local_blocks, a.N = dcp_size, a.I = interleave;
+  if (rope) {
+    a.rot_dim = rope->rot_dim, a.rot_offset = rope->rot_offset;
+    a.interleaved = rope->layout == DCP_ROPE_INTERLEAVED, a.mscale = rope->mscale;
+  }
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.status = status_ptr(a.stream);
+  if (!a.status) return DCP_ERR_CUDA;
+  return DCP_OK;
+}
+
+// Checks and arguments of an append's norms (null: none).
+dcp_status_t make_norm_args(const dcp_attn_desc_t* d, const dcp_norm_desc_t* norm, NormAppendArgs* a) {
+  if (!d) return DCP_ERR_INVALID_ARG;
+  if (norm && (norm->q_weight || norm->k_weight)) {
+    if (norm->norm_dim < 8 || norm->norm_dim % 8 || norm->norm_dim > d->head_dim_qk) return DCP_ERR_INVALID_ARG;
+    if (!(norm->eps >= 1e-20f && norm->eps <= 1e20f)) return DCP_ERR_INVALID_ARG;
+    if (!aligned(norm->q_weight, 4) || !aligned(norm->k_weight, 4)) return DCP_ERR_INVALID_ARG;
+    a->norm_dim = norm->norm_dim;
+    a->eps = norm->eps;
+    a->q_weight = norm->q_weight;
+    a->k_weight = norm->k_weight;
+  }
+  return d->head_dim_qk > DCP_APPEND_MAX_HEAD_DIM ? DCP_ERR_UNSUPPORTED : DCP_OK;
+}
+
+// Arguments of a call over the 8-bit cache: those of dcp_decode_attn and the pool's limits.
+dcp_status_t make_kv8_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave, float scale,
+                           int32_t causal_q_len, AttnArgs* a) {
+  const dcp_status_t st = make_args(d, dcp_size, interleave, scale, causal_q_len, a);
+  if (st != DCP_OK) return st;
+  static const uint8_t any = 0;
+  a->kv_scales = &any;               // (says which kernels there are; the call sets the scales)
+  return DCP_OK;
 }
 
 }  // namespace
@@ -502,48 +582,118 @@ dcp_status_t dcp_kv_cache_append(const dcp_attn_desc_t* d, const dcp_rope_desc_t
                                  const int32_t* block_tables, const int32_t* seq_lens, int32_t dcp_size,
                                  int32_t interleave, void* stream) {
   NvtxRange range("dcp_kv_cache_append");
-  if (!d || !rope_steps || !new_k || !kv_cache || !block_tables || !seq_lens) return DCP_ERR_INVALID_ARG;
-  if (!cache_desc_ok(d, dcp_size, interleave) || !rope_ok(rope)) return DCP_ERR_INVALID_ARG;
-  const bool gqa = d->kind == DCP_ATTN_GQA;
-  if (gqa != (new_v != nullptr) || (q != nullptr) != (q_out != nullptr)) return DCP_ERR_INVALID_ARG;
-  if (rope->rot_offset > d->head_dim_qk - rope->rot_dim) return DCP_ERR_INVALID_ARG;
-  if (q && (d->num_q_heads < 1 || (long long)d->num_q_heads * d->head_dim_qk > (1LL << 24))) return DCP_ERR_INVALID_ARG;
-  if (!aligned(new_k, 16) || !aligned(kv_cache, 16) || !aligned(rope_steps, 8) || (new_v && !aligned(new_v, 16)) ||
-      (q && (!aligned(q, 16) || !aligned(q_out, 16))) || (pos_offsets && !aligned(pos_offsets, 4)))
-    return DCP_ERR_INVALID_ARG;
-  if (pos_offsets && pos_offsets_stride != 0 && pos_offsets_stride < d->q_len) return DCP_ERR_INVALID_ARG;
-  if ((long long)d->batch * d->q_len > INT_MAX) return DCP_ERR_INVALID_ARG;
-  const long long k_row = (long long)d->num_kv_heads * d->head_dim_qk;
-  const long long q_row = q ? (long long)d->num_q_heads * d->head_dim_qk : 0;
+  if (!rope_steps) return DCP_ERR_INVALID_ARG;
   AppendArgs a{};
-  a.k_batch = k_row * d->q_len, a.k_token = k_row;
-  a.v_batch = k_row * d->q_len, a.v_token = k_row;
-  a.q_batch = q_row * d->q_len, a.q_token = q_row;
-  if (strides) {
-    auto stride_ok = [](int64_t batch, int64_t token, long long row) {
-      return batch % 8 == 0 && token % 8 == 0 && batch >= 0 && (token == 0 || token >= row);
-    };
-    if (!stride_ok(strides->k_batch, strides->k_token, k_row) ||
-        (gqa && !stride_ok(strides->v_batch, strides->v_token, k_row)) ||
-        (q && !stride_ok(strides->q_batch, strides->q_token, q_row)))
-      return DCP_ERR_INVALID_ARG;
-    if (q && q == q_out && (strides->q_token != a.q_token || strides->q_batch != a.q_batch)) return DCP_ERR_INVALID_ARG;
-    a.k_batch = strides->k_batch, a.k_token = strides->k_token;
-    a.v_batch = strides->v_batch, a.v_token = strides->v_token;
-    a.q_batch = strides->q_batch, a.q_token = strides->q_token;
-  }
-  a.k = new_k, a.v = new_v, a.q = q, a.q_out = q_out;
-  a.steps = reinterpret_cast<const unsigned long long*>(rope_steps);
-  a.pos_offsets = pos_offsets, a.pos_stride = pos_offsets_stride, a.q_lens = q_lens;
-  a.cache = kv_cache, a.block_tables = block_tables, a.seq_lens = seq_lens;
-  a.B = d->batch, a.L = d->q_len, a.Hq = q ? d->num_q_heads : 0, a.Hkv = d->num_kv_heads, a.D = d->head_dim_qk;
+  const dcp_status_t st = make_append_args(d, rope, rope_steps, new_k, new_v, q, strides, q_out, pos_offsets,
+                                           pos_offsets_stride, q_lens, kv_cache, block_tables, seq_lens, dcp_size,
+                                           interleave, stream, &a);
+  return st != DCP_OK ? st : from_cuda(launch_kv_append(a));
+}
+
+dcp_status_t dcp_kv_cache_append_norm(const dcp_attn_desc_t* d, const dcp_rope_desc_t* rope, const uint64_t* rope_steps,
+                                      const dcp_norm_desc_t* norm, const void* new_k, const void* new_v, const void* q,
+                                      const dcp_append_strides_t* strides, void* q_out, const int32_t* pos_offsets,
+                                      int64_t pos_offsets_stride, const int32_t* q_lens, void* kv_cache,
+                                      const int32_t* block_tables, const int32_t* seq_lens, int32_t dcp_size,
+                                      int32_t interleave, void* stream) {
+  NvtxRange range("dcp_kv_cache_append_norm");
+  NormAppendArgs a{};
+  dcp_status_t st = make_norm_args(d, norm, &a);
+  if (st == DCP_OK)
+    st = make_append_args(d, rope, rope_steps, new_k, new_v, q, strides, q_out, pos_offsets, pos_offsets_stride, q_lens,
+                          kv_cache, block_tables, seq_lens, dcp_size, interleave, stream, &a);
+  return st != DCP_OK ? st : from_cuda(launch_kv_append_norm(a));
+}
+
+dcp_status_t dcp_kv8_append(const dcp_attn_desc_t* d, const dcp_rope_desc_t* rope, const uint64_t* rope_steps,
+                            const dcp_norm_desc_t* norm, const void* new_k, const void* new_v, const void* q,
+                            const dcp_append_strides_t* strides, void* q_out, const int32_t* pos_offsets,
+                            int64_t pos_offsets_stride, const int32_t* q_lens, void* kv8_cache, uint8_t* kv8_scales,
+                            const int32_t* block_tables, const int32_t* seq_lens, int32_t dcp_size, int32_t interleave,
+                            void* stream) {
+  NvtxRange range("dcp_kv8_append");
+  if (!kv8_scales) return DCP_ERR_INVALID_ARG;
+  NormAppendArgs a{};
+  dcp_status_t st = make_norm_args(d, norm, &a);
+  if (st == DCP_OK)
+    st = make_append_args(d, rope, rope_steps, new_k, new_v, q, strides, q_out, pos_offsets, pos_offsets_stride, q_lens,
+                          kv8_cache, block_tables, seq_lens, dcp_size, interleave, stream, &a);
+  a.scales = kv8_scales;
+  return st != DCP_OK ? st : from_cuda(launch_kv_append_norm(a));
+}
+
+dcp_status_t dcp_kv8_read(const dcp_attn_desc_t* d, const void* kv8_cache, const uint8_t* kv8_scales,
+                          const int32_t* block_tables, const int32_t* seq_lens, const int32_t* starts, int32_t n,
+                          void* out_k, void* out_v, int32_t dcp_size, int32_t interleave, void* stream) {
+  NvtxRange range("dcp_kv8_read");
+  if (!d || !kv8_cache || !kv8_scales || !block_tables || !seq_lens || (!out_k && !out_v) || n < 1)
+    return DCP_ERR_INVALID_ARG;
+  if (!cache_desc_ok(d, dcp_size, interleave)) return DCP_ERR_INVALID_ARG;
+  if (d->kind == DCP_ATTN_MLA && (!out_k || out_v)) return DCP_ERR_INVALID_ARG;
+  if (!aligned(kv8_cache, 16) || (out_k && !aligned(out_k, 16)) || (out_v && !aligned(out_v, 16)))
+    return DCP_ERR_INVALID_ARG;
+  if ((long long)d->batch * n > INT_MAX) return DCP_ERR_INVALID_ARG;
+  ReadArgs a{};
+  a.cache = static_cast<const uint8_t*>(kv8_cache), a.scales = kv8_scales;
+  a.block_tables = block_tables, a.seq_lens = seq_lens, a.starts = starts;
+  a.out_k = out_k, a.out_v = out_v;
+  a.B = d->batch, a.n = n, a.Hkv = d->num_kv_heads, a.D = d->head_dim_qk;
   a.bs = d->block_size, a.num_blocks = d->num_blocks, a.max_lb = d->max_local_blocks, a.N = dcp_size, a.I = interleave;
-  a.rot_dim = rope->rot_dim, a.rot_offset = rope->rot_offset;
-  a.interleaved = rope->layout == DCP_ROPE_INTERLEAVED, a.mscale = rope->mscale;
   a.stream = static_cast<cudaStream_t>(stream);
   a.status = status_ptr(a.stream);
   if (!a.status) return DCP_ERR_CUDA;
-  return from_cuda(launch_kv_append(a));
+  return from_cuda(launch_kv8_read(a));
+}
+
+size_t dcp_kv8_decode_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dcp_size) {
+  AttnArgs a{};
+  if (make_kv8_args(d, dcp_size, 1, 1.0f, d ? d->q_len : 1, &a) != DCP_OK) return 0;
+  return plan_for(a, select_impl(a), device_sm_count()).ws_bytes;
+}
+
+int32_t dcp_kv8_decode_attn_launches(const dcp_attn_desc_t* d, int32_t dcp_size) {
+  AttnArgs a{};
+  if (make_kv8_args(d, dcp_size, 1, 1.0f, d ? d->q_len : 1, &a) != DCP_OK) return 0;
+  const SplitPlan plan = plan_for(a, select_impl(a), device_sm_count());
+  return 1 + (plan.n_split > 1 ? 1 : 0);
+}
+
+int32_t dcp_kv8_decode_attn_kernel_kind(const dcp_attn_desc_t* d, int32_t dcp_size) {
+  AttnArgs a{};
+  if (make_kv8_args(d, dcp_size, 1, 1.0f, d ? d->q_len : 1, &a) != DCP_OK) return DCP_KERNEL_NONE;
+  return kind_of(select_impl(a));
+}
+
+dcp_status_t dcp_kv8_decode_attn(const dcp_attn_desc_t* d, const void* q, const void* kv8_cache,
+                                 const uint8_t* kv8_scales, const int32_t* block_tables, const int32_t* seq_lens,
+                                 const int32_t* q_lens, int32_t dcp_size, int32_t interleave, float scale,
+                                 int32_t causal_q_len, float* partial_out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  NvtxRange range("dcp_kv8_decode_attn");
+  AttnArgs a{};
+  const dcp_status_t st = make_kv8_args(d, dcp_size, interleave, scale, causal_q_len, &a);
+  if (st != DCP_OK) return st;
+  if (!q || !kv8_cache || !kv8_scales || !block_tables || !seq_lens || !partial_out || !lse) return DCP_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv8_cache, 16) || !aligned(partial_out, 16) || !aligned(lse, 4))
+    return DCP_ERR_INVALID_ARG;
+  const Impl impl = select_impl(a);
+  const SplitPlan plan = plan_for(a, impl, device_sm_count());
+  if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes || !aligned(workspace, 256)))
+    return DCP_ERR_INVALID_ARG;
+  a.q = q;
+  a.kv = kv8_cache;
+  a.kv_scales = kv8_scales;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.q_lens = q_lens;
+  a.partial_out = partial_out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.status = status_ptr(a.stream);
+  if (!a.status) return DCP_ERR_CUDA;
+  return launch_impl(a, impl, plan);
 }
 
 dcp_status_t dcp_kv_cache_commit(const dcp_attn_desc_t* d, void* kv_cache, const int32_t* block_tables,

@@ -44,4 +44,9 @@ __device__ __forceinline__ int local_count_upto(long long p, int r, int I, int N
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// The factor that a scale byte of the 8-bit cache stands for: 2^(s - 127), 255 NaN.
+__device__ __forceinline__ float scale_factor(uint32_t s) {
+  return __uint_as_float(s == 0 ? 0x400000u : s == 255 ? 0x7fc00000u : s << 23);
+}
+
 }  // namespace dcp

@@ -29,7 +29,9 @@ struct AttnArgs {
   const uint32_t* tree_mask;       // [B][Lq][tree_words], requests tree_mask_stride words apart
   long long tree_mask_stride;
   int tree_words;                  // ceil(Lq / 32)
-  const int32_t* q_lens;           // [B] nodes per request, or null (Lq each)
+  const int32_t* q_lens;           // [B] nodes (8-bit cache: queries) per request, or null (Lq each)
+  // the cache in 8 bits (null: bf16): exponent bytes [2][num_blocks][Hkv], MLA [num_blocks]
+  const uint8_t* kv_scales;
 };
 
 // How a call is cut into work units along the local KV axis.
@@ -103,6 +105,27 @@ struct AppendArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_kv_append(const AppendArgs& a);
+
+// The same with norms (norm_dim 0: none) and rotation (rot_dim 0: none) on the way, into the
+// bf16 cache or (scales set) the 8-bit one: see dcp_kv_cache_append_norm, dcp_kv8_append.
+struct NormAppendArgs : AppendArgs {
+  const float *q_weight, *k_weight;
+  int norm_dim;
+  float eps;
+  uint8_t* scales;
+};
+cudaError_t launch_kv_append_norm(const NormAppendArgs& a);
+
+// Rows of the 8-bit cache as bf16: see dcp_kv8_read.
+struct ReadArgs {
+  const uint8_t *cache, *scales;
+  const int32_t *block_tables, *seq_lens, *starts;
+  void *out_k, *out_v;
+  int B, n, Hkv, D, bs, num_blocks, max_lb, N, I;
+  int* status;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv8_read(const ReadArgs& a);
 
 // Move the accepted nodes' rows behind the context: see dcp_kv_cache_commit.
 struct CommitArgs {

@@ -1,0 +1,83 @@
+// Reading rows of the 8-bit cache back as bf16: value = code * 2^(s - 127), the
+// product exact for every scale that dcp_kv8_append writes.
+//
+// Bound by HBM: one byte read and two written per value.  A warp takes a token
+// and walks its row (every KV head, keys then values), a lane 8 codes at a time;
+// the token's table entry and its scales come first, the codes of up to kAhead
+// vectors of a lane together.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "dcp_device.cuh"
+#include "dcp_internal.h"
+
+namespace dcp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 4;          // vectors of a lane in flight
+
+__global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long token = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (token >= (long long)a.B * a.n) return;
+  const int b = (int)(token / a.n), i = (int)(token % a.n);
+  const int S = a.seq_lens[b], start = a.starts ? a.starts[b] : 0;
+  if (S < 0 || start < 0) {
+    if (lane == 0) set_status(a.status, DCP_ERR_BOUNDS);
+    return;
+  }
+  const long long t = (long long)start + i;
+  if (t >= S) return;
+  const int r = (int)((t / a.I) % a.N);
+  const long long j = (t / ((long long)a.I * a.N)) * a.I + t % a.I, jb = j / a.bs;
+  const int blk = jb < a.max_lb ? a.block_tables[((long long)r * a.B + b) * a.max_lb + jb] : -1;
+  if ((unsigned)blk >= (unsigned)a.num_blocks) {
+    if (lane == 0) set_status(a.status, DCP_ERR_BOUNDS);
+    return;
+  }
+  const int per_head = a.D / 8, vecs = a.Hkv * per_head;
+  const long long pool = (long long)a.num_blocks * a.bs * a.Hkv * a.D;
+  for (int kind = 0; kind < 2; ++kind) {
+    void* out = kind == 0 ? a.out_k : a.out_v;
+    if (out == nullptr) continue;
+    const uint2* src = reinterpret_cast<const uint2*>(a.cache + kind * pool + ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D);
+    const uint8_t* scales = a.scales + ((long long)kind * a.num_blocks + blk) * a.Hkv;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + token * a.Hkv * a.D);
+    for (int c0 = lane; c0 < vecs; c0 += 32 * kAhead) {
+      uint2 u[kAhead];
+      float f[kAhead];
+#pragma unroll
+      for (int m = 0; m < kAhead; ++m) {
+        const int c = min(c0 + 32 * m, vecs - 1);
+        u[m] = __ldcs(src + c);
+        f[m] = scale_factor(scales[c / per_head]);
+      }
+#pragma unroll
+      for (int m = 0; m < kAhead; ++m) {
+        const uint32_t w[2] = {u[m].x, u[m].y};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t pair;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+          const __nv_bfloat162 q = __floats2bfloat162_rn(v.x * f[m], v.y * f[m]);
+          o[k] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        if (c0 + 32 * m < vecs) __stcs(dst + c0 + 32 * m, make_uint4(o[0], o[1], o[2], o[3]));
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_read(const ReadArgs& a) {
+  const long long blocks = ((long long)a.B * a.n + kWarps - 1) / kWarps;
+  kv8_read_kernel<<<(unsigned)blocks, kThreads, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace dcp

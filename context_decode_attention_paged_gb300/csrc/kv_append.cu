@@ -33,6 +33,7 @@
 
 #include <algorithm>
 
+#include "dcp_append.cuh"
 #include "dcp_device.cuh"
 #include "dcp_internal.h"
 
@@ -42,7 +43,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlocks = 3;         // resident blocks of an SM
 constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
-constexpr int kCopies = 8;         // vectors of a lane in flight while copying
 constexpr int kTaskBytes = 8192;   // rows of a task, at most (when tokens abound)
 constexpr int kMaxPairs = DCP_ROPE_MAX_DIM / 2;   // rotated pairs of a head (shared memory)
 constexpr int kScan = 1024;        // requests whose token counts a block sums
@@ -88,13 +88,6 @@ __device__ __forceinline__ void turn_interleaved(uint4& u, const float* c, const
     const float a = bf16_lo(x[w]), b = bf16_hi(x[w]);
     x[w] = pack2(a * c[w] - b * s[w], b * c[w] + a * s[w]);
   }
-}
-
-// Tokens of a request that are there (0 for a request whose lengths are out of range).
-__device__ __forceinline__ int present(const AppendArgs& a, int b, bool* bad) {
-  const int n = a.q_lens ? a.q_lens[b] : a.L;
-  *bad = n < 0 || n > a.L || a.seq_lens[b] < n;
-  return *bad ? 0 : n;
 }
 
 // ends[b] = tokens of requests 0 .. b, for all b < B <= kScan (whole block).
@@ -157,33 +150,6 @@ __device__ __forceinline__ long long cell_of(const AppendArgs& a, int b, long lo
   if ((unsigned)blk < (unsigned)a.num_blocks) return ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D;
   if (reports) set_status(a.status, DCP_ERR_BOUNDS);
   return -1;
-}
-
-// A warp copies n vectors, vector c from src + at(c) to dst + at(c).
-template <typename At>
-__device__ __forceinline__ void copy_vectors(const uint4* src, uint4* dst, int n, int lane, At at) {
-  uint4 v[kCopies];
-  int off[kCopies];
-  int c = lane;
-  for (; c + 32 * (kCopies - 1) < n; c += 32 * kCopies) {
-#pragma unroll
-    for (int m = 0; m < kCopies; ++m) {
-      off[m] = at(c + 32 * m);
-      v[m] = src[off[m]];
-    }
-#pragma unroll
-    for (int m = 0; m < kCopies; ++m) dst[off[m]] = v[m];
-  }
-  if (c < n) {
-    // past the end the last vector again: the same value to the same place
-#pragma unroll
-    for (int m = 0; m < kCopies; ++m) {
-      off[m] = at(min(c + 32 * m, n - 1));
-      v[m] = src[off[m]];
-    }
-#pragma unroll
-    for (int m = 0; m < kCopies; ++m) dst[off[m]] = v[m];
-  }
 }
 
 template <bool kHalfLayout>

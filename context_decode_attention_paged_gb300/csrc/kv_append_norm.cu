@@ -1,0 +1,614 @@
+// Appending keys and values to the sharded cache with RMS norms of the heads and
+// the rotary position applied on the way, into the bf16 cache or into the 8-bit
+// one, and the same for the queries of these tokens.
+//
+// "Context Parallel Guide", section "Overview": a token's KV is stored once, by
+// the shard that owns its position (interleave rule, section "Decode Context
+// Parallel").
+//
+// Mathematics.  y = x w / sqrt(mean x^2 + eps) over the first norm_dim dims of a
+// head; pair k at position p then turns by p f_k.  As in kv_append.cu the table
+// holds frac(f_k / 2 pi) 2^64, so the top 32 bits of the wrapped product are the
+// phase at any position; what is left of the nearest quarter turn goes through
+// the Taylor series of sin and cos (|x| <= pi / 4: the first terms left out are
+// below 2e-9), about 1e-7 in all.
+// The 8-bit cache has one scale 2^e per block, KV head and K or V: the new rows'
+// largest magnitude a sets it where the block was empty (a <= 112 2^e), it stays
+// while a <= 448 2^e and otherwise the block's earlier codes are rounded to the
+// scale that a wants.  A quarter of the range is left free at first, so a later
+// row seldom makes a block read and written again; codes have exponents of their
+// own, so what that costs is two of the 15 binades below the largest value.
+//
+// Layout.  SG lanes hold a row of one head, SLOTS 16-byte vectors each (128 dims:
+// 16 lanes, two rows a warp), so a norm is one pass of shuffles in the group.
+// Pairs of the interleaved layout lie in a lane; in the half layout the partner
+// vector is another lane's (a shuffle); any other rotated part goes through
+// shared memory.  Queries: a warp takes a token's heads in turn, its angles and
+// weights in registers.  Rows of the 8-bit cache: a team (a warp where a block
+// gets few rows, else a CTA) takes all new rows of one block and KV head: norm,
+// rotation and maximum, then the codes; rows that its registers do not hold are
+// read (from L2) and turned again.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <float.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "dcp_append.cuh"
+#include "dcp_device.cuh"
+#include "dcp_internal.h"
+
+namespace dcp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
+constexpr int kTaskBytes = 8192;   // rows of a query task, at most (when tokens abound)
+
+enum Rot { kPair = 0, kSwap = 1, kAny = 2 };
+
+struct Params {
+  NormAppendArgs a;
+  __nv_bfloat16 *pool_k, *pool_v;  // bf16 cache
+  uint8_t *codes_k, *codes_v;      // 8-bit cache
+  int groups;                      // (block, shard) groups of a request, or its tokens
+  int nblk;                        // blocks of a shard that may get rows; 0: groups are tokens
+  unsigned kv_blocks;              // CTAs of the 8-bit cache's rows, before the queries'
+  long long kv_tasks;
+  int parts, part_heads;           // query heads of a token in parts
+  long long q_tasks;
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// cos and sin (times mscale) of position pos in pair k
+__device__ __forceinline__ void turn_of(const AppendArgs& a, long long pos, int k, float& c, float& s) {
+  const uint32_t phase = (uint32_t)(((unsigned long long)pos * a.steps[k]) >> 32);   // 2^-32 turns
+  const uint32_t quarter = (phase + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(phase - (quarter << 30)) * (0x1p-31f * 3.14159265358979f);
+  const float z = x * x;
+  const float sn = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), 1.f);
+  const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+  const bool odd = quarter & 1u;
+  c = (odd ? sn : cs) * ((quarter + 1) & 2u ? -a.mscale : a.mscale);
+  s = (odd ? cs : sn) * (quarter & 2u ? -a.mscale : a.mscale);
+}
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[2 * k] = bf16_lo(w[k]), x[2 * k + 1] = bf16_hi(w[k]);
+}
+
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+
+// Floats of shared memory that a warp needs to rotate.
+__host__ __device__ constexpr int scratch_floats(int rot, int sg, int rot_dim) {
+  return rot == kAny ? 2 * (32 / sg) * rot_dim : 0;
+}
+
+// A lane's part of a row of one head: dims 8 (sl + SG s) .. + 7, s < SLOTS.
+template <int SG, int SLOTS, int kRot>
+struct Rows {
+  static constexpr int kAngles = kRot == kPair ? 4 : kRot == kSwap ? 8 : 1;
+  const AppendArgs& a;
+  int sl, vecs, norm_vecs;
+  float eps, per_dim;              // 1 / norm_dim
+  bool normed;
+  float w[SLOTS][8];
+  float c[SLOTS][kAngles], s[SLOTS][kAngles];
+  uint32_t turns;                  // kPair: bit 4 slot + pair; kSwap: 1 where the lane turns
+  int partner;                     // kSwap: lane of the partner vector
+  float *values, *angles;          // kAny: this group's shared memory
+
+  __device__ __forceinline__ Rows(const NormAppendArgs& n, int lane, float* scratch)
+      : a(n), sl(lane % SG), vecs(n.D / 8), norm_vecs(n.norm_dim / 8), eps(n.eps), per_dim(1.f / (float)n.norm_dim),
+        normed(false), turns(0), partner(lane), values(nullptr), angles(nullptr) {
+    if constexpr (kRot == kPair) {
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = 8 * (sl + SG * m) + 2 * e - a.rot_offset;
+          if (d >= 0 && d < a.rot_dim) turns |= 1u << (4 * m + e);
+        }
+    } else if constexpr (kRot == kSwap) {
+      const int half = a.rot_dim / 16, v = sl - a.rot_offset / 8;
+      if (v >= 0 && v < 2 * half) {
+        turns = 1;
+        partner = lane + (v < half ? half : -half);
+      }
+    } else {
+      values = scratch + (lane / SG) * 2 * a.rot_dim;
+      angles = values + a.rot_dim;
+    }
+  }
+
+  __device__ __forceinline__ void set_weights(const float* weight) {
+    normed = weight != nullptr;
+#pragma unroll
+    for (int m = 0; m < SLOTS; ++m)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[m][e] = normed && sl + SG * m < norm_vecs ? weight[8 * (sl + SG * m) + e] : 1.f;
+  }
+
+  __device__ __forceinline__ void set_position(long long pos) {
+    if constexpr (kRot == kPair) {
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (turns >> (4 * m + e) & 1u) turn_of(a, pos, (8 * (sl + SG * m) + 2 * e - a.rot_offset) / 2, c[m][e], s[m][e]);
+    } else if constexpr (kRot == kSwap) {
+      if (turns) {
+        const int half = a.rot_dim / 16, v = sl - a.rot_offset / 8;
+        const bool second = v >= half;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          turn_of(a, pos, 8 * (second ? v - half : v) + e, c[0][e], s[0][e]);
+          if (!second) s[0][e] = -s[0][e];
+        }
+      }
+    } else {
+      __syncwarp();                 // (the last row's angles have been read)
+      for (int k = sl; k < a.rot_dim / 2; k += SG) turn_of(a, pos, k, angles[2 * k], angles[2 * k + 1]);
+      __syncwarp();
+    }
+  }
+
+  // a row of zeros where src is null
+  __device__ __forceinline__ void load(const __nv_bfloat16* src, uint4 (&raw)[SLOTS]) const {
+#pragma unroll
+    for (int m = 0; m < SLOTS; ++m)
+      raw[m] = src != nullptr && sl + SG * m < vecs ? reinterpret_cast<const uint4*>(src)[sl + SG * m] : make_uint4(0, 0, 0, 0);
+  }
+
+  __device__ __forceinline__ float group_sum(float v) const {
+#pragma unroll
+    for (int o = SG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+
+  // norm and rotation of the row, in place (whole warp)
+  __device__ __forceinline__ void turn(float (&x)[SLOTS][8]) const {
+    if (normed) {
+      float sum = 0.f;
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m)
+        if (sl + SG * m < norm_vecs)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum = fmaf(x[m][e], x[m][e], sum);
+      sum = group_sum(sum);
+      float r = rsqrtf(fmaf(sum, per_dim, eps)), by = 1.f;
+      if (__any_sync(0xffffffffu, sum > FLT_MAX)) {
+        // squares past fp32's range (or an infinity): the row scaled down first; eps is below rounding then
+        float small = 0.f;
+#pragma unroll
+        for (int m = 0; m < SLOTS; ++m)
+          if (sl + SG * m < norm_vecs)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) small = fmaf(x[m][e] * 0x1p-70f, x[m][e] * 0x1p-70f, small);
+        small = group_sum(small);
+        if (sum > FLT_MAX) r = rsqrtf(small * per_dim), by = 0x1p-70f;
+      }
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m)
+        if (sl + SG * m < norm_vecs)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[m][e] = x[m][e] * by * r * w[m][e];
+    }
+    if constexpr (kRot == kPair) {
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (turns >> (4 * m + e) & 1u) {
+            const float x0 = x[m][2 * e], x1 = x[m][2 * e + 1];
+            x[m][2 * e] = x0 * c[m][e] - x1 * s[m][e];
+            x[m][2 * e + 1] = x1 * c[m][e] + x0 * s[m][e];
+          }
+    } else if constexpr (kRot == kSwap) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float other = __shfl_sync(0xffffffffu, x[0][e], partner);
+        if (turns) x[0][e] = x[0][e] * c[0][e] + other * s[0][e];
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = 8 * (sl + SG * m) + e - a.rot_offset;
+          if (d >= 0 && d < a.rot_dim) values[d] = x[m][e];
+        }
+      __syncwarp();
+      const int half = a.rot_dim / 2;
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = 8 * (sl + SG * m) + e - a.rot_offset;
+          if (d < 0 || d >= a.rot_dim) continue;
+          const bool second = a.interleaved ? d & 1 : d >= half;
+          const int k = a.interleaved ? d >> 1 : second ? d - half : d;
+          const float other = values[a.interleaved ? d ^ 1 : second ? d - half : d + half];
+          x[m][e] = x[m][e] * angles[2 * k] + other * (second ? angles[2 * k + 1] : -angles[2 * k + 1]);
+        }
+      __syncwarp();
+    }
+  }
+
+  __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const float (&x)[SLOTS][8]) const {
+    if (dst == nullptr) return;
+#pragma unroll
+    for (int m = 0; m < SLOTS; ++m)
+      if (sl + SG * m < vecs) reinterpret_cast<uint4*>(dst)[sl + SG * m] = pack(x[m]);
+  }
+};
+
+__device__ __forceinline__ long long position_of(const AppendArgs& a, int b, int i, long long base) {
+  return base + (a.pos_offsets ? a.pos_offsets[b * a.pos_stride + i] : i);
+}
+
+// Block of local token l of request b on shard r; -1 (and DCP_ERR_BOUNDS) where the table has none.
+__device__ __forceinline__ int block_of(const AppendArgs& a, int b, int r, int jb, bool reports) {
+  const int blk = jb < a.max_lb ? a.block_tables[((long long)r * a.B + b) * a.max_lb + jb] : -1;
+  if ((unsigned)blk < (unsigned)a.num_blocks) return blk;
+  if (reports) set_status(a.status, DCP_ERR_BOUNDS);
+  return -1;
+}
+
+// Heads [h0, h1) of a token: src + h D -> dst + h D, in turn over the warp's groups.
+template <int SG, int SLOTS, int kRot>
+__device__ __forceinline__ void head_rows(const Rows<SG, SLOTS, kRot>& rows, const __nv_bfloat16* src, __nv_bfloat16* dst,
+                                          int h0, int h1, int lane, int D) {
+  constexpr int kStep = 32 / SG, kDeep = SLOTS > 1 ? 2 : kAhead;
+  uint4 raw[kDeep][SLOTS];
+  const int first = h0 + lane / SG;
+  auto load = [&](int h) {
+#pragma unroll
+    for (int m = 0; m < kDeep; ++m)
+      rows.load(h + m * kStep < h1 ? src + (long long)(h + m * kStep) * D : nullptr, raw[m]);
+  };
+  load(first);
+  for (int h = h0; h < h1; h += kDeep * kStep) {             // (whole warps: the norms shuffle)
+    float x[kDeep][SLOTS][8];
+#pragma unroll
+    for (int m = 0; m < kDeep; ++m)
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) unpack(raw[m][k], x[m][k]);
+    const int next = h + kDeep * kStep;
+    if (next < h1) load(next + lane / SG);
+#pragma unroll
+    for (int m = 0; m < kDeep; ++m) {
+      if (h + m * kStep >= h1) break;
+      rows.turn(x[m]);
+      const int hh = h + m * kStep + lane / SG;
+      rows.store_bf16(hh < h1 ? dst + (long long)hh * D : nullptr, x[m]);
+    }
+  }
+}
+
+// Task (token, part of its query heads, or behind them its keys and values into the bf16 cache).
+template <int SG, int SLOTS, int kRot>
+__device__ __forceinline__ void token_task(const Params& p, long long task, bool keys, int lane, float* scratch) {
+  const NormAppendArgs& a = p.a;
+  const int parts = p.parts + (keys ? 1 : 0);
+  const int part = (int)(task % parts);
+  const long long token = task / parts;
+  const int b = (int)(token / a.L), i = (int)(token % a.L);
+  bool bad;
+  const int n = present(a, b, &bad);
+  if (bad && lane == 0) set_status(a.status, DCP_ERR_BOUNDS);
+  if (i >= n) return;
+  const long long base = (long long)a.seq_lens[b] - n;
+  Rows<SG, SLOTS, kRot> rows(a, lane, scratch);
+  rows.set_position(position_of(a, b, i, base));
+  if (part < p.parts) {
+    rows.set_weights(a.q_weight);
+    head_rows(rows, static_cast<const __nv_bfloat16*>(a.q) + b * a.q_batch + i * a.q_token,
+              static_cast<__nv_bfloat16*>(a.q_out) + token * a.Hq * a.D, part * p.part_heads,
+              min(a.Hq, (part + 1) * p.part_heads), lane, a.D);
+    return;
+  }
+  const long long t = base + i;
+  const int r = (int)((t / a.I) % a.N);
+  const long long j = (t / ((long long)a.I * a.N)) * a.I + t % a.I;
+  const int blk = block_of(a, b, r, (int)(j / a.bs), lane == 0);
+  if (blk < 0) return;
+  const long long cell = ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D;
+  rows.set_weights(a.k_weight);
+  head_rows(rows, static_cast<const __nv_bfloat16*>(a.k) + b * a.k_batch + i * a.k_token, p.pool_k + cell, 0, a.Hkv, lane,
+            a.D);
+  if (a.v != nullptr)
+    copy_vectors(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + b * a.v_batch + i * a.v_token),
+                 reinterpret_cast<uint4*>(p.pool_v + cell), a.Hkv * a.D / 8, lane, [](int c) { return c; });
+}
+
+template <int SG, int SLOTS, int kRot>
+__global__ void __launch_bounds__(kThreads) append_norm_kernel(const Params p) {
+  extern __shared__ float scratch[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long task = (long long)blockIdx.x * kWarps + warp;
+  if (task < p.q_tasks)
+    token_task<SG, SLOTS, kRot>(p, task, true, lane, scratch + warp * scratch_floats(kRot, SG, p.a.rot_dim));
+}
+
+// Codes of a vector: y / 2^e to nearest (y by = 2^-e), NaN where y is not finite.
+__device__ __forceinline__ uint2 codes_of(const float (&y)[8], float by) {
+  uint32_t out[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint16_t half[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = y[4 * k + 2 * m + e];
+        v[e] = fabsf(x) <= FLT_MAX ? x * by : NAN;
+      }
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(half[m]) : "f"(v[1]), "f"(v[0]));
+    }
+    out[k] = (uint32_t)half[0] | (uint32_t)half[1] << 16;
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+__device__ __forceinline__ void values_of(const uint2& u, float (&y)[8]) {
+  const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t pair;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+    y[2 * k] = f.x, y[2 * k + 1] = f.y;
+  }
+}
+
+// 2^e, e within the exponents of normal numbers
+__device__ __forceinline__ float power(int e) { return __int_as_float((127 + e) << 23); }
+
+// Exponent of the scale that a largest magnitude wants: the smallest e with most <= 112 2^e.
+__device__ __forceinline__ int exponent_for(float most) {
+  const uint32_t bits = __float_as_uint(most);
+  const int e = (int)(bits >> 23) - 127 - 6 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);   // 112 = 1.75 2^6
+  return min(max(e, -DCP_KV8_MAX_EXP), DCP_KV8_MAX_EXP);
+}
+
+// The new rows of one block, KV head and K or V, by a team of kTeam warps.
+template <int SG, int SLOTS, int kRot, int kTeam>
+__device__ __forceinline__ void block_rows(const Params& p, long long task, int team_warp, int lane, float* scratch,
+                                           float* shared) {
+  constexpr int kGroups = kTeam * 32 / SG;                    // rows at a time
+  constexpr int kHeld = kTeam == 1 ? 1 : SLOTS > 1 ? 2 : 4;   // rows of a group in registers
+  const NormAppendArgs& a = p.a;
+  const int kinds = a.v != nullptr ? 2 : 1;
+  const bool values = kinds == 2 && (task & 1);
+  long long rest = kinds == 2 ? task >> 1 : task;
+  const int h = (int)(rest % a.Hkv);
+  rest /= a.Hkv;
+  const int g = (int)(rest % p.groups), b = (int)(rest / p.groups);
+  bool bad;
+  const int n = present(a, b, &bad);
+  if (bad && lane == 0 && team_warp == 0) set_status(a.status, DCP_ERR_BOUNDS);
+  if (n == 0 || (p.nblk == 0 && g >= n)) return;
+  const int S = a.seq_lens[b], base = S - n;
+  // local tokens [lo, hi) of shard r, in block jb of its table
+  int r, jb, lo, hi;
+  if (p.nblk == 0) {
+    // token g leads a block's new rows: it is the first of them
+    const int t = base + g;
+    r = (int)(((unsigned)t / (unsigned)a.I) % (unsigned)a.N);
+    lo = local_len(t, r, a.I, a.N);
+    if (lo != local_len(base, r, a.I, a.N) && lo % a.bs) return;
+    jb = lo / a.bs;
+  } else {
+    r = g / p.nblk;
+    const int from = local_len(base, r, a.I, a.N);
+    jb = from / a.bs + g % p.nblk;
+    lo = max(from, (int)min((long long)jb * a.bs, (long long)INT_MAX));
+  }
+  hi = (int)min((long long)local_len(S, r, a.I, a.N), ((long long)jb + 1) * a.bs);
+  if (lo >= hi) return;
+  const int count = hi - lo, before = lo % a.bs;              // new rows, slots of earlier ones
+  const int group = (team_warp * 32 + lane) / SG;
+  const __nv_bfloat16* src = values ? static_cast<const __nv_bfloat16*>(a.v) + b * a.v_batch + (long long)h * a.D
+                                    : static_cast<const __nv_bfloat16*>(a.k) + b * a.k_batch + (long long)h * a.D;
+  const long long token = values ? a.v_token : a.k_token;
+  Rows<SG, SLOTS, kRot> rows(a, lane, scratch);
+  auto index_of = [&](int k) { return (int)(global_pos(lo + min(k, count - 1), r, a.I, a.N) - base); };
+  auto load = [&](int k, uint4 (&raw)[SLOTS]) { rows.load(k < count ? src + index_of(k) * token : nullptr, raw); };
+  auto make = [&](int k, const uint4 (&raw)[SLOTS], float (&y)[SLOTS][8]) {
+#pragma unroll
+    for (int m = 0; m < SLOTS; ++m) unpack(raw[m], y[m]);
+    if (!values) {
+      rows.set_position(position_of(a, b, index_of(k), base));
+      rows.turn(y);
+    }
+  };
+  float y[kHeld][SLOTS][8], most = 0.f;
+  {
+    uint4 raw[kHeld][SLOTS];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) load(k * kGroups + group, raw[k]);
+    if (!values) rows.set_weights(a.k_weight);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      if (k > 0 && k * kGroups >= count) break;
+      make(k * kGroups + group, raw[k], y[k]);
+    }
+  }
+  const int blk = block_of(a, b, r, jb, lane == 0 && team_warp == 0);
+  const long long scale_at = ((values ? (long long)a.num_blocks : 0) + max(blk, 0)) * a.Hkv + h;
+  const int old = (int)a.scales[scale_at] - 127;
+  auto largest = [&](const float (&v)[SLOTS][8]) {
+#pragma unroll
+    for (int m = 0; m < SLOTS; ++m)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = fabsf(v[m][e]);
+        if (x <= FLT_MAX) most = fmaxf(most, x);
+      }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (k * kGroups < count) largest(y[k]);
+  for (int k = kHeld * kGroups; k < count; k += kGroups) {    // rows that the registers do not hold
+    uint4 raw[SLOTS];
+    float v[SLOTS][8];
+    load(k + group, raw);
+    make(k + group, raw, v);
+    largest(v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if constexpr (kTeam > 1) {
+    if (lane == 0) shared[team_warp] = most;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kTeam; ++k) most = fmaxf(most, shared[k]);
+  }
+  if (blk < 0) return;
+  uint8_t* pool = (values ? p.codes_v : p.codes_k) + ((long long)blk * a.bs * a.Hkv + h) * a.D;
+  const long long pitch = (long long)a.Hkv * a.D;
+  int e = old;
+  if (before == 0 || !(most <= 448.f * power(min(max(old, -126), 110)))) {
+    e = exponent_for(most);
+    if (lane == 0 && team_warp == 0) a.scales[scale_at] = (uint8_t)(127 + e);
+    // the earlier rows' codes, to the new scale
+    const float ratio = power(max(min(max(old, -126), 110) - e, -126));
+    const int vecs = a.D / 8, total = before * vecs;
+    for (int c0 = team_warp * 32 + lane; c0 < total; c0 += kTeam * 32 * 4) {
+      uint2 u[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int c = c0 + m * kTeam * 32;
+        if (c < total) u[m] = *reinterpret_cast<const uint2*>(pool + (c / vecs) * pitch + (c % vecs) * 8);
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int c = c0 + m * kTeam * 32;
+        float v[8];
+        values_of(u[m], v);
+        if (c < total) *reinterpret_cast<uint2*>(pool + (c / vecs) * pitch + (c % vecs) * 8) = codes_of(v, ratio);
+      }
+    }
+  }
+  const float by = power(-min(max(e, -126), 126));
+  auto store = [&](int k, const float (&v)[SLOTS][8]) {
+    if (k >= count) return;
+#pragma unroll
+    for (int m = 0; m < SLOTS; ++m)
+      if (rows.sl + SG * m < rows.vecs)
+        *reinterpret_cast<uint2*>(pool + (before + k) * pitch + (rows.sl + SG * m) * 8) = codes_of(v[m], by);
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) store(k * kGroups + group, y[k]);
+  for (int k = kHeld * kGroups; k < count; k += kGroups) {
+    uint4 raw[SLOTS];
+    float v[SLOTS][8];
+    load(k + group, raw);
+    make(k + group, raw, v);
+    store(k + group, v);
+  }
+}
+
+template <int SG, int SLOTS, int kRot, int kTeam>
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Params p) {
+  extern __shared__ float scratch[];
+  __shared__ float shared[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* mine = scratch + warp * scratch_floats(kRot, SG, p.a.rot_dim);
+  if (blockIdx.x < p.kv_blocks) {
+    const long long task = kTeam == 1 ? (long long)blockIdx.x * kWarps + warp : (long long)blockIdx.x;
+    if (task < p.kv_tasks) block_rows<SG, SLOTS, kRot, kTeam>(p, task, kTeam == 1 ? 0 : warp, lane, mine, shared);
+  } else {
+    const long long task = (long long)(blockIdx.x - p.kv_blocks) * kWarps + warp;
+    if (task < p.q_tasks) token_task<SG, SLOTS, kRot>(p, task, false, lane, mine);
+  }
+}
+
+template <int SG, int SLOTS, int kRot>
+cudaError_t launch(const Params& p, int team, unsigned grid, cudaStream_t stream) {
+  const size_t smem = (size_t)kWarps * scratch_floats(kRot, SG, p.a.rot_dim) * sizeof(float);
+  void (*kernel)(Params) = p.a.scales == nullptr ? append_norm_kernel<SG, SLOTS, kRot>
+                           : team == 1           ? kv8_append_kernel<SG, SLOTS, kRot, 1>
+                                                 : kv8_append_kernel<SG, SLOTS, kRot, kWarps>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
+  Params p{};
+  p.a = a;
+  const long long pool = (long long)a.num_blocks * a.bs * a.Hkv * a.D;
+  const long long tokens = (long long)a.B * a.L;
+  const int sms = device_sm_count();
+  const int sg = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
+  int team = 1;
+  if (a.scales == nullptr) {
+    p.pool_k = static_cast<__nv_bfloat16*>(a.cache);
+    p.pool_v = a.v ? p.pool_k + pool : nullptr;
+  } else {
+    p.codes_k = static_cast<uint8_t*>(a.cache);
+    p.codes_v = a.v ? p.codes_k + pool : nullptr;
+    // rows that L tokens in a row can bring a shard, and the blocks they can fall in; for few
+    // tokens each of them looks whether it is the first of its block instead
+    const long long period = (long long)a.I * a.N;
+    const long long most = std::min<long long>(a.L, a.L / period * a.I + std::min<long long>(a.I, a.L % period));
+    const long long nblk = (most + a.bs - 2) / a.bs + 1;
+    const bool by_token = a.L <= nblk * a.N;
+    p.nblk = by_token ? 0 : (int)nblk;
+    p.groups = by_token ? a.L : (int)(nblk * a.N);
+    team = std::min<long long>(most, a.bs) > 4 * (32 / sg) ? kWarps : 1;
+    p.kv_tasks = (long long)a.B * p.groups * a.Hkv * (a.v ? 2 : 1);
+    p.kv_blocks = (unsigned)(team == 1 ? (p.kv_tasks + kWarps - 1) / kWarps : p.kv_tasks);
+  }
+  // query heads of a task: up to kTaskBytes of rows, fewer when the tokens alone would not
+  // fill the SMs' warps
+  if (a.Hq > 0) {
+    const int step = 32 / sg, passes = (a.Hq + step - 1) / step;
+    const long long warps = (long long)sms * 2 * kWarps;
+    const long long wanted = std::max((warps + tokens - 1) / tokens, ((long long)a.Hq * a.D * 2 + kTaskBytes - 1) / kTaskBytes);
+    p.parts = (int)std::min<long long>(std::max<long long>(wanted, 1), passes);
+    p.part_heads = (passes + p.parts - 1) / p.parts * step;
+    p.parts = (a.Hq + p.part_heads - 1) / p.part_heads;
+  }
+  p.q_tasks = tokens * (p.parts + (a.scales == nullptr ? 1 : 0));
+  const long long grid = p.kv_blocks + (p.q_tasks + kWarps - 1) / kWarps;
+  if (grid >= (1LL << 31) || p.kv_tasks >= (1LL << 31) * kWarps) return cudaErrorInvalidValue;
+  // interleaved pairs within a lane's vector; whole vectors of halves; anything else
+  const int rot = a.rot_dim == 0 || (a.interleaved && a.rot_offset % 2 == 0) ? kPair
+                  : !a.interleaved && a.rot_offset % 8 == 0 && a.rot_dim % 16 == 0 && a.D <= 256 ? kSwap
+                                                                                                : kAny;
+  const unsigned g = (unsigned)grid;
+  if (a.D <= 64)
+    return rot == kPair   ? launch<8, 1, kPair>(p, team, g, a.stream)
+           : rot == kSwap ? launch<8, 1, kSwap>(p, team, g, a.stream)
+                          : launch<8, 1, kAny>(p, team, g, a.stream);
+  if (a.D <= 128)
+    return rot == kPair   ? launch<16, 1, kPair>(p, team, g, a.stream)
+           : rot == kSwap ? launch<16, 1, kSwap>(p, team, g, a.stream)
+                          : launch<16, 1, kAny>(p, team, g, a.stream);
+  if (a.D <= 256)
+    return rot == kPair   ? launch<32, 1, kPair>(p, team, g, a.stream)
+           : rot == kSwap ? launch<32, 1, kSwap>(p, team, g, a.stream)
+                          : launch<32, 1, kAny>(p, team, g, a.stream);
+  return rot == kPair ? launch<32, 3, kPair>(p, team, g, a.stream) : launch<32, 3, kAny>(p, team, g, a.stream);
+}
+
+}  // namespace dcp

@@ -436,6 +436,133 @@ DCP_API dcp_status_t dcp_kv_cache_commit(const dcp_attn_desc_t* d, void* kv_cach
                                          int32_t* new_seq_lens, int32_t dcp_size,
                                          int32_t interleave, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Norms of query and key heads in the append.  Models that normalise their heads do so
+ * right before the rotation; the calls below do both on the way to the cache.
+ * ------------------------------------------------------------------------- */
+
+/* Most dims of a head in the calls below. */
+#define DCP_APPEND_MAX_HEAD_DIM 768
+
+/* RMS norm of the first norm_dim dims of a head, by learned weights:
+ *   y_d = x_d w_d / sqrt(mean_{e < norm_dim} x_e^2 + eps)   for d < norm_dim;
+ * the other dims are left as they are.  (GQA: norm_dim is usually the head dim; MLA
+ * normalises the 512 latent dims of its row.) */
+typedef struct {
+  int32_t norm_dim;          /* a multiple of 8, 8 to the head dim                        */
+  float eps;                 /* 1e-20 to 1e20                                             */
+  const float* q_weight;     /* device, fp32 [norm_dim]; NULL: queries are not normalised */
+  const float* k_weight;     /* device, fp32 [norm_dim]; NULL: keys are not normalised    */
+} dcp_norm_desc_t;
+
+/* dcp_kv_cache_append with RMS norms of the key heads (MLA: of the row) and the query
+ * heads before the rotation.  Sums of squares, norms and rotation run in fp32, each value
+ * is rounded to bf16 once.  As the formula has it, a NaN in a head makes all its normalised dims NaN,
+ * an infinity makes its own dim NaN and the other normalised ones 0 (before the rotation).
+ * Arguments as there, and
+ *  rope, rope_steps  may be NULL together: no rotation
+ *  norm              NULL: no norms
+ * Alignment: the weights 4 bytes.
+ * Errors: as there; UNSUPPORTED for a head dim above DCP_APPEND_MAX_HEAD_DIM. */
+DCP_API dcp_status_t dcp_kv_cache_append_norm(const dcp_attn_desc_t* d, const dcp_rope_desc_t* rope,
+                                              const uint64_t* rope_steps, const dcp_norm_desc_t* norm,
+                                              const void* new_k, const void* new_v, const void* q,
+                                              const dcp_append_strides_t* strides, void* q_out,
+                                              const int32_t* pos_offsets, int64_t pos_offsets_stride,
+                                              const int32_t* q_lens, void* kv_cache,
+                                              const int32_t* block_tables, const int32_t* seq_lens,
+                                              int32_t dcp_size, int32_t interleave, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The cache in 8 bits: half the bytes of what bounds a decode step.
+ *
+ *  kv8_cache   e4m3 codes (4 significant bits, magnitudes 2^-9 to 448, one NaN, no
+ *              infinity), laid out as the bf16 cache: GQA [2][num_blocks][block_size][Hkv][D],
+ *              MLA [num_blocks][block_size][Dqk]
+ *  kv8_scales  one byte per block and KV head, GQA [2][num_blocks][Hkv] (keys, then
+ *              values), MLA [num_blocks]: a byte s stands for the factor 2^(s - 127) (255:
+ *              NaN), and the cache's value is code * 2^(s - 127)
+ *
+ * Powers of two keep every product with a scale exact, and codes have exponents of their
+ * own, so a block whose scale grows loses bits only where codes become subnormal.  Scales
+ * that dcp_kv8_append writes lie between 2^-40 and 2^40; the calls take others too, within
+ * what is said there.  Blocks and tables are as for the bf16 cache.  A block that gets rows
+ * belongs to one request (prefixes are shared by whole blocks).
+ * ------------------------------------------------------------------------- */
+
+/* Exponents of the scales that dcp_kv8_append writes: -DCP_KV8_MAX_EXP to DCP_KV8_MAX_EXP. */
+#define DCP_KV8_MAX_EXP 40
+
+/* dcp_kv_cache_append_norm into the 8-bit cache (queries are not quantised).
+ * The new rows of one block, KV head and K or V (after norm and rotation, fp32) have the
+ * largest finite magnitude a.  e(a) is the smallest exponent with a <= 112 * 2^e, between
+ * -40 and 40: a quarter of the codes' range stays free, so that later rows seldom need more.
+ *  - The rows start at the block's slot 0: its scale becomes 2^e(a).
+ *  - The block holds earlier rows, and a <= 448 times its scale: the scale stays.
+ *  - Otherwise: the scale becomes 2^e(a) and the earlier rows' codes are rounded to it.
+ * Then each value is rounded to its code once (to nearest, ties to even; beyond 448 times the
+ * scale to 448, a value that is not finite to NaN).  Slots behind the new rows keep their bytes.
+ * The first of a block's new rows tells whether it held rows before: the rows of positions
+ * below a request's new tokens must be there.
+ * Errors: as dcp_kv_cache_append_norm; a bad block's rows are skipped, whole. */
+DCP_API dcp_status_t dcp_kv8_append(const dcp_attn_desc_t* d, const dcp_rope_desc_t* rope,
+                                    const uint64_t* rope_steps, const dcp_norm_desc_t* norm,
+                                    const void* new_k, const void* new_v, const void* q,
+                                    const dcp_append_strides_t* strides, void* q_out,
+                                    const int32_t* pos_offsets, int64_t pos_offsets_stride,
+                                    const int32_t* q_lens, void* kv8_cache, uint8_t* kv8_scales,
+                                    const int32_t* block_tables, const int32_t* seq_lens,
+                                    int32_t dcp_size, int32_t interleave, void* stream);
+
+/* Reads rows back: position starts[b] + i of request b, for i < n and starts[b] + i <
+ * seq_lens[b], as bf16 (the product of code and scale rounded once; exact for the scales
+ * that dcp_kv8_append writes).  Rows of other i are left as they were.
+ *  d             kind, batch, num_kv_heads, head_dim_qk, block_size, num_blocks,
+ *                max_local_blocks are used
+ *  starts        int32 [B], each >= 0, or NULL (0)
+ *  out_k, out_v  bf16, GQA [B][n][Hkv][D] (either may be NULL, not both); MLA out_k
+ *                [B][n][Dqk], out_v NULL
+ * Alignment: kv8_cache, out_k, out_v 16 bytes.
+ * Errors: INVALID_ARG; on the device, a length or start below 0, a local index past the
+ * block table or a block id >= num_blocks sets DCP_ERR_BOUNDS; that row is left as it was. */
+DCP_API dcp_status_t dcp_kv8_read(const dcp_attn_desc_t* d, const void* kv8_cache,
+                                  const uint8_t* kv8_scales, const int32_t* block_tables,
+                                  const int32_t* seq_lens, const int32_t* starts, int32_t n,
+                                  void* out_k, void* out_v, int32_t dcp_size, int32_t interleave,
+                                  void* stream);
+
+/* Bytes of device scratch dcp_kv8_decode_attn needs for this shape, as
+ * dcp_decode_attn_workspace_size. */
+DCP_API size_t dcp_kv8_decode_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dcp_size);
+
+/* dcp_decode_attn over the 8-bit cache.  Query i < n_b of request b (n_b = q_lens[b], or
+ * q_len where q_lens is NULL) sits at position S_b - n_b + i and sees the positions up to
+ * its own.  partial_out fp32 [dcp][B][Lq][Hq][Dv] and lse fp32 [dcp][B][Lq][Hq] per shard, for
+ * dcp_merge.  A row that sees no key of a shard, and every row i >= n_b, gives partial_out = 0
+ * and lse = -inf there; of a request with n_b = 0 the lengths alone are read.
+ * Keys and values that a row does not see never reach it, whatever they hold.  A key or query
+ * that is not finite makes the rows that see it NaN; a value code of NaN makes that entry NaN
+ * in the rows that see it, except where a shard weighs 0 in fp32 against the row's others.
+ *  kv8_scales    any bytes; the accuracy holds for scales within 2^-40 to 2^40
+ *  q_lens        int32 [B], each in [0, q_len] and <= S_b, or NULL; other values set
+ *                DCP_ERR_BOUNDS and the request's rows are 0 and -inf
+ *  workspace     as in dcp_tree_attn
+ * Accuracy: codes and scales are taken as they are.  The tensor-core kernel splits a query value
+ * into two e4m3 terms, which is exact down to 2^-10 of the row's largest and an absolute error
+ * of at most 2^-18 of that below; products accumulate in fp32; a probability, times its value's
+ * scale, is rounded to fp16 once (2^-11 of it, or 2^-32 of the row's largest).
+ * Errors: as dcp_decode_attn; INVALID_ARG for kv8_scales NULL. */
+DCP_API dcp_status_t dcp_kv8_decode_attn(const dcp_attn_desc_t* d, const void* q, const void* kv8_cache,
+                                         const uint8_t* kv8_scales, const int32_t* block_tables,
+                                         const int32_t* seq_lens, const int32_t* q_lens,
+                                         int32_t dcp_size, int32_t interleave, float scale,
+                                         int32_t causal_q_len, float* partial_out, float* lse,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* dcp_decode_attn_kernel_kind and dcp_decode_attn_launches for dcp_kv8_decode_attn. */
+DCP_API int32_t dcp_kv8_decode_attn_kernel_kind(const dcp_attn_desc_t* d, int32_t dcp_size);
+DCP_API int32_t dcp_kv8_decode_attn_launches(const dcp_attn_desc_t* d, int32_t dcp_size);
+
 /* Reads `stream`'s status word (the first device-side error of the calls
  * enqueued on that stream since the last read; DCP_OK if none) and clears it.
  * The read and the clear are enqueued on `stream` and the call then waits for

@@ -1,0 +1,1012 @@
+// Step a3 over the 8-bit cache: per-shard partial attention for GQA on tcgen05
+// tensor cores, e4m3 keys and values with a power-of-two scale per block and KV
+// head.
+//
+// vLLM DCP blog, "DCP 執行流程", Compute step (each shard attends the full
+// query to its local KV slice and returns a partial output with its LSE).
+//
+// Mathematics, per query row and key t (log2 domain):
+//   x_t = scale log2 e * 2^ek_t q.k8_t,   y_t = x_t + ev_t
+//   l = sum 2^(x_t - R),  o = sum 2^(y_t - R) v8_t / l,  lse = (R + log2 l) ln 2
+// with ek, ev the exponents of the scales of t's block.  The value's scale goes
+// into the probability's exponent, so what the value product multiplies by is
+// P_t = 2^(y_t - R), and R follows the largest y, lazily: P stays below 2^15 and
+// the row's largest one above 2^7.  fp16 then holds P to 2^-11 of itself down to
+// 2^-21 of the row's largest.
+//
+// Products.  Few query rows, many keys: the keys sit on the MMA's 128 rows.
+//   S^T = K8 Q^T     kind::f8f6f4.  A bf16 query value has 8 significant bits and
+//                    is the sum of two e4m3 values (4 bits each) once its row is
+//                    scaled to at most 256, so q.k8 takes two products on codes
+//                    as they are: no key is converted.
+//   O^T += V^T P^T   kind::f16.  P in e4m3 would need three terms and their
+//                    conversion for every row; instead the values of a tile turn
+//                    into fp16 (exact) on the way, once for all rows, by four
+//                    warps of their own.
+// Roles (768 threads): warp 0 TMA producer (K and V tiles of 128 keys in rings of
+// their own, the tile's scale bytes beside them), 1 QK issuer, 2 PV issuer, 3
+// scheduler, 4-7 query split and value conversion, 8-23 softmax and epilogue (four
+// per TMEM lane quadrant, a thread owning one key and a quarter of the rows).
+//
+// Work.  A unit is (request, shard, KV head, row tile); its tiles and a constant
+// for its start and end are its weight.  One CTA per SM takes an equal share of
+// the summed weight, whatever the lengths: units that a border cuts leave partial
+// rows in the workspace (two at most per CTA), joined by kv8_join_kernel.  CTAs
+// go from unit to unit without a stop: the scheduler warp reads lengths and
+// tables ahead and publishes unit descriptors, O has two TMEM buffers.
+//
+// Every wait is bounded; when one runs out the CTA records DCP_ERR_TIMEOUT, goes
+// through its remaining units without work and leaves zeros and -inf for them.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "dcp_device.cuh"
+#include "dcp_internal.h"
+#include "dcp_sm100.cuh"
+#include "dcp_tma.h"
+
+namespace dcp {
+namespace {
+
+using namespace sm100;
+
+constexpr int kNt = 128;                       // keys per tile (MMA M of S^T)
+constexpr int kMaxStages = 6;
+constexpr int kMaxBoxes = 16;                  // blocks of 8 tokens
+constexpr int kMeta = 16;                      // tiles whose scale bytes are kept
+constexpr int kConvWarp = 4, kSoftWarp = 8, kWarps = 24;
+constexpr uint32_t kThreads = 32 * kWarps;
+constexpr uint32_t kSoftThreads = 512;
+constexpr int kSoftWarps = 16, kConvWarps = 4;
+constexpr int kReleases = 3 + kConvWarps + kSoftWarps;   // warps that read a unit descriptor
+constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of it after a move
+constexpr uint32_t kBarSoftmax = 1;
+constexpr int kMaxCols = 64;
+constexpr int kUnitCost = 1;                   // start and end of a unit, in tiles
+constexpr size_t kSmemLimit = 232448;
+constexpr uint32_t kV16Chunk = kNt * 128;      // 128 keys x 64 dims of fp16
+
+struct Params {
+  const __nv_bfloat16* q;
+  const uint8_t* codes_v;                      // (NaN codes of hidden tokens)
+  const uint8_t* scales;
+  const int32_t *block_tables, *seq_lens, *q_lens;
+  float *out, *lse;
+  float *ws_o, *ws_lse;                        // partial rows: slots 2c (head) and 2c + 1 (tail) of CTA c
+  long long* cut;                              // [2 grid] unit of a slot, -1
+  int* status;
+  int B, Lq, Hq, Hkv, N, I, max_lb, bs, num_blocks, m_tiles, gsize;
+  int box_shift;                               // log2 of the tokens of a TMA box
+  float scale_log2;
+  unsigned long long wait_ns;
+  int skip_tile;
+};
+
+struct Unit {
+  int b, r, g, row0, rows;                     // rows: query rows of the tile
+  int t0, tiles;                               // first tile, tiles (-1: no more units)
+  int ke, lim_min;                             // keys of the shard; those below lim_min are seen by every live row
+  int slot;                                    // partial slot, -1: final rows
+  int nan_values;                              // hidden or ragged keys hold NaN values
+  int lim[kMaxCols];                           // keys that a row sees (0: no such query)
+  float qf[kMaxCols];                          // scale of the split query row
+};
+
+template <int NCOL, int D>
+struct Cfg {
+  static constexpr uint32_t kTile = kNt * D;                      // bytes of a K or V tile
+  static constexpr uint32_t kQBytes = 2 * NCOL * D;               // split query: hi rows, lo rows
+  static constexpr int kUnits = NCOL == 16 ? 4 : NCOL == 32 ? 3 : 2;
+  static constexpr uint32_t kPitch = NCOL * 2;                    // bytes of one P^T row (key)
+  static constexpr uint32_t kPBytes = kNt * kPitch;
+  static constexpr uint32_t kPSwz = NCOL == 16 ? kSw32 : NCOL == 32 ? kSw64 : kSw128;
+  static constexpr uint32_t kKSwz = D == 128 ? kSw128 : kSw64;
+  static constexpr uint32_t kTmemCols = 4 * NCOL < 64 ? 64 : 4 * NCOL;   // two S, two O buffers
+  static constexpr uint32_t kV16 = 2 * kV16Chunk * (D / 64) + (D == 64 ? kV16Chunk : 0);   // (M = 128 reads two chunks)
+  __device__ static __forceinline__ uint32_t pchunk(uint32_t c, uint32_t k) {
+    return NCOL == 16 ? (c ^ ((k >> 2) & 1u)) : NCOL == 32 ? (c ^ ((k >> 1) & 3u)) : (c ^ (k & 7u));
+  }
+  // 16-byte chunk c of row k of a tile or query as stored under its swizzle
+  __device__ static __forceinline__ uint32_t kchunk(uint32_t c, uint32_t k) {
+    return D == 128 ? (c ^ (k & 7u)) : (c ^ ((k >> 1) & 3u));
+  }
+};
+
+template <int NCOL, int D>
+struct Smem {
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+  uint64_t w_full[2], w_empty[2];              // fp16 value tiles
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], drain[2];
+  uint64_t unit_full[4], unit_empty[4], q_full[4];
+  uint32_t tmem_base;
+  int abort;
+  int start_e;                                 // first entry of this CTA's share
+  long long start_at;                          // weight before it
+  long long sums[kWarps];
+  uint16_t meta[kMeta][kMaxBoxes];             // scale bytes of a tile's boxes: K, V << 8
+  float red[4][kMaxCols];
+  Unit unit[Cfg<NCOL, D>::kUnits];
+};
+
+template <int NCOL, int D>
+constexpr size_t fixed_bytes() {
+  using C = Cfg<NCOL, D>;
+  return 1024 + C::kV16 + 2 * C::kPBytes + C::kUnits * C::kQBytes + sizeof(Smem<NCOL, D>) + 64;
+}
+
+// Ring stages of the K and of the V tiles.
+template <int NCOL, int D>
+constexpr int stages(bool values) {
+  const int all = (int)((kSmemLimit - fixed_bytes<NCOL, D>()) / Cfg<NCOL, D>::kTile);
+  const int n = values ? all / 2 : all - all / 2;
+  return n > kMaxStages ? kMaxStages : n;
+}
+
+template <int NCOL, int D>
+constexpr size_t smem_bytes() {
+  return fixed_bytes<NCOL, D>() + (size_t)(stages<NCOL, D>(false) + stages<NCOL, D>(true)) * Cfg<NCOL, D>::kTile;
+}
+
+// Instruction descriptors with fp32 accumulation: e4m3 x e4m3, both K-major
+// (kind::f8f6f4), and fp16 x fp16, both MN-major (kind::f16).
+__host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_fp16_mn(int N) {
+  return (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem] on 8-bit operands
+__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t codes_of(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Queries of request b (0 where its lengths are out of range) and the keys of shard r that they see.
+struct Request {
+  int S, n, keys;
+  bool bad;                                    // lengths out of range, or more keys than the table holds
+};
+
+__device__ __forceinline__ Request request_of(const Params& p, int b, int r) {
+  Request q;
+  q.S = p.seq_lens[b];
+  q.n = p.q_lens ? p.q_lens[b] : p.Lq;
+  q.bad = q.n < 0 || q.n > p.Lq || q.S < q.n;
+  if (q.bad) q.n = 0;
+  q.keys = q.n > 0 ? local_len(q.S, r, p.I, p.N) : 0;
+  const long long room = (long long)p.max_lb * p.bs;
+  if (q.keys > room) q.keys = (int)room, q.bad = true;
+  return q;
+}
+
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kNt - 1) / kNt; }
+
+// Weight of a unit: its tiles (an empty one still writes its rows), its start and end.
+__device__ __forceinline__ int weight_of(const Params& p, int e) {
+  return max(1, tiles_of(request_of(p, e / p.N, e % p.N).keys)) + kUnitCost;
+}
+
+template <int NCOL, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using C = Cfg<NCOL, D>;
+  constexpr int kKStages = stages<NCOL, D>(false), kVStages = stages<NCOL, D>(true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kring = base;
+  uint8_t* vring = kring + kKStages * C::kTile;
+  uint8_t* v16 = vring + kVStages * C::kTile;
+  uint8_t* ps = v16 + C::kV16;
+  uint8_t* qs = ps + 2 * C::kPBytes;
+  Smem<NCOL, D>& sm = *reinterpret_cast<Smem<NCOL, D>*>(qs + C::kUnits * C::kQBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &sm.abort;
+  if (tid == 0) {
+    for (int k = 0; k < kMaxStages; ++k) {
+      mbar_init(smem_u32(&sm.k_full[k]), 1);
+      mbar_init(smem_u32(&sm.k_empty[k]), 1);
+      mbar_init(smem_u32(&sm.v_full[k]), 1);
+      mbar_init(smem_u32(&sm.v_empty[k]), kConvWarps);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&sm.w_full[k]), kConvWarps);
+      mbar_init(smem_u32(&sm.w_empty[k]), 1);
+      mbar_init(smem_u32(&sm.s_full[k]), 1);
+      mbar_init(smem_u32(&sm.s_free[k]), kSoftWarps);
+      mbar_init(smem_u32(&sm.p_full[k]), kSoftWarps);
+      mbar_init(smem_u32(&sm.p_free[k]), 1);
+      mbar_init(smem_u32(&sm.o_free[k]), kSoftWarps);
+      mbar_init(smem_u32(&sm.drain[k]), 1);
+    }
+    for (int k = 0; k < C::kUnits; ++k) {
+      mbar_init(smem_u32(&sm.unit_full[k]), 1);
+      mbar_init(smem_u32(&sm.unit_empty[k]), kReleases);
+      mbar_init(smem_u32(&sm.q_full[k]), kConvWarps);
+    }
+    sm.abort = 0;
+    sm.start_e = -1;
+    fence_mbar_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&sm.tmem_base), C::kTmemCols);
+
+  // this CTA's share of the summed weight: entries (request, shard) in order, a run of them per thread
+  const int entries = p.B * p.N, per = (entries + (int)kThreads - 1) / (int)kThreads;
+  const long long units_per = (long long)p.Hkv * p.m_tiles;
+  long long mine = 0;
+  for (int k = 0; k < per; ++k)
+    if (tid * (long long)per + k < entries) mine += weight_of(p, tid * per + k);
+  mine *= units_per;
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sm.sums[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) upto += total;
+    total += sm.sums[w];
+  }
+  // (no share is empty, so the parts of a cut unit are neighbours; CTAs past the summed weight have none)
+  const long long ctas = min((long long)gridDim.x, total);
+  const long long lo = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+  const long long hi = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+  if (upto - mine <= lo && lo < upto) {
+    long long at = upto - mine;
+    int e = tid * per;
+    for (;; ++e) {
+      const long long next = at + weight_of(p, e) * units_per;
+      if (lo < next) break;
+      at = next;
+    }
+    sm.start_e = e;
+    sm.start_at = at;
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  auto fail = [&](void) {
+    set_status(p.status, DCP_ERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+  // the next unit's descriptor (a whole warp); false: there are no more, or the wait ran out
+  auto unit_wait = [&](int u, int limits = 4) -> bool {
+    const int slot = u % C::kUnits;
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.unit_full[slot]), (uint32_t)(u / C::kUnits) & 1u, limits * p.wait_ns))) {
+      fail();
+      return false;
+    }
+    return sm.unit[slot].tiles >= 0;
+  };
+  auto unit_done = [&](int u) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.unit_empty[u % C::kUnits]));
+  };
+  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&bar), parity, p.wait_ns));
+  };
+
+  if (warp == 3) {
+    // ---------------- scheduler ----------------
+    if (lane == 0) p.cut[2 * blockIdx.x] = p.cut[2 * blockIdx.x + 1] = -1;
+    int e = sm.start_e, u = 0;
+    long long at = sm.start_at;
+    bool ok = true;
+    if (e >= 0) {
+      for (; ok && e < entries && at < hi; ++e) {
+        const int b = e / p.N, r = e % p.N;
+        const Request q = request_of(p, b, r);
+        const int tiles = tiles_of(q.keys), weight = max(1, tiles) + kUnitCost;
+        const int32_t* bt = p.block_tables + ((long long)r * p.B + b) * p.max_lb;
+        // a block id past the pool among the keys empties the request in this shard
+        bool bad_block = false;
+        for (int k = lane; k < (q.keys + p.bs - 1) / p.bs; k += 32) bad_block |= (unsigned)bt[k] >= (unsigned)p.num_blocks;
+        bad_block = __any_sync(0xffffffffu, bad_block);
+        if (lane == 0 && (q.bad || bad_block)) set_status(p.status, DCP_ERR_BOUNDS);
+        long long k0 = at < lo ? (lo - at) / weight : 0;      // first unit of the entry in this share
+        for (; k0 < units_per; ++k0) {
+          const long long first = at + k0 * weight;
+          if (first >= hi) break;
+          const int g = (int)(k0 / p.m_tiles), mt = (int)(k0 % p.m_tiles);
+          const int row0 = mt * NCOL, rows = min(NCOL, p.Lq * p.gsize - row0);
+          const int live = bad_block || row0 / p.gsize >= q.n ? 0 : tiles;      // tiles that count
+          const int t0 = (int)min(max(lo - first, 0LL), (long long)live), t1 = (int)min(hi - first, (long long)live);
+          if (live > 0 ? t1 <= t0 : first < lo) continue;     // (another CTA's)
+          const int slot = u % C::kUnits;
+          if (u >= C::kUnits &&
+              !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.unit_empty[slot]), (uint32_t)(u / C::kUnits - 1) & 1u, 4 * p.wait_ns))) {
+            fail();
+            ok = false;
+            break;
+          }
+          Unit& w = sm.unit[slot];
+          const int i_last = min(q.n - 1, (row0 + rows - 1) / p.gsize);
+          for (int h = lane; h < NCOL; h += 32) {
+            const int i = (row0 + h) / p.gsize;
+            w.lim[h] = h < rows && i < q.n ? min(q.keys, local_count_upto((long long)q.S - q.n + i, r, p.I, p.N)) : 0;
+          }
+          if (lane == 0) {
+            w.b = b, w.r = r, w.g = g, w.row0 = row0, w.rows = rows;
+            w.t0 = t0, w.tiles = t1 - t0;
+            w.ke = live > 0 ? min(q.keys, local_count_upto((long long)q.S - q.n + i_last, r, p.I, p.N)) : 0;
+            w.lim_min = live > 0 ? min(w.ke, local_count_upto((long long)q.S - q.n + row0 / p.gsize, r, p.I, p.N)) : 0;
+            w.slot = live == 0 || (t0 == 0 && t1 == live) ? -1 : 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1);
+            w.nan_values = 0;
+            if (w.slot >= 0) p.cut[w.slot] = (long long)e * units_per + k0;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.unit_full[slot]));
+          ++u;
+        }
+        at += weight * units_per;
+      }
+    }
+    const int slot = u % C::kUnits;
+    if (ok && u >= C::kUnits &&
+        !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.unit_empty[slot]), (uint32_t)(u / C::kUnits - 1) & 1u, 4 * p.wait_ns))) {
+      fail();
+      ok = false;
+    }
+    if (ok && lane == 0) {
+      sm.unit[slot].tiles = -1;
+      mbar_arrive(smem_u32(&sm.unit_full[slot]));
+    }
+  } else if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    const int box = 1 << p.box_shift, boxes = kNt >> p.box_shift, window = 32 >> (7 - p.box_shift);   // tiles of a window
+    int kst = 0, vst = 0, tt = 0;
+    uint32_t kph = 1, vph = 1;
+    int k_issued = 0, v_issued = 0;
+    for (int u = 0; unit_wait(u); ++u) {
+      const Unit& w = sm.unit[u % C::kUnits];
+      const int tiles = *abort_flag ? 0 : w.tiles, t0 = w.t0, ke = w.ke, g = w.g;
+      const int32_t* bt = p.block_tables + ((long long)w.r * p.B + w.b) * p.max_lb;
+      // lane's box of a window of tiles: pool row, scale bytes; the next window's are on their way
+      auto entry = [&](int t) {
+        const int j = (t0 + t) * kNt + lane * box;
+        return t < tiles && j < ke ? bt[j / p.bs] : -1;
+      };
+      auto scale_bytes = [&](int blk) {
+        if (blk < 0) return 127u | 127u << 8;
+        const uint8_t* s = p.scales + (long long)blk * p.Hkv + g;
+        return (uint32_t)s[0] | (uint32_t)s[(long long)p.num_blocks * p.Hkv] << 8;
+      };
+      int blk = entry(0), blk1 = entry(window);
+      uint32_t sc = scale_bytes(blk);
+      for (int t = 0; t < tiles; ++t) {
+        const int in = t & (window - 1);
+        if (in == 0 && t > 0) {
+          blk = blk1;
+          sc = scale_bytes(blk);
+          blk1 = entry(t + window);
+        }
+        if (!wait(sm.k_empty[kst], kph)) {
+          fail();
+          break;
+        }
+        const int k = lane - in * boxes;                      // this lane's box of the tile
+        const bool has = k >= 0 && k < boxes;
+        if (has) sm.meta[tt & (kMeta - 1)][k] = (uint16_t)sc;
+        __syncwarp();
+        if (t0 + t != p.skip_tile) {                          // (test hook: a tile that is never loaded)
+          const int j = (t0 + t) * kNt + k * box;
+          const int row = has && blk >= 0 ? blk * p.bs + j % p.bs : 0;
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sm.k_full[kst]), C::kTile);
+          __syncwarp();
+          if (has) tma_load_3d(smem_u32(kring + kst * C::kTile + k * box * D), &tm_k, 0, g, row, smem_u32(&sm.k_full[kst]));
+          ++k_issued;
+          if (++kst == kKStages) kst = 0, kph ^= 1;
+          if (!wait(sm.v_empty[vst], vph)) {
+            fail();
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sm.v_full[vst]), C::kTile);
+          __syncwarp();
+          if (has) tma_load_3d(smem_u32(vring + vst * C::kTile + k * box * D), &tm_v, 0, g, row, smem_u32(&sm.v_full[vst]));
+          ++v_issued;
+          if (++vst == kVStages) vst = 0, vph ^= 1;
+        }
+        ++tt;
+      }
+      unit_done(u);
+    }
+    if (*abort_flag) {
+      // copies in flight land before the CTA leaves
+      for (int k = max(0, k_issued - kKStages); k < k_issued; ++k)
+        mbar_wait(smem_u32(&sm.k_full[k % kKStages]), (uint32_t)(k / kKStages) & 1u, p.wait_ns);
+      for (int k = max(0, v_issued - kVStages); k < v_issued; ++k)
+        mbar_wait(smem_u32(&sm.v_full[k % kVStages]), (uint32_t)(k / kVStages) & 1u, p.wait_ns);
+    }
+  } else if (warp == 1) {
+    // ---------------- QK issuer: S^T(t) = K(t) (Q_hi + Q_lo)^T ----------------
+    constexpr uint32_t id = idesc_e4m3(NCOL);
+    const bool lead = elect_one();
+    const uint32_t tm = uniform(tmem), ring = uniform(smem_u32(kring)), qaddr = uniform(smem_u32(qs));
+    int st = 0, tt = 0;
+    uint32_t ph = 0;
+    for (int u = 0; unit_wait(u); ++u) {
+      const int slot = u % C::kUnits;
+      const int tiles = (int)uniform((uint32_t)sm.unit[slot].tiles);
+      if (tiles > 0 && *abort_flag == 0) {
+        bool good = wait(sm.q_full[slot], (uint32_t)(u / C::kUnits) & 1u);
+        for (int t = 0; good && t < tiles; ++t, ++tt) {
+          good = wait(sm.k_full[st], ph) && (tt < 2 || wait(sm.s_free[tt & 1], (uint32_t)((tt >> 1) - 1) & 1u));
+          if (!good) break;
+          if (lead) {
+            tc_fence_after();
+            const uint32_t kt = ring + st * C::kTile, qt = qaddr + slot * C::kQBytes;
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                mma_ss_f8(tm + (uint32_t)(tt & 1) * NCOL, smem_desc(kt + k * 32, 16, 8 * D, C::kKSwz),
+                          smem_desc(qt + term * NCOL * D + k * 32, 16, 8 * D, C::kKSwz), id, term + k > 0 ? 1u : 0u);
+            mma_commit(smem_u32(&sm.k_empty[st]));
+            mma_commit(smem_u32(&sm.s_full[tt & 1]));
+          }
+          __syncwarp();
+          if (++st == kKStages) st = 0, ph ^= 1;
+        }
+        if (!good) fail();
+      }
+      unit_done(u);
+    }
+    if (lead) mma_commit(smem_u32(&sm.drain[0]));
+    __syncwarp();
+    if (!mbar_wait(smem_u32(&sm.drain[0]), 0, p.wait_ns)) fail();
+  } else if (warp == 2) {
+    // ---------------- PV issuer: O^T += V16^T(t) P^T(t) ----------------
+    constexpr uint32_t id = idesc_fp16_mn(NCOL);
+    const bool lead = elect_one();
+    const uint32_t tm = uniform(tmem), vaddr = uniform(smem_u32(v16)), paddr = uniform(smem_u32(ps));
+    int tt = 0, o_units = 0;
+    for (int u = 0; unit_wait(u); ++u) {
+      const int tiles = (int)uniform((uint32_t)sm.unit[u % C::kUnits].tiles);
+      if (tiles > 0 && *abort_flag == 0) {
+        bool good = o_units < 2 || wait(sm.o_free[o_units & 1], (uint32_t)((o_units >> 1) - 1) & 1u);
+        const uint32_t dO = tm + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL;
+        for (int t = 0; good && t < tiles; ++t, ++tt) {
+          const uint32_t par = (uint32_t)(tt >> 1) & 1u;
+          good = wait(sm.w_full[tt & 1], par) && wait(sm.p_full[tt & 1], par);
+          if (!good) break;
+          if (lead) {
+            tc_fence_after();
+            const uint32_t vt = vaddr + (tt & 1) * (D / 64) * kV16Chunk, pt = paddr + (tt & 1) * C::kPBytes;
+#pragma unroll
+            for (int k = 0; k < kNt / 16; ++k)
+              mma_ss(dO, smem_desc(vt + k * 2048, kV16Chunk, 1024, kSw128),
+                     smem_desc(pt + k * 16 * C::kPitch, C::kPBytes, 8 * C::kPitch, C::kPSwz), id, t + k > 0 ? 1u : 0u);
+            mma_commit(smem_u32(&sm.w_empty[tt & 1]));
+            mma_commit(smem_u32(&sm.p_free[tt & 1]));
+          }
+          __syncwarp();
+        }
+        if (!good) fail();
+        ++o_units;
+      }
+      unit_done(u);
+    }
+    if (lead) mma_commit(smem_u32(&sm.drain[1]));
+    __syncwarp();
+    if (!mbar_wait(smem_u32(&sm.drain[1]), 0, p.wait_ns)) fail();
+  } else if (warp < kSoftWarp) {
+    // ---------------- query split, then value tiles to fp16 ----------------
+    const int ct = tid - 32 * kConvWarp;
+    int st = 0, tt = 0;
+    uint32_t ph = 0;
+    for (int u = 0; unit_wait(u); ++u) {
+      const int slot = u % C::kUnits;
+      Unit& w = sm.unit[slot];
+      const int tiles = w.tiles, t0 = w.t0, ke = w.ke, lim_min = w.lim_min;
+      if (tiles > 0 && *abort_flag == 0) {
+        // query rows: D / 8 lanes a row; the row's largest magnitude goes to [128, 256), hi = e4m3(q),
+        // lo = e4m3(q - hi); a value that is not finite makes its row NaN
+        constexpr int kLanes = D / 8, kRowsAt = 128 / kLanes;
+        const int c8 = ct % kLanes;
+        uint8_t* qd = qs + slot * C::kQBytes;
+        constexpr int kDeep = NCOL * kLanes / 128 < 4 ? NCOL * kLanes / 128 : 4;
+        for (int h0 = ct / kLanes; h0 < NCOL; h0 += kRowsAt * kDeep) {
+          uint4 raw[kDeep];
+#pragma unroll
+          for (int m = 0; m < kDeep; ++m) {
+            const int h = h0 + m * kRowsAt;
+            raw[m] = make_uint4(0, 0, 0, 0);
+            if (w.lim[h] > 0) {
+              const int i = (w.row0 + h) / p.gsize, head = w.g * p.gsize + (w.row0 + h) % p.gsize;
+              raw[m] = __ldg(reinterpret_cast<const uint4*>(p.q + (((long long)w.b * p.Lq + i) * p.Hq + head) * D) + c8);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < kDeep; ++m) {
+            const int h = h0 + m * kRowsAt;
+            const uint32_t words[4] = {raw[m].x, raw[m].y, raw[m].z, raw[m].w};
+            float x[8], most = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[2 * k] = bf16_lo(words[k]), x[2 * k + 1] = bf16_hi(words[k]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[k]));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            // 2^e <= most < 2^(e + 1): the row times 2^(7 - e), in two steps (either may leave fp32's exponents)
+            const int e = max((int)(__float_as_uint(most) >> 23) - 127, -126);
+            const int by = 7 - e, by1 = by / 2, by2 = by - by1;
+            const float f1 = __uint_as_float((uint32_t)(127 + by1) << 23), f2 = __uint_as_float((uint32_t)(127 + by2) << 23);
+            uint32_t hi[2], lo2[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t h16[2], l16[2];
+#pragma unroll
+              for (int m2 = 0; m2 < 2; ++m2) {
+                float v[2], rest[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  v[z] = x[4 * k + 2 * m2 + z] * f1 * f2;
+                  if (!(fabsf(v[z]) <= 448.f)) v[z] = NAN;
+                }
+                h16[m2] = codes_of(v[0], v[1]);
+                const uint32_t back = f16x2_of_codes(h16[m2]);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                rest[0] = v[0] - f.x, rest[1] = v[1] - f.y;
+                l16[m2] = codes_of(rest[0], rest[1]);
+              }
+              hi[k] = h16[0] | h16[1] << 16;
+              lo2[k] = l16[0] | l16[1] << 16;
+            }
+            const uint32_t off = h * D + (C::kchunk((uint32_t)(c8 >> 1), (uint32_t)h) << 4) + (c8 & 1) * 8;
+            *reinterpret_cast<uint2*>(qd + off) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(qd + NCOL * D + off) = make_uint2(lo2[0], lo2[1]);
+            if (c8 == 0) w.qf[h] = __uint_as_float((uint32_t)max(127 - by, 1) << 23);
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));     // (once per unit: its parity goes by them)
+      if (tiles > 0 && *abort_flag == 0) {
+        bool good = true;
+        for (int t = 0; t < tiles; ++t, ++tt) {
+          const int j0 = (t0 + t) * kNt;
+          const bool edge = j0 + kNt > lim_min;               // keys that some row does not see
+          good = wait(sm.v_full[st], ph) && (tt < 2 || wait(sm.w_empty[tt & 1], (uint32_t)((tt >> 1) - 1) & 1u));
+          if (!good) break;
+          const uint8_t* src = vring + st * C::kTile;
+          uint8_t* dst = v16 + (tt & 1) * (D / 64) * kV16Chunk;
+          constexpr int kChunks = D / 16, kKeysAt = 128 / kChunks;
+          const uint32_t c = ct % kChunks;
+#pragma unroll
+          for (int it = 0; it < kNt / kKeysAt; ++it) {
+            const uint32_t key = it * kKeysAt + ct / kChunks;
+            const uint4 v = *reinterpret_cast<const uint4*>(src + key * D + (C::kchunk(c, key) << 4));
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = f16x2_of_codes(words[k]);
+              o[2 * k + 1] = f16x2_of_codes(words[k] >> 16);
+            }
+            if (edge) {
+              // a key past the range is 0; of a key that some row does not see, NaN becomes 0 here and the
+              // epilogue puts it into the rows that see it
+              const int j = j0 + (int)key;
+              if (j >= ke) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = 0u;
+              } else if (j >= lim_min) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t bad = ((o[k] & 0x7fffu) > 0x7c00u ? 0xffffu : 0u) | ((o[k] & 0x7fff0000u) > 0x7c000000u ? 0xffff0000u : 0u);
+                  if (bad) w.nan_values = 1;
+                  o[k] &= ~bad;
+                }
+              }
+            }
+            // two 16-byte units of the key's row; neighbouring lanes take them in turn (no bank twice)
+            const uint32_t unit = 2 * (c & 3);
+            uint8_t* row = dst + (c >> 2) * kV16Chunk + key * 128;
+            const bool swap = c >> 2;
+            const uint4 first = swap ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+            const uint4 second = swap ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(row + (((unit + (swap ? 1 : 0)) ^ (key & 7u)) << 4)) = first;
+            *reinterpret_cast<uint4*>(row + (((unit + (swap ? 0 : 1)) ^ (key & 7u)) << 4)) = second;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.v_empty[st]));
+            mbar_arrive(smem_u32(&sm.w_full[tt & 1]));
+          }
+          if (++st == kVStages) st = 0, ph ^= 1;
+        }
+        if (!good) fail();
+      }
+      unit_done(u);
+    }
+  } else {
+    // ---------------- softmax and epilogue ----------------
+    constexpr int HC = NCOL / 4;                              // columns (query rows) of a thread
+    const int qd = warp & 3;                                  // TMEM lane quadrant
+    const int h0 = ((warp - kSoftWarp) >> 2) * HC;
+    const int lrow = qd * 32 + lane;                          // key of the tile; value dim of O^T
+    const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
+    auto ld_cols = [&](uint32_t addr, uint32_t (&v)[HC]) {
+      if constexpr (HC == 4) tmem_ld4(addr, v);
+      else if constexpr (HC == 8) tmem_ld8(addr, v);
+      else tmem_ld16(addr, v);
+    };
+    auto st_cols = [&](uint32_t addr, const uint32_t (&v)[HC]) {
+      if constexpr (HC == 4) tmem_st4(addr, v);
+      else if constexpr (HC == 8) tmem_st8(addr, v);
+      else tmem_st16(addr, v);
+    };
+    int tt = 0, o_units = 0;
+    bool dead = false;                                        // a wait ran out: the same in every softmax thread
+    // (they meet at barriers, so none may give up alone on a unit that comes late: the scheduler has
+    // given up on its own wait long before this limit)
+    for (int u = 0; unit_wait(u, 16); ++u) {
+      const int slot = u % C::kUnits;
+      const Unit& w = sm.unit[slot];
+      const int tiles = w.tiles, ke = w.ke, lim_min = w.lim_min;
+      float m[HC], l[HC], qf[HC];                             // reference (R), sum, scale of a row
+      const uint32_t tO = lane_base + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL + h0;
+      bool bad = false, broke = dead || tiles == 0;
+#pragma unroll
+      for (int h = 0; h < HC; ++h) m[h] = -INFINITY, l[h] = 0.f;
+      for (int t = 0; !broke && t < tiles; ++t, ++tt) {
+        const uint32_t buf = tt & 1, par = (uint32_t)(tt >> 1) & 1u;
+        const bool okw = wait(sm.s_full[buf], par);
+        if (!okw) bad = true;
+        if (t == 0)                                           // (written before the query's barrier, so before S)
+#pragma unroll
+          for (int h = 0; h < HC; ++h) qf[h] = w.qf[h0 + h];
+        float y[HC];
+        {
+          uint32_t v[HC];
+#pragma unroll
+          for (int h = 0; h < HC; ++h) v[h] = 0u;
+          if (okw) {
+            tc_fence_after();
+            ld_cols(lane_base + buf * NCOL + h0, v);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int h = 0; h < HC; ++h) y[h] = __uint_as_float(v[h]);
+        }
+        const uint32_t meta = sm.meta[tt & (kMeta - 1)][lrow >> p.box_shift];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_free[buf]));
+        const float kf = scale_factor(meta & 255u) * p.scale_log2;
+        const int sv = (int)(meta >> 8);
+        const float ev = sv == 255 ? NAN : (float)(sv - 127), inv = scale_factor((uint32_t)max(254 - sv, 0));
+
+        const int j = (w.t0 + t) * kNt + lrow;
+        const bool full = (w.t0 + t) * kNt + kNt <= lim_min;
+        float most = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < HC; ++h) {
+          y[h] = fmaf(y[h], kf * qf[h], ev);
+          if (!full && j >= w.lim[h0 + h]) y[h] = -INFINITY;
+          most = fmaxf(most, y[h] - m[h]);
+        }
+        // one barrier per tile: does any row's reference have to move?
+        if (bar_red_or(kBarSoftmax, kSoftThreads, most > kTop || bad)) {
+          if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) {
+            broke = dead = true;
+            break;
+          }
+#pragma unroll
+          for (int h = 0; h < HC; ++h) {
+            float v = y[h];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+            if (lane == 0) sm.red[qd][h0 + h] = v;
+          }
+          // O^T is rescaled: the previous tile's product must have landed
+          if (t > 0 && !wait(sm.p_free[(tt - 1) & 1], (uint32_t)((tt - 1) >> 1) & 1u)) bad = true;
+          if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) {
+            broke = dead = true;
+            break;
+          }
+          float alpha[HC];
+#pragma unroll
+          for (int h = 0; h < HC; ++h) {
+            const int hh = h0 + h;
+            const float top = fmaxf(fmaxf(sm.red[0][hh], sm.red[1][hh]), fmaxf(sm.red[2][hh], sm.red[3][hh]));
+            const float ref = fmaxf(m[h], top - kStart);
+            alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - ref);
+            m[h] = ref;
+            l[h] *= alpha[h];
+          }
+          if (t > 0) {
+            tc_fence_after();
+            uint32_t o[HC];
+            ld_cols(tO, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < HC; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha[k]);
+            st_cols(tO, o);
+            tmem_wait_st();
+          }
+        }
+        uint32_t pk[HC / 2];
+#pragma unroll
+        for (int h = 0; h < HC; h += 2) {
+          float p0 = ex2(y[h] - m[h]), p1 = ex2(y[h + 1] - m[h + 1]);
+          if (!full) {
+            p0 = y[h] == -INFINITY ? 0.f : p0;
+            p1 = y[h + 1] == -INFINITY ? 0.f : p1;
+          }
+          l[h] = fmaf(p0, inv, l[h]);
+          l[h + 1] = fmaf(p1, inv, l[h + 1]);
+          pk[h / 2] = pack_f16x2(p0, p1);
+        }
+        if (tt >= 2 && !wait(sm.p_free[buf], par ^ 1u)) bad = true;
+        uint8_t* prow = ps + buf * C::kPBytes + lrow * C::kPitch;
+        if constexpr (HC == 4) {
+          const uint32_t off = (C::pchunk((uint32_t)(h0 / 8), (uint32_t)lrow) << 4) + (h0 % 8) * 2;
+          *reinterpret_cast<uint2*>(prow + off) = make_uint2(pk[0], pk[1]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < HC / 8; ++c)
+            *reinterpret_cast<uint4*>(prow + (C::pchunk((uint32_t)(h0 / 8 + c), (uint32_t)lrow) << 4)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[buf]));
+      }
+
+      // the last product, row sums over the 128 key threads, outputs
+      bool have = !broke;
+      if (have && !wait(sm.p_free[(tt - 1) & 1], (uint32_t)((tt - 1) >> 1) & 1u)) bad = true;
+      if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) have = false, dead = true;
+      if (bad) fail();
+#pragma unroll
+      for (int h = 0; h < HC; ++h) {
+        float v = l[h];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (lane == 0) sm.red[qd][h0 + h] = v;
+      }
+      uint32_t o[HC];
+#pragma unroll
+      for (int h = 0; h < HC; ++h) o[h] = 0u;
+      if (have) {
+        tc_fence_after();
+        ld_cols(tO, o);
+        tmem_wait_ld();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (tiles > 0) {
+        if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[o_units & 1]));
+        ++o_units;
+      }
+      named_bar_sync(kBarSoftmax, kSoftThreads);
+      if (have && *(volatile int*)&w.nan_values && lrow < D) {
+        // NaN values among the keys that some row does not see: into the rows that see them
+        const int32_t* bt = p.block_tables + ((long long)w.r * p.B + w.b) * p.max_lb;
+        for (int j = max(lim_min, w.t0 * kNt); j < min(ke, (w.t0 + tiles) * kNt); ++j) {
+          const long long row = (long long)bt[j / p.bs] * p.bs + j % p.bs;
+          const bool nan = (p.codes_v[(row * p.Hkv + w.g) * D + lrow] & 0x7f) == 0x7f;
+#pragma unroll
+          for (int h = 0; h < HC; ++h)
+            if (nan && j < w.lim[h0 + h]) o[h] = 0x7fc00000u;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < HC; ++h) {
+        const int hh = h0 + h;
+        if (hh < w.rows) {
+          const float sum = (sm.red[0][hh] + sm.red[1][hh]) + (sm.red[2][hh] + sm.red[3][hh]);
+          const bool live = have && w.lim[hh] > 0 && !(sum == 0.f);      // (NaN sums make NaN rows)
+          long long at;
+          float *dst_o = p.out, *dst_lse = p.lse;
+          if (w.slot >= 0) {
+            at = (long long)w.slot * NCOL + hh;
+            dst_o = p.ws_o, dst_lse = p.ws_lse;
+          } else {
+            const int rr = w.row0 + hh, i = rr / p.gsize, head = w.g * p.gsize + rr % p.gsize;
+            at = (((long long)w.r * p.B + w.b) * p.Lq + i) * p.Hq + head;
+          }
+          if (lrow < D) dst_o[at * D + lrow] = live ? __uint_as_float(o[h]) * (1.f / sum) : 0.f;
+          if (lrow == 0) dst_lse[at] = live ? (m[h] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+      unit_done(u);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the partial rows of the units that borders of the CTAs' shares cut: a unit's first part
+// is a CTA's tail slot, the others are the head slots of the CTAs behind it.
+//   LSE = log sum exp lse_k,  o = sum exp(lse_k - LSE) o_k
+template <int NCOL, int D>
+__global__ void __launch_bounds__(256) kv8_join_kernel(const Params p, int grid) {
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long unit = p.cut[2 * c + 1];
+  if (unit < 0) return;
+  int n = 1;
+  while (c + n < grid && p.cut[2 * (c + n)] == unit) ++n;
+  const long long units_per = (long long)p.Hkv * p.m_tiles;
+  const int e = (int)(unit / units_per), k = (int)(unit % units_per);
+  const int b = e / p.N, r = e % p.N, g = k / p.m_tiles, row0 = k % p.m_tiles * NCOL;
+  const int rows = min(NCOL, p.Lq * p.gsize - row0);
+  constexpr int V = D / 32;
+  auto slot_of = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
+  for (int h = warp; h < rows; h += 8) {
+    float top = -INFINITY;
+    bool nan = false;
+    for (int s = lane; s < n; s += 32) {
+      const float v = p.ws_lse[(long long)slot_of(s) * NCOL + h];
+      nan |= v != v;
+      top = fmaxf(top, v);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    nan = __any_sync(0xffffffffu, nan);
+    float sum = 0.f, o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = 0.f;
+    if (top != -INFINITY)
+      for (int s = 0; s < n; ++s) {
+        const long long at = (long long)slot_of(s) * NCOL + h;
+        const float lse = p.ws_lse[at];
+        if (lse == -INFINITY) continue;                       // (what it holds does not count)
+        const float weight = exp2f((lse - top) * 1.4426950408889634f);
+        sum += weight;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = fmaf(weight, p.ws_o[at * D + v * 32 + lane], o[v]);
+      }
+    const int rr = row0 + h, i = rr / p.gsize, head = g * p.gsize + rr % p.gsize;
+    const long long at = (((long long)r * p.B + b) * p.Lq + i) * p.Hq + head;
+    const bool any = top != -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.out[at * D + v * 32 + lane] = nan ? NAN : any ? o[v] / sum : 0.f;
+    if (lane == 0) p.lse[at] = nan ? NAN : any ? top + logf(sum) : -INFINITY;
+  }
+}
+
+int ncol_of(const AttnArgs& a) {
+  const long long rows = (long long)a.Lq * (a.Hq / a.Hkv);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : kMaxCols;
+}
+
+int m_tiles_of(const AttnArgs& a) {
+  const int n = ncol_of(a);
+  return (int)(((long long)a.Lq * (a.Hq / a.Hkv) + n - 1) / n);
+}
+
+// One CTA per SM, fewer where there are not that many tiles.
+int grid_of(const AttnArgs& a, int sm_count) {
+  const long long tiles = ((long long)a.max_lb * a.bs + kNt - 1) / kNt;
+  const long long units = (long long)a.N * a.B * a.Hkv * m_tiles_of(a);
+  return (int)std::min<long long>(sm_count, units * std::min<long long>(tiles, sm_count));
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <int NCOL, int D>
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, int grid, cudaStream_t stream) {
+  constexpr size_t smem = smem_bytes<NCOL, D>();
+  static_assert(smem <= kSmemLimit && stages<NCOL, D>(true) >= 2, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(kv8_gqa_kernel<NCOL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kv8_gqa_kernel<NCOL, D><<<(unsigned)grid, kThreads, smem, stream>>>(tm_k, tm_v, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 1) return e;
+  kv8_join_kernel<NCOL, D><<<(unsigned)(grid - 1), 256, 0, stream>>>(p, grid);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool kv8_gqa_supported(const AttnArgs& a) {
+  if (a.kind != DCP_ATTN_GQA || (a.Dqk != 64 && a.Dqk != 128) || a.Dv != a.Dqk) return false;
+  if ((long long)a.Lq * (a.Hq / a.Hkv) > (1LL << 20)) return false;
+  if (a.bs % 8) return false;
+  if (a.bs >= kNt ? (a.bs % kNt) : (kNt % a.bs)) return false;
+  return (long long)a.num_blocks * a.bs < (1LL << 31) && (long long)a.N * a.B * a.Hkv * m_tiles_of(a) < (1LL << 31);
+}
+
+SplitPlan plan_kv8_gqa(const AttnArgs& a, int sm_count) {
+  const int grid = grid_of(a, sm_count);
+  SplitPlan plan{};
+  plan.n_split = grid > 1 ? 2 : 1;             // (says that a join follows)
+  plan.split_tokens = kNt;
+  const size_t rows = (size_t)2 * grid * ncol_of(a);
+  plan.ws_bytes = align256(2 * (size_t)grid * sizeof(long long)) + align256(rows * a.Dv * sizeof(float)) + rows * sizeof(float);
+  return plan;
+}
+
+cudaError_t launch_kv8_gqa(const AttnArgs& a) {
+  CUtensorMap tm_k, tm_v;
+  const uint64_t rows = (uint64_t)a.num_blocks * a.bs;
+  const uint64_t dims[3] = {(uint64_t)a.Dqk, (uint64_t)a.Hkv, rows};
+  const uint64_t strides[2] = {(uint64_t)a.Dqk, (uint64_t)a.Hkv * a.Dqk};
+  const int box_rows = a.bs < kNt ? a.bs : kNt;
+  const uint32_t box[3] = {(uint32_t)a.Dqk, 1, (uint32_t)box_rows};
+  const uint8_t* k_pool = static_cast<const uint8_t*>(a.kv);
+  const uint8_t* v_pool = k_pool + rows * a.Hkv * a.Dqk;
+  const CUtensorMapSwizzle swizzle = a.Dqk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!make_tensor_map(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_pool, 3, dims, strides, box, swizzle) ||
+      !make_tensor_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_pool, 3, dims, strides, box, swizzle))
+    return cudaErrorInvalidValue;
+  const int grid = grid_of(a, device_sm_count()), ncol = ncol_of(a);
+  Params p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.codes_v = v_pool;
+  p.scales = a.kv_scales;
+  p.block_tables = a.block_tables, p.seq_lens = a.seq_lens, p.q_lens = a.q_lens;
+  p.out = a.partial_out, p.lse = a.lse;
+  char* ws = static_cast<char*>(a.workspace);
+  p.cut = reinterpret_cast<long long*>(ws);
+  ws += align256(2 * (size_t)grid * sizeof(long long));
+  p.ws_o = reinterpret_cast<float*>(ws);
+  ws += align256((size_t)2 * grid * ncol * a.Dv * sizeof(float));
+  p.ws_lse = reinterpret_cast<float*>(ws);
+  p.status = a.status;
+  p.B = a.B, p.Lq = a.Lq, p.Hq = a.Hq, p.Hkv = a.Hkv, p.N = a.N, p.I = a.I;
+  p.max_lb = a.max_lb, p.bs = a.bs, p.num_blocks = a.num_blocks;
+  p.m_tiles = m_tiles_of(a), p.gsize = a.Hq / a.Hkv;
+  for (p.box_shift = 0; (1 << p.box_shift) < box_rows;) ++p.box_shift;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.wait_ns = test_hooks().wait_ns;
+  p.skip_tile = test_hooks().skip_tile;
+  if (a.Dqk == 64)
+    return ncol == 16   ? launch<16, 64>(tm_k, tm_v, p, grid, a.stream)
+           : ncol == 32 ? launch<32, 64>(tm_k, tm_v, p, grid, a.stream)
+                        : launch<64, 64>(tm_k, tm_v, p, grid, a.stream);
+  return ncol == 16   ? launch<16, 128>(tm_k, tm_v, p, grid, a.stream)
+         : ncol == 32 ? launch<32, 128>(tm_k, tm_v, p, grid, a.stream)
+                      : launch<64, 128>(tm_k, tm_v, p, grid, a.stream);
+}
+
+}  // namespace dcp

@@ -102,10 +102,10 @@ dcp_status_t make_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t inter
 }
 
 // The kernel that will run for these arguments, and its split plan.
-enum class Impl { kSimt, kMlaTc, kGqaTc, kTreeGqa };
+enum class Impl { kSimt, kMlaTc, kGqaTc, kTreeGqa, kKv8Gqa };
 
 Impl select_impl(const AttnArgs& a) {
-  if (a.kv_scales != nullptr) return Impl::kSimt;
+  if (a.kv_scales != nullptr) return kv8_gqa_supported(a) ? Impl::kKv8Gqa : Impl::kSimt;
   if (a.tree_words > 0 && tree_gqa_supported(a)) return Impl::kTreeGqa;
   if (mla_tc_supported(a)) return Impl::kMlaTc;
   if (a.tree_words == 0 && gqa_tc_supported(a)) return Impl::kGqaTc;
@@ -120,6 +120,8 @@ SplitPlan plan_for(const AttnArgs& a, Impl impl, int sm_count) {
       return plan_attn_gqa_tc(a, sm_count);
     case Impl::kTreeGqa:
       return plan_tree_gqa(a, sm_count);
+    case Impl::kKv8Gqa:
+      return plan_kv8_gqa(a, sm_count);
     case Impl::kSimt:
     default:
       return plan_attn_simt(a, sm_count);
@@ -135,6 +137,8 @@ dcp_status_t launch_impl(const AttnArgs& a, Impl impl, const SplitPlan& plan) {
       return from_cuda(launch_attn_gqa_tc(a, plan));
     case Impl::kTreeGqa:
       return from_cuda(launch_tree_gqa(a, plan));
+    case Impl::kKv8Gqa:
+      return from_cuda(launch_kv8_gqa(a));
     case Impl::kSimt:
     default:
       return from_cuda(launch_attn_simt(a, plan));
@@ -145,7 +149,8 @@ int32_t kind_of(Impl impl) {
   switch (impl) {
     case Impl::kMlaTc: return DCP_KERNEL_MLA_TC;
     case Impl::kGqaTc:
-    case Impl::kTreeGqa: return DCP_KERNEL_GQA_TC;
+    case Impl::kTreeGqa:
+    case Impl::kKv8Gqa: return DCP_KERNEL_GQA_TC;
     case Impl::kSimt:
     default: return DCP_KERNEL_SIMT;
   }

@@ -86,6 +86,11 @@ bool tree_gqa_supported(const AttnArgs& a);
 SplitPlan plan_tree_gqa(const AttnArgs& a, int sm_count);
 cudaError_t launch_tree_gqa(const AttnArgs& a, const SplitPlan& p);
 
+// GQA over the 8-bit cache on tcgen05 (head dim 64/128, block sizes of the decode kernel).
+bool kv8_gqa_supported(const AttnArgs& a);
+SplitPlan plan_kv8_gqa(const AttnArgs& a, int sm_count);
+cudaError_t launch_kv8_gqa(const AttnArgs& a);
+
 // Rotary append: see dcp_kv_cache_append (strides in elements).
 struct AppendArgs {
   const void *k, *v, *q;

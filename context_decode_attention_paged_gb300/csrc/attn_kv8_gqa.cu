@@ -58,17 +58,12 @@ constexpr int kNt = 128;                       // keys per tile (MMA M of S^T)
 constexpr int kMaxStages = 6;
 constexpr int kMaxBoxes = 16;                  // blocks of 8 tokens
 constexpr int kMeta = 16;                      // tiles whose scale bytes are kept
-constexpr int kConvWarp = 4, kSoftWarp = 8, kWarps = 24;
-constexpr uint32_t kThreads = 32 * kWarps;
-constexpr uint32_t kSoftThreads = 512;
-constexpr int kSoftWarps = 16, kConvWarps = 4;
-constexpr int kReleases = 3 + kConvWarps + kSoftWarps;   // warps that read a unit descriptor
+constexpr int kConvWarp = 4, kSoftWarp = 8, kConvWarps = 4;
 constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of it after a move
 constexpr uint32_t kBarSoftmax = 1;
 constexpr int kMaxCols = 64;
 constexpr int kUnitCost = 1;                   // start and end of a unit, in tiles
-constexpr size_t kSmemLimit = 232448;
-constexpr uint32_t kV16Chunk = kNt * 128;      // 128 keys x 64 dims of fp16
+constexpr uint32_t kWCols = kNt / 2;           // TMEM columns of an fp16 value tile
 
 struct Params {
   const __nv_bfloat16* q;
@@ -98,15 +93,21 @@ struct Unit {
 
 template <int NCOL, int D>
 struct Cfg {
+  // two CTAs an SM, with 8 softmax warps each; 64 rows take one of 16 (a thread holds 16 rows at most)
+  static constexpr int kCtas = NCOL == 64 ? 1 : 2, kGroups = NCOL == 64 ? 4 : 2;
+  static constexpr int kSoftWarps = 4 * kGroups, kWarps = kSoftWarp + kSoftWarps;
+  static constexpr uint32_t kThreads = 32 * kWarps, kSoftThreads = 32 * kSoftWarps;
+  static constexpr int kReleases = 3 + kConvWarps + kSoftWarps;   // warps that read a unit descriptor
+  static constexpr int kBufs = kCtas == 1 ? 2 : 1;                // P^T tiles
+  static constexpr size_t kSmemLimit = kCtas == 1 ? 232448 : 115712;
   static constexpr uint32_t kTile = kNt * D;                      // bytes of a K or V tile
   static constexpr uint32_t kQBytes = 2 * NCOL * D;               // split query: hi rows, lo rows
-  static constexpr int kUnits = NCOL == 16 ? 4 : NCOL == 32 ? 3 : 2;
+  static constexpr int kUnits = 2;
   static constexpr uint32_t kPitch = NCOL * 2;                    // bytes of one P^T row (key)
   static constexpr uint32_t kPBytes = kNt * kPitch;
   static constexpr uint32_t kPSwz = NCOL == 16 ? kSw32 : NCOL == 32 ? kSw64 : kSw128;
   static constexpr uint32_t kKSwz = D == 128 ? kSw128 : kSw64;
-  static constexpr uint32_t kTmemCols = 4 * NCOL < 64 ? 64 : 4 * NCOL;   // two S, two O buffers
-  static constexpr uint32_t kV16 = 2 * kV16Chunk * (D / 64) + (D == 64 ? kV16Chunk : 0);   // (M = 128 reads two chunks)
+  static constexpr uint32_t kTmemCols = kCtas == 1 ? 512 : 256;   // two S, two O buffers, two fp16 value tiles
   __device__ static __forceinline__ uint32_t pchunk(uint32_t c, uint32_t k) {
     return NCOL == 16 ? (c ^ ((k >> 2) & 1u)) : NCOL == 32 ? (c ^ ((k >> 1) & 3u)) : (c ^ (k & 7u));
   }
@@ -121,12 +122,12 @@ struct Smem {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t w_full[2], w_empty[2];              // fp16 value tiles
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], drain[2];
-  uint64_t unit_full[4], unit_empty[4], q_full[4];
+  uint64_t unit_full[2], unit_empty[2], q_full[2];
   uint32_t tmem_base;
   int abort;
   int start_e;                                 // first entry of this CTA's share
   long long start_at;                          // weight before it
-  long long sums[kWarps];
+  long long sums[Cfg<NCOL, D>::kWarps];
   uint16_t meta[kMeta][kMaxBoxes];             // scale bytes of a tile's boxes: K, V << 8
   float red[4][kMaxCols];
   Unit unit[Cfg<NCOL, D>::kUnits];
@@ -135,13 +136,13 @@ struct Smem {
 template <int NCOL, int D>
 constexpr size_t fixed_bytes() {
   using C = Cfg<NCOL, D>;
-  return 1024 + C::kV16 + 2 * C::kPBytes + C::kUnits * C::kQBytes + sizeof(Smem<NCOL, D>) + 64;
+  return 1024 + C::kBufs * C::kPBytes + C::kUnits * C::kQBytes + sizeof(Smem<NCOL, D>) + 64;
 }
 
 // Ring stages of the K and of the V tiles.
 template <int NCOL, int D>
 constexpr int stages(bool values) {
-  const int all = (int)((kSmemLimit - fixed_bytes<NCOL, D>()) / Cfg<NCOL, D>::kTile);
+  const int all = (int)((Cfg<NCOL, D>::kSmemLimit - fixed_bytes<NCOL, D>()) / Cfg<NCOL, D>::kTile);
   const int n = values ? all / 2 : all - all / 2;
   return n > kMaxStages ? kMaxStages : n;
 }
@@ -152,12 +153,12 @@ constexpr size_t smem_bytes() {
 }
 
 // Instruction descriptors with fp32 accumulation: e4m3 x e4m3, both K-major
-// (kind::f8f6f4), and fp16 x fp16, both MN-major (kind::f16).
+// (kind::f8f6f4), and fp16 (TMEM, K-major) x fp16 (MN-major) (kind::f16).
 __host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 __host__ __device__ constexpr uint32_t idesc_fp16_mn(int N) {
-  return (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+  return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
 // D[tmem] (+)= A[smem] * B[smem] on 8-bit operands
@@ -167,6 +168,24 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint
                "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
                :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
                : "memory");
+}
+
+// Two transposed 16 x 16 matrices of bytes; lane k gives the address of row k of the 32.  Lane t gets
+// bytes 4 (t % 4) .. + 3 of columns t / 4 (r0) and t / 4 + 8 (r1) of the first, r2 and r3 of the second.
+__device__ __forceinline__ void ldmatrix_t_b8(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// 16 lanes x 32 columns: lane t stores columns 8 k + 2 (t % 4), + 1 of TMEM lanes t / 4 (v[4 k], v[4 k + 1])
+// and t / 4 + 8 (v[4 k + 2], v[4 k + 3]).
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};"
+      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -219,17 +238,18 @@ __device__ __forceinline__ int weight_of(const Params& p, int e) {
 }
 
 template <int NCOL, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<NCOL, D>::kThreads, Cfg<NCOL, D>::kCtas)
 kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using C = Cfg<NCOL, D>;
+  constexpr int kWarps = C::kWarps, kSoftWarps = C::kSoftWarps, kBufs = C::kBufs;
+  constexpr uint32_t kThreads = C::kThreads, kSoftThreads = C::kSoftThreads;
   constexpr int kKStages = stages<NCOL, D>(false), kVStages = stages<NCOL, D>(true);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kring = base;
   uint8_t* vring = kring + kKStages * C::kTile;
-  uint8_t* v16 = vring + kVStages * C::kTile;
-  uint8_t* ps = v16 + C::kV16;
-  uint8_t* qs = ps + 2 * C::kPBytes;
+  uint8_t* ps = vring + kVStages * C::kTile;
+  uint8_t* qs = ps + kBufs * C::kPBytes;
   Smem<NCOL, D>& sm = *reinterpret_cast<Smem<NCOL, D>*>(qs + C::kUnits * C::kQBytes);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -253,7 +273,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     for (int k = 0; k < C::kUnits; ++k) {
       mbar_init(smem_u32(&sm.unit_full[k]), 1);
-      mbar_init(smem_u32(&sm.unit_empty[k]), kReleases);
+      mbar_init(smem_u32(&sm.unit_empty[k]), C::kReleases);
       mbar_init(smem_u32(&sm.q_full[k]), kConvWarps);
     }
     sm.abort = 0;
@@ -321,8 +341,11 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.unit_empty[u % C::kUnits]));
   };
+  // (a phase that is over needs no look at the abort flag)
   auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(smem_u32(&bar), parity, p.wait_ns));
+    const uint32_t at = smem_u32(&bar);
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(at, parity, p.wait_ns));
   };
 
   if (warp == 3) {
@@ -497,7 +520,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     // ---------------- PV issuer: O^T += V16^T(t) P^T(t) ----------------
     constexpr uint32_t id = idesc_fp16_mn(NCOL);
     const bool lead = elect_one();
-    const uint32_t tm = uniform(tmem), vaddr = uniform(smem_u32(v16)), paddr = uniform(smem_u32(ps));
+    const uint32_t tm = uniform(tmem), paddr = uniform(smem_u32(ps));
     int tt = 0, o_units = 0;
     for (int u = 0; unit_wait(u); ++u) {
       const int tiles = (int)uniform((uint32_t)sm.unit[u % C::kUnits].tiles);
@@ -505,18 +528,18 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         bool good = o_units < 2 || wait(sm.o_free[o_units & 1], (uint32_t)((o_units >> 1) - 1) & 1u);
         const uint32_t dO = tm + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL;
         for (int t = 0; good && t < tiles; ++t, ++tt) {
-          const uint32_t par = (uint32_t)(tt >> 1) & 1u;
-          good = wait(sm.w_full[tt & 1], par) && wait(sm.p_full[tt & 1], par);
+          const uint32_t buf = tt % kBufs;
+          good = wait(sm.w_full[tt & 1], (uint32_t)(tt >> 1) & 1u) && wait(sm.p_full[buf], (uint32_t)(tt / kBufs) & 1u);
           if (!good) break;
           if (lead) {
             tc_fence_after();
-            const uint32_t vt = vaddr + (tt & 1) * (D / 64) * kV16Chunk, pt = paddr + (tt & 1) * C::kPBytes;
+            const uint32_t vt = tm + 4 * NCOL + (uint32_t)(tt & 1) * kWCols, pt = paddr + buf * C::kPBytes;
 #pragma unroll
             for (int k = 0; k < kNt / 16; ++k)
-              mma_ss(dO, smem_desc(vt + k * 2048, kV16Chunk, 1024, kSw128),
+              mma_ts(dO, vt + k * 8,
                      smem_desc(pt + k * 16 * C::kPitch, C::kPBytes, 8 * C::kPitch, C::kPSwz), id, t + k > 0 ? 1u : 0u);
             mma_commit(smem_u32(&sm.w_empty[tt & 1]));
-            mma_commit(smem_u32(&sm.p_free[tt & 1]));
+            mma_commit(smem_u32(&sm.p_free[buf]));
           }
           __syncwarp();
         }
@@ -530,7 +553,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (!mbar_wait(smem_u32(&sm.drain[1]), 0, p.wait_ns)) fail();
   } else if (warp < kSoftWarp) {
     // ---------------- query split, then value tiles to fp16 ----------------
-    const int ct = tid - 32 * kConvWarp;
+    const int ct = tid - 32 * kConvWarp, dim0 = 32 * (warp - kConvWarp);
     int st = 0, tt = 0;
     uint32_t ph = 0;
     for (int u = 0; unit_wait(u); ++u) {
@@ -608,47 +631,49 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const bool edge = j0 + kNt > lim_min;               // keys that some row does not see
           good = wait(sm.v_full[st], ph) && (tt < 2 || wait(sm.w_empty[tt & 1], (uint32_t)((tt >> 1) - 1) & 1u));
           if (!good) break;
-          const uint8_t* src = vring + st * C::kTile;
-          uint8_t* dst = v16 + (tt & 1) * (D / 64) * kV16Chunk;
-          constexpr int kChunks = D / 16, kKeysAt = 128 / kChunks;
-          const uint32_t c = ct % kChunks;
+          // this warp's 32 dims: the tile's bytes transposed on the way out of shared memory (16 keys x 16
+          // dims a matrix: a lane gets 4 keys of dim lane / 4), fp16, to TMEM lane = dim, column = key / 2
+          if (dim0 < D) {
+            tc_fence_after();
+            const uint32_t src = smem_u32(vring + st * C::kTile) + lane * D;
+            const uint32_t dst = tmem + ((uint32_t)dim0 << 16) + 4 * NCOL + (uint32_t)(tt & 1) * kWCols;
 #pragma unroll
-          for (int it = 0; it < kNt / kKeysAt; ++it) {
-            const uint32_t key = it * kKeysAt + ct / kChunks;
-            const uint4 v = *reinterpret_cast<const uint4*>(src + key * D + (C::kchunk(c, key) << 4));
-            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[8];
+            for (int half = 0; half < 2; ++half) {
+              uint32_t r[4][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              o[2 * k] = f16x2_of_codes(words[k]);
-              o[2 * k + 1] = f16x2_of_codes(words[k] >> 16);
-            }
-            if (edge) {
-              // a key past the range is 0; of a key that some row does not see, NaN becomes 0 here and the
-              // epilogue puts it into the rows that see it
-              const int j = j0 + (int)key;
-              if (j >= ke) {
+              for (int m = 0; m < 4; ++m)                     // 32 keys each
+                ldmatrix_t_b8(src + m * 32 * D + (C::kchunk((uint32_t)(dim0 / 16 + half), (uint32_t)lane) << 4), r[m]);
+              if (edge) {
+                // a key past the range is 0; of a key that some row does not see, NaN becomes 0 here and the
+                // epilogue puts it into the rows that see it
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = 0u;
-              } else if (j >= lim_min) {
+                for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const uint32_t bad = ((o[k] & 0x7fffu) > 0x7c00u ? 0xffffu : 0u) | ((o[k] & 0x7fff0000u) > 0x7c000000u ? 0xffff0000u : 0u);
-                  if (bad) w.nan_values = 1;
-                  o[k] &= ~bad;
+                  for (int q = 0; q < 4; ++q) {
+                    const int j = j0 + m * 32 + (q >> 1) * 16 + 4 * (lane & 3);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                      const uint32_t byte = 0xffu << (8 * z);
+                      const bool nan = j + z >= lim_min && (r[m][q] & byte & 0x7f7f7f7fu) == (byte & 0x7f7f7f7fu);
+                      if (nan && j + z < ke) w.nan_values = 1;
+                      if (nan || j + z >= ke) r[m][q] &= ~byte;
+                    }
+                  }
+              }
+#pragma unroll
+              for (int m = 0; m < 4; m += 2) {
+                uint32_t o[16];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  o[2 * q] = f16x2_of_codes(r[m + (q >> 2)][q & 3]);
+                  o[2 * q + 1] = f16x2_of_codes(r[m + (q >> 2)][q & 3] >> 16);
                 }
+                tmem_st_16x256b_x4(dst + ((uint32_t)(half * 16) << 16) + m * 16, o);
               }
             }
-            // two 16-byte units of the key's row; neighbouring lanes take them in turn (no bank twice)
-            const uint32_t unit = 2 * (c & 3);
-            uint8_t* row = dst + (c >> 2) * kV16Chunk + key * 128;
-            const bool swap = c >> 2;
-            const uint4 first = swap ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-            const uint4 second = swap ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4*>(row + (((unit + (swap ? 1 : 0)) ^ (key & 7u)) << 4)) = first;
-            *reinterpret_cast<uint4*>(row + (((unit + (swap ? 0 : 1)) ^ (key & 7u)) << 4)) = second;
+            tmem_wait_st();
+            tc_fence_before();
           }
-          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(smem_u32(&sm.v_empty[st]));
@@ -662,7 +687,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
   } else {
     // ---------------- softmax and epilogue ----------------
-    constexpr int HC = NCOL / 4;                              // columns (query rows) of a thread
+    constexpr int HC = NCOL / C::kGroups;                              // columns (query rows) of a thread
     const int qd = warp & 3;                                  // TMEM lane quadrant
     const int h0 = ((warp - kSoftWarp) >> 2) * HC;
     const int lrow = qd * 32 + lane;                          // key of the tile; value dim of O^T
@@ -741,7 +766,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if (lane == 0) sm.red[qd][h0 + h] = v;
           }
           // O^T is rescaled: the previous tile's product must have landed
-          if (t > 0 && !wait(sm.p_free[(tt - 1) & 1], (uint32_t)((tt - 1) >> 1) & 1u)) bad = true;
+          if (t > 0 && !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u)) bad = true;
           if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) {
             broke = dead = true;
             break;
@@ -779,8 +804,8 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           l[h + 1] = fmaf(p1, inv, l[h + 1]);
           pk[h / 2] = pack_f16x2(p0, p1);
         }
-        if (tt >= 2 && !wait(sm.p_free[buf], par ^ 1u)) bad = true;
-        uint8_t* prow = ps + buf * C::kPBytes + lrow * C::kPitch;
+        if (tt >= kBufs && !wait(sm.p_free[tt % kBufs], (uint32_t)(tt / kBufs - 1) & 1u)) bad = true;
+        uint8_t* prow = ps + (tt % kBufs) * C::kPBytes + lrow * C::kPitch;
         if constexpr (HC == 4) {
           const uint32_t off = (C::pchunk((uint32_t)(h0 / 8), (uint32_t)lrow) << 4) + (h0 % 8) * 2;
           *reinterpret_cast<uint2*>(prow + off) = make_uint2(pk[0], pk[1]);
@@ -793,12 +818,12 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[buf]));
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[tt % kBufs]));
       }
 
       // the last product, row sums over the 128 key threads, outputs
       bool have = !broke;
-      if (have && !wait(sm.p_free[(tt - 1) & 1], (uint32_t)((tt - 1) >> 1) & 1u)) bad = true;
+      if (have && !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u)) bad = true;
       if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) have = false, dead = true;
       if (bad) fail();
 #pragma unroll
@@ -924,11 +949,12 @@ int m_tiles_of(const AttnArgs& a) {
   return (int)(((long long)a.Lq * (a.Hq / a.Hkv) + n - 1) / n);
 }
 
-// One CTA per SM, fewer where there are not that many tiles.
+// One CTA per SM (64 rows) or two, fewer where there are not that many tiles.
 int grid_of(const AttnArgs& a, int sm_count) {
+  const int ctas = sm_count * (ncol_of(a) == 64 ? 1 : 2);
   const long long tiles = ((long long)a.max_lb * a.bs + kNt - 1) / kNt;
   const long long units = (long long)a.N * a.B * a.Hkv * m_tiles_of(a);
-  return (int)std::min<long long>(sm_count, units * std::min<long long>(tiles, sm_count));
+  return (int)std::min<long long>(ctas, units * std::min<long long>(tiles, ctas));
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -936,10 +962,10 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 template <int NCOL, int D>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, int grid, cudaStream_t stream) {
   constexpr size_t smem = smem_bytes<NCOL, D>();
-  static_assert(smem <= kSmemLimit && stages<NCOL, D>(true) >= 2, "shared memory");
+  static_assert(smem <= Cfg<NCOL, D>::kSmemLimit && stages<NCOL, D>(true) >= 1, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kv8_gqa_kernel<NCOL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kv8_gqa_kernel<NCOL, D><<<(unsigned)grid, kThreads, smem, stream>>>(tm_k, tm_v, p);
+  kv8_gqa_kernel<NCOL, D><<<(unsigned)grid, Cfg<NCOL, D>::kThreads, smem, stream>>>(tm_k, tm_v, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid == 1) return e;
   kv8_join_kernel<NCOL, D><<<(unsigned)(grid - 1), 256, 0, stream>>>(p, grid);
@@ -976,8 +1002,10 @@ cudaError_t launch_kv8_gqa(const AttnArgs& a) {
   const uint8_t* k_pool = static_cast<const uint8_t*>(a.kv);
   const uint8_t* v_pool = k_pool + rows * a.Hkv * a.Dqk;
   const CUtensorMapSwizzle swizzle = a.Dqk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (!make_tensor_map(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_pool, 3, dims, strides, box, swizzle) ||
-      !make_tensor_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_pool, 3, dims, strides, box, swizzle))
+  // a KV head's row is what L2 fetches at a time: the next head's is another unit's
+  const CUtensorMapL2promotion fetch = a.Dqk == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+  if (!make_tensor_map(&tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_pool, 3, dims, strides, box, swizzle, fetch) ||
+      !make_tensor_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_pool, 3, dims, strides, box, swizzle, fetch))
     return cudaErrorInvalidValue;
   const int grid = grid_of(a, device_sm_count()), ncol = ncol_of(a);
   Params p{};

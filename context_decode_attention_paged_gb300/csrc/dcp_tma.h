@@ -25,10 +25,12 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // Tensor of `rank` dims (dims[0] innermost, in elements; strides[k] in bytes
 // for dims 1..rank-1), box `box` (elements), given element type and swizzle.
+// promotion: bytes that L2 fetches together (more than a contiguous run of a box brings its neighbours in).
 // Returns false when the map cannot be encoded (alignment, extents).
 inline bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int rank,
                             const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                            CUtensorMapSwizzle swizzle) {
+                            CUtensorMapSwizzle swizzle,
+                            CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t gdim[5];
@@ -43,7 +45,7 @@ inline bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dtype, const voi
   }
   CUresult r = enc(m, dtype, (cuuint32_t)rank, const_cast<void*>(base),
                    gdim, gstride, bdim, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -57,7 +57,7 @@ using namespace sm100;
 constexpr int kNt = 128;                       // keys per tile (MMA M of S^T)
 constexpr int kMaxStages = 6;
 constexpr int kMaxBoxes = 16;                  // blocks of 8 tokens
-constexpr int kMeta = 16;                      // tiles whose scale bytes are kept
+constexpr int kMeta = 8;                       // tiles whose scale bytes are kept (K stages and 2 more at least)
 constexpr int kConvWarp = 4, kSoftWarp = 8, kConvWarps = 4;
 constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of it after a move
 constexpr uint32_t kBarSoftmax = 1;
@@ -81,25 +81,32 @@ struct Params {
   int skip_tile;
 };
 
+template <int NCOL>
 struct Unit {
   int b, r, g, row0, rows;                     // rows: query rows of the tile
   int t0, tiles;                               // first tile, tiles (-1: no more units)
   int ke, lim_min;                             // keys of the shard; those below lim_min are seen by every live row
   int slot;                                    // partial slot, -1: final rows
   int nan_values;                              // hidden or ragged keys hold NaN values
-  int lim[kMaxCols];                           // keys that a row sees (0: no such query)
-  float qf[kMaxCols];                          // scale of the split query row
+  alignas(16) int lim[NCOL];                   // keys that a row sees (0: no such query)
+  alignas(16) float qf[NCOL];                  // scale of the split query row
+  long long at[NCOL];                          // where its output goes, in rows
 };
 
 template <int NCOL, int D>
 struct Cfg {
-  // two CTAs an SM, with 8 softmax warps each; 64 rows take one of 16 (a thread holds 16 rows at most)
-  static constexpr int kCtas = NCOL == 64 ? 1 : 2, kGroups = NCOL == 64 ? 4 : 2;
+  // a softmax thread holds 16 rows of its key: 4, 8 or 16 softmax warps, three, two or one CTA an SM
+  static constexpr int kGroups = NCOL / 16, kCtas = NCOL == 16 ? 3 : NCOL == 32 ? 2 : 1;
   static constexpr int kSoftWarps = 4 * kGroups, kWarps = kSoftWarp + kSoftWarps;
   static constexpr uint32_t kThreads = 32 * kWarps, kSoftThreads = 32 * kSoftWarps;
   static constexpr int kReleases = 3 + kConvWarps + kSoftWarps;   // warps that read a unit descriptor
   static constexpr int kBufs = kCtas == 1 ? 2 : 1;                // P^T tiles
-  static constexpr size_t kSmemLimit = kCtas == 1 ? 232448 : 115712;
+  static constexpr int kWBufs = NCOL == 16 ? 1 : 2;               // fp16 value tiles
+  static constexpr size_t kSmemLimit = (kCtas == 1 ? 233472 : kCtas == 2 ? 116736 : 77824) - 1024;
+  // registers of a thread at launch, and what setmaxnreg makes of them
+  static constexpr int kLaunchRegs = NCOL == 16 ? 56 : NCOL == 32 ? 64 : 80;
+  static constexpr int kCtrlRegs = NCOL == 64 ? 48 : 40, kConvRegs = NCOL == 64 ? 48 : 40, kSoftRegs = NCOL == 64 ? 96 : 88;
+  static_assert(128 * (kCtrlRegs + kConvRegs) + (int)kSoftThreads * kSoftRegs <= (int)kThreads * kLaunchRegs, "registers");
   static constexpr uint32_t kTile = kNt * D;                      // bytes of a K or V tile
   static constexpr uint32_t kQBytes = 2 * NCOL * D;               // split query: hi rows, lo rows
   static constexpr int kUnits = 2;
@@ -107,7 +114,7 @@ struct Cfg {
   static constexpr uint32_t kPBytes = kNt * kPitch;
   static constexpr uint32_t kPSwz = NCOL == 16 ? kSw32 : NCOL == 32 ? kSw64 : kSw128;
   static constexpr uint32_t kKSwz = D == 128 ? kSw128 : kSw64;
-  static constexpr uint32_t kTmemCols = kCtas == 1 ? 512 : 256;   // two S, two O buffers, two fp16 value tiles
+  static constexpr uint32_t kTmemCols = NCOL == 16 ? 128 : NCOL == 32 ? 256 : 512;   // two S, two O, the value tiles
   __device__ static __forceinline__ uint32_t pchunk(uint32_t c, uint32_t k) {
     return NCOL == 16 ? (c ^ ((k >> 2) & 1u)) : NCOL == 32 ? (c ^ ((k >> 1) & 3u)) : (c ^ (k & 7u));
   }
@@ -122,28 +129,29 @@ struct Smem {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t w_full[2], w_empty[2];              // fp16 value tiles
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], drain[2];
-  uint64_t unit_full[2], unit_empty[2], q_full[2];
+  uint64_t unit_full[2], unit_empty[2], q_full, q_free;
   uint32_t tmem_base;
   int abort;
   int start_e;                                 // first entry of this CTA's share
   long long start_at;                          // weight before it
   long long sums[Cfg<NCOL, D>::kWarps];
   uint16_t meta[kMeta][kMaxBoxes];             // scale bytes of a tile's boxes: K, V << 8
-  float red[4][kMaxCols];
-  Unit unit[Cfg<NCOL, D>::kUnits];
+  alignas(16) float red[4][NCOL];              // maxima and sums of the rows by lane quadrant
+  alignas(16) float ref[NCOL], inv[NCOL];      // at a unit's end: references, 1 / sum (-1: no output)
+  Unit<NCOL> unit[Cfg<NCOL, D>::kUnits];
 };
 
 template <int NCOL, int D>
 constexpr size_t fixed_bytes() {
   using C = Cfg<NCOL, D>;
-  return 1024 + C::kBufs * C::kPBytes + C::kUnits * C::kQBytes + sizeof(Smem<NCOL, D>) + 64;
+  return 1024 + C::kBufs * C::kPBytes + C::kQBytes + sizeof(Smem<NCOL, D>);
 }
 
 // Ring stages of the K and of the V tiles.
 template <int NCOL, int D>
 constexpr int stages(bool values) {
   const int all = (int)((Cfg<NCOL, D>::kSmemLimit - fixed_bytes<NCOL, D>()) / Cfg<NCOL, D>::kTile);
-  const int n = values ? all / 2 : all - all / 2;
+  const int n = values ? all - all / 2 : all / 2;             // (a value tile is held longer)
   return n > kMaxStages ? kMaxStages : n;
 }
 
@@ -186,6 +194,27 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
       :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+// v[c] of the 32 lanes joined by op, for every c: lane t returns that of c = t / 2.
+template <typename Op>
+__device__ __forceinline__ float across_lanes(const float (&v)[16], int lane, Op op) {
+  float a[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const bool up = lane & 16;
+    a[k] = op(up ? v[k + 8] : v[k], __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + 8], 16));
+  }
+#pragma unroll
+  for (int half = 4; half > 0; half >>= 1) {
+    const bool up = lane & (2 * half);
+#pragma unroll
+    for (int k = 0; k < half; ++k) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? a[k] : a[k + half], 2 * half);
+      a[k] = op(up ? a[k + half] : a[k], other);
+    }
+  }
+  return op(a[0], __shfl_xor_sync(0xffffffffu, a[0], 1));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -250,7 +279,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint8_t* vring = kring + kKStages * C::kTile;
   uint8_t* ps = vring + kVStages * C::kTile;
   uint8_t* qs = ps + kBufs * C::kPBytes;
-  Smem<NCOL, D>& sm = *reinterpret_cast<Smem<NCOL, D>*>(qs + C::kUnits * C::kQBytes);
+  Smem<NCOL, D>& sm = *reinterpret_cast<Smem<NCOL, D>*>(qs + C::kQBytes);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &sm.abort;
@@ -274,8 +303,9 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int k = 0; k < C::kUnits; ++k) {
       mbar_init(smem_u32(&sm.unit_full[k]), 1);
       mbar_init(smem_u32(&sm.unit_empty[k]), C::kReleases);
-      mbar_init(smem_u32(&sm.q_full[k]), kConvWarps);
     }
+    mbar_init(smem_u32(&sm.q_full), kConvWarps);
+    mbar_init(smem_u32(&sm.q_free), 1);
     sm.abort = 0;
     sm.start_e = -1;
     fence_mbar_init();
@@ -348,6 +378,8 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(at, parity, p.wait_ns));
   };
 
+  if (warp < kConvWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kCtrlRegs));
   if (warp == 3) {
     // ---------------- scheduler ----------------
     if (lane == 0) p.cut[2 * blockIdx.x] = p.cut[2 * blockIdx.x + 1] = -1;
@@ -381,10 +413,13 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             ok = false;
             break;
           }
-          Unit& w = sm.unit[slot];
+          Unit<NCOL>& w = sm.unit[slot];
+          const int slot_at = live == 0 || (t0 == 0 && t1 == live) ? -1 : 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1);
           const int i_last = min(q.n - 1, (row0 + rows - 1) / p.gsize);
           for (int h = lane; h < NCOL; h += 32) {
             const int i = (row0 + h) / p.gsize;
+            w.at[h] = slot_at >= 0 ? (long long)slot_at * NCOL + h
+                                   : (((long long)r * p.B + b) * p.Lq + i) * p.Hq + g * p.gsize + (row0 + h) % p.gsize;
             w.lim[h] = h < rows && i < q.n ? min(q.keys, local_count_upto((long long)q.S - q.n + i, r, p.I, p.N)) : 0;
           }
           if (lane == 0) {
@@ -392,9 +427,9 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             w.t0 = t0, w.tiles = t1 - t0;
             w.ke = live > 0 ? min(q.keys, local_count_upto((long long)q.S - q.n + i_last, r, p.I, p.N)) : 0;
             w.lim_min = live > 0 ? min(w.ke, local_count_upto((long long)q.S - q.n + row0 / p.gsize, r, p.I, p.N)) : 0;
-            w.slot = live == 0 || (t0 == 0 && t1 == live) ? -1 : 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1);
+            w.slot = slot_at;
             w.nan_values = 0;
-            if (w.slot >= 0) p.cut[w.slot] = (long long)e * units_per + k0;
+            if (slot_at >= 0) p.cut[slot_at] = (long long)e * units_per + k0;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.unit_full[slot]));
@@ -420,7 +455,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     uint32_t kph = 1, vph = 1;
     int k_issued = 0, v_issued = 0;
     for (int u = 0; unit_wait(u); ++u) {
-      const Unit& w = sm.unit[u % C::kUnits];
+      const Unit<NCOL>& w = sm.unit[u % C::kUnits];
       const int tiles = *abort_flag ? 0 : w.tiles, t0 = w.t0, ke = w.ke, g = w.g;
       const int32_t* bt = p.block_tables + ((long long)w.r * p.B + w.b) * p.max_lb;
       // lane's box of a window of tiles: pool row, scale bytes; the next window's are on their way
@@ -489,14 +524,15 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int u = 0; unit_wait(u); ++u) {
       const int slot = u % C::kUnits;
       const int tiles = (int)uniform((uint32_t)sm.unit[slot].tiles);
+      // (waited for in units without tiles too: a phase left out would make the next wait pass early)
+      bool good = wait(sm.q_full, (uint32_t)u & 1u);
       if (tiles > 0 && *abort_flag == 0) {
-        bool good = wait(sm.q_full[slot], (uint32_t)(u / C::kUnits) & 1u);
         for (int t = 0; good && t < tiles; ++t, ++tt) {
           good = wait(sm.k_full[st], ph) && (tt < 2 || wait(sm.s_free[tt & 1], (uint32_t)((tt >> 1) - 1) & 1u));
           if (!good) break;
           if (lead) {
             tc_fence_after();
-            const uint32_t kt = ring + st * C::kTile, qt = qaddr + slot * C::kQBytes;
+            const uint32_t kt = ring + st * C::kTile, qt = qaddr;
 #pragma unroll
             for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -511,6 +547,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         if (!good) fail();
       }
+      if (lead) mma_commit(smem_u32(&sm.q_free));             // (once per unit: its parity goes by them)
       unit_done(u);
     }
     if (lead) mma_commit(smem_u32(&sm.drain[0]));
@@ -529,16 +566,16 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const uint32_t dO = tm + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL;
         for (int t = 0; good && t < tiles; ++t, ++tt) {
           const uint32_t buf = tt % kBufs;
-          good = wait(sm.w_full[tt & 1], (uint32_t)(tt >> 1) & 1u) && wait(sm.p_full[buf], (uint32_t)(tt / kBufs) & 1u);
+          good = wait(sm.w_full[tt % C::kWBufs], (uint32_t)(tt / C::kWBufs) & 1u) && wait(sm.p_full[buf], (uint32_t)(tt / kBufs) & 1u);
           if (!good) break;
           if (lead) {
             tc_fence_after();
-            const uint32_t vt = tm + 4 * NCOL + (uint32_t)(tt & 1) * kWCols, pt = paddr + buf * C::kPBytes;
+            const uint32_t vt = tm + 4 * NCOL + (uint32_t)(tt % C::kWBufs) * kWCols, pt = paddr + buf * C::kPBytes;
 #pragma unroll
             for (int k = 0; k < kNt / 16; ++k)
               mma_ts(dO, vt + k * 8,
                      smem_desc(pt + k * 16 * C::kPitch, C::kPBytes, 8 * C::kPitch, C::kPSwz), id, t + k > 0 ? 1u : 0u);
-            mma_commit(smem_u32(&sm.w_empty[tt & 1]));
+            mma_commit(smem_u32(&sm.w_empty[tt % C::kWBufs]));
             mma_commit(smem_u32(&sm.p_free[buf]));
           }
           __syncwarp();
@@ -551,21 +588,25 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (lead) mma_commit(smem_u32(&sm.drain[1]));
     __syncwarp();
     if (!mbar_wait(smem_u32(&sm.drain[1]), 0, p.wait_ns)) fail();
+  }
   } else if (warp < kSoftWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kConvRegs));
     // ---------------- query split, then value tiles to fp16 ----------------
     const int ct = tid - 32 * kConvWarp, dim0 = 32 * (warp - kConvWarp);
     int st = 0, tt = 0;
     uint32_t ph = 0;
     for (int u = 0; unit_wait(u); ++u) {
       const int slot = u % C::kUnits;
-      Unit& w = sm.unit[slot];
+      Unit<NCOL>& w = sm.unit[slot];
       const int tiles = w.tiles, t0 = w.t0, ke = w.ke, lim_min = w.lim_min;
+      // the last unit's scores are done with the query's buffer
+      if (u > 0 && !wait(sm.q_free, (uint32_t)(u - 1) & 1u)) fail();
       if (tiles > 0 && *abort_flag == 0) {
         // query rows: D / 8 lanes a row; the row's largest magnitude goes to [128, 256), hi = e4m3(q),
         // lo = e4m3(q - hi); a value that is not finite makes its row NaN
         constexpr int kLanes = D / 8, kRowsAt = 128 / kLanes;
         const int c8 = ct % kLanes;
-        uint8_t* qd = qs + slot * C::kQBytes;
+        uint8_t* qd = qs;
         constexpr int kDeep = NCOL * kLanes / 128 < 4 ? NCOL * kLanes / 128 : 4;
         for (int h0 = ct / kLanes; h0 < NCOL; h0 += kRowsAt * kDeep) {
           uint4 raw[kDeep];
@@ -623,20 +664,20 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));     // (once per unit: its parity goes by them)
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));     // (once per unit: its parity goes by them)
       if (tiles > 0 && *abort_flag == 0) {
         bool good = true;
         for (int t = 0; t < tiles; ++t, ++tt) {
           const int j0 = (t0 + t) * kNt;
           const bool edge = j0 + kNt > lim_min;               // keys that some row does not see
-          good = wait(sm.v_full[st], ph) && (tt < 2 || wait(sm.w_empty[tt & 1], (uint32_t)((tt >> 1) - 1) & 1u));
+          good = wait(sm.v_full[st], ph) && (tt < C::kWBufs || wait(sm.w_empty[tt % C::kWBufs], (uint32_t)(tt / C::kWBufs - 1) & 1u));
           if (!good) break;
           // this warp's 32 dims: the tile's bytes transposed on the way out of shared memory (16 keys x 16
           // dims a matrix: a lane gets 4 keys of dim lane / 4), fp16, to TMEM lane = dim, column = key / 2
           if (dim0 < D) {
             tc_fence_after();
             const uint32_t src = smem_u32(vring + st * C::kTile) + lane * D;
-            const uint32_t dst = tmem + ((uint32_t)dim0 << 16) + 4 * NCOL + (uint32_t)(tt & 1) * kWCols;
+            const uint32_t dst = tmem + ((uint32_t)dim0 << 16) + 4 * NCOL + (uint32_t)(tt % C::kWBufs) * kWCols;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               uint32_t r[4][4];
@@ -677,7 +718,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(smem_u32(&sm.v_empty[st]));
-            mbar_arrive(smem_u32(&sm.w_full[tt & 1]));
+            mbar_arrive(smem_u32(&sm.w_full[tt % C::kWBufs]));
           }
           if (++st == kVStages) st = 0, ph ^= 1;
         }
@@ -686,31 +727,22 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       unit_done(u);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::kSoftRegs));
     // ---------------- softmax and epilogue ----------------
-    constexpr int HC = NCOL / C::kGroups;                              // columns (query rows) of a thread
+    constexpr int HC = 16;                                    // columns (query rows) of a thread
     const int qd = warp & 3;                                  // TMEM lane quadrant
     const int h0 = ((warp - kSoftWarp) >> 2) * HC;
     const int lrow = qd * 32 + lane;                          // key of the tile; value dim of O^T
     const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
-    auto ld_cols = [&](uint32_t addr, uint32_t (&v)[HC]) {
-      if constexpr (HC == 4) tmem_ld4(addr, v);
-      else if constexpr (HC == 8) tmem_ld8(addr, v);
-      else tmem_ld16(addr, v);
-    };
-    auto st_cols = [&](uint32_t addr, const uint32_t (&v)[HC]) {
-      if constexpr (HC == 4) tmem_st4(addr, v);
-      else if constexpr (HC == 8) tmem_st8(addr, v);
-      else tmem_st16(addr, v);
-    };
     int tt = 0, o_units = 0;
     bool dead = false;                                        // a wait ran out: the same in every softmax thread
     // (they meet at barriers, so none may give up alone on a unit that comes late: the scheduler has
     // given up on its own wait long before this limit)
     for (int u = 0; unit_wait(u, 16); ++u) {
       const int slot = u % C::kUnits;
-      const Unit& w = sm.unit[slot];
+      const Unit<NCOL>& w = sm.unit[slot];
       const int tiles = w.tiles, ke = w.ke, lim_min = w.lim_min;
-      float m[HC], l[HC], qf[HC];                             // reference (R), sum, scale of a row
+      float m[HC], l[HC];                                     // reference (R) and sum of a row
       const uint32_t tO = lane_base + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL + h0;
       bool bad = false, broke = dead || tiles == 0;
 #pragma unroll
@@ -719,9 +751,6 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const uint32_t buf = tt & 1, par = (uint32_t)(tt >> 1) & 1u;
         const bool okw = wait(sm.s_full[buf], par);
         if (!okw) bad = true;
-        if (t == 0)                                           // (written before the query's barrier, so before S)
-#pragma unroll
-          for (int h = 0; h < HC; ++h) qf[h] = w.qf[h0 + h];
         float y[HC];
         {
           uint32_t v[HC];
@@ -729,7 +758,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           for (int h = 0; h < HC; ++h) v[h] = 0u;
           if (okw) {
             tc_fence_after();
-            ld_cols(lane_base + buf * NCOL + h0, v);
+            tmem_ld16(lane_base + buf * NCOL + h0, v);
             tmem_wait_ld();
           }
 #pragma unroll
@@ -748,7 +777,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         float most = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HC; ++h) {
-          y[h] = fmaf(y[h], kf * qf[h], ev);
+          y[h] = fmaf(y[h], kf * w.qf[h0 + h], ev);           // (written before the query's barrier, so before S)
           if (!full && j >= w.lim[h0 + h]) y[h] = -INFINITY;
           most = fmaxf(most, y[h] - m[h]);
         }
@@ -758,13 +787,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             broke = dead = true;
             break;
           }
-#pragma unroll
-          for (int h = 0; h < HC; ++h) {
-            float v = y[h];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-            if (lane == 0) sm.red[qd][h0 + h] = v;
-          }
+          sm.red[qd][h0 + (lane >> 1)] = across_lanes(y, lane, [](float a, float b) { return fmaxf(a, b); });
           // O^T is rescaled: the previous tile's product must have landed
           if (t > 0 && !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u)) bad = true;
           if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) {
@@ -784,11 +807,11 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (t > 0) {
             tc_fence_after();
             uint32_t o[HC];
-            ld_cols(tO, o);
+            tmem_ld16(tO, o);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < HC; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha[k]);
-            st_cols(tO, o);
+            tmem_st16(tO, o);
             tmem_wait_st();
           }
         }
@@ -806,15 +829,10 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         if (tt >= kBufs && !wait(sm.p_free[tt % kBufs], (uint32_t)(tt / kBufs - 1) & 1u)) bad = true;
         uint8_t* prow = ps + (tt % kBufs) * C::kPBytes + lrow * C::kPitch;
-        if constexpr (HC == 4) {
-          const uint32_t off = (C::pchunk((uint32_t)(h0 / 8), (uint32_t)lrow) << 4) + (h0 % 8) * 2;
-          *reinterpret_cast<uint2*>(prow + off) = make_uint2(pk[0], pk[1]);
-        } else {
 #pragma unroll
-          for (int c = 0; c < HC / 8; ++c)
-            *reinterpret_cast<uint4*>(prow + (C::pchunk((uint32_t)(h0 / 8 + c), (uint32_t)lrow) << 4)) =
-                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        }
+        for (int c = 0; c < HC / 8; ++c)
+          *reinterpret_cast<uint4*>(prow + (C::pchunk((uint32_t)(h0 / 8 + c), (uint32_t)lrow) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -826,19 +844,16 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       if (have && !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u)) bad = true;
       if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) have = false, dead = true;
       if (bad) fail();
+      sm.red[qd][h0 + (lane >> 1)] = across_lanes(l, lane, [](float a, float b) { return a + b; });
+      if (qd == 0 && lane == 0)
 #pragma unroll
-      for (int h = 0; h < HC; ++h) {
-        float v = l[h];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (lane == 0) sm.red[qd][h0 + h] = v;
-      }
+        for (int h = 0; h < HC; ++h) sm.ref[h0 + h] = m[h];
       uint32_t o[HC];
 #pragma unroll
       for (int h = 0; h < HC; ++h) o[h] = 0u;
       if (have) {
         tc_fence_after();
-        ld_cols(tO, o);
+        tmem_ld16(tO, o);
         tmem_wait_ld();
         tc_fence_before();
       }
@@ -846,6 +861,14 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       if (tiles > 0) {
         if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[o_units & 1]));
         ++o_units;
+      }
+      named_bar_sync(kBarSoftmax, kSoftThreads);
+      float* const dst_o = w.slot >= 0 ? p.ws_o : p.out;
+      if (const int h = tid - 32 * kSoftWarp; h < w.rows) {
+        const float sum = (sm.red[0][h] + sm.red[1][h]) + (sm.red[2][h] + sm.red[3][h]);
+        const bool live = have && w.lim[h] > 0 && !(sum == 0.f);          // (NaN sums make NaN rows)
+        sm.inv[h] = live ? 1.f / sum : -1.f;
+        (w.slot >= 0 ? p.ws_lse : p.lse)[w.at[h]] = live ? (sm.ref[h] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
       named_bar_sync(kBarSoftmax, kSoftThreads);
       if (have && *(volatile int*)&w.nan_values && lrow < D) {
@@ -860,24 +883,11 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
       }
 #pragma unroll
-      for (int h = 0; h < HC; ++h) {
-        const int hh = h0 + h;
-        if (hh < w.rows) {
-          const float sum = (sm.red[0][hh] + sm.red[1][hh]) + (sm.red[2][hh] + sm.red[3][hh]);
-          const bool live = have && w.lim[hh] > 0 && !(sum == 0.f);      // (NaN sums make NaN rows)
-          long long at;
-          float *dst_o = p.out, *dst_lse = p.lse;
-          if (w.slot >= 0) {
-            at = (long long)w.slot * NCOL + hh;
-            dst_o = p.ws_o, dst_lse = p.ws_lse;
-          } else {
-            const int rr = w.row0 + hh, i = rr / p.gsize, head = w.g * p.gsize + rr % p.gsize;
-            at = (((long long)w.r * p.B + w.b) * p.Lq + i) * p.Hq + head;
-          }
-          if (lrow < D) dst_o[at * D + lrow] = live ? __uint_as_float(o[h]) * (1.f / sum) : 0.f;
-          if (lrow == 0) dst_lse[at] = live ? (m[h] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      for (int h = 0; h < HC; ++h)
+        if (h0 + h < w.rows && lrow < D) {
+          const float inv = sm.inv[h0 + h];
+          dst_o[w.at[h0 + h] * D + lrow] = inv < 0.f ? 0.f : __uint_as_float(o[h]) * inv;
         }
-      }
       unit_done(u);
     }
   }
@@ -949,9 +959,9 @@ int m_tiles_of(const AttnArgs& a) {
   return (int)(((long long)a.Lq * (a.Hq / a.Hkv) + n - 1) / n);
 }
 
-// One CTA per SM (64 rows) or two, fewer where there are not that many tiles.
+// One to three CTAs per SM, fewer where there are not that many tiles.
 int grid_of(const AttnArgs& a, int sm_count) {
-  const int ctas = sm_count * (ncol_of(a) == 64 ? 1 : 2);
+  const int n = ncol_of(a), ctas = sm_count * (n == 16 ? 3 : n == 32 ? 2 : 1);
   const long long tiles = ((long long)a.max_lb * a.bs + kNt - 1) / kNt;
   const long long units = (long long)a.N * a.B * a.Hkv * m_tiles_of(a);
   return (int)std::min<long long>(ctas, units * std::min<long long>(tiles, ctas));
@@ -963,7 +973,12 @@ template <int NCOL, int D>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, int grid, cudaStream_t stream) {
   constexpr size_t smem = smem_bytes<NCOL, D>();
   static_assert(smem <= Cfg<NCOL, D>::kSmemLimit && stages<NCOL, D>(true) >= 1, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kv8_gqa_kernel<NCOL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the register split assumes the launch count (setmaxnreg.inc would wait for registers that do not exist)
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kv8_gqa_kernel<NCOL, D>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs != Cfg<NCOL, D>::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kv8_gqa_kernel<NCOL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kv8_gqa_kernel<NCOL, D><<<(unsigned)grid, Cfg<NCOL, D>::kThreads, smem, stream>>>(tm_k, tm_v, p);
   e = cudaGetLastError();

@@ -60,7 +60,7 @@ constexpr int kMaxBoxes = 16;                  // blocks of 8 tokens
 constexpr int kMeta = 8;                       // tiles whose scale bytes are kept (K stages and 2 more at least)
 constexpr int kConvWarp = 4, kSoftWarp = 8, kConvWarps = 4;
 constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of it after a move
-constexpr uint32_t kBarSoftmax = 1;
+constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;
 constexpr int kMaxCols = 64;
 constexpr int kUnitCost = 1;                   // start and end of a unit, in tiles
 constexpr uint32_t kWCols = kNt / 2;           // TMEM columns of an fp16 value tile
@@ -241,6 +241,14 @@ __device__ __forceinline__ uint32_t codes_of(float lo, float hi) {
   return r;
 }
 
+// Tokens of the first `upto` positions that shard r holds (local_len without its 64-bit division).
+__device__ __forceinline__ int held_below(int upto, int r, int I, int N) {
+  const long long period = (long long)I * N;
+  const unsigned full = period > upto ? 0u : (unsigned)upto / (unsigned)period;
+  const long long rest = upto - full * period - (long long)r * I;
+  return (int)(full * (unsigned)I) + (int)min(max(rest, 0LL), (long long)I);
+}
+
 // Queries of request b (0 where its lengths are out of range) and the keys of shard r that they see.
 struct Request {
   int S, n, keys;
@@ -253,7 +261,7 @@ __device__ __forceinline__ Request request_of(const Params& p, int b, int r) {
   q.n = p.q_lens ? p.q_lens[b] : p.Lq;
   q.bad = q.n < 0 || q.n > p.Lq || q.S < q.n;
   if (q.bad) q.n = 0;
-  q.keys = q.n > 0 ? local_len(q.S, r, p.I, p.N) : 0;
+  q.keys = q.n > 0 ? held_below(q.S, r, p.I, p.N) : 0;
   const long long room = (long long)p.max_lb * p.bs;
   if (q.keys > room) q.keys = (int)room, q.bad = true;
   return q;
@@ -358,10 +366,25 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     set_status(p.status, DCP_ERR_TIMEOUT);
     *abort_flag = 1;
   };
+  // A whole warp waits for the phase of `parity`; false: it did not come within the limit (or, with
+  // `heeds`, the CTA has given up).  Compact on purpose: every role's code shares the instruction cache.
+  auto wait_at = [&](uint32_t bar, uint32_t parity, bool heeds, unsigned long long limit_ns) -> bool {
+    unsigned long long start = 0;
+    for (uint32_t polls = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++polls) {
+      if (heeds && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
+      if ((polls & 63u) == 0) {
+        const unsigned long long now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+        if (polls == 0) start = now;
+        else if (now - start > limit_ns) return false;
+      }
+    }
+    return true;
+  };
+  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_at(smem_u32(&bar), parity, true, p.wait_ns); };
   // the next unit's descriptor (a whole warp); false: there are no more, or the wait ran out
   auto unit_wait = [&](int u, int limits = 4) -> bool {
     const int slot = u % C::kUnits;
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.unit_full[slot]), (uint32_t)(u / C::kUnits) & 1u, limits * p.wait_ns))) {
+    if (!wait_at(smem_u32(&sm.unit_full[slot]), (uint32_t)(u / C::kUnits) & 1u, false, limits * p.wait_ns)) {
       fail();
       return false;
     }
@@ -371,18 +394,19 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.unit_empty[u % C::kUnits]));
   };
-  // (a phase that is over needs no look at the abort flag)
-  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
-    const uint32_t at = smem_u32(&bar);
-    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
-    return __all_sync(0xffffffffu, *abort_flag == 0 && mbar_wait(at, parity, p.wait_ns));
-  };
 
   if (warp < kConvWarp) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kCtrlRegs));
   if (warp == 3) {
     // ---------------- scheduler ----------------
     if (lane == 0) p.cut[2 * blockIdx.x] = p.cut[2 * blockIdx.x + 1] = -1;
+    auto slot_free = [&](int u) -> bool {
+      if (u < C::kUnits ||
+          wait_at(smem_u32(&sm.unit_empty[u % C::kUnits]), (uint32_t)(u / C::kUnits - 1) & 1u, false, 4 * p.wait_ns))
+        return true;
+      fail();
+      return false;
+    };
     int e = sm.start_e, u = 0;
     long long at = sm.start_at;
     bool ok = true;
@@ -407,12 +431,8 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const int t0 = (int)min(max(lo - first, 0LL), (long long)live), t1 = (int)min(hi - first, (long long)live);
           if (live > 0 ? t1 <= t0 : first < lo) continue;     // (another CTA's)
           const int slot = u % C::kUnits;
-          if (u >= C::kUnits &&
-              !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.unit_empty[slot]), (uint32_t)(u / C::kUnits - 1) & 1u, 4 * p.wait_ns))) {
-            fail();
-            ok = false;
-            break;
-          }
+          ok = slot_free(u);
+          if (!ok) break;
           Unit<NCOL>& w = sm.unit[slot];
           const int slot_at = live == 0 || (t0 == 0 && t1 == live) ? -1 : 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1);
           const int i_last = min(q.n - 1, (row0 + rows - 1) / p.gsize);
@@ -420,13 +440,13 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int i = (row0 + h) / p.gsize;
             w.at[h] = slot_at >= 0 ? (long long)slot_at * NCOL + h
                                    : (((long long)r * p.B + b) * p.Lq + i) * p.Hq + g * p.gsize + (row0 + h) % p.gsize;
-            w.lim[h] = h < rows && i < q.n ? min(q.keys, local_count_upto((long long)q.S - q.n + i, r, p.I, p.N)) : 0;
+            w.lim[h] = h < rows && i < q.n ? min(q.keys, held_below(q.S - q.n + i + 1, r, p.I, p.N)) : 0;
           }
           if (lane == 0) {
             w.b = b, w.r = r, w.g = g, w.row0 = row0, w.rows = rows;
             w.t0 = t0, w.tiles = t1 - t0;
-            w.ke = live > 0 ? min(q.keys, local_count_upto((long long)q.S - q.n + i_last, r, p.I, p.N)) : 0;
-            w.lim_min = live > 0 ? min(w.ke, local_count_upto((long long)q.S - q.n + row0 / p.gsize, r, p.I, p.N)) : 0;
+            w.ke = live > 0 ? min(q.keys, held_below(q.S - q.n + i_last + 1, r, p.I, p.N)) : 0;
+            w.lim_min = live > 0 ? min(w.ke, held_below(q.S - q.n + row0 / p.gsize + 1, r, p.I, p.N)) : 0;
             w.slot = slot_at;
             w.nan_values = 0;
             if (slot_at >= 0) p.cut[slot_at] = (long long)e * units_per + k0;
@@ -439,12 +459,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
     }
     const int slot = u % C::kUnits;
-    if (ok && u >= C::kUnits &&
-        !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.unit_empty[slot]), (uint32_t)(u / C::kUnits - 1) & 1u, 4 * p.wait_ns))) {
-      fail();
-      ok = false;
-    }
-    if (ok && lane == 0) {
+    if (ok && slot_free(u) && lane == 0) {
       sm.unit[slot].tiles = -1;
       mbar_arrive(smem_u32(&sm.unit_full[slot]));
     }
@@ -458,7 +473,8 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const Unit<NCOL>& w = sm.unit[u % C::kUnits];
       const int tiles = *abort_flag ? 0 : w.tiles, t0 = w.t0, ke = w.ke, g = w.g;
       const int32_t* bt = p.block_tables + ((long long)w.r * p.B + w.b) * p.max_lb;
-      // lane's box of a window of tiles: pool row, scale bytes; the next window's are on their way
+      // A lane's box of a window of tiles: pool block and scale bytes.  The next window's bytes and the table
+      // entries of the one behind it are on their way meanwhile.
       auto entry = [&](int t) {
         const int j = (t0 + t) * kNt + lane * box;
         return t < tiles && j < ke ? bt[j / p.bs] : -1;
@@ -468,14 +484,14 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const uint8_t* s = p.scales + (long long)blk * p.Hkv + g;
         return (uint32_t)s[0] | (uint32_t)s[(long long)p.num_blocks * p.Hkv] << 8;
       };
-      int blk = entry(0), blk1 = entry(window);
-      uint32_t sc = scale_bytes(blk);
+      int blk = entry(0), blk1 = entry(window), blk2 = entry(2 * window);
+      uint32_t sc = scale_bytes(blk), sc1 = scale_bytes(blk1);
       for (int t = 0; t < tiles; ++t) {
         const int in = t & (window - 1);
         if (in == 0 && t > 0) {
-          blk = blk1;
-          sc = scale_bytes(blk);
-          blk1 = entry(t + window);
+          blk = blk1, sc = sc1;
+          blk1 = blk2, sc1 = scale_bytes(blk1);
+          blk2 = entry(t + 2 * window);
         }
         if (!wait(sm.k_empty[kst], kph)) {
           fail();
@@ -483,14 +499,14 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         }
         const int k = lane - in * boxes;                      // this lane's box of the tile
         const bool has = k >= 0 && k < boxes;
+        const int row = has && blk >= 0 ? blk * p.bs + ((t0 + t) * kNt + k * box) % p.bs : 0;
+        const bool loads = t0 + t != p.skip_tile;             // (test hook: a tile that is never loaded)
+        if (has && loads) tma_load_3d(smem_u32(kring + kst * C::kTile + k * box * D), &tm_k, 0, g, row, smem_u32(&sm.k_full[kst]));
+        // the scale bytes arrive behind the copies' start; the barrier's one arrival follows both
         if (has) sm.meta[tt & (kMeta - 1)][k] = (uint16_t)sc;
         __syncwarp();
-        if (t0 + t != p.skip_tile) {                          // (test hook: a tile that is never loaded)
-          const int j = (t0 + t) * kNt + k * box;
-          const int row = has && blk >= 0 ? blk * p.bs + j % p.bs : 0;
+        if (loads) {
           if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sm.k_full[kst]), C::kTile);
-          __syncwarp();
-          if (has) tma_load_3d(smem_u32(kring + kst * C::kTile + k * box * D), &tm_k, 0, g, row, smem_u32(&sm.k_full[kst]));
           ++k_issued;
           if (++kst == kKStages) kst = 0, kph ^= 1;
           if (!wait(sm.v_empty[vst], vph)) {
@@ -510,9 +526,9 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (*abort_flag) {
       // copies in flight land before the CTA leaves
       for (int k = max(0, k_issued - kKStages); k < k_issued; ++k)
-        mbar_wait(smem_u32(&sm.k_full[k % kKStages]), (uint32_t)(k / kKStages) & 1u, p.wait_ns);
+        wait_at(smem_u32(&sm.k_full[k % kKStages]), (uint32_t)(k / kKStages) & 1u, false, p.wait_ns);
       for (int k = max(0, v_issued - kVStages); k < v_issued; ++k)
-        mbar_wait(smem_u32(&sm.v_full[k % kVStages]), (uint32_t)(k / kVStages) & 1u, p.wait_ns);
+        wait_at(smem_u32(&sm.v_full[k % kVStages]), (uint32_t)(k / kVStages) & 1u, false, p.wait_ns);
     }
   } else if (warp == 1) {
     // ---------------- QK issuer: S^T(t) = K(t) (Q_hi + Q_lo)^T ----------------
@@ -552,7 +568,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     if (lead) mma_commit(smem_u32(&sm.drain[0]));
     __syncwarp();
-    if (!mbar_wait(smem_u32(&sm.drain[0]), 0, p.wait_ns)) fail();
+    if (!wait_at(smem_u32(&sm.drain[0]), 0, false, p.wait_ns)) fail();
   } else if (warp == 2) {
     // ---------------- PV issuer: O^T += V16^T(t) P^T(t) ----------------
     constexpr uint32_t id = idesc_fp16_mn(NCOL);
@@ -587,7 +603,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     if (lead) mma_commit(smem_u32(&sm.drain[1]));
     __syncwarp();
-    if (!mbar_wait(smem_u32(&sm.drain[1]), 0, p.wait_ns)) fail();
+    if (!wait_at(smem_u32(&sm.drain[1]), 0, false, p.wait_ns)) fail();
   }
   } else if (warp < kSoftWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kConvRegs));
@@ -607,22 +623,14 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         constexpr int kLanes = D / 8, kRowsAt = 128 / kLanes;
         const int c8 = ct % kLanes;
         uint8_t* qd = qs;
-        constexpr int kDeep = NCOL * kLanes / 128 < 4 ? NCOL * kLanes / 128 : 4;
-        for (int h0 = ct / kLanes; h0 < NCOL; h0 += kRowsAt * kDeep) {
-          uint4 raw[kDeep];
-#pragma unroll
-          for (int m = 0; m < kDeep; ++m) {
-            const int h = h0 + m * kRowsAt;
-            raw[m] = make_uint4(0, 0, 0, 0);
-            if (w.lim[h] > 0) {
-              const int i = (w.row0 + h) / p.gsize, head = w.g * p.gsize + (w.row0 + h) % p.gsize;
-              raw[m] = __ldg(reinterpret_cast<const uint4*>(p.q + (((long long)w.b * p.Lq + i) * p.Hq + head) * D) + c8);
-            }
+#pragma unroll 1
+        for (int h = ct / kLanes; h < NCOL; h += kRowsAt) {
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          if (w.lim[h] > 0) {
+            const int i = (w.row0 + h) / p.gsize, head = w.g * p.gsize + (w.row0 + h) % p.gsize;
+            raw = __ldg(reinterpret_cast<const uint4*>(p.q + (((long long)w.b * p.Lq + i) * p.Hq + head) * D) + c8);
           }
-#pragma unroll
-          for (int m = 0; m < kDeep; ++m) {
-            const int h = h0 + m * kRowsAt;
-            const uint32_t words[4] = {raw[m].x, raw[m].y, raw[m].z, raw[m].w};
+            const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
             float x[8], most = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[2 * k] = bf16_lo(words[k]), x[2 * k + 1] = bf16_hi(words[k]);
@@ -659,7 +667,6 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             *reinterpret_cast<uint2*>(qd + off) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(qd + NCOL * D + off) = make_uint2(lo2[0], lo2[1]);
             if (c8 == 0) w.qf[h] = __uint_as_float((uint32_t)max(127 - by, 1) << 23);
-          }
         }
         fence_proxy_async_smem();
       }
@@ -672,6 +679,27 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const bool edge = j0 + kNt > lim_min;               // keys that some row does not see
           good = wait(sm.v_full[st], ph) && (tt < C::kWBufs || wait(sm.w_empty[tt % C::kWBufs], (uint32_t)(tt / C::kWBufs - 1) & 1u));
           if (!good) break;
+          if (edge) {
+            // one thread a key: a key past the range is 0; of a key that some row does not see, NaN becomes 0
+            // here and the epilogue puts it into the rows that see it
+            const int j = j0 + ct;
+            uint4* row = reinterpret_cast<uint4*>(vring + st * C::kTile + ct * D);
+            if (j >= lim_min)
+#pragma unroll 1
+              for (int k = 0; k < D / 16; ++k) {
+                uint4 v = row[k];
+                uint32_t* words = &v.x;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                  const uint32_t nan = (((words[m] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                  if (nan != 0 && j < ke) w.nan_values = 1;
+                  words[m] = j < ke ? words[m] & ~(nan * 0xffu) : 0u;
+                }
+                row[k] = v;
+              }
+            fence_proxy_async_smem();                         // (the stage's next tile comes by a copy)
+            named_bar_sync(kBarConvert, 32 * kConvWarps);
+          }
           // this warp's 32 dims: the tile's bytes transposed on the way out of shared memory (16 keys x 16
           // dims a matrix: a lane gets 4 keys of dim lane / 4), fp16, to TMEM lane = dim, column = key / 2
           if (dim0 < D) {
@@ -684,23 +712,6 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
               for (int m = 0; m < 4; ++m)                     // 32 keys each
                 ldmatrix_t_b8(src + m * 32 * D + (C::kchunk((uint32_t)(dim0 / 16 + half), (uint32_t)lane) << 4), r[m]);
-              if (edge) {
-                // a key past the range is 0; of a key that some row does not see, NaN becomes 0 here and the
-                // epilogue puts it into the rows that see it
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const int j = j0 + m * 32 + (q >> 1) * 16 + 4 * (lane & 3);
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                      const uint32_t byte = 0xffu << (8 * z);
-                      const bool nan = j + z >= lim_min && (r[m][q] & byte & 0x7f7f7f7fu) == (byte & 0x7f7f7f7fu);
-                      if (nan && j + z < ke) w.nan_values = 1;
-                      if (nan || j + z >= ke) r[m][q] &= ~byte;
-                    }
-                  }
-              }
 #pragma unroll
               for (int m = 0; m < 4; m += 2) {
                 uint32_t o[16];

@@ -60,6 +60,7 @@ constexpr int kMaxBoxes = 16;                  // blocks of 8 tokens
 constexpr int kMeta = 8;                       // tiles whose scale bytes are kept (K stages and 2 more at least)
 constexpr int kConvWarp = 4, kSoftWarp = 8, kConvWarps = 4;
 constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of it after a move
+constexpr float kNoRef = 1e30f;                // -R of a row that has seen no key: any y + kNoRef is above kTop, -inf stays
 constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;
 constexpr int kMaxCols = 64;
 constexpr int kUnitCost = 1;                   // start and end of a unit, in tiles
@@ -77,17 +78,19 @@ struct Params {
   int B, Lq, Hq, Hkv, N, I, max_lb, bs, num_blocks, m_tiles, gsize;
   int box_shift;                               // log2 of the tokens of a TMA box
   float scale_log2;
-  unsigned long long wait_ns;
+  uint32_t wait_ns;                            // limit of a wait, below 2^32
   int skip_tile;
 };
 
 template <int NCOL>
 struct Unit {
   int b, r, g, row0, rows;                     // rows: query rows of the tile
+  int n, first, keys;                          // queries of the request, position of the first; keys of the shard
   int t0, tiles;                               // first tile, tiles (-1: no more units)
-  int ke, lim_min;                             // keys of the shard; those below lim_min are seen by every live row
+  int ke, lim_min;                             // keys that some row sees; those below lim_min every live row sees
   int slot;                                    // partial slot, -1: final rows
   int nan_values;                              // hidden or ragged keys hold NaN values
+  // written by the warps that split the query
   alignas(16) int lim[NCOL];                   // keys that a row sees (0: no such query)
   alignas(16) float qf[NCOL];                  // scale of the split query row
   long long at[NCOL];                          // where its output goes, in rows
@@ -137,7 +140,8 @@ struct Smem {
   long long sums[Cfg<NCOL, D>::kWarps];
   uint16_t meta[kMeta][kMaxBoxes];             // scale bytes of a tile's boxes: K, V << 8
   alignas(16) float red[4][NCOL];              // maxima and sums of the rows by lane quadrant
-  alignas(16) float ref[NCOL], inv[NCOL];      // at a unit's end: references, 1 / sum (-1: no output)
+  alignas(16) float nref[NCOL];                // references of the rows, negated
+  alignas(16) float by[NCOL];                  // what a move of them scales by; at a unit's end 1 / sum (-1: no output)
   Unit<NCOL> unit[Cfg<NCOL, D>::kUnits];
 };
 
@@ -217,6 +221,12 @@ __device__ __forceinline__ float across_lanes(const float (&v)[16], int lane, Op
   return op(a[0], __shfl_xor_sync(0xffffffffu, a[0], 1));
 }
 
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -265,6 +275,11 @@ __device__ __forceinline__ Request request_of(const Params& p, int b, int r) {
   const long long room = (long long)p.max_lb * p.bs;
   if (q.keys > room) q.keys = (int)room, q.bad = true;
   return q;
+}
+
+// a / b (a 64-bit division costs several times as much)
+__device__ __forceinline__ long long quotient(long long a, unsigned b) {
+  return (unsigned long long)a >> 32 ? a / b : (long long)((unsigned)a / b);
 }
 
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kNt - 1) / kNt; }
@@ -326,6 +341,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   const int entries = p.B * p.N, per = (entries + (int)kThreads - 1) / (int)kThreads;
   const long long units_per = (long long)p.Hkv * p.m_tiles;
   long long mine = 0;
+#pragma unroll 1
   for (int k = 0; k < per; ++k)
     if (tid * (long long)per + k < entries) mine += weight_of(p, tid * per + k);
   mine *= units_per;
@@ -345,11 +361,13 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   }
   // (no share is empty, so the parts of a cut unit are neighbours; CTAs past the summed weight have none)
   const long long ctas = min((long long)gridDim.x, total);
-  const long long lo = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
-  const long long hi = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+  const long long each = quotient(total, (unsigned)ctas), over = total - each * ctas;    // (the first `over` take one more)
+  const long long c = min((long long)blockIdx.x, ctas), lo = each * c + min(c, over);
+  const long long hi = blockIdx.x < ctas ? lo + each + (c < over ? 1 : 0) : lo;
   if (upto - mine <= lo && lo < upto) {
     long long at = upto - mine;
     int e = tid * per;
+#pragma unroll 1
     for (;; ++e) {
       const long long next = at + weight_of(p, e) * units_per;
       if (lo < next) break;
@@ -366,25 +384,26 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     set_status(p.status, DCP_ERR_TIMEOUT);
     *abort_flag = 1;
   };
-  // A whole warp waits for the phase of `parity`; false: it did not come within the limit (or, with
-  // `heeds`, the CTA has given up).  Compact on purpose: every role's code shares the instruction cache.
-  auto wait_at = [&](uint32_t bar, uint32_t parity, bool heeds, unsigned long long limit_ns) -> bool {
-    unsigned long long start = 0;
-    for (uint32_t polls = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++polls) {
-      if (heeds && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
-      if ((polls & 63u) == 0) {
-        const unsigned long long now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
-        if (polls == 0) start = now;
-        else if (now - start > limit_ns) return false;
-      }
+  // A whole warp waits for the phase of `parity`; false: it did not come within `limits` times the limit (or,
+  // with `heeds`, the CTA has given up).  Compact on purpose: every role's code shares the instruction cache.
+  auto wait_at = [&](uint32_t bar, uint32_t parity, bool heeds, int limits) -> bool {
+    uint32_t start = 0;
+    bool first = true;
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+      const uint32_t now = globaltimer_lo();
+      if (first) start = now, first = false;
+      bool stop = heeds && *abort_flag != 0;
+      if (now - start > p.wait_ns) start = now, stop |= --limits == 0;
+      if (__any_sync(0xffffffffu, stop)) return false;
     }
     return true;
   };
-  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_at(smem_u32(&bar), parity, true, p.wait_ns); };
+  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool { return wait_at(smem_u32(&bar), parity, true, 1); };
   // the next unit's descriptor (a whole warp); false: there are no more, or the wait ran out
   auto unit_wait = [&](int u, int limits = 4) -> bool {
     const int slot = u % C::kUnits;
-    if (!wait_at(smem_u32(&sm.unit_full[slot]), (uint32_t)(u / C::kUnits) & 1u, false, limits * p.wait_ns)) {
+    if (!wait_at(smem_u32(&sm.unit_full[slot]), (uint32_t)(u / C::kUnits) & 1u, false, limits)) {
       fail();
       return false;
     }
@@ -402,7 +421,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (lane == 0) p.cut[2 * blockIdx.x] = p.cut[2 * blockIdx.x + 1] = -1;
     auto slot_free = [&](int u) -> bool {
       if (u < C::kUnits ||
-          wait_at(smem_u32(&sm.unit_empty[u % C::kUnits]), (uint32_t)(u / C::kUnits - 1) & 1u, false, 4 * p.wait_ns))
+          wait_at(smem_u32(&sm.unit_empty[u % C::kUnits]), (uint32_t)(u / C::kUnits - 1) & 1u, false, 4))
         return true;
       fail();
       return false;
@@ -411,6 +430,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     long long at = sm.start_at;
     bool ok = true;
     if (e >= 0) {
+#pragma unroll 1
       for (; ok && e < entries && at < hi; ++e) {
         const int b = e / p.N, r = e % p.N;
         const Request q = request_of(p, b, r);
@@ -418,14 +438,16 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int32_t* bt = p.block_tables + ((long long)r * p.B + b) * p.max_lb;
         // a block id past the pool among the keys empties the request in this shard
         bool bad_block = false;
+#pragma unroll 1
         for (int k = lane; k < (q.keys + p.bs - 1) / p.bs; k += 32) bad_block |= (unsigned)bt[k] >= (unsigned)p.num_blocks;
         bad_block = __any_sync(0xffffffffu, bad_block);
         if (lane == 0 && (q.bad || bad_block)) set_status(p.status, DCP_ERR_BOUNDS);
-        long long k0 = at < lo ? (lo - at) / weight : 0;      // first unit of the entry in this share
+        long long k0 = at < lo ? quotient(lo - at, (unsigned)weight) : 0;      // first unit of the entry in this share
+#pragma unroll 1
         for (; k0 < units_per; ++k0) {
           const long long first = at + k0 * weight;
           if (first >= hi) break;
-          const int g = (int)(k0 / p.m_tiles), mt = (int)(k0 % p.m_tiles);
+          const int g = (int)((unsigned)k0 / (unsigned)p.m_tiles), mt = (int)k0 - g * p.m_tiles;
           const int row0 = mt * NCOL, rows = min(NCOL, p.Lq * p.gsize - row0);
           const int live = bad_block || row0 / p.gsize >= q.n ? 0 : tiles;      // tiles that count
           const int t0 = (int)min(max(lo - first, 0LL), (long long)live), t1 = (int)min(hi - first, (long long)live);
@@ -434,25 +456,19 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           ok = slot_free(u);
           if (!ok) break;
           Unit<NCOL>& w = sm.unit[slot];
-          const int slot_at = live == 0 || (t0 == 0 && t1 == live) ? -1 : 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1);
-          const int i_last = min(q.n - 1, (row0 + rows - 1) / p.gsize);
-          for (int h = lane; h < NCOL; h += 32) {
-            const int i = (row0 + h) / p.gsize;
-            w.at[h] = slot_at >= 0 ? (long long)slot_at * NCOL + h
-                                   : (((long long)r * p.B + b) * p.Lq + i) * p.Hq + g * p.gsize + (row0 + h) % p.gsize;
-            w.lim[h] = h < rows && i < q.n ? min(q.keys, held_below(q.S - q.n + i + 1, r, p.I, p.N)) : 0;
-          }
           if (lane == 0) {
+            const int slot_at = live == 0 || (t0 == 0 && t1 == live) ? -1 : 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1);
             w.b = b, w.r = r, w.g = g, w.row0 = row0, w.rows = rows;
+            w.n = q.n, w.first = q.S - q.n, w.keys = q.keys;
             w.t0 = t0, w.tiles = t1 - t0;
-            w.ke = live > 0 ? min(q.keys, held_below(q.S - q.n + i_last + 1, r, p.I, p.N)) : 0;
-            w.lim_min = live > 0 ? min(w.ke, held_below(q.S - q.n + row0 / p.gsize + 1, r, p.I, p.N)) : 0;
+            w.ke = live == 0 ? 0 : min(q.keys, held_below(w.first + min(q.n, (row0 + rows - 1) / p.gsize + 1), r, p.I, p.N));
+            w.lim_min = live == 0 ? 0 : min(w.ke, held_below(w.first + row0 / p.gsize + 1, r, p.I, p.N));
             w.slot = slot_at;
             w.nan_values = 0;
             if (slot_at >= 0) p.cut[slot_at] = (long long)e * units_per + k0;
+            mbar_arrive(smem_u32(&sm.unit_full[slot]));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.unit_full[slot]));
           ++u;
         }
         at += weight * units_per;
@@ -469,6 +485,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     int kst = 0, vst = 0, tt = 0;
     uint32_t kph = 1, vph = 1;
     int k_issued = 0, v_issued = 0;
+#pragma unroll 1
     for (int u = 0; unit_wait(u); ++u) {
       const Unit<NCOL>& w = sm.unit[u % C::kUnits];
       const int tiles = *abort_flag ? 0 : w.tiles, t0 = w.t0, ke = w.ke, g = w.g;
@@ -486,6 +503,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       };
       int blk = entry(0), blk1 = entry(window), blk2 = entry(2 * window);
       uint32_t sc = scale_bytes(blk), sc1 = scale_bytes(blk1);
+#pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
         const int in = t & (window - 1);
         if (in == 0 && t > 0) {
@@ -525,10 +543,12 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     if (*abort_flag) {
       // copies in flight land before the CTA leaves
+#pragma unroll 1
       for (int k = max(0, k_issued - kKStages); k < k_issued; ++k)
-        wait_at(smem_u32(&sm.k_full[k % kKStages]), (uint32_t)(k / kKStages) & 1u, false, p.wait_ns);
+        wait_at(smem_u32(&sm.k_full[k % kKStages]), (uint32_t)(k / kKStages) & 1u, false, 1);
+#pragma unroll 1
       for (int k = max(0, v_issued - kVStages); k < v_issued; ++k)
-        wait_at(smem_u32(&sm.v_full[k % kVStages]), (uint32_t)(k / kVStages) & 1u, false, p.wait_ns);
+        wait_at(smem_u32(&sm.v_full[k % kVStages]), (uint32_t)(k / kVStages) & 1u, false, 1);
     }
   } else if (warp == 1) {
     // ---------------- QK issuer: S^T(t) = K(t) (Q_hi + Q_lo)^T ----------------
@@ -537,12 +557,14 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const uint32_t tm = uniform(tmem), ring = uniform(smem_u32(kring)), qaddr = uniform(smem_u32(qs));
     int st = 0, tt = 0;
     uint32_t ph = 0;
+#pragma unroll 1
     for (int u = 0; unit_wait(u); ++u) {
       const int slot = u % C::kUnits;
       const int tiles = (int)uniform((uint32_t)sm.unit[slot].tiles);
       // (waited for in units without tiles too: a phase left out would make the next wait pass early)
       bool good = wait(sm.q_full, (uint32_t)u & 1u);
       if (tiles > 0 && *abort_flag == 0) {
+#pragma unroll 1
         for (int t = 0; good && t < tiles; ++t, ++tt) {
           good = wait(sm.k_full[st], ph) && (tt < 2 || wait(sm.s_free[tt & 1], (uint32_t)((tt >> 1) - 1) & 1u));
           if (!good) break;
@@ -568,18 +590,20 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     if (lead) mma_commit(smem_u32(&sm.drain[0]));
     __syncwarp();
-    if (!wait_at(smem_u32(&sm.drain[0]), 0, false, p.wait_ns)) fail();
+    if (!wait_at(smem_u32(&sm.drain[0]), 0, false, 1)) fail();
   } else if (warp == 2) {
     // ---------------- PV issuer: O^T += V16^T(t) P^T(t) ----------------
     constexpr uint32_t id = idesc_fp16_mn(NCOL);
     const bool lead = elect_one();
     const uint32_t tm = uniform(tmem), paddr = uniform(smem_u32(ps));
     int tt = 0, o_units = 0;
+#pragma unroll 1
     for (int u = 0; unit_wait(u); ++u) {
       const int tiles = (int)uniform((uint32_t)sm.unit[u % C::kUnits].tiles);
       if (tiles > 0 && *abort_flag == 0) {
         bool good = o_units < 2 || wait(sm.o_free[o_units & 1], (uint32_t)((o_units >> 1) - 1) & 1u);
         const uint32_t dO = tm + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL;
+#pragma unroll 1
         for (int t = 0; good && t < tiles; ++t, ++tt) {
           const uint32_t buf = tt % kBufs;
           good = wait(sm.w_full[tt % C::kWBufs], (uint32_t)(tt / C::kWBufs) & 1u) && wait(sm.p_full[buf], (uint32_t)(tt / kBufs) & 1u);
@@ -603,7 +627,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     }
     if (lead) mma_commit(smem_u32(&sm.drain[1]));
     __syncwarp();
-    if (!wait_at(smem_u32(&sm.drain[1]), 0, false, p.wait_ns)) fail();
+    if (!wait_at(smem_u32(&sm.drain[1]), 0, false, 1)) fail();
   }
   } else if (warp < kSoftWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::kConvRegs));
@@ -611,13 +635,14 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int ct = tid - 32 * kConvWarp, dim0 = 32 * (warp - kConvWarp);
     int st = 0, tt = 0;
     uint32_t ph = 0;
+#pragma unroll 1
     for (int u = 0; unit_wait(u); ++u) {
       const int slot = u % C::kUnits;
       Unit<NCOL>& w = sm.unit[slot];
       const int tiles = w.tiles, t0 = w.t0, ke = w.ke, lim_min = w.lim_min;
       // the last unit's scores are done with the query's buffer
       if (u > 0 && !wait(sm.q_free, (uint32_t)(u - 1) & 1u)) fail();
-      if (tiles > 0 && *abort_flag == 0) {
+      {
         // query rows: D / 8 lanes a row; the row's largest magnitude goes to [128, 256), hi = e4m3(q),
         // lo = e4m3(q - hi); a value that is not finite makes its row NaN
         constexpr int kLanes = D / 8, kRowsAt = 128 / kLanes;
@@ -626,9 +651,13 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll 1
         for (int h = ct / kLanes; h < NCOL; h += kRowsAt) {
           uint4 raw = make_uint4(0, 0, 0, 0);
-          if (w.lim[h] > 0) {
-            const int i = (w.row0 + h) / p.gsize, head = w.g * p.gsize + (w.row0 + h) % p.gsize;
-            raw = __ldg(reinterpret_cast<const uint4*>(p.q + (((long long)w.b * p.Lq + i) * p.Hq + head) * D) + c8);
+          const int i = (w.row0 + h) / p.gsize, head = w.g * p.gsize + (w.row0 + h) - i * p.gsize;
+          const bool there = h < w.rows && i < w.n;
+          const long long row = ((long long)w.b * p.Lq + i) * p.Hq + head;
+          if (there) raw = __ldg(reinterpret_cast<const uint4*>(p.q + row * D) + c8);
+          if (c8 == 0) {
+            w.lim[h] = there && tiles > 0 ? min(w.keys, held_below(w.first + i + 1, w.r, p.I, p.N)) : 0;
+            w.at[h] = w.slot >= 0 ? (long long)w.slot * NCOL + h : (long long)w.r * p.B * p.Lq * p.Hq + row;
           }
             const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
             float x[8], most = 0.f;
@@ -674,6 +703,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));     // (once per unit: its parity goes by them)
       if (tiles > 0 && *abort_flag == 0) {
         bool good = true;
+#pragma unroll 1
         for (int t = 0; t < tiles; ++t, ++tt) {
           const int j0 = (t0 + t) * kNt;
           const bool edge = j0 + kNt > lim_min;               // keys that some row does not see
@@ -745,36 +775,29 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int h0 = ((warp - kSoftWarp) >> 2) * HC;
     const int lrow = qd * 32 + lane;                          // key of the tile; value dim of O^T
     const uint32_t lane_base = tmem + ((uint32_t)(qd * 32) << 16);
+    const int st = tid - 32 * kSoftWarp;                      // thread st looks after row st where one has to
     int tt = 0, o_units = 0;
     bool dead = false;                                        // a wait ran out: the same in every softmax thread
     // (they meet at barriers, so none may give up alone on a unit that comes late: the scheduler has
     // given up on its own wait long before this limit)
+#pragma unroll 1
     for (int u = 0; unit_wait(u, 16); ++u) {
-      const int slot = u % C::kUnits;
-      const Unit<NCOL>& w = sm.unit[slot];
-      const int tiles = w.tiles, ke = w.ke, lim_min = w.lim_min;
-      float m[HC], l[HC];                                     // reference (R) and sum of a row
+      const Unit<NCOL>& w = sm.unit[u % C::kUnits];
+      const int tiles = w.tiles, t0 = w.t0, lim_min = w.lim_min;
+      float nm[HC], l[HC];                                    // -R and the sum of a row
       const uint32_t tO = lane_base + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL + h0;
-      bool bad = false, broke = dead || tiles == 0;
+      bool bad = !wait(sm.q_full, (uint32_t)u & 1u), broke = dead || tiles == 0;
+      if (st < NCOL) sm.nref[st] = kNoRef;
 #pragma unroll
-      for (int h = 0; h < HC; ++h) m[h] = -INFINITY, l[h] = 0.f;
+      for (int h = 0; h < HC; ++h) nm[h] = kNoRef, l[h] = 0.f;
+#pragma unroll 1
       for (int t = 0; !broke && t < tiles; ++t, ++tt) {
-        const uint32_t buf = tt & 1, par = (uint32_t)(tt >> 1) & 1u;
-        const bool okw = wait(sm.s_full[buf], par);
-        if (!okw) bad = true;
-        float y[HC];
-        {
-          uint32_t v[HC];
-#pragma unroll
-          for (int h = 0; h < HC; ++h) v[h] = 0u;
-          if (okw) {
-            tc_fence_after();
-            tmem_ld16(lane_base + buf * NCOL + h0, v);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int h = 0; h < HC; ++h) y[h] = __uint_as_float(v[h]);
-        }
+        const uint32_t buf = tt & 1;
+        bad |= !wait(sm.s_full[buf], (uint32_t)(tt >> 1) & 1u);           // (whatever is read then is not used)
+        uint32_t v[HC];
+        tc_fence_after();
+        tmem_ld16(lane_base + buf * NCOL + h0, v);
+        tmem_wait_ld();
         const uint32_t meta = sm.meta[tt & (kMeta - 1)][lrow >> p.box_shift];
         tc_fence_before();
         __syncwarp();
@@ -783,37 +806,43 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int sv = (int)(meta >> 8);
         const float ev = sv == 255 ? NAN : (float)(sv - 127), inv = scale_factor((uint32_t)max(254 - sv, 0));
 
-        const int j = (w.t0 + t) * kNt + lrow;
-        const bool full = (w.t0 + t) * kNt + kNt <= lim_min;
-        float most = -INFINITY;
+        // y = x + ev of this key's rows; hidden keys -inf
+        const int j = (t0 + t) * kNt + lrow;
+        const bool full = (t0 + t) * kNt + kNt <= lim_min;
+        float y[HC], most = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < HC; ++h) {
-          y[h] = fmaf(y[h], kf * w.qf[h0 + h], ev);           // (written before the query's barrier, so before S)
-          if (!full && j >= w.lim[h0 + h]) y[h] = -INFINITY;
-          most = fmaxf(most, y[h] - m[h]);
+        for (int h = 0; h < HC; h += 4) {
+          const float4 qf = *reinterpret_cast<const float4*>(&w.qf[h0 + h]);
+          y[h] = fmaf(__uint_as_float(v[h]), kf * qf.x, ev);
+          y[h + 1] = fmaf(__uint_as_float(v[h + 1]), kf * qf.y, ev);
+          y[h + 2] = fmaf(__uint_as_float(v[h + 2]), kf * qf.z, ev);
+          y[h + 3] = fmaf(__uint_as_float(v[h + 3]), kf * qf.w, ev);
         }
+        if (!full)
+#pragma unroll
+          for (int h = 0; h < HC; ++h) y[h] = j < w.lim[h0 + h] ? y[h] : -INFINITY;
+#pragma unroll
+        for (int h = 0; h < HC; ++h) most = fmaxf(most, y[h] + nm[h]);
         // one barrier per tile: does any row's reference have to move?
         if (bar_red_or(kBarSoftmax, kSoftThreads, most > kTop || bad)) {
-          if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) {
-            broke = dead = true;
-            break;
-          }
           sm.red[qd][h0 + (lane >> 1)] = across_lanes(y, lane, [](float a, float b) { return fmaxf(a, b); });
           // O^T is rescaled: the previous tile's product must have landed
-          if (t > 0 && !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u)) bad = true;
+          if (t > 0) bad |= !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u);
           if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) {
             broke = dead = true;
             break;
           }
-          float alpha[HC];
+          if (st < NCOL) {
+            const float top = fmaxf(fmaxf(sm.red[0][st], sm.red[1][st]), fmaxf(sm.red[2][st], sm.red[3][st]));
+            const float was = sm.nref[st], is = fminf(was, kStart - top);
+            sm.nref[st] = is;
+            sm.by[st] = was == kNoRef ? 0.f : ex2(is - was);
+          }
+          named_bar_sync(kBarSoftmax, kSoftThreads);
 #pragma unroll
           for (int h = 0; h < HC; ++h) {
-            const int hh = h0 + h;
-            const float top = fmaxf(fmaxf(sm.red[0][hh], sm.red[1][hh]), fmaxf(sm.red[2][hh], sm.red[3][hh]));
-            const float ref = fmaxf(m[h], top - kStart);
-            alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - ref);
-            m[h] = ref;
-            l[h] *= alpha[h];
+            nm[h] = sm.nref[h0 + h];
+            l[h] *= sm.by[h0 + h];
           }
           if (t > 0) {
             tc_fence_after();
@@ -821,24 +850,21 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             tmem_ld16(tO, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < HC; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha[k]);
+            for (int k = 0; k < HC; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.by[h0 + k]);
             tmem_st16(tO, o);
             tmem_wait_st();
           }
         }
+        // (a hidden key's y is -inf, its P 0)
         uint32_t pk[HC / 2];
 #pragma unroll
         for (int h = 0; h < HC; h += 2) {
-          float p0 = ex2(y[h] - m[h]), p1 = ex2(y[h + 1] - m[h + 1]);
-          if (!full) {
-            p0 = y[h] == -INFINITY ? 0.f : p0;
-            p1 = y[h + 1] == -INFINITY ? 0.f : p1;
-          }
+          const float p0 = ex2(y[h] + nm[h]), p1 = ex2(y[h + 1] + nm[h + 1]);
           l[h] = fmaf(p0, inv, l[h]);
           l[h + 1] = fmaf(p1, inv, l[h + 1]);
           pk[h / 2] = pack_f16x2(p0, p1);
         }
-        if (tt >= kBufs && !wait(sm.p_free[tt % kBufs], (uint32_t)(tt / kBufs - 1) & 1u)) bad = true;
+        if (tt >= kBufs) bad |= !wait(sm.p_free[tt % kBufs], (uint32_t)(tt / kBufs - 1) & 1u);
         uint8_t* prow = ps + (tt % kBufs) * C::kPBytes + lrow * C::kPitch;
 #pragma unroll
         for (int c = 0; c < HC / 8; ++c)
@@ -852,40 +878,32 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
       // the last product, row sums over the 128 key threads, outputs
       bool have = !broke;
-      if (have && !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u)) bad = true;
+      if (have) bad |= !wait(sm.p_free[(tt - 1) % kBufs], (uint32_t)((tt - 1) / kBufs) & 1u);
+      sm.red[qd][h0 + (lane >> 1)] = across_lanes(l, lane, [](float a, float b) { return a + b; });
       if (bar_red_or(kBarSoftmax, kSoftThreads, bad)) have = false, dead = true;
       if (bad) fail();
-      sm.red[qd][h0 + (lane >> 1)] = across_lanes(l, lane, [](float a, float b) { return a + b; });
-      if (qd == 0 && lane == 0)
-#pragma unroll
-        for (int h = 0; h < HC; ++h) sm.ref[h0 + h] = m[h];
-      uint32_t o[HC];
-#pragma unroll
-      for (int h = 0; h < HC; ++h) o[h] = 0u;
-      if (have) {
-        tc_fence_after();
-        tmem_ld16(tO, o);
-        tmem_wait_ld();
-        tc_fence_before();
+      if (st < w.rows) {
+        const float sum = (sm.red[0][st] + sm.red[1][st]) + (sm.red[2][st] + sm.red[3][st]);
+        const bool live = have && w.lim[st] > 0 && !(sum == 0.f);         // (NaN sums make NaN rows)
+        sm.by[st] = live ? 1.f / sum : -1.f;
+        (w.slot >= 0 ? p.ws_lse : p.lse)[w.at[st]] = live ? (log2f(sum) - sm.nref[st]) * 0.69314718055994531f : -INFINITY;
       }
+      uint32_t o[HC];                                         // (without a product whatever is there: not used)
+      tc_fence_after();
+      tmem_ld16(tO, o);
+      tmem_wait_ld();
+      tc_fence_before();
       __syncwarp();
       if (tiles > 0) {
         if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[o_units & 1]));
         ++o_units;
       }
       named_bar_sync(kBarSoftmax, kSoftThreads);
-      float* const dst_o = w.slot >= 0 ? p.ws_o : p.out;
-      if (const int h = tid - 32 * kSoftWarp; h < w.rows) {
-        const float sum = (sm.red[0][h] + sm.red[1][h]) + (sm.red[2][h] + sm.red[3][h]);
-        const bool live = have && w.lim[h] > 0 && !(sum == 0.f);          // (NaN sums make NaN rows)
-        sm.inv[h] = live ? 1.f / sum : -1.f;
-        (w.slot >= 0 ? p.ws_lse : p.lse)[w.at[h]] = live ? (sm.ref[h] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      }
-      named_bar_sync(kBarSoftmax, kSoftThreads);
-      if (have && *(volatile int*)&w.nan_values && lrow < D) {
+      if (have && *(volatile const int*)&w.nan_values && lrow < D) {
         // NaN values among the keys that some row does not see: into the rows that see them
         const int32_t* bt = p.block_tables + ((long long)w.r * p.B + w.b) * p.max_lb;
-        for (int j = max(lim_min, w.t0 * kNt); j < min(ke, (w.t0 + tiles) * kNt); ++j) {
+#pragma unroll 1
+        for (int j = max(lim_min, t0 * kNt); j < min(w.ke, (t0 + tiles) * kNt); ++j) {
           const long long row = (long long)bt[j / p.bs] * p.bs + j % p.bs;
           const bool nan = (p.codes_v[(row * p.Hkv + w.g) * D + lrow] & 0x7f) == 0x7f;
 #pragma unroll
@@ -893,11 +911,12 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             if (nan && j < w.lim[h0 + h]) o[h] = 0x7fc00000u;
         }
       }
+      float* const dst = (w.slot >= 0 ? p.ws_o : p.out) + lrow;
 #pragma unroll
       for (int h = 0; h < HC; ++h)
         if (h0 + h < w.rows && lrow < D) {
-          const float inv = sm.inv[h0 + h];
-          dst_o[w.at[h0 + h] * D + lrow] = inv < 0.f ? 0.f : __uint_as_float(o[h]) * inv;
+          const float by = sm.by[h0 + h];
+          dst[w.at[h0 + h] * D] = by < 0.f ? 0.f : __uint_as_float(o[h]) * by;
         }
       unit_done(u);
     }
@@ -1052,7 +1071,7 @@ cudaError_t launch_kv8_gqa(const AttnArgs& a) {
   p.m_tiles = m_tiles_of(a), p.gsize = a.Hq / a.Hkv;
   for (p.box_shift = 0; (1 << p.box_shift) < box_rows;) ++p.box_shift;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.wait_ns = test_hooks().wait_ns;
+  p.wait_ns = (uint32_t)std::min<unsigned long long>(test_hooks().wait_ns, 4000000000ull);
   p.skip_tile = test_hooks().skip_tile;
   if (a.Dqk == 64)
     return ncol == 16   ? launch<16, 64>(tm_k, tm_v, p, grid, a.stream)

@@ -63,7 +63,7 @@ constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of 
 constexpr float kNoRef = 1e30f;                // -R of a row that has seen no key: any y + kNoRef is above kTop, -inf stays
 constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;
 constexpr int kMaxCols = 64;
-constexpr int kUnitCost = 1;                   // start and end of a unit, in tiles
+constexpr int kUnitCost = 2;                   // start and end of a unit, in tiles
 constexpr uint32_t kWCols = kNt / 2;           // TMEM columns of an fp16 value tile
 
 struct Params {
@@ -379,6 +379,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   auto fail = [&](void) {
     set_status(p.status, DCP_ERR_TIMEOUT);
@@ -933,44 +934,70 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 // Joins the partial rows of the units that borders of the CTAs' shares cut: a unit's first part
 // is a CTA's tail slot, the others are the head slots of the CTAs behind it.
 //   LSE = log sum exp lse_k,  o = sum exp(lse_k - LSE) o_k
+// A warp takes rows in turn: a lane holds the weight of one part (32 at a time), then the parts' rows
+// are summed, kAhead of them in flight.  Started while the attention kernel still runs
+// (griddepcontrol), it waits for that one's memory here.
 template <int NCOL, int D>
-__global__ void __launch_bounds__(256) kv8_join_kernel(const Params p, int grid) {
+__global__ void __launch_bounds__(128) kv8_join_kernel(const Params p, int grid) {
+  constexpr int V = D / 32, kAhead = 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = p.cut[2 * c + 1];
   if (unit < 0) return;
-  int n = 1;
-  while (c + n < grid && p.cut[2 * (c + n)] == unit) ++n;
-  const long long units_per = (long long)p.Hkv * p.m_tiles;
-  const int e = (int)(unit / units_per), k = (int)(unit % units_per);
-  const int b = e / p.N, r = e % p.N, g = k / p.m_tiles, row0 = k % p.m_tiles * NCOL;
+  int n = 1;                                                  // parts
+  for (bool more = true; more;) {
+    const int k = c + n + lane;
+    const unsigned same = __ballot_sync(0xffffffffu, k < grid && p.cut[2 * min(k, grid - 1)] == unit);
+    more = same == 0xffffffffu;
+    n += more ? 32 : __ffs(~same) - 1;
+  }
+  const unsigned units_per = (unsigned)p.Hkv * (unsigned)p.m_tiles;
+  const int e = (int)quotient(unit, units_per), k = (int)(unit - (long long)e * units_per);
+  const int b = e / p.N, r = e - b * p.N, g = k / p.m_tiles, row0 = (k - g * p.m_tiles) * NCOL;
   const int rows = min(NCOL, p.Lq * p.gsize - row0);
-  constexpr int V = D / 32;
-  auto slot_of = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
-  for (int h = warp; h < rows; h += 8) {
-    float top = -INFINITY;
-    bool nan = false;
-    for (int s = lane; s < n; s += 32) {
-      const float v = p.ws_lse[(long long)slot_of(s) * NCOL + h];
-      nan |= v != v;
-      top = fmaxf(top, v);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    nan = __any_sync(0xffffffffu, nan);
-    float sum = 0.f, o[V];
+  auto row_of = [&](int s, int h) { return (long long)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * NCOL + h; };
+#pragma unroll 1
+  for (int h = warp; h < rows; h += 4) {
+    float top = -INFINITY, sum = 0.f, o[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = 0.f;
-    if (top != -INFINITY)
-      for (int s = 0; s < n; ++s) {
-        const long long at = (long long)slot_of(s) * NCOL + h;
-        const float lse = p.ws_lse[at];
-        if (lse == -INFINITY) continue;                       // (what it holds does not count)
-        const float weight = exp2f((lse - top) * 1.4426950408889634f);
-        sum += weight;
+    bool nan = false;
+#pragma unroll 1
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const float lse = s0 + lane < n ? p.ws_lse[row_of(s0 + lane, h)] : -INFINITY;
+      nan |= __any_sync(0xffffffffu, lse != lse);
+      float is = lse;
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(weight, p.ws_o[at * D + v * 32 + lane], o[v]);
+      for (int off = 16; off > 0; off >>= 1) is = fmaxf(is, __shfl_xor_sync(0xffffffffu, is, off));
+      is = fmaxf(is, top);
+      if (is == -INFINITY) continue;
+      const float by = top == -INFINITY ? 0.f : exp2f((top - is) * 1.4426950408889634f);
+      const float weight = lse == -INFINITY ? 0.f : exp2f((lse - is) * 1.4426950408889634f);
+      top = is;
+      sum *= by;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] *= by;
+#pragma unroll 1
+      for (int s = 0; s < min(32, n - s0); s += kAhead) {
+        float x[kAhead][V], w[kAhead];
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m) {
+          w[m] = __shfl_sync(0xffffffffu, weight, (s + m) & 31);
+          if (s0 + s + m >= n) w[m] = 0.f;
+          const float* src = p.ws_o + row_of(min(s0 + s + m, n - 1), h) * D + lane;
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[m][v] = src[32 * v];
+        }
+#pragma unroll
+        for (int m = 0; m < kAhead; ++m)
+          if (w[m] != 0.f) {                                  // (what a part without weight holds does not count)
+            sum += w[m];
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = fmaf(w[m], x[m][v], o[v]);
+          }
       }
-    const int rr = row0 + h, i = rr / p.gsize, head = g * p.gsize + rr % p.gsize;
+    }
+    const int rr = row0 + h, i = rr / p.gsize, head = g * p.gsize + rr - i * p.gsize;
     const long long at = (((long long)r * p.B + b) * p.Lq + i) * p.Hq + head;
     const bool any = top != -INFINITY;
 #pragma unroll
@@ -1013,8 +1040,17 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Param
   kv8_gqa_kernel<NCOL, D><<<(unsigned)grid, Cfg<NCOL, D>::kThreads, smem, stream>>>(tm_k, tm_v, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid == 1) return e;
-  kv8_join_kernel<NCOL, D><<<(unsigned)(grid - 1), 256, 0, stream>>>(p, grid);
-  return cudaGetLastError();
+  // (its start overlaps the attention kernel's end)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(grid - 1));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_join_kernel<NCOL, D>, p, grid);
 }
 
 }  // namespace

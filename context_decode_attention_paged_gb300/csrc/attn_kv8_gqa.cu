@@ -439,8 +439,15 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int32_t* bt = p.block_tables + ((long long)r * p.B + b) * p.max_lb;
         // a block id past the pool among the keys empties the request in this shard
         bool bad_block = false;
+        const int blocks = (q.keys + p.bs - 1) / p.bs;
 #pragma unroll 1
-        for (int k = lane; k < (q.keys + p.bs - 1) / p.bs; k += 32) bad_block |= (unsigned)bt[k] >= (unsigned)p.num_blocks;
+        for (int k = lane; k < blocks; k += 32 * 8) {
+          int blk[8];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) blk[m] = k + 32 * m < blocks ? bt[k + 32 * m] : 0;
+#pragma unroll
+          for (int m = 0; m < 8; ++m) bad_block |= (unsigned)blk[m] >= (unsigned)p.num_blocks;
+        }
         bad_block = __any_sync(0xffffffffu, bad_block);
         if (lane == 0 && (q.bad || bad_block)) set_status(p.status, DCP_ERR_BOUNDS);
         long long k0 = at < lo ? quotient(lo - at, (unsigned)weight) : 0;      // first unit of the entry in this share

@@ -45,7 +45,6 @@ constexpr int kBlocks = 3;         // resident blocks of an SM
 constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
 constexpr int kTaskBytes = 8192;   // rows of a task, at most (when tokens abound)
 constexpr int kMaxPairs = DCP_ROPE_MAX_DIM / 2;   // rotated pairs of a head (shared memory)
-constexpr int kScan = 1024;        // requests whose token counts a block sums
 
 enum Mode { kHalf = 0, kInterleaved = 1, kScalar = 2 };
 
@@ -90,48 +89,6 @@ __device__ __forceinline__ void turn_interleaved(uint4& u, const float* c, const
   }
 }
 
-// ends[b] = tokens of requests 0 .. b, for all b < B <= kScan (whole block).
-__device__ __forceinline__ void sum_counts(const AppendArgs& a, int* ends) {
-  constexpr int kPer = kScan / kThreads;
-  __shared__ int warps[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31;
-  int sums[kPer], run = 0;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int b = tid * kPer + e;
-    bool bad = false;
-    if (b < a.B) run += present(a, b, &bad);
-    if (bad && blockIdx.x == 0) set_status(a.status, DCP_ERR_BOUNDS);
-    sums[e] = run;
-  }
-  int inc = run;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) warps[tid >> 5] = inc;
-  __syncthreads();
-  int before = inc - run;
-  for (int w = 0; w < tid >> 5; ++w) before += warps[w];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    if (tid * kPer + e < a.B) ends[tid * kPer + e] = before + sums[e];
-  __syncthreads();
-}
-
-// (request, index) of the summed-up token, by bisection of the sums
-__device__ __forceinline__ int find_token(const int* ends, int B, unsigned token, int* i) {
-  int b = 0;
-  for (int hi = B - 1; b < hi;) {
-    const int mid = (b + hi) >> 1;
-    if ((unsigned)ends[mid] > token) hi = mid;
-    else b = mid + 1;
-  }
-  *i = (int)token - (b > 0 ? ends[b - 1] : 0);
-  return b;
-}
-
 // cos and sin (times mscale) of position pos in pair e
 __device__ __forceinline__ void turn_of(const AppendArgs& a, long long pos, int e, float& c, float& s) {
   const unsigned long long phase = (unsigned long long)pos * a.steps[e];
@@ -163,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const Para
   const int skip = kHalfLayout ? 2 * turned : turned;    // vectors of the rotated part
   const int unit = lane % turned, first = lane / turned, step = 32 / turned;   // this lane's vector; heads of a pass
   if (p.summed) {
-    sum_counts(a, ends);
+    sum_counts<kThreads>(a, ends);
     tasks = (unsigned)ends[a.B - 1] * (unsigned)parts;
   }
   for (unsigned task = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); task < tasks;

@@ -46,8 +46,15 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
 constexpr int kTaskBytes = 8192;   // rows of a query task, at most (when tokens abound)
+constexpr int kWarpRows = 32;      // rows of a block that a warp takes alone
 
 enum Rot { kPair = 0, kSwap = 1, kAny = 2 };
+
+// Vectors of a head that norm and rotation touch; the `rest` others are copied as they are.
+struct Window {
+  int first, count, rest;
+  unsigned per_rest;               // ceil(2^32 / rest): quotients of small numbers by a multiplication
+};
 
 struct Params {
   NormAppendArgs a;
@@ -59,6 +66,8 @@ struct Params {
   long long kv_tasks;
   int parts, part_heads;           // query heads of a token in parts
   long long q_tasks;
+  bool summed;                     // tasks are numbered over the tokens that are there
+  Window q, k;
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -94,12 +103,13 @@ __host__ __device__ constexpr int scratch_floats(int rot, int sg, int rot_dim) {
   return rot == kAny ? 2 * (32 / sg) * rot_dim : 0;
 }
 
-// A lane's part of a row of one head: dims 8 (sl + SG s) .. + 7, s < SLOTS.
+// A lane's part of a row of one head: dims 8 (first + sl + SG s) .. + 7, s < SLOTS, of the vectors
+// [first, first + vecs) that norm and rotation touch (all of the head where it is quantised).
 template <int SG, int SLOTS, int kRot>
 struct Rows {
   static constexpr int kAngles = kRot == kPair ? 4 : kRot == kSwap ? 8 : 1;
   const AppendArgs& a;
-  int sl, vecs, norm_vecs;
+  int sl, vecs, norm_vecs, dim0;   // dim0: first dim of the window
   float eps, per_dim;              // 1 / norm_dim
   bool normed;
   float w[SLOTS][8];
@@ -108,19 +118,19 @@ struct Rows {
   int partner;                     // kSwap: lane of the partner vector
   float *values, *angles;          // kAny: this group's shared memory
 
-  __device__ __forceinline__ Rows(const NormAppendArgs& n, int lane, float* scratch)
-      : a(n), sl(lane % SG), vecs(n.D / 8), norm_vecs(n.norm_dim / 8), eps(n.eps), per_dim(1.f / (float)n.norm_dim),
-        normed(false), turns(0), partner(lane), values(nullptr), angles(nullptr) {
+  __device__ __forceinline__ Rows(const NormAppendArgs& n, int lane, float* scratch, int first, int count)
+      : a(n), sl(lane % SG), vecs(count), norm_vecs(n.norm_dim / 8), dim0(8 * first), eps(n.eps),
+        per_dim(1.f / (float)n.norm_dim), normed(false), turns(0), partner(lane), values(nullptr), angles(nullptr) {
     if constexpr (kRot == kPair) {
 #pragma unroll
       for (int m = 0; m < SLOTS; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int d = 8 * (sl + SG * m) + 2 * e - a.rot_offset;
+          const int d = dim0 + 8 * (sl + SG * m) + 2 * e - a.rot_offset;
           if (d >= 0 && d < a.rot_dim) turns |= 1u << (4 * m + e);
         }
     } else if constexpr (kRot == kSwap) {
-      const int half = a.rot_dim / 16, v = sl - a.rot_offset / 8;
+      const int half = a.rot_dim / 16, v = sl + (dim0 - a.rot_offset) / 8;
       if (v >= 0 && v < 2 * half) {
         turns = 1;
         partner = lane + (v < half ? half : -half);
@@ -145,16 +155,21 @@ struct Rows {
       for (int m = 0; m < SLOTS; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (turns >> (4 * m + e) & 1u) turn_of(a, pos, (8 * (sl + SG * m) + 2 * e - a.rot_offset) / 2, c[m][e], s[m][e]);
+          if (turns >> (4 * m + e) & 1u) turn_of(a, pos, (dim0 + 8 * (sl + SG * m) + 2 * e - a.rot_offset) / 2, c[m][e], s[m][e]);
     } else if constexpr (kRot == kSwap) {
-      if (turns) {
-        const int half = a.rot_dim / 16, v = sl - a.rot_offset / 8;
-        const bool second = v >= half;
+      // the lanes of both halves need the same 8 angles: each finds 4 and gets the others from its partner
+      const int half = a.rot_dim / 16, v = sl + (dim0 - a.rot_offset) / 8;
+      const bool second = v >= half;
+      float mc[4], ms[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          turn_of(a, pos, 8 * (second ? v - half : v) + e, c[0][e], s[0][e]);
-          if (!second) s[0][e] = -s[0][e];
-        }
+      for (int e = 0; e < 4; ++e)
+        if (turns) turn_of(a, pos, second ? 8 * (v - half) + 4 + e : 8 * v + e, mc[e], ms[e]);
+        else mc[e] = ms[e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float oc = __shfl_sync(0xffffffffu, mc[e], partner), os = __shfl_sync(0xffffffffu, ms[e], partner);
+        c[0][e] = second ? oc : mc[e], c[0][e + 4] = second ? mc[e] : oc;
+        s[0][e] = second ? os : -ms[e], s[0][e + 4] = second ? ms[e] : -os;
       }
     } else {
       __syncwarp();                 // (the last row's angles have been read)
@@ -167,7 +182,8 @@ struct Rows {
   __device__ __forceinline__ void load(const __nv_bfloat16* src, uint4 (&raw)[SLOTS]) const {
 #pragma unroll
     for (int m = 0; m < SLOTS; ++m)
-      raw[m] = src != nullptr && sl + SG * m < vecs ? reinterpret_cast<const uint4*>(src)[sl + SG * m] : make_uint4(0, 0, 0, 0);
+      raw[m] = src != nullptr && sl + SG * m < vecs ? reinterpret_cast<const uint4*>(src + dim0)[sl + SG * m]
+                                                    : make_uint4(0, 0, 0, 0);
   }
 
   __device__ __forceinline__ float group_sum(float v) const {
@@ -186,23 +202,27 @@ struct Rows {
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum = fmaf(x[m][e], x[m][e], sum);
       sum = group_sum(sum);
-      float r = rsqrtf(fmaf(sum, per_dim, eps)), by = 1.f;
+      float r = rsqrtf(fmaf(sum, per_dim, eps));
       if (__any_sync(0xffffffffu, sum > FLT_MAX)) {
         // squares past fp32's range (or an infinity): the row scaled down first; eps is below rounding then
+        const float by = sum > FLT_MAX ? 0x1p-70f : 1.f;
         float small = 0.f;
 #pragma unroll
         for (int m = 0; m < SLOTS; ++m)
           if (sl + SG * m < norm_vecs)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) small = fmaf(x[m][e] * 0x1p-70f, x[m][e] * 0x1p-70f, small);
+            for (int e = 0; e < 8; ++e) {
+              x[m][e] *= by;
+              small = fmaf(x[m][e], x[m][e], small);
+            }
         small = group_sum(small);
-        if (sum > FLT_MAX) r = rsqrtf(small * per_dim), by = 0x1p-70f;
+        if (sum > FLT_MAX) r = rsqrtf(small * per_dim);
       }
 #pragma unroll
       for (int m = 0; m < SLOTS; ++m)
         if (sl + SG * m < norm_vecs)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[m][e] = x[m][e] * by * r * w[m][e];
+          for (int e = 0; e < 8; ++e) x[m][e] = x[m][e] * r * w[m][e];
     }
     if constexpr (kRot == kPair) {
 #pragma unroll
@@ -225,7 +245,7 @@ struct Rows {
       for (int m = 0; m < SLOTS; ++m)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int d = 8 * (sl + SG * m) + e - a.rot_offset;
+          const int d = dim0 + 8 * (sl + SG * m) + e - a.rot_offset;
           if (d >= 0 && d < a.rot_dim) values[d] = x[m][e];
         }
       __syncwarp();
@@ -234,7 +254,7 @@ struct Rows {
       for (int m = 0; m < SLOTS; ++m)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int d = 8 * (sl + SG * m) + e - a.rot_offset;
+          const int d = dim0 + 8 * (sl + SG * m) + e - a.rot_offset;
           if (d < 0 || d >= a.rot_dim) continue;
           const bool second = a.interleaved ? d & 1 : d >= half;
           const int k = a.interleaved ? d >> 1 : second ? d - half : d;
@@ -249,7 +269,7 @@ struct Rows {
     if (dst == nullptr) return;
 #pragma unroll
     for (int m = 0; m < SLOTS; ++m)
-      if (sl + SG * m < vecs) reinterpret_cast<uint4*>(dst)[sl + SG * m] = pack(x[m]);
+      if (sl + SG * m < vecs) reinterpret_cast<uint4*>(dst + dim0)[sl + SG * m] = pack(x[m]);
   }
 };
 
@@ -271,74 +291,105 @@ __device__ __forceinline__ void head_rows(const Rows<SG, SLOTS, kRot>& rows, con
                                           int h0, int h1, int lane, int D) {
   constexpr int kStep = 32 / SG, kDeep = SLOTS > 1 ? 2 : kAhead;
   uint4 raw[kDeep][SLOTS];
-  const int first = h0 + lane / SG;
-  auto load = [&](int h) {
+  const int mine = lane / SG;
+  auto row = [&](int h) { return h < h1 ? src + (long long)h * D : nullptr; };
 #pragma unroll
-    for (int m = 0; m < kDeep; ++m)
-      rows.load(h + m * kStep < h1 ? src + (long long)(h + m * kStep) * D : nullptr, raw[m]);
-  };
-  load(first);
+  for (int m = 0; m < kDeep; ++m) rows.load(row(h0 + m * kStep + mine), raw[m]);
   for (int h = h0; h < h1; h += kDeep * kStep) {             // (whole warps: the norms shuffle)
-    float x[kDeep][SLOTS][8];
-#pragma unroll
-    for (int m = 0; m < kDeep; ++m)
-#pragma unroll
-      for (int k = 0; k < SLOTS; ++k) unpack(raw[m][k], x[m][k]);
-    const int next = h + kDeep * kStep;
-    if (next < h1) load(next + lane / SG);
 #pragma unroll
     for (int m = 0; m < kDeep; ++m) {
       if (h + m * kStep >= h1) break;
-      rows.turn(x[m]);
-      const int hh = h + m * kStep + lane / SG;
-      rows.store_bf16(hh < h1 ? dst + (long long)hh * D : nullptr, x[m]);
+      float x[SLOTS][8];
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) unpack(raw[m][k], x[k]);
+      const int hh = h + m * kStep + mine;
+      rows.load(row(hh + kDeep * kStep), raw[m]);
+      rows.turn(x);
+      rows.store_bf16(hh < h1 ? dst + (long long)hh * D : nullptr, x);
     }
   }
 }
 
-// Task (token, part of its query heads, or behind them its keys and values into the bf16 cache).
-template <int SG, int SLOTS, int kRot>
-__device__ __forceinline__ void token_task(const Params& p, long long task, bool keys, int lane, float* scratch) {
+// The vectors around the window of heads [h0, h1).
+__device__ __forceinline__ void copy_rest(const Window& w, const __nv_bfloat16* src, __nv_bfloat16* dst, int h0, int h1,
+                                          int row16, int lane) {
+  if (w.rest == 0 || src == dst) return;
+  copy_vectors(reinterpret_cast<const uint4*>(src) + (long long)h0 * row16, reinterpret_cast<uint4*>(dst) + (long long)h0 * row16,
+               (h1 - h0) * w.rest, lane, [&](int c) {
+                 const int h = w.rest == 1 ? c : (int)__umulhi((unsigned)c, w.per_rest), v = c - h * w.rest;
+                 return h * row16 + (v < w.first ? v : v + w.count);
+               });
+}
+
+// Task (token, part of its query heads, or (kKeys) behind them its keys and values into the bf16 cache).
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot, bool kKeys>
+__device__ __forceinline__ void token_task(const Params& p, int b, int i, int part, int lane, float* scratch) {
   const NormAppendArgs& a = p.a;
-  const int parts = p.parts + (keys ? 1 : 0);
-  const int part = (int)(task % parts);
-  const long long token = task / parts;
-  const int b = (int)(token / a.L), i = (int)(token % a.L);
   bool bad;
   const int n = present(a, b, &bad);
   if (bad && lane == 0) set_status(a.status, DCP_ERR_BOUNDS);
   if (i >= n) return;
   const long long base = (long long)a.seq_lens[b] - n;
-  Rows<SG, SLOTS, kRot> rows(a, lane, scratch);
-  rows.set_position(position_of(a, b, i, base));
-  if (part < p.parts) {
-    rows.set_weights(a.q_weight);
-    head_rows(rows, static_cast<const __nv_bfloat16*>(a.q) + b * a.q_batch + i * a.q_token,
-              static_cast<__nv_bfloat16*>(a.q_out) + token * a.Hq * a.D, part * p.part_heads,
-              min(a.Hq, (part + 1) * p.part_heads), lane, a.D);
+  const int row16 = a.D / 8;
+  if (!kKeys || part < p.parts) {
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_batch + i * a.q_token;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + ((long long)b * a.L + i) * a.Hq * a.D;
+    const int h0 = part * p.part_heads, h1 = min(a.Hq, h0 + p.part_heads);
+    if (p.q.count > 0) {
+      Rows<QSG, QSLOTS, kRot> rows(a, lane, scratch, p.q.first, p.q.count);
+      rows.set_position(position_of(a, b, i, base));
+      rows.set_weights(a.q_weight);
+      head_rows(rows, src, dst, h0, h1, lane, a.D);
+    }
+    copy_rest(p.q, src, dst, h0, h1, row16, lane);
     return;
   }
-  const long long t = base + i;
-  const int r = (int)((t / a.I) % a.N);
-  const long long j = (t / ((long long)a.I * a.N)) * a.I + t % a.I;
-  const int blk = block_of(a, b, r, (int)(j / a.bs), lane == 0);
-  if (blk < 0) return;
-  const long long cell = ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D;
-  rows.set_weights(a.k_weight);
-  head_rows(rows, static_cast<const __nv_bfloat16*>(a.k) + b * a.k_batch + i * a.k_token, p.pool_k + cell, 0, a.Hkv, lane,
-            a.D);
-  if (a.v != nullptr)
-    copy_vectors(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + b * a.v_batch + i * a.v_token),
-                 reinterpret_cast<uint4*>(p.pool_v + cell), a.Hkv * a.D / 8, lane, [](int c) { return c; });
+  if constexpr (kKeys) {
+    const long long t = base + i;
+    const int r = (int)((t / a.I) % a.N);
+    const long long j = (t / ((long long)a.I * a.N)) * a.I + t % a.I;
+    const int blk = block_of(a, b, r, (int)(j / a.bs), lane == 0);
+    if (blk < 0) return;
+    const long long cell = ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.k) + b * a.k_batch + i * a.k_token;
+    if (p.k.count > 0) {
+      Rows<SG, SLOTS, kRot> rows(a, lane, scratch, p.k.first, p.k.count);
+      rows.set_position(position_of(a, b, i, base));
+      rows.set_weights(a.k_weight);
+      head_rows(rows, src, p.pool_k + cell, 0, a.Hkv, lane, a.D);
+    }
+    copy_rest(p.k, src, p.pool_k + cell, 0, a.Hkv, row16, lane);
+    if (a.v != nullptr)
+      copy_vectors(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + b * a.v_batch + i * a.v_token),
+                   reinterpret_cast<uint4*>(p.pool_v + cell), a.Hkv * row16, lane, [](int c) { return c; });
+  }
 }
 
-template <int SG, int SLOTS, int kRot>
-__global__ void __launch_bounds__(kThreads) append_norm_kernel(const Params p) {
+// The token tasks of blocks [0, blocks), a warp each in turn.
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot, bool kKeys>
+__device__ __forceinline__ void token_tasks(const Params& p, int* ends, unsigned block, unsigned blocks, float* scratch) {
+  const NormAppendArgs& a = p.a;
+  const unsigned parts = p.parts + (kKeys ? 1 : 0);
+  long long tasks = p.q_tasks;
+  if (p.summed) {
+    sum_counts<kThreads>(a, ends);
+    tasks = (long long)ends[a.B - 1] * parts;
+  }
+#pragma unroll 1
+  for (long long task = (long long)block * kWarps + (threadIdx.x >> 5); task < tasks; task += (long long)blocks * kWarps) {
+    const unsigned token = (unsigned)task / parts, part = (unsigned)task - token * parts;
+    int b = (int)(token / (unsigned)a.L), i = (int)(token % (unsigned)a.L);
+    if (p.summed) b = find_token(ends, a.B, token, &i);
+    token_task<SG, SLOTS, QSG, QSLOTS, kRot, kKeys>(p, b, i, (int)part, threadIdx.x & 31, scratch);
+  }
+}
+
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
+__global__ void __launch_bounds__(kThreads, SLOTS == 1 ? 3 : 2) append_norm_kernel(const Params p) {
   extern __shared__ float scratch[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long task = (long long)blockIdx.x * kWarps + warp;
-  if (task < p.q_tasks)
-    token_task<SG, SLOTS, kRot>(p, task, true, lane, scratch + warp * scratch_floats(kRot, SG, p.a.rot_dim));
+  __shared__ int ends[kScan];
+  token_tasks<SG, SLOTS, QSG, QSLOTS, kRot, true>(p, ends, blockIdx.x, gridDim.x,
+                                                  scratch + (threadIdx.x >> 5) * scratch_floats(kRot, QSG < SG ? QSG : SG, p.a.rot_dim));
 }
 
 // Codes of a vector: y / 2^e to nearest (y by = 2^-e), NaN where y is not finite.
@@ -423,7 +474,7 @@ __device__ __forceinline__ void block_rows(const Params& p, long long task, int 
   const __nv_bfloat16* src = values ? static_cast<const __nv_bfloat16*>(a.v) + b * a.v_batch + (long long)h * a.D
                                     : static_cast<const __nv_bfloat16*>(a.k) + b * a.k_batch + (long long)h * a.D;
   const long long token = values ? a.v_token : a.k_token;
-  Rows<SG, SLOTS, kRot> rows(a, lane, scratch);
+  Rows<SG, SLOTS, kRot> rows(a, lane, scratch, 0, a.D / 8);
   auto index_of = [&](int k) { return (int)(global_pos(lo + min(k, count - 1), r, a.I, a.N) - base); };
   auto load = [&](int k, uint4 (&raw)[SLOTS]) { rows.load(k < count ? src + index_of(k) * token : nullptr, raw); };
   auto make = [&](int k, const uint4 (&raw)[SLOTS], float (&y)[SLOTS][8]) {
@@ -521,28 +572,28 @@ __device__ __forceinline__ void block_rows(const Params& p, long long task, int 
   }
 }
 
-template <int SG, int SLOTS, int kRot, int kTeam>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Params p) {
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot, int kTeam>
+__global__ void __launch_bounds__(kThreads, kTeam == 1 && SLOTS == 1 ? 3 : 2) kv8_append_kernel(const Params p) {
   extern __shared__ float scratch[];
+  __shared__ int ends[kScan];
   __shared__ float shared[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* mine = scratch + warp * scratch_floats(kRot, SG, p.a.rot_dim);
+  float* mine = scratch + warp * scratch_floats(kRot, QSG < SG ? QSG : SG, p.a.rot_dim);
   if (blockIdx.x < p.kv_blocks) {
     const long long task = kTeam == 1 ? (long long)blockIdx.x * kWarps + warp : (long long)blockIdx.x;
     if (task < p.kv_tasks) block_rows<SG, SLOTS, kRot, kTeam>(p, task, kTeam == 1 ? 0 : warp, lane, mine, shared);
   } else {
-    const long long task = (long long)(blockIdx.x - p.kv_blocks) * kWarps + warp;
-    if (task < p.q_tasks) token_task<SG, SLOTS, kRot>(p, task, false, lane, mine);
+    token_tasks<SG, SLOTS, QSG, QSLOTS, kRot, false>(p, ends, blockIdx.x - p.kv_blocks, gridDim.x - p.kv_blocks, mine);
   }
 }
 
-template <int SG, int SLOTS, int kRot>
-cudaError_t launch(const Params& p, int team, unsigned grid, cudaStream_t stream) {
-  const size_t smem = (size_t)kWarps * scratch_floats(kRot, SG, p.a.rot_dim) * sizeof(float);
-  void (*kernel)(Params) = p.a.scales == nullptr ? append_norm_kernel<SG, SLOTS, kRot>
-                           : team == 1           ? kv8_append_kernel<SG, SLOTS, kRot, 1>
-                                                 : kv8_append_kernel<SG, SLOTS, kRot, kWarps>;
-  if (smem > 48 * 1024) {
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
+cudaError_t launch_rot(const Params& p, int team, unsigned grid, cudaStream_t stream) {
+  const size_t smem = (size_t)kWarps * scratch_floats(kRot, std::min(QSG, SG), p.a.rot_dim) * sizeof(float);
+  void (*kernel)(Params) = p.a.scales == nullptr ? append_norm_kernel<SG, SLOTS, QSG, QSLOTS, kRot>
+                           : team == 1           ? kv8_append_kernel<SG, SLOTS, QSG, QSLOTS, kRot, 1>
+                                                 : kv8_append_kernel<SG, SLOTS, QSG, QSLOTS, kRot, kWarps>;
+  if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
@@ -550,15 +601,38 @@ cudaError_t launch(const Params& p, int team, unsigned grid, cudaStream_t stream
   return cudaGetLastError();
 }
 
+template <int SG, int SLOTS, int QSG, int QSLOTS>
+cudaError_t launch(const Params& p, int rot, int team, unsigned grid, cudaStream_t stream) {
+  if (rot == kPair) return launch_rot<SG, SLOTS, QSG, QSLOTS, kPair>(p, team, grid, stream);
+  if constexpr (SLOTS == 1)
+    if (rot == kSwap) return launch_rot<SG, SLOTS, QSG, QSLOTS, kSwap>(p, team, grid, stream);
+  return launch_rot<SG, SLOTS, QSG, QSLOTS, kAny>(p, team, grid, stream);
+}
+
+Window window_of(const NormAppendArgs& a, bool normed) {
+  const int row16 = a.D / 8, lo = a.rot_dim ? a.rot_offset / 8 : 0, hi = a.rot_dim ? (a.rot_offset + a.rot_dim + 7) / 8 : 0;
+  Window w;
+  w.first = normed ? 0 : lo;
+  w.count = (normed ? std::max(hi, a.norm_dim / 8) : hi) - w.first;
+  w.rest = row16 - w.count;
+  w.per_rest = w.rest > 1 ? (unsigned)(((1ull << 32) + w.rest - 1) / w.rest) : 0u;
+  return w;
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
   Params p{};
   p.a = a;
+  p.q = window_of(a, a.q_weight != nullptr);
+  p.k = window_of(a, a.k_weight != nullptr);
   const long long pool = (long long)a.num_blocks * a.bs * a.Hkv * a.D;
   const long long tokens = (long long)a.B * a.L;
   const int sms = device_sm_count();
   const int sg = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
+  // queries without a norm have their rotated vectors turned alone, by 8 lanes where they are 8 at most
+  const bool narrow = sg > 8 && p.q.count <= 8;
+  const int qsg = narrow ? 8 : sg;
   int team = 1;
   if (a.scales == nullptr) {
     p.pool_k = static_cast<__nv_bfloat16*>(a.cache);
@@ -574,41 +648,41 @@ cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
     const bool by_token = a.L <= nblk * a.N;
     p.nblk = by_token ? 0 : (int)nblk;
     p.groups = by_token ? a.L : (int)(nblk * a.N);
-    team = std::min<long long>(most, a.bs) > 4 * (32 / sg) ? kWarps : 1;
+    team = std::min<long long>(most, a.bs) > kWarpRows ? kWarps : 1;
     p.kv_tasks = (long long)a.B * p.groups * a.Hkv * (a.v ? 2 : 1);
+    if (p.kv_tasks >= (1LL << 31)) return cudaErrorInvalidValue;
     p.kv_blocks = (unsigned)(team == 1 ? (p.kv_tasks + kWarps - 1) / kWarps : p.kv_tasks);
   }
   // query heads of a task: up to kTaskBytes of rows, fewer when the tokens alone would not
   // fill the SMs' warps
+  const long long warps = (long long)sms * 3 * kWarps;
   if (a.Hq > 0) {
-    const int step = 32 / sg, passes = (a.Hq + step - 1) / step;
-    const long long warps = (long long)sms * 2 * kWarps;
+    const int step = 32 / qsg, passes = (a.Hq + step - 1) / step;
     const long long wanted = std::max((warps + tokens - 1) / tokens, ((long long)a.Hq * a.D * 2 + kTaskBytes - 1) / kTaskBytes);
     p.parts = (int)std::min<long long>(std::max<long long>(wanted, 1), passes);
     p.part_heads = (passes + p.parts - 1) / p.parts * step;
     p.parts = (a.Hq + p.part_heads - 1) / p.part_heads;
   }
   p.q_tasks = tokens * (p.parts + (a.scales == nullptr ? 1 : 0));
-  const long long grid = p.kv_blocks + (p.q_tasks + kWarps - 1) / kWarps;
-  if (grid >= (1LL << 31) || p.kv_tasks >= (1LL << 31) * kWarps) return cudaErrorInvalidValue;
+  // (quotients by per_rest: numbers below 2^32 / rest)
+  if (p.q_tasks >= (1LL << 31) || (long long)std::max(p.part_heads, a.Hkv) * p.q.rest * p.q.rest >= (1LL << 32) ||
+      (long long)a.Hkv * p.k.rest * p.k.rest >= (1LL << 32))
+    return cudaErrorInvalidValue;
+  // more tasks than the SMs hold at once, some of them absent tokens': the blocks sum the counts
+  // and stay for several tasks
+  p.summed = a.q_lens != nullptr && a.B <= kScan && p.q_tasks > warps;
+  const long long q_blocks = p.summed ? (long long)sms * 3 : (p.q_tasks + kWarps - 1) / kWarps;
+  const unsigned grid = (unsigned)(p.kv_blocks + q_blocks);
   // interleaved pairs within a lane's vector; whole vectors of halves; anything else
   const int rot = a.rot_dim == 0 || (a.interleaved && a.rot_offset % 2 == 0) ? kPair
                   : !a.interleaved && a.rot_offset % 8 == 0 && a.rot_dim % 16 == 0 && a.D <= 256 ? kSwap
                                                                                                 : kAny;
-  const unsigned g = (unsigned)grid;
-  if (a.D <= 64)
-    return rot == kPair   ? launch<8, 1, kPair>(p, team, g, a.stream)
-           : rot == kSwap ? launch<8, 1, kSwap>(p, team, g, a.stream)
-                          : launch<8, 1, kAny>(p, team, g, a.stream);
+  if (a.D <= 64) return launch<8, 1, 8, 1>(p, rot, team, grid, a.stream);
   if (a.D <= 128)
-    return rot == kPair   ? launch<16, 1, kPair>(p, team, g, a.stream)
-           : rot == kSwap ? launch<16, 1, kSwap>(p, team, g, a.stream)
-                          : launch<16, 1, kAny>(p, team, g, a.stream);
+    return narrow ? launch<16, 1, 8, 1>(p, rot, team, grid, a.stream) : launch<16, 1, 16, 1>(p, rot, team, grid, a.stream);
   if (a.D <= 256)
-    return rot == kPair   ? launch<32, 1, kPair>(p, team, g, a.stream)
-           : rot == kSwap ? launch<32, 1, kSwap>(p, team, g, a.stream)
-                          : launch<32, 1, kAny>(p, team, g, a.stream);
-  return rot == kPair ? launch<32, 3, kPair>(p, team, g, a.stream) : launch<32, 3, kAny>(p, team, g, a.stream);
+    return narrow ? launch<32, 1, 8, 1>(p, rot, team, grid, a.stream) : launch<32, 1, 32, 1>(p, rot, team, grid, a.stream);
+  return narrow ? launch<32, 3, 8, 1>(p, rot, team, grid, a.stream) : launch<32, 3, 32, 3>(p, rot, team, grid, a.stream);
 }
 
 }  // namespace dcp

@@ -39,34 +39,33 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs a) {
   }
   const int per_head = a.D / 8, vecs = a.Hkv * per_head;
   const long long pool = (long long)a.num_blocks * a.bs * a.Hkv * a.D;
-  for (int kind = 0; kind < 2; ++kind) {
-    void* out = kind == 0 ? a.out_k : a.out_v;
-    if (out == nullptr) continue;
-    const uint2* src = reinterpret_cast<const uint2*>(a.cache + kind * pool + ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D);
-    const uint8_t* scales = a.scales + ((long long)kind * a.num_blocks + blk) * a.Hkv;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + token * a.Hkv * a.D);
-    for (int c0 = lane; c0 < vecs; c0 += 32 * kAhead) {
-      uint2 u[kAhead];
-      float f[kAhead];
+  const int first = a.out_k != nullptr ? 0 : vecs, last = a.out_v != nullptr ? 2 * vecs : vecs;   // keys, then values
+  const long long cell = ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D;
+  for (int c0 = first + lane; c0 < last; c0 += 32 * kAhead) {
+    uint2 u[kAhead];
+    float f[kAhead];
 #pragma unroll
-      for (int m = 0; m < kAhead; ++m) {
-        const int c = min(c0 + 32 * m, vecs - 1);
-        u[m] = __ldcs(src + c);
-        f[m] = scale_factor(scales[c / per_head]);
+    for (int m = 0; m < kAhead; ++m) {
+      const int c = min(c0 + 32 * m, last - 1), kind = c >= vecs, v = kind ? c - vecs : c;
+      u[m] = __ldcs(reinterpret_cast<const uint2*>(a.cache + kind * pool + cell) + v);
+      f[m] = scale_factor(a.scales[((long long)kind * a.num_blocks + blk) * a.Hkv + v / per_head]);
+    }
+#pragma unroll
+    for (int m = 0; m < kAhead; ++m) {
+      const int c = c0 + 32 * m, kind = c >= vecs, v = kind ? c - vecs : c;
+      const uint32_t w[2] = {u[m].x, u[m].y};
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t pair;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+        const __nv_bfloat162 q = __floats2bfloat162_rn(x.x * f[m], x.y * f[m]);
+        o[k] = *reinterpret_cast<const uint32_t*>(&q);
       }
-#pragma unroll
-      for (int m = 0; m < kAhead; ++m) {
-        const uint32_t w[2] = {u[m].x, u[m].y};
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t pair;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pair));
-          const __nv_bfloat162 q = __floats2bfloat162_rn(v.x * f[m], v.y * f[m]);
-          o[k] = *reinterpret_cast<const uint32_t*>(&q);
-        }
-        if (c0 + 32 * m < vecs) __stcs(dst + c0 + 32 * m, make_uint4(o[0], o[1], o[2], o[3]));
+      if (c < last) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(kind ? a.out_v : a.out_k) + token * a.Hkv * a.D);
+        __stcs(dst + v, make_uint4(o[0], o[1], o[2], o[3]));
       }
     }
   }

@@ -45,7 +45,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
-constexpr int kTaskBytes = 8192;   // rows of a query task, at most (when tokens abound)
+// Rows of a query task, at most (when tokens abound).  Rows that are mostly copied take the larger one (latent
+// prompt rows 83 us; at 8192 88), rows that are worked on the smaller (prompt chunks 26 us; at 16384 34).
+constexpr int kTaskBytes = 8192, kCopyTaskBytes = 16384;
+constexpr int kKeptBytes = 96 * 1024;   // shared memory of a CTA for made rows
 constexpr int kWarpRows = 32;      // rows of a block that a warp takes alone
 
 enum Rot { kPair = 0, kSwap = 1, kAny = 2 };
@@ -66,6 +69,8 @@ struct Params {
   long long kv_tasks;
   int parts, part_heads;           // query heads of a token in parts
   long long q_tasks;
+  int kept_rows, kept_floats;      // rows that a group of lanes keeps in shared memory; floats of a warp for them
+  bool keys;                       // the token tasks store the bf16 cache's rows too
   bool summed;                     // tasks are numbered over the tokens that are there
   Window q, k;
 };
@@ -285,12 +290,14 @@ __device__ __forceinline__ int block_of(const AppendArgs& a, int b, int r, int j
   return -1;
 }
 
-// Heads [h0, h1) of a token: src + h D -> dst + h D, in turn over the warp's groups.
+// Heads [h0, h1) of a token at position pos: src + h D -> dst + h D, in turn over the warp's groups.
 template <int SG, int SLOTS, int kRot>
-__device__ __forceinline__ void head_rows(const Rows<SG, SLOTS, kRot>& rows, const __nv_bfloat16* src, __nv_bfloat16* dst,
-                                          int h0, int h1, int lane, int D) {
+__device__ __forceinline__ void head_rows(Rows<SG, SLOTS, kRot>& rows, const __nv_bfloat16* src, __nv_bfloat16* dst, int h0,
+                                          int h1, int lane, int D, long long pos, const float* weight) {
   constexpr int kStep = 32 / SG, kDeep = SLOTS > 1 ? 2 : kAhead;
   uint4 raw[kDeep][SLOTS];
+  rows.set_position(pos);
+  rows.set_weights(weight);
   const int mine = lane / SG;
   auto row = [&](int h) { return h < h1 ? src + (long long)h * D : nullptr; };
 #pragma unroll
@@ -321,8 +328,8 @@ __device__ __forceinline__ void copy_rest(const Window& w, const __nv_bfloat16* 
                });
 }
 
-// Task (token, part of its query heads, or (kKeys) behind them its keys and values into the bf16 cache).
-template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot, bool kKeys>
+// Task (token, part of its query heads, or (with `keys`) behind them its keys and values into the bf16 cache).
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
 __device__ __forceinline__ void token_task(const Params& p, int b, int i, int part, int lane, float* scratch) {
   const NormAppendArgs& a = p.a;
   bool bad;
@@ -331,45 +338,39 @@ __device__ __forceinline__ void token_task(const Params& p, int b, int i, int pa
   if (i >= n) return;
   const long long base = (long long)a.seq_lens[b] - n;
   const int row16 = a.D / 8;
-  if (!kKeys || part < p.parts) {
+  if (part < p.parts) {
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_batch + i * a.q_token;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + ((long long)b * a.L + i) * a.Hq * a.D;
     const int h0 = part * p.part_heads, h1 = min(a.Hq, h0 + p.part_heads);
     if (p.q.count > 0) {
       Rows<QSG, QSLOTS, kRot> rows(a, lane, scratch, p.q.first, p.q.count);
-      rows.set_position(position_of(a, b, i, base));
-      rows.set_weights(a.q_weight);
-      head_rows(rows, src, dst, h0, h1, lane, a.D);
+      head_rows(rows, src, dst, h0, h1, lane, a.D, position_of(a, b, i, base), a.q_weight);
     }
     copy_rest(p.q, src, dst, h0, h1, row16, lane);
     return;
   }
-  if constexpr (kKeys) {
-    const long long t = base + i;
-    const int r = (int)((t / a.I) % a.N);
-    const long long j = (t / ((long long)a.I * a.N)) * a.I + t % a.I;
-    const int blk = block_of(a, b, r, (int)(j / a.bs), lane == 0);
-    if (blk < 0) return;
-    const long long cell = ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.k) + b * a.k_batch + i * a.k_token;
-    if (p.k.count > 0) {
-      Rows<SG, SLOTS, kRot> rows(a, lane, scratch, p.k.first, p.k.count);
-      rows.set_position(position_of(a, b, i, base));
-      rows.set_weights(a.k_weight);
-      head_rows(rows, src, p.pool_k + cell, 0, a.Hkv, lane, a.D);
-    }
-    copy_rest(p.k, src, p.pool_k + cell, 0, a.Hkv, row16, lane);
-    if (a.v != nullptr)
-      copy_vectors(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + b * a.v_batch + i * a.v_token),
-                   reinterpret_cast<uint4*>(p.pool_v + cell), a.Hkv * row16, lane, [](int c) { return c; });
+  const long long t = base + i;
+  const int r = (int)((t / a.I) % a.N);
+  const long long j = (t / ((long long)a.I * a.N)) * a.I + t % a.I;
+  const int blk = block_of(a, b, r, (int)(j / a.bs), lane == 0);
+  if (blk < 0) return;
+  const long long cell = ((long long)blk * a.bs + j % a.bs) * a.Hkv * a.D;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.k) + b * a.k_batch + i * a.k_token;
+  if (p.k.count > 0) {
+    Rows<SG, SLOTS, kRot> rows(a, lane, scratch, p.k.first, p.k.count);
+    head_rows(rows, src, p.pool_k + cell, 0, a.Hkv, lane, a.D, position_of(a, b, i, base), a.k_weight);
   }
+  copy_rest(p.k, src, p.pool_k + cell, 0, a.Hkv, row16, lane);
+  if (a.v != nullptr)
+    copy_vectors(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + b * a.v_batch + i * a.v_token),
+                 reinterpret_cast<uint4*>(p.pool_v + cell), a.Hkv * row16, lane, [](int c) { return c; });
 }
 
 // The token tasks of blocks [0, blocks), a warp each in turn.
-template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot, bool kKeys>
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
 __device__ __forceinline__ void token_tasks(const Params& p, int* ends, unsigned block, unsigned blocks, float* scratch) {
   const NormAppendArgs& a = p.a;
-  const unsigned parts = p.parts + (kKeys ? 1 : 0);
+  const unsigned parts = p.parts + (p.keys ? 1 : 0);
   long long tasks = p.q_tasks;
   if (p.summed) {
     sum_counts<kThreads>(a, ends);
@@ -380,16 +381,20 @@ __device__ __forceinline__ void token_tasks(const Params& p, int* ends, unsigned
     const unsigned token = (unsigned)task / parts, part = (unsigned)task - token * parts;
     int b = (int)(token / (unsigned)a.L), i = (int)(token % (unsigned)a.L);
     if (p.summed) b = find_token(ends, a.B, token, &i);
-    token_task<SG, SLOTS, QSG, QSLOTS, kRot, kKeys>(p, b, i, (int)part, threadIdx.x & 31, scratch);
+    token_task<SG, SLOTS, QSG, QSLOTS, kRot>(p, b, i, (int)part, threadIdx.x & 31, scratch);
   }
 }
 
+// Queries, and (with `keys`) the bf16 cache's rows.  Beside kv8_rows_kernel (`beside`) it starts while that
+// one runs and ends behind it.
 template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
-__global__ void __launch_bounds__(kThreads, SLOTS == 1 ? 3 : 2) append_norm_kernel(const Params p) {
-  extern __shared__ float scratch[];
+__global__ void __launch_bounds__(kThreads, SLOTS == 1 ? 3 : 2) token_kernel(const Params p, bool beside) {
+  extern __shared__ float4 scratch[];
   __shared__ int ends[kScan];
-  token_tasks<SG, SLOTS, QSG, QSLOTS, kRot, true>(p, ends, blockIdx.x, gridDim.x,
-                                                  scratch + (threadIdx.x >> 5) * scratch_floats(kRot, QSG < SG ? QSG : SG, p.a.rot_dim));
+  token_tasks<SG, SLOTS, QSG, QSLOTS, kRot>(p, ends, blockIdx.x, gridDim.x,
+                                            reinterpret_cast<float*>(scratch) +
+                                                (threadIdx.x >> 5) * scratch_floats(kRot, QSG < SG ? QSG : SG, p.a.rot_dim));
+  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Codes of a vector: y / 2^e to nearest (y by = 2^-e), NaN where y is not finite.
@@ -437,9 +442,9 @@ __device__ __forceinline__ int exponent_for(float most) {
 // The new rows of one block, KV head and K or V, by a team of kTeam warps.
 template <int SG, int SLOTS, int kRot, int kTeam>
 __device__ __forceinline__ void block_rows(const Params& p, long long task, int team_warp, int lane, float* scratch,
-                                           float* shared) {
+                                           float* shared, float4* kept) {
   constexpr int kGroups = kTeam * 32 / SG;                    // rows at a time
-  constexpr int kHeld = kTeam == 1 ? 1 : SLOTS > 1 ? 2 : 4;   // rows of a group in registers
+  constexpr int kLoads = SLOTS > 1 ? 2 : 4;                   // rows of a group whose loads are in flight
   const NormAppendArgs& a = p.a;
   const int kinds = a.v != nullptr ? 2 : 1;
   const bool values = kinds == 2 && (task & 1);
@@ -485,40 +490,40 @@ __device__ __forceinline__ void block_rows(const Params& p, long long task, int 
       rows.turn(y);
     }
   };
-  float y[kHeld][SLOTS][8], most = 0.f;
-  {
-    uint4 raw[kHeld][SLOTS];
+  // A lane keeps its part of the made rows in shared memory (its own alone: two float4 a vector, lanes side by
+  // side), as far as there is room; rows behind that are read and made again.
+  const int room = p.kept_rows;
+  auto keep = [&](int step, int m, int half) -> float4& { return kept[((step * SLOTS + m) * 2 + half) * 32 + lane]; };
+  float most = 0.f;
+  uint4 raw[kLoads][SLOTS];
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) load(k * kGroups + group, raw[k]);
-    if (!values) rows.set_weights(a.k_weight);
+  for (int m = 0; m < kLoads; ++m) load(m * kGroups + group, raw[m]);
+  if (!values) rows.set_weights(a.k_weight);
+  for (int k0 = 0, step = 0; k0 < count; k0 += kLoads * kGroups) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      if (k > 0 && k * kGroups >= count) break;
-      make(k * kGroups + group, raw[k], y[k]);
+    for (int q = 0; q < kLoads; ++q, ++step) {
+      const int k = k0 + q * kGroups;
+      if (k >= count) break;
+      float y[SLOTS][8];
+      make(k + group, raw[q], y);
+      load(k + kLoads * kGroups + group, raw[q]);
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = fabsf(y[m][e]);
+          if (x <= FLT_MAX) most = fmaxf(most, x);
+        }
+        if (step < room) {
+          keep(step, m, 0) = make_float4(y[m][0], y[m][1], y[m][2], y[m][3]);
+          keep(step, m, 1) = make_float4(y[m][4], y[m][5], y[m][6], y[m][7]);
+        }
+      }
     }
   }
   const int blk = block_of(a, b, r, jb, lane == 0 && team_warp == 0);
   const long long scale_at = ((values ? (long long)a.num_blocks : 0) + max(blk, 0)) * a.Hkv + h;
   const int old = (int)a.scales[scale_at] - 127;
-  auto largest = [&](const float (&v)[SLOTS][8]) {
-#pragma unroll
-    for (int m = 0; m < SLOTS; ++m)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = fabsf(v[m][e]);
-        if (x <= FLT_MAX) most = fmaxf(most, x);
-      }
-  };
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    if (k * kGroups < count) largest(y[k]);
-  for (int k = kHeld * kGroups; k < count; k += kGroups) {    // rows that the registers do not hold
-    uint4 raw[SLOTS];
-    float v[SLOTS][8];
-    load(k + group, raw);
-    make(k + group, raw, v);
-    largest(v);
-  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   if constexpr (kTeam > 1) {
@@ -561,52 +566,95 @@ __device__ __forceinline__ void block_rows(const Params& p, long long task, int 
       if (rows.sl + SG * m < rows.vecs)
         *reinterpret_cast<uint2*>(pool + (before + k) * pitch + (rows.sl + SG * m) * 8) = codes_of(v[m], by);
   };
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) store(k * kGroups + group, y[k]);
-  for (int k = kHeld * kGroups; k < count; k += kGroups) {
-    uint4 raw[SLOTS];
+  for (int k = 0, step = 0; k < count; k += kGroups, ++step) {
     float v[SLOTS][8];
-    load(k + group, raw);
-    make(k + group, raw, v);
+    if (step < room) {
+#pragma unroll
+      for (int m = 0; m < SLOTS; ++m) {
+        const float4 lo = keep(step, m, 0), up = keep(step, m, 1);
+        v[m][0] = lo.x, v[m][1] = lo.y, v[m][2] = lo.z, v[m][3] = lo.w;
+        v[m][4] = up.x, v[m][5] = up.y, v[m][6] = up.z, v[m][7] = up.w;
+      }
+    } else {
+      load(k + group, raw[0]);
+      make(k + group, raw[0], v);
+    }
     store(k + group, v);
   }
 }
 
-template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot, int kTeam>
-__global__ void __launch_bounds__(kThreads, kTeam == 1 && SLOTS == 1 ? 3 : 2) kv8_append_kernel(const Params p) {
-  extern __shared__ float scratch[];
+// Few rows a block: a warp a block's rows, and the queries behind them in the same launch.
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
+__global__ void __launch_bounds__(kThreads, SLOTS == 1 ? 3 : 2) kv8_step_kernel(const Params p) {
+  extern __shared__ float4 scratch[];
   __shared__ int ends[kScan];
-  __shared__ float shared[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* mine = scratch + warp * scratch_floats(kRot, QSG < SG ? QSG : SG, p.a.rot_dim);
+  float* kept = reinterpret_cast<float*>(scratch);             // (16-byte aligned: first)
+  float* mine = kept + kWarps * p.kept_floats + warp * scratch_floats(kRot, QSG < SG ? QSG : SG, p.a.rot_dim);
   if (blockIdx.x < p.kv_blocks) {
-    const long long task = kTeam == 1 ? (long long)blockIdx.x * kWarps + warp : (long long)blockIdx.x;
-    if (task < p.kv_tasks) block_rows<SG, SLOTS, kRot, kTeam>(p, task, kTeam == 1 ? 0 : warp, lane, mine, shared);
+    const long long task = (long long)blockIdx.x * kWarps + warp;
+    if (task < p.kv_tasks)
+      block_rows<SG, SLOTS, kRot, 1>(p, task, 0, lane, mine, nullptr, reinterpret_cast<float4*>(kept + warp * p.kept_floats));
   } else {
-    token_tasks<SG, SLOTS, QSG, QSLOTS, kRot, false>(p, ends, blockIdx.x - p.kv_blocks, gridDim.x - p.kv_blocks, mine);
+    token_tasks<SG, SLOTS, QSG, QSLOTS, kRot>(p, ends, blockIdx.x - p.kv_blocks, gridDim.x - p.kv_blocks, mine);
   }
 }
 
-template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
-cudaError_t launch_rot(const Params& p, int team, unsigned grid, cudaStream_t stream) {
-  const size_t smem = (size_t)kWarps * scratch_floats(kRot, std::min(QSG, SG), p.a.rot_dim) * sizeof(float);
-  void (*kernel)(Params) = p.a.scales == nullptr ? append_norm_kernel<SG, SLOTS, QSG, QSLOTS, kRot>
-                           : team == 1           ? kv8_append_kernel<SG, SLOTS, QSG, QSLOTS, kRot, 1>
-                                                 : kv8_append_kernel<SG, SLOTS, QSG, QSLOTS, kRot, kWarps>;
+// Many rows a block: a CTA a block's rows.  The queries' kernel runs beside it.
+template <int SG, int SLOTS, int kRot, int kTeam>
+__global__ void __launch_bounds__(32 * kTeam, kTeam == 16 ? 1 : 2) kv8_rows_kernel(const Params p) {
+  extern __shared__ float4 scratch[];
+  __shared__ float shared[kTeam];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* kept = reinterpret_cast<float*>(scratch);
+  block_rows<SG, SLOTS, kRot, kTeam>(p, blockIdx.x, warp, lane, kept + kTeam * p.kept_floats + warp * scratch_floats(kRot, SG, p.a.rot_dim),
+                                     shared, reinterpret_cast<float4*>(kept + warp * p.kept_floats));
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t start(Kernel kernel, unsigned grid, int threads, size_t smem, cudaStream_t stream, bool beside, Args... args) {
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int SG, int SLOTS, int QSG, int QSLOTS, int kRot>
+cudaError_t launch_rot(const Params& p, int team, unsigned q_blocks, cudaStream_t stream) {
+  const size_t turning = scratch_floats(kRot, SG, p.a.rot_dim), q_turning = scratch_floats(kRot, std::min(QSG, SG), p.a.rot_dim);
+  const size_t q_smem = kWarps * q_turning * sizeof(float);
+  if (p.a.scales == nullptr)
+    return start(token_kernel<SG, SLOTS, QSG, QSLOTS, kRot>, q_blocks, kThreads, q_smem, stream, false, p, false);
+  if (team == 1)
+    return start(kv8_step_kernel<SG, SLOTS, QSG, QSLOTS, kRot>, p.kv_blocks + q_blocks, kThreads,
+                 kWarps * (q_turning + p.kept_floats) * sizeof(float), stream, false, p);
+  constexpr int kTeam = SLOTS == 1 ? 8 : 16;
+  const cudaError_t e = start(kv8_rows_kernel<SG, SLOTS, kRot, kTeam>, p.kv_blocks, 32 * kTeam,
+                              kTeam * (turning + p.kept_floats) * sizeof(float), stream, false, p);
+  if (e != cudaSuccess || q_blocks == 0) return e;
+  // (without keys: the instance of the queries' own shape)
+  return start(token_kernel<QSG, QSLOTS, QSG, QSLOTS, kRot>, q_blocks, kThreads, kWarps * scratch_floats(kRot, QSG, p.a.rot_dim) * sizeof(float),
+               stream, true, p, true);
 }
 
 template <int SG, int SLOTS, int QSG, int QSLOTS>
-cudaError_t launch(const Params& p, int rot, int team, unsigned grid, cudaStream_t stream) {
-  if (rot == kPair) return launch_rot<SG, SLOTS, QSG, QSLOTS, kPair>(p, team, grid, stream);
+cudaError_t launch(const Params& p, int rot, int team, unsigned q_blocks, cudaStream_t stream) {
+  if (rot == kPair) return launch_rot<SG, SLOTS, QSG, QSLOTS, kPair>(p, team, q_blocks, stream);
   if constexpr (SLOTS == 1)
-    if (rot == kSwap) return launch_rot<SG, SLOTS, QSG, QSLOTS, kSwap>(p, team, grid, stream);
-  return launch_rot<SG, SLOTS, QSG, QSLOTS, kAny>(p, team, grid, stream);
+    if (rot == kSwap) return launch_rot<SG, SLOTS, QSG, QSLOTS, kSwap>(p, team, q_blocks, stream);
+  return launch_rot<SG, SLOTS, QSG, QSLOTS, kAny>(p, team, q_blocks, stream);
 }
 
 Window window_of(const NormAppendArgs& a, bool normed) {
@@ -648,22 +696,31 @@ cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
     const bool by_token = a.L <= nblk * a.N;
     p.nblk = by_token ? 0 : (int)nblk;
     p.groups = by_token ? a.L : (int)(nblk * a.N);
-    team = std::min<long long>(most, a.bs) > kWarpRows ? kWarps : 1;
+    // long rows: 16 warps (and all of an SM's registers and memory); else 8
+    team = std::min<long long>(most, a.bs) <= kWarpRows ? 1 : a.D <= 256 ? 8 : 16;
+    // made rows that a warp's groups of lanes keep, up to kKeptBytes of a CTA
+    const int cta = team == 1 ? kWarps : team, at_once = team * 32 / sg, slots = a.D <= 256 ? 1 : 3;
+    const long long steps = (std::min<long long>(most, a.bs) + at_once - 1) / at_once;
+    p.kept_rows = (int)std::min<long long>(steps, (team == 16 ? kKeptBytes + kKeptBytes / 2 : kKeptBytes) / (cta * 32 * slots * 32));
+    p.kept_floats = p.kept_rows * 32 * slots * 8;
     p.kv_tasks = (long long)a.B * p.groups * a.Hkv * (a.v ? 2 : 1);
     if (p.kv_tasks >= (1LL << 31)) return cudaErrorInvalidValue;
-    p.kv_blocks = (unsigned)(team == 1 ? (p.kv_tasks + kWarps - 1) / kWarps : p.kv_tasks);
+    p.kv_blocks = (unsigned)(team == 1 ? (p.kv_tasks + cta - 1) / cta : p.kv_tasks);
   }
   // query heads of a task: up to kTaskBytes of rows, fewer when the tokens alone would not
   // fill the SMs' warps
-  const long long warps = (long long)sms * 3 * kWarps;
+  const int resident = a.D <= 256 || (team > 1 && narrow) ? 3 : 2;
+  const long long warps = (long long)sms * resident * kWarps;
   if (a.Hq > 0) {
+    const int task_bytes = 2 * p.q.rest > a.D / 8 ? kCopyTaskBytes : kTaskBytes;
     const int step = 32 / qsg, passes = (a.Hq + step - 1) / step;
-    const long long wanted = std::max((warps + tokens - 1) / tokens, ((long long)a.Hq * a.D * 2 + kTaskBytes - 1) / kTaskBytes);
+    const long long wanted = std::max((warps + tokens - 1) / tokens, ((long long)a.Hq * a.D * 2 + task_bytes - 1) / task_bytes);
     p.parts = (int)std::min<long long>(std::max<long long>(wanted, 1), passes);
     p.part_heads = (passes + p.parts - 1) / p.parts * step;
     p.parts = (a.Hq + p.part_heads - 1) / p.part_heads;
   }
-  p.q_tasks = tokens * (p.parts + (a.scales == nullptr ? 1 : 0));
+  p.keys = a.scales == nullptr;
+  p.q_tasks = tokens * (p.parts + (p.keys ? 1 : 0));
   // (quotients by per_rest: numbers below 2^32 / rest)
   if (p.q_tasks >= (1LL << 31) || (long long)std::max(p.part_heads, a.Hkv) * p.q.rest * p.q.rest >= (1LL << 32) ||
       (long long)a.Hkv * p.k.rest * p.k.rest >= (1LL << 32))
@@ -671,18 +728,17 @@ cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
   // more tasks than the SMs hold at once, some of them absent tokens': the blocks sum the counts
   // and stay for several tasks
   p.summed = a.q_lens != nullptr && a.B <= kScan && p.q_tasks > warps;
-  const long long q_blocks = p.summed ? (long long)sms * 3 : (p.q_tasks + kWarps - 1) / kWarps;
-  const unsigned grid = (unsigned)(p.kv_blocks + q_blocks);
+  const long long q_blocks = p.summed ? (long long)sms * resident : (p.q_tasks + kWarps - 1) / kWarps;
   // interleaved pairs within a lane's vector; whole vectors of halves; anything else
   const int rot = a.rot_dim == 0 || (a.interleaved && a.rot_offset % 2 == 0) ? kPair
                   : !a.interleaved && a.rot_offset % 8 == 0 && a.rot_dim % 16 == 0 && a.D <= 256 ? kSwap
                                                                                                 : kAny;
-  if (a.D <= 64) return launch<8, 1, 8, 1>(p, rot, team, grid, a.stream);
+  if (a.D <= 64) return launch<8, 1, 8, 1>(p, rot, team, (unsigned)q_blocks, a.stream);
   if (a.D <= 128)
-    return narrow ? launch<16, 1, 8, 1>(p, rot, team, grid, a.stream) : launch<16, 1, 16, 1>(p, rot, team, grid, a.stream);
+    return narrow ? launch<16, 1, 8, 1>(p, rot, team, (unsigned)q_blocks, a.stream) : launch<16, 1, 16, 1>(p, rot, team, (unsigned)q_blocks, a.stream);
   if (a.D <= 256)
-    return narrow ? launch<32, 1, 8, 1>(p, rot, team, grid, a.stream) : launch<32, 1, 32, 1>(p, rot, team, grid, a.stream);
-  return narrow ? launch<32, 3, 8, 1>(p, rot, team, grid, a.stream) : launch<32, 3, 32, 3>(p, rot, team, grid, a.stream);
+    return narrow ? launch<32, 1, 8, 1>(p, rot, team, (unsigned)q_blocks, a.stream) : launch<32, 1, 32, 1>(p, rot, team, (unsigned)q_blocks, a.stream);
+  return narrow ? launch<32, 3, 8, 1>(p, rot, team, (unsigned)q_blocks, a.stream) : launch<32, 3, 32, 3>(p, rot, team, (unsigned)q_blocks, a.stream);
 }
 
 }  // namespace dcp

@@ -433,8 +433,11 @@ def _append_args(call, kind, new_k, new_v, kv_cache, scales, block_tables, seq_l
     if (new_v is not None) != gqa:
         _refuse(call, "GQA takes new_v, MLA none")
     device = torch.cuda.current_device()
-    _check_tensors(call, kv_cache.dtype if scales is not None else _bf16, device, kv_cache)
-    _check_tensors(call, _bf16, device, None if q_out is q else q_out)
+    if scales is None:
+        _check_tensors(call, _bf16, device, kv_cache, None if q_out is q else q_out)
+    else:
+        _check_kv8(call, device, kind, kv_cache, scales)
+        _check_tensors(call, _bf16, device, None if q_out is q else q_out)
     _check_tensors(call, _int32, device, block_tables, pos_offsets)
     _check_lens(call, B, device, seq_lens, q_lens)
     rotation = None, None
@@ -506,22 +509,23 @@ def _norm_desc(call, device, q_weight, k_weight, eps):
     """The norms' descriptor (None: none); the weights are fp32 [norm_dim]."""
     if q_weight is None and k_weight is None:
         return None
-    _check_tensors(call, torch.float32, device, q_weight, k_weight)
-    dims = {w.numel() for w in (q_weight, k_weight) if w is not None}
-    if len(dims) != 1 or any(w is not None and w.dim() != 1 for w in (q_weight, k_weight)):
-        _refuse(call, "norm weights are [norm_dim], both of one length")
-    return DcpNormDesc(dims.pop(), eps, None if q_weight is None else q_weight.data_ptr(),
+    shape = (k_weight if q_weight is None else q_weight).shape
+    for w in (q_weight, k_weight):
+        if w is not None and (w.shape != shape or len(shape) != 1 or w.dtype is not torch.float32
+                              or w.get_device() != device or not w.is_contiguous()):
+            _refuse(call, "norm weights are contiguous float32 [norm_dim] on the current device, both of one length")
+    return DcpNormDesc(shape[0], eps, None if q_weight is None else q_weight.data_ptr(),
                        None if k_weight is None else k_weight.data_ptr())
 
 
 def _check_kv8(call, device, kind, kv_cache, kv_scales):
     """The codes and scales of an 8-bit cache."""
-    for t, types, what in ((kv_cache, _codes, "cache is float8_e4m3fn"), (kv_scales, _scales, "scales are float8_e8m0fnu")):
-        if t.dtype not in types or t.get_device() != device or not t.is_contiguous():
-            _refuse(call, f"the {what} or uint8, contiguous on the current device")
+    if kv_cache.dtype not in _codes or kv_cache.get_device() != device or not kv_cache.is_contiguous():
+        _refuse(call, "the cache is float8_e4m3fn or uint8, contiguous on the current device")
+    if kv_scales.dtype not in _scales or kv_scales.get_device() != device or not kv_scales.is_contiguous():
+        _refuse(call, "the scales are float8_e8m0fnu or uint8, contiguous on the current device")
     shape = kv_cache.shape
-    want = (2, shape[1], shape[3]) if kind == DCP_ATTN_GQA else (shape[0],)
-    if kv_scales.shape != want:
+    if kv_scales.shape != ((2, shape[1], shape[3]) if kind == DCP_ATTN_GQA else (shape[0],)):
         _refuse(call, "kv_scales is [2][blocks][Hkv] (GQA) or [blocks] (MLA)")
 
 
@@ -554,7 +558,6 @@ def dcp_kv8_append(kind, new_k, new_v, kv_cache, kv_scales, block_tables, seq_le
     call = "dcp_kv8_append"
     shape, rows, q_out, device = _append_args(call, kind, new_k, new_v, kv_cache, kv_scales, block_tables, seq_lens,
                                               dcp_size, rope, q, q_out, q_lens, pos_offsets, stream)
-    _check_kv8(call, device, KINDS.get(kind, kind), kv_cache, kv_scales)
     code = _lib.dcp_kv8_append(*shape, _norm_desc(call, device, q_weight, k_weight, eps), *rows, kv_cache.data_ptr(),
                                kv_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), dcp_size, interleave,
                                _stream(stream, device))

@@ -19,21 +19,40 @@
 //                    is the sum of two e4m3 values (4 bits each) once its row is
 //                    scaled to at most 256, so q.k8 takes two products on codes
 //                    as they are: no key is converted.
-//   O^T += V^T P^T   kind::f16.  P in e4m3 would need three terms and their
-//                    conversion for every row; instead the values of a tile turn
-//                    into fp16 (exact) on the way, once for all rows, by four
-//                    warps of their own.
-// Roles (768 threads): warp 0 TMA producer (K and V tiles of 128 keys in rings of
-// their own, the tile's scale bytes beside them), 1 QK issuer, 2 PV issuer, 3
-// scheduler, 4-7 query split and value conversion, 8-23 softmax and epilogue (four
-// per TMEM lane quadrant, a thread owning one key and a quarter of the rows).
+//   O^T += V^T P^T   kind::f16.  P in e4m3 would need three terms, and rows whose
+//                    weights lie far below the largest (a sink beside a hundred
+//                    thousand others) more; instead a tile's values turn into fp16
+//                    (exact), once for all rows: ldmatrix transposes their bytes
+//                    (keys x dims -> dims x keys), and they go to tensor memory as
+//                    the A operand.  Through shared memory (values written as fp16
+//                    and read by the MMA) 256 requests took 1,300 us, so 1,140.
+// Roles: warp 0 TMA producer (K and V tiles of 128 keys in rings of their own, the
+// tile's scale bytes beside them), 1 QK issuer, 2 PV issuer, 3 scheduler, 4-7 query
+// split and value conversion, 8 and up softmax and epilogue (a thread owns one key
+// of the tile and 16 rows).  16 rows: 4 softmax warps and three CTAs an SM, 32: 8
+// and two, 64: 16 and one; a CTA that starts or ends a unit leaves the SM to the
+// others (one CTA an SM with 16 softmax warps: 1,546 us, two with 8: 906, three: 791).
 //
 // Work.  A unit is (request, shard, KV head, row tile); its tiles and a constant
-// for its start and end are its weight.  One CTA per SM takes an equal share of
-// the summed weight, whatever the lengths: units that a border cuts leave partial
-// rows in the workspace (two at most per CTA), joined by kv8_join_kernel.  CTAs
-// go from unit to unit without a stop: the scheduler warp reads lengths and
-// tables ahead and publishes unit descriptors, O has two TMEM buffers.
+// for its start and end are its weight.  A CTA takes an equal share of the summed
+// weight, whatever the lengths: units that a border cuts leave partial rows in the
+// workspace (two at most per CTA), joined by kv8_join_kernel.  CTAs go from unit
+// to unit without a stop: the scheduler warp reads lengths and tables ahead and
+// publishes unit descriptors, O has two TMEM buffers.
+//
+// Bound: HBM (128 bytes of a key and of a value a token and KV head; TMA fetches
+// exactly these: with 256-byte L2 fetches the next head's row came along, 1.39 of
+// the bytes and 1,142 against 906 us).  Measured (GB300, in a graph, with the merge):
+//   256 requests of 8,192 - 32,768 tokens, 64 + 4 heads (4.66 GB)  764-786 us, 5.9-6.1 TB/s
+//   one request of 200,000 tokens, 64 + 8 heads (410 MB)            93-99 us, 4.1-4.4 TB/s
+//   33 requests, 4 ragged queries, blocks of 16 (370 MB)            111 us, 3.3 TB/s
+//   one request of 1,024 tokens, 8 + 2 heads of 64                  15 us
+// What is left of the first: unit ends (about 15,000 cycles, the others' time on the
+// SM), of the second and third the first tiles (code fetched behind the rings' first
+// copies) and the last CTAs.  Code counts: all roles share the instruction cache, and
+// compact waits, ragged tiles masked by a loop and the rest of it took 139 to 96 KB
+// and the ragged queries from 181 to 124 us.  A unit of nothing that warms the cache
+// up before the first copies measured 1 to 5% slower.
 //
 // Every wait is bounded; when one runs out the CTA records DCP_ERR_TIMEOUT, goes
 // through its remaining units without work and leaves zeros and -inf for them.
@@ -63,7 +82,8 @@ constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of 
 constexpr float kNoRef = 1e30f;                // -R of a row that has seen no key: any y + kNoRef is above kTop, -inf stays
 constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;
 constexpr int kMaxCols = 64;
-constexpr int kUnitCost = 2;                   // start and end of a unit, in tiles
+// Start and end of a unit, in tiles (1, 2, 4: the ragged queries 124, 110, 109 us, 256 long requests 769, 765, 769)
+constexpr int kUnitCost = 2;
 constexpr uint32_t kWCols = kNt / 2;           // TMEM columns of an fp16 value tile
 
 struct Params {
@@ -1037,6 +1057,7 @@ template <int NCOL, int D>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, int grid, cudaStream_t stream) {
   constexpr size_t smem = smem_bytes<NCOL, D>();
   static_assert(smem <= Cfg<NCOL, D>::kSmemLimit && stages<NCOL, D>(true) >= 1, "shared memory");
+  static_assert(stages<NCOL, D>(false) + 2 <= kMeta, "a tile's scale bytes are read before their slot is used again");
   // the register split assumes the launch count (setmaxnreg.inc would wait for registers that do not exist)
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kv8_gqa_kernel<NCOL, D>);

@@ -4,7 +4,9 @@
 // Bound by HBM: one byte read and two written per value.  A warp takes a token
 // and walks its row (every KV head, keys then values), a lane 8 codes at a time;
 // the token's table entry and its scales come first, the codes of up to kAhead
-// vectors of a lane together.
+// vectors of a lane together.  Measured (GB300, in a graph): 29,000 rows of 2 x 4
+// heads of 128 (90 MB) 24 us, 3.7 TB/s; 2,700 latent rows 4.4 us.  Keys and values
+// in one loop: 29 to 24 us; two tokens a warp: 27.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

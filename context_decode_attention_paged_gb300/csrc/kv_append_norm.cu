@@ -24,10 +24,21 @@
 // Pairs of the interleaved layout lie in a lane; in the half layout the partner
 // vector is another lane's (a shuffle); any other rotated part goes through
 // shared memory.  Queries: a warp takes a token's heads in turn, its angles and
-// weights in registers.  Rows of the 8-bit cache: a team (a warp where a block
-// gets few rows, else a CTA) takes all new rows of one block and KV head: norm,
-// rotation and maximum, then the codes; rows that its registers do not hold are
-// read (from L2) and turned again.
+// weights in registers; vectors that neither norm nor rotation touch are copied.
+// Rows of the 8-bit cache: a team takes all new rows of one block and KV head: norm,
+// rotation and maximum, then the codes from what it kept in shared memory (rows that
+// do not fit are read, from L2, and made again).  Up to kWarpRows rows a team is a
+// warp, in one launch with the queries; more take a CTA, and the queries' kernel runs
+// beside that one (a programmatic launch; one launch for both held the queries to the
+// rows' registers).
+//
+// Bound: HBM and, for prompts, instruction issue (about 190 a pass of two rows of
+// 128); for a decode step the launch and dependent loads.  Measured (GB300, in a
+// graph; 64 + 4 heads of 128 unless said): 64 tokens 5.5 us into either cache; 2,154
+// tokens of ragged prompts into the bf16 cache 26 us (79 MB, 3.1 TB/s), into the
+// 8-bit one 31; 400 drafted tokens of 40 + 8 heads 11; 1,352 latent rows with 128
+// query heads of 576 84 (401 MB, 4.8 TB/s).  Packed two-value arithmetic and a
+// fourth CTA an SM gained nothing (26.5 and 28.8 us for 26).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -49,7 +60,7 @@ constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
 // prompt rows 83 us; at 8192 88), rows that are worked on the smaller (prompt chunks 26 us; at 16384 34).
 constexpr int kTaskBytes = 8192, kCopyTaskBytes = 16384;
 constexpr int kKeptBytes = 96 * 1024;   // shared memory of a CTA for made rows
-constexpr int kWarpRows = 32;      // rows of a block that a warp takes alone
+constexpr int kWarpRows = 32;      // rows of a block that a warp takes alone (drafted tokens, 12 rows: 11 us; by a CTA 22)
 
 enum Rot { kPair = 0, kSwap = 1, kAny = 2 };
 

@@ -535,7 +535,9 @@ DCP_API dcp_status_t dcp_kv8_read(const dcp_attn_desc_t* d, const void* kv8_cach
  * dcp_decode_attn_workspace_size. */
 DCP_API size_t dcp_kv8_decode_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dcp_size);
 
-/* dcp_decode_attn over the 8-bit cache.  Query i < n_b of request b (n_b = q_lens[b], or
+/* dcp_decode_attn over the 8-bit cache.  GQA with heads of 64 or 128 dims and the block sizes
+ * of the decode kernel runs on the tensor cores, every other shape, MLA among them, on the
+ * CUDA cores (dcp_kv8_decode_attn_kernel_kind tells).  Query i < n_b of request b (n_b = q_lens[b], or
  * q_len where q_lens is NULL) sits at position S_b - n_b + i and sees the positions up to
  * its own.  partial_out fp32 [dcp][B][Lq][Hq][Dv] and lse fp32 [dcp][B][Lq][Hq] per shard, for
  * dcp_merge.  A row that sees no key of a shard, and every row i >= n_b, gives partial_out = 0
@@ -543,7 +545,8 @@ DCP_API size_t dcp_kv8_decode_attn_workspace_size(const dcp_attn_desc_t* d, int3
  * Keys and values that a row does not see never reach it, whatever they hold.  A key or query
  * that is not finite makes the rows that see it NaN; a value code of NaN makes that entry NaN
  * in the rows that see it, except where a shard weighs 0 in fp32 against the row's others.
- *  kv8_scales    any bytes; the accuracy holds for scales within 2^-40 to 2^40
+ *  kv8_scales    any bytes; the accuracy holds for scales within 2^-40 to 2^40 (255 makes
+ *                the rows that see its block NaN)
  *  q_lens        int32 [B], each in [0, q_len] and <= S_b, or NULL; other values set
  *                DCP_ERR_BOUNDS and the request's rows are 0 and -inf
  *  workspace     as in dcp_tree_attn

@@ -425,7 +425,7 @@ def _attn_buffers(call, size_of, desc, dcp_size, shape, on, device, partial_out,
 
 def _append_args(call, kind, new_k, new_v, kv_cache, scales, block_tables, seq_lens, dcp_size, rope, q, q_out, q_lens,
                  pos_offsets, stream):
-    """The checked arguments of an append: (desc, rope desc, rope steps), (new_k .. q_lens pointers), q_out, device."""
+    """The checked arguments of an append with norms or into the 8-bit cache: (desc, rope desc, rope steps), (new_k .. q_lens pointers), q_out, device."""
     B, n = new_k.shape[:2]
     kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
     gqa = kind == DCP_ATTN_GQA
@@ -486,12 +486,46 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
     request's q_lens are left alone.  Returns (kv_cache, q_out); q_out may be q, and without one a
     zeroed tensor is allocated."""
     call = "dcp_kv_cache_append"
-    if rope is None:
-        _refuse(call, "rope is a RopeTable")
-    shape, rows, q_out, device = _append_args(call, kind, new_k, new_v, kv_cache, None, block_tables, seq_lens, dcp_size,
-                                              rope, q, q_out, q_lens, pos_offsets, stream)
-    code = _lib.dcp_kv_cache_append(*shape, *rows, kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-                                    dcp_size, interleave, _stream(stream, device))
+    B, n = new_k.shape[:2]
+    kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
+    gqa = kind == DCP_ATTN_GQA
+    rows = (B, n, hkv, dim) if gqa else (B, n, dim)
+    if (new_v is not None) != gqa:
+        _refuse(call, "GQA takes new_v, MLA none")
+    device = torch.cuda.current_device()
+    _check_tensors(call, _bf16, device, kv_cache, None if q_out is q else q_out)
+    _check_tensors(call, _int32, device, block_tables, pos_offsets)
+    _check_lens(call, B, device, seq_lens, q_lens)
+    steps = rope.steps
+    if steps.get_device() != device:
+        _refuse(call, "the rope table is not on the current device")
+    if steps.dtype is not torch.int64 or not steps.is_contiguous() or 2 * steps.numel() < rope.desc.rot_dim:
+        _refuse(call, "the rope table is not contiguous int64 [rot_dim / 2]")
+    k_batch, k_token = _row_strides(call, new_k, device, rows)
+    v_batch, v_token = _row_strides(call, new_v, device, rows) if gqa else (0, 0)
+    hq, q_batch, q_token = hkv, 0, 0
+    if q is not None:
+        if q.dim() != 4:
+            _refuse(call, "q is [batch][n][Hq][Dqk]")
+        hq = q.shape[2]
+        q_batch, q_token = _row_strides(call, q, device, (B, n, hq, dim))
+        if q_out is None:
+            with torch.cuda.stream(stream):
+                q_out = torch.zeros((B, n, hq, dim), dtype=torch.bfloat16, device=q.device)
+        elif q_out.shape != q.shape:
+            _refuse(call, "q_out is shaped as q")
+    offsets_stride = 0
+    if pos_offsets is not None:
+        if pos_offsets.dim() != 2 or pos_offsets.shape[1] != n or pos_offsets.shape[0] not in (1, B):
+            _refuse(call, "pos_offsets is [batch or 1][n]")
+        offsets_stride = n if pos_offsets.shape[0] == B else 0
+    code = _lib.dcp_kv_cache_append(
+        _cached_desc(kind, B, n, hq, hkv, dim, dim, bs, nb, max_lb), rope.desc, steps.data_ptr(), new_k.data_ptr(),
+        new_v.data_ptr() if gqa else None, None if q is None else q.data_ptr(),
+        _cached_strides(k_batch, k_token, v_batch, v_token, q_batch, q_token), None if q is None else q_out.data_ptr(),
+        None if pos_offsets is None else pos_offsets.data_ptr(), offsets_stride,
+        None if q_lens is None else q_lens.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        dcp_size, interleave, _stream(stream, device))
     if code != DCP_OK:
         raise DcpError(code, call)
     return kv_cache, q_out

@@ -59,7 +59,8 @@ constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
 // Rows of a query task, at most (when tokens abound).  Rows that are mostly copied take the larger one (latent
 // prompt rows 83 us; at 8192 88), rows that are worked on the smaller (prompt chunks 26 us; at 16384 34).
 constexpr int kTaskBytes = 8192, kCopyTaskBytes = 16384;
-constexpr int kKeptBytes = 96 * 1024;   // shared memory of a CTA for made rows
+constexpr int kKeptBytes = 96 * 1024;   // shared memory of a CTA for made rows (of 16 warps: half as much again)
+constexpr int kSmemBytes = 220 * 1024;  // of a CTA in all
 constexpr int kWarpRows = 32;      // rows of a block that a warp takes alone (drafted tokens, 12 rows: 11 us; by a CTA 22)
 
 enum Rot { kPair = 0, kSwap = 1, kAny = 2 };
@@ -692,6 +693,10 @@ cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
   // queries without a norm have their rotated vectors turned alone, by 8 lanes where they are 8 at most
   const bool narrow = sg > 8 && p.q.count <= 8;
   const int qsg = narrow ? 8 : sg;
+  // interleaved pairs within a lane's vector; whole vectors of halves; anything else
+  const int rot = a.rot_dim == 0 || (a.interleaved && a.rot_offset % 2 == 0) ? kPair
+                  : !a.interleaved && a.rot_offset % 8 == 0 && a.rot_dim % 16 == 0 && a.D <= 256 ? kSwap
+                                                                                                : kAny;
   int team = 1;
   if (a.scales == nullptr) {
     p.pool_k = static_cast<__nv_bfloat16*>(a.cache);
@@ -712,7 +717,10 @@ cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
     // made rows that a warp's groups of lanes keep, up to kKeptBytes of a CTA
     const int cta = team == 1 ? kWarps : team, at_once = team * 32 / sg, slots = a.D <= 256 ? 1 : 3;
     const long long steps = (std::min<long long>(most, a.bs) + at_once - 1) / at_once;
-    p.kept_rows = (int)std::min<long long>(steps, (team == 16 ? kKeptBytes + kKeptBytes / 2 : kKeptBytes) / (cta * 32 * slots * 32));
+    // (beside what the rotation takes, within an SM's memory)
+    const int turning = cta * scratch_floats(rot, qsg, a.rot_dim) * (int)sizeof(float);
+    const int room = team == 16 ? std::min(kKeptBytes + kKeptBytes / 2, kSmemBytes - turning) : kKeptBytes;
+    p.kept_rows = (int)std::min<long long>(steps, room / (cta * 32 * slots * 32));
     p.kept_floats = p.kept_rows * 32 * slots * 8;
     p.kv_tasks = (long long)a.B * p.groups * a.Hkv * (a.v ? 2 : 1);
     if (p.kv_tasks >= (1LL << 31)) return cudaErrorInvalidValue;
@@ -740,10 +748,6 @@ cudaError_t launch_kv_append_norm(const NormAppendArgs& a) {
   // and stay for several tasks
   p.summed = a.q_lens != nullptr && a.B <= kScan && p.q_tasks > warps;
   const long long q_blocks = p.summed ? (long long)sms * resident : (p.q_tasks + kWarps - 1) / kWarps;
-  // interleaved pairs within a lane's vector; whole vectors of halves; anything else
-  const int rot = a.rot_dim == 0 || (a.interleaved && a.rot_offset % 2 == 0) ? kPair
-                  : !a.interleaved && a.rot_offset % 8 == 0 && a.rot_dim % 16 == 0 && a.D <= 256 ? kSwap
-                                                                                                : kAny;
   if (a.D <= 64) return launch<8, 1, 8, 1>(p, rot, team, (unsigned)q_blocks, a.stream);
   if (a.D <= 128)
     return narrow ? launch<16, 1, 8, 1>(p, rot, team, (unsigned)q_blocks, a.stream) : launch<16, 1, 16, 1>(p, rot, team, (unsigned)q_blocks, a.stream);

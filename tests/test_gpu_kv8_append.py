@@ -60,6 +60,13 @@ CASES = [
     ("mla_32", dict(batch=3, num_q_heads=16, lengths=("uniform", 129, 3000), interleave=1), 5, LATENT, 512, 0, None, None),
     ("mla_32", dict(batch=2, num_q_heads=4, dcp_size=2, lengths=("uniform", 300, 900)), 250,
      dict(rot_dim=64, rot_offset=512), 512, 0, [250, 131], None),
+    # the longest heads, all dims rotated in halves: most shared memory, for few rows a block and for many
+    ("tiny_gqa", dict(batch=1, num_q_heads=2, num_kv_heads=1, head_dim_qk=768, head_dim_v=768, lengths=("fixed", 90)), 20,
+     dict(rot_dim=768), 768, 768, None, None),
+    ("tiny_gqa", dict(batch=1, num_q_heads=2, num_kv_heads=1, head_dim_qk=768, head_dim_v=768, block_size=256, dcp_size=1,
+                      lengths=("fixed", 400)), 200, dict(rot_dim=768), 768, 768, None, None),
+    ("tiny_gqa", dict(batch=1, num_q_heads=2, num_kv_heads=1, head_dim_qk=8, head_dim_v=8, lengths=("fixed", 90)), 20,
+     dict(rot_dim=8, layout="interleaved"), 8, 8, None, None),
 ]
 
 

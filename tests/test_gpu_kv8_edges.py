@@ -356,6 +356,52 @@ def test_bad_appends_are_skipped_and_reported(which, what):
     assert torch.equal(sc[:, sorted(own[1] - own[0] - own[2])], sc_before[:, sorted(own[1] - own[0] - own[2])])
 
 
+@pytest.mark.parametrize("which", ["norm", "kv8"])
+@pytest.mark.parametrize("n", [1, 20, 150])
+def test_appends_without_queries_on_another_stream_and_replayed(which, n):
+    """Rows alone, and with queries, on a stream of their own and from a graph: the same bytes."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    inst = H.build_instance(H.small("qwen_gqa", batch=2, num_q_heads=8, lengths=("uniform", 200, 400)))
+    w = inst.w
+    codes, scales = A._cache8(inst)
+    g = torch.Generator().manual_seed(2)
+    k, v, q = (torch.randn((2, n, h, 128), generator=g).to(torch.bfloat16).cuda() for h in (4, 4, 8))
+    start = inst.kv_cache.cuda() if which == "norm" else torch.from_numpy(codes).cuda()
+    wt, rt = torch.rand((128,)).cuda(), dcp.dcp_rope_table(128)
+    table, lens = inst.block_tables.cuda(), inst.seq_lens.cuda()
+    call = dcp.dcp_kv8_append if which == "kv8" else dcp.dcp_kv_cache_append_norm
+    results = []
+    for mode in ("plain", "rows", "stream", "graph"):
+        cache, sc = start.clone(), torch.from_numpy(scales).cuda()
+        q_out = torch.zeros_like(q)
+        args = ("gqa", k, v, cache) + ((sc,) if which == "kv8" else ()) + (table, lens, w.dcp_size, w.interleave, rt)
+        kw = dict(k_weight=wt, **({} if mode == "rows" else dict(q_weight=wt, q=q, q_out=q_out)))
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        if mode == "stream":
+            call(*args, **kw, stream=side)
+        elif mode == "graph":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                call(*args, **kw)
+            graph.replay()
+            graph.replay()                     # (the second time the rows are there already: the same bytes)
+        else:
+            call(*args, **kw)
+        torch.cuda.synchronize()
+        results.append((cache, sc, q_out))
+    for cache, sc, q_out in results[1:]:
+        assert torch.equal(cache.view(torch.uint8), results[0][0].view(torch.uint8)) and torch.equal(sc, results[0][1])
+    assert torch.equal(results[0][2], results[2][2]) and torch.equal(results[0][2], results[3][2])
+    assert not results[1][2].any()
+
+
+def test_a_batch_of_more_entries_than_threads():
+    inst, codes, scales, _ = K.kv8_case("tiny_gqa", 1, batch=500, num_q_heads=4, num_kv_heads=1, dcp_size=4, interleave=2,
+                                        lengths=("uniform", 1, 60))
+    K.check_attn(K.run_attn(inst, codes, scales), K.oracle_attn(inst, codes, scales), codes, scales)
+
+
 def test_far_and_negative_positions_in_both_layouts():
     inst = H.build_instance(H.small("tiny_gqa", batch=2, lengths=("fixed", 40)))
     for rope in (A.HALF, A.INTER):

@@ -59,6 +59,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include <algorithm>
 #include <climits>
@@ -79,7 +80,7 @@ constexpr int kMaxBoxes = 16;                  // blocks of 8 tokens
 constexpr int kMeta = 8;                       // tiles whose scale bytes are kept (K stages and 2 more at least)
 constexpr int kConvWarp = 4, kSoftWarp = 8, kConvWarps = 4;
 constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of it after a move
-constexpr float kNoRef = 1e30f;                // -R of a row that has seen no key: any y + kNoRef is above kTop, -inf stays
+constexpr float kNoRef = FLT_MAX;              // -R of a row that has seen no key: any y + kNoRef is above kTop, -inf stays
 constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;
 constexpr int kMaxCols = 64;
 // Start and end of a unit, in tiles (1, 2, 4: the ragged queries 124, 110, 109 us, 256 long requests 769, 765, 769)

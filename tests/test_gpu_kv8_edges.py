@@ -128,6 +128,36 @@ def test_scores_that_grow_along_the_sequence(name, Lq, kw):
     K.check_attn(K.run_attn(inst, codes, scales), want, codes, scales)
 
 
+@pytest.mark.parametrize("name,Lq,kw", SHAPES[:4])
+@pytest.mark.parametrize("size", [-2.0 ** 110, 2.0 ** 110])
+def test_scores_of_any_finite_size(name, Lq, kw, size):
+    """All keys are ones, so a row's scores are one number, about 2^114.  LSE: the product is exact, then 4 roundings and
+    that of the logarithm.  The weights are equal within a part of the work; parts are joined by their fp32 LSEs, whose step
+    is 2^90 here, so the logarithm of a part's count is lost and parts of any counts weigh the same: what holds of an output
+    is that it lies among the values seen, but for the roundings of the sums and quotients (a few times 2^-24 of the largest)."""
+    inst, codes, scales, _ = K.kv8_case(name, Lq, **kw)
+    codes[0] = k8o.encode(np.ones(codes[0].shape))
+    scales[...] = 127
+    inst.q.fill_(size)
+    got, want = K.run_attn(inst, codes, scales), K.oracle_attn(inst, codes, scales)
+    seen = want["lse"] != -np.inf
+    assert np.isfinite(want["lse"][seen]).all() and np.array_equal(got["lse"] != -np.inf, seen)
+    vmax = np.abs(k8o.dequantise(codes, scales)[1]).max()
+    values, w = k8o.dequantise(codes, scales), inst.w
+    for b, S in enumerate(inst.seq_lens.tolist()):
+        rows = np.stack([_row(inst, values, b, t, 1) for t in range(S)])                  # [S][Hkv][D]
+        shard = np.arange(S) // w.interleave % w.dcp_size
+        for r in range(w.dcp_size):
+            for i in range(Lq):
+                held = np.repeat(rows[(shard == r) & (np.arange(S) <= S - Lq + i)], w.num_q_heads // w.num_kv_heads, axis=1)
+                out = got["partial_out"][r, b, i]
+                if len(held):
+                    assert (out >= held.min(0) - 2.0 ** -20 * vmax).all() and (out <= held.max(0) + 2.0 ** -20 * vmax).all()
+                else:
+                    assert not out.any()
+    assert (np.abs(got["lse"][seen] - want["lse"][seen]) <= 2.0 ** -21 * np.abs(want["lse"][seen])).all()
+
+
 def test_a_sink_beside_a_hundred_thousand_small_weights():
     """One key 12 above the rest (e^-12 is 2^-17.3) over 100,000 others that together outweigh it."""
     inst, codes, scales, _ = K.kv8_case("qwen_gqa", 1, batch=1, num_q_heads=16, num_kv_heads=1, lengths=("fixed", 100000),

@@ -45,14 +45,15 @@
 // the bytes and 1,142 against 906 us).  Measured (GB300, in a graph, with the merge):
 //   256 requests of 8,192 - 32,768 tokens, 64 + 4 heads (4.66 GB)  764-786 us, 5.9-6.1 TB/s
 //   one request of 200,000 tokens, 64 + 8 heads (410 MB)            93-99 us, 4.1-4.4 TB/s
-//   33 requests, 4 ragged queries, blocks of 16 (370 MB)            111 us, 3.3 TB/s
+//   33 requests, 4 ragged queries, blocks of 16 (370 MB)            104 us, 3.6 TB/s
 //   one request of 1,024 tokens, 8 + 2 heads of 64                  15 us
 // What is left of the first: unit ends (about 15,000 cycles, the others' time on the
 // SM), of the second and third the first tiles (code fetched behind the rings' first
 // copies) and the last CTAs.  Code counts: all roles share the instruction cache, and
 // compact waits, ragged tiles masked by a loop and the rest of it took 139 to 96 KB
 // and the ragged queries from 181 to 124 us.  A unit of nothing that warms the cache
-// up before the first copies measured 1 to 5% slower.
+// up before the first copies measured 1 to 5% slower, softmax warps that leave out absent
+// rows (a loop of their own, of barriers alone) 3%.
 //
 // Every wait is bounded; when one runs out the CTA records DCP_ERR_TIMEOUT, goes
 // through its remaining units without work and leaves zeros and -inf for them.
@@ -83,8 +84,6 @@ constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of 
 constexpr float kNoRef = FLT_MAX;              // -R of a row that has seen no key: any y + kNoRef is above kTop, -inf stays
 constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;
 constexpr int kMaxCols = 64;
-// Start and end of a unit, in tiles (1, 2, 4: the ragged queries 124, 110, 109 us, 256 long requests 769, 765, 769)
-constexpr int kUnitCost = 2;
 constexpr uint32_t kWCols = kNt / 2;           // TMEM columns of an fp16 value tile
 
 struct Params {
@@ -124,7 +123,11 @@ struct Cfg {
   static constexpr int kSoftWarps = 4 * kGroups, kWarps = kSoftWarp + kSoftWarps;
   static constexpr uint32_t kThreads = 32 * kWarps, kSoftThreads = 32 * kSoftWarps;
   static constexpr int kReleases = 3 + kConvWarps + kSoftWarps;   // warps that read a unit descriptor
-  static constexpr int kBufs = kCtas == 1 ? 2 : 1;                // P^T tiles
+  // P^T tiles: a second one costs a stage with 16 rows alone (32 rows, one and two: 110 and 109 us)
+  static constexpr int kBufs = NCOL == 16 ? 1 : 2;
+  // Start and end of a unit, in tiles.  2, 4, 6: 33 requests of 4 ragged queries 109, 104, 109 us; 64 of one query 90,
+  // 83, 82; of 12 queries (64 rows: nobody else on the SM meanwhile) 252, 213, 201; 256 long requests 789, 794, 794.
+  static constexpr int kUnitCost = NCOL == 64 ? 6 : 4;
   static constexpr int kWBufs = NCOL == 16 ? 1 : 2;               // fp16 value tiles
   static constexpr size_t kSmemLimit = (kCtas == 1 ? 233472 : kCtas == 2 ? 116736 : 77824) - 1024;
   // registers of a thread at launch, and what setmaxnreg makes of them
@@ -306,8 +309,8 @@ __device__ __forceinline__ long long quotient(long long a, unsigned b) {
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kNt - 1) / kNt; }
 
 // Weight of a unit: its tiles (an empty one still writes its rows), its start and end.
-__device__ __forceinline__ int weight_of(const Params& p, int e) {
-  return max(1, tiles_of(request_of(p, e / p.N, e % p.N).keys)) + kUnitCost;
+__device__ __forceinline__ int weight_of(const Params& p, int e, int unit_cost) {
+  return max(1, tiles_of(request_of(p, e / p.N, e % p.N).keys)) + unit_cost;
 }
 
 template <int NCOL, int D>
@@ -364,7 +367,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   long long mine = 0;
 #pragma unroll 1
   for (int k = 0; k < per; ++k)
-    if (tid * (long long)per + k < entries) mine += weight_of(p, tid * per + k);
+    if (tid * (long long)per + k < entries) mine += weight_of(p, tid * per + k, C::kUnitCost);
   mine *= units_per;
   long long upto = mine;
 #pragma unroll
@@ -390,7 +393,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     int e = tid * per;
 #pragma unroll 1
     for (;; ++e) {
-      const long long next = at + weight_of(p, e) * units_per;
+      const long long next = at + weight_of(p, e, C::kUnitCost) * units_per;
       if (lo < next) break;
       at = next;
     }
@@ -456,7 +459,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       for (; ok && e < entries && at < hi; ++e) {
         const int b = e / p.N, r = e % p.N;
         const Request q = request_of(p, b, r);
-        const int tiles = tiles_of(q.keys), weight = max(1, tiles) + kUnitCost;
+        const int tiles = tiles_of(q.keys), weight = max(1, tiles) + C::kUnitCost;
         const int32_t* bt = p.block_tables + ((long long)r * p.B + b) * p.max_lb;
         // a block id past the pool among the keys empties the request in this shard
         bool bad_block = false;

@@ -43,7 +43,7 @@
 // Bound: HBM (128 bytes of a key and of a value a token and KV head; TMA fetches
 // exactly these: with 256-byte L2 fetches the next head's row came along, 1.39 of
 // the bytes and 1,142 against 906 us).  Measured (GB300, in a graph, with the merge):
-//   256 requests of 8,192 - 32,768 tokens, 64 + 4 heads (4.66 GB)  764-786 us, 5.9-6.1 TB/s
+//   256 requests of 8,192 - 32,768 tokens, 64 + 4 heads (4.66 GB)  769-790 us, 5.9-6.1 TB/s
 //   one request of 200,000 tokens, 64 + 8 heads (410 MB)            93-99 us, 4.1-4.4 TB/s
 //   33 requests, 4 ragged queries, blocks of 16 (370 MB)            104 us, 3.6 TB/s
 //   one request of 1,024 tokens, 8 + 2 heads of 64                  15 us

@@ -156,7 +156,9 @@ struct Smem {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t w_full[2], w_empty[2];              // fp16 value tiles
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_free[2], drain[2];
-  uint64_t unit_full[2], unit_empty[2], q_full, q_free;
+  // (q_full goes by descriptors, so that its next phase needs every reader's release of the unit: with one barrier a
+  // unit of few tiles let the query's next phase end too before a softmax warp had looked, and that warp waited on)
+  uint64_t unit_full[2], unit_empty[2], q_full[2], q_free;
   uint32_t tmem_base;
   int abort;
   int start_e;                                 // first entry of this CTA's share
@@ -350,8 +352,8 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int k = 0; k < C::kUnits; ++k) {
       mbar_init(smem_u32(&sm.unit_full[k]), 1);
       mbar_init(smem_u32(&sm.unit_empty[k]), C::kReleases);
+      mbar_init(smem_u32(&sm.q_full[k]), kConvWarps);
     }
-    mbar_init(smem_u32(&sm.q_full), kConvWarps);
     mbar_init(smem_u32(&sm.q_free), 1);
     sm.abort = 0;
     sm.start_e = -1;
@@ -594,7 +596,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int slot = u % C::kUnits;
       const int tiles = (int)uniform((uint32_t)sm.unit[slot].tiles);
       // (waited for in units without tiles too: a phase left out would make the next wait pass early)
-      bool good = wait(sm.q_full, (uint32_t)u & 1u);
+      bool good = wait(sm.q_full[u % C::kUnits], (uint32_t)(u / C::kUnits) & 1u);
       if (tiles > 0 && *abort_flag == 0) {
 #pragma unroll 1
         for (int t = 0; good && t < tiles; ++t, ++tt) {
@@ -732,7 +734,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));     // (once per unit: its parity goes by them)
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));   // (once per unit: its parity goes by them)
       if (tiles > 0 && *abort_flag == 0) {
         bool good = true;
 #pragma unroll 1
@@ -818,7 +820,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int tiles = w.tiles, t0 = w.t0, lim_min = w.lim_min;
       float nm[HC], l[HC];                                    // -R and the sum of a row
       const uint32_t tO = lane_base + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL + h0;
-      bool bad = !wait(sm.q_full, (uint32_t)u & 1u), broke = dead || tiles == 0;
+      bool bad = !wait(sm.q_full[u % C::kUnits], (uint32_t)(u / C::kUnits) & 1u), broke = dead || tiles == 0;
       if (st < NCOL) sm.nref[st] = kNoRef;
 #pragma unroll
       for (int h = 0; h < HC; ++h) nm[h] = kNoRef, l[h] = 0.f;

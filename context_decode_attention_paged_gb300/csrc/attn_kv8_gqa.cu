@@ -820,7 +820,10 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const int tiles = w.tiles, t0 = w.t0, lim_min = w.lim_min;
       float nm[HC], l[HC];                                    // -R and the sum of a row
       const uint32_t tO = lane_base + 2 * NCOL + (uint32_t)(o_units & 1) * NCOL + h0;
-      bool bad = !wait(sm.q_full[u % C::kUnits], (uint32_t)(u / C::kUnits) & 1u), broke = dead || tiles == 0;
+      // The split warps write where the unit's rows go, in a CTA that has given up too: this wait does not heed that,
+      // and without what it waits for nothing is written.
+      const bool placed = wait_at(smem_u32(&sm.q_full[u % C::kUnits]), (uint32_t)(u / C::kUnits) & 1u, false, 16);
+      bool bad = !placed, broke = dead || tiles == 0;
       if (st < NCOL) sm.nref[st] = kNoRef;
 #pragma unroll
       for (int h = 0; h < HC; ++h) nm[h] = kNoRef, l[h] = 0.f;
@@ -920,7 +923,8 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const float sum = (sm.red[0][st] + sm.red[1][st]) + (sm.red[2][st] + sm.red[3][st]);
         const bool live = have && w.lim[st] > 0 && !(sum == 0.f);         // (NaN sums make NaN rows)
         sm.by[st] = live ? 1.f / sum : -1.f;
-        (w.slot >= 0 ? p.ws_lse : p.lse)[w.at[st]] = live ? (log2f(sum) - sm.nref[st]) * 0.69314718055994531f : -INFINITY;
+        if (placed)
+          (w.slot >= 0 ? p.ws_lse : p.lse)[w.at[st]] = live ? (log2f(sum) - sm.nref[st]) * 0.69314718055994531f : -INFINITY;
       }
       uint32_t o[HC];                                         // (without a product whatever is there: not used)
       tc_fence_after();
@@ -948,7 +952,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       float* const dst = (w.slot >= 0 ? p.ws_o : p.out) + lrow;
 #pragma unroll
       for (int h = 0; h < HC; ++h)
-        if (h0 + h < w.rows && lrow < D) {
+        if (placed && h0 + h < w.rows && lrow < D) {
           const float by = sm.by[h0 + h];
           dst[w.at[h0 + h] * D] = by < 0.f ? 0.f : __uint_as_float(o[h]) * by;
         }

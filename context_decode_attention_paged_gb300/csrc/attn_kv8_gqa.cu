@@ -82,7 +82,7 @@ constexpr int kMeta = 8;                       // tiles whose scale bytes are ke
 constexpr int kConvWarp = 4, kSoftWarp = 8, kConvWarps = 4;
 constexpr float kTop = 15.0f, kStart = 7.0f;   // log2 of the largest P, and of it after a move
 constexpr float kNoRef = FLT_MAX;              // -R of a row that has seen no key: any y + kNoRef is above kTop, -inf stays
-constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;
+constexpr uint32_t kBarSoftmax = 1;            // (the one barrier where warps meet, and they leave it with one answer)
 constexpr int kMaxCols = 64;
 constexpr uint32_t kWCols = kNt / 2;           // TMEM columns of an fp16 value tile
 
@@ -743,15 +743,19 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const bool edge = j0 + kNt > lim_min;               // keys that some row does not see
           good = wait(sm.v_full[st], ph) && (tt < C::kWBufs || wait(sm.w_empty[tt % C::kWBufs], (uint32_t)(tt / C::kWBufs - 1) & 1u));
           if (!good) break;
-          if (edge) {
-            // one thread a key: a key past the range is 0; of a key that some row does not see, NaN becomes 0
-            // here and the epilogue puts it into the rows that see it
-            const int j = j0 + ct;
-            uint4* row = reinterpret_cast<uint4*>(vring + st * C::kTile + ct * D);
-            if (j >= lim_min)
+          if (edge && dim0 < D) {
+            // This warp's dims of a key past the range become 0; of a key that some row does not see, NaN becomes 0
+            // here and the epilogue puts it into the rows that see it.  (The warps do not meet here: one that gives up
+            // would leave the others waiting.)
 #pragma unroll 1
-              for (int k = 0; k < D / 16; ++k) {
-                uint4 v = row[k];
+            for (int key = lane; key < kNt; key += 32) {
+              const int j = j0 + key;
+              if (j < lim_min) continue;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint4* at = reinterpret_cast<uint4*>(vring + st * C::kTile + key * D +
+                                                     (C::kchunk((uint32_t)(dim0 / 16 + half), (uint32_t)key) << 4));
+                uint4 v = *at;
                 uint32_t* words = &v.x;
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
@@ -759,10 +763,11 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                   if (nan != 0 && j < ke) w.nan_values = 1;
                   words[m] = j < ke ? words[m] & ~(nan * 0xffu) : 0u;
                 }
-                row[k] = v;
+                *at = v;
               }
+            }
             fence_proxy_async_smem();                         // (the stage's next tile comes by a copy)
-            named_bar_sync(kBarConvert, 32 * kConvWarps);
+            __syncwarp();
           }
           // this warp's 32 dims: the tile's bytes transposed on the way out of shared memory (16 keys x 16
           // dims a matrix: a lane gets 4 keys of dim lane / 4), fp16, to TMEM lane = dim, column = key / 2

@@ -121,3 +121,12 @@ def test_a_ctas_units_have_their_rows_places_after_it_gave_up(units):
 
 def test_a_wait_that_heeds_would_let_places_be_used_that_are_not_there():
     assert orders(*roles(2, 2, gave_up=True, heeds=True))[1] is not None
+
+
+def test_warps_that_may_give_up_alone_meet_at_no_barrier():
+    """The warps that convert values wait each for themselves, and one of them may give up where the others do not: a
+    barrier of theirs would then wait for ever."""
+    with open(SOURCE) as f:
+        text = f.read()
+    part = text[text.index("query split, then value tiles"):text.index("softmax and epilogue ----")]
+    assert not re.search(r"named_bar_sync|bar_red_or|__syncthreads", part)

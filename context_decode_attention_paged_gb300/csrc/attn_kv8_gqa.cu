@@ -575,15 +575,14 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
       unit_done(u);
     }
-    if (*abort_flag) {
-      // copies in flight land before the CTA leaves
+    // Copies in flight land before the CTA leaves.  (They have, where it did not give up; another role may do that behind
+    // the last copy, and the CTA leaves then without having waited for it elsewhere.)
 #pragma unroll 1
-      for (int k = max(0, k_issued - kKStages); k < k_issued; ++k)
-        wait_at(smem_u32(&sm.k_full[k % kKStages]), (uint32_t)(k / kKStages) & 1u, false, 1);
+    for (int k = max(0, k_issued - kKStages); k < k_issued; ++k)
+      wait_at(smem_u32(&sm.k_full[k % kKStages]), (uint32_t)(k / kKStages) & 1u, false, 1);
 #pragma unroll 1
-      for (int k = max(0, v_issued - kVStages); k < v_issued; ++k)
-        wait_at(smem_u32(&sm.v_full[k % kVStages]), (uint32_t)(k / kVStages) & 1u, false, 1);
-    }
+    for (int k = max(0, v_issued - kVStages); k < v_issued; ++k)
+      wait_at(smem_u32(&sm.v_full[k % kVStages]), (uint32_t)(k / kVStages) & 1u, false, 1);
   } else if (warp == 1) {
     // ---------------- QK issuer: S^T(t) = K(t) (Q_hi + Q_lo)^T ----------------
     constexpr uint32_t id = idesc_e4m3(NCOL);

@@ -42,3 +42,42 @@ def test_many_short_and_empty_units_give_the_same_answer_every_time(Lq, ragged, 
         assert again["status"] == dcp.DCP_OK
         for key in ("partial_out", "lse", "out"):
             assert np.array_equal(got[key], again[key]), key
+
+
+@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("Lq,kw", [(1, dict(batch=150, lengths=("uniform", 1, 900), dcp_size=2, interleave=1)),
+                                   (3, dict(batch=120, lengths=("uniform", 3, 900), dcp_size=2, num_q_heads=16)),
+                                   (8, dict(batch=60, lengths=("uniform", 8, 700), dcp_size=1, num_q_heads=16)),
+                                   (1, dict(batch=90, lengths=("uniform", 1, 900), dcp_size=1, head_dim_qk=128, head_dim_v=128))])
+def test_waits_that_run_out_write_the_outputs_alone(Lq, kw, tile):
+    """Waits of 5 ms, and one tile of every unit is never loaded: CTAs give up early or late in their units, ragged ones
+    among them.  What lies around the outputs and the workspace stays; rows are the oracle's or 0 and -inf."""
+    import ctypes
+
+    from context_decode_attention_paged_gb300 import binding as dcp
+    hooks = dcp.raw_lib().dcp_testing_set_hooks
+    hooks.restype, hooks.argtypes = None, [ctypes.c_ulonglong, ctypes.c_int32]
+    inst, codes, scales, _ = K.kv8_case("tiny_gqa", Lq, **kw)
+    w = inst.w
+    desc = dcp.desc_from_tensors(w.kind, inst.q, inst.kv_cache, inst.block_tables, w.head_dim_v)
+    sizes = (w.dcp_size * w.batch * Lq * w.num_q_heads * w.head_dim_v, w.dcp_size * w.batch * Lq * w.num_q_heads,
+             (dcp.dcp_kv8_decode_attn_workspace_size(desc, w.dcp_size) + 3) // 4)
+    around = 1 << 16
+    held = [torch.full((n + 2 * around,), 1234.5, dtype=torch.float32, device="cuda") for n in sizes]
+    po, lse, ws = (t[around:around + n] for t, n in zip(held, sizes))
+    shape = (w.dcp_size, w.batch, Lq, w.num_q_heads)
+    kw = dict(partial_out=po.view(*shape, w.head_dim_v), lse=lse.view(*shape), workspace=ws.view(torch.uint8))
+    hooks(5_000_000, tile)
+    try:
+        got = K.run_attn(inst, codes, scales, **kw)
+    finally:
+        hooks(0, -1)
+    assert got["status"] == dcp.DCP_ERR_TIMEOUT
+    for t in held:
+        assert bool((t[:around] == 1234.5).all()) and bool((t[-around:] == 1234.5).all())
+    want = K.oracle_attn(inst, codes, scales)
+    gave_up = (got["lse"] == -np.inf) & (want["lse"] != -np.inf)
+    assert gave_up.any() and (got["partial_out"][gave_up] == 0).all() and np.isfinite(got["partial_out"]).all()
+    got = K.run_attn(inst, codes, scales, **kw)
+    assert got["status"] == dcp.DCP_OK
+    K.check_attn(got, want, codes, scales)

@@ -130,3 +130,13 @@ def test_warps_that_may_give_up_alone_meet_at_no_barrier():
         text = f.read()
     part = text[text.index("query split, then value tiles"):text.index("softmax and epilogue ----")]
     assert not re.search(r"named_bar_sync|bar_red_or|__syncthreads", part)
+
+
+def test_the_copies_in_flight_land_whoever_gives_up():
+    """The producer waits for its last copies whether or not it has seen that the CTA has given up: another role may do so
+    behind its last look."""
+    with open(SOURCE) as f:
+        text = f.read()
+    part = text[text.index("TMA producer ----"):text.index("QK issuer: S^T")]
+    tail = part[part.rindex("unit_done(u);"):]
+    assert tail.count("wait_at(") == 2 and "abort_flag" not in tail

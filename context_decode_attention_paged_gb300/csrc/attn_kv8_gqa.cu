@@ -1030,12 +1030,15 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const Params p, int grid)
           for (int v = 0; v < V; ++v) x[m][v] = src[32 * v];
         }
 #pragma unroll
-        for (int m = 0; m < kAhead; ++m)
-          if (w[m] != 0.f) {                                  // (what a part without weight holds does not count)
-            sum += w[m];
+        for (int m = 0; m < kAhead; ++m) {
+          // (a part without keys holds zeros; what is not finite counts however light its part is, as it does within one)
+          sum += w[m];
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = fmaf(w[m], x[m][v], o[v]);
+          for (int v = 0; v < V; ++v) {
+            const bool light = w[m] == 0.f && !(fabsf(x[m][v]) < INFINITY);
+            o[v] = light ? o[v] + x[m][v] : fmaf(w[m], x[m][v], o[v]);
           }
+        }
       }
     }
     const int rr = row0 + h, i = rr / p.gsize, head = g * p.gsize + rr - i * p.gsize;

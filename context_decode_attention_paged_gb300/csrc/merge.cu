@@ -54,16 +54,18 @@ __device__ __forceinline__ void load_batch(const float* __restrict__ src, long l
 
 // out row = sum over n sources (stride src_stride floats) of w_k * src_k.
 // Dv4 = Dv / 4 float4 per row.  Loads go out kBatch sources at a time, the first
-// ones (in `v`, vector `lane`) before the weights are known; a source of weight
-// 0 does not count, whatever it holds.
-template <bool kBf16Out>
+// ones (in `v`, vector `lane`) before the weights are known.  `counts`: this lane's
+// source does.  A source of weight 0 does not, whatever it holds; with kLight it
+// does where it has keys, and what is not finite shows however small its weight.
+template <bool kBf16Out, bool kLight = false>
 __device__ __forceinline__ void weighted_row(const float* __restrict__ src, long long src_stride,
-                                             int n, float w_lane, int Dv4, float4 (&v)[kBatch], void* dst_row) {
+                                             int n, float w_lane, bool counts, int Dv4, float4 (&v)[kBatch],
+                                             void* dst_row) {
   const int lane = threadIdx.x & 31;
   // tokens and splits are dealt from the first source on, so those without keys are
   // the last ones
   // (a NaN LSE makes the weights of lanes without a source NaN too)
-  n = 32 - __clz(__ballot_sync(0xffffffffu, lane < n && w_lane != 0.f));
+  n = 32 - __clz(__ballot_sync(0xffffffffu, lane < n && counts));
   for (int c = lane; c - lane < Dv4; c += 32) {
     const bool in = c < Dv4;                         // (the shuffles below take the whole warp)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -73,7 +75,15 @@ __device__ __forceinline__ void weighted_row(const float* __restrict__ src, long
       for (int k = 0; k < kBatch; ++k) {
         if (k0 + k >= n) break;
         const float w = __shfl_sync(0xffffffffu, w_lane, k0 + k);
-        if (w == 0.f) continue;
+        if (w == 0.f) {
+          if constexpr (kLight) {                      // (a source without keys holds zeros)
+            acc.x = fabsf(v[k].x) < INFINITY ? acc.x : acc.x + v[k].x;
+            acc.y = fabsf(v[k].y) < INFINITY ? acc.y : acc.y + v[k].y;
+            acc.z = fabsf(v[k].z) < INFINITY ? acc.z : acc.z + v[k].z;
+            acc.w = fabsf(v[k].w) < INFINITY ? acc.w : acc.w + v[k].w;
+          }
+          continue;
+        }
         acc.x = fmaf(w, v[k].x, acc.x);
         acc.y = fmaf(w, v[k].y, acc.y);
         acc.z = fmaf(w, v[k].z, acc.z);
@@ -115,11 +125,13 @@ merge_kernel(const float* __restrict__ partial_out, const float* __restrict__ ls
   const int hs = Hq / N;
   const int r = h / hs;
   const long long dst = (((long long)r * B * Lq + bi) * hs + (h % hs));
-  weighted_row<true>(src, stride, N, w, Dv / 4, v, out + dst * Dv);
+  weighted_row<true>(src, stride, N, w, w != 0.f, Dv / 4, v, out + dst * Dv);
   if (out_lse && lane == 0) out_lse[dst] = merged;
 }
 
-// One warp per (r, b, i, h): merge n_split workspace partials into partial_out.
+// One warp per (r, b, i, h): merge n_split workspace partials into partial_out (kLight: the
+// 8-bit cache's, where a NaN value shows in every row that sees it, wherever splits begin).
+template <bool kLight>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32, 5)
 split_combine_kernel(const float* __restrict__ ws_o, const float* __restrict__ ws_lse, int n_split,
                      long long rows, int Hq, int Dv, float* __restrict__ partial_out,
@@ -138,7 +150,8 @@ split_combine_kernel(const float* __restrict__ ws_o, const float* __restrict__ w
   if (lane < Dv / 4) load_batch(src, stride, n_split, 0, lane, v);
   float merged;
   const float w = lse_weights(lane_lse, &merged);
-  weighted_row<false>(src, stride, n_split, w, Dv / 4, v, partial_out + row * Dv);
+  weighted_row<false, kLight>(src, stride, n_split, w, kLight ? lane_lse != -INFINITY : w != 0.f, Dv / 4, v,
+                              partial_out + row * Dv);
   if (lane == 0) lse[row] = merged;
 }
 
@@ -162,8 +175,9 @@ cudaError_t launch_split_combine(const AttnArgs& a, const SplitPlan& p) {
   const float* ws_lse = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) +
                                                        ((o_bytes + 255) & ~size_t(255)));
   const long long blocks = (rows + kWarpsPerBlock - 1) / kWarpsPerBlock;
-  split_combine_kernel<<<(unsigned)blocks, kWarpsPerBlock * 32, 0, a.stream>>>(
-      ws_o, ws_lse, p.n_split, rows, a.Hq, a.Dv, a.partial_out, a.lse);
+  auto* kernel = a.kv_scales ? split_combine_kernel<true> : split_combine_kernel<false>;
+  kernel<<<(unsigned)blocks, kWarpsPerBlock * 32, 0, a.stream>>>(ws_o, ws_lse, p.n_split, rows, a.Hq, a.Dv, a.partial_out,
+                                                                 a.lse);
   return cudaGetLastError();
 }
 

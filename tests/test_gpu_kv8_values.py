@@ -1,0 +1,56 @@
+"""Values at the ends of their ranges in the 8-bit cache's operators: what a formula makes of them whichever kernel, and
+wherever a border between CTAs falls."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import kv8_common as K
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from context_decode_attention_paged_gb300 import build
+    build.build()
+
+
+LONG = dict(batch=1, dcp_size=1, num_kv_heads=1, num_q_heads=8)
+
+
+@pytest.mark.parametrize("S", [100, 3000, 60000])
+@pytest.mark.parametrize("name,kw", [("tiny_gqa", LONG), ("tiny_gqa", dict(LONG, num_q_heads=32)),
+                                     ("tiny_gqa", dict(LONG, block_size=48)), ("mla_32", dict(batch=1, dcp_size=1, num_q_heads=8))])
+@pytest.mark.parametrize("at", [0.1, 0.95])
+def test_a_nan_value_shows_however_light_its_part_of_the_shard(name, kw, S, at):
+    """Keys of one tenth score 256 below the others: their weights are 0 in fp32, a part of the shard that holds them
+    alone weighs 0 against the others, and a NaN among their values makes its dim NaN all the same."""
+    inst, codes, scales, _ = K.kv8_case(name, 1, None, (0, 0), lengths=("fixed", S), **kw)
+    w = inst.w
+    gqa = w.kind == "gqa"
+    one = int(K.k8o.encode([1.0])[0])
+    d_k, v_dim = (w.head_dim_qk if gqa else 64), 5
+    inst.q.zero_()
+    inst.q[..., -d_k:] = 128.0 / (d_k * w.scale)       # scores of 128 (to bf16) for keys of 1, -128 for keys of -1
+    (codes[0] if gqa else codes)[..., -d_k:] = one
+    light = range(int(at * S) - S // 20, int(at * S) + S // 20)
+    table = inst.block_tables.numpy()[0, 0]
+    for t in light:
+        cell = (table[t // w.block_size], t % w.block_size)
+        (codes[0][cell] if gqa else codes[cell])[..., -d_k:] = one | 128
+    t = int(at * S)
+    cell = (table[t // w.block_size], t % w.block_size)
+    if gqa:
+        codes[1][cell][..., v_dim] = 127
+    else:
+        # (a latent row's values are its keys: the score of a row with NaN is NaN, so the whole output row is)
+        codes[cell][..., v_dim] = 127
+    want = K.oracle_attn(inst, codes, scales)
+    assert np.isnan(want["out"][..., v_dim]).all()
+    got = K.run_attn(inst, codes, scales)
+    K.check_attn(got, want, codes, scales)

@@ -604,7 +604,7 @@ template <int NCOL>
 cudaError_t launch_ncol(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const GqaParams& p, long long units,
                         cudaStream_t stream) {
   const size_t smem = gqa_smem_bytes(p.D, NCOL, p.stages);
-  cudaError_t e = cudaFuncSetAttribute(gqa_attn_kernel<NCOL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(gqa_attn_kernel<NCOL>);
   if (e != cudaSuccess) return e;
   gqa_attn_kernel<NCOL><<<(unsigned)units, kThreads, smem, stream>>>(tm_k, tm_v, p);
   return cudaGetLastError();

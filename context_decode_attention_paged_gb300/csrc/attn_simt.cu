@@ -276,7 +276,7 @@ cudaError_t launch_attn_simt(const AttnArgs& a, const SplitPlan& p) {
   void (*kern)(SimtParams) = a.kv_scales   ? attn_simt_kernel<false, true>
                              : a.tree_mask ? attn_simt_kernel<true, false>
                                            : attn_simt_kernel<false, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   const int gsize = a.Hq / a.Hkv;
   dim3 grid((unsigned)(a.N * a.B * p.n_split), (unsigned)a.Hkv,

@@ -899,7 +899,7 @@ cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, Params& p, 
   cudaError_t e = cudaFuncGetAttributes(&fa, tree_gqa_kernel<D>);
   if (e != cudaSuccess) return e;
   if (fa.numRegs * kThreads < 128 * kCtrlRegs + 256 * kSoftRegs) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(tree_gqa_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = allow_smem(tree_gqa_kernel<D>);
   if (e != cudaSuccess) return e;
   const int grid = std::min(p.units, device_sm_count());
   tree_gqa_kernel<D><<<(unsigned)grid, kThreads, smem, stream>>>(tm_k, tm_v, p);

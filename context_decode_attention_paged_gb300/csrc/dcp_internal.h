@@ -55,6 +55,15 @@ SplitPlan plan_splits(const AttnArgs& a, int sm_count, int tile_tokens, int unit
 
 int device_sm_count();
 
+// Shared memory that a CTA may have (sm_103).  A kernel whose size goes by the call has this as its limit, whatever
+// the call's size: the limit belongs to the function, and a smaller one that another host thread sets between a
+// call's setting and its launch would refuse that launch.
+constexpr int kCtaSmem = 227 * 1024;
+template <typename... Params>
+cudaError_t allow_smem(void (*kernel)(Params...), int limit = kCtaSmem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+}
+
 // Test-only knobs of the attention kernels, read at each launch: the limit of
 // every bounded wait (default 2 s) and a tile that the first CTA's TMA
 // producer of every work unit never loads (-1: none), so that the kernels'

@@ -60,7 +60,7 @@ constexpr int kAhead = 4;          // heads of a lane whose loads are in flight
 // prompt rows 83 us; at 8192 88), rows that are worked on the smaller (prompt chunks 26 us; at 16384 34).
 constexpr int kTaskBytes = 8192, kCopyTaskBytes = 16384;
 constexpr int kKeptBytes = 96 * 1024;   // shared memory of a CTA for made rows (of 16 warps: half as much again)
-constexpr int kSmemBytes = 220 * 1024;  // of a CTA in all
+constexpr int kSmemBytes = 220 * 1024;  // of a CTA in all (the counts' sums are beside it)
 constexpr int kWarpRows = 32;      // rows of a block that a warp takes alone (drafted tokens, 12 rows: 11 us; by a CTA 22)
 
 enum Rot { kPair = 0, kSwap = 1, kAny = 2 };
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(32 * kTeam, kTeam == 16 ? 1 : 2) kv8_rows_kern
 template <typename Kernel, typename... Args>
 cudaError_t start(Kernel kernel, unsigned grid, int threads, size_t smem, cudaStream_t stream, bool beside, Args... args) {
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(kernel, kSmemBytes);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};

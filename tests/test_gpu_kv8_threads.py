@@ -103,42 +103,44 @@ def test_appends_of_two_shapes_from_two_threads(name, one, other):
     assert dcp.dcp_get_last_device_status() == dcp.DCP_OK
 
 
+def _attention(which, dim, L, name="tiny_gqa", **kw):
+    """An attention call with buffers of its own: (the C call on a stream, its outputs)."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    dims = {} if name == "mla_32" else dict(head_dim_qk=dim, head_dim_v=dim)
+    inst, codes, scales, _ = K.kv8_case(name, L, None, batch=2, lengths=("fixed", 80), **dims, **kw)
+    w = inst.w
+    q, table, lens = inst.q.cuda(), inst.block_tables.cuda(), inst.seq_lens.cuda()
+    cache = torch.from_numpy(codes).cuda() if which == "kv8" else inst.kv_cache.cuda()
+    sc, mask = torch.from_numpy(scales).cuda(), torch.from_numpy(K.chain(L)).cuda()
+    shape = (w.dcp_size, 2, L, w.num_q_heads)
+    po, lse = torch.empty((*shape, w.head_dim_v), device="cuda"), torch.empty(shape, device="cuda")
+    ws = torch.empty((1 << 24,), dtype=torch.uint8, device="cuda")
+    desc = dcp.desc_from_tensors(w.kind, inst.q, inst.kv_cache, inst.block_tables, w.head_dim_v)
+    at = lambda t: ctypes.c_void_p(t.data_ptr())                 # noqa: E731
+    head, out = (ctypes.byref(desc), at(q), at(cache)), (at(po), at(lse), at(ws), ws.numel())
+    if which == "kv8":
+        fn, args = dcp.raw_lib().dcp_kv8_decode_attn, (*head, at(sc), at(table), at(lens), None, w.dcp_size, w.interleave,
+                                                       w.scale, L, *out)
+    elif which == "bf16":
+        fn, args = dcp.raw_lib().dcp_decode_attn, (*head, at(table), at(lens), w.dcp_size, w.interleave, w.scale, L, *out)
+    else:
+        fn, args = dcp.raw_lib().dcp_tree_attn, (*head, at(table), at(lens), None, at(mask), 0, w.dcp_size, w.interleave,
+                                                 w.scale, *out)
+    held = (desc, q, cache, sc, mask, table, lens, ws)
+
+    def call(stream=None):
+        code = fn(*args, stream)
+        assert code == dcp.DCP_OK and held, dcp.status_string(code)
+
+    return call, (po, lse)
+
+
 @pytest.mark.parametrize("which,one,other", [
     # (head dim, tokens a request): the CUDA cores; the decode kernel; row blocks of one and of two tiles of a drafted tree
     ("kv8", (72, 1), (512, 1)), ("bf16", (72, 1), (512, 1)), ("bf16", (64, 1), (128, 1)), ("tree", (128, 4), (128, 64)),
 ])
 def test_attention_of_two_shapes_from_two_threads(which, one, other):
-    from context_decode_attention_paged_gb300 import binding as dcp
-
-    def make(dim, L):
-        inst, codes, scales, _ = K.kv8_case("tiny_gqa", L, None, batch=2, head_dim_qk=dim, head_dim_v=dim, lengths=("fixed", 80))
-        w = inst.w
-        q, table, lens = inst.q.cuda(), inst.block_tables.cuda(), inst.seq_lens.cuda()
-        cache = torch.from_numpy(codes).cuda() if which == "kv8" else inst.kv_cache.cuda()
-        sc, mask = torch.from_numpy(scales).cuda(), torch.from_numpy(K.chain(L)).cuda()
-        shape = (w.dcp_size, 2, L, w.num_q_heads)
-        po, lse = torch.empty((*shape, dim), device="cuda"), torch.empty(shape, device="cuda")
-        ws = torch.empty((1 << 24,), dtype=torch.uint8, device="cuda")
-        desc = dcp.desc_from_tensors("gqa", inst.q, inst.kv_cache, inst.block_tables, dim)
-        at = lambda t: ctypes.c_void_p(t.data_ptr())             # noqa: E731
-        head, out = (ctypes.byref(desc), at(q), at(cache)), (at(po), at(lse), at(ws), ws.numel())
-        if which == "kv8":
-            fn, args = dcp.raw_lib().dcp_kv8_decode_attn, (*head, at(sc), at(table), at(lens), None, w.dcp_size, w.interleave,
-                                                           w.scale, L, *out)
-        elif which == "bf16":
-            fn, args = dcp.raw_lib().dcp_decode_attn, (*head, at(table), at(lens), w.dcp_size, w.interleave, w.scale, L, *out)
-        else:
-            fn, args = dcp.raw_lib().dcp_tree_attn, (*head, at(table), at(lens), None, at(mask), 0, w.dcp_size, w.interleave,
-                                                     w.scale, *out)
-        held = (desc, q, cache, sc, mask, table, lens, ws)
-
-        def call(stream=None):
-            code = fn(*args, stream)
-            assert code == dcp.DCP_OK and held, dcp.status_string(code)
-
-        return call, (po, lse)
-
-    made = [make(*one), make(*other)]
+    made = [_attention(which, *one), _attention(which, *other)]
     for call, _ in made:
         call()
     torch.cuda.synchronize()
@@ -147,3 +149,30 @@ def test_attention_of_two_shapes_from_two_threads(which, one, other):
     assert not raised, (len(raised), raised[0])
     for (_, held), copy in zip(made, want):
         assert all(torch.equal(a, b) for a, b in zip(held, copy))
+
+
+@pytest.mark.parametrize("which,dim,name,kw", [("kv8", 64, "tiny_gqa", {}), ("kv8", 128, "tiny_gqa", {}), ("kv8", 72, "tiny_gqa", {}),
+                                               ("bf16", 128, "tiny_gqa", {}), ("tree", 128, "tiny_gqa", {}),
+                                               ("bf16", 576, "mla_32", dict(num_q_heads=64))])
+def test_the_first_call_of_a_host_thread(which, dim, name, kw):
+    """A thread that has made no CUDA call yet, so that no context is current in it."""
+    call, held = _attention(which, dim, 2, name, **kw)
+    call()
+    torch.cuda.synchronize()
+    want, raised = [t.clone() for t in held], []
+    for t in held:
+        t.zero_()
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            call()
+        except Exception as e:                                   # noqa: BLE001
+            raised.append(e)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not raised, raised
+    assert all(torch.equal(a, b) for a, b in zip(held, want))

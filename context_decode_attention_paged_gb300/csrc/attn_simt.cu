@@ -251,6 +251,12 @@ size_t simt_smem_bytes(const AttnArgs& a) {
 
 }  // namespace
 
+// (GQA: heads of up to 592 dims.  KV heads and row blocks are the grid's second and third dimension.)
+bool attn_simt_supported(const AttnArgs& a) {
+  const long long rows = (long long)a.Lq * (a.Hq / a.Hkv);
+  return simt_smem_bytes(a) <= (size_t)kCtaSmem && a.Hkv <= 65535 && (rows + kRows - 1) / kRows <= 65535;
+}
+
 SplitPlan plan_attn_simt(const AttnArgs& a, int sm_count) {
   const int gsize = a.Hq / a.Hkv;
   const int row_blocks = (a.Lq * gsize + kRows - 1) / kRows;

@@ -64,10 +64,15 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-dcp_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? DCP_OK : DCP_ERR_CUDA; }
+// (an error of this call is not left for the next one's launch to find)
+dcp_status_t from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return DCP_OK;
+  cudaGetLastError();
+  return DCP_ERR_CUDA;
+}
 
 // Fill AttnArgs from the public arguments; INVALID_ARG / UNSUPPORTED on bad input.
-dcp_status_t make_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave,
+dcp_status_t make_shape_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave,
                        float scale, int32_t causal_q_len, AttnArgs* a) {
   if (!d) return DCP_ERR_INVALID_ARG;
   if (d->kind != DCP_ATTN_GQA && d->kind != DCP_ATTN_MLA) return DCP_ERR_INVALID_ARG;
@@ -110,6 +115,18 @@ Impl select_impl(const AttnArgs& a) {
   if (mla_tc_supported(a)) return Impl::kMlaTc;
   if (a.tree_words == 0 && gqa_tc_supported(a)) return Impl::kGqaTc;
   return Impl::kSimt;
+}
+
+// UNSUPPORTED for a shape that no kernel takes.
+dcp_status_t kernel_status(const AttnArgs& a) {
+  return select_impl(a) == Impl::kSimt && !attn_simt_supported(a) ? DCP_ERR_UNSUPPORTED : DCP_OK;
+}
+
+// Arguments of dcp_decode_attn.
+dcp_status_t make_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave, float scale, int32_t causal_q_len,
+                       AttnArgs* a) {
+  const dcp_status_t st = make_shape_args(d, dcp_size, interleave, scale, causal_q_len, a);
+  return st != DCP_OK ? st : kernel_status(*a);
 }
 
 SplitPlan plan_for(const AttnArgs& a, Impl impl, int sm_count) {
@@ -158,11 +175,11 @@ int32_t kind_of(Impl impl) {
 
 // Arguments of a drafted-tree call: those of dcp_decode_attn and the node limit.
 dcp_status_t make_tree_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave, float scale, AttnArgs* a) {
-  const dcp_status_t st = make_args(d, dcp_size, interleave, scale, d ? d->q_len : 1, a);
+  const dcp_status_t st = make_shape_args(d, dcp_size, interleave, scale, d ? d->q_len : 1, a);
   if (st != DCP_OK) return st;
   if (d->q_len > DCP_TREE_MAX_NODES) return DCP_ERR_UNSUPPORTED;
   a->tree_words = (d->q_len + 31) / 32;
-  return DCP_OK;
+  return kernel_status(*a);
 }
 
 // The cache side of an append or commit call (the checks of dcp_kv_cache_write).
@@ -253,14 +270,14 @@ dcp_status_t make_norm_args(const dcp_attn_desc_t* d, const dcp_norm_desc_t* nor
   return d->head_dim_qk > DCP_APPEND_MAX_HEAD_DIM ? DCP_ERR_UNSUPPORTED : DCP_OK;
 }
 
-// Arguments of a call over the 8-bit cache: those of dcp_decode_attn and the pool's limits.
+// Arguments of a call over the 8-bit cache: those of dcp_decode_attn.
 dcp_status_t make_kv8_args(const dcp_attn_desc_t* d, int32_t dcp_size, int32_t interleave, float scale,
                            int32_t causal_q_len, AttnArgs* a) {
-  const dcp_status_t st = make_args(d, dcp_size, interleave, scale, causal_q_len, a);
+  const dcp_status_t st = make_shape_args(d, dcp_size, interleave, scale, causal_q_len, a);
   if (st != DCP_OK) return st;
   static const uint8_t any = 0;
   a->kv_scales = &any;               // (says which kernels there are; the call sets the scales)
-  return DCP_OK;
+  return kernel_status(*a);
 }
 
 }  // namespace

@@ -158,6 +158,7 @@ cudaError_t launch_split_combine(const AttnArgs& a, const SplitPlan& p);
 
 // Generic SIMT kernel (any head dims); used for shapes the tensor-core kernels
 // do not take.
+bool attn_simt_supported(const AttnArgs& a);   // (rows of long heads do not fit its shared memory)
 cudaError_t launch_attn_simt(const AttnArgs& a, const SplitPlan& p);
 SplitPlan plan_attn_simt(const AttnArgs& a, int sm_count);
 

@@ -158,7 +158,8 @@ DCP_API size_t dcp_decode_attn_workspace_size(const dcp_attn_desc_t* d, int32_t 
  * Alignment: q, kv_cache, partial_out 16 bytes.
  * Errors: INVALID_ARG (NULL pointers, sizes < 1, Hq % Hkv != 0, MLA with
  * Hkv != 1 or Dv > Dqk, GQA with Dv != Dqk, causal_q_len != q_len, small
- * workspace, misalignment); UNSUPPORTED (head dims without a kernel); CUDA.
+ * workspace, misalignment); UNSUPPORTED (head dims without a kernel: not a multiple of 8,
+ * GQA beyond 592, MLA where 48 Dqk + 16 Dv is above 57,536); CUDA.
  * Arithmetic and accuracy: products of the bf16 inputs accumulate in fp32;
  * the softmax runs in fp32 in the log2 domain.  Each probability is rounded to
  * bf16 once before the value product (the GQA tensor-core kernel carries it as
@@ -536,8 +537,9 @@ DCP_API dcp_status_t dcp_kv8_read(const dcp_attn_desc_t* d, const void* kv8_cach
 DCP_API size_t dcp_kv8_decode_attn_workspace_size(const dcp_attn_desc_t* d, int32_t dcp_size);
 
 /* dcp_decode_attn over the 8-bit cache.  GQA with heads of 64 or 128 dims and the block sizes
- * of the decode kernel runs on the tensor cores, every other shape, MLA among them, on the
- * CUDA cores (dcp_kv8_decode_attn_kernel_kind tells).  Query i < n_b of request b (n_b = q_lens[b], or
+ * of the decode kernel runs on the tensor cores, every other shape that dcp_decode_attn takes,
+ * MLA among them, on the CUDA cores (dcp_kv8_decode_attn_kernel_kind tells; GQA heads beyond
+ * 592 dims can be stored and read, not attended).  Query i < n_b of request b (n_b = q_lens[b], or
  * q_len where q_lens is NULL) sits at position S_b - n_b + i and sees the positions up to
  * its own.  partial_out fp32 [dcp][B][Lq][Hq][Dv] and lse fp32 [dcp][B][Lq][Hq] per shard, for
  * dcp_merge.  A row that sees no key of a shard, and every row i >= n_b, gives partial_out = 0

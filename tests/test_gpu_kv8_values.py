@@ -54,3 +54,22 @@ def test_a_nan_value_shows_however_light_its_part_of_the_shard(name, kw, S, at):
     assert np.isnan(want["out"][..., v_dim]).all()
     got = K.run_attn(inst, codes, scales)
     K.check_attn(got, want, codes, scales)
+
+
+@pytest.mark.parametrize("dim", [512, 592])
+def test_long_heads_on_the_cuda_cores(dim):
+    inst, codes, scales, _ = K.kv8_case("tiny_gqa", 2, None, batch=2, head_dim_qk=dim, head_dim_v=dim, lengths=("uniform", 20, 200))
+    got = K.run_attn(inst, codes, scales)
+    assert got["status"] == 0
+    K.check_attn(got, K.oracle_attn(inst, codes, scales), codes, scales)
+
+
+@pytest.mark.parametrize("dim", [600, 768])
+def test_heads_too_long_to_attend_are_refused_and_leave_the_next_call_alone(dim):
+    from context_decode_attention_paged_gb300 import binding as dcp
+    inst, codes, scales, _ = K.kv8_case("tiny_gqa", 1, None, batch=2, head_dim_qk=dim, head_dim_v=dim, lengths=("fixed", 30))
+    with pytest.raises(dcp.DcpError) as e:
+        K.run_attn(inst, codes, scales)
+    assert e.value.code == dcp.DCP_ERR_UNSUPPORTED
+    inst, codes, scales, _ = K.kv8_case("tiny_gqa", 1, None, batch=2, lengths=("fixed", 30))
+    K.check_attn(K.run_attn(inst, codes, scales), K.oracle_attn(inst, codes, scales), codes, scales)

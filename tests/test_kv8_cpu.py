@@ -206,3 +206,25 @@ def test_prepared_rows_rotate_as_the_append_oracle():
     b, _ = k8o.ref_append_norm("gqa", orc.to_f64(inst.kv_cache), k, v, None, *args, w.block_size, (freqs, "half", 0, 1.0),
                                None, None, 1e-6)
     assert np.abs(a - b).max() < 1e-12
+
+
+@pytest.mark.parametrize("dim,fits", [(584, True), (592, True), (600, False), (768, False)])
+def test_heads_that_no_attention_kernel_takes_are_refused(lib, dim, fits):
+    """The CUDA-core kernel's rows of long heads do not fit a CTA's shared memory: 384 bytes a dim and 2,304 for GQA."""
+    assert (384 * dim + 2304 <= 227 * 1024) == fits
+    d = _desc(lib, head_dim_qk=dim, head_dim_v=dim)
+    kind = lib.DCP_KERNEL_SIMT if fits else lib.DCP_KERNEL_NONE
+    assert lib.dcp_kv8_decode_attn_kernel_kind(d, 2) == lib.dcp_decode_attn_kernel_kind(d, 2) == kind
+    assert lib.dcp_tree_attn_kernel_kind(d, 2) == kind
+    assert (lib.dcp_kv8_decode_attn_launches(d, 2) > 0) == fits
+    if not fits:
+        assert lib.dcp_kv8_decode_attn_workspace_size(d, 2) == lib.dcp_decode_attn_workspace_size(d, 2) == 0
+        assert _attn(lib, d) == lib.DCP_ERR_UNSUPPORTED
+
+
+def test_shapes_past_the_cuda_core_kernels_grid_are_refused(lib):
+    for kw in (dict(num_kv_heads=65536, num_q_heads=65536, head_dim_qk=8, head_dim_v=8),
+               dict(q_len=1 << 20, num_q_heads=2, num_kv_heads=1, head_dim_qk=72, head_dim_v=72)):
+        d = _desc(lib, **kw)
+        assert lib.dcp_kv8_decode_attn_kernel_kind(d, 2) == lib.DCP_KERNEL_NONE
+        assert _attn(lib, d, causal=d.q_len) == lib.DCP_ERR_UNSUPPORTED

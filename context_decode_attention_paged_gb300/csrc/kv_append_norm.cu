@@ -535,7 +535,7 @@ __device__ __forceinline__ void block_rows(const Params& p, long long task, int 
   }
   const int blk = block_of(a, b, r, jb, lane == 0 && team_warp == 0);
   const long long scale_at = ((values ? (long long)a.num_blocks : 0) + max(blk, 0)) * a.Hkv + h;
-  const int old = (int)a.scales[scale_at] - 127;
+  const uint32_t old = a.scales[scale_at];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   if constexpr (kTeam > 1) {
@@ -547,12 +547,12 @@ __device__ __forceinline__ void block_rows(const Params& p, long long task, int 
   if (blk < 0) return;
   uint8_t* pool = (values ? p.codes_v : p.codes_k) + ((long long)blk * a.bs * a.Hkv + h) * a.D;
   const long long pitch = (long long)a.Hkv * a.D;
-  int e = old;
-  if (before == 0 || !(most <= 448.f * power(min(max(old, -126), 110)))) {
-    e = exponent_for(most);
-    if (lane == 0 && team_warp == 0) a.scales[scale_at] = (uint8_t)(127 + e);
-    // the earlier rows' codes, to the new scale
-    const float ratio = power(max(min(max(old, -126), 110) - e, -126));
+  uint32_t byte = old;
+  if (before == 0 || !(most <= 448.f * scale_factor(old))) {  // (a factor of NaN holds nothing)
+    byte = (uint32_t)(127 + exponent_for(most));
+    if (lane == 0 && team_warp == 0) a.scales[scale_at] = (uint8_t)byte;
+    // the earlier rows' codes, to the new scale (2^-126 of a code is 0, as less of it is)
+    const float ratio = old == 255 ? NAN : power(min(max((int)old - (int)byte, -126), 127));
     const int vecs = a.D / 8, total = before * vecs;
     for (int c0 = team_warp * 32 + lane; c0 < total; c0 += kTeam * 32 * 4) {
       uint2 u[4];
@@ -570,7 +570,7 @@ __device__ __forceinline__ void block_rows(const Params& p, long long task, int 
       }
     }
   }
-  const float by = power(-min(max(e, -126), 126));
+  const float by = scale_factor(254 - byte);                  // 1 / the factor
   auto store = [&](int k, const float (&v)[SLOTS][8]) {
     if (k >= count) return;
 #pragma unroll

@@ -131,7 +131,7 @@ def ref_kv8_append(kind, codes, scales, k, new_v, table, seq_lens, N, interleave
                 finite = [np.abs(r[np.isfinite(r)]).max(initial=0.0) for r in new.values()]
                 a = max(finite)
                 s = float(scale_values(view_s[pool, blk, h]))
-                if first == 0 or a > 448.0 * s:
+                if first == 0 or not a <= 448.0 * s:             # (a scale of NaN holds nothing)
                     e = exponent_for(a)
                     old = VALUES[view_c[pool, blk, :first, h]] * (s / 2.0 ** e)
                     view_c[pool, blk, :first, h] = encode(old)

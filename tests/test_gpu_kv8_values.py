@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import helpers as H
 import kv8_common as K
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +74,31 @@ def test_heads_too_long_to_attend_are_refused_and_leave_the_next_call_alone(dim)
     assert e.value.code == dcp.DCP_ERR_UNSUPPORTED
     inst, codes, scales, _ = K.kv8_case("tiny_gqa", 1, None, batch=2, lengths=("fixed", 30))
     K.check_attn(K.run_attn(inst, codes, scales), K.oracle_attn(inst, codes, scales), codes, scales)
+
+
+@pytest.mark.parametrize("byte", [0, 1, 2, 60, 86, 87, 127, 167, 168, 200, 236, 237, 238, 240, 245, 246, 247, 253, 254, 255])
+@pytest.mark.parametrize("n,kw", [(3, dict()), (40, dict(block_size=64, interleave=64, dcp_size=1))])
+def test_appends_into_blocks_of_any_scale(byte, n, kw):
+    """Blocks whose scale byte is none that an append writes: it stays where the new rows are within 448 of its factor,
+    else the earlier codes are rounded to the new one (of 255 they are NaN).  Powers of two make every step exact but the
+    rounding to codes, so codes and scales are the oracle's bit for bit."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    inst = H.build_instance(H.small("tiny_gqa", batch=2, lengths=("uniform", 150, 170), **kw))
+    w = inst.w
+    rng = np.random.default_rng(byte)
+    shape = tuple(inst.kv_cache.shape)
+    codes = rng.integers(0, 256, shape).astype(np.uint8)
+    scales = np.full((2, shape[1], shape[3]), byte, dtype=np.uint8)
+    table, lens = inst.block_tables, inst.seq_lens
+    for at in (-12, -3, 4, 7, 9, 12, 60, 200):                   # largest magnitude of the rows over the factor, log2
+        e = int(np.clip(byte - 127 + at, -130, 127))
+        rows = [torch.from_numpy(rng.uniform(-1, 1, (2, n, shape[3], w.head_dim_qk)) * 2.0 ** (e - 1)).to(torch.bfloat16)
+                for _ in range(2)]
+        c, s = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+        dcp.dcp_kv8_append("gqa", rows[0].cuda(), rows[1].cuda(), c, s, table.cuda(), lens.cuda(), w.dcp_size, w.interleave)
+        assert dcp.dcp_get_last_device_status() == dcp.DCP_OK
+        with np.errstate(all="ignore"):
+            want_c, want_s, _ = K.k8o.ref_kv8_append("gqa", codes, scales, rows[0].double().numpy(), rows[1].double().numpy(),
+                                                     table.numpy(), lens.tolist(), w.dcp_size, w.interleave, w.block_size)
+        assert np.array_equal(s.cpu().numpy(), want_s), (at, np.unique(s.cpu().numpy()), np.unique(want_s))
+        assert np.array_equal(c.cpu().numpy(), want_c), (at, int((c.cpu().numpy() != want_c).sum()))

@@ -847,17 +847,18 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int sv = (int)(meta >> 8);
         const float ev = sv == 255 ? NAN : (float)(sv - 127), inv = scale_factor((uint32_t)max(254 - sv, 0));
 
-        // y = x + ev of this key's rows; hidden keys -inf
+        // y = x + ev of this key's rows; hidden keys -inf.  (The query's factor times the product first: it is a power
+        // of two, and no product of two factors leaves fp32's range on the way to a score that does not.)
         const int j = (t0 + t) * kNt + lrow;
         const bool full = (t0 + t) * kNt + kNt <= lim_min;
         float y[HC], most = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HC; h += 4) {
           const float4 qf = *reinterpret_cast<const float4*>(&w.qf[h0 + h]);
-          y[h] = fmaf(__uint_as_float(v[h]), kf * qf.x, ev);
-          y[h + 1] = fmaf(__uint_as_float(v[h + 1]), kf * qf.y, ev);
-          y[h + 2] = fmaf(__uint_as_float(v[h + 2]), kf * qf.z, ev);
-          y[h + 3] = fmaf(__uint_as_float(v[h + 3]), kf * qf.w, ev);
+          y[h] = fmaf(__uint_as_float(v[h]) * qf.x, kf, ev);
+          y[h + 1] = fmaf(__uint_as_float(v[h + 1]) * qf.y, kf, ev);
+          y[h + 2] = fmaf(__uint_as_float(v[h + 2]) * qf.z, kf, ev);
+          y[h + 3] = fmaf(__uint_as_float(v[h + 3]) * qf.w, kf, ev);
         }
         if (!full)
 #pragma unroll

@@ -102,3 +102,22 @@ def test_appends_into_blocks_of_any_scale(byte, n, kw):
                                                      table.numpy(), lens.tolist(), w.dcp_size, w.interleave, w.block_size)
         assert np.array_equal(s.cpu().numpy(), want_s), (at, np.unique(s.cpu().numpy()), np.unique(want_s))
         assert np.array_equal(c.cpu().numpy(), want_c), (at, int((c.cpu().numpy() != want_c).sum()))
+
+
+@pytest.mark.parametrize("name,Lq,kw", [("tiny_gqa", 1, {}), ("qwen_gqa", 3, dict(block_size=32)), ("qwen_gqa", 9, {}),
+                                        ("tiny_gqa", 2, dict(block_size=48)), ("mla_32", 1, dict(num_q_heads=8))])
+@pytest.mark.parametrize("power", [100, 120, -100, -130])
+def test_huge_and_tiny_queries_against_keys_of_zero(name, Lq, kw, power):
+    """Scores are 0 whatever the query's and the block's factors are, and the rows the values' means: no product of the
+    factors alone may leave fp32's range."""
+    inst, codes, scales, _ = K.kv8_case(name, Lq, None, (40, 40) if power > 0 else (-40, -40), batch=2,
+                                        lengths=("uniform", 200, 700), **kw)
+    gqa = inst.w.kind == "gqa"
+    keys, values = (codes[0], codes[1]) if gqa else (codes, None)
+    keys[...] = np.where(np.random.default_rng(1).random(keys.shape) < 0.5, 0, 128)
+    if gqa:
+        scales[1] = 127
+    inst.q.copy_(torch.where(torch.rand(inst.q.shape) < 0.5, -1.0, 1.0) * 2.0 ** power)
+    want = K.oracle_attn(inst, codes, scales)
+    assert np.isfinite(want["out"]).all()
+    K.check_attn(K.run_attn(inst, codes, scales), want, codes, scales)

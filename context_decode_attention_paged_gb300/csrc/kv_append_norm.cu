@@ -221,7 +221,7 @@ struct Rows {
       sum = group_sum(sum);
       float r = rsqrtf(fmaf(sum, per_dim, eps));
       if (__any_sync(0xffffffffu, sum > FLT_MAX)) {
-        // squares past fp32's range (or an infinity): the row scaled down first; eps is below rounding then
+        // squares past fp32's range (or an infinity): the sum from values scaled down; eps is below rounding then
         const float by = sum > FLT_MAX ? 0x1p-70f : 1.f;
         float small = 0.f;
 #pragma unroll
@@ -229,11 +229,11 @@ struct Rows {
           if (sl + SG * m < norm_vecs)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              x[m][e] *= by;
-              small = fmaf(x[m][e], x[m][e], small);
+              const float y = x[m][e] * by;
+              small = fmaf(y, y, small);
             }
         small = group_sum(small);
-        if (sum > FLT_MAX) r = rsqrtf(small * per_dim);
+        if (sum > FLT_MAX) r = rsqrtf(small * per_dim) * by;
       }
 #pragma unroll
       for (int m = 0; m < SLOTS; ++m)

@@ -457,8 +457,9 @@ typedef struct {
 } dcp_norm_desc_t;
 
 /* dcp_kv_cache_append with RMS norms of the key heads (MLA: of the row) and the query
- * heads before the rotation.  Sums of squares, norms and rotation run in fp32, each value
- * is rounded to bf16 once.  As the formula has it, a NaN in a head makes all its normalised dims NaN,
+ * heads before the rotation.  Sums of squares, norms (x / root first, then the weight: a
+ * quotient below 2^-126 loses bits) and rotation run in fp32, each value is rounded to bf16
+ * once.  As the formula has it, a NaN in a head makes all its normalised dims NaN,
  * an infinity makes its own dim NaN and the other normalised ones 0 (before the rotation).
  * Arguments as there, and
  *  rope, rope_steps  may be NULL together: no rotation

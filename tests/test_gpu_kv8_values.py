@@ -121,3 +121,40 @@ def test_huge_and_tiny_queries_against_keys_of_zero(name, Lq, kw, power):
     want = K.oracle_attn(inst, codes, scales)
     assert np.isfinite(want["out"]).all()
     K.check_attn(K.run_attn(inst, codes, scales), want, codes, scales)
+
+
+@pytest.mark.parametrize("dim,norm_dim", [(64, 64), (128, 96), (256, 256), (576, 512)])
+@pytest.mark.parametrize("top", [63, 66, 100])
+def test_norms_of_heads_that_span_many_binades(dim, norm_dim, top):
+    """One dim whose square is at the end of fp32's range or past it, others far below it that large weights bring back:
+    each is within a bf16 rounding of the formula (2^-8, and 2^-18 for fp32 sums) as far as fp32 holds x / root.
+    That quotient is one fp32 product, whose smallest step is 2^-149: below 2^-126 it is off by up to half of that,
+    2^-150, and the value by 2^-150 times the weight."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    inst = H.build_instance(H.small("tiny_gqa", batch=2, lengths=("uniform", 20, 60), head_dim_qk=dim, head_dim_v=dim,
+                                    num_q_heads=4, num_kv_heads=2))
+    w = inst.w
+    g = torch.Generator().manual_seed(dim)
+    rows = lambda h: (1 + torch.rand((2, 3, h, dim), generator=g)) * 2.0 ** -60   # noqa: E731
+    k, q = rows(2).to(torch.bfloat16), rows(4).to(torch.bfloat16)
+    for t in (k, q):
+        t[..., 3] = 2.0 ** top
+        t[..., 5] *= 2.0 ** -18
+    weight = torch.full((norm_dim,), 2.0 ** 60)
+    weight[3] = 1.0
+    cache, q_out = inst.kv_cache.cuda(), torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda")
+    dcp.dcp_kv_cache_append_norm("gqa", k.cuda(), k.cuda(), cache, inst.block_tables.cuda(), inst.seq_lens.cuda(), w.dcp_size,
+                                 w.interleave, k_weight=weight.cuda(), q_weight=weight.cuda(), eps=1e-6, q=q.cuda(), q_out=q_out)
+    want = K.k8o.norm(q.double().numpy(), weight.double().numpy(), 1e-6)
+    want_k = K.k8o.norm(k.double().numpy(), weight.double().numpy(), 1e-6)
+    got = q_out.double().cpu().numpy()
+    step = np.zeros(dim)
+    step[:norm_dim] = 2.0 ** -150 * weight.double().numpy()
+    near = lambda g, r: (np.abs(g - r) <= (2.0 ** -8 + 2.0 ** -18) * np.abs(r) + step).all()   # noqa: E731
+    assert near(got, want)
+    for b in range(2):
+        for i in range(3):
+            blk, slot = K.tro.cell_of(inst.block_tables.numpy(), b, int(inst.seq_lens[b]) - 3 + i, w.interleave, w.dcp_size,
+                                      w.block_size)
+            row = cache[0, blk, slot].double().cpu().numpy()
+            assert near(row, want_k[b, i])

@@ -228,3 +228,27 @@ def test_shapes_past_the_cuda_core_kernels_grid_are_refused(lib):
         d = _desc(lib, **kw)
         assert lib.dcp_kv8_decode_attn_kernel_kind(d, 2) == lib.DCP_KERNEL_NONE
         assert _attn(lib, d, causal=d.q_len) == lib.DCP_ERR_UNSUPPORTED
+
+
+# ---------------------------------------------------------------------------
+# what the header says of the query's split
+# ---------------------------------------------------------------------------
+
+def test_the_headers_bounds_of_the_query_split_hold():
+    """A query row is scaled by a power of two so that its largest value lies in [128, 256), and each value becomes the sum
+    of two codes: every bf16 value of that range, split so."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "dcp.h")) as f:
+        text = " ".join(f.read().replace("*", " ").split())
+    said = re.search(r"two e4m3 terms, which is exact down to 2\^-(\d+) of the row's largest and an absolute error of at "
+                     r"most 2\^-(\d+) of that below", text)
+    exact, error = 2.0 ** -int(said.group(1)), 2.0 ** -int(said.group(2))
+    x = torch.arange(0x4380, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).double()       # 0 up to 256
+    assert x[-1] < 256.0 and bool((x[1:] > x[:-1]).all())
+    hi = x.float().to(torch.float8_e4m3fn).double()
+    rest = (x - hi - (x - hi).float().to(torch.float8_e4m3fn).double()).abs()
+    inexact = x[rest > 0]
+    # of a largest of 128, which is the least that rows are scaled to
+    assert float(inexact.max()) < exact * 128 <= 2 * float(inexact.max())
+    assert float(rest.max()) <= error * 128 < 2 * float(rest.max())

@@ -425,7 +425,9 @@ def _attn_buffers(call, size_of, desc, dcp_size, shape, on, device, partial_out,
 
 def _append_args(call, kind, new_k, new_v, kv_cache, scales, block_tables, seq_lens, dcp_size, rope, q, q_out, q_lens,
                  pos_offsets, stream):
-    """The checked arguments of an append with norms or into the 8-bit cache: (desc, rope desc, rope steps), (new_k .. q_lens pointers), q_out, device."""
+    """The checked arguments of an append with norms or into the 8-bit cache: (desc, rope desc, rope steps),
+    (new_k .. q_lens pointers), q_out, device.  (dcp_kv_cache_append has the same checks in its own body, 0.8 us a call
+    less: what changes in one changes in the other.)"""
     B, n = new_k.shape[:2]
     kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
     gqa = kind == DCP_ATTN_GQA
@@ -486,6 +488,7 @@ def dcp_kv_cache_append(kind, new_k, new_v, kv_cache, block_tables, seq_lens, dc
     request's q_lens are left alone.  Returns (kv_cache, q_out); q_out may be q, and without one a
     zeroed tensor is allocated."""
     call = "dcp_kv_cache_append"
+    # (the checks of _append_args, in a body of their own for 0.8 us a call: what changes in one changes in the other)
     B, n = new_k.shape[:2]
     kind, hkv, dim, bs, nb, max_lb = _cache_fields(call, kind, kv_cache, block_tables, B, dcp_size)
     gqa = kind == DCP_ATTN_GQA

@@ -45,7 +45,7 @@
 // the bytes and 1,142 against 906 us).  Measured (GB300, in a graph, with the merge):
 //   256 requests of 8,192 - 32,768 tokens, 64 + 4 heads (4.66 GB)  769-790 us, 5.9-6.1 TB/s
 //   one request of 200,000 tokens, 64 + 8 heads (410 MB)            93-99 us, 4.1-4.4 TB/s
-//   33 requests, 4 ragged queries, blocks of 16 (370 MB)            104 us, 3.6 TB/s
+//   33 requests, 4 ragged queries, blocks of 16 (370 MB)            104-106 us, 3.5 TB/s
 //   one request of 1,024 tokens, 8 + 2 heads of 64                  15 us
 // What is left of the first: unit ends (about 15,000 cycles, the others' time on the
 // SM), of the second and third the first tiles (code fetched behind the rings' first
@@ -55,8 +55,13 @@
 // up before the first copies measured 1 to 5% slower, softmax warps that leave out absent
 // rows (a loop of their own, of barriers alone) 3%.
 //
+// Few units are cut into up to a part a CTA, which one CTA joins: one request of 50,000
+// tokens, 1 KV head and 16 rows takes 187 us, of 200,000 and 8 KV heads 116.
+//
 // Every wait is bounded; when one runs out the CTA records DCP_ERR_TIMEOUT, goes
-// through its remaining units without work and leaves zeros and -inf for them.
+// through its remaining units without work and leaves zeros and -inf for them.  So
+// no warp that may give up alone meets others at a barrier, and nothing is written
+// without the wait for where it goes.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -16,7 +16,9 @@
 // round to 0 there.
 // kKv8: the 8-bit cache (codes times 2^(byte - 127) of their block and KV head),
 // causal queries with counts of their own; hidden and non-finite values as in the
-// tree form.
+// tree form.  Codes are turned into floats one at a time, again for every 16 rows:
+// 32 requests of 8,192 latent rows and 128 heads take 150 ms (GB300), where reading
+// them back and the bf16 kernel take 0.37.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <float.h>

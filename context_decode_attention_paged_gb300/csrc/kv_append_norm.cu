@@ -32,8 +32,10 @@
 // beside that one (a programmatic launch; one launch for both held the queries to the
 // rows' registers).
 //
-// Bound: HBM and, for prompts, instruction issue (about 190 a pass of two rows of
-// 128); for a decode step the launch and dependent loads.  Measured (GB300, in a
+// Bound: for latent rows HBM; for prompts loads that 24 warps an SM wait for and a
+// second wave of tasks that is not full (issue slots at 0.56 and, in 8 bits, 0.43:
+// about 190 instructions a pass of two rows of 128); for a decode step the launch
+// and dependent loads.  Measured (GB300, in a
 // graph; 64 + 4 heads of 128 unless said): 64 tokens 5.5 us into either cache; 2,154
 // tokens of ragged prompts into the bf16 cache 26 us (79 MB, 3.1 TB/s), into the
 // 8-bit one 31; 400 drafted tokens of 40 + 8 heads 11; 1,352 latent rows with 128

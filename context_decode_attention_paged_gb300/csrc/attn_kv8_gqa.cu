@@ -313,7 +313,7 @@ __device__ __forceinline__ long long quotient(long long a, unsigned b) {
   return (unsigned long long)a >> 32 ? a / b : (long long)((unsigned)a / b);
 }
 
-__device__ __forceinline__ int tiles_of(int keys) { return (keys + kNt - 1) / kNt; }
+__device__ __forceinline__ int tiles_of(int keys) { return (int)(((unsigned)keys + kNt - 1) / kNt); }   // (keys up to 2^31 - 1)
 
 // Weight of a unit: its tiles (an empty one still writes its rows), its start and end.
 __device__ __forceinline__ int weight_of(const Params& p, int e, int unit_cost) {
@@ -470,7 +470,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int32_t* bt = p.block_tables + ((long long)r * p.B + b) * p.max_lb;
         // a block id past the pool among the keys empties the request in this shard
         bool bad_block = false;
-        const int blocks = (q.keys + p.bs - 1) / p.bs;
+        const int blocks = (int)(((unsigned)q.keys + (unsigned)p.bs - 1) / (unsigned)p.bs);
 #pragma unroll 1
         for (int k = lane; k < blocks; k += 32 * 8) {
           int blk[8];
@@ -532,8 +532,8 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       // A lane's box of a window of tiles: pool block and scale bytes.  The next window's bytes and the table
       // entries of the one behind it are on their way meanwhile.
       auto entry = [&](int t) {
-        const int j = (t0 + t) * kNt + lane * box;
-        return t < tiles && j < ke ? bt[j / p.bs] : -1;
+        const unsigned j = (unsigned)(t0 + t) * kNt + (unsigned)(lane * box);      // (may pass 2^31 behind the last tile)
+        return t < tiles && j < (unsigned)ke ? bt[j / (unsigned)p.bs] : -1;
       };
       auto scale_bytes = [&](int blk) {
         if (blk < 0) return 127u | 127u << 8;
@@ -744,7 +744,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t, ++tt) {
           const int j0 = (t0 + t) * kNt;
-          const bool edge = j0 + kNt > lim_min;               // keys that some row does not see
+          const bool edge = j0 > lim_min - kNt;               // keys that some row does not see
           good = wait(sm.v_full[st], ph) && (tt < C::kWBufs || wait(sm.w_empty[tt % C::kWBufs], (uint32_t)(tt / C::kWBufs - 1) & 1u));
           if (!good) break;
           if (edge && dim0 < D) {
@@ -855,7 +855,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // y = x + ev of this key's rows; hidden keys -inf.  (The query's factor times the product first: it is a power
         // of two, and no product of two factors leaves fp32's range on the way to a score that does not.)
         const int j = (t0 + t) * kNt + lrow;
-        const bool full = (t0 + t) * kNt + kNt <= lim_min;
+        const bool full = (t0 + t) * kNt <= lim_min - kNt;
         float y[HC], most = -INFINITY;
 #pragma unroll
         for (int h = 0; h < HC; h += 4) {
@@ -951,7 +951,7 @@ kv8_gqa_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // NaN values among the keys that some row does not see: into the rows that see them
         const int32_t* bt = p.block_tables + ((long long)w.r * p.B + w.b) * p.max_lb;
 #pragma unroll 1
-        for (int j = max(lim_min, t0 * kNt); j < min(w.ke, (t0 + tiles) * kNt); ++j) {
+        for (int j = max(lim_min, t0 * kNt); (unsigned)j < min((unsigned)w.ke, (unsigned)(t0 + tiles) * kNt); ++j) {
           const long long row = (long long)bt[j / p.bs] * p.bs + j % p.bs;
           const bool nan = (p.codes_v[(row * p.Hkv + w.g) * D + lrow] & 0x7f) == 0x7f;
 #pragma unroll

@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
     // split of it: zero partial, -inf LSE) and reports DCP_ERR_BOUNDS
     const int* btr = a.block_tables + ((long long)r * a.B + b) * a.max_lb;
     bool bad_blk = false;
-    for (int jb = tid; jb < (L + a.bs - 1) / a.bs; jb += kThreads)
+    const int blocks = (int)(((unsigned)L + (unsigned)a.bs - 1) / (unsigned)a.bs);   // (L up to 2^31 - 1)
+    for (int jb = tid; jb < blocks; jb += kThreads)
       bad_blk |= (unsigned)btr[jb] >= (unsigned)a.num_blocks;
     if (__syncthreads_or(bad_blk)) {
       j_end = j_begin;
@@ -126,7 +127,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(SimtParams P) {
   const long long pool_elems = (long long)a.num_blocks * a.bs * a.Hkv * a.Dqk;
   const int* bt = a.block_tables + ((long long)r * a.B + b) * a.max_lb;
 
-  for (int j0 = j_begin; j0 < j_end; j0 += kTile) {
+  // (j0 + kTile may not fit behind the last tile)
+  for (int j0 = j_begin; j0 < j_end; j0 = j_end - j0 > kTile ? j0 + kTile : j_end) {
     const int nt = min(kTile, j_end - j0);
     // stage keys (and values) of this tile
     for (int idx = tid; idx < kTile * a.Dqk; idx += kThreads) {

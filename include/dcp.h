@@ -564,7 +564,8 @@ DCP_API size_t dcp_kv8_decode_attn_workspace_size(const dcp_attn_desc_t* d, int3
  *  workspace     as in dcp_tree_attn
  * Accuracy: codes and scales are taken as they are.  The tensor-core kernel splits a query value
  * into two e4m3 terms, which is exact down to 2^-9 of the row's largest and an absolute error
- * of at most 2^-17 of that below; products accumulate in fp32; a probability, times its value's
+ * of at most 2^-17 of that below; products accumulate in fp32 (the tensor cores' sums of values
+ * truncate: about 8e-4 of an output where one CTA sums 128,000 keys); a probability, times its value's
  * scale, is rounded to fp16 once (2^-11 of it, or 2^-32 of the row's largest).
  * Errors: as dcp_decode_attn; INVALID_ARG for kv8_scales NULL. */
 DCP_API dcp_status_t dcp_kv8_decode_attn(const dcp_attn_desc_t* d, const void* q, const void* kv8_cache,

@@ -81,3 +81,43 @@ def test_waits_that_run_out_write_the_outputs_alone(Lq, kw, tile):
     got = K.run_attn(inst, codes, scales, **kw)
     assert got["status"] == dcp.DCP_OK
     K.check_attn(got, want, codes, scales)
+
+
+@pytest.mark.parametrize("S", [2 ** 31 - 1, 2 ** 31 - 128, 2 ** 31 - 4000])
+@pytest.mark.parametrize("Lq", [1, 3])
+def test_lengths_up_to_the_end_of_32_bits(S, Lq):
+    """One request whose table names three blocks over and over, and at its end one whose slots behind the last token hold
+    NaN.  A CTA of 444 sums 37,786 tiles or so one after the other: fp32 sums of n terms of like size are off by up to
+    n / 2 2^-24 (a softmax thread's, n one a tile: 1.2e-3), where each addition truncates n / 2 2^-23.  In what portions
+    the tensor cores add a tile's 128 products is theirs to choose; one by one, the most, n is 128 a tile: 0.29 of an
+    output of up to 2.  (2.8e-2 was seen.)  The LSE is what tells that every key counts once."""
+    from context_decode_attention_paged_gb300 import binding as dcp
+    D, H, bs = 64, 8, 128
+    rng = np.random.default_rng(3)
+    codes = np.empty((2, 4, bs, 1, D), dtype=np.uint8)
+    codes[0] = K.k8o.encode(rng.standard_normal((4, bs, 1, D)))
+    codes[1] = K.k8o.encode(rng.uniform(1, 2, (4, bs, 1, D)))
+    scales = np.full((2, 4, 1), 127, dtype=np.uint8)
+    entries = -(-S // bs)
+    table = (torch.arange(2 ** 24, dtype=torch.int32, device="cuda") % 3).view(1, 1, -1)
+    table[0, 0, entries - 1] = 3
+    last = S - (entries - 1) * bs                                # tokens of the last block
+    codes[:, 3, last:] = 127
+    q = torch.randn((1, Lq, H, D), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    c, s, lens = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), torch.tensor([S], dtype=torch.int32).cuda()
+    po, lse = dcp.dcp_kv8_decode_attn("gqa", q.cuda(), c, s, table, lens, 1, 128, 0.125, Lq, D)
+    assert dcp.dcp_get_last_device_status() == dcp.DCP_OK
+    vals = np.nan_to_num(K.k8o.VALUES[codes])[:, :, :, 0]
+    x = np.exp(0.125 * np.einsum("ihd,bkd->ihbk", q[0].double().numpy(), vals[0]))
+    for i in range(Lq):
+        full = np.bincount(np.arange(entries - 1) % 3, minlength=4).astype(np.float64)
+        count = np.repeat(full[:, None], bs, axis=1)
+        seen = last - (Lq - 1 - i)                               # (negative: in the block before)
+        count[3, :max(seen, 0)] += 1
+        if seen < 0:
+            count[(entries - 2) % 3, bs + seen:] -= 1
+        w = x[i] * count
+        z = w.sum((1, 2))
+        want = np.einsum("hbk,bkd->hd", w, vals[1]) / z[:, None]
+        assert np.abs(lse[0, 0, i].double().cpu().numpy() - np.log(z)).max() <= 1.2e-3 + 2e-4
+        assert np.abs(po[0, 0, i].double().cpu().numpy() - want).max() <= (1.2e-3 + 0.29 + 2.0 ** -11 + 2.0 ** -12) * 2
